@@ -235,6 +235,111 @@ int qmm_gather_dequant(const int32_t *ids, int64_t T, const uint32_t *packed, co
                        qmm_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * 4-bit key/value cache: plan, append, read, attend
+ *
+ * The pages keep keys and values in a cache and rewrite attention as its own
+ * stage ("I Built an LLM Inference Engine on a 15 year old GPU ...", KV cache
+ * arena and fused online-softmax attention; "... Tesla C2075 ..." paper,
+ * section 5); these entry points give that stage in this library's number
+ * format, the group-affine INT4 of the weights: for each token, kv head and group
+ * of `group` consecutive elements of the head, w = s * q + b with q in 0..15 and binary16 s and b.
+ *
+ * The cache of one layer is caller-owned device memory of qmm_kv_cache_size()
+ * bytes, [pages][kv_heads][page / 16] tiles of 16 tokens (16 * head_dim +
+ * 128 * head_dim / group bytes each).  A slot is page_id * page + offset.
+ * Every page of a request holds `page` consecutive positions; its page ids
+ * stand in a row of the block table.  Bytes never written may hold anything:
+ * no call lets them reach a result.
+ *
+ * Common rules.  head_dim in {64, 128, 256}; group in {32, 64, 128} and a
+ * divisor of head_dim; page in {16, 32, 64, 128, 256} (QMM_ERR_UNSUPPORTED
+ * otherwise); pages * page < 2^31 (QMM_ERR_SHAPE).  int32 arrays need 4-byte alignment, everything
+ * else 16 bytes: the base of a tensor and each of its strides, in bytes, are
+ * multiples of 16 (QMM_ERR_ALIGN).  dtype is QMM_F32 or QMM_BF16.  Lengths,
+ * slots, tables and offsets live in device memory, so one captured graph
+ * serves changing requests; no value in them makes a call read or write
+ * outside the arrays that it was given.
+ */
+#define QMM_F32 0
+#define QMM_BF16 1
+
+/* Bytes of a cache of `pages` pages; 0 for arguments outside the common rules. */
+size_t qmm_kv_cache_size(int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int group);
+
+/*
+ * qmm_kv_plan -- block tables, slots and positions of one step, from the
+ *   requests' lengths, in one kernel.  Request b holds cached[b] tokens and
+ *   adds fresh[b] (negative lengths count as 0).  It has
+ *   have_b = ceil(cached[b] / page) pages and needs
+ *   ceil((cached[b] + fresh[b]) / page) - have_b more, which are taken from the
+ *   front of free_pages[n_free] in request order.
+ *   block_table [B, max_blocks]: row b's first have_b entries are read, the new
+ *     ones are written after them; other entries are left alone.
+ *   cu [B + 1]: exclusive prefix sums of fresh.  lens [B] = cached + fresh.
+ *   slots [tokens], positions [tokens]: token t of the step (requests one
+ *     after the other) stands at positions[t] of its request and in slots[t].
+ *     Entries past the step's tokens get slot -1 and position 0, so a
+ *     fixed `tokens` may exceed the step; a smaller one cuts the list.
+ *   need [1]: pages the step needs.  Where need > n_free, or a row runs past
+ *     max_blocks, the pages that are missing get table entry -1 (past
+ *     max_blocks: none) and their tokens slot -1; the rest is as usual.
+ *   0 <= B <= 8192.
+ */
+int qmm_kv_plan(const int32_t *cached, const int32_t *fresh, const int32_t *free_pages, int64_t n_free,
+                int32_t *block_table, int64_t B, int64_t max_blocks, int page, int64_t tokens, int32_t *slots,
+                int32_t *positions, int32_t *cu, int32_t *lens, int32_t *need, qmm_stream_t stream);
+
+/*
+ * qmm_kv_append -- quantize k, v [tokens, kv_heads, head_dim] (strides in
+ *   elements between tokens and between heads, elements of a head contiguous)
+ *   into the slots, with qmm_quantize's arithmetic per group: scale =
+ *   binary16((hi - lo) / 15), bias = binary16(lo), q = clamp(round((w - bias) / scale), 0, 15),
+ *   halves away from zero, NaN rules included.  A slot outside
+ *   [0, pages * page) (such as -1) is skipped.  Two tokens of a call must not
+ *   have the same slot.
+ */
+int qmm_kv_append(const void *k, const void *v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                  int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots, void *cache, int64_t tokens,
+                  int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int group, qmm_stream_t stream);
+
+/*
+ * qmm_kv_read -- the keys and values that the slots hold, s * q + b as in
+ *   qmm_dequant (float32; rounded once for QMM_BF16), to k, v [tokens,
+ *   kv_heads, head_dim], contiguous.  A slot outside the cache is not read
+ *   through and yields quiet NaNs, as in qmm_gather_dequant.
+ */
+int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int dtype, int64_t tokens, int64_t pages,
+                int64_t kv_heads, int64_t head_dim, int page, int group, qmm_stream_t stream);
+
+/*
+ * qmm_kv_attend -- softmax attention of a step's queries over the cache.
+ *   q [tokens, heads, head_dim] (strides as above), out the same, contiguous,
+ *   q's type.  heads is a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads).
+ *   Request b's queries are tokens [cu[b], cu[b + 1]) (cu == NULL: one query a
+ *   request, token b; then tokens == B).  lens[b] counts its tokens in the cache, those of the
+ *   queries among them: query i of n stands at position p = lens[b] - n + i
+ *   and sees the keys j with 0 <= j <= p and, if window > 0, j > p - window.
+ *     out = sum_j softmax_j(scale * q . k_j) v_j
+ *   A query that sees no key gets zeros.  A page id outside [0, pages), and what
+ *   lies past max_blocks, is not read: its tokens are left out.  Tokens of no request are not written.
+ *   max_fresh >= every request's queries (it picks the kernel).  scale > 0, finite.
+ *   Scores, maxima, sums and the accumulation are float32; for QMM_F32 the
+ *   queries and probabilities enter the tensor cores as two binary16 terms.
+ *   For QMM_BF16 they enter as one, rounded to binary16 (11 bits).
+ *   The result is the same on every run on the same GPU model.
+ *   workspace: qmm_kv_attend_workspace_size() bytes, whose first 4096 bytes
+ *   are zero before the first call; every call leaves them zero again.  Two calls in
+ *   flight at the same time must not share one.
+ */
+size_t qmm_kv_attend_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
+int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_head_stride, const void *cache,
+                  const int32_t *block_table, const int32_t *lens, const int32_t *cu, void *out, int64_t tokens,
+                  int64_t B, int64_t max_blocks, int64_t max_fresh, int64_t pages, int64_t heads, int64_t kv_heads,
+                  int64_t head_dim, int page, int group, float scale, int64_t window, void *workspace,
+                  size_t workspace_bytes, qmm_stream_t stream);
+
+/*
  * qmm_check -- synchronize `stream`, then report QMM_ERR_CUDA if a kernel
  * failed, QMM_ERR_DEVICE_TIMEOUT if a bounded wait in any kernel ran out
  * since the last qmm_check (and clear that record), else QMM_OK.

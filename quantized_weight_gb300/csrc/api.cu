@@ -5,8 +5,10 @@
 // then does it call one launcher of qmm_launch.h on the caller's stream.  No
 // entry point allocates or frees device memory.
 #include <cstdint>
+#include <initializer_list>
 #include <cuda_runtime.h>
 
+#include "kv_attend.h"
 #include "qmm.h"
 #include "qmm_launch.h"
 
@@ -32,6 +34,17 @@ int check_coeffs(const uint16_t *scales, const uint16_t *biases, int bits) {
   if (!aligned16(scales) || (biases && !aligned16(biases))) return QMM_ERR_ALIGN;
   return QMM_OK;
 }
+
+// Shared checks for the cache entries.
+int check_kv(int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int group) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QMM_ERR_UNSUPPORTED;
+  if (!group_ok(group) || head_dim % group != 0) return QMM_ERR_UNSUPPORTED;
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0) return QMM_ERR_UNSUPPORTED;
+  if (pages < 0 || pages >= kMaxDim || pages * page >= kMaxDim || kv_heads < 1 || kv_heads > 4096) return QMM_ERR_SHAPE;
+  return QMM_OK;
+}
+// A tensor's strides (elements of `size` bytes) keep every head's row 16-byte aligned.
+bool strides_ok(int64_t token, int64_t head, int size) { return token * size % 16 == 0 && head * size % 16 == 0; }
 
 }  // namespace
 
@@ -168,6 +181,95 @@ int qmm_gather_dequant(const int32_t *ids, int64_t T, const uint32_t *packed, co
   if (st != QMM_OK) return st;
   if (!aligned16(ids) || !aligned16(packed) || !aligned16(out)) return QMM_ERR_ALIGN;
   return cuda_status(qmm::launch_gather_dequant(ids, T, packed, scales, biases, out, N, K, bits, group, stream));
+}
+
+size_t qmm_kv_cache_size(int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int group) {
+  if (check_kv(pages, kv_heads, head_dim, page, group) != QMM_OK) return 0;
+  return (size_t)pages * (size_t)kv_heads * (size_t)(page / 16) * (size_t)(16 * head_dim + 128 * (head_dim / group));
+}
+
+int qmm_kv_plan(const int32_t *cached, const int32_t *fresh, const int32_t *free_pages, int64_t n_free,
+                int32_t *block_table, int64_t B, int64_t max_blocks, int page, int64_t tokens, int32_t *slots,
+                int32_t *positions, int32_t *cu, int32_t *lens, int32_t *need, qmm_stream_t stream) {
+  if (page < 16 || page > 256 || (page & (page - 1)) != 0) return QMM_ERR_UNSUPPORTED;
+  if (B < 0 || B > qmm::kKvPlanMaxB || n_free < 0 || n_free >= kMaxDim || max_blocks < 0 || max_blocks >= kMaxDim ||
+      tokens < 0 || tokens >= kMaxDim)
+    return QMM_ERR_SHAPE;
+  if (!cu || !need) return QMM_ERR_ARG;
+  if (B > 0 && (!cached || !fresh || !lens || (max_blocks > 0 && !block_table))) return QMM_ERR_ARG;
+  if ((n_free > 0 && !free_pages) || (tokens > 0 && (!slots || !positions))) return QMM_ERR_ARG;
+  for (const void *p : {(const void *)cached, (const void *)fresh, (const void *)free_pages, (const void *)block_table,
+                        (const void *)slots, (const void *)positions, (const void *)cu, (const void *)lens,
+                        (const void *)need})
+    if (!aligned4(p)) return QMM_ERR_ALIGN;
+  return cuda_status(qmm::launch_kv_plan(cached, fresh, free_pages, n_free, block_table, B, max_blocks, page, tokens,
+                                         slots, positions, cu, lens, need, stream));
+}
+
+int qmm_kv_append(const void *k, const void *v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                  int64_t v_token_stride, int64_t v_head_stride, const int32_t *slots, void *cache, int64_t tokens,
+                  int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int group, qmm_stream_t stream) {
+  if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+  int st = check_kv(pages, kv_heads, head_dim, page, group);
+  if (st != QMM_OK) return st;
+  if (tokens < 0 || tokens >= kMaxDim / 4096) return QMM_ERR_SHAPE;
+  if (tokens == 0 || pages == 0) return QMM_OK;
+  if (!k || !v || !slots || !cache) return QMM_ERR_ARG;
+  const int size = dtype == QMM_BF16 ? 2 : 4;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots) ||
+      !strides_ok(k_token_stride, k_head_stride, size) || !strides_ok(v_token_stride, v_head_stride, size))
+    return QMM_ERR_ALIGN;
+  return cuda_status(qmm::launch_kv_append(k, v, dtype == QMM_BF16, k_token_stride, k_head_stride, v_token_stride,
+                                           v_head_stride, slots, cache, tokens, pages, kv_heads, head_dim, page, group,
+                                           stream));
+}
+
+int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int dtype, int64_t tokens, int64_t pages,
+                int64_t kv_heads, int64_t head_dim, int page, int group, qmm_stream_t stream) {
+  if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+  int st = check_kv(pages, kv_heads, head_dim, page, group);
+  if (st != QMM_OK) return st;
+  if (tokens < 0 || tokens >= kMaxDim / 4096) return QMM_ERR_SHAPE;
+  if (tokens == 0) return QMM_OK;
+  if (!slots || (pages > 0 && !cache) || !k || !v) return QMM_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots)) return QMM_ERR_ALIGN;
+  return cuda_status(qmm::launch_kv_read(slots, cache, k, v, dtype == QMM_BF16, tokens, pages, kv_heads, head_dim, page,
+                                         group, stream));
+}
+
+size_t qmm_kv_attend_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh) {
+  if (check_kv(0, kv_heads, head_dim, 16, 32) != QMM_OK || B < 0 || max_fresh < 0 || heads < 1 || heads % kv_heads != 0)
+    return 0;
+  return qmm::kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh);
+}
+
+int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_head_stride, const void *cache,
+                  const int32_t *block_table, const int32_t *lens, const int32_t *cu, void *out, int64_t tokens,
+                  int64_t B, int64_t max_blocks, int64_t max_fresh, int64_t pages, int64_t heads, int64_t kv_heads,
+                  int64_t head_dim, int page, int group, float scale, int64_t window, void *workspace,
+                  size_t workspace_bytes, qmm_stream_t stream) {
+  if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+  int st = check_kv(pages, kv_heads, head_dim, page, group);
+  if (st != QMM_OK) return st;
+  if (tokens < 0 || tokens >= kMaxDim / 4096 || B < 0 || B >= kMaxDim || max_blocks < 0 || max_blocks * page >= kMaxDim ||
+      max_fresh < 1 || max_fresh >= kMaxDim / 4096 || heads < 1 || heads > 4096 || heads % kv_heads != 0 || window < 0)
+    return QMM_ERR_SHAPE;
+  if (!cu && (tokens != B || max_fresh != 1)) return QMM_ERR_SHAPE;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return QMM_ERR_ARG;
+  if (tokens == 0 || B == 0) return QMM_OK;
+  if (!q || !out || !lens || (max_blocks > 0 && !block_table) || (pages > 0 && !cache) || !workspace) return QMM_ERR_ARG;
+  if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace) || !aligned4(block_table) ||
+      !aligned4(lens) || !aligned4(cu) || !strides_ok(q_token_stride, q_head_stride, dtype == QMM_BF16 ? 2 : 4))
+    return QMM_ERR_ALIGN;
+  if (workspace_bytes < qmm_kv_attend_workspace_size(B, heads, kv_heads, head_dim, max_fresh)) return QMM_ERR_SHAPE;
+  qmm::KvAttendArgs a{};
+  a.q = q, a.out = out, a.cache = cache, a.table = block_table, a.lens = lens, a.cu = cu, a.workspace = workspace;
+  a.q_token = q_token_stride, a.q_head = q_head_stride;
+  a.tokens = tokens, a.B = B, a.max_blocks = max_blocks, a.max_fresh = max_fresh;
+  a.pages = pages, a.kv_heads = kv_heads, a.head_dim = head_dim, a.heads = heads;
+  a.page = page, a.group = group, a.bf16 = dtype == QMM_BF16;
+  a.scale = scale, a.window = window;
+  return cuda_status(qmm::launch_kv_attend(a, stream));
 }
 
 int qmm_test_timeout_next_decode(int64_t limit_ns) {

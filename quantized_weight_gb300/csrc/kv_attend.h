@@ -1,0 +1,30 @@
+// kv_attend.h -- arguments of the attention over the 4-bit cache, between the
+// C ABI (api.cu, which has validated them) and the kernels.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace qmm {
+
+struct KvAttendArgs {
+  const void *q;                        // [tokens, heads, head_dim], strided
+  void *out;                            // [tokens, heads, head_dim], contiguous, q's type
+  const void *cache;
+  const int32_t *table;                 // [B, max_blocks]
+  const int32_t *lens;                  // [B]
+  const int32_t *cu;                    // [B + 1], or null: query b is request b's only one
+  void *workspace;
+  int64_t q_token, q_head;              // strides in elements
+  int64_t tokens, B, max_blocks, max_fresh;
+  int64_t pages, kv_heads, head_dim, heads;
+  int page, group;
+  int bf16;                             // q and out: bfloat16, else float32
+  float scale;
+  int64_t window;                       // 0: none
+};
+
+size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
+cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
+
+}  // namespace qmm

@@ -89,6 +89,17 @@ cudaError_t launch_gemm(const uint16_t *x_bf16, const uint32_t *codes, const uin
                         const uint16_t *biases, float *y, int64_t M, int64_t N, int64_t K, int bits,
                         int group, cudaStream_t s);
 
+// 4-bit key/value cache (kv_cache.cu); the attention's launcher is in kv_attend.h.
+constexpr int64_t kKvPlanMaxB = 8192;   // 64 KB of shared memory: two prefix sums a request
+cudaError_t launch_kv_plan(const int32_t *cached, const int32_t *fresh, const int32_t *free_pages, int64_t n_free,
+                           int32_t *table, int64_t B, int64_t max_blocks, int page, int64_t tokens, int32_t *slots,
+                           int32_t *positions, int32_t *cu, int32_t *lens, int32_t *need, cudaStream_t s);
+cudaError_t launch_kv_append(const void *k, const void *v, bool bf16, int64_t k_token, int64_t k_head, int64_t v_token,
+                             int64_t v_head, const int32_t *slots, void *cache, int64_t tokens, int64_t pages,
+                             int64_t kv_heads, int64_t D, int page, int group, cudaStream_t s);
+cudaError_t launch_kv_read(const int32_t *slots, const void *cache, void *k, void *v, bool bf16, int64_t tokens,
+                           int64_t pages, int64_t kv_heads, int64_t D, int page, int group, cudaStream_t s);
+
 // Device status words written by kernels whose bounded waits ran out (one per
 // translation unit); each call synchronizes `s`, returns the word and clears it.
 cudaError_t read_clear_gemm_status(int *status, cudaStream_t s);

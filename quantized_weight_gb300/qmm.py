@@ -68,6 +68,15 @@ def lib():
             L.qmm_gemv_argmax_workspace_size.restype = ctypes.c_size_t
             L.qmm_gemv_argmax.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, ctypes.c_size_t, vp]
             L.qmm_gemv_argmax_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, vp]
+            sz, f32 = ctypes.c_size_t, ctypes.c_float
+            L.qmm_kv_cache_size.argtypes = [i64, i64, i64, i32, i32]
+            L.qmm_kv_plan.argtypes = [vp, vp, vp, i64, vp, i64, i64, i32, i64, vp, vp, vp, vp, vp, vp]
+            L.qmm_kv_append.argtypes = [vp, vp, i32, i64, i64, i64, i64, vp, vp, i64, i64, i64, i64, i32, i32, vp]
+            L.qmm_kv_read.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, i32, i32, vp]
+            L.qmm_kv_attend_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+            L.qmm_kv_attend.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64,
+                                        i32, i32, f32, i64, vp, sz, vp]
+            L.qmm_kv_cache_size.restype = L.qmm_kv_attend_workspace_size.restype = sz
             L.qmm_check.argtypes = [vp]
             L.qmm_test_timeout_next_decode.argtypes = [i64]
             L.qmm_status_string.argtypes = [i32]
@@ -75,7 +84,8 @@ def lib():
             L.qmm_abi_version.argtypes = []
             for f in ("qmm_pack", "qmm_unpack", "qmm_dequant", "qmm_gemv", "qmm_gemm", "qmm_quantize",
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
-                      "qmm_test_timeout_next_decode", "qmm_abi_version"):
+                      "qmm_test_timeout_next_decode", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
+                      "qmm_kv_attend"):
                 getattr(L, f).restype = i32
             _lib = L
     return _lib
@@ -254,6 +264,132 @@ def gather_dequant(ids, packed, scales, biases, N, K, bits, group, out=None, str
     _need(out, "out", torch.float32, (T, K))
     _call("qmm_gather_dequant", lib().qmm_gather_dequant(_ptr(ids), T, _ptr(packed), _ptr(scales), _ptr(biases),
                                                          _ptr(out), N, K, bits, group, _stream(stream)))
+    return out
+
+
+_KV_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _kv_rows(t, name, dtype, shape):
+    """A [tokens, heads, head_dim] tensor whose last dimension is contiguous; its strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)   # a lone row has no stride to keep
+
+
+def _kv_dtype(dtype):
+    if dtype not in _KV_DTYPE:
+        raise TypeError(f"keys, values and queries are float32 or bfloat16, got {dtype}")
+    return _KV_DTYPE[dtype]
+
+
+def _kv_cache_ok(cache, D, page, group):
+    _need(cache, "cache", torch.uint8)
+    if cache.dim() != 3 or cache.shape[2] * 16 != page * (16 * D + 128 * (D // group)):
+        raise ValueError(f"cache must be [pages, kv_heads, bytes] as kv_cache() makes it for head_dim {D}, page {page}, "
+                         f"group {group}; got {tuple(cache.shape)}")
+
+
+def kv_cache(pages, kv_heads, head_dim, page, group=64, device="cuda") -> torch.Tensor:
+    """The 4-bit key/value cache of one layer: uint8 [pages, kv_heads, bytes of a head's page]."""
+    n = int(lib().qmm_kv_cache_size(pages, kv_heads, head_dim, page, group))
+    if n == 0 and pages != 0:
+        raise ValueError(f"no cache of head_dim {head_dim}, page {page}, group {group} with {pages} pages of {kv_heads} heads")
+    return torch.zeros((pages, kv_heads, n // (pages * kv_heads) if pages else 0), dtype=torch.uint8, device=device)
+
+
+def kv_plan(cached, fresh, free_pages, block_table, tokens, page, out=None, stream=None):
+    """One step's (slots [tokens], positions [tokens], cu [B + 1], lens [B], need [1]), int32, from the requests'
+    lengths; block_table [B, max_blocks] is completed in place with pages from the front of free_pages."""
+    i32 = torch.int32
+    _need(cached, "cached", i32)
+    B = cached.numel()
+    _need(fresh, "fresh", i32, (B,))
+    _need(free_pages, "free_pages", i32)
+    _need(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
+    if out is None:
+        buf = torch.empty((2 * tokens + 2 * B + 2,), dtype=i32, device=cached.device)
+        out = buf.split((tokens, tokens, B + 1, B, 1))
+    slots, positions, cu, lens, need = out
+    for t, name, n in ((slots, "slots", tokens), (positions, "positions", tokens), (cu, "cu", B + 1), (lens, "lens", B),
+                       (need, "need", 1)):
+        _need(t, name, i32, (n,))
+    _call("qmm_kv_plan", lib().qmm_kv_plan(_ptr(cached), _ptr(fresh), _ptr(free_pages), free_pages.numel(),
+                                           _ptr(block_table), B, block_table.shape[1], page, tokens, _ptr(slots),
+                                           _ptr(positions), _ptr(cu), _ptr(lens), _ptr(need), _stream(stream)))
+    return out
+
+
+def kv_append(k, v, slots, cache, page, group=64, stream=None) -> None:
+    """Quantize k, v [T, kv_heads, head_dim] (float32 or bfloat16) into the cache's slots; a slot outside it is skipped."""
+    T, H, D = k.shape
+    dt = _kv_dtype(k.dtype)
+    ks = _kv_rows(k, "k", k.dtype, k.shape)
+    vs = _kv_rows(v, "v", k.dtype, k.shape)
+    _need(slots, "slots", torch.int32, (T,))
+    _kv_cache_ok(cache, D, page, group)
+    if cache.shape[1] != H:
+        raise ValueError(f"cache has {cache.shape[1]} kv heads, k has {H}")
+    _call("qmm_kv_append", lib().qmm_kv_append(_ptr(k), _ptr(v), dt, *ks, *vs, _ptr(slots), _ptr(cache), T,
+                                               cache.shape[0], H, D, page, group, _stream(stream)))
+
+
+def kv_read(slots, cache, head_dim, page, group=64, dtype=torch.float32, out=None, stream=None):
+    """The (keys, values) [T, kv_heads, head_dim] that the slots hold; a slot outside the cache gives NaN rows."""
+    _need(slots, "slots", torch.int32)
+    _kv_cache_ok(cache, head_dim, page, group)
+    dt, shape = _kv_dtype(dtype), (slots.numel(), cache.shape[1], head_dim)
+    if out is None:
+        out = torch.empty((2,) + shape, dtype=dtype, device=cache.device).unbind(0)
+    k, v = out
+    _need(k, "k", dtype, shape)
+    _need(v, "v", dtype, shape)
+    _call("qmm_kv_read", lib().qmm_kv_read(_ptr(slots), _ptr(cache), _ptr(k), _ptr(v), dt, shape[0], cache.shape[0],
+                                           shape[1], head_dim, page, group, _stream(stream)))
+    return k, v
+
+
+def kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh=1, device="cuda") -> torch.Tensor:
+    """A zeroed work area for kv_attend (reusable: every call leaves it ready)."""
+    n = int(lib().qmm_kv_attend_workspace_size(B, heads, kv_heads, head_dim, max_fresh))
+    if n == 0:
+        raise ValueError(f"no attention of {heads} heads over {kv_heads} kv heads of {head_dim}")
+    return torch.zeros(((n + 15) // 16 * 16,), dtype=torch.uint8, device=device)
+
+
+def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_fresh=1, scale=None, window=0, out=None,
+              stream=None) -> torch.Tensor:
+    """Attention of q [T, heads, head_dim] (float32 or bfloat16) over each request's cached tokens, causal, with an
+    optional sliding window: request b's queries are tokens cu[b] .. cu[b + 1] - 1 (cu None: token b), the last of
+    its lens[b] tokens.  scale defaults to head_dim ** -0.5."""
+    T, H, D = q.shape
+    dt = _kv_dtype(q.dtype)
+    qs = _kv_rows(q, "q", q.dtype, q.shape)
+    _kv_cache_ok(cache, D, page, group)
+    _need(lens, "lens", torch.int32)
+    B = lens.numel()
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
+    if cu is not None:
+        _need(cu, "cu", torch.int32, (B + 1,))
+    _need(workspace, "workspace", torch.uint8)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    _need(out, "out", q.dtype, (T, H, D))
+    _call("qmm_kv_attend", lib().qmm_kv_attend(
+        _ptr(q), dt, *qs, _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(cu), _ptr(out), T, B, block_table.shape[1],
+        max_fresh, cache.shape[0], H, cache.shape[1], D, page, group, D ** -0.5 if scale is None else scale, window,
+        _ptr(workspace), workspace.numel(), _stream(stream)))
     return out
 
 
