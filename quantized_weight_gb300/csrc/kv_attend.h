@@ -24,7 +24,33 @@ struct KvAttendArgs {
   int64_t window;                       // 0: none
 };
 
+// CTAs of a launch: one an SM, at most 1024 (their counters are the workspace's first 4096 bytes).
+constexpr int kKvMaxCtas = 1024;
+inline int kv_max_ctas() {
+  static int n = 0;
+  if (n == 0) {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        v <= 0) {
+      (void)cudaGetLastError();          // no device here: the size that a GB300 needs
+      return 152;
+    }
+    n = v > kKvMaxCtas ? kKvMaxCtas : v;
+  }
+  return n;
+}
+
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
+cudaError_t read_clear_kv_status(int *status, cudaStream_t s);
+
+// Per head dimension (one translation unit each); nt: tiles of 8 rows of q an item
+// (heads of 256: one, since registers and shared memory hold no more).
+cudaError_t launch_kv_warp_d64(const KvAttendArgs &a, int nt, cudaStream_t s);
+cudaError_t launch_kv_warp_d128(const KvAttendArgs &a, int nt, cudaStream_t s);
+cudaError_t launch_kv_warp_d256(const KvAttendArgs &a, cudaStream_t s);
+cudaError_t read_clear_kv_d64_status(int *status, cudaStream_t s);
+cudaError_t read_clear_kv_d128_status(int *status, cudaStream_t s);
+cudaError_t read_clear_kv_d256_status(int *status, cudaStream_t s);
 
 }  // namespace qmm

@@ -1,0 +1,941 @@
+// kv_attend_warp.cuh -- attention over the 4-bit cache on the warp-level tensor
+// cores (mma.sync m16n8k16): single tokens, drafts of a few tokens, and float32
+// queries of any number.
+//
+// For one kv head and R = queries * (heads / kv_heads) rows of q,
+//   s[t, r] = scale * sum_g ( sk[t,g] * sum_{d in g} code_k[t,d] q[r,d] + bk[t,g] * sum_{d in g} q[r,d] )
+//   o[r, d] = sum_t p[t,r] sv[t,g(d)] code_v[t,d] + sum_t p[t,r] bv[t,g(d)],   p = exp(s - max)
+// so the codes enter the tensor cores as they are, as exact binary16 integers
+// (a masked nibble is the integer times 2^-24, and 16 times it for the upper nibble of
+// a byte), and scales and biases act on 16 x 8 score tiles in float32.
+//
+// Orientation.  Tokens (keys) and elements (values) are the 16-wide M side, up
+// to 8 rows of q the N side: S^T = K q^T, O^T = V^T P^T.  A group of up to 8
+// query heads then fills an MMA's N (16 rows of q on the M side would leave half of it
+// empty), and the transposed score tile becomes the B operand of the value
+// product by one movmatrix per 8 x 8 block.  q is scaled per row by the power
+// of two that puts its largest element in [2^14, 2^15).
+//
+// Precision.  HL (float32 queries): q and p * sv enter as two binary16 terms
+// each, and value codes as q - 8 (one HADD2), with bv + 8 sv as the bias: the
+// products then have the size of the result, instead of a large positive
+// sum that the bias takes back.  Otherwise (bfloat16) as one term: q is exact
+// in it, p * sv is rounded to 11 bits.  p * sv is scaled by a power of two that follows the
+// largest sv met, so small scales do not fall into binary16's
+// subnormals.  MMA chains run over 32 tokens and are then added to
+// float32 registers (chains over the whole context would pick up the tensor core's truncation at every step).
+//
+// Work split.  Items are (request, kv head, tile of 8 NT rows); the units of
+// 32 tokens of all items form one line, which is cut into equal runs, one a
+// CTA, wherever the cuts fall: ragged batches and single long requests load
+// all SMs alike, decided on the device from the lengths.  Inside a CTA the warps take
+// units in turn, each with a ring of its own (bulk copies into shared
+// memory, S units deep, issued across the ends of items), and join at the end of
+// an item.  An item cut between CTAs leaves partial results in the workspace; the CTA
+// that finishes last (a counter) adds them up in CTA order, so the result does not depend
+// on which it is.
+//
+// What bounds it: HBM for long contexts (144 bytes a token and head at D = 128,
+// group 64).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "bounded_wait.cuh"
+#include "kv_attend.h"
+#include "kv_layout.cuh"
+#include "qmm_device.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qmm {
+namespace kvw {
+
+using namespace sm100;
+
+static __device__ int g_status = 0;    // QMM_OK or QMM_ERR_DEVICE_TIMEOUT (-6), one a translation unit
+
+constexpr int kUnit = 32;              // tokens a warp takes at a time: two tiles
+constexpr int kMaxSegs = 32;           // items a CTA lists at a time
+constexpr int kSmemMax = 227 * 1024;
+
+struct Params {
+  KvAttendArgs a;
+  KvGeom g;
+  int ratio;             // query heads per kv head
+  int min_units;         // units worth a CTA of its own
+};
+
+// One item (or the part of it) that this CTA works on.
+struct Seg {
+  int b, kvh, r0, rows;           // rows r0 .. r0 + rows - 1 of the request's R
+  int a, e;                       // units [a, e) of 32 tokens, clipped to what the rows see
+  int vlo, vhi;                   // tokens that any of the rows sees
+  int flo, fhi;                   // tokens that all rows see
+  int base;                       // position of the request's first query
+  int hi;                         // tokens that can be read
+  int cu0;
+  int c0, nseg;                   // first CTA and number of CTAs that share the item
+};
+
+template <int D, int NT, bool HL>
+struct Cfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int W = (D == 256 || NT == 2) ? 8 : 12;       // warps (registers: 64 K / threads)
+  static constexpr int THREADS = 32 * W;
+  static constexpr int KS = D / 16;                              // MMA k-steps of a score
+  static constexpr int QW = HL ? 4 : 2;                          // 32-bit words of q per lane and k-step
+  static constexpr bool QREG = KS * NT * QW <= 32;               // q fragments stay in registers
+  static constexpr int OS = D + 4;                               // row stride of the join area (floats)
+  static constexpr int ESZ = HL ? 4 : 2;
+  // shared memory: ring | q fragments | raw q | join area | small arrays
+  static constexpr int QF = KS * NT * 32 * QW * 4;
+  static constexpr int RAW = ROWS * D * ESZ;
+  static constexpr int JOIN = W / 2 * ROWS * OS * 4;
+  __host__ __device__ static constexpr int fixed(int G) {
+    return QF + RAW + JOIN + ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ +
+           2 * W * ROWS * 4 /* m, l per warp */ + 2 * ROWS * 4 /* M, L */ + kMaxSegs * (int)sizeof(Seg) +
+           W * 4 * 12 /* barriers, notes: up to 4 stages */ + 256 + W * 8;
+  }
+  // units in flight a warp: what shared memory holds, up to four
+  __host__ __device__ static constexpr int stages(int G) {
+    const int n = (kSmemMax - fixed(G)) / (W * 2 * (16 * D + 128 * G));
+    return n > 4 ? 4 : n;
+  }
+};
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  const __half2 h = *reinterpret_cast<const __half2 *>(&v);
+  return __half22float2(h);
+}
+__device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// Exponent S with max * 2^S in [2^14, 2^15) from the largest |x|'s bits; 0 for zero and non-finite.
+__device__ __forceinline__ int row_exp(uint32_t mbits) {
+  if (mbits == 0u || mbits >= 0x7F800000u) return 0;
+  const int S = 14 - ((int)(mbits >> 23) - 127);
+  return S > 126 ? 126 : S;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// A request as the split sees it.
+struct Req {
+  int n, len, hi, lo, base, cu0;      // queries; tokens; readable end; first unit; ...
+  int units, tiles;                   // units an item spans; row tiles
+};
+
+__device__ __forceinline__ Req request(const Params &p, int b, int rows_tile) {
+  Req r;
+  const KvAttendArgs &a = p.a;
+  r.len = max(0, a.lens[b]);
+  if (a.cu) {
+    const int c0 = max(0, min(a.cu[b], (int)a.tokens)), c1 = max(c0, min(a.cu[b + 1], (int)a.tokens));
+    r.cu0 = c0;
+    r.n = c1 - c0;
+  } else {
+    r.cu0 = b;
+    r.n = 1;
+  }
+  r.base = r.len - r.n;                                     // may be negative: such queries see nothing
+  r.hi = (int)min((int64_t)r.len, a.max_blocks << p.g.lg_page);
+  const int64_t first = a.window > 0 ? (int64_t)r.base + 1 - a.window : 0;
+  r.lo = first > 0 ? (int)min(first, (int64_t)r.hi) / kUnit : 0;
+  r.tiles = (int)(((int64_t)r.n * p.ratio + rows_tile - 1) / rows_tile);
+  // an item without tokens still has its zeros written
+  r.units = r.n == 0 ? 0 : max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
+  return r;
+}
+
+template <int G>
+__device__ __forceinline__ void load_coefs(const uint8_t *p, uint32_t (&c)[G]) {
+  if constexpr (G == 1) {
+    c[0] = *reinterpret_cast<const uint32_t *>(p);
+  } else if constexpr (G == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    c[0] = v.x, c[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < G; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+      c[i] = v.x, c[i + 1] = v.y, c[i + 2] = v.z, c[i + 3] = v.w;
+    }
+  }
+}
+
+template <int D, int G, int NT, bool HL>
+__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, NT, HL>;
+  constexpr int W = C::W, ROWS = C::ROWS, KS = C::KS, QW = C::QW, OS = C::OS;
+  constexpr int TILE = 16 * D + 128 * G, STAGE = 2 * TILE;
+  constexpr int WPL = D / 32;                    // key words per lane and row
+  constexpr int WPG = WPL / G;                   // of them in a group
+  constexpr int VW = D / 16;                     // value words per lane
+  constexpr int S = C::stages(G);
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
+  uint8_t *at = smem + W * S * STAGE;
+  uint32_t *qf = reinterpret_cast<uint32_t *>(at);
+  at += C::QF;
+  uint8_t *raw = at;
+  at += C::RAW;
+  float *join = reinterpret_cast<float *>(at);
+  at += C::JOIN;
+  float *qsum = reinterpret_cast<float *>(at);   // [G][ROWS]
+  at += ROWS * G * 4;
+  float *fq = reinterpret_cast<float *>(at);     // [ROWS]
+  at += ROWS * 4;
+  int *lim = reinterpret_cast<int *>(at);        // [ROWS][2]: tokens [lo, hi) a row sees
+  at += ROWS * 8;
+  float *wm = reinterpret_cast<float *>(at), *wl = wm + W * ROWS;   // [W][ROWS]
+  at += 2 * W * ROWS * 4;
+  float *cm = reinterpret_cast<float *>(at), *cl = cm + ROWS;       // [ROWS]
+  at += 2 * ROWS * 4;
+  Seg *segs = reinterpret_cast<Seg *>(at);
+  at += kMaxSegs * sizeof(Seg);
+  at = smem + ((at - smem + 15) & ~15);
+  const uint32_t bars = smem_addr(at);                              // [W][4]
+  at += W * 4 * 8;
+  int *notes = reinterpret_cast<int *>(at);                         // [W][4]: tiles of the unit that were not copied
+  at += W * 4 * 4;
+  int64_t *sh64 = reinterpret_cast<int64_t *>(at);                  // [W]
+  at += W * 8;
+  volatile int *ctrl = reinterpret_cast<volatile int *>(at);        // abort, b, off, segments, next b, next off, last
+  const WaitCtl ctl{ctrl, &g_status};
+
+  const uint32_t my_bar = bars + warp * 32;
+  const uint32_t my_ring = smem_addr(smem) + warp * S * STAGE;
+  const uint8_t *ring_ptr = smem + warp * S * STAGE;
+  int *my_note = notes + warp * 4;
+  if (lane == 0)
+    for (int s = 0; s < S; s++) mbar_init(my_bar + 8 * s, 1);
+  if (threadIdx.x == 0) ctrl[0] = 0;
+  fence_mbar_init();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---------------------------------------------------------------- this CTA's run of units
+  const KvAttendArgs &a = p.a;
+  const int B = (int)a.B, hkv = p.g.kv_heads;
+  const int per = (B + C::THREADS - 1) / C::THREADS;
+  const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; b++) {
+    const Req r = request(p, b, ROWS);
+    mine += (int64_t)r.units * r.tiles * hkv;
+  }
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) sh64[warp] = inc;
+  __syncthreads();
+  int64_t total = 0, before = inc - mine;
+#pragma unroll
+  for (int w = 0; w < W; w++) {
+    if (w < warp) before += sh64[w];
+    total += sh64[w];
+  }
+  const int64_t want = (total + p.min_units - 1) / p.min_units;
+  const int A = (int)(want < gridDim.x ? want : gridDim.x);
+  if ((int)blockIdx.x >= A) return;                                  // also when there is nothing to do
+  const int64_t u0 = total * blockIdx.x / A, u1 = total * (blockIdx.x + 1) / A;
+  if (before <= u0 && u0 < before + mine) {
+    int b = b0;
+    int64_t off = u0 - before;
+    for (;; b++) {
+      const Req r = request(p, b, ROWS);
+      const int64_t n = (int64_t)r.units * r.tiles * hkv;
+      if (off < n) break;
+      off -= n;
+    }
+    ctrl[1] = b;
+    *reinterpret_cast<volatile int64_t *>(ctrl + 2) = off;
+  }
+  __syncthreads();
+  int cb = ctrl[1];
+  int64_t coff = *reinterpret_cast<volatile int64_t *>(ctrl + 2);
+  int64_t cu_ = u0;                                                  // the line's unit that (cb, coff) stands for
+
+  int islot = 0, tslot = 0, flight = 0;                              // this warp's ring: next slot to fill, to take, copies out
+  uint32_t tphase = 0;
+  bool ok = true;
+  while (cu_ < u1 && ok) {
+    // -------------------------------------------------------------- list the next items (warp 0, a request a lane)
+    __syncthreads();
+    if (warp == 0) {
+      const int b = cb + lane;
+      Req r{};
+      if (b < B) r = request(p, b, ROWS);
+      const int items = r.tiles * hkv;
+      const int64_t n = (int64_t)r.units * items;
+      int64_t end = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += u;
+      }
+      const int64_t first = end - n;                                 // the request's units, relative to request cb's start
+      const int64_t lo = coff, hi = coff + (u1 - cu_);               // this CTA's, relative too
+      const int64_t s0 = first > lo ? first : lo, s1 = end < hi ? end : hi;
+      const int i0 = s1 > s0 ? (int)((s0 - first) / r.units) : 0;
+      const int cnt = s1 > s0 ? (int)((s1 - 1 - first) / r.units) - i0 + 1 : 0;
+      int place = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, place, o);
+        if (lane >= o) place += u;
+      }
+      place -= cnt;
+      for (int i = 0; i < cnt && place + i < kMaxSegs; i++) {
+        const int idx = i0 + i;
+        const int64_t i_s = first + (int64_t)idx * r.units, i_e = i_s + r.units;   // the item's units, relative
+        const int64_t x0 = i_s > lo ? i_s : lo, x1 = i_e < hi ? i_e : hi;
+        Seg s;
+        s.b = b;
+        s.kvh = idx / r.tiles;
+        s.r0 = idx % r.tiles * ROWS;
+        s.rows = min(ROWS, r.n * p.ratio - s.r0);
+        const int f = s.r0 / p.ratio, l = (s.r0 + s.rows - 1) / p.ratio;   // first and last query of the tile
+        const int64_t w = a.window > 0 ? a.window : (int64_t)1 << 40;
+        auto clip = [&](int64_t v) { return (int)(v < 0 ? 0 : v > r.hi ? r.hi : v); };
+        s.vlo = clip((int64_t)r.base + f + 1 - w);
+        s.vhi = clip((int64_t)r.base + l + 1);
+        s.flo = clip((int64_t)r.base + l + 1 - w);
+        s.fhi = clip((int64_t)r.base + f + 1);
+        s.a = max(r.lo + (int)(x0 - i_s), s.vlo / kUnit);
+        s.e = min(r.lo + (int)(x1 - i_s), (s.vhi + kUnit - 1) / kUnit);
+        if (s.vhi <= s.vlo) s.e = s.a;
+        s.base = r.base;
+        s.hi = r.hi;
+        s.cu0 = r.cu0;
+        // the line's units of the item -> the CTAs they fall to: CTA c takes from floor(total c / A) on
+        const int64_t g0 = cu_ - coff + i_s, g1 = cu_ - coff + i_e - 1;
+        s.c0 = (int)(((g0 + 1) * A - 1) / total);
+        s.nseg = (int)(((g1 + 1) * A - 1) / total) - s.c0 + 1;
+        segs[place + i] = s;
+      }
+      // where the list ends: after kMaxSegs items or these 32 requests
+      const int listed = __reduce_add_sync(0xffffffffu, max(0, min(cnt, kMaxSegs - place)));
+      int64_t stop = 0;
+      if (cnt > 0 && place < kMaxSegs) {
+        const int last = min(cnt, kMaxSegs - place);
+        const int64_t e = first + (int64_t)(i0 + last) * r.units;
+        stop = e < hi ? e : hi;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const int64_t u = __shfl_xor_sync(0xffffffffu, stop, o);
+        stop = u > stop ? u : stop;
+      }
+      if (listed == 0) stop = __shfl_sync(0xffffffffu, end, 31);     // 32 requests without queries
+      // the request that holds unit `stop`, and the place in it
+      const unsigned m = __ballot_sync(0xffffffffu, end > stop);
+      const int src = m ? __ffs(m) - 1 : 31;
+      const int64_t src_first = __shfl_sync(0xffffffffu, first, src), src_end = __shfl_sync(0xffffffffu, end, src);
+      if (lane == 0) {
+        ctrl[4] = listed;
+        ctrl[5] = m ? cb + src : cb + 32;
+        *reinterpret_cast<volatile int64_t *>(ctrl + 6) = m ? stop - src_first : stop - src_end;
+        *reinterpret_cast<volatile int64_t *>(ctrl + 8) = stop - coff;
+      }
+    }
+    __syncthreads();
+    const int nsegs = ctrl[4];
+    cb = ctrl[5];
+    coff = *reinterpret_cast<volatile int64_t *>(ctrl + 6);
+    cu_ += *reinterpret_cast<volatile int64_t *>(ctrl + 8);
+    if (nsegs == 0) continue;
+
+    // -------------------------------------------------------------- producer: this warp's units, in order
+    int ps = 0, pu = 0;                                              // segment, unit
+    int pg0 = -1, pg1 = -1;                                          // its page ids, fetched one unit ahead
+    const int32_t *ptab = nullptr;
+    int pvhi = 0, pe = 0, pkvh = 0;
+    auto fetch_pages = [&]() {
+      const int tok = pu * kUnit;
+      pg0 = tok < pvhi ? ptab[tok >> p.g.lg_page] : -1;
+      pg1 = p.g.page == kKvTile ? (tok + kKvTile < pvhi ? ptab[(tok + kKvTile) >> p.g.lg_page] : -1) : pg0;
+    };
+    auto open_seg = [&]() {                                          // first unit of the next segment that has one for this warp
+      for (; ps < nsegs; ps++) {
+        const Seg &s = segs[ps];
+        pu = s.a + warp;
+        pe = s.e;
+        if (pu < pe) {
+          pvhi = s.vhi;
+          pkvh = s.kvh;
+          ptab = a.table + (int64_t)s.b * a.max_blocks;
+          fetch_pages();
+          return;
+        }
+      }
+    };
+    auto issue = [&]() {
+      if (ps >= nsegs) return;
+      const int slot = islot;
+      if (lane == 0) {
+        const bool v0 = pg0 >= 0 && pg0 < p.g.pages, v1 = pg1 >= 0 && pg1 < p.g.pages;
+        my_note[slot] = (v0 ? 0 : 1) | (v1 ? 0 : 2);
+        const uint32_t bar = my_bar + 8 * slot, dst = my_ring + slot * STAGE;
+        const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
+        const int off = (pu * kUnit) & (p.g.page - 1);
+        const uint8_t *s0 = cache + ((int64_t)pg0 * hkv + pkvh) * p.g.head_bytes + (off >> 4) * TILE;
+        if (p.g.page != kKvTile) {
+          if (v0) {
+            mbar_arrive_expect_tx(bar, STAGE);
+            bulk_copy(dst, s0, STAGE, bar);
+          } else {
+            mbar_arrive(bar);
+          }
+        } else {
+          const uint32_t bytes = (v0 ? TILE : 0) + (v1 ? TILE : 0);
+          if (bytes) mbar_arrive_expect_tx(bar, bytes);
+          else mbar_arrive(bar);
+          if (v0) bulk_copy(dst, s0, TILE, bar);
+          if (v1) bulk_copy(dst + TILE, cache + ((int64_t)pg1 * hkv + pkvh) * p.g.head_bytes, TILE, bar);
+        }
+      }
+      islot = islot + 1 == S ? 0 : islot + 1;
+      flight++;
+      pu += W;
+      if (pu < pe) fetch_pages();
+      else ps++, open_seg();
+    };
+    open_seg();
+    for (int s = 0; s < S; s++) issue();
+
+    // raw q of a segment, fetched while the one before it runs
+    auto fetch_q = [&](const Seg &s) {
+      constexpr int CH = D * C::ESZ / 16;                            // 16-byte pieces a row
+      for (int i = threadIdx.x; i < ROWS * CH; i += C::THREADS) {
+        const int row = i / CH, c = i % CH;
+        if (row < s.rows) {
+          const int r = s.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
+          const int64_t off = (int64_t)(s.cu0 + qi) * a.q_token + (int64_t)(s.kvh * p.ratio + hq) * a.q_head;
+          cp_async16(smem_addr(raw) + i * 16, static_cast<const uint8_t *>(a.q) + off * C::ESZ + c * 16);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch_q(segs[0]);
+
+    for (int si = 0; si < nsegs; si++) {
+      const Seg &sg = segs[si];
+      const int rows = sg.rows;
+      // ------------------------------------------------------------ q -> fragments, sums, limits
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      for (int i = threadIdx.x; i < ROWS * (D / 8); i += C::THREADS) {   // whole warps: D / 8 threads a row
+        const int row = i / (D / 8), m = i % (D / 8);
+        float v[8];
+        if (row < rows) {
+          if constexpr (HL) {
+            const float4 x = *reinterpret_cast<const float4 *>(raw + row * D * 4 + m * 32);
+            const float4 y = *reinterpret_cast<const float4 *>(raw + row * D * 4 + m * 32 + 16);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D * 2 + m * 16);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) v[2 * j] = __uint_as_float(u[j] << 16), v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; j++) v[j] = 0.0f;
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < 8; j++) mx = max(mx, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < D / 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int ex = row_exp(mx);
+        const float f = pow2i(ex);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] *= f, sum += v[j];
+#pragma unroll
+        for (int o = 1; o < D / G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (m % (D / G / 8) == 0) qsum[m / (D / G / 8) * ROWS + row] = sum * pow2i(-24);
+        if (m == 0) {
+          fq[row] = ldexpf(a.scale * 1.44269504088896340736f, 24 - ex);     // log2(e)
+          const int qi = (sg.r0 + row) / p.ratio;
+          const int64_t pos = (int64_t)sg.base + qi;
+          const int64_t lo = a.window > 0 ? pos + 1 - a.window : 0;
+          lim[2 * row] = (int)max((int64_t)0, min(lo, (int64_t)sg.hi));
+          lim[2 * row + 1] = row < rows ? (int)max((int64_t)0, min(pos + 1, (int64_t)sg.hi)) : 0;
+        }
+        // word w = m / 4 of lane (row % 8, t = m % 4): k-steps 2w (nibbles 0 4 | 1 5) and 2w + 1 (2 6 | 3 7)
+        const int w = m >> 2, t = m & 3, n = row >> 3, ln = (row & 7) * 4 + t;
+#pragma unroll
+        for (int st = 0; st < 2; st++) {
+          const float x0 = v[2 * st], x1 = v[2 * st + 4], z0 = v[2 * st + 1] * 0.0625f, z1 = v[2 * st + 5] * 0.0625f;
+          uint32_t *dst = qf + (((2 * w + st) * NT + n) * 32 + ln) * QW;
+          const uint32_t h0 = pack_f16(x0, x1), h1 = pack_f16(z0, z1);
+          dst[0] = h0, dst[1] = h1;
+          if constexpr (HL) {
+            const float2 e0 = unpack_f16(h0), e1 = unpack_f16(h1);
+            dst[2] = pack_f16(x0 - e0.x, x1 - e0.y), dst[3] = pack_f16(z0 - e1.x, z1 - e1.y);
+          }
+        }
+      }
+      __syncthreads();
+      if (si + 1 < nsegs) fetch_q(segs[si + 1]);
+
+      uint32_t qr[C::QREG ? KS : 1][NT][QW];
+      auto load_q = [&](int ks, int n, uint32_t (&d)[QW]) {
+        const uint32_t *src = qf + ((ks * NT + n) * 32 + lane) * QW;
+        if constexpr (HL) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(src);
+          d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2 *>(src);
+          d[0] = v.x, d[1] = v.y;
+        }
+      };
+      if constexpr (C::QREG) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ks++)
+#pragma unroll
+          for (int n = 0; n < NT; n++) load_q(ks, n, qr[ks][n]);
+      }
+      float f[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) f[n][0] = fq[8 * n + 2 * lt], f[n][1] = fq[8 * n + 2 * lt + 1];
+
+      const float NINF = __int_as_float(0xFF800000);
+      float o[NT][VW][4], ob[NT][2][G], mr[NT][2], lr[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+#pragma unroll
+        for (int w = 0; w < VW; w++) o[n][w][0] = o[n][w][1] = o[n][w][2] = o[n][w][3] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          mr[n][c] = NINF, lr[n][c] = 0.0f;
+#pragma unroll
+          for (int g = 0; g < G; g++) ob[n][c][g] = 0.0f;
+        }
+      }
+      int ve = 0;                                                    // largest exponent field among the value scales so far
+      const int tk = 4 * (lg >> 1) + 2 * (lg & 1);                   // token of row lg in its tile; row lg + 8 is the next one
+
+      for (int u = sg.a + warp; u < sg.e; u += W) {
+        const int slot = tslot;
+        if (!__all_sync(0xffffffffu, wait_bounded(my_bar + 8 * slot, tphase, ctl))) { ok = false; break; }
+        if (++tslot == S) tslot = 0, tphase ^= 1u;
+        flight--;
+        const uint8_t *st = ring_ptr + slot * STAGE;
+        const int note = my_note[slot];
+        const bool full = note == 0 && u * kUnit >= sg.flo && u * kUnit + kUnit <= sg.fhi;
+
+        // ---------------------------------------------------------- scores of 32 tokens
+        float y[2][NT][4];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          const uint8_t *tile = st + i * TILE;
+          uint32_t kw[2][WPL], kc[2][G];
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const int row = lg + 8 * h;
+            if constexpr (WPL == 2) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(tile + (row * 4 + lt) * 8);
+              kw[h][0] = v.x, kw[h][1] = v.y;
+            } else {
+#pragma unroll
+              for (int c = 0; c < WPL / 4; c++) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(tile + ((c * 16 + row) * 4 + lt) * 16);
+                kw[h][4 * c] = v.x, kw[h][4 * c + 1] = v.y, kw[h][4 * c + 2] = v.z, kw[h][4 * c + 3] = v.w;
+              }
+            }
+            load_coefs<G>(tile + 16 * D + row * G * 4, kc[h]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; n++) y[i][n][0] = y[i][n][1] = y[i][n][2] = y[i][n][3] = 0.0f;
+#pragma unroll
+          for (int g = 0; g < G; g++) {
+            float c[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; n++) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+#pragma unroll
+            for (int w = g * WPG; w < (g + 1) * WPG; w++) {
+#pragma unroll
+              for (int s2 = 0; s2 < 2; s2++) {
+                const uint32_t x0 = kw[0][w] >> (8 * s2), x1 = kw[1][w] >> (8 * s2);
+                const uint32_t a0 = x0 & 0x000F000Fu, a1 = x1 & 0x000F000Fu, a2 = x0 & 0x00F000F0u, a3 = x1 & 0x00F000F0u;
+#pragma unroll
+                for (int n = 0; n < NT; n++) {
+                  uint32_t qv[QW];
+                  if constexpr (C::QREG) {
+#pragma unroll
+                    for (int j = 0; j < QW; j++) qv[j] = qr[2 * w + s2][n][j];
+                  } else {
+                    load_q(2 * w + s2, n, qv);
+                  }
+                  mma(c[n], a0, a1, a2, a3, qv[0], qv[1]);
+                  if constexpr (HL) mma(c[n], a0, a1, a2, a3, qv[2], qv[3]);
+                }
+              }
+            }
+            const float2 k0 = unpack_f16(kc[0][g]), k1 = unpack_f16(kc[1][g]);   // scale, bias
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+              const float2 qs = *reinterpret_cast<const float2 *>(qsum + g * ROWS + 8 * n + 2 * lt);
+              y[i][n][0] = fmaf(k0.x, c[n][0], fmaf(k0.y, qs.x, y[i][n][0]));
+              y[i][n][1] = fmaf(k0.x, c[n][1], fmaf(k0.y, qs.y, y[i][n][1]));
+              y[i][n][2] = fmaf(k1.x, c[n][2], fmaf(k1.y, qs.x, y[i][n][2]));
+              y[i][n][3] = fmaf(k1.x, c[n][3], fmaf(k1.y, qs.y, y[i][n][3]));
+            }
+          }
+        }
+        uint32_t vc[2][2][G];                                        // value scale and bias: tile, row half, group
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) load_coefs<G>(st + i * TILE + 16 * D + 64 * G + (lg + 8 * h) * G * 4, vc[i][h]);
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const int tok = u * kUnit + 16 * i + tk + h;
+              const bool there = ((note >> i) & 1) == 0 && tok >= sg.vlo && tok < sg.vhi;
+#pragma unroll
+              for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                  const int2 l = *reinterpret_cast<const int2 *>(lim + 2 * (8 * n + 2 * lt + c));
+                  if (!there || tok < l.x || tok >= l.y) y[i][n][2 * h + c] = NINF;
+                }
+              if (!there)
+#pragma unroll
+                for (int g = 0; g < G; g++) vc[i][h][g] = 0u;
+            }
+        }
+
+        // ---------------------------------------------------------- running maximum, probabilities
+        uint32_t smax = 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int g = 0; g < G; g++) smax = max(smax, vc[i][h][g] & 0x7FFFu);
+        smax = __reduce_max_sync(0xffffffffu, smax);
+        const int ve2 = max(ve, max(1, (int)(smax >> 10)));
+        const float vf = pow2i(29 - ve2);                            // largest scale -> [2^14, 2^15)
+        const float vr = ve == 0 ? 1.0f : pow2i(ve - ve2);           // what is summed so far, in the new units
+        ve = ve2;
+        float alpha[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            float mx = fmaxf(fmaxf(y[0][n][c], y[0][n][2 + c]), fmaxf(y[1][n][c], y[1][n][2 + c]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(mr[n][c], mx * f[n][c]);
+            const float mu = mn == NINF ? 0.0f : mn;
+            alpha[n][c] = ex2(mr[n][c] - mu);
+            mr[n][c] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; i++)
+#pragma unroll
+              for (int h = 0; h < 2; h++) {
+                const float e = ex2(fmaf(y[i][n][2 * h + c], f[n][c], -mu));
+                y[i][n][2 * h + c] = e;
+                sum += e;
+              }
+            lr[n][c] = fmaf(lr[n][c], alpha[n][c], sum);
+          }
+        // ---------------------------------------------------------- p * sv as B operands, bias sums
+        uint32_t pf[2][G][NT][HL ? 4 : 2];
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+#pragma unroll
+          for (int n = 0; n < NT; n++) ob[n][0][g] *= alpha[n][0], ob[n][1][g] *= alpha[n][1];
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const float2 sv = unpack_f16(vc[i][h][g]);
+              const float bias = HL ? fmaf(8.0f, sv.x, sv.y) : sv.y, ss = sv.x * vf;
+#pragma unroll
+              for (int n = 0; n < NT; n++) {
+                const float p0 = y[i][n][2 * h], p1 = y[i][n][2 * h + 1];
+                float e0 = p0 * ss, e1 = p1 * ss, g0 = p0 * bias, g1 = p1 * bias;
+                if (!full) {                                         // a masked token's coefficients may be NaN
+                  if (p0 == 0.0f) e0 = g0 = 0.0f;
+                  if (p1 == 0.0f) e1 = g1 = 0.0f;
+                }
+                ob[n][0][g] += g0;
+                ob[n][1][g] += g1;
+                const uint32_t hi = pack_f16(e0, e1);
+                pf[i][g][n][h] = movmatrix(hi);
+                if constexpr (HL) {
+                  const float2 r = unpack_f16(hi);
+                  pf[i][g][n][2 + h] = movmatrix(pack_f16(e0 - r.x, e1 - r.y));
+                }
+              }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++) alpha[n][0] *= vr, alpha[n][1] *= vr;
+        // ---------------------------------------------------------- values
+#pragma unroll
+        for (int c = 0; c < VW / 4; c++) {
+          uint32_t vw[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(st + i * TILE + 8 * D + (c * 32 + lane) * 16);
+            vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
+          }
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            const int w = 4 * c + x, g = w / (VW / G);
+            float d[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; n++) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+              const uint32_t x0 = vw[i][x], x1 = x0 >> 8;
+              uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
+              if constexpr (HL) {                                    // code - 8, exact: 8 and 128 times 2^-24
+                a0 = sub_f16(a0, 0x00080008u), a1 = sub_f16(a1, 0x00800080u);
+                a2 = sub_f16(a2, 0x00080008u), a3 = sub_f16(a3, 0x00800080u);
+              }
+#pragma unroll
+              for (int n = 0; n < NT; n++) {
+                mma(d[n], a0, a1, a2, a3, pf[i][g][n][0], pf[i][g][n][1]);
+                if constexpr (HL) mma(d[n], a0, a1, a2, a3, pf[i][g][n][2], pf[i][g][n][3]);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+              o[n][w][0] = fmaf(o[n][w][0], alpha[n][0], d[n][0]);
+              o[n][w][1] = fmaf(o[n][w][1], alpha[n][1], d[n][1]);
+              o[n][w][2] = fmaf(o[n][w][2], alpha[n][0], d[n][2]);
+              o[n][w][3] = fmaf(o[n][w][3], alpha[n][1], d[n][3]);
+            }
+          }
+        }
+        __syncwarp();                                                // every lane has read the unit
+        issue();
+      }
+
+      // ------------------------------------------------------------ join the warps
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) {
+            lr[n][c] += __shfl_xor_sync(0xffffffffu, lr[n][c], off);
+#pragma unroll
+            for (int g = 0; g < G; g++) ob[n][c][g] += __shfl_xor_sync(0xffffffffu, ob[n][c][g], off);
+          }
+          if (lg == 0) wm[warp * ROWS + 8 * n + 2 * lt + c] = mr[n][c], wl[warp * ROWS + 8 * n + 2 * lt + c] = lr[n][c];
+        }
+      if (!__syncthreads_and(ok)) { ok = false; break; }             // a wait of some warp ran out: all leave
+      // every warp's share in units of the common maximum
+      const float unit = pow2i(ve == 0 ? 0 : ve - 5);                // 2^24 / 2^(29 - ve)
+      float sc[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+          const int row = 8 * n + 2 * lt + c;
+          float M = NINF;
+#pragma unroll
+          for (int w = 0; w < W; w++) M = fmaxf(M, wm[w * ROWS + row]);
+          const float mu = M == NINF ? 0.0f : M;
+          sc[n][c] = ex2(mr[n][c] - mu);
+          if (warp == 0 && lg == 0) {
+            float L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; w++) L = fmaf(wl[w * ROWS + row], ex2(wm[w * ROWS + row] - mu), L);
+            cm[row] = M, cl[row] = L;
+          }
+        }
+      auto each = [&](auto fn) {                                     // fn(row, element, value) over this lane's outputs
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int w = 0; w < VW; w++) {
+            const int g = w / (VW / G);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+              const int c = r & 1;
+              const float v = fmaf(o[n][w][r], r < 2 ? unit : unit * 0.0625f, ob[n][c][g]) * sc[n][c];
+              fn(8 * n + 2 * lt + c, 16 * w + lg + (r < 2 ? 0 : 8), v);
+            }
+          }
+      };
+      if (warp >= W / 2) {
+        float *j = join + (warp - W / 2) * ROWS * OS;
+        each([&](int row, int d, float v) { j[row * OS + d] = v; });
+      }
+      __syncthreads();
+      if (warp < W / 2) {
+        float *j = join + warp * ROWS * OS;
+        each([&](int row, int d, float v) { j[row * OS + d] += v; });
+      }
+      __syncthreads();
+      // ------------------------------------------------------------ the item's rows, whole or as a partial result
+      auto put_row = [&](int row, int d, float4 v) {
+        const int r = sg.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
+        const int64_t off = ((int64_t)(sg.cu0 + qi) * a.heads + sg.kvh * p.ratio + hq) * D + d;
+        if constexpr (HL) {
+          *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + off) = v;
+        } else {
+          const __nv_bfloat162 h0 = __floats2bfloat162_rn(v.x, v.y), h1 = __floats2bfloat162_rn(v.z, v.w);
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + off) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+        }
+      };
+      constexpr int PART = ROWS * (D + 2);                           // floats of a partial result: maxima, sums, rows
+      float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + 4 * kKvMaxCtas);
+      const bool whole = sg.nseg == 1;
+      float *mine_p = parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == sg.c0 ? 1 : 0)) * PART;
+      for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < W / 2; w++) {
+          const float4 x = *reinterpret_cast<const float4 *>(join + (w * ROWS + row) * OS + d);
+          v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+        }
+        if (whole) {
+          const float L = cl[row], inv = L == 0.0f ? 0.0f : 1.0f / L;
+          v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+          put_row(row, d, v);
+        } else {
+          __stcg(reinterpret_cast<float4 *>(mine_p + 2 * ROWS + row * D + d), v);
+        }
+      }
+      if (!whole) {
+        if (threadIdx.x < rows) __stcg(mine_p + threadIdx.x, cm[threadIdx.x]), __stcg(mine_p + ROWS + threadIdx.x, cl[threadIdx.x]);
+        __threadfence();
+        __syncthreads();
+        unsigned *count = static_cast<unsigned *>(a.workspace) + sg.c0;
+        if (threadIdx.x == 0) {
+          const unsigned old = atomicAdd(count, 1u);
+          ctrl[10] = old == (unsigned)sg.nseg - 1;
+        }
+        __syncthreads();
+        if (ctrl[10]) {                                              // every other part is in: add them in CTA order
+          __threadfence();
+          auto part = [&](int k) { return parts + (int64_t)(2 * (sg.c0 + k) + (k == 0 ? 1 : 0)) * PART; };
+          for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            float M = NINF;
+            for (int k = 0; k < sg.nseg; k++) M = fmaxf(M, __ldcg(part(k) + row));
+            const float mu = M == NINF ? 0.0f : M;
+            float L = 0.0f;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+            for (int k = 0; k < sg.nseg; k++) {
+              const float *s = part(k);
+              const float w = ex2(__ldcg(s + row) - mu);
+              const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + 2 * ROWS + row * D + d));
+              L = fmaf(w, __ldcg(s + ROWS + row), L);
+              v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+            }
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+            put_row(row, d, v);
+          }
+          if (threadIdx.x == 0) *count = 0u;
+        }
+      }
+    }
+  }
+  // a wait ran out: copies still in flight land before the shared memory goes
+  if (!ok && lane == 0)
+    for (; flight > 0; flight--) {
+      wait_drain(my_bar + 8 * tslot, tphase);
+      if (++tslot == S) tslot = 0, tphase ^= 1u;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <int D, int G, int NT, bool HL>
+cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
+  using C = Cfg<D, NT, HL>;
+  static_assert(C::stages(G) >= 2, "the ring needs two units a warp");
+  constexpr int alloc = C::W * C::stages(G) * 2 * (16 * D + 128 * G) + C::fixed(G);
+  Params p{};
+  p.a = a;
+  p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
+  p.ratio = (int)(a.heads / a.kv_heads);
+  p.min_units = C::W;
+  auto kern = attend_warp_kernel<D, G, NT, HL>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, alloc);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kv_max_ctas());
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = alloc;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+inline cudaError_t read_clear_status(int *status, cudaStream_t s) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+  }
+  *status = v;
+  return cudaSuccess;
+}
+
+}  // namespace kvw
+}  // namespace qmm
