@@ -4,8 +4,8 @@
 namespace qmm {
 
 size_t kv_attend_workspace(int64_t, int64_t, int64_t, int64_t head_dim, int64_t) {
-  // counters, then two partial results a CTA: 16 rows, each with its maximum and sum
-  return 4 * 1024 + (size_t)kv_max_ctas() * 2 * 16 * (size_t)(head_dim + 2) * sizeof(float);
+  // counters, then two partial results a CTA: 8 rows for each of 4 an SM, or 16 of 2, with their maxima and sums
+  return 4 * 1024 + (size_t)kv_max_ctas(2) * 2 * 16 * (size_t)(head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s) {

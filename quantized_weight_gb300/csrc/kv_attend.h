@@ -24,20 +24,20 @@ struct KvAttendArgs {
   int64_t window;                       // 0: none
 };
 
-// CTAs of a launch: one an SM, at most 1024 (their counters are the workspace's first 4096 bytes).
+// CTAs of a launch with `per_sm` CTAs an SM: at most 1024 (their counters are the workspace's first 4096 bytes).
 constexpr int kKvMaxCtas = 1024;
-inline int kv_max_ctas() {
+inline int kv_max_ctas(int per_sm) {
   static int n = 0;
   if (n == 0) {
     int dev = 0, v = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         v <= 0) {
       (void)cudaGetLastError();          // no device here: the size that a GB300 needs
-      return 152;
+      v = 152;
     }
-    n = v > kKvMaxCtas ? kKvMaxCtas : v;
+    n = v;
   }
-  return n;
+  return n * per_sm > kKvMaxCtas ? kKvMaxCtas : n * per_sm;
 }
 
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);

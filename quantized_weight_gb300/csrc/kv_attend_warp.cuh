@@ -40,6 +40,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "bounded_wait.cuh"
 #include "kv_attend.h"
@@ -56,7 +57,10 @@ static __device__ int g_status = 0;    // QMM_OK or QMM_ERR_DEVICE_TIMEOUT (-6),
 
 constexpr int kUnit = 32;              // tokens a warp takes at a time: two tiles
 constexpr int kMaxSegs = 32;           // items a CTA lists at a time
-constexpr int kSmemMax = 227 * 1024;
+constexpr int kMinUnits = 32;
+constexpr int kNear = 8;               // units: see the cuts
+constexpr int kHead = 8;               // an item's start counts as this many units more in the split
+constexpr int kSmemSm = 228 * 1024;    // shared memory of an SM; each CTA also takes 1 KB of it
 
 struct Params {
   KvAttendArgs a;
@@ -80,25 +84,27 @@ struct Seg {
 template <int D, int NT, bool HL>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int W = (D == 256 || NT == 2) ? 8 : 12;       // warps (registers: 64 K / threads)
+  // Small CTAs, several an SM: while one joins its warps or waits for its next item's q, the others run.
+  static constexpr int W = 4;
+  static constexpr int PER_SM = D == 256 || NT == 2 ? 2 : 4;     // registers: 64 K / threads
   static constexpr int THREADS = 32 * W;
   static constexpr int KS = D / 16;                              // MMA k-steps of a score
   static constexpr int QW = HL ? 4 : 2;                          // 32-bit words of q per lane and k-step
-  static constexpr bool QREG = KS * NT * QW <= 32;               // q fragments stay in registers
+  static constexpr bool QREG = KS * NT * QW <= 16;               // q fragments stay in registers
   static constexpr int OS = D + 4;                               // row stride of the join area (floats)
   static constexpr int ESZ = HL ? 4 : 2;
-  // shared memory: ring | q fragments | raw q | join area | small arrays
+  // shared memory: ring | q fragments, then the warps' results (never at the same time) | raw q | small arrays
   static constexpr int QF = KS * NT * 32 * QW * 4;
   static constexpr int RAW = ROWS * D * ESZ;
-  static constexpr int JOIN = W / 2 * ROWS * OS * 4;
+  static constexpr int JOIN = W / 2 * ROWS * OS * 4 > QF ? W / 2 * ROWS * OS * 4 : QF;
   __host__ __device__ static constexpr int fixed(int G) {
-    return QF + RAW + JOIN + ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ +
+    return RAW + JOIN + ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ +
            2 * W * ROWS * 4 /* m, l per warp */ + 2 * ROWS * 4 /* M, L */ + kMaxSegs * (int)sizeof(Seg) +
-           W * 4 * 12 /* barriers, notes: up to 4 stages */ + 256 + W * 8;
+           W * 4 * 12 /* barriers, notes: up to 4 stages */ + 256 + W * 16;
   }
   // units in flight a warp: what shared memory holds, up to four
   __host__ __device__ static constexpr int stages(int G) {
-    const int n = (kSmemMax - fixed(G)) / (W * 2 * (16 * D + 128 * G));
+    const int n = (kSmemSm / PER_SM - 1024 - fixed(G)) / (W * 2 * (16 * D + 128 * G));
     return n > 4 ? 4 : n;
   }
 };
@@ -108,6 +114,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
@@ -154,7 +166,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 // A request as the split sees it.
 struct Req {
   int n, len, hi, lo, base, cu0;      // queries; tokens; readable end; first unit; ...
-  int units, tiles;                   // units an item spans; row tiles
+  int units, tiles;                   // units of an item on the line, kHead of them for its start; row tiles
 };
 
 __device__ __forceinline__ Req request(const Params &p, int b, int rows_tile) {
@@ -175,7 +187,7 @@ __device__ __forceinline__ Req request(const Params &p, int b, int rows_tile) {
   r.lo = first > 0 ? (int)min(first, (int64_t)r.hi) / kUnit : 0;
   r.tiles = (int)(((int64_t)r.n * p.ratio + rows_tile - 1) / rows_tile);
   // an item without tokens still has its zeros written
-  r.units = r.n == 0 ? 0 : max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
+  r.units = r.n == 0 ? 0 : kHead + max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
   return r;
 }
 
@@ -196,7 +208,7 @@ __device__ __forceinline__ void load_coefs(const uint8_t *p, uint32_t (&c)[G]) {
 }
 
 template <int D, int G, int NT, bool HL>
-__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_SM)) attend_warp_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D, NT, HL>;
   constexpr int W = C::W, ROWS = C::ROWS, KS = C::KS, QW = C::QW, OS = C::OS;
   constexpr int TILE = 16 * D + 128 * G, STAGE = 2 * TILE;
@@ -208,11 +220,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
   uint8_t *at = smem + W * S * STAGE;
   uint32_t *qf = reinterpret_cast<uint32_t *>(at);
-  at += C::QF;
-  uint8_t *raw = at;
-  at += C::RAW;
   float *join = reinterpret_cast<float *>(at);
   at += C::JOIN;
+  uint8_t *raw = at;
+  at += C::RAW;
   float *qsum = reinterpret_cast<float *>(at);   // [G][ROWS]
   at += ROWS * G * 4;
   float *fq = reinterpret_cast<float *>(at);     // [ROWS]
@@ -230,8 +241,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
   at += W * 4 * 8;
   int *notes = reinterpret_cast<int *>(at);                         // [W][4]: tiles of the unit that were not copied
   at += W * 4 * 4;
-  int64_t *sh64 = reinterpret_cast<int64_t *>(at);                  // [W]
-  at += W * 8;
+  int64_t *sh64 = reinterpret_cast<int64_t *>(at);                  // [2][W]
+  at += W * 16;
   volatile int *ctrl = reinterpret_cast<volatile int *>(at);        // abort, b, off, segments, next b, next off, last
   const WaitCtl ctl{ctrl, &g_status};
 
@@ -251,10 +262,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
   const int B = (int)a.B, hkv = p.g.kv_heads;
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  int64_t mine = 0;
+  int64_t mine = 0, parts_b = 0;
   for (int b = b0; b < b1; b++) {
     const Req r = request(p, b, ROWS);
     mine += (int64_t)r.units * r.tiles * hkv;
+    parts_b += (int64_t)((max(r.units - kHead, 0) + p.min_units - 1) / p.min_units) * r.tiles * hkv;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -262,34 +274,52 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
     const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  if (lane == 31) sh64[warp] = inc;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) parts_b += __shfl_xor_sync(0xffffffffu, parts_b, o);
+  if (lane == 31) sh64[warp] = inc, sh64[W + warp] = parts_b;
   __syncthreads();
-  int64_t total = 0, before = inc - mine;
+  int64_t total = 0, before = inc - mine, want = 0;                  // want: CTAs, each item having one per min_units begun
 #pragma unroll
   for (int w = 0; w < W; w++) {
     if (w < warp) before += sh64[w];
     total += sh64[w];
+    want += sh64[W + w];
   }
-  const int64_t want = (total + p.min_units - 1) / p.min_units;
   const int A = (int)(want < gridDim.x ? want : gridDim.x);
   if ((int)blockIdx.x >= A) return;                                  // also when there is nothing to do
-  const int64_t u0 = total * blockIdx.x / A, u1 = total * (blockIdx.x + 1) / A;
-  if (before <= u0 && u0 < before + mine) {
-    int b = b0;
-    int64_t off = u0 - before;
-    for (;; b++) {
-      const Req r = request(p, b, ROWS);
-      const int64_t n = (int64_t)r.units * r.tiles * hkv;
-      if (off < n) break;
-      off -= n;
+  // Cut c is at total * c / A, moved to the border of its item where that is
+  // near: an item begun for a few units costs this CTA more (q, join, partial result) than the units do.
+  const int near = (int)min((int64_t)kNear, total / A * 3 / 4);
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    const int64_t cut = total * (blockIdx.x + k) / A;
+    if (cut == total && threadIdx.x == 0) {
+      ctrl[12 + k] = B;
+      *reinterpret_cast<volatile int64_t *>(ctrl + 2 + 2 * k) = 0;
+      *reinterpret_cast<volatile int64_t *>(ctrl + 6 + 2 * k) = total;
     }
-    ctrl[1] = b;
-    *reinterpret_cast<volatile int64_t *>(ctrl + 2) = off;
+    if (before <= cut && cut < before + mine) {
+      int b = b0;
+      int64_t off = cut - before;
+      Req r;
+      for (;; b++) {
+        r = request(p, b, ROWS);
+        const int64_t n = (int64_t)r.units * r.tiles * hkv;
+        if (off < n) break;
+        off -= n;
+      }
+      const int in = (int)(off % r.units);
+      const int move = in < near ? -in : r.units - in < near ? r.units - in : 0;
+      ctrl[12 + k] = b;
+      *reinterpret_cast<volatile int64_t *>(ctrl + 2 + 2 * k) = off + move;
+      *reinterpret_cast<volatile int64_t *>(ctrl + 6 + 2 * k) = cut + move;
+    }
   }
   __syncthreads();
-  int cb = ctrl[1];
-  int64_t coff = *reinterpret_cast<volatile int64_t *>(ctrl + 2);
-  int64_t cu_ = u0;                                                  // the line's unit that (cb, coff) stands for
+  int cb = ctrl[12];
+  int64_t coff = *reinterpret_cast<volatile int64_t *>(ctrl + 2);    // from request cb's first unit on
+  int64_t cu_ = *reinterpret_cast<volatile int64_t *>(ctrl + 6);     // the line's unit that (cb, coff) stands for
+  const int64_t u1 = *reinterpret_cast<volatile int64_t *>(ctrl + 8);
 
   int islot = 0, tslot = 0, flight = 0;                              // this warp's ring: next slot to fill, to take, copies out
   uint32_t tphase = 0;
@@ -337,16 +367,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         s.vhi = clip((int64_t)r.base + l + 1);
         s.flo = clip((int64_t)r.base + l + 1 - w);
         s.fhi = clip((int64_t)r.base + f + 1);
-        s.a = max(r.lo + (int)(x0 - i_s), s.vlo / kUnit);
-        s.e = min(r.lo + (int)(x1 - i_s), (s.vhi + kUnit - 1) / kUnit);
+        s.a = max(r.lo + max(0, (int)(x0 - i_s) - kHead), s.vlo / kUnit);
+        s.e = min(r.lo + max(0, (int)(x1 - i_s) - kHead), (s.vhi + kUnit - 1) / kUnit);
         if (s.vhi <= s.vlo) s.e = s.a;
         s.base = r.base;
         s.hi = r.hi;
         s.cu0 = r.cu0;
-        // the line's units of the item -> the CTAs they fall to: CTA c takes from floor(total c / A) on
-        const int64_t g0 = cu_ - coff + i_s, g1 = cu_ - coff + i_e - 1;
-        s.c0 = (int)(((g0 + 1) * A - 1) / total);
-        s.nseg = (int)(((g1 + 1) * A - 1) / total) - s.c0 + 1;
+        // The CTAs of the item: cut c, at floor(total c / A) before it is moved, is at or before the item's
+        // first unit g0 if it falls before g0 + near (or the item's end), and before the item's end
+        // if it is not moved there.
+        const int64_t g0 = cu_ - coff + i_s;
+        const int head = min(near, r.units), body = near > 0 ? max(r.units - near + 1, head) : r.units;
+        s.c0 = (int)(((g0 + max(head, 1)) * A - 1) / total);
+        s.nseg = (int)(((g0 + body) * A - 1) / total) - s.c0 + 1;
         segs[place + i] = s;
       }
       // where the list ends: after kMaxSegs items or these 32 requests
@@ -382,62 +415,58 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
     if (nsegs == 0) continue;
 
     // -------------------------------------------------------------- producer: this warp's units, in order
-    int ps = 0, pu = 0;                                              // segment, unit
-    int pg0 = -1, pg1 = -1;                                          // its page ids, fetched one unit ahead
-    const int32_t *ptab = nullptr;
-    int pvhi = 0, pe = 0, pkvh = 0;
+    // Each lane holds where one of the warp's next 32 units lies (of the next
+    // 16, one of the two tiles, where a page holds a single one).
+    const bool two = p.g.page == kKvTile;
+    const int batch = two ? 16 : 32;
+    int ps = -1, pu = 0, pe = 0, pk = 0;                             // segment, next unit, end, place in the batch
+    const uint8_t *paddr = nullptr;                                  // null: no such page
     auto fetch_pages = [&]() {
-      const int tok = pu * kUnit;
-      pg0 = tok < pvhi ? ptab[tok >> p.g.lg_page] : -1;
-      pg1 = p.g.page == kKvTile ? (tok + kKvTile < pvhi ? ptab[(tok + kKvTile) >> p.g.lg_page] : -1) : pg0;
+      const Seg &s = segs[ps];
+      const int64_t tok = two ? (int64_t)(pu + (lane >> 1) * W) * kUnit + (lane & 1) * kKvTile : (int64_t)(pu + lane * W) * kUnit;
+      const int pg = tok < s.vhi && tok < (int64_t)pe * kUnit ? a.table[s.b * a.max_blocks + (tok >> p.g.lg_page)] : -1;
+      paddr = nullptr;
+      if (pg >= 0 && pg < p.g.pages)
+        paddr = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + s.kvh) * p.g.head_bytes +
+                (((int)tok & (p.g.page - 1)) >> 4) * TILE;
+      pk = 0;
     };
-    auto open_seg = [&]() {                                          // first unit of the next segment that has one for this warp
-      for (; ps < nsegs; ps++) {
-        const Seg &s = segs[ps];
-        pu = s.a + warp;
-        pe = s.e;
-        if (pu < pe) {
-          pvhi = s.vhi;
-          pkvh = s.kvh;
-          ptab = a.table + (int64_t)s.b * a.max_blocks;
-          fetch_pages();
-          return;
-        }
+    auto open_seg = [&]() {                                          // the next segment that has a unit for this warp
+      while (++ps < nsegs) {
+        pu = segs[ps].a + warp;
+        pe = segs[ps].e;
+        if (pu < pe) return fetch_pages();
       }
     };
     auto issue = [&]() {
       if (ps >= nsegs) return;
-      const int slot = islot;
+      const unsigned long long pa = reinterpret_cast<unsigned long long>(paddr);
+      const unsigned long long s0 = __shfl_sync(0xffffffffu, pa, two ? 2 * pk : pk);
+      const unsigned long long s1 = two ? __shfl_sync(0xffffffffu, pa, 2 * pk + 1) : s0;
       if (lane == 0) {
-        const bool v0 = pg0 >= 0 && pg0 < p.g.pages, v1 = pg1 >= 0 && pg1 < p.g.pages;
-        my_note[slot] = (v0 ? 0 : 1) | (v1 ? 0 : 2);
-        const uint32_t bar = my_bar + 8 * slot, dst = my_ring + slot * STAGE;
-        const uint8_t *cache = static_cast<const uint8_t *>(a.cache);
-        const int off = (pu * kUnit) & (p.g.page - 1);
-        const uint8_t *s0 = cache + ((int64_t)pg0 * hkv + pkvh) * p.g.head_bytes + (off >> 4) * TILE;
-        if (p.g.page != kKvTile) {
-          if (v0) {
+        const uint32_t bar = my_bar + 8 * islot, dst = my_ring + islot * STAGE;
+        my_note[islot] = (s0 ? 0 : 1) | (s1 ? 0 : 2);
+        if (!two) {
+          if (s0) {
             mbar_arrive_expect_tx(bar, STAGE);
-            bulk_copy(dst, s0, STAGE, bar);
+            bulk_copy(dst, reinterpret_cast<const void *>(s0), STAGE, bar);
           } else {
             mbar_arrive(bar);
           }
         } else {
-          const uint32_t bytes = (v0 ? TILE : 0) + (v1 ? TILE : 0);
+          const uint32_t bytes = (s0 ? TILE : 0) + (s1 ? TILE : 0);
           if (bytes) mbar_arrive_expect_tx(bar, bytes);
           else mbar_arrive(bar);
-          if (v0) bulk_copy(dst, s0, TILE, bar);
-          if (v1) bulk_copy(dst + TILE, cache + ((int64_t)pg1 * hkv + pkvh) * p.g.head_bytes, TILE, bar);
+          if (s0) bulk_copy(dst, reinterpret_cast<const void *>(s0), TILE, bar);
+          if (s1) bulk_copy(dst + TILE, reinterpret_cast<const void *>(s1), TILE, bar);
         }
       }
       islot = islot + 1 == S ? 0 : islot + 1;
       flight++;
       pu += W;
-      if (pu < pe) fetch_pages();
-      else ps++, open_seg();
+      if (pu >= pe) open_seg();
+      else if (++pk == batch) fetch_pages();
     };
-    open_seg();
-    for (int s = 0; s < S; s++) issue();
 
     // raw q of a segment, fetched while the one before it runs
     auto fetch_q = [&](const Seg &s) {
@@ -453,6 +482,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch_q(segs[0]);
+    open_seg();
+    for (int s = 0; s < S; s++) issue();
 
     for (int si = 0; si < nsegs; si++) {
       const Seg &sg = segs[si];
@@ -539,18 +570,20 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
 
       const float NINF = __int_as_float(0xFF800000);
       float o[NT][VW][4], ob[NT][2][G], mr[NT][2], lr[NT][2];
+      float mu[NT][2];                                               // the running maximum, 0 where nothing was seen
 #pragma unroll
       for (int n = 0; n < NT; n++) {
 #pragma unroll
         for (int w = 0; w < VW; w++) o[n][w][0] = o[n][w][1] = o[n][w][2] = o[n][w][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < 2; c++) {
-          mr[n][c] = NINF, lr[n][c] = 0.0f;
+          mr[n][c] = NINF, mu[n][c] = 0.0f, lr[n][c] = 0.0f;
 #pragma unroll
           for (int g = 0; g < G; g++) ob[n][c][g] = 0.0f;
         }
       }
-      int ve = 0;                                                    // largest exponent field among the value scales so far
+      int ve = 1;                                                    // largest exponent field among the value scales so far
+      float vf = pow2i(28);                                          // 2^(29 - ve)
       const int tk = 4 * (lg >> 1) + 2 * (lg & 1);                   // token of row lg in its tile; row lg + 8 is the next one
 
       for (int u = sg.a + warp; u < sg.e; u += W) {
@@ -564,60 +597,69 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
 
         // ---------------------------------------------------------- scores of 32 tokens
         float y[2][NT][4];
+        {
+          uint32_t kw[2][2][WPL], kc[2][2][G];                       // tile, row half
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-          const uint8_t *tile = st + i * TILE;
-          uint32_t kw[2][WPL], kc[2][G];
+          for (int i = 0; i < 2; i++)
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const int row = lg + 8 * h;
-            if constexpr (WPL == 2) {
-              const uint2 v = *reinterpret_cast<const uint2 *>(tile + (row * 4 + lt) * 8);
-              kw[h][0] = v.x, kw[h][1] = v.y;
-            } else {
+            for (int h = 0; h < 2; h++) {
+              const uint8_t *tile = st + i * TILE;
+              const int row = lg + 8 * h;
+              if constexpr (WPL == 2) {
+                const uint2 v = *reinterpret_cast<const uint2 *>(tile + (row * 4 + lt) * 8);
+                kw[i][h][0] = v.x, kw[i][h][1] = v.y;
+              } else {
 #pragma unroll
-              for (int c = 0; c < WPL / 4; c++) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(tile + ((c * 16 + row) * 4 + lt) * 16);
-                kw[h][4 * c] = v.x, kw[h][4 * c + 1] = v.y, kw[h][4 * c + 2] = v.z, kw[h][4 * c + 3] = v.w;
+                for (int c = 0; c < WPL / 4; c++) {
+                  const uint4 v = *reinterpret_cast<const uint4 *>(tile + ((c * 16 + row) * 4 + lt) * 16);
+                  kw[i][h][4 * c] = v.x, kw[i][h][4 * c + 1] = v.y, kw[i][h][4 * c + 2] = v.z, kw[i][h][4 * c + 3] = v.w;
+                }
               }
+              load_coefs<G>(tile + 16 * D + row * G * 4, kc[i][h]);
             }
-            load_coefs<G>(tile + 16 * D + row * G * 4, kc[h]);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; n++) y[i][n][0] = y[i][n][1] = y[i][n][2] = y[i][n][3] = 0.0f;
 #pragma unroll
           for (int g = 0; g < G; g++) {
-            float c[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; n++) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
+            float c[2][NT][4];
 #pragma unroll
             for (int w = g * WPG; w < (g + 1) * WPG; w++) {
 #pragma unroll
               for (int s2 = 0; s2 < 2; s2++) {
-                const uint32_t x0 = kw[0][w] >> (8 * s2), x1 = kw[1][w] >> (8 * s2);
-                const uint32_t a0 = x0 & 0x000F000Fu, a1 = x1 & 0x000F000Fu, a2 = x0 & 0x00F000F0u, a3 = x1 & 0x00F000F0u;
+                uint32_t qv[NT][QW];
 #pragma unroll
                 for (int n = 0; n < NT; n++) {
-                  uint32_t qv[QW];
                   if constexpr (C::QREG) {
 #pragma unroll
-                    for (int j = 0; j < QW; j++) qv[j] = qr[2 * w + s2][n][j];
+                    for (int j = 0; j < QW; j++) qv[n][j] = qr[2 * w + s2][n][j];
                   } else {
-                    load_q(2 * w + s2, n, qv);
+                    load_q(2 * w + s2, n, qv[n]);
                   }
-                  mma(c[n], a0, a1, a2, a3, qv[0], qv[1]);
-                  if constexpr (HL) mma(c[n], a0, a1, a2, a3, qv[2], qv[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                  const uint32_t x0 = kw[i][0][w] >> (8 * s2), x1 = kw[i][1][w] >> (8 * s2);
+                  const uint32_t a0 = x0 & 0x000F000Fu, a1 = x1 & 0x000F000Fu, a2 = x0 & 0x00F000F0u, a3 = x1 & 0x00F000F0u;
+#pragma unroll
+                  for (int n = 0; n < NT; n++) {
+                    if (w == g * WPG && s2 == 0) mma_z(c[i][n], a0, a1, a2, a3, qv[n][0], qv[n][1]);
+                    else mma(c[i][n], a0, a1, a2, a3, qv[n][0], qv[n][1]);
+                    if constexpr (HL) mma(c[i][n], a0, a1, a2, a3, qv[n][2], qv[n][3]);
+                  }
                 }
               }
             }
-            const float2 k0 = unpack_f16(kc[0][g]), k1 = unpack_f16(kc[1][g]);   // scale, bias
 #pragma unroll
             for (int n = 0; n < NT; n++) {
               const float2 qs = *reinterpret_cast<const float2 *>(qsum + g * ROWS + 8 * n + 2 * lt);
-              y[i][n][0] = fmaf(k0.x, c[n][0], fmaf(k0.y, qs.x, y[i][n][0]));
-              y[i][n][1] = fmaf(k0.x, c[n][1], fmaf(k0.y, qs.y, y[i][n][1]));
-              y[i][n][2] = fmaf(k1.x, c[n][2], fmaf(k1.y, qs.x, y[i][n][2]));
-              y[i][n][3] = fmaf(k1.x, c[n][3], fmaf(k1.y, qs.y, y[i][n][3]));
+#pragma unroll
+              for (int i = 0; i < 2; i++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                  const float2 k = unpack_f16(kc[i][h][g]);          // scale, bias
+                  const float t0 = g == 0 ? k.y * qs.x : fmaf(k.y, qs.x, y[i][n][2 * h]);
+                  const float t1 = g == 0 ? k.y * qs.y : fmaf(k.y, qs.y, y[i][n][2 * h + 1]);
+                  y[i][n][2 * h] = fmaf(k.x, c[i][n][2 * h], t0);
+                  y[i][n][2 * h + 1] = fmaf(k.x, c[i][n][2 * h + 1], t1);
+                }
             }
           }
         }
@@ -646,75 +688,96 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
             }
         }
 
-        // ---------------------------------------------------------- running maximum, probabilities
-        uint32_t smax = 0;
+        // ---------------------------------------------------------- running maximum and largest value scale
+        // Both move in the first units of an item and seldom after: one vote
+        // asks whether any lane met a larger one, and only then is what is summed so far rescaled.
+        uint32_t smax = vc[0][0][0];
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
           for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int g = 0; g < G; g++) smax = max(smax, vc[i][h][g] & 0x7FFFu);
-        smax = __reduce_max_sync(0xffffffffu, smax);
-        const int ve2 = max(ve, max(1, (int)(smax >> 10)));
-        const float vf = pow2i(29 - ve2);                            // largest scale -> [2^14, 2^15)
-        const float vr = ve == 0 ? 1.0f : pow2i(ve - ve2);           // what is summed so far, in the new units
-        ve = ve2;
-        float alpha[NT][2];
+            for (int g = 0; g < G; g++) smax = __vmaxu2(smax, vc[i][h][g]);
+        smax &= 0x7FFFu;
+        bool grow = (int)(smax >> 10) > ve;
+        float mx[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
           for (int c = 0; c < 2; c++) {
-            float mx = fmaxf(fmaxf(y[0][n][c], y[0][n][2 + c]), fmaxf(y[1][n][c], y[1][n][2 + c]));
+            mx[n][c] = fmaxf(fmaxf(y[0][n][c], y[0][n][2 + c]), fmaxf(y[1][n][c], y[1][n][2 + c])) * f[n][c];
+            grow |= mx[n][c] > mr[n][c];
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+          const int ve2 = max(ve, (int)(__reduce_max_sync(0xffffffffu, smax) >> 10));
+          const float vr = pow2i(ve - ve2);                          // what is summed so far, in the new units
+          ve = ve2;
+          vf = pow2i(29 - ve2);                                      // largest scale -> [2^14, 2^15)
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const float mn = fmaxf(mr[n][c], mx * f[n][c]);
-            const float mu = mn == NINF ? 0.0f : mn;
-            alpha[n][c] = ex2(mr[n][c] - mu);
-            mr[n][c] = mn;
-            float sum = 0.0f;
+          for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) mx[n][c] = fmaxf(mx[n][c], __shfl_xor_sync(0xffffffffu, mx[n][c], off));
+              const float mn = fmaxf(mr[n][c], mx[n][c]);
+              const float alpha = mn == mr[n][c] ? 1.0f : ex2(mr[n][c] - mn);
+              mr[n][c] = mn;
+              mu[n][c] = mn == NINF ? 0.0f : mn;
+              lr[n][c] *= alpha;
+#pragma unroll
+              for (int g = 0; g < G; g++) ob[n][c][g] *= alpha;
+#pragma unroll
+              for (int w = 0; w < VW; w++) o[n][w][c] *= alpha * vr, o[n][w][2 + c] *= alpha * vr;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int c = 0; c < 2; c++)
 #pragma unroll
             for (int i = 0; i < 2; i++)
 #pragma unroll
               for (int h = 0; h < 2; h++) {
-                const float e = ex2(fmaf(y[i][n][2 * h + c], f[n][c], -mu));
+                const float e = ex2(fmaf(y[i][n][2 * h + c], f[n][c], -mu[n][c]));
                 y[i][n][2 * h + c] = e;
-                sum += e;
+                lr[n][c] += e;
               }
-            lr[n][c] = fmaf(lr[n][c], alpha[n][c], sum);
-          }
         // ---------------------------------------------------------- p * sv as B operands, bias sums
         uint32_t pf[2][G][NT][HL ? 4 : 2];
+        auto weigh = [&](auto guard) {
 #pragma unroll
-        for (int g = 0; g < G; g++) {
+          for (int g = 0; g < G; g++)
 #pragma unroll
-          for (int n = 0; n < NT; n++) ob[n][0][g] *= alpha[n][0], ob[n][1][g] *= alpha[n][1];
+            for (int i = 0; i < 2; i++)
 #pragma unroll
-          for (int i = 0; i < 2; i++)
+              for (int h = 0; h < 2; h++) {
+                const float2 sv = unpack_f16(vc[i][h][g]);
+                const float bias = HL ? fmaf(8.0f, sv.x, sv.y) : sv.y, ss = sv.x * vf;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-              const float2 sv = unpack_f16(vc[i][h][g]);
-              const float bias = HL ? fmaf(8.0f, sv.x, sv.y) : sv.y, ss = sv.x * vf;
-#pragma unroll
-              for (int n = 0; n < NT; n++) {
-                const float p0 = y[i][n][2 * h], p1 = y[i][n][2 * h + 1];
-                float e0 = p0 * ss, e1 = p1 * ss, g0 = p0 * bias, g1 = p1 * bias;
-                if (!full) {                                         // a masked token's coefficients may be NaN
-                  if (p0 == 0.0f) e0 = g0 = 0.0f;
-                  if (p1 == 0.0f) e1 = g1 = 0.0f;
-                }
-                ob[n][0][g] += g0;
-                ob[n][1][g] += g1;
-                const uint32_t hi = pack_f16(e0, e1);
-                pf[i][g][n][h] = movmatrix(hi);
-                if constexpr (HL) {
-                  const float2 r = unpack_f16(hi);
-                  pf[i][g][n][2 + h] = movmatrix(pack_f16(e0 - r.x, e1 - r.y));
+                for (int n = 0; n < NT; n++) {
+                  const float p0 = y[i][n][2 * h], p1 = y[i][n][2 * h + 1];
+                  float e0 = p0 * ss, e1 = p1 * ss;
+                  if constexpr (decltype(guard)::value) {
+                    if (p0 == 0.0f) e0 = 0.0f;
+                    else ob[n][0][g] = fmaf(p0, bias, ob[n][0][g]);
+                    if (p1 == 0.0f) e1 = 0.0f;
+                    else ob[n][1][g] = fmaf(p1, bias, ob[n][1][g]);
+                  } else {
+                    ob[n][0][g] = fmaf(p0, bias, ob[n][0][g]);
+                    ob[n][1][g] = fmaf(p1, bias, ob[n][1][g]);
+                  }
+                  const uint32_t hi = pack_f16(e0, e1);
+                  pf[i][g][n][h] = movmatrix(hi);
+                  if constexpr (HL) {
+                    const float2 r = unpack_f16(hi);
+                    pf[i][g][n][2 + h] = movmatrix(pack_f16(e0 - r.x, e1 - r.y));
+                  }
                 }
               }
-            }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; n++) alpha[n][0] *= vr, alpha[n][1] *= vr;
+        };
+        // a token that some rows do not see may hold infinite or NaN coefficients
+        if (full) weigh(std::false_type());
+        else weigh(std::true_type());
         // ---------------------------------------------------------- values
 #pragma unroll
         for (int c = 0; c < VW / 4; c++) {
@@ -729,8 +792,6 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
             const int w = 4 * c + x, g = w / (VW / G);
             float d[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; n++) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
-#pragma unroll
             for (int i = 0; i < 2; i++) {
               const uint32_t x0 = vw[i][x], x1 = x0 >> 8;
               uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
@@ -740,16 +801,15 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
               }
 #pragma unroll
               for (int n = 0; n < NT; n++) {
-                mma(d[n], a0, a1, a2, a3, pf[i][g][n][0], pf[i][g][n][1]);
+                if (i == 0) mma_z(d[n], a0, a1, a2, a3, pf[i][g][n][0], pf[i][g][n][1]);
+                else mma(d[n], a0, a1, a2, a3, pf[i][g][n][0], pf[i][g][n][1]);
                 if constexpr (HL) mma(d[n], a0, a1, a2, a3, pf[i][g][n][2], pf[i][g][n][3]);
               }
             }
 #pragma unroll
             for (int n = 0; n < NT; n++) {
-              o[n][w][0] = fmaf(o[n][w][0], alpha[n][0], d[n][0]);
-              o[n][w][1] = fmaf(o[n][w][1], alpha[n][1], d[n][1]);
-              o[n][w][2] = fmaf(o[n][w][2], alpha[n][0], d[n][2]);
-              o[n][w][3] = fmaf(o[n][w][3], alpha[n][1], d[n][3]);
+#pragma unroll
+              for (int r = 0; r < 4; r++) o[n][w][r] += d[n][r];
             }
           }
         }
@@ -772,7 +832,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         }
       if (!__syncthreads_and(ok)) { ok = false; break; }             // a wait of some warp ran out: all leave
       // every warp's share in units of the common maximum
-      const float unit = pow2i(ve == 0 ? 0 : ve - 5);                // 2^24 / 2^(29 - ve)
+      const float unit = pow2i(ve - 5);                              // 2^24 / 2^(29 - ve)
       float sc[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; n++)
@@ -782,12 +842,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
           float M = NINF;
 #pragma unroll
           for (int w = 0; w < W; w++) M = fmaxf(M, wm[w * ROWS + row]);
-          const float mu = M == NINF ? 0.0f : M;
-          sc[n][c] = ex2(mr[n][c] - mu);
+          const float m0 = M == NINF ? 0.0f : M;
+          sc[n][c] = ex2(mr[n][c] - m0);
           if (warp == 0 && lg == 0) {
             float L = 0.0f;
 #pragma unroll
-            for (int w = 0; w < W; w++) L = fmaf(wl[w * ROWS + row], ex2(wm[w * ROWS + row] - mu), L);
+            for (int w = 0; w < W; w++) L = fmaf(wl[w * ROWS + row], ex2(wm[w * ROWS + row] - m0), L);
             cm[row] = M, cl[row] = L;
           }
         }
@@ -860,23 +920,40 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         if (ctrl[10]) {                                              // every other part is in: add them in CTA order
           __threadfence();
           auto part = [&](int k) { return parts + (int64_t)(2 * (sg.c0 + k) + (k == 0 ? 1 : 0)) * PART; };
+          // weights of the parts a row: 2^(m_k - M) / L, kept where the warps' results were
+          float *wt = join;                                          // [nseg][ROWS], as many parts at a time as fit
+          constexpr int FIT = C::JOIN / 4 / ROWS;
+          for (int row = warp; row < rows; row += W) {
+            float M = NINF, L = 0.0f;                                // online over the lane's parts, then over lanes
+            for (int k = lane; k < sg.nseg; k += 32) {
+              const float m = __ldcg(part(k) + row), l = __ldcg(part(k) + ROWS + row);
+              const float mn = fmaxf(M, m), m0 = mn == NINF ? 0.0f : mn;
+              L = L * ex2(M - m0) + l * ex2(m - m0);
+              M = mn;
+              if (k < FIT) wt[k * ROWS + row] = m;
+            }
+            float mx = M;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float m0 = mx == NINF ? 0.0f : mx;
+            L *= ex2(M - m0);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+            for (int k = lane; k < min(sg.nseg, FIT); k += 32) wt[k * ROWS + row] = ex2(wt[k * ROWS + row] - m0) * inv;
+            if (lane == 0) cm[row] = m0, cl[row] = inv;
+          }
+          __syncthreads();
           for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
-            float M = NINF;
-            for (int k = 0; k < sg.nseg; k++) M = fmaxf(M, __ldcg(part(k) + row));
-            const float mu = M == NINF ? 0.0f : M;
-            float L = 0.0f;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
             for (int k = 0; k < sg.nseg; k++) {
               const float *s = part(k);
-              const float w = ex2(__ldcg(s + row) - mu);
               const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + 2 * ROWS + row * D + d));
-              L = fmaf(w, __ldcg(s + ROWS + row), L);
+              const float w = k < FIT ? wt[k * ROWS + row] : ex2(__ldcg(s + row) - cm[row]) * cl[row];
               v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
             }
-            const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-            v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
             put_row(row, d, v);
           }
           if (threadIdx.x == 0) *count = 0u;
@@ -903,12 +980,12 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
   p.ratio = (int)(a.heads / a.kv_heads);
-  p.min_units = C::W;
+  p.min_units = kMinUnits;
   auto kern = attend_warp_kernel<D, G, NT, HL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, alloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kv_max_ctas());
+  cfg.gridDim = dim3(kv_max_ctas(C::PER_SM));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = alloc;
   cfg.stream = s;
