@@ -4,7 +4,7 @@
 namespace qmm {
 
 size_t kv_attend_workspace(int64_t, int64_t, int64_t, int64_t head_dim, int64_t) {
-  // counters, then two partial results a CTA: 8 rows for each of 4 an SM, or 16 of 2, with their maxima and sums
+  // counters, then two partial results a team: 8 rows for each of 3 teams an SM, or 16 of 2, with maxima and sums
   return 4 * 1024 + (size_t)kv_max_ctas(2) * 2 * 16 * (size_t)(head_dim + 2) * sizeof(float);
 }
 
@@ -14,15 +14,6 @@ cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s) {
   if (a.head_dim == 128) return launch_kv_warp_d128(a, nt, s);
   if (a.head_dim == 256) return launch_kv_warp_d256(a, s);
   return cudaErrorNotSupported;
-}
-
-cudaError_t read_clear_kv_status(int *status, cudaStream_t s) {
-  int v[3] = {0, 0, 0};
-  cudaError_t e = read_clear_kv_d64_status(&v[0], s);
-  if (e == cudaSuccess) e = read_clear_kv_d128_status(&v[1], s);
-  if (e == cudaSuccess) e = read_clear_kv_d256_status(&v[2], s);
-  *status = v[0] | v[1] | v[2];
-  return e;
 }
 
 }  // namespace qmm

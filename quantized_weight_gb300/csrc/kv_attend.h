@@ -42,15 +42,11 @@ inline int kv_max_ctas(int per_sm) {
 
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
-cudaError_t read_clear_kv_status(int *status, cudaStream_t s);
 
 // Per head dimension (one translation unit each); nt: tiles of 8 rows of q an item
 // (heads of 256: one, since registers and shared memory hold no more).
 cudaError_t launch_kv_warp_d64(const KvAttendArgs &a, int nt, cudaStream_t s);
 cudaError_t launch_kv_warp_d128(const KvAttendArgs &a, int nt, cudaStream_t s);
 cudaError_t launch_kv_warp_d256(const KvAttendArgs &a, cudaStream_t s);
-cudaError_t read_clear_kv_d64_status(int *status, cudaStream_t s);
-cudaError_t read_clear_kv_d128_status(int *status, cudaStream_t s);
-cudaError_t read_clear_kv_d256_status(int *status, cudaStream_t s);
 
 }  // namespace qmm

@@ -17,6 +17,4 @@ cudaError_t launch_kv_warp_d128(const KvAttendArgs &a, int nt, cudaStream_t s) {
   return cudaErrorNotSupported;
 }
 
-cudaError_t read_clear_kv_d128_status(int *status, cudaStream_t s) { return kvw::read_clear_status(status, s); }
-
 }  // namespace qmm

@@ -11,6 +11,4 @@ cudaError_t launch_kv_warp_d256(const KvAttendArgs &a, cudaStream_t s) {
   return cudaErrorNotSupported;
 }
 
-cudaError_t read_clear_kv_d256_status(int *status, cudaStream_t s) { return kvw::read_clear_status(status, s); }
-
 }  // namespace qmm

@@ -14,6 +14,4 @@ cudaError_t launch_kv_warp_d64(const KvAttendArgs &a, int nt, cudaStream_t s) {
   return cudaErrorNotSupported;
 }
 
-cudaError_t read_clear_kv_d64_status(int *status, cudaStream_t s) { return kvw::read_clear_status(status, s); }
-
 }  // namespace qmm

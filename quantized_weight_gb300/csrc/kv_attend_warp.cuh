@@ -42,7 +42,6 @@
 #include <cuda_fp16.h>
 #include <type_traits>
 
-#include "bounded_wait.cuh"
 #include "kv_attend.h"
 #include "kv_layout.cuh"
 #include "qmm_device.cuh"
@@ -53,23 +52,19 @@ namespace kvw {
 
 using namespace sm100;
 
-static __device__ int g_status = 0;    // QMM_OK or QMM_ERR_DEVICE_TIMEOUT (-6), one a translation unit
-
 constexpr int kUnit = 32;              // tokens a warp takes at a time: two tiles
-constexpr int kMaxSegs = 32;           // items a CTA lists at a time
-constexpr int kMinUnits = 32;
-constexpr int kNear = 8;               // units: see the cuts
-constexpr int kHead = 8;               // an item's start counts as this many units more in the split
-constexpr int kSmemSm = 228 * 1024;    // shared memory of an SM; each CTA also takes 1 KB of it
+constexpr int kMaxSegs = 32;           // items a team lists at a time
+constexpr int kSmemMax = 227 * 1024;
 
 struct Params {
   KvAttendArgs a;
   KvGeom g;
   int ratio;             // query heads per kv head
-  int min_units;         // units worth a CTA of its own
+  int team;              // warps that share an item: 4 or all
+  int min_units;         // units worth a team of its own
 };
 
-// One item (or the part of it) that this CTA works on.
+// One item (or the part of it) that a team works on.
 struct Seg {
   int b, kvh, r0, rows;           // rows r0 .. r0 + rows - 1 of the request's R
   int a, e;                       // units [a, e) of 32 tokens, clipped to what the rows see
@@ -78,33 +73,41 @@ struct Seg {
   int base;                       // position of the request's first query
   int hi;                         // tokens that can be read
   int cu0;
-  int c0, nseg;                   // first CTA and number of CTAs that share the item
+  int c0, nseg;                   // first team and number of teams that share the item
+};
+
+// A team's place on the line of units (shared memory).
+struct Line {
+  int64_t at, off, end;           // next unit to list; the same from request b's first unit on; end of the team's run
+  int b, segs, last;              // request; items listed; this team adds the parts up
 };
 
 template <int D, int NT, bool HL>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  // Small CTAs, several an SM: while one joins its warps or waits for its next item's q, the others run.
-  static constexpr int W = 4;
-  static constexpr int PER_SM = D == 256 || NT == 2 ? 2 : 4;     // registers: 64 K / threads
+  static constexpr int W = D == 256 || NT == 2 ? 8 : 12;         // warps (registers: 64 K / threads)
+  static constexpr int TW = 4;                                   // warps of a small team
+  static constexpr int TEAMS = W / TW;
   static constexpr int THREADS = 32 * W;
   static constexpr int KS = D / 16;                              // MMA k-steps of a score
   static constexpr int QW = HL ? 4 : 2;                          // 32-bit words of q per lane and k-step
   static constexpr bool QREG = KS * NT * QW <= 16;               // q fragments stay in registers
   static constexpr int OS = D + 4;                               // row stride of the join area (floats)
   static constexpr int ESZ = HL ? 4 : 2;
-  // shared memory: ring | q fragments, then the warps' results (never at the same time) | raw q | small arrays
+  // Shared memory: the warps' rings, then an area a small team (a team of all
+  // warps has them all): q fragments or, later, half the warps' results | small arrays.
   static constexpr int QF = KS * NT * 32 * QW * 4;
-  static constexpr int RAW = ROWS * D * ESZ;
-  static constexpr int JOIN = W / 2 * ROWS * OS * 4 > QF ? W / 2 * ROWS * OS * 4 : QF;
+  static constexpr int JOIN = TW / 2 * ROWS * OS * 4 > QF ? TW / 2 * ROWS * OS * 4 : QF;
+  __host__ __device__ static constexpr int small(int G) {
+    return (ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ + 2 * ROWS * 4 /* M, L */ + 15) / 16 * 16 +
+           kMaxSegs * (int)sizeof(Seg);
+  }
   __host__ __device__ static constexpr int fixed(int G) {
-    return RAW + JOIN + ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ +
-           2 * W * ROWS * 4 /* m, l per warp */ + 2 * ROWS * 4 /* M, L */ + kMaxSegs * (int)sizeof(Seg) +
-           W * 4 * 12 /* barriers, notes: up to 4 stages */ + 256 + W * 16;
+    return TEAMS * (JOIN + small(G)) + 2 * W * ROWS * 4 /* m, l per warp */ + W * 16 /* scan */ + TEAMS * (int)sizeof(Line);
   }
   // units in flight a warp: what shared memory holds, up to four
   __host__ __device__ static constexpr int stages(int G) {
-    const int n = (kSmemSm / PER_SM - 1024 - fixed(G)) / (W * 2 * (16 * D + 128 * G));
+    const int n = (kSmemMax - fixed(G)) / (W * 2 * (16 * D + 128 * G));
     return n > 4 ? 4 : n;
   }
 };
@@ -157,19 +160,25 @@ __device__ __forceinline__ int row_exp(uint32_t mbits) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+// 16 bytes, or zeros for `bytes` 0 (nothing is read then)
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// The warps of a team; `all` is a constant of the launch.
+__device__ __forceinline__ void team_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
 }
 
 // A request as the split sees it.
 struct Req {
   int n, len, hi, lo, base, cu0;      // queries; tokens; readable end; first unit; ...
-  int units, tiles;                   // units of an item on the line, kHead of them for its start; row tiles
+  int units, tiles;                   // units of an item on the line, `head` of them for its start; row tiles
 };
 
-__device__ __forceinline__ Req request(const Params &p, int b, int rows_tile) {
+__device__ __forceinline__ Req request(const Params &p, int b, int rows_tile, int head) {
   Req r;
   const KvAttendArgs &a = p.a;
   r.len = max(0, a.lens[b]);
@@ -187,7 +196,7 @@ __device__ __forceinline__ Req request(const Params &p, int b, int rows_tile) {
   r.lo = first > 0 ? (int)min(first, (int64_t)r.hi) / kUnit : 0;
   r.tiles = (int)(((int64_t)r.n * p.ratio + rows_tile - 1) / rows_tile);
   // an item without tokens still has its zeros written
-  r.units = r.n == 0 ? 0 : kHead + max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
+  r.units = r.n == 0 ? 0 : head + max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
   return r;
 }
 
@@ -208,7 +217,7 @@ __device__ __forceinline__ void load_coefs(const uint8_t *p, uint32_t (&c)[G]) {
 }
 
 template <int D, int G, int NT, bool HL>
-__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_SM)) attend_warp_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D, NT, HL>;
   constexpr int W = C::W, ROWS = C::ROWS, KS = C::KS, QW = C::QW, OS = C::OS;
   constexpr int TILE = 16 * D + 128 * G, STAGE = 2 * TILE;
@@ -218,55 +227,40 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
   constexpr int S = C::stages(G);
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
-  uint8_t *at = smem + W * S * STAGE;
+  const int tw = p.team, tid = threadIdx.x % (tw * 32), tthreads = tw * 32;    // this team's warps and threads
+  const int team = warp / tw, twarp = warp % tw;
+  const int areas = tw / C::TW;                  // areas of a small team that this team has
+  uint8_t *at = smem + W * S * STAGE + team * areas * (C::JOIN + C::small(G));
   uint32_t *qf = reinterpret_cast<uint32_t *>(at);
   float *join = reinterpret_cast<float *>(at);
-  at += C::JOIN;
-  uint8_t *raw = at;
-  at += C::RAW;
+  at += areas * C::JOIN;
   float *qsum = reinterpret_cast<float *>(at);   // [G][ROWS]
-  at += ROWS * G * 4;
-  float *fq = reinterpret_cast<float *>(at);     // [ROWS]
-  at += ROWS * 4;
-  int *lim = reinterpret_cast<int *>(at);        // [ROWS][2]: tokens [lo, hi) a row sees
-  at += ROWS * 8;
-  float *wm = reinterpret_cast<float *>(at), *wl = wm + W * ROWS;   // [W][ROWS]
-  at += 2 * W * ROWS * 4;
-  float *cm = reinterpret_cast<float *>(at), *cl = cm + ROWS;       // [ROWS]
-  at += 2 * ROWS * 4;
-  Seg *segs = reinterpret_cast<Seg *>(at);
-  at += kMaxSegs * sizeof(Seg);
-  at = smem + ((at - smem + 15) & ~15);
-  const uint32_t bars = smem_addr(at);                              // [W][4]
-  at += W * 4 * 8;
-  int *notes = reinterpret_cast<int *>(at);                         // [W][4]: tiles of the unit that were not copied
-  at += W * 4 * 4;
-  int64_t *sh64 = reinterpret_cast<int64_t *>(at);                  // [2][W]
-  at += W * 16;
-  volatile int *ctrl = reinterpret_cast<volatile int *>(at);        // abort, b, off, segments, next b, next off, last
-  const WaitCtl ctl{ctrl, &g_status};
+  float *fq = qsum + ROWS * G;                   // [ROWS]
+  int *lim = reinterpret_cast<int *>(fq + ROWS); // [ROWS][2]: tokens [lo, hi) a row sees
+  float *cm = reinterpret_cast<float *>(lim + 2 * ROWS), *cl = cm + ROWS;    // [ROWS]
+  Seg *segs = reinterpret_cast<Seg *>(smem + ((reinterpret_cast<uint8_t *>(cl + ROWS) - smem + 15) & ~15));
+  at = smem + W * S * STAGE + C::TEAMS * (C::JOIN + C::small(G));
+  float *wm = reinterpret_cast<float *>(at) + team * tw * ROWS, *wl = wm + W * ROWS;    // [warp][ROWS]
+  int64_t *sh64 = reinterpret_cast<int64_t *>(at + 2 * W * ROWS * 4);        // [2][W]
+  Line *lines = reinterpret_cast<Line *>(sh64 + 2 * W);                      // [teams]
 
-  const uint32_t my_bar = bars + warp * 32;
   const uint32_t my_ring = smem_addr(smem) + warp * S * STAGE;
   const uint8_t *ring_ptr = smem + warp * S * STAGE;
-  int *my_note = notes + warp * 4;
-  if (lane == 0)
-    for (int s = 0; s < S; s++) mbar_init(my_bar + 8 * s, 1);
-  if (threadIdx.x == 0) ctrl[0] = 0;
-  fence_mbar_init();
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---------------------------------------------------------------- this CTA's run of units
+  // ---------------------------------------------------------------- the team's run of units
+  // An item's start counts as `head` units: q, the join and the partial result
+  // take a team about as long.
   const KvAttendArgs &a = p.a;
-  const int B = (int)a.B, hkv = p.g.kv_heads;
+  const int B = (int)a.B, hkv = p.g.kv_heads, head = 2 * tw;
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
   int64_t mine = 0, parts_b = 0;
   for (int b = b0; b < b1; b++) {
-    const Req r = request(p, b, ROWS);
+    const Req r = request(p, b, ROWS, head);
     mine += (int64_t)r.units * r.tiles * hkv;
-    parts_b += (int64_t)((max(r.units - kHead, 0) + p.min_units - 1) / p.min_units) * r.tiles * hkv;
+    if (r.n > 0) parts_b += (int64_t)((r.units - head + p.min_units - 1) / p.min_units) * r.tiles * hkv;
   }
   int64_t inc = mine;
 #pragma unroll
@@ -278,69 +272,72 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
   for (int o = 16; o > 0; o >>= 1) parts_b += __shfl_xor_sync(0xffffffffu, parts_b, o);
   if (lane == 31) sh64[warp] = inc, sh64[W + warp] = parts_b;
   __syncthreads();
-  int64_t total = 0, before = inc - mine, want = 0;                  // want: CTAs, each item having one per min_units begun
+  int64_t total = 0, before = inc - mine, want = 0;                  // want: teams, an item having one per min_units begun
 #pragma unroll
   for (int w = 0; w < W; w++) {
     if (w < warp) before += sh64[w];
     total += sh64[w];
     want += sh64[W + w];
   }
-  const int A = (int)(want < gridDim.x ? want : gridDim.x);
-  if ((int)blockIdx.x >= A) return;                                  // also when there is nothing to do
-  // Cut c is at total * c / A, moved to the border of its item where that is
-  // near: an item begun for a few units costs this CTA more (q, join, partial result) than the units do.
-  const int near = (int)min((int64_t)kNear, total / A * 3 / 4);
-#pragma unroll
-  for (int k = 0; k < 2; k++) {
-    const int64_t cut = total * (blockIdx.x + k) / A;
-    if (cut == total && threadIdx.x == 0) {
-      ctrl[12 + k] = B;
-      *reinterpret_cast<volatile int64_t *>(ctrl + 2 + 2 * k) = 0;
-      *reinterpret_cast<volatile int64_t *>(ctrl + 6 + 2 * k) = total;
-    }
-    if (before <= cut && cut < before + mine) {
+  const int A = (int)min(want, (int64_t)gridDim.x * (W / tw));
+  if (A == 0) return;
+  // Team c begins at cut c, which leaves c / A of the line before it, moved to
+  // the border of its item where that is near, so that no item is begun for a few units.
+  const int64_t each = total / A, more = total - each * A;           // the first `more` teams have a unit more
+  const int near = (int)min((int64_t)head, each * 3 / 4);
+  auto cut_at = [&](int c) { return c * each + min((int64_t)c, more); };
+#pragma unroll 1
+  for (int k = 0; k < 2 * (W / tw); k++) {
+    const int c = (k >> 1) * gridDim.x + blockIdx.x + (k & 1);       // few teams: on SMs of their own
+    if (c > A) continue;
+    const int64_t x = cut_at(c);
+    Line &l = lines[k >> 1];
+    if (x == total) {
+      if (threadIdx.x == 0) {
+        if (k & 1) l.end = x;
+        else l.at = x;
+      }
+    } else if (before <= x && x < before + mine) {
       int b = b0;
-      int64_t off = cut - before;
+      int64_t off = x - before;
       Req r;
       for (;; b++) {
-        r = request(p, b, ROWS);
+        r = request(p, b, ROWS, head);
         const int64_t n = (int64_t)r.units * r.tiles * hkv;
         if (off < n) break;
         off -= n;
       }
       const int in = (int)(off % r.units);
       const int move = in < near ? -in : r.units - in < near ? r.units - in : 0;
-      ctrl[12 + k] = b;
-      *reinterpret_cast<volatile int64_t *>(ctrl + 2 + 2 * k) = off + move;
-      *reinterpret_cast<volatile int64_t *>(ctrl + 6 + 2 * k) = cut + move;
+      if (k & 1) l.end = x + move;
+      else l.at = x + move, l.off = off + move, l.b = b;
     }
   }
   __syncthreads();
-  int cb = ctrl[12];
-  int64_t coff = *reinterpret_cast<volatile int64_t *>(ctrl + 2);    // from request cb's first unit on
-  int64_t cu_ = *reinterpret_cast<volatile int64_t *>(ctrl + 6);     // the line's unit that (cb, coff) stands for
-  const int64_t u1 = *reinterpret_cast<volatile int64_t *>(ctrl + 8);
+  const int me = team * gridDim.x + blockIdx.x;
+  if (me >= A) return;
+  Line *line = lines + team;
 
-  int islot = 0, tslot = 0, flight = 0;                              // this warp's ring: next slot to fill, to take, copies out
-  uint32_t tphase = 0;
-  bool ok = true;
-  while (cu_ < u1 && ok) {
-    // -------------------------------------------------------------- list the next items (warp 0, a request a lane)
-    __syncthreads();
-    if (warp == 0) {
-      const int b = cb + lane;
+  int islot = 0, tslot = 0;                                          // this warp's ring: next slot to fill, to take
+  uint32_t notes = 0;                                                // two bits a slot: tiles without a page
+  for (;;) {
+    // -------------------------------------------------------------- list the next items (a warp, a request a lane)
+    team_sync(team, tthreads);
+    if (line->at >= line->end) break;
+    if (twarp == 0) {
+      const int cb = line->b, b = cb + lane;
+      const int64_t lo = line->off, hi = lo + (line->end - line->at);   // the team's run, from request cb's first unit on
+      const int64_t g = line->at - lo;                               // that unit on the line
       Req r{};
-      if (b < B) r = request(p, b, ROWS);
-      const int items = r.tiles * hkv;
-      const int64_t n = (int64_t)r.units * items;
+      if (b < B) r = request(p, b, ROWS, head);
+      const int64_t n = (int64_t)r.units * r.tiles * hkv;
       int64_t end = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(0xffffffffu, end, o);
         if (lane >= o) end += u;
       }
-      const int64_t first = end - n;                                 // the request's units, relative to request cb's start
-      const int64_t lo = coff, hi = coff + (u1 - cu_);               // this CTA's, relative too
+      const int64_t first = end - n;
       const int64_t s0 = first > lo ? first : lo, s1 = end < hi ? end : hi;
       const int i0 = s1 > s0 ? (int)((s0 - first) / r.units) : 0;
       const int cnt = s1 > s0 ? (int)((s1 - 1 - first) / r.units) - i0 + 1 : 0;
@@ -353,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
       place -= cnt;
       for (int i = 0; i < cnt && place + i < kMaxSegs; i++) {
         const int idx = i0 + i;
-        const int64_t i_s = first + (int64_t)idx * r.units, i_e = i_s + r.units;   // the item's units, relative
+        const int64_t i_s = first + (int64_t)idx * r.units, i_e = i_s + r.units;   // the item's units
         const int64_t x0 = i_s > lo ? i_s : lo, x1 = i_e < hi ? i_e : hi;
         Seg s;
         s.b = b;
@@ -367,27 +364,29 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
         s.vhi = clip((int64_t)r.base + l + 1);
         s.flo = clip((int64_t)r.base + l + 1 - w);
         s.fhi = clip((int64_t)r.base + f + 1);
-        s.a = max(r.lo + max(0, (int)(x0 - i_s) - kHead), s.vlo / kUnit);
-        s.e = min(r.lo + max(0, (int)(x1 - i_s) - kHead), (s.vhi + kUnit - 1) / kUnit);
+        s.a = max(r.lo + max(0, (int)(x0 - i_s) - head), s.vlo / kUnit);
+        s.e = min(r.lo + max(0, (int)(x1 - i_s) - head), (s.vhi + kUnit - 1) / kUnit);
         if (s.vhi <= s.vlo) s.e = s.a;
         s.base = r.base;
         s.hi = r.hi;
         s.cu0 = r.cu0;
-        // The CTAs of the item: cut c, at floor(total c / A) before it is moved, is at or before the item's
-        // first unit g0 if it falls before g0 + near (or the item's end), and before the item's end
-        // if it is not moved there.
-        const int64_t g0 = cu_ - coff + i_s;
-        const int head = min(near, r.units), body = near > 0 ? max(r.units - near + 1, head) : r.units;
-        s.c0 = (int)(((g0 + max(head, 1)) * A - 1) / total);
-        s.nseg = (int)(((g0 + body) * A - 1) / total) - s.c0 + 1;
+        // The teams of the item: a cut is, once moved, at or before the item's first unit if it falls before
+        // unit `near` (or the item's end), and before the item's end if it is not moved there.  The last cut
+        // at or before a unit is that of the team which has the unit before moves.
+        auto owner = [&](int64_t x) {
+          const int64_t longer = more * (each + 1);
+          return (int)(x < longer ? x / (each + 1) : more + (x - longer) / each);
+        };
+        const int to_first = max(1, min(near, r.units)), to_last = near > 0 ? max(r.units - near + 1, to_first) : r.units;
+        s.c0 = owner(g + i_s + to_first - 1);
+        s.nseg = owner(g + i_s + to_last - 1) - s.c0 + 1;
         segs[place + i] = s;
       }
       // where the list ends: after kMaxSegs items or these 32 requests
       const int listed = __reduce_add_sync(0xffffffffu, max(0, min(cnt, kMaxSegs - place)));
       int64_t stop = 0;
       if (cnt > 0 && place < kMaxSegs) {
-        const int last = min(cnt, kMaxSegs - place);
-        const int64_t e = first + (int64_t)(i0 + last) * r.units;
+        const int64_t e = first + (int64_t)(i0 + min(cnt, kMaxSegs - place)) * r.units;
         stop = e < hi ? e : hi;
       }
 #pragma unroll
@@ -401,85 +400,80 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
       const int src = m ? __ffs(m) - 1 : 31;
       const int64_t src_first = __shfl_sync(0xffffffffu, first, src), src_end = __shfl_sync(0xffffffffu, end, src);
       if (lane == 0) {
-        ctrl[4] = listed;
-        ctrl[5] = m ? cb + src : cb + 32;
-        *reinterpret_cast<volatile int64_t *>(ctrl + 6) = m ? stop - src_first : stop - src_end;
-        *reinterpret_cast<volatile int64_t *>(ctrl + 8) = stop - coff;
+        line->segs = listed;
+        line->b = m ? cb + src : cb + 32;
+        line->off = m ? stop - src_first : stop - src_end;
+        line->at = g + stop;
       }
     }
-    __syncthreads();
-    const int nsegs = ctrl[4];
-    cb = ctrl[5];
-    coff = *reinterpret_cast<volatile int64_t *>(ctrl + 6);
-    cu_ += *reinterpret_cast<volatile int64_t *>(ctrl + 8);
+    team_sync(team, tthreads);
+    const int nsegs = line->segs;
     if (nsegs == 0) continue;
 
     // -------------------------------------------------------------- producer: this warp's units, in order
-    // Each lane holds where one of the warp's next 32 units lies (of the next
-    // 16, one of the two tiles, where a page holds a single one).
+    // Each lane holds the page of one of the warp's next 32 units (of the next
+    // 16, of one of the two tiles, where a page holds a single one).
     const bool two = p.g.page == kKvTile;
-    const int batch = two ? 16 : 32;
-    int ps = -1, pu = 0, pe = 0, pk = 0;                             // segment, next unit, end, place in the batch
-    const uint8_t *paddr = nullptr;                                  // null: no such page
+    int ps = -1, pu = 0, pe = 0, pk = 0, pid = -1;                   // segment, next unit, end, place among the lanes
     auto fetch_pages = [&]() {
       const Seg &s = segs[ps];
-      const int64_t tok = two ? (int64_t)(pu + (lane >> 1) * W) * kUnit + (lane & 1) * kKvTile : (int64_t)(pu + lane * W) * kUnit;
-      const int pg = tok < s.vhi && tok < (int64_t)pe * kUnit ? a.table[s.b * a.max_blocks + (tok >> p.g.lg_page)] : -1;
-      paddr = nullptr;
-      if (pg >= 0 && pg < p.g.pages)
-        paddr = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + s.kvh) * p.g.head_bytes +
-                (((int)tok & (p.g.page - 1)) >> 4) * TILE;
+      const int64_t tok = two ? (int64_t)(pu + (lane >> 1) * tw) * kUnit + (lane & 1) * kKvTile : (int64_t)(pu + lane * tw) * kUnit;
+      pid = tok < s.vhi && tok < (int64_t)pe * kUnit ? a.table[s.b * a.max_blocks + (tok >> p.g.lg_page)] : -1;
       pk = 0;
     };
     auto open_seg = [&]() {                                          // the next segment that has a unit for this warp
       while (++ps < nsegs) {
-        pu = segs[ps].a + warp;
+        pu = segs[ps].a + twarp;
         pe = segs[ps].e;
         if (pu < pe) return fetch_pages();
       }
     };
+    // One unit into the ring, as one group of copies (an empty one past the end,
+    // so that the count of groups stays that of units).  A tile without a page is zeros.
     auto issue = [&]() {
-      if (ps >= nsegs) return;
-      const unsigned long long pa = reinterpret_cast<unsigned long long>(paddr);
-      const unsigned long long s0 = __shfl_sync(0xffffffffu, pa, two ? 2 * pk : pk);
-      const unsigned long long s1 = two ? __shfl_sync(0xffffffffu, pa, 2 * pk + 1) : s0;
-      if (lane == 0) {
-        const uint32_t bar = my_bar + 8 * islot, dst = my_ring + islot * STAGE;
-        my_note[islot] = (s0 ? 0 : 1) | (s1 ? 0 : 2);
-        if (!two) {
-          if (s0) {
-            mbar_arrive_expect_tx(bar, STAGE);
-            bulk_copy(dst, reinterpret_cast<const void *>(s0), STAGE, bar);
-          } else {
-            mbar_arrive(bar);
-          }
-        } else {
-          const uint32_t bytes = (s0 ? TILE : 0) + (s1 ? TILE : 0);
-          if (bytes) mbar_arrive_expect_tx(bar, bytes);
-          else mbar_arrive(bar);
-          if (s0) bulk_copy(dst, reinterpret_cast<const void *>(s0), TILE, bar);
-          if (s1) bulk_copy(dst + TILE, reinterpret_cast<const void *>(s1), TILE, bar);
+      if (ps < nsegs) {
+        const int g0 = __shfl_sync(0xffffffffu, pid, two ? 2 * pk : pk);
+        const int g1 = two ? __shfl_sync(0xffffffffu, pid, 2 * pk + 1) : g0;
+        const bool v0 = g0 >= 0 && g0 < p.g.pages, v1 = g1 >= 0 && g1 < p.g.pages;
+        const uint8_t *cache = static_cast<const uint8_t *>(a.cache) + (int64_t)segs[ps].kvh * p.g.head_bytes;
+        const int64_t page_bytes = (int64_t)hkv * p.g.head_bytes;
+        const uint8_t *s0 = cache + (v0 ? g0 * page_bytes : 0) + ((pu * kUnit & (p.g.page - 1)) >> 4) * TILE;
+        const uint8_t *s1 = two ? cache + (v1 ? g1 * page_bytes : 0) : s0 + TILE;
+        const uint32_t z0 = v0 ? 16 : 0, z1 = v1 ? 16 : 0, dst = my_ring + islot * STAGE + lane * 16;
+#pragma unroll
+        for (int o = 0; o < STAGE; o += 512) {
+          const int off = o + lane * 16;
+          if (o + 512 <= TILE) cp_async16z(dst + o, s0 + off, z0);
+          else if (o >= TILE && o + 512 <= STAGE) cp_async16z(dst + o, s1 + (off - TILE), z1);
+          else if (off < STAGE) cp_async16z(dst + o, off < TILE ? s0 + off : s1 + (off - TILE), off < TILE ? z0 : z1);
         }
+        notes = (notes & ~(3u << (2 * islot))) | ((v0 ? 0u : 1u) | (v1 ? 0u : 2u)) << (2 * islot);
+        islot = islot + 1 == S ? 0 : islot + 1;
+        pu += tw;
+        if (pu >= pe) open_seg();
+        else if (++pk == (two ? 16 : 32)) fetch_pages();
       }
-      islot = islot + 1 == S ? 0 : islot + 1;
-      flight++;
-      pu += W;
-      if (pu >= pe) open_seg();
-      else if (++pk == batch) fetch_pages();
+      cp_async_commit();
     };
 
-    // raw q of a segment, fetched while the one before it runs
+    // A segment's q: eight elements of a row a thread, fetched while the warps of the segment before it join.
+    constexpr int PIECES = ROWS * (D / 8), QI = (PIECES + C::TW * 32 - 1) / (C::TW * 32), QV = HL ? 2 : 1;
+    uint4 qraw[QI][QV];
     auto fetch_q = [&](const Seg &s) {
-      constexpr int CH = D * C::ESZ / 16;                            // 16-byte pieces a row
-      for (int i = threadIdx.x; i < ROWS * CH; i += C::THREADS) {
-        const int row = i / CH, c = i % CH;
-        if (row < s.rows) {
+#pragma unroll
+      for (int it = 0; it < QI; it++) {
+        const int i = tid + it * tthreads, row = i / (D / 8), m = i % (D / 8);
+        if (i < PIECES && row < s.rows) {
           const int r = s.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
-          const int64_t off = (int64_t)(s.cu0 + qi) * a.q_token + (int64_t)(s.kvh * p.ratio + hq) * a.q_head;
-          cp_async16(smem_addr(raw) + i * 16, static_cast<const uint8_t *>(a.q) + off * C::ESZ + c * 16);
+          const int64_t off = (int64_t)(s.cu0 + qi) * a.q_token + (int64_t)(s.kvh * p.ratio + hq) * a.q_head + 8 * m;
+          const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + off * C::ESZ);
+#pragma unroll
+          for (int j = 0; j < QV; j++) qraw[it][j] = src[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < QV; j++) qraw[it][j] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
     fetch_q(segs[0]);
     open_seg();
@@ -488,26 +482,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
     for (int si = 0; si < nsegs; si++) {
       const Seg &sg = segs[si];
       const int rows = sg.rows;
+      if (si > 0) team_sync(team, tthreads);                         // the results of the segment before are read
       // ------------------------------------------------------------ q -> fragments, sums, limits
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncthreads();
-      for (int i = threadIdx.x; i < ROWS * (D / 8); i += C::THREADS) {   // whole warps: D / 8 threads a row
-        const int row = i / (D / 8), m = i % (D / 8);
+#pragma unroll
+      for (int it = 0; it < QI; it++) {
+        const int i = tid + it * tthreads, row = i / (D / 8), m = i % (D / 8);
+        if (i >= PIECES) break;                                      // whole warps: D / 8 lanes a row
         float v[8];
-        if (row < rows) {
-          if constexpr (HL) {
-            const float4 x = *reinterpret_cast<const float4 *>(raw + row * D * 4 + m * 32);
-            const float4 y = *reinterpret_cast<const float4 *>(raw + row * D * 4 + m * 32 + 16);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(raw + row * D * 2 + m * 16);
-            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        if constexpr (HL) {
+          const uint32_t u[8] = {qraw[it][0].x, qraw[it][0].y, qraw[it][0].z, qraw[it][0].w,
+                                 qraw[it][QV - 1].x, qraw[it][QV - 1].y, qraw[it][QV - 1].z, qraw[it][QV - 1].w};
 #pragma unroll
-            for (int j = 0; j < 4; j++) v[2 * j] = __uint_as_float(u[j] << 16), v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-          }
+          for (int j = 0; j < 8; j++) v[j] = __uint_as_float(u[j]);
         } else {
+          const uint32_t u[4] = {qraw[it][0].x, qraw[it][0].y, qraw[it][0].z, qraw[it][0].w};
 #pragma unroll
-          for (int j = 0; j < 8; j++) v[j] = 0.0f;
+          for (int j = 0; j < 4; j++) v[2 * j] = __uint_as_float(u[j] << 16), v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
         }
         uint32_t mx = 0;
 #pragma unroll
@@ -544,8 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
           }
         }
       }
-      __syncthreads();
-      if (si + 1 < nsegs) fetch_q(segs[si + 1]);
+      team_sync(team, tthreads);
 
       uint32_t qr[C::QREG ? KS : 1][NT][QW];
       auto load_q = [&](int ks, int n, uint32_t (&d)[QW]) {
@@ -586,13 +575,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
       float vf = pow2i(28);                                          // 2^(29 - ve)
       const int tk = 4 * (lg >> 1) + 2 * (lg & 1);                   // token of row lg in its tile; row lg + 8 is the next one
 
-      for (int u = sg.a + warp; u < sg.e; u += W) {
-        const int slot = tslot;
-        if (!__all_sync(0xffffffffu, wait_bounded(my_bar + 8 * slot, tphase, ctl))) { ok = false; break; }
-        if (++tslot == S) tslot = 0, tphase ^= 1u;
-        flight--;
-        const uint8_t *st = ring_ptr + slot * STAGE;
-        const int note = my_note[slot];
+      for (int u = sg.a + twarp; u < sg.e; u += tw) {
+        cp_async_wait<S - 1>();
+        __syncwarp();
+        const uint8_t *st = ring_ptr + tslot * STAGE;
+        const uint32_t note = (notes >> (2 * tslot)) & 3u;
+        tslot = tslot + 1 == S ? 0 : tslot + 1;
         const bool full = note == 0 && u * kUnit >= sg.flo && u * kUnit + kUnit <= sg.fhi;
 
         // ---------------------------------------------------------- scores of 32 tokens
@@ -817,6 +805,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
         issue();
       }
 
+      if (si + 1 < nsegs) fetch_q(segs[si + 1]);
       // ------------------------------------------------------------ join the warps
 #pragma unroll
       for (int n = 0; n < NT; n++)
@@ -828,9 +817,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
 #pragma unroll
             for (int g = 0; g < G; g++) ob[n][c][g] += __shfl_xor_sync(0xffffffffu, ob[n][c][g], off);
           }
-          if (lg == 0) wm[warp * ROWS + 8 * n + 2 * lt + c] = mr[n][c], wl[warp * ROWS + 8 * n + 2 * lt + c] = lr[n][c];
+          if (lg == 0) wm[twarp * ROWS + 8 * n + 2 * lt + c] = mr[n][c], wl[twarp * ROWS + 8 * n + 2 * lt + c] = lr[n][c];
         }
-      if (!__syncthreads_and(ok)) { ok = false; break; }             // a wait of some warp ran out: all leave
+      team_sync(team, tthreads);
       // every warp's share in units of the common maximum
       const float unit = pow2i(ve - 5);                              // 2^24 / 2^(29 - ve)
       float sc[NT][2];
@@ -840,18 +829,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
         for (int c = 0; c < 2; c++) {
           const int row = 8 * n + 2 * lt + c;
           float M = NINF;
-#pragma unroll
-          for (int w = 0; w < W; w++) M = fmaxf(M, wm[w * ROWS + row]);
+          for (int w = 0; w < tw; w++) M = fmaxf(M, wm[w * ROWS + row]);
           const float m0 = M == NINF ? 0.0f : M;
           sc[n][c] = ex2(mr[n][c] - m0);
-          if (warp == 0 && lg == 0) {
+          if (twarp == 0 && lg == 0) {
             float L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; w++) L = fmaf(wl[w * ROWS + row], ex2(wm[w * ROWS + row] - m0), L);
+            for (int w = 0; w < tw; w++) L = fmaf(wl[w * ROWS + row], ex2(wm[w * ROWS + row] - m0), L);
             cm[row] = M, cl[row] = L;
           }
         }
-      auto each = [&](auto fn) {                                     // fn(row, element, value) over this lane's outputs
+      auto each_out = [&](auto fn) {                                     // fn(row, element, value) over this lane's outputs
 #pragma unroll
         for (int n = 0; n < NT; n++)
 #pragma unroll
@@ -865,16 +852,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
             }
           }
       };
-      if (warp >= W / 2) {
-        float *j = join + (warp - W / 2) * ROWS * OS;
-        each([&](int row, int d, float v) { j[row * OS + d] = v; });
+      if (twarp >= tw / 2) {
+        float *j = join + (twarp - tw / 2) * ROWS * OS;
+        each_out([&](int row, int d, float v) { j[row * OS + d] = v; });
       }
-      __syncthreads();
-      if (warp < W / 2) {
-        float *j = join + warp * ROWS * OS;
-        each([&](int row, int d, float v) { j[row * OS + d] += v; });
+      team_sync(team, tthreads);
+      if (twarp < tw / 2) {
+        float *j = join + twarp * ROWS * OS;
+        each_out([&](int row, int d, float v) { j[row * OS + d] += v; });
       }
-      __syncthreads();
+      team_sync(team, tthreads);
       // ------------------------------------------------------------ the item's rows, whole or as a partial result
       auto put_row = [&](int row, int d, float4 v) {
         const int r = sg.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
@@ -890,12 +877,11 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
       constexpr int PART = ROWS * (D + 2);                           // floats of a partial result: maxima, sums, rows
       float *parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + 4 * kKvMaxCtas);
       const bool whole = sg.nseg == 1;
-      float *mine_p = parts + (int64_t)(2 * blockIdx.x + ((int)blockIdx.x == sg.c0 ? 1 : 0)) * PART;
-      for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
+      float *mine_p = parts + (int64_t)(2 * me + (me == sg.c0 ? 1 : 0)) * PART;
+      for (int i = tid; i < rows * (D / 4); i += tthreads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < W / 2; w++) {
+        for (int w = 0; w < tw / 2; w++) {
           const float4 x = *reinterpret_cast<const float4 *>(join + (w * ROWS + row) * OS + d);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
@@ -908,22 +894,22 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
         }
       }
       if (!whole) {
-        if (threadIdx.x < rows) __stcg(mine_p + threadIdx.x, cm[threadIdx.x]), __stcg(mine_p + ROWS + threadIdx.x, cl[threadIdx.x]);
+        if (tid < rows) __stcg(mine_p + tid, cm[tid]), __stcg(mine_p + ROWS + tid, cl[tid]);
         __threadfence();
-        __syncthreads();
+        team_sync(team, tthreads);
         unsigned *count = static_cast<unsigned *>(a.workspace) + sg.c0;
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
           const unsigned old = atomicAdd(count, 1u);
-          ctrl[10] = old == (unsigned)sg.nseg - 1;
+          line->last = old == (unsigned)sg.nseg - 1;
         }
-        __syncthreads();
-        if (ctrl[10]) {                                              // every other part is in: add them in CTA order
+        team_sync(team, tthreads);
+        if (line->last) {                                              // every other part is in: add them in CTA order
           __threadfence();
           auto part = [&](int k) { return parts + (int64_t)(2 * (sg.c0 + k) + (k == 0 ? 1 : 0)) * PART; };
           // weights of the parts a row: 2^(m_k - M) / L, kept where the warps' results were
           float *wt = join;                                          // [nseg][ROWS], as many parts at a time as fit
           constexpr int FIT = C::JOIN / 4 / ROWS;
-          for (int row = warp; row < rows; row += W) {
+          for (int row = twarp; row < rows; row += tw) {
             float M = NINF, L = 0.0f;                                // online over the lane's parts, then over lanes
             for (int k = lane; k < sg.nseg; k += 32) {
               const float m = __ldcg(part(k) + row), l = __ldcg(part(k) + ROWS + row);
@@ -943,30 +929,32 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, (Cfg<D, NT, HL>::PER_
             for (int k = lane; k < min(sg.nseg, FIT); k += 32) wt[k * ROWS + row] = ex2(wt[k * ROWS + row] - m0) * inv;
             if (lane == 0) cm[row] = m0, cl[row] = inv;
           }
-          __syncthreads();
-          for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
+          team_sync(team, tthreads);
+          for (int i = tid; i < rows * (D / 4); i += tthreads) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-            for (int k = 0; k < sg.nseg; k++) {
-              const float *s = part(k);
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + 2 * ROWS + row * D + d));
-              const float w = k < FIT ? wt[k * ROWS + row] : ex2(__ldcg(s + row) - cm[row]) * cl[row];
-              v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+            constexpr int AT = 8;                                    // loads in flight
+            for (int k0 = 0; k0 < sg.nseg; k0 += AT) {
+              float4 x[AT];
+#pragma unroll
+              for (int j = 0; j < AT; j++)
+                if (k0 + j < sg.nseg) x[j] = __ldcg(reinterpret_cast<const float4 *>(part(k0 + j) + 2 * ROWS + row * D + d));
+#pragma unroll
+              for (int j = 0; j < AT; j++)
+                if (k0 + j < sg.nseg) {
+                  const int k = k0 + j;
+                  const float w = k < FIT ? wt[k * ROWS + row] : ex2(__ldcg(part(k) + row) - cm[row]) * cl[row];
+                  v.x = fmaf(w, x[j].x, v.x), v.y = fmaf(w, x[j].y, v.y);
+                  v.z = fmaf(w, x[j].z, v.z), v.w = fmaf(w, x[j].w, v.w);
+                }
             }
             put_row(row, d, v);
           }
-          if (threadIdx.x == 0) *count = 0u;
+          if (tid == 0) *count = 0u;
         }
       }
     }
   }
-  // a wait ran out: copies still in flight land before the shared memory goes
-  if (!ok && lane == 0)
-    for (; flight > 0; flight--) {
-      wait_drain(my_bar + 8 * tslot, tphase);
-      if (++tslot == S) tslot = 0, tphase ^= 1u;
-    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -980,12 +968,16 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
   p.ratio = (int)(a.heads / a.kv_heads);
-  p.min_units = kMinUnits;
+  // Items that outnumber the SMs go to small teams, whose joins overlap; few
+  // items to whole CTAs, which leave fewer parts to add up.
+  const int64_t items = a.B * a.kv_heads * ((a.max_fresh * p.ratio + C::ROWS - 1) / C::ROWS);
+  p.team = items > kv_max_ctas(1) ? C::TW : C::W;
+  p.min_units = 2 * p.team;
   auto kern = attend_warp_kernel<D, G, NT, HL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, alloc);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kv_max_ctas(C::PER_SM));
+  cfg.gridDim = dim3(kv_max_ctas(1));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = alloc;
   cfg.stream = s;
@@ -995,23 +987,6 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-inline cudaError_t read_clear_status(int *status, cudaStream_t s) {
-  int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  if (v != 0) {
-    const int zero = 0;
-    e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e != cudaSuccess) return e;
-    e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) return e;
-  }
-  *status = v;
-  return cudaSuccess;
 }
 
 }  // namespace kvw
