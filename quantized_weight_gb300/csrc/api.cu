@@ -252,7 +252,7 @@ int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_he
   int st = check_kv(pages, kv_heads, head_dim, page, group);
   if (st != QMM_OK) return st;
   if (tokens < 0 || tokens >= kMaxDim / 4096 || B < 0 || B >= kMaxDim || max_blocks < 0 || max_blocks * page >= kMaxDim ||
-      max_fresh < 1 || max_fresh >= kMaxDim / 4096 || heads < 1 || heads > 4096 || heads % kv_heads != 0 || window < 0)
+      max_fresh < 1 || max_fresh >= kMaxDim / 4096 || heads < 1 || heads > 1024 || heads % kv_heads != 0 || window < 0)
     return QMM_ERR_SHAPE;
   if (!cu && (tokens != B || max_fresh != 1)) return QMM_ERR_SHAPE;
   if (!(scale > 0.0f) || scale > 3.0e38f) return QMM_ERR_ARG;

@@ -52,7 +52,6 @@ namespace kvw {
 
 using namespace sm100;
 
-constexpr int kUnit = 32;              // tokens a warp takes at a time: two tiles
 constexpr int kMaxSegs = 32;           // items a team lists at a time
 constexpr int kSmemMax = 227 * 1024;
 
@@ -62,12 +61,14 @@ struct Params {
   int ratio;             // query heads per kv head
   int team;              // warps that share an item: 4 or all
   int min_units;         // units worth a team of its own
+  int head;              // units that an item's start counts as
+  int shift;             // the line counts units in steps of 2^shift, so that it fits 32 bits
 };
 
 // One item (or the part of it) that a team works on.
 struct Seg {
   int b, kvh, r0, rows;           // rows r0 .. r0 + rows - 1 of the request's R
-  int a, e;                       // units [a, e) of 32 tokens, clipped to what the rows see
+  int a, e;                       // units [a, e), clipped to what the rows see
   int vlo, vhi;                   // tokens that any of the rows sees
   int flo, fhi;                   // tokens that all rows see
   int base;                       // position of the request's first query
@@ -78,38 +79,40 @@ struct Seg {
 
 // A team's place on the line of units (shared memory).
 struct Line {
-  int64_t at, off, end;           // next unit to list; the same from request b's first unit on; end of the team's run
+  int at, off, end;               // next step to list; the same from request b's first one on; end of the team's run
   int b, segs, last;              // request; items listed; this team adds the parts up
 };
 
-template <int D, int NT, bool HL>
+template <int D, int G, int NT, bool HL>
 struct Cfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int W = D == 256 || NT == 2 ? 8 : 12;         // warps (registers: 64 K / threads)
+  static constexpr int W = 8;                                    // warps
   static constexpr int TW = 4;                                   // warps of a small team
   static constexpr int TEAMS = W / TW;
   static constexpr int THREADS = 32 * W;
+  static constexpr int UT = NT == 1 && D <= 128 ? 4 : 2;         // tiles a warp takes at a time (registers)
+  static constexpr int UNIT = 16 * UT;                           // their tokens
+  static constexpr int TILE = 16 * D + 128 * G;                  // bytes
   static constexpr int KS = D / 16;                              // MMA k-steps of a score
   static constexpr int QW = HL ? 4 : 2;                          // 32-bit words of q per lane and k-step
-  static constexpr bool QREG = KS * NT * QW <= 16;               // q fragments stay in registers
+  static constexpr bool QREG = KS * NT * QW <= 32;               // q fragments stay in registers
   static constexpr int OS = D + 4;                               // row stride of the join area (floats)
-  static constexpr int ESZ = HL ? 4 : 2;
   // Shared memory: the warps' rings, then an area a small team (a team of all
-  // warps has them all): q fragments or, later, half the warps' results | small arrays.
+  // warps has them all): q fragments or, later, its warps' results | small arrays.
   static constexpr int QF = KS * NT * 32 * QW * 4;
-  static constexpr int JOIN = TW / 2 * ROWS * OS * 4 > QF ? TW / 2 * ROWS * OS * 4 : QF;
-  __host__ __device__ static constexpr int small(int G) {
-    return (ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ + 2 * ROWS * 4 /* M, L */ + 15) / 16 * 16 +
-           kMaxSegs * (int)sizeof(Seg);
-  }
-  __host__ __device__ static constexpr int fixed(int G) {
-    return TEAMS * (JOIN + small(G)) + 2 * W * ROWS * 4 /* m, l per warp */ + W * 16 /* scan */ + TEAMS * (int)sizeof(Line);
-  }
-  // units in flight a warp: what shared memory holds, up to four
-  __host__ __device__ static constexpr int stages(int G) {
-    const int n = (kSmemMax - fixed(G)) / (W * 2 * (16 * D + 128 * G));
-    return n > 4 ? 4 : n;
-  }
+  static constexpr int RES = ROWS * OS * 4;                      // a warp's results
+  static constexpr int small = (ROWS * G * 4 /* qsum */ + ROWS * 4 /* fq */ + ROWS * 8 /* limits */ +
+                                2 * ROWS * 4 /* M, L */ + 15) / 16 * 16 + kMaxSegs * (int)sizeof(Seg);
+  static constexpr int rest = TEAMS * small + 2 * W * ROWS * 4 /* m, l per warp */ + W * 8 /* scan */ +
+                              TEAMS * (int)sizeof(Line);
+  // all warps leave results at once where two units a warp still fit beside them, else half of them after the other half
+  static constexpr int RW = W * RES + rest + W * 2 * UT * TILE <= kSmemMax ? TW : TW / 2;
+  static constexpr int JOIN = RW * RES > QF ? RW * RES : QF;
+  static constexpr int fixed = TEAMS * JOIN + rest;
+  static constexpr int fit = (kSmemMax - fixed) / (W * UT * TILE);
+  static constexpr int S = fit > 4 ? 4 : fit;                    // units in flight a warp
+  static_assert(S >= 2, "the ring needs two units a warp");
+  static constexpr int SMEM = W * S * UT * TILE + fixed;
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -174,11 +177,13 @@ __device__ __forceinline__ void team_sync(int id, int threads) {
 
 // A request as the split sees it.
 struct Req {
-  int n, len, hi, lo, base, cu0;      // queries; tokens; readable end; first unit; ...
-  int units, tiles;                   // units of an item on the line, `head` of them for its start; row tiles
+  int n, len, hi, lo, base, cu0;      // queries; tokens; readable end; first unit; position and token of the first query
+  int steps, tiles;                   // steps of an item on the line, its start counted as `head` units; row tiles
+  int units;
 };
 
-__device__ __forceinline__ Req request(const Params &p, int b, int rows_tile, int head) {
+template <int ROWS, int UNIT>
+__device__ __forceinline__ Req request(const Params &p, int b, int head) {
   Req r;
   const KvAttendArgs &a = p.a;
   r.len = max(0, a.lens[b]);
@@ -193,12 +198,15 @@ __device__ __forceinline__ Req request(const Params &p, int b, int rows_tile, in
   r.base = r.len - r.n;                                     // may be negative: such queries see nothing
   r.hi = (int)min((int64_t)r.len, a.max_blocks << p.g.lg_page);
   const int64_t first = a.window > 0 ? (int64_t)r.base + 1 - a.window : 0;
-  r.lo = first > 0 ? (int)min(first, (int64_t)r.hi) / kUnit : 0;
-  r.tiles = (int)(((int64_t)r.n * p.ratio + rows_tile - 1) / rows_tile);
+  r.lo = first > 0 ? (int)min(first, (int64_t)r.hi) / UNIT : 0;
+  r.tiles = r.n * p.ratio <= ROWS ? (r.n > 0) : (r.n * p.ratio + ROWS - 1) / ROWS;
   // an item without tokens still has its zeros written
-  r.units = r.n == 0 ? 0 : head + max(1, (r.hi + kUnit - 1) / kUnit - r.lo);
+  r.units = r.n == 0 ? 0 : max(1, (r.hi + UNIT - 1) / UNIT - r.lo);
+  r.steps = r.n == 0 ? 0 : ((head + r.units - 1) >> p.shift) + 1;
   return r;
 }
+
+__device__ __forceinline__ int div_small(int a, int b) { return a < b ? 0 : a / b; }   // most often 0
 
 template <int G>
 __device__ __forceinline__ void load_coefs(const uint8_t *p, uint32_t (&c)[G]) {
@@ -217,32 +225,30 @@ __device__ __forceinline__ void load_coefs(const uint8_t *p, uint32_t (&c)[G]) {
 }
 
 template <int D, int G, int NT, bool HL>
-__global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel(const __grid_constant__ Params p) {
-  using C = Cfg<D, NT, HL>;
-  constexpr int W = C::W, ROWS = C::ROWS, KS = C::KS, QW = C::QW, OS = C::OS;
-  constexpr int TILE = 16 * D + 128 * G, STAGE = 2 * TILE;
+__global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, G, NT, HL>;
+  constexpr int W = C::W, ROWS = C::ROWS, KS = C::KS, QW = C::QW, OS = C::OS, UT = C::UT, UNIT = C::UNIT, S = C::S;
+  constexpr int TILE = C::TILE, STAGE = UT * TILE;
   constexpr int WPL = D / 32;                    // key words per lane and row
   constexpr int WPG = WPL / G;                   // of them in a group
   constexpr int VW = D / 16;                     // value words per lane
-  constexpr int S = C::stages(G);
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
-  const int tw = p.team, tid = threadIdx.x % (tw * 32), tthreads = tw * 32;    // this team's warps and threads
-  const int team = warp / tw, twarp = warp % tw;
-  const int areas = tw / C::TW;                  // areas of a small team that this team has
-  uint8_t *at = smem + W * S * STAGE + team * areas * (C::JOIN + C::small(G));
+  const int tw = p.team, tthreads = tw * 32;     // this team's warps and threads
+  const int team = tw == W ? 0 : warp / C::TW, twarp = tw == W ? warp : warp % C::TW, tid = twarp * 32 + lane;
+  uint8_t *at = smem + W * S * STAGE + team * C::JOIN;
   uint32_t *qf = reinterpret_cast<uint32_t *>(at);
   float *join = reinterpret_cast<float *>(at);
-  at += areas * C::JOIN;
+  at = smem + W * S * STAGE + C::TEAMS * C::JOIN + team * C::small;
   float *qsum = reinterpret_cast<float *>(at);   // [G][ROWS]
   float *fq = qsum + ROWS * G;                   // [ROWS]
   int *lim = reinterpret_cast<int *>(fq + ROWS); // [ROWS][2]: tokens [lo, hi) a row sees
   float *cm = reinterpret_cast<float *>(lim + 2 * ROWS), *cl = cm + ROWS;    // [ROWS]
-  Seg *segs = reinterpret_cast<Seg *>(smem + ((reinterpret_cast<uint8_t *>(cl + ROWS) - smem + 15) & ~15));
-  at = smem + W * S * STAGE + C::TEAMS * (C::JOIN + C::small(G));
+  Seg *segs = reinterpret_cast<Seg *>(at + (ROWS * G * 4 + ROWS * 20 + 15) / 16 * 16);
+  at = smem + W * S * STAGE + C::TEAMS * (C::JOIN + C::small);
   float *wm = reinterpret_cast<float *>(at) + team * tw * ROWS, *wl = wm + W * ROWS;    // [warp][ROWS]
-  int64_t *sh64 = reinterpret_cast<int64_t *>(at + 2 * W * ROWS * 4);        // [2][W]
-  Line *lines = reinterpret_cast<Line *>(sh64 + 2 * W);                      // [teams]
+  int *scan = reinterpret_cast<int *>(at + 2 * W * ROWS * 4);                // [2][W]
+  Line *lines = reinterpret_cast<Line *>(scan + 2 * W);                      // [teams]
 
   const uint32_t my_ring = smem_addr(smem) + warp * S * STAGE;
   const uint8_t *ring_ptr = smem + warp * S * STAGE;
@@ -253,44 +259,43 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
   // An item's start counts as `head` units: q, the join and the partial result
   // take a team about as long.
   const KvAttendArgs &a = p.a;
-  const int B = (int)a.B, hkv = p.g.kv_heads, head = 2 * tw;
+  const int B = (int)a.B, hkv = p.g.kv_heads, head = p.head;
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  int64_t mine = 0, parts_b = 0;
+  int mine = 0, parts_b = 0;
+  Req r{};                                                           // where a thread has one request: that one
   for (int b = b0; b < b1; b++) {
-    const Req r = request(p, b, ROWS, head);
-    mine += (int64_t)r.units * r.tiles * hkv;
-    if (r.n > 0) parts_b += (int64_t)((r.units - head + p.min_units - 1) / p.min_units) * r.tiles * hkv;
+    r = request<ROWS, UNIT>(p, b, head);
+    mine += r.steps * r.tiles * hkv;
+    parts_b += (r.units + p.min_units - 1) / p.min_units * r.tiles * hkv;
   }
-  int64_t inc = mine;
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) parts_b += __shfl_xor_sync(0xffffffffu, parts_b, o);
-  if (lane == 31) sh64[warp] = inc, sh64[W + warp] = parts_b;
+  parts_b = (int)__reduce_add_sync(0xffffffffu, (unsigned)parts_b);
+  if (lane == 31) scan[warp] = inc, scan[W + warp] = parts_b;
   __syncthreads();
-  int64_t total = 0, before = inc - mine, want = 0;                  // want: teams, an item having one per min_units begun
+  int total = 0, before = inc - mine, want = 0;                      // want: teams, an item having one per min_units begun
 #pragma unroll
   for (int w = 0; w < W; w++) {
-    if (w < warp) before += sh64[w];
-    total += sh64[w];
-    want += sh64[W + w];
+    if (w < warp) before += scan[w];
+    total += scan[w];
+    want += scan[W + w];
   }
-  const int A = (int)min(want, (int64_t)gridDim.x * (W / tw));
+  const int A = min(min(want, total), (int)gridDim.x * (W / tw));
   if (A == 0) return;
   // Team c begins at cut c, which leaves c / A of the line before it, moved to
   // the border of its item where that is near, so that no item is begun for a few units.
-  const int64_t each = total / A, more = total - each * A;           // the first `more` teams have a unit more
-  const int near = (int)min((int64_t)head, each * 3 / 4);
-  auto cut_at = [&](int c) { return c * each + min((int64_t)c, more); };
+  const int each = total / A, more = total - each * A;               // the first `more` teams have a step more
+  const int near = min(head >> p.shift, each * 3 / 4);
 #pragma unroll 1
   for (int k = 0; k < 2 * (W / tw); k++) {
     const int c = (k >> 1) * gridDim.x + blockIdx.x + (k & 1);       // few teams: on SMs of their own
     if (c > A) continue;
-    const int64_t x = cut_at(c);
+    const int x = c * each + min(c, more);
     Line &l = lines[k >> 1];
     if (x == total) {
       if (threadIdx.x == 0) {
@@ -298,17 +303,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         else l.at = x;
       }
     } else if (before <= x && x < before + mine) {
-      int b = b0;
-      int64_t off = x - before;
-      Req r;
-      for (;; b++) {
-        r = request(p, b, ROWS, head);
-        const int64_t n = (int64_t)r.units * r.tiles * hkv;
-        if (off < n) break;
-        off -= n;
-      }
-      const int in = (int)(off % r.units);
-      const int move = in < near ? -in : r.units - in < near ? r.units - in : 0;
+      int b = b0, off = x - before;
+      if (per > 1)
+        for (;; b++) {
+          r = request<ROWS, UNIT>(p, b, head);
+          const int n = r.steps * r.tiles * hkv;
+          if (off < n) break;
+          off -= n;
+        }
+      const int in = off % r.steps;
+      const int move = in < near ? -in : r.steps - in < near ? r.steps - in : 0;
       if (k & 1) l.end = x + move;
       else l.at = x + move, l.off = off + move, l.b = b;
     }
@@ -319,90 +323,92 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
   Line *line = lines + team;
 
   int islot = 0, tslot = 0;                                          // this warp's ring: next slot to fill, to take
-  uint32_t notes = 0;                                                // two bits a slot: tiles without a page
+  uint32_t notes = 0;                                                // UT bits a slot: tiles without a page
   for (;;) {
-    // -------------------------------------------------------------- list the next items (a warp, a request a lane)
+    // -------------------------------------------------------------- list the next items: 32 requests, up to kMaxSegs items
     team_sync(team, tthreads);
     if (line->at >= line->end) break;
     if (twarp == 0) {
       const int cb = line->b, b = cb + lane;
-      const int64_t lo = line->off, hi = lo + (line->end - line->at);   // the team's run, from request cb's first unit on
-      const int64_t g = line->at - lo;                               // that unit on the line
-      Req r{};
-      if (b < B) r = request(p, b, ROWS, head);
-      const int64_t n = (int64_t)r.units * r.tiles * hkv;
-      int64_t end = n;
+      const int lo = line->off, hi = lo + (line->end - line->at);    // the team's run, from request cb's first step on
+      const int g = line->at - lo;                                   // that step on the line
+      Req q{};
+      if (b < B) q = request<ROWS, UNIT>(p, b, head);
+      const int n = q.steps * q.tiles * hkv;
+      int end = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, end, o);
+        const int u = __shfl_up_sync(0xffffffffu, end, o);
         if (lane >= o) end += u;
       }
-      const int64_t first = end - n;
-      const int64_t s0 = first > lo ? first : lo, s1 = end < hi ? end : hi;
-      const int i0 = s1 > s0 ? (int)((s0 - first) / r.units) : 0;
-      const int cnt = s1 > s0 ? (int)((s1 - 1 - first) / r.units) - i0 + 1 : 0;
-      int place = cnt;
+      const int first = end - n, s0 = max(first, lo), s1 = min(end, hi);
+      const int i0 = s1 > s0 ? div_small(s0 - first, q.steps) : 0;
+      const int cnt = s1 > s0 ? div_small(s1 - 1 - first, q.steps) - i0 + 1 : 0;
+      int to = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, place, o);
-        if (lane >= o) place += u;
+        const int u = __shfl_up_sync(0xffffffffu, to, o);
+        if (lane >= o) to += u;
       }
-      place -= cnt;
-      for (int i = 0; i < cnt && place + i < kMaxSegs; i++) {
-        const int idx = i0 + i;
-        const int64_t i_s = first + (int64_t)idx * r.units, i_e = i_s + r.units;   // the item's units
-        const int64_t x0 = i_s > lo ? i_s : lo, x1 = i_e < hi ? i_e : hi;
+      const int listed = min(kMaxSegs, __shfl_sync(0xffffffffu, to, 31));
+      // a lane an item: the request it is of is the first one whose items reach past it
+      int src = 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (__shfl_sync(0xffffffffu, to, src + o - 1) <= lane) src += o;
+      src = min(src, 31);
+      Req t;
+      t.steps = __shfl_sync(0xffffffffu, q.steps, src);
+      t.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
+      t.n = __shfl_sync(0xffffffffu, q.n, src);
+      t.base = __shfl_sync(0xffffffffu, q.base, src);
+      t.hi = __shfl_sync(0xffffffffu, q.hi, src);
+      t.lo = __shfl_sync(0xffffffffu, q.lo, src);
+      t.cu0 = __shfl_sync(0xffffffffu, q.cu0, src);
+      const int idx = __shfl_sync(0xffffffffu, i0, src) + lane - (__shfl_sync(0xffffffffu, to - cnt, src));
+      const int i_s = __shfl_sync(0xffffffffu, first, src) + idx * t.steps, i_e = i_s + t.steps;   // the item's steps
+      if (lane < listed) {
+        const int x0 = max(i_s, lo) - i_s, x1 = min(i_e, hi) - i_s;
         Seg s;
-        s.b = b;
-        s.kvh = idx / r.tiles;
-        s.r0 = idx % r.tiles * ROWS;
-        s.rows = min(ROWS, r.n * p.ratio - s.r0);
-        const int f = s.r0 / p.ratio, l = (s.r0 + s.rows - 1) / p.ratio;   // first and last query of the tile
+        s.b = cb + src;
+        s.kvh = t.tiles == 1 ? idx : idx / t.tiles;
+        s.r0 = (idx - s.kvh * t.tiles) * ROWS;
+        s.rows = min(ROWS, t.n * p.ratio - s.r0);
+        const int f = div_small(s.r0, p.ratio), l = div_small(s.r0 + s.rows - 1, p.ratio);   // first and last query of the tile
         const int64_t w = a.window > 0 ? a.window : (int64_t)1 << 40;
-        auto clip = [&](int64_t v) { return (int)(v < 0 ? 0 : v > r.hi ? r.hi : v); };
-        s.vlo = clip((int64_t)r.base + f + 1 - w);
-        s.vhi = clip((int64_t)r.base + l + 1);
-        s.flo = clip((int64_t)r.base + l + 1 - w);
-        s.fhi = clip((int64_t)r.base + f + 1);
-        s.a = max(r.lo + max(0, (int)(x0 - i_s) - head), s.vlo / kUnit);
-        s.e = min(r.lo + max(0, (int)(x1 - i_s) - head), (s.vhi + kUnit - 1) / kUnit);
+        auto clip = [&](int64_t v) { return (int)(v < 0 ? 0 : v > t.hi ? t.hi : v); };
+        s.vlo = clip((int64_t)t.base + f + 1 - w);
+        s.vhi = clip((int64_t)t.base + l + 1);
+        s.flo = clip((int64_t)t.base + l + 1 - w);
+        s.fhi = clip((int64_t)t.base + f + 1);
+        auto unit = [&](int x) { return t.lo + (int)max((int64_t)0, ((int64_t)x << p.shift) - head); };
+        s.a = max(unit(x0), s.vlo / UNIT);
+        s.e = min(unit(x1), (s.vhi + UNIT - 1) / UNIT);
         if (s.vhi <= s.vlo) s.e = s.a;
-        s.base = r.base;
-        s.hi = r.hi;
-        s.cu0 = r.cu0;
-        // The teams of the item: a cut is, once moved, at or before the item's first unit if it falls before
-        // unit `near` (or the item's end), and before the item's end if it is not moved there.  The last cut
-        // at or before a unit is that of the team which has the unit before moves.
-        auto owner = [&](int64_t x) {
-          const int64_t longer = more * (each + 1);
-          return (int)(x < longer ? x / (each + 1) : more + (x - longer) / each);
+        s.base = t.base;
+        s.hi = t.hi;
+        s.cu0 = t.cu0;
+        // The teams of the item: a cut is, once moved, at or before the item's first step if it falls before
+        // step `near` (or the item's end), and before the item's end if it is not moved there.  The last cut
+        // at or before a step is that of the team which has the step before cuts are moved.
+        auto owner = [&](int x) {
+          const int longer = more * (each + 1);
+          return x < longer ? x / (each + 1) : more + (x - longer) / each;
         };
-        const int to_first = max(1, min(near, r.units)), to_last = near > 0 ? max(r.units - near + 1, to_first) : r.units;
+        const int to_first = max(1, min(near, t.steps)), to_last = near > 0 ? max(t.steps - near + 1, to_first) : t.steps;
         s.c0 = owner(g + i_s + to_first - 1);
         s.nseg = owner(g + i_s + to_last - 1) - s.c0 + 1;
-        segs[place + i] = s;
+        segs[lane] = s;
       }
-      // where the list ends: after kMaxSegs items or these 32 requests
-      const int listed = __reduce_add_sync(0xffffffffu, max(0, min(cnt, kMaxSegs - place)));
-      int64_t stop = 0;
-      if (cnt > 0 && place < kMaxSegs) {
-        const int64_t e = first + (int64_t)(i0 + min(cnt, kMaxSegs - place)) * r.units;
-        stop = e < hi ? e : hi;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const int64_t u = __shfl_xor_sync(0xffffffffu, stop, o);
-        stop = u > stop ? u : stop;
-      }
-      if (listed == 0) stop = __shfl_sync(0xffffffffu, end, 31);     // 32 requests without queries
-      // the request that holds unit `stop`, and the place in it
+      // where the list ends, the request that holds that step, and the place in it
+      const int stop = listed > 0 ? __shfl_sync(0xffffffffu, min(i_e, hi), listed - 1) : __shfl_sync(0xffffffffu, end, 31);
       const unsigned m = __ballot_sync(0xffffffffu, end > stop);
-      const int src = m ? __ffs(m) - 1 : 31;
-      const int64_t src_first = __shfl_sync(0xffffffffu, first, src), src_end = __shfl_sync(0xffffffffu, end, src);
+      const int nx = m ? __ffs(m) - 1 : 31;
+      const int nx_first = __shfl_sync(0xffffffffu, first, nx), nx_end = __shfl_sync(0xffffffffu, end, nx);
       if (lane == 0) {
         line->segs = listed;
-        line->b = m ? cb + src : cb + 32;
-        line->off = m ? stop - src_first : stop - src_end;
+        line->b = m ? cb + nx : cb + 32;
+        line->off = m ? stop - nx_first : stop - nx_end;
         line->at = g + stop;
       }
     }
@@ -411,14 +417,16 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
     if (nsegs == 0) continue;
 
     // -------------------------------------------------------------- producer: this warp's units, in order
-    // Each lane holds the page of one of the warp's next 32 units (of the next
-    // 16, of one of the two tiles, where a page holds a single one).
-    const bool two = p.g.page == kKvTile;
+    // Each lane holds the page of a part of one of the warp's next units (a unit
+    // has 1, 2 or 4 parts, after the page size).
+    const int lg_parts = UNIT > p.g.page ? (UNIT == 4 * p.g.page ? 2 : 1) : 0;
+    const uint8_t *cache_lane = static_cast<const uint8_t *>(a.cache) + lane * 16;
+    const int64_t page_bytes = (int64_t)hkv * p.g.head_bytes;
     int ps = -1, pu = 0, pe = 0, pk = 0, pid = -1;                   // segment, next unit, end, place among the lanes
     auto fetch_pages = [&]() {
       const Seg &s = segs[ps];
-      const int64_t tok = two ? (int64_t)(pu + (lane >> 1) * tw) * kUnit + (lane & 1) * kKvTile : (int64_t)(pu + lane * tw) * kUnit;
-      pid = tok < s.vhi && tok < (int64_t)pe * kUnit ? a.table[s.b * a.max_blocks + (tok >> p.g.lg_page)] : -1;
+      const int64_t tok = (int64_t)(pu + (lane >> lg_parts) * tw) * UNIT + (lane & ((1 << lg_parts) - 1)) * p.g.page;
+      pid = tok < s.vhi && tok < (int64_t)pe * UNIT ? a.table[s.b * a.max_blocks + (tok >> p.g.lg_page)] : -1;
       pk = 0;
     };
     auto open_seg = [&]() {                                          // the next segment that has a unit for this warp
@@ -432,26 +440,24 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
     // so that the count of groups stays that of units).  A tile without a page is zeros.
     auto issue = [&]() {
       if (ps < nsegs) {
-        const int g0 = __shfl_sync(0xffffffffu, pid, two ? 2 * pk : pk);
-        const int g1 = two ? __shfl_sync(0xffffffffu, pid, 2 * pk + 1) : g0;
-        const bool v0 = g0 >= 0 && g0 < p.g.pages, v1 = g1 >= 0 && g1 < p.g.pages;
-        const uint8_t *cache = static_cast<const uint8_t *>(a.cache) + (int64_t)segs[ps].kvh * p.g.head_bytes;
-        const int64_t page_bytes = (int64_t)hkv * p.g.head_bytes;
-        const uint8_t *s0 = cache + (v0 ? g0 * page_bytes : 0) + ((pu * kUnit & (p.g.page - 1)) >> 4) * TILE;
-        const uint8_t *s1 = two ? cache + (v1 ? g1 * page_bytes : 0) : s0 + TILE;
-        const uint32_t z0 = v0 ? 16 : 0, z1 = v1 ? 16 : 0, dst = my_ring + islot * STAGE + lane * 16;
+        const int tile0 = (pu * UNIT & (p.g.page - 1)) >> 4, kvh = segs[ps].kvh;
+        uint32_t dst = my_ring + islot * STAGE + lane * 16, note = 0;
 #pragma unroll
-        for (int o = 0; o < STAGE; o += 512) {
-          const int off = o + lane * 16;
-          if (o + 512 <= TILE) cp_async16z(dst + o, s0 + off, z0);
-          else if (o >= TILE && o + 512 <= STAGE) cp_async16z(dst + o, s1 + (off - TILE), z1);
-          else if (off < STAGE) cp_async16z(dst + o, off < TILE ? s0 + off : s1 + (off - TILE), off < TILE ? z0 : z1);
+        for (int i = 0; i < UT; i++) {
+          const int pg = __shfl_sync(0xffffffffu, pid, (pk << lg_parts) + (i << lg_parts) / UT);
+          const bool v = pg >= 0 && pg < p.g.pages;
+          const uint8_t *src = cache_lane + (v ? pg * page_bytes : 0) + kvh * p.g.head_bytes +
+                               ((tile0 + i) & ((p.g.page >> 4) - 1)) * TILE;
+          if (!v) note |= 1u << i;
+#pragma unroll
+          for (int o = 0; o < TILE; o += 512)
+            if (o + 512 <= TILE || o + lane * 16 < TILE) cp_async16z(dst + i * TILE + o, src + o, v ? 16u : 0u);
         }
-        notes = (notes & ~(3u << (2 * islot))) | ((v0 ? 0u : 1u) | (v1 ? 0u : 2u)) << (2 * islot);
+        notes = (notes & ~(((1u << UT) - 1) << (UT * islot))) | note << (UT * islot);
         islot = islot + 1 == S ? 0 : islot + 1;
         pu += tw;
         if (pu >= pe) open_seg();
-        else if (++pk == (two ? 16 : 32)) fetch_pages();
+        else if (++pk == (32 >> lg_parts)) fetch_pages();
       }
       cp_async_commit();
     };
@@ -464,9 +470,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
       for (int it = 0; it < QI; it++) {
         const int i = tid + it * tthreads, row = i / (D / 8), m = i % (D / 8);
         if (i < PIECES && row < s.rows) {
-          const int r = s.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
+          const int r = s.r0 + row, qi = div_small(r, p.ratio), hq = r - qi * p.ratio;
           const int64_t off = (int64_t)(s.cu0 + qi) * a.q_token + (int64_t)(s.kvh * p.ratio + hq) * a.q_head + 8 * m;
-          const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + off * C::ESZ);
+          const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.q) + off * (HL ? 4 : 2));
 #pragma unroll
           for (int j = 0; j < QV; j++) qraw[it][j] = src[j];
         } else {
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         if (m % (D / G / 8) == 0) qsum[m / (D / G / 8) * ROWS + row] = sum * pow2i(-24);
         if (m == 0) {
           fq[row] = ldexpf(a.scale * 1.44269504088896340736f, 24 - ex);     // log2(e)
-          const int qi = (sg.r0 + row) / p.ratio;
+          const int qi = div_small(sg.r0 + row, p.ratio);
           const int64_t pos = (int64_t)sg.base + qi;
           const int64_t lo = a.window > 0 ? pos + 1 - a.window : 0;
           lim[2 * row] = (int)max((int64_t)0, min(lo, (int64_t)sg.hi));
@@ -579,19 +585,20 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         cp_async_wait<S - 1>();
         __syncwarp();
         const uint8_t *st = ring_ptr + tslot * STAGE;
-        const uint32_t note = (notes >> (2 * tslot)) & 3u;
+        const uint32_t note = (notes >> (UT * tslot)) & ((1u << UT) - 1);
         tslot = tslot + 1 == S ? 0 : tslot + 1;
-        const bool full = note == 0 && u * kUnit >= sg.flo && u * kUnit + kUnit <= sg.fhi;
+        const bool full = note == 0 && u * UNIT >= sg.flo && u * UNIT + UNIT <= sg.fhi;
 
-        // ---------------------------------------------------------- scores of 32 tokens
-        float y[2][NT][4];
-        {
+        // ---------------------------------------------------------- scores of the unit
+        float y[UT][NT][4];
+#pragma unroll
+        for (int i0 = 0; i0 < UT; i0 += 2) {                         // two tiles share the q operands
           uint32_t kw[2][2][WPL], kc[2][2][G];                       // tile, row half
 #pragma unroll
           for (int i = 0; i < 2; i++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-              const uint8_t *tile = st + i * TILE;
+              const uint8_t *tile = st + (i0 + i) * TILE;
               const int row = lg + 8 * h;
               if constexpr (WPL == 2) {
                 const uint2 v = *reinterpret_cast<const uint2 *>(tile + (row * 4 + lt) * 8);
@@ -643,25 +650,25 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                   const float2 k = unpack_f16(kc[i][h][g]);          // scale, bias
-                  const float t0 = g == 0 ? k.y * qs.x : fmaf(k.y, qs.x, y[i][n][2 * h]);
-                  const float t1 = g == 0 ? k.y * qs.y : fmaf(k.y, qs.y, y[i][n][2 * h + 1]);
-                  y[i][n][2 * h] = fmaf(k.x, c[i][n][2 * h], t0);
-                  y[i][n][2 * h + 1] = fmaf(k.x, c[i][n][2 * h + 1], t1);
+                  const float t0 = g == 0 ? k.y * qs.x : fmaf(k.y, qs.x, y[i0 + i][n][2 * h]);
+                  const float t1 = g == 0 ? k.y * qs.y : fmaf(k.y, qs.y, y[i0 + i][n][2 * h + 1]);
+                  y[i0 + i][n][2 * h] = fmaf(k.x, c[i][n][2 * h], t0);
+                  y[i0 + i][n][2 * h + 1] = fmaf(k.x, c[i][n][2 * h + 1], t1);
                 }
             }
           }
         }
-        uint32_t vc[2][2][G];                                        // value scale and bias: tile, row half, group
+        uint32_t vc[UT][2][G];                                        // value scale and bias: tile, row half, group
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < UT; i++)
 #pragma unroll
           for (int h = 0; h < 2; h++) load_coefs<G>(st + i * TILE + 16 * D + 64 * G + (lg + 8 * h) * G * 4, vc[i][h]);
         if (!full) {
 #pragma unroll
-          for (int i = 0; i < 2; i++)
+          for (int i = 0; i < UT; i++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-              const int tok = u * kUnit + 16 * i + tk + h;
+              const int tok = u * UNIT + 16 * i + tk + h;
               const bool there = ((note >> i) & 1) == 0 && tok >= sg.vlo && tok < sg.vhi;
 #pragma unroll
               for (int n = 0; n < NT; n++)
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         // asks whether any lane met a larger one, and only then is what is summed so far rescaled.
         uint32_t smax = vc[0][0][0];
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < UT; i++)
 #pragma unroll
           for (int h = 0; h < 2; h++)
 #pragma unroll
@@ -693,7 +700,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         for (int n = 0; n < NT; n++)
 #pragma unroll
           for (int c = 0; c < 2; c++) {
-            mx[n][c] = fmaxf(fmaxf(y[0][n][c], y[0][n][2 + c]), fmaxf(y[1][n][c], y[1][n][2 + c])) * f[n][c];
+            float v = fmaxf(y[0][n][c], y[0][n][2 + c]);
+#pragma unroll
+            for (int i = 1; i < UT; i++) v = fmaxf(v, fmaxf(y[i][n][c], y[i][n][2 + c]));
+            mx[n][c] = v * f[n][c];
             grow |= mx[n][c] > mr[n][c];
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -723,7 +733,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
 #pragma unroll
           for (int c = 0; c < 2; c++)
 #pragma unroll
-            for (int i = 0; i < 2; i++)
+            for (int i = 0; i < UT; i++)
 #pragma unroll
               for (int h = 0; h < 2; h++) {
                 const float e = ex2(fmaf(y[i][n][2 * h + c], f[n][c], -mu[n][c]));
@@ -731,12 +741,12 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
                 lr[n][c] += e;
               }
         // ---------------------------------------------------------- p * sv as B operands, bias sums
-        uint32_t pf[2][G][NT][HL ? 4 : 2];
+        uint32_t pf[UT][G][NT][HL ? 4 : 2];
         auto weigh = [&](auto guard) {
 #pragma unroll
           for (int g = 0; g < G; g++)
 #pragma unroll
-            for (int i = 0; i < 2; i++)
+            for (int i = 0; i < UT; i++)
 #pragma unroll
               for (int h = 0; h < 2; h++) {
                 const float2 sv = unpack_f16(vc[i][h][g]);
@@ -769,9 +779,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
         // ---------------------------------------------------------- values
 #pragma unroll
         for (int c = 0; c < VW / 4; c++) {
-          uint32_t vw[2][4];
+          uint32_t vw[UT][4];
 #pragma unroll
-          for (int i = 0; i < 2; i++) {
+          for (int i = 0; i < UT; i++) {
             const uint4 v = *reinterpret_cast<const uint4 *>(st + i * TILE + 8 * D + (c * 32 + lane) * 16);
             vw[i][0] = v.x, vw[i][1] = v.y, vw[i][2] = v.z, vw[i][3] = v.w;
           }
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
             const int w = 4 * c + x, g = w / (VW / G);
             float d[NT][4];
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
+            for (int i = 0; i < UT; i++) {
               const uint32_t x0 = vw[i][x], x1 = x0 >> 8;
               uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
               if constexpr (HL) {                                    // code - 8, exact: 8 and 128 times 2^-24
@@ -852,19 +862,23 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
             }
           }
       };
-      if (twarp >= tw / 2) {
-        float *j = join + (twarp - tw / 2) * ROWS * OS;
+      constexpr bool AT_ONCE = C::RW == C::TW;
+      const int half = AT_ONCE ? tw : tw / 2;                        // results side by side
+      if (AT_ONCE || twarp >= half) {
+        float *j = join + (AT_ONCE ? twarp : twarp - half) * ROWS * OS;
         each_out([&](int row, int d, float v) { j[row * OS + d] = v; });
       }
       team_sync(team, tthreads);
-      if (twarp < tw / 2) {
-        float *j = join + twarp * ROWS * OS;
-        each_out([&](int row, int d, float v) { j[row * OS + d] += v; });
+      if constexpr (!AT_ONCE) {
+        if (twarp < half) {
+          float *j = join + twarp * ROWS * OS;
+          each_out([&](int row, int d, float v) { j[row * OS + d] += v; });
+        }
+        team_sync(team, tthreads);
       }
-      team_sync(team, tthreads);
       // ------------------------------------------------------------ the item's rows, whole or as a partial result
       auto put_row = [&](int row, int d, float4 v) {
-        const int r = sg.r0 + row, qi = r / p.ratio, hq = r % p.ratio;
+        const int r = sg.r0 + row, qi = div_small(r, p.ratio), hq = r - qi * p.ratio;
         const int64_t off = ((int64_t)(sg.cu0 + qi) * a.heads + sg.kvh * p.ratio + hq) * D + d;
         if constexpr (HL) {
           *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + off) = v;
@@ -881,7 +895,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
       for (int i = tid; i < rows * (D / 4); i += tthreads) {
         const int row = i / (D / 4), d = i % (D / 4) * 4;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = 0; w < tw / 2; w++) {
+        for (int w = 0; w < half; w++) {
           const float4 x = *reinterpret_cast<const float4 *>(join + (w * ROWS + row) * OS + d);
           v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
         }
@@ -961,9 +975,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, HL>::THREADS, 1) attend_warp_kernel
 
 template <int D, int G, int NT, bool HL>
 cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
-  using C = Cfg<D, NT, HL>;
-  static_assert(C::stages(G) >= 2, "the ring needs two units a warp");
-  constexpr int alloc = C::W * C::stages(G) * 2 * (16 * D + 128 * G) + C::fixed(G);
+  using C = Cfg<D, G, NT, HL>;
   Params p{};
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
@@ -973,13 +985,18 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   const int64_t items = a.B * a.kv_heads * ((a.max_fresh * p.ratio + C::ROWS - 1) / C::ROWS);
   p.team = items > kv_max_ctas(1) ? C::TW : C::W;
   p.min_units = 2 * p.team;
+  p.head = 2 * p.team;
+  // the most steps that the line can have, in 32 bits
+  const double most = ((double)a.tokens * a.heads / C::ROWS + (double)a.tokens * a.kv_heads) *
+                      ((double)a.max_blocks * a.page / C::UNIT + 2 + p.head);
+  while (most / (1 << p.shift) > 1e9) p.shift++;
   auto kern = attend_warp_kernel<D, G, NT, HL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, alloc);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(kv_max_ctas(1));
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = alloc;
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

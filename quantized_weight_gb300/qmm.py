@@ -50,6 +50,8 @@ def declared_symbols() -> list[str]:
 def lib():
     """The loaded library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -98,9 +100,18 @@ def _status_string(status: int) -> str:
         return STATUS.get(int(status), str(status))
 
 
+try:                                   # the handle alone: a Stream object costs 3 us a call
+    from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
+
+    def _current_stream() -> int:
+        return _cuda_getCurrentRawStream(_cuda_getDevice())
+except ImportError:
+    def _current_stream() -> int:
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    return _current_stream() if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
@@ -267,34 +278,64 @@ def gather_dequant(ids, packed, scales, biases, N, K, bits, group, out=None, str
     return out
 
 
+_I32 = torch.int32
 _KV_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 
 
+# The checks of the cache calls come in two steps: one test that a good argument
+# passes, and _need's messages where it does not.  A decode step makes several such calls a layer.
+
+def _i32(t, name, shape) -> int:
+    """Pointer of a contiguous int32 CUDA tensor of the given shape."""
+    if not (t.dtype is _I32 and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, name, _I32, shape)
+    return t.data_ptr()
+
+
 def _kv_rows(t, name, dtype, shape):
-    """A [tokens, heads, head_dim] tensor whose last dimension is contiguous; its strides."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    """Token and head strides of a [tokens, heads, head_dim] tensor whose last dimension is contiguous."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1:
+    token, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)   # a lone row has no stride to keep
+    return (token if shape[0] > 1 else 0), (head if shape[1] > 1 else 0)   # a lone row has no stride to keep
 
 
-def _kv_dtype(dtype):
-    if dtype not in _KV_DTYPE:
+def _kv_dtype(dtype) -> int:
+    dt = _KV_DTYPE.get(dtype)
+    if dt is None:
         raise TypeError(f"keys, values and queries are float32 or bfloat16, got {dtype}")
-    return _KV_DTYPE[dtype]
+    return dt
 
 
-def _kv_cache_ok(cache, D, page, group):
-    _need(cache, "cache", torch.uint8)
-    if cache.dim() != 3 or cache.shape[2] * 16 != page * (16 * D + 128 * (D // group)):
+def _kv_cache(cache, D, page, group):
+    """(pages, kv_heads, pointer) of a cache."""
+    if not (cache.dtype is torch.uint8 and cache.is_cuda and cache.is_contiguous()):
+        _need(cache, "cache", torch.uint8)
+    shape = cache.shape
+    if len(shape) != 3 or shape[2] * 16 != page * (16 * D + 128 * (D // group)):
         raise ValueError(f"cache must be [pages, kv_heads, bytes] as kv_cache() makes it for head_dim {D}, page {page}, "
-                         f"group {group}; got {tuple(cache.shape)}")
+                         f"group {group}; got {tuple(shape)}")
+    return shape[0], shape[1], cache.data_ptr()
+
+
+def _kv_table(table, B):
+    """(max_blocks, pointer) of a block table."""
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(shape)}")
+    return shape[1], _i32(table, "block_table", shape)
+
+
+def _kv_out(t, name, dtype, shape) -> int:
+    if not (t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
 
 
 def kv_cache(pages, kv_heads, head_dim, page, group=64, device="cuda") -> torch.Tensor:
@@ -308,53 +349,46 @@ def kv_cache(pages, kv_heads, head_dim, page, group=64, device="cuda") -> torch.
 def kv_plan(cached, fresh, free_pages, block_table, tokens, page, out=None, stream=None):
     """One step's (slots [tokens], positions [tokens], cu [B + 1], lens [B], need [1]), int32, from the requests'
     lengths; block_table [B, max_blocks] is completed in place with pages from the front of free_pages."""
-    i32 = torch.int32
-    _need(cached, "cached", i32)
+    shape = cached.shape
     B = cached.numel()
-    _need(fresh, "fresh", i32, (B,))
-    _need(free_pages, "free_pages", i32)
-    _need(block_table, "block_table", i32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
+    pc, pf, pp = _i32(cached, "cached", shape), _i32(fresh, "fresh", (B,)), _i32(free_pages, "free_pages", free_pages.shape)
+    blocks, pt = _kv_table(block_table, B)
     if out is None:
-        buf = torch.empty((2 * tokens + 2 * B + 2,), dtype=i32, device=cached.device)
-        out = buf.split((tokens, tokens, B + 1, B, 1))
+        out = torch.empty(2 * (tokens + B + 1), dtype=_I32, device=cached.device).split_with_sizes((tokens, tokens, B + 1, B, 1))
     slots, positions, cu, lens, need = out
-    for t, name, n in ((slots, "slots", tokens), (positions, "positions", tokens), (cu, "cu", B + 1), (lens, "lens", B),
-                       (need, "need", 1)):
-        _need(t, name, i32, (n,))
-    _call("qmm_kv_plan", lib().qmm_kv_plan(_ptr(cached), _ptr(fresh), _ptr(free_pages), free_pages.numel(),
-                                           _ptr(block_table), B, block_table.shape[1], page, tokens, _ptr(slots),
-                                           _ptr(positions), _ptr(cu), _ptr(lens), _ptr(need), _stream(stream)))
+    _call("qmm_kv_plan", lib().qmm_kv_plan(
+        pc, pf, pp, free_pages.numel(), pt, B, blocks, page, tokens, _i32(slots, "slots", (tokens,)),
+        _i32(positions, "positions", (tokens,)), _i32(cu, "cu", (B + 1,)), _i32(lens, "lens", (B,)),
+        _i32(need, "need", (1,)), _stream(stream)))
     return out
 
 
 def kv_append(k, v, slots, cache, page, group=64, stream=None) -> None:
     """Quantize k, v [T, kv_heads, head_dim] (float32 or bfloat16) into the cache's slots; a slot outside it is skipped."""
-    T, H, D = k.shape
-    dt = _kv_dtype(k.dtype)
-    ks = _kv_rows(k, "k", k.dtype, k.shape)
-    vs = _kv_rows(v, "v", k.dtype, k.shape)
-    _need(slots, "slots", torch.int32, (T,))
-    _kv_cache_ok(cache, D, page, group)
-    if cache.shape[1] != H:
-        raise ValueError(f"cache has {cache.shape[1]} kv heads, k has {H}")
-    _call("qmm_kv_append", lib().qmm_kv_append(_ptr(k), _ptr(v), dt, *ks, *vs, _ptr(slots), _ptr(cache), T,
-                                               cache.shape[0], H, D, page, group, _stream(stream)))
+    dtype, shape = k.dtype, k.shape
+    T, H, D = shape
+    dt = _kv_dtype(dtype)
+    kt, kh = _kv_rows(k, "k", dtype, shape)
+    vt, vh = _kv_rows(v, "v", dtype, shape)
+    ps = _i32(slots, "slots", (T,))
+    pages, heads, pc = _kv_cache(cache, D, page, group)
+    if heads != H:
+        raise ValueError(f"cache has {heads} kv heads, k has {H}")
+    _call("qmm_kv_append", lib().qmm_kv_append(k.data_ptr(), v.data_ptr(), dt, kt, kh, vt, vh, ps, pc, T, pages, H, D,
+                                               page, group, _stream(stream)))
 
 
 def kv_read(slots, cache, head_dim, page, group=64, dtype=torch.float32, out=None, stream=None):
     """The (keys, values) [T, kv_heads, head_dim] that the slots hold; a slot outside the cache gives NaN rows."""
-    _need(slots, "slots", torch.int32)
-    _kv_cache_ok(cache, head_dim, page, group)
-    dt, shape = _kv_dtype(dtype), (slots.numel(), cache.shape[1], head_dim)
+    ps = _i32(slots, "slots", slots.shape)
+    pages, H, pc = _kv_cache(cache, head_dim, page, group)
+    T, dt = slots.numel(), _kv_dtype(dtype)
+    shape = (T, H, head_dim)
     if out is None:
-        out = torch.empty((2,) + shape, dtype=dtype, device=cache.device).unbind(0)
+        out = torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device)
     k, v = out
-    _need(k, "k", dtype, shape)
-    _need(v, "v", dtype, shape)
-    _call("qmm_kv_read", lib().qmm_kv_read(_ptr(slots), _ptr(cache), _ptr(k), _ptr(v), dt, shape[0], cache.shape[0],
-                                           shape[1], head_dim, page, group, _stream(stream)))
+    _call("qmm_kv_read", lib().qmm_kv_read(ps, pc, _kv_out(k, "k", dtype, shape), _kv_out(v, "v", dtype, shape), dt, T,
+                                           pages, H, head_dim, page, group, _stream(stream)))
     return k, v
 
 
@@ -371,25 +405,23 @@ def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_
     """Attention of q [T, heads, head_dim] (float32 or bfloat16) over each request's cached tokens, causal, with an
     optional sliding window: request b's queries are tokens cu[b] .. cu[b + 1] - 1 (cu None: token b), the last of
     its lens[b] tokens.  scale defaults to head_dim ** -0.5."""
-    T, H, D = q.shape
-    dt = _kv_dtype(q.dtype)
-    qs = _kv_rows(q, "q", q.dtype, q.shape)
-    _kv_cache_ok(cache, D, page, group)
-    _need(lens, "lens", torch.int32)
+    dtype, shape = q.dtype, q.shape
+    T, H, D = shape
+    dt = _kv_dtype(dtype)
+    qt, qh = _kv_rows(q, "q", dtype, shape)
+    pages, heads, pc = _kv_cache(cache, D, page, group)
+    pl = _i32(lens, "lens", lens.shape)
     B = lens.numel()
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must be [{B}, max_blocks], got {tuple(block_table.shape)}")
-    if cu is not None:
-        _need(cu, "cu", torch.int32, (B + 1,))
-    _need(workspace, "workspace", torch.uint8)
+    blocks, pt = _kv_table(block_table, B)
+    pcu = None if cu is None else _i32(cu, "cu", (B + 1,))
+    if not (workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous()):
+        _need(workspace, "workspace", torch.uint8)
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    _need(out, "out", q.dtype, (T, H, D))
+        out = torch.empty(shape, dtype=dtype, device=q.device)
     _call("qmm_kv_attend", lib().qmm_kv_attend(
-        _ptr(q), dt, *qs, _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(cu), _ptr(out), T, B, block_table.shape[1],
-        max_fresh, cache.shape[0], H, cache.shape[1], D, page, group, D ** -0.5 if scale is None else scale, window,
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        q.data_ptr(), dt, qt, qh, pc, pt, pl, pcu, _kv_out(out, "out", dtype, shape), T, B, blocks, max_fresh, pages, H,
+        heads, D, page, group, D ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.numel(),
+        _stream(stream)))
     return out
 
 
