@@ -280,13 +280,14 @@ int qmm_test_timeout_next_decode(int64_t limit_ns) {
 
 int qmm_check(qmm_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QMM_ERR_CUDA;
-  int st[5] = {0, 0, 0, 0, 0};
+  int st[6] = {0, 0, 0, 0, 0, 0};
   if (qmm::read_clear_gemm_status(&st[0], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_gemv_status(&st[1], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_q1_status(&st[2], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_batch_status(&st[3], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_tc_status(&st[4], stream) != cudaSuccess) return QMM_ERR_CUDA;
-  return (st[0] | st[1] | st[2] | st[3] | st[4]) != 0 ? QMM_ERR_DEVICE_TIMEOUT : QMM_OK;
+  if (qmm::read_clear_kv_status(&st[5], stream) != cudaSuccess) return QMM_ERR_CUDA;
+  return (st[0] | st[1] | st[2] | st[3] | st[4] | st[5]) != 0 ? QMM_ERR_DEVICE_TIMEOUT : QMM_OK;
 }
 
 }  // extern "C"

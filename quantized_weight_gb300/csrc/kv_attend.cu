@@ -9,7 +9,9 @@ size_t kv_attend_workspace(int64_t, int64_t, int64_t, int64_t head_dim, int64_t)
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s) {
-  const int nt = a.max_fresh * (a.heads / a.kv_heads) <= 8 ? 1 : 2;
+  const int64_t rows = a.max_fresh * (a.heads / a.kv_heads);
+  if (a.bf16 && rows > 64) return launch_kv_prefill(a, s);
+  const int nt = rows <= 8 ? 1 : 2;
   if (a.head_dim == 64) return launch_kv_warp_d64(a, nt, s);
   if (a.head_dim == 128) return launch_kv_warp_d128(a, nt, s);
   if (a.head_dim == 256) return launch_kv_warp_d256(a, s);

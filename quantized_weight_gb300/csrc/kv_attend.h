@@ -43,6 +43,10 @@ inline int kv_max_ctas(int per_sm) {
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
 
+// Many queries a request, bfloat16 (kv_prefill.cu); its waits are bounded and report here.
+cudaError_t launch_kv_prefill(const KvAttendArgs &a, cudaStream_t s);
+cudaError_t read_clear_kv_status(int *status, cudaStream_t s);
+
 // Per head dimension (one translation unit each); nt: tiles of 8 rows of q an item
 // (heads of 256: one, since registers and shared memory hold no more).
 cudaError_t launch_kv_warp_d64(const KvAttendArgs &a, int nt, cudaStream_t s);

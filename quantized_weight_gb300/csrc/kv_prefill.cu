@@ -1,0 +1,839 @@
+// kv_prefill.cu -- attention over the 4-bit cache for many queries a request
+// (prompts and their chunks), bfloat16, on tcgen05.
+//
+// An item is (request, kv head, up to NQ tiles of 128 rows of q), a row being a
+// (query token, query head of the group) pair; it walks the keys that its rows see in
+// blocks of KB tokens with a running maximum and sum:
+//
+//   S = Q K^T (TMEM) -> P = exp2(c S - m), binary16, over S (TMEM) -> O += P V (TMEM)
+//
+// Roles of the persistent CTA, one an SM (20 warps):
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, a row a thread: maximum,
+//                    exponentials, P, O's rescaling, and the tile's q and output
+//   warps 8-11       keys: 4-bit codes from the cache to binary16 in shared memory
+//   warps 12-15      values, the same, transposed
+//   warp 16          TMEM and the single-thread MMA issue
+//   warp 17          items, from a ticket counter (longest first within a request)
+//   warps 18-19      none
+// The two row tiles alternate: while one tile's softmax runs, the tensor core
+// has the other's products.  With one row tile (heads of 256, or the rest of a request) the
+// blocks alternate instead, between the same two score buffers.  Step i of an item uses score
+// buffer i % 2, and S(i + 2) is issued right after PV(i): it overwrites P(i),
+// which that product has read by then, since MMAs execute in order.
+//
+// Shared memory holds the operands K-major with the 128-byte swizzle.  The cache's
+// row order (kv_layout.cuh) is the order of a tile's tokens in both key rows and
+// value columns, so nothing is shuffled: a key word is eight elements of a row, and the words of four
+// token quads at one element are two 16-byte runs of tokens.  The order inside a
+// tile shows only in the mask.
+//
+// Precision: q is exact in binary16 after a power of two per row; keys and values are s * q + b
+// rounded once to binary16; P is rounded to binary16, at most 2^8 (the reference
+// maximum follows the true one only when that has grown by 2^8, so O is seldom
+// rescaled); sums and accumulators are float32.
+//
+// Bound: tensor cores: 4 * D flops a row and key; a block of 128 keys for two row tiles of 128 is 16.8 MFLOP against 36 KB of cache.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "bounded_wait.cuh"
+#include "kv_attend.h"
+#include "kv_layout.cuh"
+#include "qmm_device.cuh"
+#include "sm100_ptx.cuh"
+
+namespace qmm {
+
+__device__ int g_kv_status = 0;   // QMM_OK or QMM_ERR_DEVICE_TIMEOUT (-6)
+
+namespace {
+
+using namespace sm100;
+
+constexpr int QROWS = 128;                       // rows of a q tile (MMA M)
+constexpr int DQ_WARP0 = 8, MMA_WARP = 16, ITEM_WARP = 17;
+constexpr int THREADS = 32 * 20;                 // five warpgroups, the last one's last two warps without work
+// Registers a thread by warpgroup, out of the launch's.
+constexpr int REG_LAUNCH = 96;                   // 64 K / 640 threads, in steps of 8 a warp and scheduler
+constexpr int REG_SOFT = 112, REG_KEYS = 88, REG_VALUES = 104, REG_REST = 64;
+static_assert(2 * REG_SOFT + REG_KEYS + REG_VALUES + REG_REST <= 5 * REG_LAUNCH, "more registers than the launch has");
+constexpr int ITEM_SLOTS = 3;
+constexpr float GROW = 8.0f;                     // log2 by which scores may exceed the reference maximum
+
+struct Params {
+  KvAttendArgs a;
+  KvGeom g;
+  int ratio;
+};
+
+struct Item {
+  int b, kvh, r0, rows;             // rows r0 .. r0 + rows - 1 of the request
+  int tiles;                        // row tiles (1 or 2); 0: no more items
+  int blk0, blocks;                 // blocks of keys
+  int vlo, vhi;                     // tokens that any row sees
+  int flo, fhi;                     // tokens that all rows see
+  int base, hi, cu0;                // position of the first query; tokens that can be read; its token
+};
+
+template <int D_, int G_>
+struct Cfg {
+  static constexpr int D = D_, G = G_;
+  static constexpr int NQ = D == 256 ? 1 : 2;              // row tiles
+  static constexpr int KB = D == 256 ? 64 : 128;           // keys a block
+  static constexpr int TILE = 16 * D + 128 * G;
+  static constexpr int Q_BYTES = QROWS * D * 2, KV_BYTES = KB * D * 2;
+  static constexpr int OFF_K = NQ * Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES, OFF_END = OFF_V + 2 * KV_BYTES;
+  static constexpr int EDGES = 8;                          // blocks of an item that only some rows see: at most 3 at either end
+  static constexpr int NOTES = EDGES * G * (KB / 32);      // a bit a (block, group, position)
+  static constexpr int SMALL = 512 + 4 * NOTES * 4;
+  static constexpr int SMEM = OFF_END + SMALL + 1024;      // the last for alignment
+};
+
+// barriers (8 bytes each)
+enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, K_FULL = 8, K_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, IT_FULL = 16,
+       IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, BARS };
+
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// A from TMEM: lane = row, a 32-bit column = two consecutive k.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// D f32, A and B binary16, both K-major
+constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Two codes, exact: the low nibbles of a word's halves, and those above them.
+// A code below exponent 25's leading one is 1024 + code (or 1024 + 16 code).
+__device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return hsub2(and_or(x, 0x000F000Fu, 0x64006400u), 0x64006400u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
+  return hfma2(and_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u /* 1/16 */, 0xD400D400u /* -64 */);
+}
+__device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ int token_of(int pos) { return 4 * ((pos & 7) >> 1) + 2 * (pos & 1) + (pos >> 3); }   // inverse of kv_row
+
+struct Phase {
+  uint32_t v = 0;
+  __device__ __forceinline__ uint32_t next() {
+    const uint32_t p = v;
+    v ^= 1u;
+    return p;
+  }
+};
+
+// A warpgroup's registers a thread, from the launch's to N: .inc only upwards, .dec only downwards.
+template <int N>
+__device__ __forceinline__ void set_registers() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg's range");
+  if constexpr (N > REG_LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < REG_LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<D, G>;
+  constexpr int KB = C::KB, NQ = C::NQ, TILE = C::TILE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_addr(smem);
+  const uint32_t bars = sb + C::OFF_END;
+  uint8_t *small = smem + C::OFF_END;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 192);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 196);
+  uint4 *kvalid = reinterpret_cast<uint4 *>(small + 208);                    // [4] a word a key warp: tiles of the block with a page
+  Item *items = reinterpret_cast<Item *>(small + 272);                       // [ITEM_SLOTS]
+  static_assert(8 * BARS <= 192 && 272 + ITEM_SLOTS * sizeof(Item) <= 480, "small arrays");
+  int *noted = reinterpret_cast<int *>(small + 480);                         // [4] items: has notes
+  uint32_t *notes = reinterpret_cast<uint32_t *>(small + 512);               // [4] items x NOTES: values taken out
+  auto bar = [&](int i) { return bars + 8 * i; };
+  const WaitCtl ctl{abort_flag, &g_kv_status};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const KvAttendArgs &a = p.a;
+  const int hkv = p.g.kv_heads;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ITEM_SLOTS; i++) {
+      mbar_init(bar(IT_FULL + i), 1);
+      mbar_init(bar(IT_EMPTY + i), ITEM_WARP);           // a warp an arrival
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(bar(S_FULL + i), 1);
+      mbar_init(bar(P_FULL + i), 128);
+      mbar_init(bar(PV_DONE + i), 1);
+      mbar_init(bar(Q_FULL + i), 128);
+      mbar_init(bar(K_FULL + i), 128);
+      mbar_init(bar(K_EMPTY + i), 1);
+      mbar_init(bar(V_FULL + i), 128);
+      mbar_init(bar(V_EMPTY + i), 1);
+    }
+    mbar_init(bar(DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) tmem_alloc(smem_addr(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // The next item, for every warp but the one that hands them out; it stays in shared memory until the warp lets go of it.
+  int it_slot = 0;
+  uint32_t it_ph = 0;
+  auto next_item = [&]() -> const Item * {
+    if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_FULL + it_slot), it_ph, ctl))) return nullptr;
+    return items[it_slot].tiles > 0 ? items + it_slot : nullptr;
+  };
+  auto release = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(IT_EMPTY + it_slot));
+    if (++it_slot == ITEM_SLOTS) it_slot = 0, it_ph ^= 1u;
+  };
+
+  if (warp >= MMA_WARP) set_registers<REG_REST>();
+  else if (warp >= DQ_WARP0 + 4) set_registers<REG_VALUES>();
+  else if (warp >= DQ_WARP0) set_registers<REG_KEYS>();
+  else set_registers<REG_SOFT>();
+
+  if (warp > ITEM_WARP) {
+    // no work
+  } else if (warp == ITEM_WARP) {
+    // ------------------------------------------------------------ items
+    unsigned *ticket = static_cast<unsigned *>(a.workspace) + (kKvMaxCtas - 1), *done = ticket - 1;
+    int cb = 0;                               // requests before cb are behind this CTA's tickets
+    int64_t cfirst = 0;                       // items before request cb
+    uint32_t ph = 1;
+    for (int slot = 0;;) {
+      unsigned t = 0;
+      if (lane == 0) t = atomicAdd(ticket, 1u);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      Item it{};
+      for (; cb < a.B; cb += 32) {
+        const int b = cb + lane;
+        int n = 0, len = 0, c0 = 0, tiles = 0;
+        if (b < a.B) {
+          len = max(0, a.lens[b]);
+          c0 = a.cu ? max(0, min(a.cu[b], (int)a.tokens)) : b;
+          n = a.cu ? max(c0, min(a.cu[b + 1], (int)a.tokens)) - c0 : 1;
+          tiles = (n * p.ratio + NQ * QROWS - 1) / (NQ * QROWS);
+        }
+        int end = tiles * hkv;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += u;
+        }
+        const int all = __shfl_sync(0xffffffffu, end, 31);
+        if ((int64_t)t < cfirst + all) {
+          const int k = (int)((int64_t)t - cfirst);
+          const int src = __ffs(__ballot_sync(0xffffffffu, end > k)) - 1;
+          const int idx = k - (__shfl_sync(0xffffffffu, end - tiles * hkv, src));
+          n = __shfl_sync(0xffffffffu, n, src);
+          len = __shfl_sync(0xffffffffu, len, src);
+          c0 = __shfl_sync(0xffffffffu, c0, src);
+          tiles = __shfl_sync(0xffffffffu, tiles, src);
+          it.b = cb + src;
+          it.kvh = idx % hkv;
+          it.r0 = (tiles - 1 - idx / hkv) * NQ * QROWS;
+          it.rows = min(NQ * QROWS, n * p.ratio - it.r0);
+          it.tiles = it.rows > QROWS ? 2 : 1;
+          it.base = len - n;
+          it.cu0 = c0;
+          it.hi = (int)min((int64_t)len, a.max_blocks << p.g.lg_page);
+          const int64_t f = (int64_t)it.base + it.r0 / p.ratio, l = (int64_t)it.base + (it.r0 + it.rows - 1) / p.ratio;
+          const int64_t lo = a.window > 0 ? f + 1 - a.window : 0;
+          it.vlo = (int)max((int64_t)0, min(lo, (int64_t)it.hi));
+          it.vhi = (int)max((int64_t)0, min(l + 1, (int64_t)it.hi));
+          it.flo = a.window > 0 ? (int)max((int64_t)0, min(l + 1 - a.window, (int64_t)it.hi)) : 0;
+          it.fhi = (int)max((int64_t)0, min(f + 1, (int64_t)it.hi));
+          it.blk0 = it.vlo / KB;
+          it.blocks = it.vhi > it.vlo ? (it.vhi + KB - 1) / KB - it.blk0 : 0;
+          break;
+        }
+        cfirst += all;
+      }
+      if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_EMPTY + slot), ph, ctl))) break;
+      if (lane == 0) {
+        items[slot] = it;
+        mbar_arrive(bar(IT_FULL + slot));
+      }
+      if (it.tiles == 0) break;
+      if (++slot == ITEM_SLOTS) slot = 0, ph ^= 1u;
+    }
+    // the last CTA through leaves the counters zero for the next call
+    if (lane == 0) {
+      __threadfence();
+      if (atomicAdd(done, 1u) == gridDim.x - 1) {
+        *ticket = 0u;
+        *done = 0u;
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t id_s = idesc_f16(QROWS, KB), id_o = idesc_f16(QROWS, D);
+    Phase kf[2], vf[2], pf[2], qf[2];
+    int kb = 0, vb = 0;                       // blocks begun, over all items
+    bool ok = true;
+    while (const Item *ip = next_item()) {
+      const Item &it = *ip;
+      const int nt = it.tiles, N = nt * it.blocks;
+      if (lane == 0) {
+        int k_at = -1, v_at = -1;             // the block whose keys / values were waited for
+        auto scores = [&](int i) -> bool {    // S of step i
+          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
+          if (i < nt && !wait_bounded(bar(Q_FULL + x), qf[x].next(), ctl)) return false;
+          if (j != k_at) {
+            if (!wait_bounded(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl)) return false;
+            k_at = j;
+            kb++;
+          }
+          tc_fence_after();
+          const uint32_t kbuf = sb + C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES, qbuf = sb + x * C::Q_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; kk++) {
+            const uint64_t ad = smem_desc_sw128(qbuf + (kk / 4) * (QROWS * 128)) + 2 * (kk % 4);
+            const uint64_t bd = smem_desc_sw128(kbuf + (kk / 4) * (KB * 128)) + 2 * (kk % 4);
+            umma_f16_ss(tmem + buf * 128, ad, bd, id_s, kk != 0);
+          }
+          umma_commit(bar(S_FULL + buf));
+          if (x == nt - 1) umma_commit(bar(K_EMPTY + ((kb - 1) & 1)));
+          return true;
+        };
+        ok = N == 0 || (scores(0) && (N < 2 || scores(1)));
+        for (int i = 0; i < N && ok; i++) {
+          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
+          if (j != v_at) {
+            if (!wait_bounded(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl)) { ok = false; break; }
+            v_at = j;
+            vb++;
+          }
+          if (!wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t vbuf = sb + C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < KB / 16; kk++) {
+            const uint64_t bd = smem_desc_sw128(vbuf + (kk / 4) * (D * 128)) + 2 * (kk % 4);
+            umma_f16_ts(tmem + 256 + x * D, tmem + buf * 128 + 8 * kk, bd, id_o, (j | kk) != 0);
+          }
+          umma_commit(bar(PV_DONE + x));
+          if (x == nt - 1) umma_commit(bar(V_EMPTY + ((vb - 1) & 1)));
+          if (i + 2 < N) ok = scores(i + 2);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      release();
+    }
+    if (lane == 0 && *abort_flag) {           // wait (bounded) for the MMAs in flight before TMEM goes
+      umma_commit(bar(DRAIN));
+      wait_drain(bar(DRAIN), 0);
+    }
+  } else if (warp >= DQ_WARP0 + 4) {
+    // ------------------------------------------------------------ values
+    constexpr int CB = D / 64;                               // blocks of 64 elements
+    constexpr int GV = G > CB ? 2 : 1;                       // groups in one (group of 32: two)
+    constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
+    const int u = threadIdx.x - (DQ_WARP0 + 4) * 32, g8 = u & 7, c = (u >> 3) % CB, tl = (u >> 3) / CB;
+    const bool act = u < UNITS;
+    Phase ve[2];
+    ve[0].v = ve[1].v = 1;
+    int vb = 0, n_item = 0;
+    bool ok = true;
+    for (; const Item *ip = next_item(); n_item++) {
+      const Item &it = *ip;
+      // this item's notes, last used four items ago
+      uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
+      for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
+      if (u == 0) noted[n_item & 3] = 0;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const int32_t *tab = a.table + it.b * a.max_blocks;
+      auto page_of = [&](int blk) {
+        const int64_t tok = (int64_t)blk * KB + tl * 16;
+        return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+      };
+      uint4 w[4];
+      uint32_t cf[16][GV];
+      bool there = false;
+      auto fetch = [&](int blk, int pg) {
+        there = pg >= 0 && pg < p.g.pages;
+        if (there) {
+          const int64_t tok = (int64_t)blk * KB + tl * 16;
+          const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
+                             (((int)tok & (p.g.page - 1)) >> 4) * TILE;
+          const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (c * 8 + g8) * 64);
+#pragma unroll
+          for (int i = 0; i < 4; i++) w[i] = __ldg(s + i);
+          const uint8_t *cp = t + 16 * D + 64 * G + (G > CB ? 2 * c : c * G / CB) * 4;
+#pragma unroll
+          for (int r = 0; r < 16; r++) {
+            if constexpr (GV == 1) {
+              cf[r][0] = __ldg(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp + r * G * 4));
+              cf[r][0] = v.x, cf[r][GV - 1] = v.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; i++) w[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+#pragma unroll
+            for (int g = 0; g < GV; g++) cf[r][g] = 0u;
+        }
+      };
+      if (it.blocks > 0) fetch(it.blk0, page_of(it.blk0));
+      int pg_next = it.blocks > 1 ? page_of(it.blk0 + 1) : -1;
+      for (int j = 0; j < it.blocks; j++, vb++) {
+        const int blk = it.blk0 + j, buf = vb & 1;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
+        // tokens that no row sees: zeros, whatever the cache holds there
+        if (blk * KB < it.vlo || (int64_t)(blk + 1) * KB > it.vhi) {
+#pragma unroll
+          for (int r = 0; r < 16; r++) {
+            const int64_t tok = (int64_t)blk * KB + tl * 16 + token_of(r);
+            if (tok < it.vlo || tok >= it.vhi)
+#pragma unroll
+              for (int g = 0; g < GV; g++) cf[r][g] = 0u;
+          }
+        }
+        // Where only some rows see the block, a non-finite coefficient must not meet the zero probability of a row
+        // that does not: it is taken out here and noted for the rows that do.
+        if (blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi) {
+          const int edge = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+#pragma unroll
+            for (int g = 0; g < GV; g++) {
+              const uint32_t m = cf[r][g] & 0x7FFF7FFFu;
+              if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
+                const int pos = tl * 16 + r, grp = (G > CB ? 2 * c : c * G / CB) + g;
+                atomicOr(&my_notes[(edge * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
+                noted[n_item & 3] = 1;
+                cf[r][g] = 0u;
+              }
+            }
+        }
+        if (act) {
+          const uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (tl >> 2) * (D * 128);
+#pragma unroll
+          for (int odd = 0; odd < 2; odd++) {
+            const uint32_t ch = (uint32_t)((((tl & 3) * 2 + odd) ^ g8) << 4);
+#pragma unroll
+            for (int w4 = 0; w4 < 4; w4++) {
+              const int g = GV == 2 ? w4 >> 1 : 0;
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int t = 0; t < 4; t++) {
+                const uint32_t x = (w4 == 0 ? w[t].x : w4 == 1 ? w[t].y : w4 == 2 ? w[t].z : w[t].w) >> (8 * odd);
+                const uint32_t c0 = cf[8 * odd + 2 * t][g], c1 = cf[8 * odd + 2 * t + 1][g];
+                const uint32_t s2 = prmt(c0, c1, 0x5410), b2 = prmt(c0, c1, 0x7632);
+                lo[t] = hfma2(codes_lo(x), s2, b2);
+                hi[t] = hfma2(codes_hi(x), s2, b2);
+              }
+              const int d = 16 * (4 * c + w4) + g8;
+              sts128(dst + d * 128 + ch, lo[0], lo[1], lo[2], lo[3]);
+              sts128(dst + (d + 8) * 128 + ch, hi[0], hi[1], hi[2], hi[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(V_FULL + buf));
+        if (j + 1 < it.blocks) {
+          fetch(blk + 1, pg_next);
+          pg_next = j + 2 < it.blocks ? page_of(blk + 2) : -1;
+        }
+      }
+      if (!ok) break;
+      release();
+    }
+  } else if (warp >= DQ_WARP0) {
+    // ------------------------------------------------------------ keys
+    constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
+    constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
+    constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
+    const int w4 = warp - DQ_WARP0, t = lane & 3;
+    Phase ke[2];
+    ke[0].v = ke[1].v = 1;
+    int kb = 0;
+    bool ok = true;
+    while (const Item *ip = next_item()) {
+      const Item &it = *ip;
+      const int32_t *tab = a.table + it.b * a.max_blocks;
+      uint32_t w[PW][WC], cf[PW][GK];
+      int pid[PW];
+      auto pages = [&](int blk) {
+#pragma unroll
+        for (int i = 0; i < PW; i++) {
+          const int64_t tok = (int64_t)blk * KB + ((i * 4 + w4) / (2 * NC)) * 16;
+          pid[i] = tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+        }
+      };
+      uint32_t valid = 0;                                    // tiles of the block with a page, as far as this warp has them
+      auto fetch = [&](int blk) {
+        valid = 0;
+#pragma unroll
+        for (int i = 0; i < PW; i++) {
+          const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+          const bool there = pid[i] >= 0 && pid[i] < p.g.pages;
+          if (there) {
+            const int tok = blk * KB + tl * 16;
+            const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pid[i] * hkv + it.kvh) * p.g.head_bytes +
+                               ((tok & (p.g.page - 1)) >> 4) * TILE;
+            valid |= 1u << tl;
+            if constexpr (WC == 4) {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
+              w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
+              w[i][0] = v.x, w[i][1] = v.y;
+            }
+            const uint8_t *cp = s + 16 * D + (row * G + c * GK) * 4;
+            if constexpr (GK == 1) {
+              cf[i][0] = __ldg(reinterpret_cast<const uint32_t *>(cp));
+            } else if constexpr (GK == 2) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp));
+              cf[i][0] = v.x, cf[i][1] = v.y;
+            } else {
+              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(cp));
+              cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < WC; j++) w[i][j] = 0u;
+#pragma unroll
+            for (int j = 0; j < GK; j++) cf[i][j] = 0u;
+          }
+        }
+      };
+      if (it.blocks > 0) {
+        pages(it.blk0);
+        fetch(it.blk0);
+        if (it.blocks > 1) pages(it.blk0 + 1);
+      }
+      for (int j = 0; j < it.blocks; j++, kb++) {
+        const int blk = it.blk0 + j, buf = kb & 1;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar(K_EMPTY + buf), ke[buf].next(), ctl))) { ok = false; break; }
+        const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
+#pragma unroll
+        for (int i = 0; i < PW; i++) {
+          const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+          const int pos = tl * 16 + row;
+#pragma unroll
+          for (int k = 0; k < WC; k++) {
+            const uint32_t cc = cf[i][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
+            const uint32_t x = w[i][k], y = x >> 8;
+            // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
+            const uint32_t e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
+            const uint32_t e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+            const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
+            sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
+                   prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+          }
+        }
+        if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
+        fence_proxy_async_smem();
+        mbar_arrive(bar(K_FULL + buf));
+        if (j + 1 < it.blocks) {
+          fetch(blk + 1);
+          if (j + 2 < it.blocks) pages(blk + 2);
+        }
+      }
+      if (!ok) break;
+      release();
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int x = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16), o_tm = tm + 256 + x * D;
+    const float NINF = __int_as_float(0xFF800000);
+    uint32_t s_base[2] = {0, 0};                   // score tiles finished in either buffer before this item
+    int pv_base = 0, blk_base = 0, n_item = 0;     // this tile's PV products, the blocks and the items before this item
+    bool ok = true;
+    for (; const Item *ip = next_item(); n_item++) {
+      const Item &it = *ip;
+      auto leave = [&]() {
+        s_base[0] += it.tiles == 2 ? it.blocks : (it.blocks + 1) >> 1;
+        s_base[1] += it.tiles == 2 ? it.blocks : it.blocks >> 1;
+        blk_base += it.blocks;
+        release();
+      };
+      if (x >= it.tiles) {
+        leave();
+        continue;
+      }
+      const int r = it.r0 + x * QROWS + row, qi = r / p.ratio, hq = r - qi * p.ratio;
+      const bool real = x * QROWS + row < it.rows;
+      // ---------------------------------------------------------- q: binary16, the row's largest element in [2^14, 2^15)
+      float c = 0.0f;
+      const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(it.cu0 + qi) * a.q_token +
+                                                         (int64_t)(it.kvh * p.ratio + hq) * a.q_head);
+      if (it.blocks > 0) {
+        uint32_t mx = 0;
+#pragma unroll 1
+        for (int h = 0; h < D / 8; h += 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = real ? __ldg(src + h + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)),
+                          __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+        }
+        mx = max(mx & 0xFFFFu, mx >> 16);                    // bfloat16 bits of the largest |element|
+        const int ex = mx == 0u || mx >= 0x7F80u ? 0 : min(126, 14 - ((int)(mx >> 7) - 127));
+        const float f = __int_as_float((ex + 127) << 23);
+        c = ldexpf(a.scale * 1.44269504088896340736f, -ex);
+        const uint32_t dst = sb + x * C::Q_BYTES + row * 128;
+#pragma unroll 4
+        for (int h = 0; h < D / 8; h++) {
+          const uint4 v = real ? __ldg(src + h) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) o[i] = pack_f16(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xFFFF0000u) * f);
+          sts128(dst + (h >> 3) * (QROWS * 128) + (((h & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(Q_FULL + x));
+      }
+      const int64_t pos = (int64_t)it.base + qi;
+      const int khi = real ? (int)max((int64_t)0, min(pos + 1, (int64_t)it.hi)) : 0;
+      const int klo = a.window > 0 ? (int)max((int64_t)0, min(pos + 1 - a.window, (int64_t)it.hi)) : 0;
+      float m = NINF, l = 0.0f;                              // reference maximum (log2 units), sum
+      for (int k = 0; k < it.blocks; k++) {
+        const int buf = it.tiles == 2 ? x : k & 1, t0 = (it.blk0 + k) * KB;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar(S_FULL + buf), (s_base[buf] + (it.tiles == 2 ? k : k >> 1)) & 1, ctl))) { ok = false; break; }
+        tc_fence_after();
+        const uint4 kv = kvalid[(blk_base + k) & 3];
+        const uint32_t pages = kv.x | kv.y | kv.z | kv.w;
+        const bool full = __all_sync(0xffffffffu, !real || (klo <= t0 && khi >= t0 + KB)) && pages == (1u << (KB / 16)) - 1;
+        const uint32_t s_tm = tm + buf * 128;
+        // a column's score, or -inf where the row does not see its token
+        auto mask = [&](uint32_t (&v)[16], int ch) {
+          const bool page = (pages >> ch) & 1u;
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int tok = t0 + ch * 16 + token_of(i);
+            if (tok < klo || tok >= khi || !page) v[i] = 0xFF800000u;
+          }
+        };
+        float mx = NINF;
+        {
+          uint32_t v[2][16];
+          tmem_ld_32x32b_x16(s_tm, v[0]);
+#pragma unroll
+          for (int ch = 0; ch < KB / 16; ch++) {
+            tmem_ld_wait();
+            if (ch + 1 < KB / 16) tmem_ld_32x32b_x16(s_tm + 16 * (ch + 1), v[(ch + 1) & 1]);
+            if (!full) mask(v[ch & 1], ch);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              mx = fmaxf(fmaxf(mx, __uint_as_float(v[ch & 1][i])), __uint_as_float(v[ch & 1][i + 1]));
+          }
+        }
+        mx *= c;
+        const bool grow = mx > m + (k == 0 ? 0.0f : GROW) || (m == NINF && mx > NINF);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? mx : m, f = mn == m ? 1.0f : ex2(m - mn);
+          m = mn;
+          l *= f;
+          if (k > 0) {
+            if (!__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int ch = 0; ch < D / 16; ch++) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(o_tm + 16 * ch, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+              tmem_st_x16(o_tm + 16 * ch, v);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float mu = m == NINF ? 0.0f : m;
+        float l2[2] = {0.0f, 0.0f};
+        {
+          uint32_t v[2][16];
+          tmem_ld_32x32b_x16(s_tm, v[0]);
+#pragma unroll
+          for (int ch = 0; ch < KB / 16; ch++) {
+            tmem_ld_wait();
+            if (ch + 1 < KB / 16) tmem_ld_32x32b_x16(s_tm + 16 * (ch + 1), v[(ch + 1) & 1]);
+            if (!full) mask(v[ch & 1], ch);
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const float p0 = ex2(fmaf(__uint_as_float(v[ch & 1][2 * i]), c, -mu));
+              const float p1 = ex2(fmaf(__uint_as_float(v[ch & 1][2 * i + 1]), c, -mu));
+              l2[0] += p0;
+              l2[1] += p1;
+              o[i] = pack_f16(p0, p1);
+            }
+            // P's columns 8 ch .. lie over score columns that have been read
+            tmem_st_x8(s_tm + 8 * ch, o);
+          }
+        }
+        l += l2[0] + l2[1];
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(P_FULL + buf));
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- output
+      if (it.blocks > 0) {
+        if (!__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + it.blocks - 1) & 1, ctl))) { ok = false; break; }
+        tc_fence_after();
+        pv_base += it.blocks;
+      }
+      // groups that a noted (non-finite) value makes NaN
+      uint32_t nan_groups = 0;
+      if (it.blocks > 0 && noted[n_item & 3]) {
+        const uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
+        for (int e = 0; e < C::EDGES; e++) {
+          const int blk = e < 4 ? it.blk0 + e : it.fhi / KB + e - 4;
+          for (int ps = 0; ps < KB; ps++) {
+            const int tok = blk * KB + (ps & ~15) + token_of(ps & 15);
+            if (tok >= klo && tok < khi)
+              for (int g = 0; g < G; g++)
+                if ((my_notes[(e * G + g) * (KB / 32) + (ps >> 5)] >> (ps & 31)) & 1u) nan_groups |= 1u << g;
+          }
+        }
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)(it.cu0 + qi) * a.heads + it.kvh * p.ratio + hq) * D;
+#pragma unroll 1
+      for (int ch = 0; ch < D / 16; ch++) {
+        uint32_t v[16];
+        if (it.blocks > 0) {
+          __syncwarp();
+          tmem_ld_32x32b_x16(o_tm + 16 * ch, v);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i++) v[i] = 0u;
+        }
+        if (real) {
+          const bool bad = (nan_groups >> (16 * ch / (D / G))) & 1u;
+          uint32_t o[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            float y0 = __uint_as_float(v[2 * i]) * inv, y1 = __uint_as_float(v[2 * i + 1]) * inv;
+            if (bad) y0 = y1 = __int_as_float(0x7FC00000);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+            o[i] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          *reinterpret_cast<uint4 *>(out + 16 * ch) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(out + 16 * ch + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+      tc_fence_before();
+      leave();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int G>
+cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
+  using C = Cfg<D, G>;
+  Params p{};
+  p.a = a;
+  p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
+  p.ratio = (int)(a.heads / a.kv_heads);
+  auto kern = prefill_kernel<D, G>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // never more CTAs than items
+  const int64_t items = (a.tokens * p.ratio / (C::NQ * QROWS) + (a.tokens < a.B ? a.tokens : a.B)) * a.kv_heads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(items < kv_max_ctas(1) ? items : kv_max_ctas(1)));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_prefill(const KvAttendArgs &a, cudaStream_t s) {
+  const int D = (int)a.head_dim, G = D / a.group;
+  if (D == 64) return G == 1 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);
+  if (D == 128) return G == 1 ? launch<128, 1>(a, s) : G == 2 ? launch<128, 2>(a, s) : launch<128, 4>(a, s);
+  if (D == 256) return G == 2 ? launch<256, 2>(a, s) : G == 4 ? launch<256, 4>(a, s) : launch<256, 8>(a, s);
+  return cudaErrorNotSupported;
+}
+
+cudaError_t read_clear_kv_status(int *status, cudaStream_t s) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbolAsync(&v, g_kv_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  if (v != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbolAsync(g_kv_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+    e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) return e;
+  }
+  *status = v;
+  return cudaSuccess;
+}
+
+}  // namespace qmm
