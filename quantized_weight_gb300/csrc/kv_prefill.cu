@@ -55,7 +55,7 @@ constexpr int DQ_WARP0 = 8, MMA_WARP = 16, ITEM_WARP = 17;
 constexpr int THREADS = 32 * 20;                 // five warpgroups, the last one's last two warps without work
 // Registers a thread by warpgroup, out of the launch's.
 constexpr int REG_LAUNCH = 96;                   // 64 K / 640 threads, in steps of 8 a warp and scheduler
-constexpr int REG_SOFT = 112, REG_KEYS = 88, REG_VALUES = 104, REG_REST = 64;
+constexpr int REG_SOFT = 128, REG_KEYS = 72, REG_VALUES = 96, REG_REST = 56;
 static_assert(2 * REG_SOFT + REG_KEYS + REG_VALUES + REG_REST <= 5 * REG_LAUNCH, "more registers than the launch has");
 constexpr int ITEM_SLOTS = 3;
 constexpr float GROW = 8.0f;                     // log2 by which scores may exceed the reference maximum
@@ -116,10 +116,15 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -395,17 +400,17 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       };
       uint4 w[4];
       uint32_t cf[16][GV];
-      bool there = false;
+      const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
       auto fetch = [&](int blk, int pg) {
-        there = pg >= 0 && pg < p.g.pages;
-        if (there) {
+        coefs = nullptr;
+        if (pg >= 0 && pg < p.g.pages) {
           const int64_t tok = (int64_t)blk * KB + tl * 16;
           const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
                              (((int)tok & (p.g.page - 1)) >> 4) * TILE;
           const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (c * 8 + g8) * 64);
 #pragma unroll
           for (int i = 0; i < 4; i++) w[i] = __ldg(s + i);
-          const uint8_t *cp = t + 16 * D + 64 * G + (G > CB ? 2 * c : c * G / CB) * 4;
+          const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * c : c * G / CB) * 4;
 #pragma unroll
           for (int r = 0; r < 16; r++) {
             if constexpr (GV == 1) {
@@ -429,53 +434,70 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       for (int j = 0; j < it.blocks; j++, vb++) {
         const int blk = it.blk0 + j, buf = vb & 1;
         if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
-        // tokens that no row sees: zeros, whatever the cache holds there
-        if (blk * KB < it.vlo || (int64_t)(blk + 1) * KB > it.vhi) {
-#pragma unroll
+        // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
+        // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
+        // noted for the rows that do.
+        const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
+        if (edge) {
+          uint32_t out[GV] = {};                             // rows to zero, by group
+          const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
+#pragma unroll 1
           for (int r = 0; r < 16; r++) {
             const int64_t tok = (int64_t)blk * KB + tl * 16 + token_of(r);
-            if (tok < it.vlo || tok >= it.vhi)
 #pragma unroll
-              for (int g = 0; g < GV; g++) cf[r][g] = 0u;
+            for (int g = 0; g < GV; g++) {
+              if (tok < it.vlo || tok >= it.vhi) {
+                out[g] |= 1u << r;
+              } else if (coefs) {
+                const uint32_t m = __ldg(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
+                if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
+                  const int pos = tl * 16 + r, grp = (G > CB ? 2 * c : c * G / CB) + g;
+                  atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
+                  noted[n_item & 3] = 1;
+                  out[g] |= 1u << r;
+                }
+              }
+            }
           }
-        }
-        // Where only some rows see the block, a non-finite coefficient must not meet the zero probability of a row
-        // that does not: it is taken out here and noted for the rows that do.
-        if (blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi) {
-          const int edge = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
 #pragma unroll
           for (int r = 0; r < 16; r++)
 #pragma unroll
-            for (int g = 0; g < GV; g++) {
-              const uint32_t m = cf[r][g] & 0x7FFF7FFFu;
-              if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
-                const int pos = tl * 16 + r, grp = (G > CB ? 2 * c : c * G / CB) + g;
-                atomicOr(&my_notes[(edge * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
-                noted[n_item & 3] = 1;
-                cf[r][g] = 0u;
-              }
-            }
+            for (int g = 0; g < GV; g++)
+              if ((out[g] >> r) & 1u) cf[r][g] = 0u;
         }
         if (act) {
-          const uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (tl >> 2) * (D * 128);
+          uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
 #pragma unroll
-          for (int odd = 0; odd < 2; odd++) {
-            const uint32_t ch = (uint32_t)((((tl & 3) * 2 + odd) ^ g8) << 4);
+          for (int r = 0; r < 8; r++)
 #pragma unroll
-            for (int w4 = 0; w4 < 4; w4++) {
-              const int g = GV == 2 ? w4 >> 1 : 0;
+            for (int g = 0; g < GV; g++) {
+              s2[g * 8 + r] = prmt(cf[2 * r][g], cf[2 * r + 1][g], 0x5410);
+              b2[g * 8 + r] = prmt(cf[2 * r][g], cf[2 * r + 1][g], 0x7632);
+            }
+          uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (tl >> 2) * (D * 128) + (64 * c + g8) * 128;
+          const uint32_t ch0 = (uint32_t)((((tl & 3) * 2) ^ g8) << 4), ch1 = (uint32_t)((((tl & 3) * 2 + 1) ^ g8) << 4);
+          // a word of each token quad at a time; the words move up in their registers, so that the loop stays rolled
+          // (unrolled, the five roles' code does not stay in the instruction caches)
+#pragma unroll 1
+          for (int w4 = 0; w4 < 4; w4++, dst += 16 * 128) {
+#pragma unroll
+            for (int odd = 0; odd < 2; odd++) {
               uint32_t lo[4], hi[4];
 #pragma unroll
               for (int t = 0; t < 4; t++) {
-                const uint32_t x = (w4 == 0 ? w[t].x : w4 == 1 ? w[t].y : w4 == 2 ? w[t].z : w[t].w) >> (8 * odd);
-                const uint32_t c0 = cf[8 * odd + 2 * t][g], c1 = cf[8 * odd + 2 * t + 1][g];
-                const uint32_t s2 = prmt(c0, c1, 0x5410), b2 = prmt(c0, c1, 0x7632);
-                lo[t] = hfma2(codes_lo(x), s2, b2);
-                hi[t] = hfma2(codes_hi(x), s2, b2);
+                const uint32_t y = w[t].x >> (8 * odd);
+                lo[t] = hfma2(codes_lo(y), s2[4 * odd + t], b2[4 * odd + t]);
+                hi[t] = hfma2(codes_hi(y), s2[4 * odd + t], b2[4 * odd + t]);
               }
-              const int d = 16 * (4 * c + w4) + g8;
-              sts128(dst + d * 128 + ch, lo[0], lo[1], lo[2], lo[3]);
-              sts128(dst + (d + 8) * 128 + ch, hi[0], hi[1], hi[2], hi[3]);
+              sts128(dst + (odd ? ch1 : ch0), lo[0], lo[1], lo[2], lo[3]);
+              sts128(dst + 8 * 128 + (odd ? ch1 : ch0), hi[0], hi[1], hi[2], hi[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; t++) w[t].x = w[t].y, w[t].y = w[t].z, w[t].z = w[t].w;
+            if constexpr (GV == 2) {
+              if (w4 == 1)                                     // the second group's coefficients
+#pragma unroll
+                for (int r = 0; r < 8; r++) s2[r] = s2[8 * (GV - 1) + r], b2[r] = b2[8 * (GV - 1) + r];
             }
           }
         }
@@ -557,20 +579,27 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         const int blk = it.blk0 + j, buf = kb & 1;
         if (!__all_sync(0xffffffffu, wait_bounded(bar(K_EMPTY + buf), ke[buf].next(), ctl))) { ok = false; break; }
         const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
-#pragma unroll
-        for (int i = 0; i < PW; i++) {
+#pragma unroll 1
+        for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
           const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
           const int pos = tl * 16 + row;
 #pragma unroll
           for (int k = 0; k < WC; k++) {
-            const uint32_t cc = cf[i][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
-            const uint32_t x = w[i][k], y = x >> 8;
+            const uint32_t cc = cf[0][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
+            const uint32_t x = w[0][k], y = x >> 8;
             // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
             const uint32_t e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
             const uint32_t e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
             const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
             sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
                    prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+          }
+#pragma unroll
+          for (int n = 0; n + 1 < PW; n++) {
+#pragma unroll
+            for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
+#pragma unroll
+            for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
           }
         }
         if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
@@ -651,28 +680,35 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         const uint32_t pages = kv.x | kv.y | kv.z | kv.w;
         const bool full = __all_sync(0xffffffffu, !real || (klo <= t0 && khi >= t0 + KB)) && pages == (1u << (KB / 16)) - 1;
         const uint32_t s_tm = tm + buf * 128;
-        // a column's score, or -inf where the row does not see its token
-        auto mask = [&](uint32_t (&v)[16], int ch) {
-          const bool page = (pages >> ch) & 1u;
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int tok = t0 + ch * 16 + token_of(i);
-            if (tok < klo || tok >= khi || !page) v[i] = 0xFF800000u;
-          }
-        };
-        float mx = NINF;
-        {
-          uint32_t v[2][16];
-          tmem_ld_32x32b_x16(s_tm, v[0]);
-#pragma unroll
+        // Scores of tokens that the row does not see become -inf, in a pass of their own: few blocks have any.
+        if (!full) {
+#pragma unroll 1
           for (int ch = 0; ch < KB / 16; ch++) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(s_tm + 16 * ch, v);
             tmem_ld_wait();
-            if (ch + 1 < KB / 16) tmem_ld_32x32b_x16(s_tm + 16 * (ch + 1), v[(ch + 1) & 1]);
-            if (!full) mask(v[ch & 1], ch);
+            const int t1 = (pages >> ch) & 1u ? t0 + 16 * ch : 0x40000000;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              mx = fmaxf(fmaxf(mx, __uint_as_float(v[ch & 1][i])), __uint_as_float(v[ch & 1][i + 1]));
+            for (int i = 0; i < 16; i++)
+              if (t1 + token_of(i) < klo || t1 + token_of(i) >= khi) v[i] = 0xFF800000u;
+            tmem_st_x16(s_tm + 16 * ch, v);
           }
+          tmem_st_wait();
+        }
+        float mx = NINF;
+#pragma unroll 1
+        for (int h = 0; h < KB; h += 64) {
+          uint32_t v[2][32];
+          tmem_ld_32x32b_x32(s_tm + h, v[0]);
+          tmem_ld_32x32b_x32(s_tm + h + 32, v[1]);
+          tmem_ld_wait();
+          float m4[4] = {mx, NINF, NINF, NINF};
+#pragma unroll
+          for (int i = 0; i < 64; i += 8)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              m4[j] = fmaxf(fmaxf(m4[j], __uint_as_float(v[i >> 5][(i & 31) + 2 * j])), __uint_as_float(v[i >> 5][(i & 31) + 2 * j + 1]));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
         mx *= c;
         const bool grow = mx > m + (k == 0 ? 0.0f : GROW) || (m == NINF && mx > NINF);
@@ -696,31 +732,33 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
         }
         const float mu = m == NINF ? 0.0f : m;
-        float l2[2] = {0.0f, 0.0f};
-        {
-          uint32_t v[2][16];
-          tmem_ld_32x32b_x16(s_tm, v[0]);
+        const f2 c2 = f2_make(c, c), mu2 = f2_make(-mu, -mu);
+        f2 l2[2] = {f2_zero(), f2_zero()};
+#pragma unroll 1
+        for (int h = 0; h < KB; h += 64) {
+          uint32_t v[2][32], o[32];
+          tmem_ld_32x32b_x32(s_tm + h, v[0]);
+          tmem_ld_32x32b_x32(s_tm + h + 32, v[1]);
+          tmem_ld_wait();
 #pragma unroll
-          for (int ch = 0; ch < KB / 16; ch++) {
-            tmem_ld_wait();
-            if (ch + 1 < KB / 16) tmem_ld_32x32b_x16(s_tm + 16 * (ch + 1), v[(ch + 1) & 1]);
-            if (!full) mask(v[ch & 1], ch);
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const float p0 = ex2(fmaf(__uint_as_float(v[ch & 1][2 * i]), c, -mu));
-              const float p1 = ex2(fmaf(__uint_as_float(v[ch & 1][2 * i + 1]), c, -mu));
-              l2[0] += p0;
-              l2[1] += p1;
-              o[i] = pack_f16(p0, p1);
-            }
-            // P's columns 8 ch .. lie over score columns that have been read
-            tmem_st_x8(s_tm + 8 * ch, o);
+          for (int i = 0; i < 32; i++) {
+            float e0, e1;
+            f2_split(f2_fma(f2_bits(v[i >> 4][2 * (i & 15)], v[i >> 4][2 * (i & 15) + 1]), c2, mu2), e0, e1);
+            e0 = ex2(e0), e1 = ex2(e1);
+            l2[i & 1] = f2_add(l2[i & 1], f2_make(e0, e1));
+            o[i] = pack_f16(e0, e1);
           }
+          tmem_st_x32(s_tm + h / 2, o);              // over score columns that have been read
         }
-        l += l2[0] + l2[1];
+        float la, lb;
+        f2_split(f2_add(l2[0], l2[1]), la, lb);
+        l += la + lb;
         tmem_st_wait();
         tc_fence_before();
+        // A parity tells apart only a phase and the next, so no PV may finish before the one ahead of it has been seen: with
+        // two row tiles, S of this step came after that PV; with one, it is waited for here, before the next is let go.
+        if (it.tiles == 1 && k > 0 &&
+            !__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) { ok = false; break; }
         mbar_arrive(bar(P_FULL + buf));
       }
       if (!ok) break;
