@@ -91,7 +91,7 @@ struct Cfg {
 
 // barriers (8 bytes each)
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, K_FULL = 8, K_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, IT_FULL = 16,
-       IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, BARS };
+       IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, BARS };
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -114,16 +114,6 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -176,6 +166,35 @@ __device__ __forceinline__ void set_registers() {
   if constexpr (N < REG_LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// One warp, the seldom path of the softmax: this lane's row of O (unless o_tm is all ones) and of the first `cols`
+// columns of P (two binary16 values each) times f.  Not inlined, so that it takes no registers from the path that is run.
+template <int D>
+__device__ __noinline__ void rescale(uint32_t o_tm, uint32_t p_tm, int cols, float f) {
+  tc_fence_after();
+  if (o_tm != 0xFFFFFFFFu)
+    for (int ch = 0; ch < D; ch += 16) {
+      uint32_t w[16];
+      tmem_ld_32x32b_x16(o_tm + ch, w);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; i++) w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+      tmem_st_x16(o_tm + ch, w);
+    }
+  tmem_st_wait();
+  const __half2 f16 = __float2half2_rn(f);
+  for (int ch = 0; ch < cols; ch += 16) {
+    uint32_t w[16];
+    tmem_ld_32x32b_x16(p_tm + ch, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&w[i]), f16);
+      w[i] = *reinterpret_cast<const uint32_t *>(&y);
+    }
+    tmem_st_x16(p_tm + ch, w);
+  }
+}
+
 template <int D, int G>
 __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D, G>;
@@ -214,6 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       mbar_init(bar(V_EMPTY + i), 1);
     }
     mbar_init(bar(DRAIN), 1);
+    mbar_init(bar(IT_NEXT), 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -250,8 +270,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     unsigned *ticket = static_cast<unsigned *>(a.workspace) + (kKvMaxCtas - 1), *done = ticket - 1;
     int cb = 0;                               // requests before cb are behind this CTA's tickets
     int64_t cfirst = 0;                       // items before request cb
-    uint32_t ph = 1;
+    uint32_t ph = 1, next = 1;
     for (int slot = 0;;) {
+      // A ticket is drawn when the keys of the item before it are done: earlier, CTAs would sit on items that others could begin.
+      if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_NEXT), next, ctl))) break;
+      next ^= 1u;
       unsigned t = 0;
       if (lane == 0) t = atomicAdd(ticket, 1u);
       t = __shfl_sync(0xffffffffu, t, 0);
@@ -321,6 +344,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     constexpr uint32_t id_s = idesc_f16(QROWS, KB), id_o = idesc_f16(QROWS, D);
     Phase kf[2], vf[2], pf[2], qf[2];
     int kb = 0, vb = 0;                       // blocks begun, over all items
+    // Descriptors differ in the start address alone (the low word, in 16-byte units).
+    const uint64_t first = smem_desc_sw128(sb);
+    const uint32_t desc0 = (uint32_t)first, desc_hi = (uint32_t)(first >> 32);
+    auto desc = [&](uint32_t lo) { return (uint64_t)desc_hi << 32 | lo; };
     bool ok = true;
     while (const Item *ip = next_item()) {
       const Item &it = *ip;
@@ -336,13 +363,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             kb++;
           }
           tc_fence_after();
-          const uint32_t kbuf = sb + C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES, qbuf = sb + x * C::Q_BYTES;
+          const uint32_t kd = desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4), qd = desc0 + (x * C::Q_BYTES >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; kk++) {
-            const uint64_t ad = smem_desc_sw128(qbuf + (kk / 4) * (QROWS * 128)) + 2 * (kk % 4);
-            const uint64_t bd = smem_desc_sw128(kbuf + (kk / 4) * (KB * 128)) + 2 * (kk % 4);
-            umma_f16_ss(tmem + buf * 128, ad, bd, id_s, kk != 0);
-          }
+          for (int kk = 0; kk < D / 16; kk++)          // 64 elements a column of 128-byte rows, 16 a product
+            umma_f16_ss(tmem + buf * 128, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
+                        desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
           umma_commit(bar(S_FULL + buf));
           if (x == nt - 1) umma_commit(bar(K_EMPTY + ((kb - 1) & 1)));
           return true;
@@ -357,12 +382,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
           if (!wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t vbuf = sb + C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES;
+          const uint32_t vd = desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < KB / 16; kk++) {
-            const uint64_t bd = smem_desc_sw128(vbuf + (kk / 4) * (D * 128)) + 2 * (kk % 4);
-            umma_f16_ts(tmem + 256 + x * D, tmem + buf * 128 + 8 * kk, bd, id_o, (j | kk) != 0);
-          }
+          for (int kk = 0; kk < KB / 16; kk++)
+            umma_f16_ts(tmem + 256 + x * D, tmem + buf * 128 + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
+                        (j | kk) != 0);
           umma_commit(bar(PV_DONE + x));
           if (x == nt - 1) umma_commit(bar(V_EMPTY + ((vb - 1) & 1)));
           if (i + 2 < N) ok = scores(i + 2);
@@ -611,6 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
       }
       if (!ok) break;
+      if (lane == 0) mbar_arrive(bar(IT_NEXT));
       release();
     }
   } else {
@@ -695,64 +720,56 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
           tmem_st_wait();
         }
-        float mx = NINF;
-#pragma unroll 1
-        for (int h = 0; h < KB; h += 64) {
-          uint32_t v[2][32];
-          tmem_ld_32x32b_x32(s_tm + h, v[0]);
-          tmem_ld_32x32b_x32(s_tm + h + 32, v[1]);
-          tmem_ld_wait();
-          float m4[4] = {mx, NINF, NINF, NINF};
+        // 32 columns at a time, read once (reading scores is what the softmax waits for), the next 32 on their way
+        // during the exponentials: their maximum, then, with the reference, their exponentials.  Only where the maximum has outgrown the reference
+        // is what was summed before rescaled: l, O and the block's P so far.
+        const f2 c2 = f2_make(c, c);
+        auto columns = [&](const uint32_t (&v)[32], uint32_t (&ahead)[32], int h) {
+          float m4[4] = {NINF, NINF, NINF, NINF};
 #pragma unroll
-          for (int i = 0; i < 64; i += 8)
+          for (int i = 0; i < 32; i += 8)
 #pragma unroll
             for (int j = 0; j < 4; j++)
-              m4[j] = fmaxf(fmaxf(m4[j], __uint_as_float(v[i >> 5][(i & 31) + 2 * j])), __uint_as_float(v[i >> 5][(i & 31) + 2 * j + 1]));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        }
-        mx *= c;
-        const bool grow = mx > m + (k == 0 ? 0.0f : GROW) || (m == NINF && mx > NINF);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? mx : m, f = mn == m ? 1.0f : ex2(m - mn);
-          m = mn;
-          l *= f;
-          if (k > 0) {
-            if (!__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) { ok = false; break; }
-            tc_fence_after();
-#pragma unroll 1
-            for (int ch = 0; ch < D / 16; ch++) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(o_tm + 16 * ch, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 16; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              tmem_st_x16(o_tm + 16 * ch, v);
-            }
-            tmem_st_wait();
+              m4[j] = fmaxf(fmaxf(m4[j], __uint_as_float(v[i + 2 * j])), __uint_as_float(v[i + 2 * j + 1]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+          const bool grow = mx > m + GROW || (m == NINF && mx > NINF);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? mx : m, f = mn == m ? 1.0f : ex2(m - mn);
+            m = mn;
+            l *= f;
+            if (k > 0 && !__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) ok = false;
+            rescale<D>(k > 0 ? o_tm : 0xFFFFFFFFu, s_tm, h / 2, f);
           }
-        }
-        const float mu = m == NINF ? 0.0f : m;
-        const f2 c2 = f2_make(c, c), mu2 = f2_make(-mu, -mu);
-        f2 l2[2] = {f2_zero(), f2_zero()};
-#pragma unroll 1
-        for (int h = 0; h < KB; h += 64) {
-          uint32_t v[2][32], o[32];
-          tmem_ld_32x32b_x32(s_tm + h, v[0]);
-          tmem_ld_32x32b_x32(s_tm + h + 32, v[1]);
-          tmem_ld_wait();
+          if (h + 32 < KB) tmem_ld_32x32b_x32(s_tm + h + 32, ahead);   // (never on its way through a call or a loop's end)
+          const float mu = m == NINF ? 0.0f : m;
+          const f2 mu2 = f2_make(-mu, -mu);
+          f2 l2[2] = {f2_zero(), f2_zero()};
+          uint32_t o[16];
 #pragma unroll
-          for (int i = 0; i < 32; i++) {
+          for (int i = 0; i < 16; i++) {
             float e0, e1;
-            f2_split(f2_fma(f2_bits(v[i >> 4][2 * (i & 15)], v[i >> 4][2 * (i & 15) + 1]), c2, mu2), e0, e1);
+            f2_split(f2_fma(f2_bits(v[2 * i], v[2 * i + 1]), c2, mu2), e0, e1);
             e0 = ex2(e0), e1 = ex2(e1);
             l2[i & 1] = f2_add(l2[i & 1], f2_make(e0, e1));
             o[i] = pack_f16(e0, e1);
           }
-          tmem_st_x32(s_tm + h / 2, o);              // over score columns that have been read
+          tmem_st_x16(s_tm + h / 2, o);                // over score columns that have been read
+          float la, lb;
+          f2_split(f2_add(l2[0], l2[1]), la, lb);
+          l += la + lb;
+        };
+        {
+          uint32_t va[32], vb[32];
+          tmem_ld_32x32b_x32(s_tm, va);
+#pragma unroll
+          for (int h = 0; h < KB; h += 64) {
+            tmem_ld_wait();
+            columns(va, vb, h);
+            tmem_ld_wait();
+            columns(vb, va, h + 32);
+          }
         }
-        float la, lb;
-        f2_split(f2_add(l2[0], l2[1]), la, lb);
-        l += la + lb;
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         // A parity tells apart only a phase and the next, so no PV may finish before the one ahead of it has been seen: with
