@@ -7,14 +7,13 @@
 //
 //   S = Q K^T (TMEM) -> P = exp2(c S - m), binary16, over S (TMEM) -> O += P V (TMEM)
 //
-// Roles of the persistent CTA, one an SM (20 warps):
+// Roles of the persistent CTA, one an SM (16 warps):
 //   warps 0-3, 4-7   softmax of row tile 0 and 1, a row a thread: maximum,
 //                    exponentials, P, O's rescaling, and the tile's q and output
-//   warps 8-11       keys: 4-bit codes from the cache to binary16 in shared memory
-//   warps 12-15      values, the same, transposed
-//   warp 16          TMEM and the single-thread MMA issue
-//   warp 17          items, from a ticket counter (longest first within a request)
-//   warps 18-19      none
+//   warps 8-11       4-bit codes from the cache to binary16 in shared memory: keys, and values transposed
+//   warp 12          TMEM and the single-thread MMA issue
+//   warp 13          items, from a ticket counter (longest first within a request)
+//   warps 14-15      none
 // The two row tiles alternate: while one tile's softmax runs, the tensor core
 // has the other's products.  With one row tile (heads of 256, or the rest of a request) the
 // blocks alternate instead, between the same two score buffers.  Step i of an item uses score
@@ -51,12 +50,10 @@ namespace {
 using namespace sm100;
 
 constexpr int QROWS = 128;                       // rows of a q tile (MMA M)
-constexpr int DQ_WARP0 = 8, MMA_WARP = 16, ITEM_WARP = 17;
-constexpr int THREADS = 32 * 20;                 // five warpgroups, the last one's last two warps without work
-// Registers a thread by warpgroup, out of the launch's.
-constexpr int REG_LAUNCH = 96;                   // 64 K / 640 threads, in steps of 8 a warp and scheduler
-constexpr int REG_SOFT = 128, REG_KEYS = 72, REG_VALUES = 96, REG_REST = 56;
-static_assert(2 * REG_SOFT + REG_KEYS + REG_VALUES + REG_REST <= 5 * REG_LAUNCH, "more registers than the launch has");
+constexpr int DQ_WARP0 = 8, MMA_WARP = 12, ITEM_WARP = 13;
+// Four warpgroups (the last one's last two warps without work): 128 registers a thread, which every role fits in.
+// Shared memory leaves the L1 cache a few KB, so that spilled registers would come back from L2.
+constexpr int THREADS = 32 * 16;
 constexpr int ITEM_SLOTS = 3;
 constexpr float GROW = 8.0f;                     // log2 by which scores may exceed the reference maximum
 
@@ -158,14 +155,6 @@ struct Phase {
   }
 };
 
-// A warpgroup's registers a thread, from the launch's to N: .inc only upwards, .dec only downwards.
-template <int N>
-__device__ __forceinline__ void set_registers() {
-  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "setmaxnreg's range");
-  if constexpr (N > REG_LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  if constexpr (N < REG_LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // One warp, the seldom path of the softmax: this lane's row of O (unless o_tm is all ones) and of the first `cols`
 // columns of P (two binary16 values each) times f.  Not inlined, so that it takes no registers from the path that is run.
 template <int D>
@@ -257,11 +246,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     if (lane == 0) mbar_arrive(bar(IT_EMPTY + it_slot));
     if (++it_slot == ITEM_SLOTS) it_slot = 0, it_ph ^= 1u;
   };
-
-  if (warp >= MMA_WARP) set_registers<REG_REST>();
-  else if (warp >= DQ_WARP0 + 4) set_registers<REG_VALUES>();
-  else if (warp >= DQ_WARP0) set_registers<REG_KEYS>();
-  else set_registers<REG_SOFT>();
 
   if (warp > ITEM_WARP) {
     // no work
@@ -399,16 +383,21 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       umma_commit(bar(DRAIN));
       wait_drain(bar(DRAIN), 0);
     }
-  } else if (warp >= DQ_WARP0 + 4) {
-    // ------------------------------------------------------------ values
+  } else if (warp >= DQ_WARP0) {
+    // ------------------------------------------------------------ codes: keys
+    constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
+    constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
+    constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
+    const int w4 = warp - DQ_WARP0, t = lane & 3;
+    // values
     constexpr int CB = D / 64;                               // blocks of 64 elements
     constexpr int GV = G > CB ? 2 : 1;                       // groups in one (group of 32: two)
     constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
-    const int u = threadIdx.x - (DQ_WARP0 + 4) * 32, g8 = u & 7, c = (u >> 3) % CB, tl = (u >> 3) / CB;
+    const int u = threadIdx.x - DQ_WARP0 * 32, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
     const bool act = u < UNITS;
-    Phase ve[2];
-    ve[0].v = ve[1].v = 1;
-    int vb = 0, n_item = 0;
+    Phase ke[2], ve[2];
+    ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
+    int kb = 0, n_item = 0;                                  // blocks and items before
     bool ok = true;
     for (; const Item *ip = next_item(); n_item++) {
       const Item &it = *ip;
@@ -417,136 +406,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
       if (u == 0) noted[n_item & 3] = 0;
       asm volatile("bar.sync 1, 128;" ::: "memory");
-      const int32_t *tab = a.table + it.b * a.max_blocks;
-      auto page_of = [&](int blk) {
-        const int64_t tok = (int64_t)blk * KB + tl * 16;
-        return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
-      };
-      uint4 w[4];
-      uint32_t cf[16][GV];
-      const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
-      auto fetch = [&](int blk, int pg) {
-        coefs = nullptr;
-        if (pg >= 0 && pg < p.g.pages) {
-          const int64_t tok = (int64_t)blk * KB + tl * 16;
-          const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
-                             (((int)tok & (p.g.page - 1)) >> 4) * TILE;
-          const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (c * 8 + g8) * 64);
-#pragma unroll
-          for (int i = 0; i < 4; i++) w[i] = __ldg(s + i);
-          const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * c : c * G / CB) * 4;
-#pragma unroll
-          for (int r = 0; r < 16; r++) {
-            if constexpr (GV == 1) {
-              cf[r][0] = __ldg(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
-            } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp + r * G * 4));
-              cf[r][0] = v.x, cf[r][GV - 1] = v.y;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; i++) w[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int r = 0; r < 16; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++) cf[r][g] = 0u;
-        }
-      };
-      if (it.blocks > 0) fetch(it.blk0, page_of(it.blk0));
-      int pg_next = it.blocks > 1 ? page_of(it.blk0 + 1) : -1;
-      for (int j = 0; j < it.blocks; j++, vb++) {
-        const int blk = it.blk0 + j, buf = vb & 1;
-        if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
-        // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
-        // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
-        // noted for the rows that do.
-        const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
-        if (edge) {
-          uint32_t out[GV] = {};                             // rows to zero, by group
-          const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
-#pragma unroll 1
-          for (int r = 0; r < 16; r++) {
-            const int64_t tok = (int64_t)blk * KB + tl * 16 + token_of(r);
-#pragma unroll
-            for (int g = 0; g < GV; g++) {
-              if (tok < it.vlo || tok >= it.vhi) {
-                out[g] |= 1u << r;
-              } else if (coefs) {
-                const uint32_t m = __ldg(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
-                if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
-                  const int pos = tl * 16 + r, grp = (G > CB ? 2 * c : c * G / CB) + g;
-                  atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
-                  noted[n_item & 3] = 1;
-                  out[g] |= 1u << r;
-                }
-              }
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < 16; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++)
-              if ((out[g] >> r) & 1u) cf[r][g] = 0u;
-        }
-        if (act) {
-          uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
-#pragma unroll
-          for (int r = 0; r < 8; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++) {
-              s2[g * 8 + r] = prmt(cf[2 * r][g], cf[2 * r + 1][g], 0x5410);
-              b2[g * 8 + r] = prmt(cf[2 * r][g], cf[2 * r + 1][g], 0x7632);
-            }
-          uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (tl >> 2) * (D * 128) + (64 * c + g8) * 128;
-          const uint32_t ch0 = (uint32_t)((((tl & 3) * 2) ^ g8) << 4), ch1 = (uint32_t)((((tl & 3) * 2 + 1) ^ g8) << 4);
-          // a word of each token quad at a time; the words move up in their registers, so that the loop stays rolled
-          // (unrolled, the five roles' code does not stay in the instruction caches)
-#pragma unroll 1
-          for (int w4 = 0; w4 < 4; w4++, dst += 16 * 128) {
-#pragma unroll
-            for (int odd = 0; odd < 2; odd++) {
-              uint32_t lo[4], hi[4];
-#pragma unroll
-              for (int t = 0; t < 4; t++) {
-                const uint32_t y = w[t].x >> (8 * odd);
-                lo[t] = hfma2(codes_lo(y), s2[4 * odd + t], b2[4 * odd + t]);
-                hi[t] = hfma2(codes_hi(y), s2[4 * odd + t], b2[4 * odd + t]);
-              }
-              sts128(dst + (odd ? ch1 : ch0), lo[0], lo[1], lo[2], lo[3]);
-              sts128(dst + 8 * 128 + (odd ? ch1 : ch0), hi[0], hi[1], hi[2], hi[3]);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; t++) w[t].x = w[t].y, w[t].y = w[t].z, w[t].z = w[t].w;
-            if constexpr (GV == 2) {
-              if (w4 == 1)                                     // the second group's coefficients
-#pragma unroll
-                for (int r = 0; r < 8; r++) s2[r] = s2[8 * (GV - 1) + r], b2[r] = b2[8 * (GV - 1) + r];
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(V_FULL + buf));
-        if (j + 1 < it.blocks) {
-          fetch(blk + 1, pg_next);
-          pg_next = j + 2 < it.blocks ? page_of(blk + 2) : -1;
-        }
-      }
-      if (!ok) break;
-      release();
-    }
-  } else if (warp >= DQ_WARP0) {
-    // ------------------------------------------------------------ keys
-    constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
-    constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
-    constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
-    const int w4 = warp - DQ_WARP0, t = lane & 3;
-    Phase ke[2];
-    ke[0].v = ke[1].v = 1;
-    int kb = 0;
-    bool ok = true;
-    while (const Item *ip = next_item()) {
-      const Item &it = *ip;
       const int32_t *tab = a.table + it.b * a.max_blocks;
       uint32_t w[PW][WC], cf[PW][GK];
       int pid[PW];
@@ -558,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
       };
       uint32_t valid = 0;                                    // tiles of the block with a page, as far as this warp has them
-      auto fetch = [&](int blk) {
+      auto fetch_keys = [&](int blk) {
         valid = 0;
 #pragma unroll
         for (int i = 0; i < PW; i++) {
@@ -594,44 +453,161 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
         }
       };
+      auto page_of = [&](int blk) {
+        const int64_t tok = (int64_t)blk * KB + vt * 16;
+        return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+      };
+      uint4 vw[4];
+      uint32_t vf[16][GV];
+      const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
+      auto fetch_values = [&](int blk, int pg) {
+        coefs = nullptr;
+        if (pg >= 0 && pg < p.g.pages) {
+          const int64_t tok = (int64_t)blk * KB + vt * 16;
+          const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
+                             (((int)tok & (p.g.page - 1)) >> 4) * TILE;
+          const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (vc * 8 + g8) * 64);
+#pragma unroll
+          for (int i = 0; i < 4; i++) vw[i] = __ldg(s + i);
+          const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * vc : vc * G / CB) * 4;
+#pragma unroll
+          for (int r = 0; r < 16; r++) {
+            if constexpr (GV == 1) {
+              vf[r][0] = __ldg(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp + r * G * 4));
+              vf[r][0] = v.x, vf[r][GV - 1] = v.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; i++) vw[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+#pragma unroll
+            for (int g = 0; g < GV; g++) vf[r][g] = 0u;
+        }
+      };
+      int pg_next = -1;
       if (it.blocks > 0) {
         pages(it.blk0);
-        fetch(it.blk0);
-        if (it.blocks > 1) pages(it.blk0 + 1);
+        pg_next = page_of(it.blk0);
+        fetch_keys(it.blk0);
+        fetch_values(it.blk0, pg_next);
+        if (it.blocks > 1) {
+          pages(it.blk0 + 1);
+          pg_next = page_of(it.blk0 + 1);
+        }
       }
       for (int j = 0; j < it.blocks; j++, kb++) {
         const int blk = it.blk0 + j, buf = kb & 1;
         if (!__all_sync(0xffffffffu, wait_bounded(bar(K_EMPTY + buf), ke[buf].next(), ctl))) { ok = false; break; }
-        const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
+        {
+          const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
 #pragma unroll 1
-        for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
-          const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
-          const int pos = tl * 16 + row;
+          for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
+            const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+            const int pos = tl * 16 + row;
 #pragma unroll
-          for (int k = 0; k < WC; k++) {
-            const uint32_t cc = cf[0][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
-            const uint32_t x = w[0][k], y = x >> 8;
-            // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
-            const uint32_t e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
-            const uint32_t e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
-            const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
-            sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
-                   prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+            for (int k = 0; k < WC; k++) {
+              const uint32_t cc = cf[0][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
+              const uint32_t x = w[0][k], y = x >> 8;
+              // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
+              const uint32_t e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
+              const uint32_t e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+              const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
+              sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
+                     prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+            }
+#pragma unroll
+            for (int n = 0; n + 1 < PW; n++) {
+#pragma unroll
+              for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
+#pragma unroll
+              for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
+            }
           }
-#pragma unroll
-          for (int n = 0; n + 1 < PW; n++) {
-#pragma unroll
-            for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
-#pragma unroll
-            for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
-          }
+          if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
         }
-        if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
         fence_proxy_async_smem();
         mbar_arrive(bar(K_FULL + buf));
         if (j + 1 < it.blocks) {
-          fetch(blk + 1);
+          fetch_keys(blk + 1);
           if (j + 2 < it.blocks) pages(blk + 2);
+        }
+        if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
+        // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
+        // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
+        // noted for the rows that do.
+        const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
+        if (edge) {
+          uint32_t out[GV] = {};                             // rows to zero, by group
+          const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
+#pragma unroll 1
+          for (int r = 0; r < 16; r++) {
+            const int64_t tok = (int64_t)blk * KB + vt * 16 + token_of(r);
+#pragma unroll
+            for (int g = 0; g < GV; g++) {
+              if (tok < it.vlo || tok >= it.vhi) {
+                out[g] |= 1u << r;
+              } else if (coefs) {
+                const uint32_t m = __ldg(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
+                if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
+                  const int pos = vt * 16 + r, grp = (G > CB ? 2 * vc : vc * G / CB) + g;
+                  atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
+                  noted[n_item & 3] = 1;
+                  out[g] |= 1u << r;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+#pragma unroll
+            for (int g = 0; g < GV; g++)
+              if ((out[g] >> r) & 1u) vf[r][g] = 0u;
+        }
+        if (act) {
+          uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
+#pragma unroll
+          for (int r = 0; r < 8; r++)
+#pragma unroll
+            for (int g = 0; g < GV; g++) {
+              s2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x5410);
+              b2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x7632);
+            }
+          uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (vt >> 2) * (D * 128) + (64 * vc + g8) * 128;
+          const uint32_t ch0 = (uint32_t)((((vt & 3) * 2) ^ g8) << 4), ch1 = (uint32_t)((((vt & 3) * 2 + 1) ^ g8) << 4);
+          // a word of each token quad at a time; the words move up in their registers, so that the loop stays rolled
+          // (unrolled, the five roles' code does not stay in the instruction caches)
+#pragma unroll 1
+          for (int w4 = 0; w4 < 4; w4++, dst += 16 * 128) {
+#pragma unroll
+            for (int odd = 0; odd < 2; odd++) {
+              uint32_t lo[4], hi[4];
+#pragma unroll
+              for (int t = 0; t < 4; t++) {
+                const uint32_t y = vw[t].x >> (8 * odd);
+                lo[t] = hfma2(codes_lo(y), s2[4 * odd + t], b2[4 * odd + t]);
+                hi[t] = hfma2(codes_hi(y), s2[4 * odd + t], b2[4 * odd + t]);
+              }
+              sts128(dst + (odd ? ch1 : ch0), lo[0], lo[1], lo[2], lo[3]);
+              sts128(dst + 8 * 128 + (odd ? ch1 : ch0), hi[0], hi[1], hi[2], hi[3]);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; t++) vw[t].x = vw[t].y, vw[t].y = vw[t].z, vw[t].z = vw[t].w;
+            if constexpr (GV == 2) {
+              if (w4 == 1)                                     // the second group's coefficients
+#pragma unroll
+                for (int r = 0; r < 8; r++) s2[r] = s2[8 * (GV - 1) + r], b2[r] = b2[8 * (GV - 1) + r];
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(V_FULL + buf));
+        if (j + 1 < it.blocks) {
+          fetch_values(blk + 1, pg_next);
+          if (j + 2 < it.blocks) pg_next = page_of(blk + 2);
         }
       }
       if (!ok) break;
