@@ -8,12 +8,12 @@
 //   S = Q K^T (TMEM) -> P = exp2(c S - m), binary16, over S (TMEM) -> O += P V (TMEM)
 //
 // Roles of the persistent CTA, one an SM (16 warps):
-//   warps 0-3, 4-7   softmax of row tile 0 and 1, a row a thread: maximum,
+//   warp 0           TMEM and the MMA issue (one thread's)
+//   warp 1           items, from a ticket counter (longest first within a request)
+//   warps 2-3        none
+//   warps 4-7, 8-11  softmax of row tile 0 and 1, a row a thread: maximum,
 //                    exponentials, P, O's rescaling, and the tile's q and output
-//   warps 8-11       4-bit codes from the cache to binary16 in shared memory: keys, and values transposed
-//   warp 12          TMEM and the single-thread MMA issue
-//   warp 13          items, from a ticket counter (longest first within a request)
-//   warps 14-15      none
+//   warps 12-15      4-bit codes from the cache to binary16 in shared memory: keys, and values transposed
 // The two row tiles alternate: while one tile's softmax runs, the tensor core
 // has the other's products.  With one row tile (heads of 256, or the rest of a request) the
 // blocks alternate instead, between the same two score buffers.  Step i of an item uses score
@@ -50,8 +50,9 @@ namespace {
 using namespace sm100;
 
 constexpr int QROWS = 128;                       // rows of a q tile (MMA M)
-constexpr int DQ_WARP0 = 8, MMA_WARP = 12, ITEM_WARP = 13;
-// Four warpgroups (the last one's last two warps without work): 128 registers a thread, which every role fits in.
+constexpr int MMA_WARP = 0, ITEM_WARP = 1, SOFT_WARP0 = 4, DQ_WARP0 = 12;
+constexpr int ITEM_READERS = 13;                 // warps that take every item: all but the one that hands them out and the idle
+// Four warpgroups (the first one's last two warps without work): 128 registers a thread, which every role fits in.
 // Shared memory leaves the L1 cache a few KB, so that spilled registers would come back from L2.
 constexpr int THREADS = 32 * 16;
 constexpr int ITEM_SLOTS = 3;
@@ -90,17 +91,24 @@ struct Cfg {
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, K_FULL = 8, K_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, IT_FULL = 16,
        IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, BARS };
 
-__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One thread of the warp (`lead`) issues; every lane calls, so that the operands stay in uniform registers.
+__device__ __forceinline__ void umma_f16_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 // A from TMEM: lane = row, a 32-bit column = two consecutive k.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_by(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
       : "memory");
 }
 // D f32, A and B binary16, both K-major
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   if (threadIdx.x == 0) {
     for (int i = 0; i < ITEM_SLOTS; i++) {
       mbar_init(bar(IT_FULL + i), 1);
-      mbar_init(bar(IT_EMPTY + i), ITEM_WARP);           // a warp an arrival
+      mbar_init(bar(IT_EMPTY + i), ITEM_READERS);        // a warp an arrival
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(bar(S_FULL + i), 1);
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     if (++it_slot == ITEM_SLOTS) it_slot = 0, it_ph ^= 1u;
   };
 
-  if (warp > ITEM_WARP) {
+  if (warp == 2 || warp == 3) {
     // no work
   } else if (warp == ITEM_WARP) {
     // ------------------------------------------------------------ items
@@ -333,50 +341,61 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     const uint32_t desc0 = (uint32_t)first, desc_hi = (uint32_t)(first >> 32);
     auto desc = [&](uint32_t lo) { return (uint64_t)desc_hi << 32 | lo; };
     bool ok = true;
+    const uint32_t lead = lane == 0, tm0 = __shfl_sync(0xffffffffu, tmem, 0);
     while (const Item *ip = next_item()) {
       const Item &it = *ip;
-      const int nt = it.tiles, N = nt * it.blocks;
-      if (lane == 0) {
+      const int nt = __shfl_sync(0xffffffffu, it.tiles, 0), N = __shfl_sync(0xffffffffu, nt * it.blocks, 0);
+      {
         int k_at = -1, v_at = -1;             // the block whose keys / values were waited for
-        auto scores = [&](int i) -> bool {    // S of step i
-          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
-          if (i < nt && !wait_bounded(bar(Q_FULL + x), qf[x].next(), ctl)) return false;
+        // What S of step i needs, and S itself.
+        auto ready = [&](int i) -> bool {
+          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
+          if (i < nt && !__all_sync(0xffffffffu, wait_bounded(bar(Q_FULL + x), qf[x].next(), ctl))) return false;
           if (j != k_at) {
-            if (!wait_bounded(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl)) return false;
+            if (!__all_sync(0xffffffffu, wait_bounded(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl))) return false;
             k_at = j;
             kb++;
           }
-          tc_fence_after();
+          return true;
+        };
+        auto scores = [&](int i) {
+          const int x = nt == 2 ? i & 1 : 0, buf = i & 1;
           const uint32_t kd = desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4), qd = desc0 + (x * C::Q_BYTES >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; kk++)          // 64 elements a column of 128-byte rows, 16 a product
-            umma_f16_ss(tmem + buf * 128, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
+            umma_f16_ss(lead, tm0 + buf * 128, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
                         desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
-          umma_commit(bar(S_FULL + buf));
-          if (x == nt - 1) umma_commit(bar(K_EMPTY + ((kb - 1) & 1)));
-          return true;
+          commit_by(lead, bar(S_FULL + buf));
+          if (x == nt - 1) commit_by(lead, bar(K_EMPTY + ((kb - 1) & 1)));
         };
-        ok = N == 0 || (scores(0) && (N < 2 || scores(1)));
+        for (int i = 0; i < 2 && i < N && ok; i++) {
+          ok = ready(i);
+          tc_fence_after();
+          if (ok) scores(i);
+        }
         for (int i = 0; i < N && ok; i++) {
           const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
+          // A wait takes some 200 cycles even where there is nothing to wait for: all others go before the one for P,
+          // which comes last, so that both products follow it at once.
           if (j != v_at) {
-            if (!wait_bounded(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl)) { ok = false; break; }
+            if (!__all_sync(0xffffffffu, wait_bounded(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl))) { ok = false; break; }
             v_at = j;
             vb++;
           }
-          if (!wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
+          if (i + 2 < N && !ready(i + 2)) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl))) { ok = false; break; }
           tc_fence_after();
           const uint32_t vd = desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4);
 #pragma unroll
           for (int kk = 0; kk < KB / 16; kk++)
-            umma_f16_ts(tmem + 256 + x * D, tmem + buf * 128 + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
+            umma_f16_ts(lead, tm0 + 256 + x * D, tm0 + buf * 128 + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
                         (j | kk) != 0);
-          umma_commit(bar(PV_DONE + x));
-          if (x == nt - 1) umma_commit(bar(V_EMPTY + ((vb - 1) & 1)));
-          if (i + 2 < N) ok = scores(i + 2);
+          commit_by(lead, bar(PV_DONE + x));
+          if (x == nt - 1) commit_by(lead, bar(V_EMPTY + ((vb - 1) & 1)));
+          if (i + 2 < N) scores(i + 2);
         }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (!ok) break;
       release();
     }
     if (lane == 0 && *abort_flag) {           // wait (bounded) for the MMAs in flight before TMEM goes
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int x = warp >> 2, row = threadIdx.x & 127;
+    const int x = (warp - SOFT_WARP0) >> 2, row = threadIdx.x & 127;
     const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16), o_tm = tm + 256 + x * D;
     const float NINF = __int_as_float(0xFF800000);
     uint32_t s_base[2] = {0, 0};                   // score tiles finished in either buffer before this item
