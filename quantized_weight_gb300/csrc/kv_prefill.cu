@@ -715,11 +715,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
           tmem_st_wait();
         }
-        // 32 columns at a time, read once (reading scores is what the softmax waits for), the next 32 on their way
-        // during the exponentials: their maximum, then, with the reference, their exponentials.  Only where the maximum has outgrown the reference
+        // 32 columns at a time, read once: their maximum, then, with the reference, their exponentials.  Only where the maximum has outgrown the reference
         // is what was summed before rescaled: l, O and the block's P so far.
         const f2 c2 = f2_make(c, c);
-        auto columns = [&](const uint32_t (&v)[32], uint32_t (&ahead)[32], int h) {
+        auto columns = [&](const uint32_t (&v)[32], int h) {
           float m4[4] = {NINF, NINF, NINF, NINF};
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
@@ -735,7 +734,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             if (k > 0 && !__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) ok = false;
             rescale<D>(k > 0 ? o_tm : 0xFFFFFFFFu, s_tm, h / 2, f);
           }
-          if (h + 32 < KB) tmem_ld_32x32b_x32(s_tm + h + 32, ahead);   // (never on its way through a call or a loop's end)
           const float mu = m == NINF ? 0.0f : m;
           const f2 mu2 = f2_make(-mu, -mu);
           f2 l2[2] = {f2_zero(), f2_zero()};
@@ -754,14 +752,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           l += la + lb;
         };
         {
-          uint32_t va[32], vb[32];
-          tmem_ld_32x32b_x32(s_tm, va);
-#pragma unroll
-          for (int h = 0; h < KB; h += 64) {
+          uint32_t v[32];
+#pragma unroll 1
+          for (int h = 0; h < KB; h += 32) {
+            tmem_ld_32x32b_x32(s_tm + h, v);
             tmem_ld_wait();
-            columns(va, vb, h);
-            tmem_ld_wait();
-            columns(vb, va, h + 32);
+            columns(v, h);
           }
         }
         if (!ok) break;
