@@ -13,7 +13,8 @@
 //   warps 2-3        none
 //   warps 4-7, 8-11  softmax of row tile 0 and 1, a row a thread: maximum,
 //                    exponentials, P, O's rescaling, and the tile's q and output
-//   warps 12-15      4-bit codes from the cache to binary16 in shared memory: keys, and values transposed
+//   warps 12-15      4-bit codes from the cache to binary16 in shared memory: keys, and values transposed (heads of
+//                    256 have one row tile: warps 8-11 then take the keys)
 // The two row tiles alternate: while one tile's softmax runs, the tensor core
 // has the other's products.  With one row tile (heads of 256, or the rest of a request) the
 // blocks alternate instead, between the same two score buffers.  Step i of an item uses score
@@ -34,6 +35,7 @@
 // Bound: tensor cores: 4 * D flops a row and key; a block of 128 keys for two row tiles of 128 is 16.8 MFLOP against 36 KB of cache.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "bounded_wait.cuh"
 #include "kv_attend.h"
@@ -138,6 +140,11 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -149,6 +156,9 @@ __device__ __forceinline__ uint32_t codes_lo(uint32_t x) { return hsub2(and_or(x
 __device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
   return hfma2(and_or(x, 0x00F000F0u, 0x64006400u), 0x2C002C00u /* 1/16 */, 0xD400D400u /* -64 */);
 }
+// Keys stand in shared memory divided by 2^10: a masked nibble is the integer times 2^-24 as it stands (a binary16
+// subnormal), so that one multiply-add with scale * 2^14 makes the value, where 2^14 scale is in range.
+constexpr float KEY_UNIT = 1024.0f;
 __device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -347,7 +357,15 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       const int nt = __shfl_sync(0xffffffffu, it.tiles, 0), N = __shfl_sync(0xffffffffu, nt * it.blocks, 0);
       {
         int k_at = -1, v_at = -1;             // the block whose keys / values were waited for
-        // What S of step i needs, and S itself.
+        // What S of step i needs: looked for (its answer takes some 200 cycles), and waited for.
+        auto looked = [&](int i) {
+          const int j = nt == 2 ? i >> 1 : i;
+          if (i >= nt && j != k_at && __all_sync(0xffffffffu, mbar_test(bar(K_FULL + (kb & 1)), kf[kb & 1].v))) {
+            kf[kb & 1].next();
+            k_at = j;
+            kb++;
+          }
+        };
         auto ready = [&](int i) -> bool {
           const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
           if (i < nt && !__all_sync(0xffffffffu, wait_bounded(bar(Q_FULL + x), qf[x].next(), ctl))) return false;
@@ -375,14 +393,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
         for (int i = 0; i < N && ok; i++) {
           const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
-          // A wait takes some 200 cycles even where there is nothing to wait for: all others go before the one for P,
-          // which comes last, so that both products follow it at once.
+          // V, then P; the next keys are looked for before P, which mostly comes last, and waited for after its product.
           if (j != v_at) {
             if (!__all_sync(0xffffffffu, wait_bounded(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl))) { ok = false; break; }
             v_at = j;
             vb++;
           }
-          if (i + 2 < N && !ready(i + 2)) { ok = false; break; }
+          if (i + 2 < N) looked(i + 2);
           if (!__all_sync(0xffffffffu, wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl))) { ok = false; break; }
           tc_fence_after();
           const uint32_t vd = desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4);
@@ -392,7 +409,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                         (j | kk) != 0);
           commit_by(lead, bar(PV_DONE + x));
           if (x == nt - 1) commit_by(lead, bar(V_EMPTY + ((vb - 1) & 1)));
-          if (i + 2 < N) scores(i + 2);
+          if (i + 2 < N) {
+            if (!ready(i + 2)) { ok = false; break; }
+            tc_fence_after();
+            scores(i + 2);
+          }
         }
       }
       if (!ok) break;
@@ -402,17 +423,20 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       umma_commit(bar(DRAIN));
       wait_drain(bar(DRAIN), 0);
     }
-  } else if (warp >= DQ_WARP0) {
+  } else if (warp >= (NQ == 2 ? DQ_WARP0 : SOFT_WARP0 + 4)) {
     // ------------------------------------------------------------ codes: keys
+    // One warpgroup has both, or, where there is no second row tile, its softmax warps take the keys.
+    auto codes = [&](auto with_keys, auto with_values) {
+    constexpr bool KEYS = decltype(with_keys)::value, VALUES = decltype(with_values)::value;
     constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
     constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
     constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
-    const int w4 = warp - DQ_WARP0, t = lane & 3;
+    const int w4 = warp & 3, t = lane & 3;
     // values
     constexpr int CB = D / 64;                               // blocks of 64 elements
     constexpr int GV = G > CB ? 2 : 1;                       // groups in one (group of 32: two)
     constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
-    const int u = threadIdx.x - DQ_WARP0 * 32, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
+    const int u = threadIdx.x & 127, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
     const bool act = u < UNITS;
     Phase ke[2], ve[2];
     ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
@@ -422,9 +446,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       const Item &it = *ip;
       // this item's notes, last used four items ago
       uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
-      for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
-      if (u == 0) noted[n_item & 3] = 0;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if constexpr (VALUES) {
+        for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
+        if (u == 0) noted[n_item & 3] = 0;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
       const int32_t *tab = a.table + it.b * a.max_blocks;
       uint32_t w[PW][WC], cf[PW][GK];
       int pid[PW];
@@ -509,31 +535,46 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       };
       int pg_next = -1;
       if (it.blocks > 0) {
-        pages(it.blk0);
-        pg_next = page_of(it.blk0);
-        fetch_keys(it.blk0);
-        fetch_values(it.blk0, pg_next);
+        if constexpr (KEYS) pages(it.blk0);
+        if constexpr (VALUES) pg_next = page_of(it.blk0);
+        if constexpr (KEYS) fetch_keys(it.blk0);
+        if constexpr (VALUES) fetch_values(it.blk0, pg_next);
         if (it.blocks > 1) {
-          pages(it.blk0 + 1);
-          pg_next = page_of(it.blk0 + 1);
+          if constexpr (KEYS) pages(it.blk0 + 1);
+          if constexpr (VALUES) pg_next = page_of(it.blk0 + 1);
         }
       }
       for (int j = 0; j < it.blocks; j++, kb++) {
         const int blk = it.blk0 + j, buf = kb & 1;
+        if constexpr (KEYS) {
         if (!__all_sync(0xffffffffu, wait_bounded(bar(K_EMPTY + buf), ke[buf].next(), ctl))) { ok = false; break; }
         {
           const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
+          uint32_t most = 0;
+#pragma unroll
+          for (int i = 0; i < PW; i++)
+#pragma unroll
+            for (int k = 0; k < GK; k++) most = max(most, cf[i][k] & 0x7FFFu);
+          const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
 #pragma unroll 1
           for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
             const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
             const int pos = tl * 16 + row;
 #pragma unroll
             for (int k = 0; k < WC; k++) {
-              const uint32_t cc = cf[0][k / (WC / GK)], s2 = prmt(cc, cc, 0x1010), b2 = prmt(cc, cc, 0x3232);
-              const uint32_t x = w[0][k], y = x >> 8;
+              const uint32_t cc = cf[0][k / (WC / GK)], x = w[0][k], y = x >> 8;
+              const uint32_t b2 = hmul2(prmt(cc, cc, 0x3232), 0x14001400u /* 2^-10 */);
               // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
-              const uint32_t e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
-              const uint32_t e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+              uint32_t e04, e15, e26, e37;
+              if (!large) {
+                const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x74007400u /* 2^14 */), s16 = hmul2(s2, 0x2C002C00u /* 1/16 */);
+                e04 = hfma2(x & 0x000F000Fu, s2, b2), e15 = hfma2(x & 0x00F000F0u, s16, b2);
+                e26 = hfma2(y & 0x000F000Fu, s2, b2), e37 = hfma2(y & 0x00F000F0u, s16, b2);
+              } else {
+                const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x14001400u);
+                e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
+                e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+              }
               const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
               sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
                      prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
@@ -554,6 +595,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           fetch_keys(blk + 1);
           if (j + 2 < it.blocks) pages(blk + 2);
         }
+        }
+        if constexpr (VALUES) {
         if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
         // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
         // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
@@ -628,11 +671,16 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           fetch_values(blk + 1, pg_next);
           if (j + 2 < it.blocks) pg_next = page_of(blk + 2);
         }
+        }
       }
       if (!ok) break;
-      if (lane == 0) mbar_arrive(bar(IT_NEXT));
+      if (KEYS && lane == 0) mbar_arrive(bar(IT_NEXT));
       release();
     }
+    };
+    if constexpr (NQ == 2) codes(std::true_type(), std::true_type());
+    else if (warp < DQ_WARP0) codes(std::true_type(), std::false_type());
+    else codes(std::false_type(), std::true_type());
   } else {
     // ------------------------------------------------------------ softmax
     const int x = (warp - SOFT_WARP0) >> 2, row = threadIdx.x & 127;
@@ -674,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         mx = max(mx & 0xFFFFu, mx >> 16);                    // bfloat16 bits of the largest |element|
         const int ex = mx == 0u || mx >= 0x7F80u ? 0 : min(126, 14 - ((int)(mx >> 7) - 127));
         const float f = __int_as_float((ex + 127) << 23);
-        c = ldexpf(a.scale * 1.44269504088896340736f, -ex);
+        c = ldexpf(a.scale * (KEY_UNIT * 1.44269504088896340736f), -ex);
         const uint32_t dst = sb + x * C::Q_BYTES + row * 128;
 #pragma unroll 4
         for (int h = 0; h < D / 8; h++) {
