@@ -349,6 +349,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     // Descriptors differ in the start address alone (the low word, in 16-byte units).
     const uint64_t first = smem_desc_sw128(sb);
     const uint32_t desc0 = (uint32_t)first, desc_hi = (uint32_t)(first >> 32);
+    // (a reduction over equal values leaves its result in a uniform register, where an MMA's operands have to be)
+    auto uniform = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
     auto desc = [&](uint32_t lo) { return (uint64_t)desc_hi << 32 | lo; };
     bool ok = true;
     const uint32_t lead = lane == 0, tm0 = __shfl_sync(0xffffffffu, tmem, 0);
@@ -378,10 +380,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         };
         auto scores = [&](int i) {
           const int x = nt == 2 ? i & 1 : 0, buf = i & 1;
-          const uint32_t kd = desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4), qd = desc0 + (x * C::Q_BYTES >> 4);
+          const uint32_t kd = uniform(desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4)), qd = uniform(desc0 + (x * C::Q_BYTES >> 4));
+          const uint32_t dt = uniform(tm0 + buf * 128);
 #pragma unroll
           for (int kk = 0; kk < D / 16; kk++)          // 64 elements a column of 128-byte rows, 16 a product
-            umma_f16_ss(lead, tm0 + buf * 128, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
+            umma_f16_ss(lead, dt, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
                         desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
           commit_by(lead, bar(S_FULL + buf));
           if (x == nt - 1) commit_by(lead, bar(K_EMPTY + ((kb - 1) & 1)));
@@ -402,10 +405,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           if (i + 2 < N) looked(i + 2);
           if (!__all_sync(0xffffffffu, wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl))) { ok = false; break; }
           tc_fence_after();
-          const uint32_t vd = desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4);
+          const uint32_t vd = uniform(desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4));
+          const uint32_t ot = uniform(tm0 + 256 + x * D), pt = uniform(tm0 + buf * 128);
 #pragma unroll
           for (int kk = 0; kk < KB / 16; kk++)
-            umma_f16_ts(lead, tm0 + 256 + x * D, tm0 + buf * 128 + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
+            umma_f16_ts(lead, ot, pt + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
                         (j | kk) != 0);
           commit_by(lead, bar(PV_DONE + x));
           if (x == nt - 1) commit_by(lead, bar(V_EMPTY + ((vb - 1) & 1)));
