@@ -93,25 +93,23 @@ struct Cfg {
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, K_FULL = 8, K_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, IT_FULL = 16,
        IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, BARS };
 
-// One thread of the warp (`lead`) issues; every lane calls, so that the operands stay in uniform registers.
-__device__ __forceinline__ void umma_f16_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 // A from TMEM: lane = row, a 32-bit column = two consecutive k.
-__device__ __forceinline__ void umma_f16_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void commit_by(uint32_t lead, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
-      : "memory");
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // D f32, A and B binary16, both K-major
 constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
@@ -353,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     auto uniform = [](uint32_t v) { return __reduce_max_sync(0xffffffffu, v); };
     auto desc = [&](uint32_t lo) { return (uint64_t)desc_hi << 32 | lo; };
     bool ok = true;
-    const uint32_t lead = lane == 0, tm0 = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t tm0 = __shfl_sync(0xffffffffu, tmem, 0);
     while (const Item *ip = next_item()) {
       const Item &it = *ip;
       const int nt = __shfl_sync(0xffffffffu, it.tiles, 0), N = __shfl_sync(0xffffffffu, nt * it.blocks, 0);
@@ -382,12 +380,15 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           const int x = nt == 2 ? i & 1 : 0, buf = i & 1;
           const uint32_t kd = uniform(desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4)), qd = uniform(desc0 + (x * C::Q_BYTES >> 4));
           const uint32_t dt = uniform(tm0 + buf * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; kk++)          // 64 elements a column of 128-byte rows, 16 a product
-            umma_f16_ss(lead, dt, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
-                        desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
-          commit_by(lead, bar(S_FULL + buf));
-          if (x == nt - 1) commit_by(lead, bar(K_EMPTY + ((kb - 1) & 1)));
+            for (int kk = 0; kk < D / 16; kk++)        // 64 elements a column of 128-byte rows, 16 a product
+              umma_f16_ss(dt, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
+                          desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
+            umma_commit(bar(S_FULL + buf));
+            if (x == nt - 1) umma_commit(bar(K_EMPTY + ((kb - 1) & 1)));
+          }
+          __syncwarp();
         };
         for (int i = 0; i < 2 && i < N && ok; i++) {
           ok = ready(i);
@@ -407,12 +408,15 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           tc_fence_after();
           const uint32_t vd = uniform(desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4));
           const uint32_t ot = uniform(tm0 + 256 + x * D), pt = uniform(tm0 + buf * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < KB / 16; kk++)
-            umma_f16_ts(lead, ot, pt + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
-                        (j | kk) != 0);
-          commit_by(lead, bar(PV_DONE + x));
-          if (x == nt - 1) commit_by(lead, bar(V_EMPTY + ((vb - 1) & 1)));
+            for (int kk = 0; kk < KB / 16; kk++)
+              umma_f16_ts(ot, pt + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
+                          (j | kk) != 0);
+            umma_commit(bar(PV_DONE + x));
+            if (x == nt - 1) umma_commit(bar(V_EMPTY + ((vb - 1) & 1)));
+          }
+          __syncwarp();
           if (i + 2 < N) {
             if (!ready(i + 2)) { ok = false; break; }
             tc_fence_after();
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       if (!ok) break;
       release();
     }
-    if (lane == 0 && *abort_flag) {           // wait (bounded) for the MMAs in flight before TMEM goes
+    if (*abort_flag && elect_one()) {         // wait (bounded) for the MMAs in flight before TMEM goes
       umma_commit(bar(DRAIN));
       wait_drain(bar(DRAIN), 0);
     }
@@ -712,30 +716,37 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(it.cu0 + qi) * a.q_token +
                                                          (int64_t)(it.kvh * p.ratio + hq) * a.q_head);
       if (it.blocks > 0) {
+        constexpr int HOLD = D <= 128 ? D / 8 : 16;            // pieces of 8 elements in registers at a time
+        uint4 v[HOLD];
         uint32_t mx = 0;
 #pragma unroll 1
-        for (int h = 0; h < D / 8; h += 8) {
-          uint4 v[8];
+        for (int h = 0; h < D / 8; h += HOLD) {
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = real ? __ldg(src + h + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < HOLD; i++) v[i] = real ? __ldg(src + h + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int i = 0; i < 8; i++)
+          for (int i = 0; i < HOLD; i++)
             mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)),
                           __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
         }
-        mx = max(mx & 0xFFFFu, mx >> 16);                    // bfloat16 bits of the largest |element|
+        mx = max(mx & 0xFFFFu, mx >> 16);                      // bfloat16 bits of the largest |element|
         const int ex = mx == 0u || mx >= 0x7F80u ? 0 : min(126, 14 - ((int)(mx >> 7) - 127));
         const float f = __int_as_float((ex + 127) << 23);
         c = ldexpf(a.scale * (KEY_UNIT * 1.44269504088896340736f), -ex);
         const uint32_t dst = sb + x * C::Q_BYTES + row * 128;
-#pragma unroll 4
-        for (int h = 0; h < D / 8; h++) {
-          const uint4 v = real ? __ldg(src + h) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
+#pragma unroll 1
+        for (int h0 = D / 8 - HOLD; h0 >= 0; h0 -= HOLD) {     // the last pieces read are still there
+          if (h0 != D / 8 - HOLD)
 #pragma unroll
-          for (int i = 0; i < 4; i++) o[i] = pack_f16(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xFFFF0000u) * f);
-          sts128(dst + (h >> 3) * (QROWS * 128) + (((h & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < HOLD; i++) v[i] = real ? __ldg(src + h0 + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < HOLD; i++) {
+            const int h = h0 + i;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) o[k] = pack_f16(__uint_as_float(u[k] << 16) * f, __uint_as_float(u[k] & 0xFFFF0000u) * f);
+            sts128(dst + (h >> 3) * (QROWS * 128) + (((h & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(bar(Q_FULL + x));
