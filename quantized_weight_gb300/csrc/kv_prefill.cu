@@ -482,20 +482,20 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                                ((tok & (p.g.page - 1)) >> 4) * TILE;
             valid |= 1u << tl;
             if constexpr (WC == 4) {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
+              const uint4 v = *(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
               w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
             } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
+              const uint2 v = *(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
               w[i][0] = v.x, w[i][1] = v.y;
             }
             const uint8_t *cp = s + 16 * D + (row * G + c * GK) * 4;
             if constexpr (GK == 1) {
-              cf[i][0] = __ldg(reinterpret_cast<const uint32_t *>(cp));
+              cf[i][0] = *(reinterpret_cast<const uint32_t *>(cp));
             } else if constexpr (GK == 2) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp));
+              const uint2 v = *(reinterpret_cast<const uint2 *>(cp));
               cf[i][0] = v.x, cf[i][1] = v.y;
             } else {
-              const uint4 v = __ldg(reinterpret_cast<const uint4 *>(cp));
+              const uint4 v = *(reinterpret_cast<const uint4 *>(cp));
               cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
             }
           } else {
@@ -521,14 +521,14 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                              (((int)tok & (p.g.page - 1)) >> 4) * TILE;
           const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (vc * 8 + g8) * 64);
 #pragma unroll
-          for (int i = 0; i < 4; i++) vw[i] = __ldg(s + i);
+          for (int i = 0; i < 4; i++) vw[i] = s[i];
           const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * vc : vc * G / CB) * 4;
 #pragma unroll
           for (int r = 0; r < 16; r++) {
             if constexpr (GV == 1) {
-              vf[r][0] = __ldg(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
+              vf[r][0] = *(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
             } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cp + r * G * 4));
+              const uint2 v = *(reinterpret_cast<const uint2 *>(cp + r * G * 4));
               vf[r][0] = v.x, vf[r][GV - 1] = v.y;
             }
           }
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
               if (tok < it.vlo || tok >= it.vhi) {
                 out[g] |= 1u << r;
               } else if (coefs) {
-                const uint32_t m = __ldg(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
+                const uint32_t m = *(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
                 if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
                   const int pos = vt * 16 + r, grp = (G > CB ? 2 * vc : vc * G / CB) + g;
                   atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll 1
         for (int h = 0; h < D / 8; h += HOLD) {
 #pragma unroll
-          for (int i = 0; i < HOLD; i++) v[i] = real ? __ldg(src + h + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < HOLD; i++) v[i] = real ? src[h + i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int i = 0; i < HOLD; i++)
             mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu)),
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         for (int h0 = D / 8 - HOLD; h0 >= 0; h0 -= HOLD) {     // the last pieces read are still there
           if (h0 != D / 8 - HOLD)
 #pragma unroll
-            for (int i = 0; i < HOLD; i++) v[i] = real ? __ldg(src + h0 + i) : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < HOLD; i++) v[i] = real ? src[h0 + i] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int i = 0; i < HOLD; i++) {
             const int h = h0 + i;
