@@ -181,22 +181,25 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
   return v;
 }
 
+// Eight elements as they lie in memory.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void *p, float (&v)[8]) {
-  if constexpr (BF16) {
-    const uint4 w = ld_once(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+  uint4 w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const uint8_t *p) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  } else {
-    const uint4 a = ld_once(p), b = ld_once(static_cast<const uint8_t *>(p) + 16);
-    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+    for (int i = 0; i < (BF16 ? 1 : 2); i++) w[i] = ld_once(p + 16 * i);
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); i++) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[BF16 ? 0 : 1].x, w[BF16 ? 0 : 1].y, w[BF16 ? 0 : 1].z, w[BF16 ? 0 : 1].w};
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      v[i] = __uint_as_float(!BF16 ? u[i] : i & 1 ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
+  }
+};
 
 // ---------------------------------------------------------------- append
 
@@ -211,18 +214,45 @@ struct AppendParams {
   uint8_t *cache;
 };
 
-// Eight elements of a row a lane, `lanes` of them to a group: the codes, element i in nibble i, and scale | bias << 16.
-// The quotient (x - bias) / scale, correctly rounded, decides a code only through its rounding, that is only next to a
-// half-integer.  A product with the approximate reciprocal, clamped to [0, 15], is within 1e-5 of it; where no element
-// of the lane comes so near to a half the product's rounding is the code, elsewhere the division is taken.
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int lanes, uint32_t &coef) {
-  // fminf and fmaxf skip NaN and order -0 before +0; NaN is left where a group has nothing else
-  float lo = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
-  float hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-  for (int o = 1; o < lanes; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+// The least and the greatest of a group, `lanes` lanes with eight elements each.  NaN are skipped (NaN is left where a
+// group has nothing else) and -0 lies below +0: the order of fminf and fmaxf here, and of the two-element bfloat16 forms.
+template <bool BF16>
+__device__ __forceinline__ void range8(const Raw<BF16> &x, const float (&v)[8], int lanes, float &lo, float &hi) {
+  if constexpr (BF16) {
+    auto b2 = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+    const __nv_bfloat162 mn = __hmin2(__hmin2(b2(x.w[0].x), b2(x.w[0].y)), __hmin2(b2(x.w[0].z), b2(x.w[0].w)));
+    const __nv_bfloat162 mx = __hmax2(__hmax2(b2(x.w[0].x), b2(x.w[0].y)), __hmax2(b2(x.w[0].z), b2(x.w[0].w)));
+    // least and negated greatest side by side: one exchange a step
+    const uint32_t a = *reinterpret_cast<const uint32_t *>(&mn), b = *reinterpret_cast<const uint32_t *>(&mx) ^ 0x80008000u;
+    __nv_bfloat162 r = __hmin2(b2(prmt(a, b, 0x5410u)), b2(prmt(a, b, 0x7632u)));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+      if (o < lanes) r = __hmin2(r, b2(__shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t *>(&r), o)));
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(&r);
+    lo = __uint_as_float(u << 16);
+    hi = __uint_as_float((u & 0xFFFF0000u) ^ 0x80000000u);
+  } else {
+    lo = fminf(fminf(fminf(v[0], v[1]), fminf(v[2], v[3])), fminf(fminf(v[4], v[5]), fminf(v[6], v[7])));
+    hi = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1)
+      if (o < lanes) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
   }
+}
+
+// Eight elements of a row a lane: the codes, element i in nibble i, and scale | bias << 16.
+// The quotient (x - bias) / scale, correctly rounded, decides a code only through its rounding, that is only next to a
+// half-integer.  A product with the approximate reciprocal is, between 0 and 15, within 1e-5 of it; where no element of
+// the lane comes so near to a half, or rounds to something else than 0 .. 15 (NaN too), the product's roundings are
+// the codes, elsewhere the division is taken.
+template <bool BF16>
+__device__ __forceinline__ uint32_t quantize8(const Raw<BF16> &x, int lanes, uint32_t &coef) {
+  float v[8], lo, hi;
+  x.values(v);
+  range8<BF16>(x, v, lanes, lo, hi);
   const uint16_t sh = half_bits_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)), bh = half_bits_rn(lo);
   coef = sh | ((uint32_t)bh << 16);
   const float s = h2f(sh), b = h2f(bh);
@@ -230,18 +260,21 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int lanes, ui
   float inv;
   asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(s));
   constexpr float MAGIC = 12582912.0f;                     // 1.5 * 2^23: the integer lands in the low mantissa bits
-  uint32_t word = 0, bits = 0;
+  const f2 b2 = f2_make(b, b), inv2 = f2_make(inv, inv), magic2 = f2_make(MAGIC, MAGIC);
+  uint32_t word = 0, all = 0;
   float worst = 0.0f;
 #pragma unroll
-  for (int i = 7; i >= 0; i--) {
-    const float t = fminf(fmaxf((v[i] - b) * inv, 0.0f), 15.0f);
-    const float r = t + MAGIC;
-    worst = fmaxf(worst, fabsf(t - (r - MAGIC)));
-    word = word * 16u + __float_as_uint(r);
-    bits = bits * 16u + __float_as_uint(MAGIC);
+  for (int i = 6; i >= 0; i -= 2) {
+    const f2 t = f2_mul(f2_sub(f2_make(v[i], v[i + 1]), b2), inv2), r = f2_add(t, magic2);
+    float d0, d1, r0, r1;
+    f2_split(f2_sub(t, f2_sub(r, magic2)), d0, d1);
+    f2_split(r, r0, r1);
+    worst = fmaxf(worst, fmaxf(fabsf(d0), fabsf(d1)));
+    const uint32_t n0 = __float_as_uint(r0) - __float_as_uint(MAGIC), n1 = __float_as_uint(r1) - __float_as_uint(MAGIC);
+    all |= n0 | n1;
+    word = (word * 16u + n1) * 16u + n0;
   }
-  word -= bits;
-  if (worst > 0.49998f) {
+  if (worst > 0.49998f || all > 15u) {
     word = 0;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -266,36 +299,39 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
   pdl_wait();
   pdl_launch_dependents();
   if (unit * p.r.per_warp >= p.r.tokens) return;           // whole warps
-  const int lanes = g.group >> 3;
+  const int lanes = g.group >> 3, grp = m >> g.lg_group8;
 
   // `n` tokens from t on, their slots from `slot` on (n = 4: an aligned quad)
   auto rows = [&](auto count, int64_t t, int slot) {
+    constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
+    Raw<BF16> ahead[PASSES];
+    auto fetch = [&](int hv) {
+      const uint8_t *src = static_cast<const uint8_t *>(hv & 1 ? p.v : p.k);
+      const int64_t token = hv & 1 ? p.v_token : p.k_token, head = (int64_t)(hv >> 1) * (hv & 1 ? p.v_head : p.k_head);
+#pragma unroll
+      for (int ps = 0; ps < PASSES; ps++) {
+        const int r = ps * RP + sub;
+        if (r < n) ahead[ps].load(src + ((t + r) * token + head + 8 * m) * (BF16 ? 2 : 4));
+        else ahead[ps].zero();
+      }
+    };
+    fetch(hv0);
 #pragma unroll 1
     for (int hv = hv0; hv < hv1; hv++) {
     const int h = hv >> 1;
     const bool isv = hv & 1;
-    const uint8_t *src = static_cast<const uint8_t *>(isv ? p.v : p.k);
-    const int64_t token = isv ? p.v_token : p.k_token, head = (int64_t)h * (isv ? p.v_head : p.k_head);
-    constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
-    float v[PASSES][8];
+    Raw<BF16> x[PASSES];
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ps++) {
-      const int r = ps * RP + sub;
-      if (r < n) {
-        load8<BF16>(src + ((t + r) * token + head + 8 * m) * (BF16 ? 2 : 4), v[ps]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[ps][i] = 0.0f;
-      }
-    }
+    for (int ps = 0; ps < PASSES; ps++) x[ps] = ahead[ps];
+    if (hv + 1 < hv1) fetch(hv + 1);
     uint8_t *tile = p.cache + kv_tile_at(g, slot, h);
 #pragma unroll
     for (int ps = 0; ps < PASSES; ps++) {
       const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15);
       uint32_t coef;
-      const uint32_t word = quantize8(v[ps], lanes, coef), other = __shfl_xor_sync(0xffffffffu, word, 1);
-      if (r < n && m % lanes == 0)
-        *reinterpret_cast<uint32_t *>(tile + (isv ? kv_v_coef(g, row, m / lanes) : kv_k_coef(g, row, m / lanes))) = coef;
+      const uint32_t word = quantize8<BF16>(x[ps], lanes, coef), other = __shfl_xor_sync(0xffffffffu, word, 1);
+      if (r < n && (m & (lanes - 1)) == 0)
+        *reinterpret_cast<uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))) = coef;
       if (!isv) {
         if (r < n) *reinterpret_cast<uint32_t *>(tile + kv_k_word(D, row, m)) = word;
       } else {
@@ -399,7 +435,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
     uint32_t coef[PASSES], q[PASSES][2];                   // codes: bytes of elements 0..3 and 4..7
 #pragma unroll
     for (int ps = 0; ps < PASSES; ps++) {
-      const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = 8 * m / g.group;
+      const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = m >> g.lg_group8;
       coef[ps] = q[ps][0] = q[ps][1] = 0u;
       if (r < n && slot >= 0) {
         coef[ps] = *(reinterpret_cast<const uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))));

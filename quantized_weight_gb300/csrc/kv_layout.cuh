@@ -35,6 +35,7 @@ constexpr int kKvTile = 16;   // tokens per tile
 
 struct KvGeom {
   int D, group, G;            // head dimension, group, groups per head
+  int lg_group8;              // log2 of a group's eights
   int page, lg_page;          // tokens per page (a power of two, >= 16)
   int tile_bytes, head_bytes; // one tile; one head's tiles of a page
   int kv_heads;
@@ -48,6 +49,7 @@ inline KvGeom kv_geom(int64_t pages, int64_t kv_heads, int64_t D, int page, int 
   g.D = (int)D;
   g.group = group;
   g.G = (int)D / group;
+  g.lg_group8 = __builtin_ctz((unsigned)group) - 3;
   g.page = page;
   g.lg_page = __builtin_ctz((unsigned)page);
   g.tile_bytes = kv_tile_bytes(g.D, group);
