@@ -17,12 +17,10 @@
 // of two that puts its largest element in [2^14, 2^15).
 //
 // Precision.  HL (float32 queries): q and p * sv enter as two binary16 terms
-// each, and value codes as q - 8 (one HADD2), with bv + 8 sv as the bias: the
-// products then have the size of the result, instead of a large positive
-// sum that the bias takes back.  Otherwise (bfloat16) as one term: q is exact
+// each, which keeps 22 bits of them.  Otherwise (bfloat16) as one: q is exact
 // in it, p * sv is rounded to 11 bits.  p * sv is scaled by a power of two that follows the
 // largest sv met, so small scales do not fall into binary16's
-// subnormals.  MMA chains run over 32 tokens and are then added to
+// subnormals.  MMA chains run over a unit of tokens and are then added to
 // float32 registers (chains over the whole context would pick up the tensor core's truncation at every step).
 //
 // Work split.  Items are (request, kv head, tile of 8 NT rows); the units of
@@ -141,6 +139,22 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// Nibble I of both halves of a word as an MMA operand: the masked code as it lies is a binary16 subnormal, which the MMA
+// multiplies exactly.  Plain: nibbles 0 and 2 are code * 2^-24, 1 and 3 code * 2^-20.  But the MMA adds a product up to the
+// precision that its operands' exponents give, and a subnormal's leading zeros are lost from it: with codes of 2^-24 the
+// errors of float32 outputs were 5 to 10 times float32's own.  HL therefore shifts every nibble to 2^-20 (the same errors as
+// with normal numbers, at 117 against 131 us for the 117 MB of 131072 tokens).
+template <bool HL, int I>
+__device__ __forceinline__ uint32_t operand(uint32_t x) {
+  if constexpr (HL) return (I == 0 ? x << 4 : x >> (4 * I - 4)) & 0x00F000F0u;
+  return (x >> (8 * (I / 2))) & (I % 2 ? 0x00F000F0u : 0x000F000Fu);
+}
+// The same for values: HL centres them, code - 8, which is exact, and adds 8 scale to the bias.  Weights are positive,
+// so without it the sum of the products is large and the bias takes most of it back (errors 10 times as large).
+template <bool HL, int I>
+__device__ __forceinline__ uint32_t value_operand(uint32_t x) {
+  return HL ? sub_f16(operand<HL, I>(x), 0x00800080u) : operand<HL, I>(x);
+}
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -232,6 +246,8 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
   constexpr int WPL = D / 32;                    // key words per lane and row
   constexpr int WPG = WPL / G;                   // of them in a group
   constexpr int VW = D / 16;                     // value words per lane
+  constexpr int CODE = HL ? 20 : 24;             // an operand is its code times 2^-CODE;
+  constexpr float ODD = HL ? 1.0f : 0.0625f;     // 1 / ODD times that from an odd nibble
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lg = lane >> 2, lt = lane & 3;
   const int tw = p.team, tthreads = tw * 32;     // this team's warps and threads
@@ -517,9 +533,9 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         for (int j = 0; j < 8; j++) v[j] *= f, sum += v[j];
 #pragma unroll
         for (int o = 1; o < D / G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (m % (D / G / 8) == 0) qsum[m / (D / G / 8) * ROWS + row] = sum * pow2i(-24);
+        if (m % (D / G / 8) == 0) qsum[m / (D / G / 8) * ROWS + row] = sum * pow2i(-CODE);
         if (m == 0) {
-          fq[row] = ldexpf(a.scale * 1.44269504088896340736f, 24 - ex);     // log2(e)
+          fq[row] = ldexpf(a.scale * 1.44269504088896340736f, CODE - ex);   // log2(e)
           const int qi = div_small(sg.r0 + row, p.ratio);
           const int64_t pos = (int64_t)sg.base + qi;
           const int64_t lo = a.window > 0 ? pos + 1 - a.window : 0;
@@ -530,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         const int w = m >> 2, t = m & 3, n = row >> 3, ln = (row & 7) * 4 + t;
 #pragma unroll
         for (int st = 0; st < 2; st++) {
-          const float x0 = v[2 * st], x1 = v[2 * st + 4], z0 = v[2 * st + 1] * 0.0625f, z1 = v[2 * st + 5] * 0.0625f;
+          const float x0 = v[2 * st], x1 = v[2 * st + 4], z0 = v[2 * st + 1] * ODD, z1 = v[2 * st + 5] * ODD;
           uint32_t *dst = qf + (((2 * w + st) * NT + n) * 32 + ln) * QW;
           const uint32_t h0 = pack_f16(x0, x1), h1 = pack_f16(z0, z1);
           dst[0] = h0, dst[1] = h1;
@@ -631,8 +647,9 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
                 }
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                  const uint32_t x0 = kw[i][0][w] >> (8 * s2), x1 = kw[i][1][w] >> (8 * s2);
-                  const uint32_t a0 = x0 & 0x000F000Fu, a1 = x1 & 0x000F000Fu, a2 = x0 & 0x00F000F0u, a3 = x1 & 0x00F000F0u;
+                  const uint32_t x0 = kw[i][0][w], x1 = kw[i][1][w];
+                  const uint32_t a0 = s2 ? operand<HL, 2>(x0) : operand<HL, 0>(x0), a1 = s2 ? operand<HL, 2>(x1) : operand<HL, 0>(x1);
+                  const uint32_t a2 = s2 ? operand<HL, 3>(x0) : operand<HL, 1>(x0), a3 = s2 ? operand<HL, 3>(x1) : operand<HL, 1>(x1);
 #pragma unroll
                   for (int n = 0; n < NT; n++) {
                     if (w == g * WPG && s2 == 0) mma_z(c[i][n], a0, a1, a2, a3, qv[n][0], qv[n][1]);
@@ -791,12 +808,8 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
             float d[NT][4];
 #pragma unroll
             for (int i = 0; i < UT; i++) {
-              const uint32_t x0 = vw[i][x], x1 = x0 >> 8;
-              uint32_t a0 = x0 & 0x000F000Fu, a1 = x0 & 0x00F000F0u, a2 = x1 & 0x000F000Fu, a3 = x1 & 0x00F000F0u;
-              if constexpr (HL) {                                    // code - 8, exact: 8 and 128 times 2^-24
-                a0 = sub_f16(a0, 0x00080008u), a1 = sub_f16(a1, 0x00800080u);
-                a2 = sub_f16(a2, 0x00080008u), a3 = sub_f16(a3, 0x00800080u);
-              }
+              const uint32_t a0 = value_operand<HL, 0>(vw[i][x]), a1 = value_operand<HL, 1>(vw[i][x]);
+              const uint32_t a2 = value_operand<HL, 2>(vw[i][x]), a3 = value_operand<HL, 3>(vw[i][x]);
 #pragma unroll
               for (int n = 0; n < NT; n++) {
                 if (i == 0) mma_z(d[n], a0, a1, a2, a3, pf[i][g][n][0], pf[i][g][n][1]);
@@ -831,7 +844,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         }
       team_sync(team, tthreads);
       // every warp's share in units of the common maximum
-      const float unit = pow2i(ve - 5);                              // 2^24 / 2^(29 - ve)
+      const float unit = pow2i(CODE - 29 + ve);                      // 2^CODE / 2^(29 - ve)
       float sc[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; n++)
@@ -857,7 +870,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
 #pragma unroll
             for (int r = 0; r < 4; r++) {
               const int c = r & 1;
-              const float v = fmaf(o[n][w][r], r < 2 ? unit : unit * 0.0625f, ob[n][c][g]) * sc[n][c];
+              const float v = fmaf(o[n][w][r], r < 2 ? unit : unit * ODD, ob[n][c][g]) * sc[n][c];
               fn(8 * n + 2 * lt + c, 16 * w + lg + (r < 2 ? 0 : 8), v);
             }
           }
