@@ -148,6 +148,29 @@ def test_append_edge_values(qmm, oracle_mod):
     check_append(qmm, oracle_mod, x, x[::-1].copy(), list(range(3, 12)), 1, 16, 64, torch.float32)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("D,Hkv,T", [(64, 64, 1003), (128, 37, 1500), (256, 64, 701)])
+def test_append_and_read_many_heads(qmm, D, Hkv, T, dtype):
+    """Calls whose warps take several heads give the bytes and values of calls with a token each."""
+    import torch
+    torch.manual_seed(D)
+    page, pages, group = 64, 30, 64
+    k, v = torch.randn(2, T, Hkv, D, device="cuda").to(getattr(torch, dtype)).unbind(0)
+    slots = torch.arange(5, T + 5, dtype=torch.int32, device="cuda")
+    slots[100:140] = slots[100:140].flip(0)
+    slots[200:220] = -1
+    one, all_ = qmm.kv_cache(pages, Hkv, D, page, group), qmm.kv_cache(pages, Hkv, D, page, group)
+    qmm.kv_append(k, v, slots, all_, page, group)
+    for t in range(T):
+        qmm.kv_append(k[t:t + 1], v[t:t + 1], slots[t:t + 1], one, page, group)
+    assert torch.equal(one, all_) and bool(one.any())
+    rk, rv = qmm.kv_read(slots, all_, D, page, group, dtype=k.dtype)
+    for t in range(0, T, 7):
+        for whole, part in zip((rk, rv), qmm.kv_read(slots[t:t + 1], all_, D, page, group, dtype=k.dtype)):
+            assert torch.equal(whole[t].nan_to_num(7.0), part[0].nan_to_num(7.0))
+    qmm.check()
+
+
 def test_read_outside(qmm):
     import torch
     cache = qmm.kv_cache(2, 2, 64, 16, 64)
@@ -158,11 +181,11 @@ def test_read_outside(qmm):
 
 # ---------------------------------------------------------------- attend
 
-def make_cache(rng, pages, H, D, page, group, spread=1.0):
-    """Random codes; scales about 0.2 and biases at -8 scales, times a factor per page spread over its decades."""
+def make_cache(rng, pages, H, D, page, group, spread=1.0, size=1.0):
+    """Random codes; scales about 0.2 and biases at -8 scales, times `size` and a factor per page spread over its decades."""
     G, tiles = D // group, page // 16
     codes = rng.integers(0, 256, (pages, H, tiles, 16 * D), dtype=np.uint8)
-    f = spread ** rng.uniform(-1, 1, (pages, 1, 1, 1))
+    f = size * spread ** rng.uniform(-1, 1, (pages, 1, 1, 1))
     s = rng.uniform(0.1, 0.3, (pages, H, tiles, 32 * G)) * f
     b = -8 * s + 0.1 * f * rng.standard_normal(s.shape)
     coef = np.ascontiguousarray(np.stack((s, b), -1).astype(np.float16)).view(np.uint8).reshape(pages, H, tiles, -1)
@@ -186,12 +209,12 @@ def tolerance(size, want, lens_max, D, dtype):
 
 
 def check_attend(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, spread=1.0, scale=None, cu_null=False,
-                 holes=False, strided=False):
+                 holes=False, strided=False, size=1.0):
     import torch
     B = len(lens)
     per = [-(-n // page) for n in lens]
     pages = sum(per) + 2
-    cache = make_cache(rng, pages, Hkv, D, page, group, spread)
+    cache = make_cache(rng, pages, Hkv, D, page, group, spread, size)
     perm = rng.permutation(pages).astype(np.int32)
     table = np.full((B, max(1, max(per))), -1, np.int32)
     at = 0
@@ -226,9 +249,9 @@ def check_attend(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0,
     qmm.kv_attend(*args, **kw, out=out)
     qmm.check()
     assert not ws[:4096].any()
-    want, size = ref.attend(qh, cache, table, lens, cu, page, group, scale, window)
+    want, sizes = ref.attend(qh, cache, table, lens, cu, page, group, scale, window)
     got = out.float().cpu().numpy().astype(np.float64)
-    err, tol = np.abs(got - want), tolerance(size, want, max(lens), D, dtype)
+    err, tol = np.abs(got - want), tolerance(sizes, want, max(lens), D, dtype)
     assert np.isfinite(got).all()
     assert (err <= tol).all(), f"{np.max(err / tol):.2f} of the tolerance"
     again = qmm.kv_attend(*args, **kw)
@@ -290,6 +313,111 @@ def test_attend_scales_over_many_decades(qmm, dtype):
     rng = np.random.default_rng(29)
     check_attend(qmm, rng, [400, 65], [1, 1], 4, 2, 128, 64, 16, dtype, spread=1e3, scale=0.01)
     check_attend(qmm, rng, [120], [90], 4, 2, 128, 64, 16, dtype, spread=1e3, scale=0.01)
+
+
+def many_rows(D):
+    """Rows of q of all requests and kv heads beyond which a bfloat16 call's prompts fill the GPU with tiles of them."""
+    return {64: 8700, 128: 7400, 256: 4000}[D]
+
+
+@pytest.mark.parametrize("D,group,page", [(64, 32, 16), (64, 64, 64), (128, 32, 32), (128, 64, 16), (128, 64, 256),
+                                          (128, 128, 64), (256, 32, 128), (256, 64, 64), (256, 128, 16)])
+def test_attend_many_rows(qmm, D, group, page):
+    rng = np.random.default_rng(D + group + page)
+    assert 5 * 130 * 16 > many_rows(D) and 280 * 33 > many_rows(D)
+    check_attend(qmm, rng, [130, 61, 200, 0, 1], [130, 33, 65, 0, 1], 16, 2, D, group, page, "bfloat16")
+    check_attend(qmm, rng, [150, 140], [140, 40], 33, 1, D, group, page, "bfloat16", window=37, strided=True)
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+def test_attend_many_rows_of_few_tokens(qmm, D, group):
+    """One partly filled tile a request and head, some requests empty, some with queries before their start."""
+    rng = np.random.default_rng(D)
+    fresh = [8] + rng.integers(0, 9, 29).tolist()
+    lens = rng.integers(0, 150, 30).tolist()
+    lens[3], lens[7] = 0, 3
+    assert 30 * 5 * 64 > many_rows(D)
+    check_attend(qmm, rng, lens, fresh, 40, 5, D, group, 32, "bfloat16")
+    check_attend(qmm, rng, lens, fresh, 40, 5, D, group, 16, "bfloat16", window=5, holes=True)
+
+
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 128)])
+def test_attend_many_rows_small_large_and_missing(qmm, D, group):
+    rng = np.random.default_rng(D + 1)
+    case = ([260, 90], [130, 60], 64, 2, D, group, 16, "bfloat16")
+    check_attend(qmm, rng, *case, holes=True)
+    check_attend(qmm, rng, *case, spread=1e3, scale=0.01)               # scales up to 300
+    check_attend(qmm, rng, *case, spread=1.0, scale=2.0 * D ** -0.5)    # peaked: the maxima keep growing
+    check_attend(qmm, rng, *case, size=2.0 ** -8, scale=256 * D ** -0.5)   # keys and values of 0.004
+
+
+@pytest.mark.parametrize("H,Hkv", [(4, 2), (64, 2)])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_attend_non_finite_values(qmm, D, group, H, Hkv, dtype):
+    """A value whose coefficients are not finite reaches the queries that see it, its head and its group, nothing else;
+    an infinite key is as good as any where it is not seen."""
+    import torch
+    rng = np.random.default_rng(D + H)
+    page, n, length, G = 16, 140, 150, D // group
+    cache = make_cache(rng, 12, Hkv, D, page, group)
+    table = rng.permutation(12).astype(np.int32)[None, :10]
+    clean = cache.copy()
+
+    def coef(token, head, part, g, k):
+        tile = cache[table[0, token // page], head].reshape(page // 16, -1)[token % page // 16]
+        at = 16 * D + part * 64 * G + ((8 * (token % 2) + 2 * (token % 16 // 4) + (token // 2) % 2) * G + g) * 4 + 2 * k
+        return tile[at:at + 2].view(np.uint16)
+
+    spots = [(77, 1, G - 1), (139, 0, 0)]                   # token, head, group
+    first, ratio = length - n, H // Hkv
+    q = dev(rng.standard_normal((n, H, D)).astype(np.float32)).to(getattr(torch, dtype))
+    cu = np.array([0, n], np.int32)
+    want, sizes = ref.attend(q.float().cpu().numpy(), clean, table, [length], cu, page, group, D ** -0.5, 0)
+    tol = np.broadcast_to(tolerance(sizes, want, length, D, dtype), want.shape)
+    hit = np.zeros(want.shape, bool)
+    for token, head, g in spots:
+        hit[token - first:, head * ratio:(head + 1) * ratio, g * group:(g + 1) * group] = True
+    rest = ~hit
+    rest[-1, :ratio] = False                                # what an infinite key does to the query that sees it is not
+    hit[-1, :ratio] = False                                 # looked at
+    ws = qmm.kv_attend_workspace(1, H, Hkv, D, n)
+    for k, bits in ((0, 0x7E01), (1, 0x7C00), (0, 0x7C00)):     # a NaN scale, an infinite bias, an infinite scale
+        cache[:] = clean
+        for token, head, g in spots:
+            coef(token, head, 1, g, k)[:] = bits
+        coef(149, 0, 0, 0, 1)[:] = 0x7C00                   # the last key: seen by the last query alone
+        got = qmm.kv_attend(q, dev(cache), dev(table), dev(np.array([length], np.int32)), page, group, ws, cu=dev(cu),
+                            max_fresh=n).float().cpu().numpy()
+        qmm.check()
+        assert not np.isfinite(got[hit]).any()
+        assert (np.abs(got - want)[rest] <= tol[rest]).all()
+
+
+def test_large_cache(qmm):
+    """Pages beyond 4 GiB of a cache hold and give what pages at its start do."""
+    import torch
+    page, Hkv, D, group, n = 256, 8, 128, 64, 1300
+    pages = (1 << 32) // (Hkv * (page // 16) * ref.tile_bytes(D, group)) + 40
+    cache = qmm.kv_cache(pages, Hkv, D, page, group)
+    torch.manual_seed(5)
+    k, v = torch.randn(2, n, Hkv, D, device="cuda").unbind(0)
+    cu, lens, ws = dev(np.array([0, n], np.int32)), dev(np.array([n], np.int32)), qmm.kv_attend_workspace(1, 32, Hkv, D, n)
+    got = []
+    for first in (0, pages - 6):
+        table = torch.arange(first, first + 6, dtype=torch.int32, device="cuda")[None].contiguous()
+        slots = first * page + torch.arange(n, dtype=torch.int32, device="cuda")
+        qmm.kv_append(k, v, slots, cache, page, group)
+        outs = list(qmm.kv_read(slots, cache, D, page, group))
+        for dtype in (torch.float32, torch.bfloat16):
+            torch.manual_seed(6)
+            q = torch.randn(n, 32, D, device="cuda").to(dtype)
+            outs.append(qmm.kv_attend(q, cache, table, lens, page, group, ws, cu=cu, max_fresh=n))
+            outs.append(qmm.kv_attend(q[:1], cache, table, lens, page, group, ws))
+        qmm.check()
+        got.append(outs)
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert all(bool((x != 0).any()) for x in got[1])
 
 
 def test_attend_more_requests_than_threads(qmm):
