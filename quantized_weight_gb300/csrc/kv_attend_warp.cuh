@@ -174,9 +174,6 @@ __device__ __forceinline__ int row_exp(uint32_t mbits) {
   return S > 126 ? 126 : S;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // 16 bytes, or zeros for `bytes` 0 (nothing is read then)
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -278,29 +275,34 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
   const int B = (int)a.B, hkv = p.g.kv_heads, head = p.head;
   const int per = (B + C::THREADS - 1) / C::THREADS;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  int mine = 0, parts_b = 0;
+  int64_t mine64 = 0;
+  int parts_b = 0;
   Req r{};                                                           // where a thread has one request: that one
   for (int b = b0; b < b1; b++) {
     r = request<ROWS, UNIT>(p, b, head);
-    mine += r.steps * r.tiles * hkv;
-    parts_b += (r.units + p.min_units - 1) / p.min_units * r.tiles * hkv;
+    mine64 += (int64_t)r.steps * r.tiles * hkv;
+    parts_b = (int)min((int64_t)parts_b + (int64_t)((r.units + p.min_units - 1) / p.min_units) * r.tiles * hkv, (int64_t)1024);
   }
+  const int mine = (int)min(mine64, (int64_t)0x7FFFFFFF);
   int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
-  parts_b = (int)__reduce_add_sync(0xffffffffu, (unsigned)parts_b);
-  if (lane == 31) scan[warp] = inc, scan[W + warp] = parts_b;
+  // teams asked for, and the line's length again in 2^20 steps, which does not wrap where the one in steps does
+  const unsigned sums = __reduce_add_sync(0xffffffffu, (unsigned)parts_b | (unsigned)min(mine >> 20, 2047) << 16);
+  if (lane == 31) scan[warp] = inc, scan[W + warp] = (int)sums;
   __syncthreads();
-  int total = 0, before = inc - mine, want = 0;                      // want: teams, an item having one per min_units begun
+  int total = 0, before = inc - mine, want = 0, long_line = 0;       // want: teams, an item having one per min_units begun
 #pragma unroll
   for (int w = 0; w < W; w++) {
     if (w < warp) before += scan[w];
     total += scan[w];
-    want += scan[W + w];
+    want += scan[W + w] & 0xFFFF;
+    long_line += (unsigned)scan[W + w] >> 16;
   }
+  if (long_line >= 1536) return;                                     // offsets that overlap: not a step's
   const int A = min(min(want, total), (int)gridDim.x * (W / tw));
   if (A == 0) return;
   // Team c begins at cut c, which leaves c / A of the line before it, moved to

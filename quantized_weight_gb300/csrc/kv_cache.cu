@@ -318,53 +318,53 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(const AppendParams 
     fetch(hv0);
 #pragma unroll 1
     for (int hv = hv0; hv < hv1; hv++) {
-    const int h = hv >> 1;
-    const bool isv = hv & 1;
-    Raw<BF16> x[PASSES];
+      const int h = hv >> 1;
+      const bool isv = hv & 1;
+      Raw<BF16> x[PASSES];
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ps++) x[ps] = ahead[ps];
-    if (hv + 1 < hv1) fetch(hv + 1);
-    uint8_t *tile = p.cache + kv_tile_at(g, slot, h);
+      for (int ps = 0; ps < PASSES; ps++) x[ps] = ahead[ps];
+      if (hv + 1 < hv1) fetch(hv + 1);
+      uint8_t *tile = p.cache + kv_tile_at(g, slot, h);
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ps++) {
-      const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15);
-      uint32_t coef;
-      const uint32_t word = quantize8<BF16>(x[ps], lanes, coef), other = __shfl_xor_sync(0xffffffffu, word, 1);
-      if (r < n && (m & (lanes - 1)) == 0)
-        *reinterpret_cast<uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))) = coef;
-      if (!isv) {
-        if (r < n) *reinterpret_cast<uint32_t *>(tile + kv_k_word(D, row, m)) = word;
-      } else {
-        // this lane's four bytes: elements e, e + 8 of its 16, e from 0 (even m) or 4 (odd m)
-        const uint32_t lw = (m & 1 ? other : word) >> (16 * (m & 1)), hw = (m & 1 ? word : other) >> (16 * (m & 1));
-        const uint32_t lx = (lw & 0xFu) | (lw & 0xF0u) << 4 | (lw & 0xF00u) << 8 | (lw & 0xF000u) << 12;
-        const uint32_t hx = (hw & 0xFu) | (hw & 0xF0u) << 4 | (hw & 0xF00u) << 8 | (hw & 0xF000u) << 12;
-        const uint32_t by = lx | hx << 4;
-        if constexpr (n == 4) {
-          *reinterpret_cast<uint32_t *>(bytes + r * (D / 2) + 4 * m) = by;
-        } else if (r < n) {
+      for (int ps = 0; ps < PASSES; ps++) {
+        const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15);
+        uint32_t coef;
+        const uint32_t word = quantize8<BF16>(x[ps], lanes, coef), other = __shfl_xor_sync(0xffffffffu, word, 1);
+        if (r < n && (m & (lanes - 1)) == 0)
+          *reinterpret_cast<uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))) = coef;
+        if (!isv) {
+          if (r < n) *reinterpret_cast<uint32_t *>(tile + kv_k_word(D, row, m)) = word;
+        } else {
+          // this lane's four bytes: elements e, e + 8 of its 16, e from 0 (even m) or 4 (odd m)
+          const uint32_t lw = (m & 1 ? other : word) >> (16 * (m & 1)), hw = (m & 1 ? word : other) >> (16 * (m & 1));
+          const uint32_t lx = (lw & 0xFu) | (lw & 0xF0u) << 4 | (lw & 0xF00u) << 8 | (lw & 0xF000u) << 12;
+          const uint32_t hx = (hw & 0xFu) | (hw & 0xF0u) << 4 | (hw & 0xF00u) << 8 | (hw & 0xF000u) << 12;
+          const uint32_t by = lx | hx << 4;
+          if constexpr (n == 4) {
+            *reinterpret_cast<uint32_t *>(bytes + r * (D / 2) + 4 * m) = by;
+          } else if (r < n) {
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            tile[kv_v_word(D, 16 * (m >> 1) + 4 * (m & 1) + i, j >> 2) + (j & 3)] = (uint8_t)(by >> (8 * i));
-        }
-      }
-    }
-    if constexpr (n == 4) {
-      if (isv) {
-        __syncwarp();
-        if (lane < D / 8) {                                // (c, e): a word of each 16 elements of 64, four tokens a word
-          const int c = lane >> 3, e = lane & 7;
-          uint32_t o[4];
-#pragma unroll
-          for (int w = 0; w < 4; w++) {
-            const uint8_t *b = bytes + (4 * c + w) * 8 + e;
-            o[w] = b[0] | (uint32_t)b[D / 2] << 8 | (uint32_t)b[2 * (D / 2)] << 16 | (uint32_t)b[3 * (D / 2)] << 24;
+            for (int i = 0; i < 4; i++)
+              tile[kv_v_word(D, 16 * (m >> 1) + 4 * (m & 1) + i, j >> 2) + (j & 3)] = (uint8_t)(by >> (8 * i));
           }
-          *reinterpret_cast<uint4 *>(tile + kv_v_word(D, 64 * c + e, (slot & 15) >> 2)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        __syncwarp();
       }
-    }
+      if constexpr (n == 4) {
+        if (isv) {
+          __syncwarp();
+          if (lane < D / 8) {                                // (c, e): a word of each 16 elements of 64, four tokens a word
+            const int c = lane >> 3, e = lane & 7;
+            uint32_t o[4];
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+              const uint8_t *b = bytes + (4 * c + w) * 8 + e;
+              o[w] = b[0] | (uint32_t)b[D / 2] << 8 | (uint32_t)b[2 * (D / 2)] << 16 | (uint32_t)b[3 * (D / 2)] << 24;
+            }
+            *reinterpret_cast<uint4 *>(tile + kv_v_word(D, 64 * c + e, (slot & 15) >> 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          __syncwarp();
+        }
+      }
     }
   };
   each_run(p.r, unit, [&](int64_t t, int slot) { rows(std::integral_constant<int, 4>(), t, slot); },
@@ -427,70 +427,70 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
   auto rows = [&](auto count, int64_t t, int slot) {
 #pragma unroll 1
     for (int hv = hv0; hv < hv1; hv++) {
-    const int h = hv >> 1;
-    const bool isv = hv & 1;
-    uint8_t *dst = static_cast<uint8_t *>(isv ? p.v : p.k);
-    constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
-    const uint8_t *tile = p.cache + (slot >= 0 ? kv_tile_at(g, slot, h) : 0);
-    uint32_t coef[PASSES], q[PASSES][2];                   // codes: bytes of elements 0..3 and 4..7
+      const int h = hv >> 1;
+      const bool isv = hv & 1;
+      uint8_t *dst = static_cast<uint8_t *>(isv ? p.v : p.k);
+      constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
+      const uint8_t *tile = p.cache + (slot >= 0 ? kv_tile_at(g, slot, h) : 0);
+      uint32_t coef[PASSES], q[PASSES][2];                   // codes: bytes of elements 0..3 and 4..7
 #pragma unroll
-    for (int ps = 0; ps < PASSES; ps++) {
-      const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = m >> g.lg_group8;
-      coef[ps] = q[ps][0] = q[ps][1] = 0u;
-      if (r < n && slot >= 0) {
-        coef[ps] = *(reinterpret_cast<const uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))));
-        if (!isv) {
-          const uint32_t w = *(reinterpret_cast<const uint32_t *>(tile + kv_k_word(D, row, m)));
-          const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;   // even and odd elements
-          q[ps][0] = prmt(a, b, 0x5140u);
-          q[ps][1] = prmt(a, b, 0x7362u);
-        } else if (n == 1) {
-          uint32_t x = 0, y = 0;
+      for (int ps = 0; ps < PASSES; ps++) {
+        const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = m >> g.lg_group8;
+        coef[ps] = q[ps][0] = q[ps][1] = 0u;
+        if (r < n && slot >= 0) {
+          coef[ps] = *(reinterpret_cast<const uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))));
+          if (!isv) {
+            const uint32_t w = *(reinterpret_cast<const uint32_t *>(tile + kv_k_word(D, row, m)));
+            const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;   // even and odd elements
+            q[ps][0] = prmt(a, b, 0x5140u);
+            q[ps][1] = prmt(a, b, 0x7362u);
+          } else if (n == 1) {
+            uint32_t x = 0, y = 0;
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            x |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + i, j >> 2) + (j & 3)] << (8 * i);
-            y |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + 4 + i, j >> 2) + (j & 3)] << (8 * i);
+            for (int i = 0; i < 4; i++) {
+              x |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + i, j >> 2) + (j & 3)] << (8 * i);
+              y |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + 4 + i, j >> 2) + (j & 3)] << (8 * i);
+            }
+            q[ps][0] = (x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+            q[ps][1] = (y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
           }
-          q[ps][0] = (x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-          q[ps][1] = (y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
         }
       }
-    }
-    if constexpr (n == 4) {
-      if (isv) {
-        if (lane < D / 8) {
-          const int c = lane >> 3, e = lane & 7;
-          const uint4 o = *(reinterpret_cast<const uint4 *>(tile + kv_v_word(D, 64 * c + e, (slot & 15) >> 2)));
-          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+      if constexpr (n == 4) {
+        if (isv) {
+          if (lane < D / 8) {
+            const int c = lane >> 3, e = lane & 7;
+            const uint4 o = *(reinterpret_cast<const uint4 *>(tile + kv_v_word(D, 64 * c + e, (slot & 15) >> 2)));
+            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-          for (int i = 0; i < 4; i++)
+            for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) bytes[r * (D / 2) + (4 * c + i) * 8 + e] = (uint8_t)(w[i] >> (8 * r));
+              for (int r = 0; r < 4; r++) bytes[r * (D / 2) + (4 * c + i) * 8 + e] = (uint8_t)(w[i] >> (8 * r));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int ps = 0; ps < PASSES; ps++) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(bytes + (ps * RP + sub) * (D / 2) + 8 * (m >> 1));
+            q[ps][0] = (x.x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+            q[ps][1] = (x.y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+          }
+          __syncwarp();
         }
-        __syncwarp();
+      }
 #pragma unroll
-        for (int ps = 0; ps < PASSES; ps++) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(bytes + (ps * RP + sub) * (D / 2) + 8 * (m >> 1));
-          q[ps][0] = (x.x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-          q[ps][1] = (x.y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+      for (int ps = 0; ps < PASSES; ps++) {
+        const int r = ps * RP + sub;
+        if (r < n) {
+          float v[8];
+          const float s = h2f((uint16_t)coef[ps]), b = h2f((uint16_t)(coef[ps] >> 16));
+          values4(q[ps][0], s, b, v);
+          values4(q[ps][1], s, b, v + 4);
+          if (slot < 0)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = __int_as_float(0x7FC00000);
+          store8<BF16>(dst + (((t + r) * g.kv_heads + h) * D + 8 * m) * (BF16 ? 2 : 4), v);
         }
-        __syncwarp();
       }
-    }
-#pragma unroll
-    for (int ps = 0; ps < PASSES; ps++) {
-      const int r = ps * RP + sub;
-      if (r < n) {
-        float v[8];
-        const float s = h2f((uint16_t)coef[ps]), b = h2f((uint16_t)(coef[ps] >> 16));
-        values4(q[ps][0], s, b, v);
-        values4(q[ps][1], s, b, v + 4);
-        if (slot < 0)
-#pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = __int_as_float(0x7FC00000);
-        store8<BF16>(dst + (((t + r) * g.kv_heads + h) * D + 8 * m) * (BF16 ? 2 : 4), v);
-      }
-    }
     }
   };
   each_run(p.r, unit, [&](int64_t t, int slot) { rows(std::integral_constant<int, 4>(), t, slot); },

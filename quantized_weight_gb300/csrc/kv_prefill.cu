@@ -174,6 +174,16 @@ struct Phase {
   }
 };
 
+// A warp's wait.  What waits longer than a first look does it in one place for all: the roles' code has to stay in the
+// instruction caches.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, WaitCtl{abort, &g_kv_status}));
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, ctl.abort);
+}
+
 // One warp, the seldom path of the softmax: this lane's row of O (unless o_tm is all ones) and of the first `cols`
 // columns of P (two binary16 values each) times f.  Not inlined, so that it takes no registers from the path that is run.
 template <int D>
@@ -257,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   int it_slot = 0;
   uint32_t it_ph = 0;
   auto next_item = [&]() -> const Item * {
-    if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_FULL + it_slot), it_ph, ctl))) return nullptr;
+    if (!warp_wait(bar(IT_FULL + it_slot), it_ph, ctl)) return nullptr;
     return items[it_slot].tiles > 0 ? items + it_slot : nullptr;
   };
   auto release = [&]() {
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     uint32_t ph = 1, next = 1;
     for (int slot = 0;;) {
       // A ticket is drawn when the keys of the item before it are done: earlier, CTAs would sit on items that others could begin.
-      if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_NEXT), next, ctl))) break;
+      if (!warp_wait(bar(IT_NEXT), next, ctl)) break;
       next ^= 1u;
       unsigned t = 0;
       if (lane == 0) t = atomicAdd(ticket, 1u);
@@ -326,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
         cfirst += all;
       }
-      if (!__all_sync(0xffffffffu, wait_bounded(bar(IT_EMPTY + slot), ph, ctl))) break;
+      if (!warp_wait(bar(IT_EMPTY + slot), ph, ctl)) break;
       if (lane == 0) {
         items[slot] = it;
         mbar_arrive(bar(IT_FULL + slot));
@@ -371,9 +381,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         };
         auto ready = [&](int i) -> bool {
           const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
-          if (i < nt && !__all_sync(0xffffffffu, wait_bounded(bar(Q_FULL + x), qf[x].next(), ctl))) return false;
+          if (i < nt && !warp_wait(bar(Q_FULL + x), qf[x].next(), ctl)) return false;
           if (j != k_at) {
-            if (!__all_sync(0xffffffffu, wait_bounded(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl))) return false;
+            if (!warp_wait(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl)) return false;
             k_at = j;
             kb++;
           }
@@ -402,12 +412,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
           // V, then P; the next keys are looked for before P, which mostly comes last, and waited for after its product.
           if (j != v_at) {
-            if (!__all_sync(0xffffffffu, wait_bounded(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl))) { ok = false; break; }
+            if (!warp_wait(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl)) { ok = false; break; }
             v_at = j;
             vb++;
           }
           if (i + 2 < N) looked(i + 2);
-          if (!__all_sync(0xffffffffu, wait_bounded(bar(P_FULL + buf), pf[buf].next(), ctl))) { ok = false; break; }
+          if (!warp_wait(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
           tc_fence_after();
           const uint32_t vd = uniform(desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4));
           const uint32_t ot = uniform(tm0 + 256 + x * D), pt = uniform(tm0 + buf * 128);
@@ -438,256 +448,256 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     // ------------------------------------------------------------ codes: keys
     // One warpgroup has both, or, where there is no second row tile, its softmax warps take the keys.
     auto codes = [&](auto with_keys, auto with_values) {
-    constexpr bool KEYS = decltype(with_keys)::value, VALUES = decltype(with_values)::value;
-    constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
-    constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
-    constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
-    const int w4 = warp & 3, t = lane & 3;
-    // values
-    constexpr int CB = D / 64;                               // blocks of 64 elements
-    constexpr int GV = G > CB ? 2 : 1;                       // groups in one (group of 32: two)
-    constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
-    const int u = threadIdx.x & 127, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
-    const bool act = u < UNITS;
-    Phase ke[2], ve[2];
-    ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
-    int kb = 0, n_item = 0;                                  // blocks and items before
-    bool ok = true;
-    for (; const Item *ip = next_item(); n_item++) {
-      const Item &it = *ip;
-      // this item's notes, last used four items ago
-      uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
-      if constexpr (VALUES) {
-        for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
-        if (u == 0) noted[n_item & 3] = 0;
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      }
-      const int32_t *tab = a.table + it.b * a.max_blocks;
-      uint32_t w[PW][WC], cf[PW][GK];
-      int pid[PW];
-      auto pages = [&](int blk) {
-#pragma unroll
-        for (int i = 0; i < PW; i++) {
-          const int64_t tok = (int64_t)blk * KB + ((i * 4 + w4) / (2 * NC)) * 16;
-          pid[i] = tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+      constexpr bool KEYS = decltype(with_keys)::value, VALUES = decltype(with_values)::value;
+      constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
+      constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
+      constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
+      const int w4 = warp & 3, t = lane & 3;
+      // values
+      constexpr int CB = D / 64;                               // blocks of 64 elements
+      constexpr int GV = G > CB ? 2 : 1;                       // groups in one (group of 32: two)
+      constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
+      const int u = threadIdx.x & 127, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
+      const bool act = u < UNITS;
+      Phase ke[2], ve[2];
+      ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
+      int kb = 0, n_item = 0;                                  // blocks and items before
+      bool ok = true;
+      for (; const Item *ip = next_item(); n_item++) {
+        const Item &it = *ip;
+        // this item's notes, last used four items ago
+        uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
+        if constexpr (VALUES) {
+          for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
+          if (u == 0) noted[n_item & 3] = 0;
+          asm volatile("bar.sync 1, 128;" ::: "memory");
         }
-      };
-      uint32_t valid = 0;                                    // tiles of the block with a page, as far as this warp has them
-      auto fetch_keys = [&](int blk) {
-        valid = 0;
+        const int32_t *tab = a.table + it.b * a.max_blocks;
+        uint32_t w[PW][WC], cf[PW][GK];
+        int pid[PW];
+        auto pages = [&](int blk) {
 #pragma unroll
-        for (int i = 0; i < PW; i++) {
-          const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
-          const bool there = pid[i] >= 0 && pid[i] < p.g.pages;
-          if (there) {
-            const int tok = blk * KB + tl * 16;
-            const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pid[i] * hkv + it.kvh) * p.g.head_bytes +
-                               ((tok & (p.g.page - 1)) >> 4) * TILE;
-            valid |= 1u << tl;
-            if constexpr (WC == 4) {
-              const uint4 v = *(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
-              w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+          for (int i = 0; i < PW; i++) {
+            const int64_t tok = (int64_t)blk * KB + ((i * 4 + w4) / (2 * NC)) * 16;
+            pid[i] = tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+          }
+        };
+        uint32_t valid = 0;                                    // tiles of the block with a page, as far as this warp has them
+        auto fetch_keys = [&](int blk) {
+          valid = 0;
+#pragma unroll
+          for (int i = 0; i < PW; i++) {
+            const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+            const bool there = pid[i] >= 0 && pid[i] < p.g.pages;
+            if (there) {
+              const int tok = blk * KB + tl * 16;
+              const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pid[i] * hkv + it.kvh) * p.g.head_bytes +
+                                 ((tok & (p.g.page - 1)) >> 4) * TILE;
+              valid |= 1u << tl;
+              if constexpr (WC == 4) {
+                const uint4 v = *(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
+                w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+              } else {
+                const uint2 v = *(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
+                w[i][0] = v.x, w[i][1] = v.y;
+              }
+              const uint8_t *cp = s + 16 * D + (row * G + c * GK) * 4;
+              if constexpr (GK == 1) {
+                cf[i][0] = *(reinterpret_cast<const uint32_t *>(cp));
+              } else if constexpr (GK == 2) {
+                const uint2 v = *(reinterpret_cast<const uint2 *>(cp));
+                cf[i][0] = v.x, cf[i][1] = v.y;
+              } else {
+                const uint4 v = *(reinterpret_cast<const uint4 *>(cp));
+                cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
+              }
             } else {
-              const uint2 v = *(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
-              w[i][0] = v.x, w[i][1] = v.y;
+#pragma unroll
+              for (int j = 0; j < WC; j++) w[i][j] = 0u;
+#pragma unroll
+              for (int j = 0; j < GK; j++) cf[i][j] = 0u;
             }
-            const uint8_t *cp = s + 16 * D + (row * G + c * GK) * 4;
-            if constexpr (GK == 1) {
-              cf[i][0] = *(reinterpret_cast<const uint32_t *>(cp));
-            } else if constexpr (GK == 2) {
-              const uint2 v = *(reinterpret_cast<const uint2 *>(cp));
-              cf[i][0] = v.x, cf[i][1] = v.y;
-            } else {
-              const uint4 v = *(reinterpret_cast<const uint4 *>(cp));
-              cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
+          }
+        };
+        auto page_of = [&](int blk) {
+          const int64_t tok = (int64_t)blk * KB + vt * 16;
+          return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+        };
+        uint4 vw[4];
+        uint32_t vf[16][GV];
+        const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
+        auto fetch_values = [&](int blk, int pg) {
+          coefs = nullptr;
+          if (pg >= 0 && pg < p.g.pages) {
+            const int64_t tok = (int64_t)blk * KB + vt * 16;
+            const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
+                               (((int)tok & (p.g.page - 1)) >> 4) * TILE;
+            const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (vc * 8 + g8) * 64);
+#pragma unroll
+            for (int i = 0; i < 4; i++) vw[i] = s[i];
+            const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * vc : vc * G / CB) * 4;
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+              if constexpr (GV == 1) {
+                vf[r][0] = *(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
+              } else {
+                const uint2 v = *(reinterpret_cast<const uint2 *>(cp + r * G * 4));
+                vf[r][0] = v.x, vf[r][GV - 1] = v.y;
+              }
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < WC; j++) w[i][j] = 0u;
+            for (int i = 0; i < 4; i++) vw[i] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int j = 0; j < GK; j++) cf[i][j] = 0u;
+            for (int r = 0; r < 16; r++)
+#pragma unroll
+              for (int g = 0; g < GV; g++) vf[r][g] = 0u;
+          }
+        };
+        int pg_next = -1;
+        if (it.blocks > 0) {
+          if constexpr (KEYS) pages(it.blk0);
+          if constexpr (VALUES) pg_next = page_of(it.blk0);
+          if constexpr (KEYS) fetch_keys(it.blk0);
+          if constexpr (VALUES) fetch_values(it.blk0, pg_next);
+          if (it.blocks > 1) {
+            if constexpr (KEYS) pages(it.blk0 + 1);
+            if constexpr (VALUES) pg_next = page_of(it.blk0 + 1);
           }
         }
-      };
-      auto page_of = [&](int blk) {
-        const int64_t tok = (int64_t)blk * KB + vt * 16;
-        return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
-      };
-      uint4 vw[4];
-      uint32_t vf[16][GV];
-      const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
-      auto fetch_values = [&](int blk, int pg) {
-        coefs = nullptr;
-        if (pg >= 0 && pg < p.g.pages) {
-          const int64_t tok = (int64_t)blk * KB + vt * 16;
-          const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
-                             (((int)tok & (p.g.page - 1)) >> 4) * TILE;
-          const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (vc * 8 + g8) * 64);
+        for (int j = 0; j < it.blocks; j++, kb++) {
+          const int blk = it.blk0 + j, buf = kb & 1;
+          if constexpr (KEYS) {
+            if (!warp_wait(bar(K_EMPTY + buf), ke[buf].next(), ctl)) { ok = false; break; }
+            {
+              const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
+              uint32_t most = 0;
 #pragma unroll
-          for (int i = 0; i < 4; i++) vw[i] = s[i];
-          const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * vc : vc * G / CB) * 4;
+              for (int i = 0; i < PW; i++)
 #pragma unroll
-          for (int r = 0; r < 16; r++) {
-            if constexpr (GV == 1) {
-              vf[r][0] = *(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
-            } else {
-              const uint2 v = *(reinterpret_cast<const uint2 *>(cp + r * G * 4));
-              vf[r][0] = v.x, vf[r][GV - 1] = v.y;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; i++) vw[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int r = 0; r < 16; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++) vf[r][g] = 0u;
-        }
-      };
-      int pg_next = -1;
-      if (it.blocks > 0) {
-        if constexpr (KEYS) pages(it.blk0);
-        if constexpr (VALUES) pg_next = page_of(it.blk0);
-        if constexpr (KEYS) fetch_keys(it.blk0);
-        if constexpr (VALUES) fetch_values(it.blk0, pg_next);
-        if (it.blocks > 1) {
-          if constexpr (KEYS) pages(it.blk0 + 1);
-          if constexpr (VALUES) pg_next = page_of(it.blk0 + 1);
-        }
-      }
-      for (int j = 0; j < it.blocks; j++, kb++) {
-        const int blk = it.blk0 + j, buf = kb & 1;
-        if constexpr (KEYS) {
-        if (!__all_sync(0xffffffffu, wait_bounded(bar(K_EMPTY + buf), ke[buf].next(), ctl))) { ok = false; break; }
-        {
-          const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
-          uint32_t most = 0;
-#pragma unroll
-          for (int i = 0; i < PW; i++)
-#pragma unroll
-            for (int k = 0; k < GK; k++) most = max(most, cf[i][k] & 0x7FFFu);
-          const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
+                for (int k = 0; k < GK; k++) most = max(most, cf[i][k] & 0x7FFFu);
+              const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
 #pragma unroll 1
-          for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
-            const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
-            const int pos = tl * 16 + row;
+              for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
+                const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+                const int pos = tl * 16 + row;
 #pragma unroll
-            for (int k = 0; k < WC; k++) {
-              const uint32_t cc = cf[0][k / (WC / GK)], x = w[0][k];
-              const uint32_t b2 = hmul2(prmt(cc, cc, 0x3232), 0x2C002C00u /* 1/16 */);
-              // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
-              uint32_t e04, e15, e26, e37;
-              if (!large) {
-                const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x74007400u /* 2^14 */);
-                e04 = hfma2(x << 6 & 0x03C003C0u, s2, b2), e15 = hfma2(x << 2 & 0x03C003C0u, s2, b2);
-                e26 = hfma2(x >> 2 & 0x03C003C0u, s2, b2), e37 = hfma2(x >> 6 & 0x03C003C0u, s2, b2);
-              } else {
-                const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x2C002C00u), y = x >> 8;
-                e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
-                e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+                for (int k = 0; k < WC; k++) {
+                  const uint32_t cc = cf[0][k / (WC / GK)], x = w[0][k];
+                  const uint32_t b2 = hmul2(prmt(cc, cc, 0x3232), 0x2C002C00u /* 1/16 */);
+                  // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
+                  uint32_t e04, e15, e26, e37;
+                  if (!large) {
+                    const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x74007400u /* 2^14 */);
+                    e04 = hfma2(x << 6 & 0x03C003C0u, s2, b2), e15 = hfma2(x << 2 & 0x03C003C0u, s2, b2);
+                    e26 = hfma2(x >> 2 & 0x03C003C0u, s2, b2), e37 = hfma2(x >> 6 & 0x03C003C0u, s2, b2);
+                  } else {
+                    const uint32_t s2 = hmul2(prmt(cc, cc, 0x1010), 0x2C002C00u), y = x >> 8;
+                    e04 = hfma2(codes_lo(x), s2, b2), e15 = hfma2(codes_hi(x), s2, b2);
+                    e26 = hfma2(codes_lo(y), s2, b2), e37 = hfma2(codes_hi(y), s2, b2);
+                  }
+                  const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
+                  sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
+                         prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+                }
+#pragma unroll
+                for (int n = 0; n + 1 < PW; n++) {
+#pragma unroll
+                  for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
+#pragma unroll
+                  for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
+                }
               }
-              const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
-              sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
-                     prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
+              if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
             }
-#pragma unroll
-            for (int n = 0; n + 1 < PW; n++) {
-#pragma unroll
-              for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
-#pragma unroll
-              for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
+            fence_proxy_async_smem();
+            mbar_arrive(bar(K_FULL + buf));
+            if (j + 1 < it.blocks) {
+              fetch_keys(blk + 1);
+              if (j + 2 < it.blocks) pages(blk + 2);
             }
           }
-          if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(K_FULL + buf));
-        if (j + 1 < it.blocks) {
-          fetch_keys(blk + 1);
-          if (j + 2 < it.blocks) pages(blk + 2);
-        }
-        }
-        if constexpr (VALUES) {
-        if (!__all_sync(0xffffffffu, wait_bounded(bar(V_EMPTY + buf), ve[buf].next(), ctl))) { ok = false; break; }
-        // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
-        // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
-        // noted for the rows that do.
-        const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
-        if (edge) {
-          uint32_t out[GV] = {};                             // rows to zero, by group
-          const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
+          if constexpr (VALUES) {
+            if (!warp_wait(bar(V_EMPTY + buf), ve[buf].next(), ctl)) { ok = false; break; }
+            // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
+            // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
+            // noted for the rows that do.
+            const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
+            if (edge) {
+              uint32_t out[GV] = {};                             // rows to zero, by group
+              const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
 #pragma unroll 1
-          for (int r = 0; r < 16; r++) {
-            const int64_t tok = (int64_t)blk * KB + vt * 16 + token_of(r);
+              for (int r = 0; r < 16; r++) {
+                const int64_t tok = (int64_t)blk * KB + vt * 16 + token_of(r);
 #pragma unroll
-            for (int g = 0; g < GV; g++) {
-              if (tok < it.vlo || tok >= it.vhi) {
-                out[g] |= 1u << r;
-              } else if (coefs) {
-                const uint32_t m = *(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
-                if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
-                  const int pos = vt * 16 + r, grp = (G > CB ? 2 * vc : vc * G / CB) + g;
-                  atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
-                  noted[n_item & 3] = 1;
-                  out[g] |= 1u << r;
+                for (int g = 0; g < GV; g++) {
+                  if (tok < it.vlo || tok >= it.vhi) {
+                    out[g] |= 1u << r;
+                  } else if (coefs) {
+                    const uint32_t m = *(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
+                    if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
+                      const int pos = vt * 16 + r, grp = (G > CB ? 2 * vc : vc * G / CB) + g;
+                      atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
+                      noted[n_item & 3] = 1;
+                      out[g] |= 1u << r;
+                    }
+                  }
+                }
+              }
+#pragma unroll
+              for (int r = 0; r < 16; r++)
+#pragma unroll
+                for (int g = 0; g < GV; g++)
+                  if ((out[g] >> r) & 1u) vf[r][g] = 0u;
+            }
+            if (act) {
+              uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
+#pragma unroll
+              for (int r = 0; r < 8; r++)
+#pragma unroll
+                for (int g = 0; g < GV; g++) {
+                  s2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x5410);
+                  b2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x7632);
+                }
+              uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (vt >> 2) * (D * 128) + (64 * vc + g8) * 128;
+              const uint32_t ch0 = (uint32_t)((((vt & 3) * 2) ^ g8) << 4), ch1 = (uint32_t)((((vt & 3) * 2 + 1) ^ g8) << 4);
+              // a word of each token quad at a time; the words move up in their registers, so that the loop stays rolled
+              // (unrolled, the five roles' code does not stay in the instruction caches)
+#pragma unroll 1
+              for (int w4 = 0; w4 < 4; w4++, dst += 16 * 128) {
+#pragma unroll
+                for (int odd = 0; odd < 2; odd++) {
+                  uint32_t lo[4], hi[4];
+#pragma unroll
+                  for (int t = 0; t < 4; t++) {
+                    const uint32_t y = vw[t].x >> (8 * odd);
+                    lo[t] = hfma2(codes_lo(y), s2[4 * odd + t], b2[4 * odd + t]);
+                    hi[t] = hfma2(codes_hi(y), s2[4 * odd + t], b2[4 * odd + t]);
+                  }
+                  sts128(dst + (odd ? ch1 : ch0), lo[0], lo[1], lo[2], lo[3]);
+                  sts128(dst + 8 * 128 + (odd ? ch1 : ch0), hi[0], hi[1], hi[2], hi[3]);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; t++) vw[t].x = vw[t].y, vw[t].y = vw[t].z, vw[t].z = vw[t].w;
+                if constexpr (GV == 2) {
+                  if (w4 == 1)                                     // the second group's coefficients
+#pragma unroll
+                    for (int r = 0; r < 8; r++) s2[r] = s2[8 * (GV - 1) + r], b2[r] = b2[8 * (GV - 1) + r];
                 }
               }
             }
-          }
-#pragma unroll
-          for (int r = 0; r < 16; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++)
-              if ((out[g] >> r) & 1u) vf[r][g] = 0u;
-        }
-        if (act) {
-          uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
-#pragma unroll
-          for (int r = 0; r < 8; r++)
-#pragma unroll
-            for (int g = 0; g < GV; g++) {
-              s2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x5410);
-              b2[g * 8 + r] = prmt(vf[2 * r][g], vf[2 * r + 1][g], 0x7632);
-            }
-          uint32_t dst = sb + C::OFF_V + buf * C::KV_BYTES + (vt >> 2) * (D * 128) + (64 * vc + g8) * 128;
-          const uint32_t ch0 = (uint32_t)((((vt & 3) * 2) ^ g8) << 4), ch1 = (uint32_t)((((vt & 3) * 2 + 1) ^ g8) << 4);
-          // a word of each token quad at a time; the words move up in their registers, so that the loop stays rolled
-          // (unrolled, the five roles' code does not stay in the instruction caches)
-#pragma unroll 1
-          for (int w4 = 0; w4 < 4; w4++, dst += 16 * 128) {
-#pragma unroll
-            for (int odd = 0; odd < 2; odd++) {
-              uint32_t lo[4], hi[4];
-#pragma unroll
-              for (int t = 0; t < 4; t++) {
-                const uint32_t y = vw[t].x >> (8 * odd);
-                lo[t] = hfma2(codes_lo(y), s2[4 * odd + t], b2[4 * odd + t]);
-                hi[t] = hfma2(codes_hi(y), s2[4 * odd + t], b2[4 * odd + t]);
-              }
-              sts128(dst + (odd ? ch1 : ch0), lo[0], lo[1], lo[2], lo[3]);
-              sts128(dst + 8 * 128 + (odd ? ch1 : ch0), hi[0], hi[1], hi[2], hi[3]);
-            }
-#pragma unroll
-            for (int t = 0; t < 4; t++) vw[t].x = vw[t].y, vw[t].y = vw[t].z, vw[t].z = vw[t].w;
-            if constexpr (GV == 2) {
-              if (w4 == 1)                                     // the second group's coefficients
-#pragma unroll
-                for (int r = 0; r < 8; r++) s2[r] = s2[8 * (GV - 1) + r], b2[r] = b2[8 * (GV - 1) + r];
+            fence_proxy_async_smem();
+            mbar_arrive(bar(V_FULL + buf));
+            if (j + 1 < it.blocks) {
+              fetch_values(blk + 1, pg_next);
+              if (j + 2 < it.blocks) pg_next = page_of(blk + 2);
             }
           }
         }
-        fence_proxy_async_smem();
-        mbar_arrive(bar(V_FULL + buf));
-        if (j + 1 < it.blocks) {
-          fetch_values(blk + 1, pg_next);
-          if (j + 2 < it.blocks) pg_next = page_of(blk + 2);
-        }
-        }
+        if (!ok) break;
+        if (KEYS && lane == 0) mbar_arrive(bar(IT_NEXT));
+        release();
       }
-      if (!ok) break;
-      if (KEYS && lane == 0) mbar_arrive(bar(IT_NEXT));
-      release();
-    }
     };
     if constexpr (NQ == 2) codes(std::true_type(), std::true_type());
     else if (warp < DQ_WARP0) codes(std::true_type(), std::false_type());
@@ -760,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       float m = NINF, l = 0.0f;                              // reference maximum (log2 units), sum
       for (int k = 0; k < it.blocks; k++) {
         const int buf = it.tiles == 2 ? x : k & 1, t0 = (it.blk0 + k) * KB;
-        if (!__all_sync(0xffffffffu, wait_bounded(bar(S_FULL + buf), (s_base[buf] + (it.tiles == 2 ? k : k >> 1)) & 1, ctl))) { ok = false; break; }
+        if (!warp_wait(bar(S_FULL + buf), (s_base[buf] + (it.tiles == 2 ? k : k >> 1)) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         const uint4 kv = kvalid[(blk_base + k) & 3];
         const uint32_t pages = kv.x | kv.y | kv.z | kv.w;
@@ -797,7 +807,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             const float mn = grow ? mx : m, f = mn == m ? 1.0f : ex2(m - mn);
             m = mn;
             l *= f;
-            if (k > 0 && !__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) ok = false;
+            if (k > 0 && !warp_wait(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl)) ok = false;
             rescale<D>(k > 0 ? o_tm : 0xFFFFFFFFu, s_tm, h / 2, f);
           }
           const float mu = m == NINF ? 0.0f : m;
@@ -832,13 +842,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         // A parity tells apart only a phase and the next, so no PV may finish before the one ahead of it has been seen: with
         // two row tiles, S of this step came after that PV; with one, it is waited for here, before the next is let go.
         if (it.tiles == 1 && k > 0 &&
-            !__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl))) { ok = false; break; }
+            !warp_wait(bar(PV_DONE + x), (pv_base + k - 1) & 1, ctl)) { ok = false; break; }
         mbar_arrive(bar(P_FULL + buf));
       }
       if (!ok) break;
       // ---------------------------------------------------------- output
       if (it.blocks > 0) {
-        if (!__all_sync(0xffffffffu, wait_bounded(bar(PV_DONE + x), (pv_base + it.blocks - 1) & 1, ctl))) { ok = false; break; }
+        if (!warp_wait(bar(PV_DONE + x), (pv_base + it.blocks - 1) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         pv_base += it.blocks;
       }
