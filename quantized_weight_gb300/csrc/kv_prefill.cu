@@ -451,7 +451,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       constexpr bool KEYS = decltype(with_keys)::value, VALUES = decltype(with_values)::value;
       constexpr int NC = D >= 128 ? D / 128 : 1, WC = D >= 128 ? 4 : D / 32;   // pieces of WC words
       constexpr int GK = G / NC;                               // groups in a piece's 32 WC elements
-      constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time
+      constexpr int PW = KB / 16 * NC * 2 / 4;                 // pieces a thread: a warp has 8 rows x 4 of them at a time,
+      constexpr int TW = KB / 64;                              // and whole tiles in all
       const int w4 = warp & 3, t = lane & 3;
       // values
       constexpr int CB = D / 64;                               // blocks of 64 elements
@@ -474,11 +475,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
         const int32_t *tab = a.table + it.b * a.max_blocks;
         uint32_t w[PW][WC], cf[PW][GK];
-        int pid[PW];
+        int pid[TW];
         auto pages = [&](int blk) {
 #pragma unroll
-          for (int i = 0; i < PW; i++) {
-            const int64_t tok = (int64_t)blk * KB + ((i * 4 + w4) / (2 * NC)) * 16;
+          for (int i = 0; i < TW; i++) {
+            const int64_t tok = (int64_t)blk * KB + (w4 * TW + i) * 16;
             pid[i] = tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
           }
         };
@@ -487,11 +488,11 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           valid = 0;
 #pragma unroll
           for (int i = 0; i < PW; i++) {
-            const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
-            const bool there = pid[i] >= 0 && pid[i] < p.g.pages;
+            const int c = i / 2 % NC, row = (i & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3), pg = pid[i / (2 * NC)];
+            const bool there = pg >= 0 && pg < p.g.pages;
             if (there) {
-              const int tok = blk * KB + tl * 16;
-              const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pid[i] * hkv + it.kvh) * p.g.head_bytes +
+              const int tl = w4 * TW + i / (2 * NC), tok = blk * KB + tl * 16;
+              const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
                                  ((tok & (p.g.page - 1)) >> 4) * TILE;
               valid |= 1u << tl;
               if constexpr (WC == 4) {
@@ -579,8 +580,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
               const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
 #pragma unroll 1
               for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
-                const int gi = i * 4 + w4, tl = gi / (2 * NC), c = gi / 2 % NC, row = (gi & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
-                const int pos = tl * 16 + row;
+                const int c = i / 2 % NC, row = (i & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+                const int pos = (w4 * TW + i / (2 * NC)) * 16 + row;
 #pragma unroll
                 for (int k = 0; k < WC; k++) {
                   const uint32_t cc = cf[0][k / (WC / GK)], x = w[0][k];
