@@ -52,8 +52,8 @@ namespace {
 using namespace sm100;
 
 constexpr int QROWS = 128;                       // rows of a q tile (MMA M)
-constexpr int MMA_WARP = 0, ITEM_WARP = 1, SOFT_WARP0 = 4, DQ_WARP0 = 12;
-constexpr int ITEM_READERS = 13;                 // warps that take every item: all but the one that hands them out and the idle
+constexpr int MMA_WARP = 0, ITEM_WARP = 1, COPY_WARP0 = 2, SOFT_WARP0 = 4, DQ_WARP0 = 12;
+constexpr int ITEM_READERS = 15;                 // warps that take every item: all but the one that hands them out
 // Four warpgroups (the first one's last two warps without work): 128 registers a thread, which every role fits in.
 // Shared memory leaves the L1 cache a few KB, so that spilled registers would come back from L2.
 constexpr int THREADS = 32 * 16;
@@ -82,7 +82,9 @@ struct Cfg {
   static constexpr int KB = D == 256 ? 64 : 128;           // keys a block
   static constexpr int TILE = 16 * D + 128 * G;
   static constexpr int Q_BYTES = QROWS * D * 2, KV_BYTES = KB * D * 2;
-  static constexpr int OFF_K = NQ * Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES, OFF_END = OFF_V + 2 * KV_BYTES;
+  static constexpr int OFF_K = NQ * Q_BYTES, OFF_V = OFF_K + 2 * KV_BYTES, OFF_RAW = OFF_V + 2 * KV_BYTES;
+  static constexpr int HALF = 8 * D + 64 * G;              // a tile's keys or values in the cache: codes, coefficients
+  static constexpr int RAW = KB / 16 * HALF, OFF_END = OFF_RAW + 2 * RAW;
   static constexpr int EDGES = 8;                          // blocks of an item that only some rows see: at most 3 at either end
   static constexpr int NOTES = EDGES * G * (KB / 32);      // a bit a (block, group, position)
   static constexpr int SMALL = 512 + 4 * NOTES * 4;
@@ -90,8 +92,9 @@ struct Cfg {
 };
 
 // barriers (8 bytes each)
-enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, K_FULL = 8, K_EMPTY = 10, V_FULL = 12, V_EMPTY = 14, IT_FULL = 16,
-       IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, BARS };
+enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, FULL = 8, K_EMPTY = 16, V_EMPTY = 18, IT_FULL = 20,
+       IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, RAW_FULL, RAW_EMPTY = RAW_FULL + 2,
+       BARS = RAW_EMPTY + 2 };
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -165,6 +168,12 @@ __device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uin
 }
 __device__ __forceinline__ int token_of(int pos) { return 4 * ((pos & 7) >> 1) + 2 * (pos & 1) + (pos >> 3); }   // inverse of kv_row
 
+// 16 bytes, or zeros for `bytes` 0 (nothing is read then)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct Phase {
   uint32_t v = 0;
   __device__ __forceinline__ uint32_t next() {
@@ -222,12 +231,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   const uint32_t sb = smem_addr(smem);
   const uint32_t bars = sb + C::OFF_END;
   uint8_t *small = smem + C::OFF_END;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 192);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 196);
-  uint4 *kvalid = reinterpret_cast<uint4 *>(small + 208);                    // [4] a word a key warp: tiles of the block with a page
-  Item *items = reinterpret_cast<Item *>(small + 272);                       // [ITEM_SLOTS]
-  static_assert(8 * BARS <= 192 && 272 + ITEM_SLOTS * sizeof(Item) <= 480, "small arrays");
-  int *noted = reinterpret_cast<int *>(small + 480);                         // [4] items: has notes
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 256);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 260);
+  uint32_t *kvalid = reinterpret_cast<uint32_t *>(small + 288);              // [8] blocks: tiles with a page
+  Item *items = reinterpret_cast<Item *>(small + 320);                       // [ITEM_SLOTS]
+  static_assert(8 * BARS <= 256 && 320 + ITEM_SLOTS * sizeof(Item) <= 512, "small arrays");
+  int *noted = reinterpret_cast<int *>(small + 264);                         // [4] items: has notes
   uint32_t *notes = reinterpret_cast<uint32_t *>(small + 512);               // [4] items x NOTES: values taken out
   auto bar = [&](int i) { return bars + 8 * i; };
   const WaitCtl ctl{abort_flag, &g_kv_status};
@@ -245,11 +254,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       mbar_init(bar(P_FULL + i), 128);
       mbar_init(bar(PV_DONE + i), 1);
       mbar_init(bar(Q_FULL + i), 128);
-      mbar_init(bar(K_FULL + i), 128);
       mbar_init(bar(K_EMPTY + i), 1);
-      mbar_init(bar(V_FULL + i), 128);
       mbar_init(bar(V_EMPTY + i), 1);
+      mbar_init(bar(RAW_FULL + i), 32);
+      mbar_init(bar(RAW_EMPTY + i), 128);
     }
+    for (int i = 0; i < 8; i++) mbar_init(bar(FULL + i), NQ == 2 ? 128 : 256);
     mbar_init(bar(DRAIN), 1);
     mbar_init(bar(IT_NEXT), 4);
     *abort_flag = 0;
@@ -276,8 +286,48 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     if (++it_slot == ITEM_SLOTS) it_slot = 0, it_ph ^= 1u;
   };
 
-  if (warp == 2 || warp == 3) {
-    // no work
+  if (warp == COPY_WARP0 || warp == COPY_WARP0 + 1) {
+    // ------------------------------------------------------------ copies: a block's keys, or its values, as the cache has them
+    const bool vals = warp != COPY_WARP0;
+    const uint32_t raw = sb + C::OFF_RAW + (vals ? C::RAW : 0);
+    const uint8_t *cache = static_cast<const uint8_t *>(a.cache) + 16 * lane;
+    uint32_t ph = 1;
+    int kb = 0;
+    bool ok = true;
+    while (const Item *ip = next_item()) {
+      const Item &it = *ip;
+      const int32_t *tab = a.table + it.b * a.max_blocks;
+      auto page_of = [&](int blk) {                          // a tile a lane
+        const int64_t tok = (int64_t)blk * KB + lane * 16;
+        return lane < KB / 16 && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
+      };
+      int pg = it.blocks > 0 ? page_of(it.blk0) : -1;
+      for (int n = 0; n < it.blocks; n++, kb++, ph ^= 1u) {
+        const int blk = it.blk0 + n, next = n + 1 < it.blocks ? page_of(blk + 1) : -1;
+        const bool there = pg >= 0 && pg < p.g.pages;
+        const uint32_t valid = __ballot_sync(0xffffffffu, there);
+        const int64_t at = !there ? 0 : ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
+                                            ((((int64_t)blk * KB + lane * 16) & (p.g.page - 1)) >> 4) * TILE;
+        if (!warp_wait(bar(RAW_EMPTY + vals), ph, ctl)) { ok = false; break; }
+#pragma unroll 1
+        for (int tl = 0; tl < KB / 16; tl++) {
+          const uint8_t *src = cache + __shfl_sync(0xffffffffu, at, tl);
+          const uint32_t bytes = (valid >> tl) & 1u ? 16u : 0u, dst = raw + tl * C::HALF;   // zeros without a page
+#pragma unroll
+          for (int c = 0; c < D / 64; c++) {
+            const int q = c * 32 + lane;                     // values: so that eight lanes with one quad of tokens each read 8 banks' groups
+            cp_async16(dst + (vals ? q ^ ((q >> 3) & 3) : q) * 16, src + (vals ? 8 * D : 0) + c * 512, bytes);
+          }
+          if (lane < 4 * G) cp_async16(dst + 8 * D + lane * 16, src + 16 * D + (vals ? 64 * G : 0), bytes);
+        }
+        cp_async_wait_all();
+        if (!vals && lane == 0) kvalid[kb & 7] = valid;
+        mbar_arrive(bar(RAW_FULL + vals));
+        pg = next;
+      }
+      if (!ok) break;
+      release();
+    }
   } else if (warp == ITEM_WARP) {
     // ------------------------------------------------------------ items
     unsigned *ticket = static_cast<unsigned *>(a.workspace) + (kKvMaxCtas - 1), *done = ticket - 1;
@@ -355,8 +405,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   } else if (warp == MMA_WARP) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t id_s = idesc_f16(QROWS, KB), id_o = idesc_f16(QROWS, D);
-    Phase kf[2], vf[2], pf[2], qf[2];
-    int kb = 0, vb = 0;                       // blocks begun, over all items
+    Phase pf[2], qf[2];
+    int kb = 0, full = 0;                     // blocks and phases of FULL before this item
     // Descriptors differ in the start address alone (the low word, in 16-byte units).
     const uint64_t first = smem_desc_sw128(sb);
     const uint32_t desc0 = (uint32_t)first, desc_hi = (uint32_t)(first >> 32);
@@ -369,29 +419,15 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       const Item &it = *ip;
       const int nt = __shfl_sync(0xffffffffu, it.tiles, 0), N = __shfl_sync(0xffffffffu, nt * it.blocks, 0);
       {
-        int k_at = -1, v_at = -1;             // the block whose keys / values were waited for
-        // What S of step i needs: looked for (its answer takes some 200 cycles), and waited for.
-        auto looked = [&](int i) {
-          const int j = nt == 2 ? i >> 1 : i;
-          if (i >= nt && j != k_at && __all_sync(0xffffffffu, mbar_test(bar(K_FULL + (kb & 1)), kf[kb & 1].v))) {
-            kf[kb & 1].next();
-            k_at = j;
-            kb++;
-          }
-        };
-        auto ready = [&](int i) -> bool {
-          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i;
-          if (i < nt && !warp_wait(bar(Q_FULL + x), qf[x].next(), ctl)) return false;
-          if (j != k_at) {
-            if (!warp_wait(bar(K_FULL + (kb & 1)), kf[kb & 1].next(), ctl)) return false;
-            k_at = j;
-            kb++;
-          }
+        int have = 0;                         // phases of FULL waited for: keys of blocks below it, values of those before them
+        auto up_to = [&](int n) -> bool {
+          for (; have < n; have++, full++)
+            if (!warp_wait(bar(FULL + (full & 7)), (full >> 3) & 1, ctl)) return false;
           return true;
         };
         auto scores = [&](int i) {
-          const int x = nt == 2 ? i & 1 : 0, buf = i & 1;
-          const uint32_t kd = uniform(desc0 + ((C::OFF_K + ((kb - 1) & 1) * C::KV_BYTES) >> 4)), qd = uniform(desc0 + (x * C::Q_BYTES >> 4));
+          const int x = nt == 2 ? i & 1 : 0, kbuf = (kb + (nt == 2 ? i >> 1 : i)) & 1, buf = i & 1;
+          const uint32_t kd = uniform(desc0 + ((C::OFF_K + kbuf * C::KV_BYTES) >> 4)), qd = uniform(desc0 + (x * C::Q_BYTES >> 4));
           const uint32_t dt = uniform(tm0 + buf * 128);
           if (elect_one()) {
 #pragma unroll
@@ -399,27 +435,21 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
               umma_f16_ss(dt, desc(qd + (kk / 4) * (QROWS * 128 / 16) + 2 * (kk % 4)),
                           desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
             umma_commit(bar(S_FULL + buf));
-            if (x == nt - 1) umma_commit(bar(K_EMPTY + ((kb - 1) & 1)));
+            if (x == nt - 1) umma_commit(bar(K_EMPTY + kbuf));
           }
           __syncwarp();
         };
         for (int i = 0; i < 2 && i < N && ok; i++) {
-          ok = ready(i);
+          ok = up_to(nt == 2 ? 1 : i + 1) && (i >= nt || warp_wait(bar(Q_FULL + i), qf[i].next(), ctl));
           tc_fence_after();
           if (ok) scores(i);
         }
         for (int i = 0; i < N && ok; i++) {
-          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1;
-          // V, then P; the next keys are looked for before P, which mostly comes last, and waited for after its product.
-          if (j != v_at) {
-            if (!warp_wait(bar(V_FULL + (vb & 1)), vf[vb & 1].next(), ctl)) { ok = false; break; }
-            v_at = j;
-            vb++;
-          }
-          if (i + 2 < N) looked(i + 2);
-          if (!warp_wait(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
+          const int x = nt == 2 ? i & 1 : 0, j = nt == 2 ? i >> 1 : i, buf = i & 1, vbuf = (kb + j) & 1;
+          // values of this block (and, with two row tiles, keys of the next), then P
+          if (!up_to(j + 2) || !warp_wait(bar(P_FULL + buf), pf[buf].next(), ctl)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t vd = uniform(desc0 + ((C::OFF_V + ((vb - 1) & 1) * C::KV_BYTES) >> 4));
+          const uint32_t vd = uniform(desc0 + ((C::OFF_V + vbuf * C::KV_BYTES) >> 4));
           const uint32_t ot = uniform(tm0 + 256 + x * D), pt = uniform(tm0 + buf * 128);
           if (elect_one()) {
 #pragma unroll
@@ -427,17 +457,20 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
               umma_f16_ts(ot, pt + 8 * kk, desc(vd + (kk / 4) * (D * 128 / 16) + 2 * (kk % 4)), id_o,
                           (j | kk) != 0);
             umma_commit(bar(PV_DONE + x));
-            if (x == nt - 1) umma_commit(bar(V_EMPTY + ((vb - 1) & 1)));
+            if (x == nt - 1) umma_commit(bar(V_EMPTY + vbuf));
           }
           __syncwarp();
           if (i + 2 < N) {
-            if (!ready(i + 2)) { ok = false; break; }
-            tc_fence_after();
+            if (nt == 1) {
+              if (!up_to(i + 3)) { ok = false; break; }
+              tc_fence_after();
+            }
             scores(i + 2);
           }
         }
       }
       if (!ok) break;
+      kb += it.blocks;
       release();
     }
     if (*abort_flag && elect_one()) {         // wait (bounded) for the MMAs in flight before TMEM goes
@@ -460,9 +493,9 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
       const int u = threadIdx.x & 127, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
       const bool act = u < UNITS;
-      Phase ke[2], ve[2];
+      Phase ke[2], ve[2], kr, vr;
       ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
-      int kb = 0, n_item = 0;                                  // blocks and items before
+      int kb = 0, full = 0, n_item = 0;                        // blocks, phases of FULL and items before
       bool ok = true;
       for (; const Item *ip = next_item(); n_item++) {
         const Item &it = *ip;
@@ -473,102 +506,55 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           if (u == 0) noted[n_item & 3] = 0;
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
-        const int32_t *tab = a.table + it.b * a.max_blocks;
         uint32_t w[PW][WC], cf[PW][GK];
-        int pid[TW];
-        auto pages = [&](int blk) {
-#pragma unroll
-          for (int i = 0; i < TW; i++) {
-            const int64_t tok = (int64_t)blk * KB + (w4 * TW + i) * 16;
-            pid[i] = tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
-          }
-        };
-        uint32_t valid = 0;                                    // tiles of the block with a page, as far as this warp has them
-        auto fetch_keys = [&](int blk) {
-          valid = 0;
+        auto take_keys = [&]() {
 #pragma unroll
           for (int i = 0; i < PW; i++) {
-            const int c = i / 2 % NC, row = (i & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3), pg = pid[i / (2 * NC)];
-            const bool there = pg >= 0 && pg < p.g.pages;
-            if (there) {
-              const int tl = w4 * TW + i / (2 * NC), tok = blk * KB + tl * 16;
-              const uint8_t *s = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
-                                 ((tok & (p.g.page - 1)) >> 4) * TILE;
-              valid |= 1u << tl;
-              if constexpr (WC == 4) {
-                const uint4 v = *(reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16));
-                w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
-              } else {
-                const uint2 v = *(reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8));
-                w[i][0] = v.x, w[i][1] = v.y;
-              }
-              const uint8_t *cp = s + 16 * D + (row * G + c * GK) * 4;
-              if constexpr (GK == 1) {
-                cf[i][0] = *(reinterpret_cast<const uint32_t *>(cp));
-              } else if constexpr (GK == 2) {
-                const uint2 v = *(reinterpret_cast<const uint2 *>(cp));
-                cf[i][0] = v.x, cf[i][1] = v.y;
-              } else {
-                const uint4 v = *(reinterpret_cast<const uint4 *>(cp));
-                cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
-              }
+            const int c = i / 2 % NC, row = (i & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
+            const uint8_t *s = smem + C::OFF_RAW + (w4 * TW + i / (2 * NC)) * C::HALF;
+            if constexpr (WC == 4) {
+              const uint4 v = *reinterpret_cast<const uint4 *>(s + ((c * 16 + row) * 4 + t) * 16);
+              w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
             } else {
-#pragma unroll
-              for (int j = 0; j < WC; j++) w[i][j] = 0u;
-#pragma unroll
-              for (int j = 0; j < GK; j++) cf[i][j] = 0u;
+              const uint2 v = *reinterpret_cast<const uint2 *>(s + (row * 4 + t) * 8);
+              w[i][0] = v.x, w[i][1] = v.y;
+            }
+            const uint8_t *cp = s + 8 * D + (row * G + c * GK) * 4;
+            if constexpr (GK == 1) {
+              cf[i][0] = *reinterpret_cast<const uint32_t *>(cp);
+            } else if constexpr (GK == 2) {
+              const uint2 v = *reinterpret_cast<const uint2 *>(cp);
+              cf[i][0] = v.x, cf[i][1] = v.y;
+            } else {
+              const uint4 v = *reinterpret_cast<const uint4 *>(cp);
+              cf[i][0] = v.x, cf[i][1] = v.y, cf[i][2] = v.z, cf[i][3] = v.w;
             }
           }
-        };
-        auto page_of = [&](int blk) {
-          const int64_t tok = (int64_t)blk * KB + vt * 16;
-          return act && tok < it.vhi ? tab[tok >> p.g.lg_page] : -1;
         };
         uint4 vw[4];
         uint32_t vf[16][GV];
-        const uint8_t *coefs = nullptr;                        // of the block in registers; null: no such page
-        auto fetch_values = [&](int blk, int pg) {
-          coefs = nullptr;
-          if (pg >= 0 && pg < p.g.pages) {
-            const int64_t tok = (int64_t)blk * KB + vt * 16;
-            const uint8_t *t = static_cast<const uint8_t *>(a.cache) + ((int64_t)pg * hkv + it.kvh) * p.g.head_bytes +
-                               (((int)tok & (p.g.page - 1)) >> 4) * TILE;
-            const uint4 *s = reinterpret_cast<const uint4 *>(t + 8 * D + (vc * 8 + g8) * 64);
+        const uint8_t *raw_v = smem + C::OFF_RAW + C::RAW + (act ? vt : 0) * C::HALF;
+        const uint8_t *coefs = raw_v + 8 * D + (G > CB ? 2 * vc : vc * G / CB) * 4;
+        auto take_values = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; i++) vw[i] = s[i];
-            const uint8_t *cp = coefs = t + 16 * D + 64 * G + (G > CB ? 2 * vc : vc * G / CB) * 4;
+          for (int i = 0; i < 4; i++) vw[i] = *reinterpret_cast<const uint4 *>(raw_v + ((vc * 8 + g8) * 4 + (i ^ (g8 >> 1))) * 16);
 #pragma unroll
-            for (int r = 0; r < 16; r++) {
-              if constexpr (GV == 1) {
-                vf[r][0] = *(reinterpret_cast<const uint32_t *>(cp + r * G * 4));
-              } else {
-                const uint2 v = *(reinterpret_cast<const uint2 *>(cp + r * G * 4));
-                vf[r][0] = v.x, vf[r][GV - 1] = v.y;
-              }
+          for (int r = 0; r < 16; r++) {
+            if constexpr (GV == 1) {
+              vf[r][0] = *reinterpret_cast<const uint32_t *>(coefs + r * G * 4);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2 *>(coefs + r * G * 4);
+              vf[r][0] = v.x, vf[r][GV - 1] = v.y;
             }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++) vw[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int r = 0; r < 16; r++)
-#pragma unroll
-              for (int g = 0; g < GV; g++) vf[r][g] = 0u;
           }
         };
-        int pg_next = -1;
-        if (it.blocks > 0) {
-          if constexpr (KEYS) pages(it.blk0);
-          if constexpr (VALUES) pg_next = page_of(it.blk0);
-          if constexpr (KEYS) fetch_keys(it.blk0);
-          if constexpr (VALUES) fetch_values(it.blk0, pg_next);
-          if (it.blocks > 1) {
-            if constexpr (KEYS) pages(it.blk0 + 1);
-            if constexpr (VALUES) pg_next = page_of(it.blk0 + 1);
-          }
-        }
-        for (int j = 0; j < it.blocks; j++, kb++) {
-          const int blk = it.blk0 + j, buf = kb & 1;
-          if constexpr (KEYS) {
+        // a phase: keys of block n, values of the block before
+        for (int n = 0; it.blocks > 0 && n <= it.blocks; n++, full++) {
+          if (KEYS && n < it.blocks) {
+            const int buf = (kb + n) & 1;
+            if (!warp_wait(bar(RAW_FULL), kr.next(), ctl)) { ok = false; break; }
+            take_keys();
+            mbar_arrive(bar(RAW_EMPTY));
             if (!warp_wait(bar(K_EMPTY + buf), ke[buf].next(), ctl)) { ok = false; break; }
             {
               const uint32_t dst = sb + C::OFF_K + buf * C::KV_BYTES;
@@ -609,22 +595,17 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                   for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
                 }
               }
-              if (lane == 0) reinterpret_cast<uint32_t *>(kvalid + (kb & 3))[w4] = valid;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(bar(K_FULL + buf));
-            if (j + 1 < it.blocks) {
-              fetch_keys(blk + 1);
-              if (j + 2 < it.blocks) pages(blk + 2);
             }
           }
-          if constexpr (VALUES) {
-            if (!warp_wait(bar(V_EMPTY + buf), ve[buf].next(), ctl)) { ok = false; break; }
+          if (VALUES && n > 0) {
+            const int j = n - 1, blk = it.blk0 + j, buf = (kb + j) & 1;
+            if (!warp_wait(bar(RAW_FULL + 1), vr.next(), ctl)) { ok = false; break; }
+            take_values();
             // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
             // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
             // noted for the rows that do.
             const bool edge = blk * KB < it.flo || (int64_t)(blk + 1) * KB > it.fhi;
-            if (edge) {
+            if (edge && act) {
               uint32_t out[GV] = {};                             // rows to zero, by group
               const int e = blk * KB < it.flo ? j : 4 + blk - it.fhi / KB;
 #pragma unroll 1
@@ -634,7 +615,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 for (int g = 0; g < GV; g++) {
                   if (tok < it.vlo || tok >= it.vhi) {
                     out[g] |= 1u << r;
-                  } else if (coefs) {
+                  } else {
                     const uint32_t m = *(reinterpret_cast<const uint32_t *>(coefs + r * G * 4) + g) & 0x7FFF7FFFu;
                     if ((m & 0xFFFFu) >= 0x7C00u || (m >> 16) >= 0x7C00u) {
                       const int pos = vt * 16 + r, grp = (G > CB ? 2 * vc : vc * G / CB) + g;
@@ -651,6 +632,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 for (int g = 0; g < GV; g++)
                   if ((out[g] >> r) & 1u) vf[r][g] = 0u;
             }
+            mbar_arrive(bar(RAW_EMPTY + 1));
+            if (!warp_wait(bar(V_EMPTY + buf), ve[buf].next(), ctl)) { ok = false; break; }
             if (act) {
               uint32_t s2[16 * GV / 2], b2[16 * GV / 2];           // per pair of tokens (rows 2t, 2t + 1)
 #pragma unroll
@@ -687,15 +670,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 }
               }
             }
-            fence_proxy_async_smem();
-            mbar_arrive(bar(V_FULL + buf));
-            if (j + 1 < it.blocks) {
-              fetch_values(blk + 1, pg_next);
-              if (j + 2 < it.blocks) pg_next = page_of(blk + 2);
-            }
           }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(FULL + (full & 7)));
         }
         if (!ok) break;
+        kb += it.blocks;
         if (KEYS && lane == 0) mbar_arrive(bar(IT_NEXT));
         release();
       }
@@ -773,8 +753,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         const int buf = it.tiles == 2 ? x : k & 1, t0 = (it.blk0 + k) * KB;
         if (!warp_wait(bar(S_FULL + buf), (s_base[buf] + (it.tiles == 2 ? k : k >> 1)) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        const uint4 kv = kvalid[(blk_base + k) & 3];
-        const uint32_t pages = kv.x | kv.y | kv.z | kv.w;
+        const uint32_t pages = kvalid[(blk_base + k) & 7];
         const bool full = __all_sync(0xffffffffu, !real || (klo <= t0 && khi >= t0 + KB)) && pages == (1u << (KB / 16)) - 1;
         const uint32_t s_tm = tm + buf * 128;
         // Scores of tokens that the row does not see become -inf, in a pass of their own: few blocks have any.
