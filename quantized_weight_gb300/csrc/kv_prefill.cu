@@ -751,13 +751,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       float m = NINF, l = 0.0f;                              // reference maximum (log2 units), sum
       for (int k = 0; k < it.blocks; k++) {
         const int buf = it.tiles == 2 ? x : k & 1, t0 = (it.blk0 + k) * KB;
+        const bool seen = __all_sync(0xffffffffu, !real || (klo <= t0 && khi >= t0 + KB));
         if (!warp_wait(bar(S_FULL + buf), (s_base[buf] + (it.tiles == 2 ? k : k >> 1)) & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         const uint32_t pages = kvalid[(blk_base + k) & 7];
-        const bool full = __all_sync(0xffffffffu, !real || (klo <= t0 && khi >= t0 + KB)) && pages == (1u << (KB / 16)) - 1;
         const uint32_t s_tm = tm + buf * 128;
         // Scores of tokens that the row does not see become -inf, in a pass of their own: few blocks have any.
-        if (!full) {
+        if (!seen || pages != (1u << (KB / 16)) - 1) {
 #pragma unroll 1
           for (int ch = 0; ch < KB / 16; ch++) {
             uint32_t v[16];
