@@ -165,8 +165,8 @@ inline int64_t row_grid(Rows &p) {
   const int64_t units = (p.tokens + p.per_warp - 1) / p.per_warp;
   int64_t part = units * rows / (152 * 64);
   part = part < 1 ? 1 : part > rows ? rows : part;
-  p.part = (int)part;
   p.parts = (int)((rows + part - 1) / part);
+  p.part = (int)((rows + p.parts - 1) / p.parts);
   return (units * p.parts + kRowWarps - 1) / kRowWarps;
 }
 
@@ -425,57 +425,72 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
   if (unit * p.r.per_warp >= p.r.tokens) return;
 
   auto rows = [&](auto count, int64_t t, int slot) {
+    constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
+    // what the next row has in the cache: coefficients; a key's words, a single value's bytes or a lane's words of a quad's
+    uint32_t coef_ahead[PASSES], ahead[4];
+    auto fetch = [&](int hv) {
+      const bool isv = hv & 1;
+      const uint8_t *tile = p.cache + (slot >= 0 ? kv_tile_at(g, slot, hv >> 1) : 0);
+#pragma unroll
+      for (int i = 0; i < 4; i++) ahead[i] = 0u;
+#pragma unroll
+      for (int ps = 0; ps < PASSES; ps++) {
+        const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = m >> g.lg_group8;
+        coef_ahead[ps] = 0u;
+        if (r < n && slot >= 0) {
+          coef_ahead[ps] = *reinterpret_cast<const uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp)));
+          if (!isv) {
+            ahead[ps] = *reinterpret_cast<const uint32_t *>(tile + kv_k_word(D, row, m));
+          } else if (n == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+              ahead[i >> 2] |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + i, j >> 2) + (j & 3)] << (8 * (i & 3));
+          }
+        }
+      }
+      if (n == 4 && isv && lane < D / 8) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(tile + kv_v_word(D, 64 * (lane >> 3) + (lane & 7), (slot & 15) >> 2));
+        ahead[0] = o.x, ahead[1] = o.y, ahead[2] = o.z, ahead[3] = o.w;
+      }
+    };
+    fetch(hv0);
 #pragma unroll 1
     for (int hv = hv0; hv < hv1; hv++) {
       const int h = hv >> 1;
       const bool isv = hv & 1;
       uint8_t *dst = static_cast<uint8_t *>(isv ? p.v : p.k);
-      constexpr int n = decltype(count)::value, PASSES = n > RP ? n / RP : 1;
-      const uint8_t *tile = p.cache + (slot >= 0 ? kv_tile_at(g, slot, h) : 0);
-      uint32_t coef[PASSES], q[PASSES][2];                   // codes: bytes of elements 0..3 and 4..7
+      uint32_t coef[PASSES], raw[4], q[PASSES][2];           // q: codes, bytes of elements 0..3 and 4..7
 #pragma unroll
-      for (int ps = 0; ps < PASSES; ps++) {
-        const int r = ps * RP + sub, j = (slot & 15) + r, row = kv_row(j & 15), grp = m >> g.lg_group8;
-        coef[ps] = q[ps][0] = q[ps][1] = 0u;
-        if (r < n && slot >= 0) {
-          coef[ps] = *(reinterpret_cast<const uint32_t *>(tile + (isv ? kv_v_coef(g, row, grp) : kv_k_coef(g, row, grp))));
-          if (!isv) {
-            const uint32_t w = *(reinterpret_cast<const uint32_t *>(tile + kv_k_word(D, row, m)));
-            const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;   // even and odd elements
-            q[ps][0] = prmt(a, b, 0x5140u);
-            q[ps][1] = prmt(a, b, 0x7362u);
-          } else if (n == 1) {
-            uint32_t x = 0, y = 0;
+      for (int i = 0; i < 4; i++) raw[i] = ahead[i];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-              x |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + i, j >> 2) + (j & 3)] << (8 * i);
-              y |= (uint32_t)tile[kv_v_word(D, 16 * (m >> 1) + 4 + i, j >> 2) + (j & 3)] << (8 * i);
-            }
-            q[ps][0] = (x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-            q[ps][1] = (y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-          }
+      for (int ps = 0; ps < PASSES; ps++) coef[ps] = coef_ahead[ps];
+      if (hv + 1 < hv1) fetch(hv + 1);
+      if (!isv) {
+#pragma unroll
+        for (int ps = 0; ps < PASSES; ps++) {
+          const uint32_t a = raw[ps] & 0x0F0F0F0Fu, b = (raw[ps] >> 4) & 0x0F0F0F0Fu;   // even and odd elements
+          q[ps][0] = prmt(a, b, 0x5140u);
+          q[ps][1] = prmt(a, b, 0x7362u);
         }
-      }
-      if constexpr (n == 4) {
-        if (isv) {
-          if (lane < D / 8) {
-            const int c = lane >> 3, e = lane & 7;
-            const uint4 o = *(reinterpret_cast<const uint4 *>(tile + kv_v_word(D, 64 * c + e, (slot & 15) >> 2)));
-            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+      } else if constexpr (n == 1) {
+        q[0][0] = (raw[0] >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+        q[0][1] = (raw[1] >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+      } else {
+        if (lane < D / 8) {
+          const int c = lane >> 3, e = lane & 7;
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+          for (int i = 0; i < 4; i++)
 #pragma unroll
-              for (int r = 0; r < 4; r++) bytes[r * (D / 2) + (4 * c + i) * 8 + e] = (uint8_t)(w[i] >> (8 * r));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int ps = 0; ps < PASSES; ps++) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(bytes + (ps * RP + sub) * (D / 2) + 8 * (m >> 1));
-            q[ps][0] = (x.x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-            q[ps][1] = (x.y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
-          }
-          __syncwarp();
+            for (int r = 0; r < 4; r++) bytes[r * (D / 2) + (4 * c + i) * 8 + e] = (uint8_t)(raw[i] >> (8 * r));
         }
+        __syncwarp();
+#pragma unroll
+        for (int ps = 0; ps < PASSES; ps++) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(bytes + (ps * RP + sub) * (D / 2) + 8 * (m >> 1));
+          q[ps][0] = (x.x >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+          q[ps][1] = (x.y >> (4 * (m & 1))) & 0x0F0F0F0Fu;
+        }
+        __syncwarp();
       }
 #pragma unroll
       for (int ps = 0; ps < PASSES; ps++) {
