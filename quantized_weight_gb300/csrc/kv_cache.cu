@@ -381,6 +381,7 @@ struct ReadParams {
   void *k, *v;
 };
 
+// Eight values, written past the caches' keeping: bfloat16 in one piece; float32 in two, 8 elements apart (see read_kernel).
 template <bool BF16>
 __device__ __forceinline__ void store8(void *p, const float (&v)[8]) {
   if constexpr (BF16) {
@@ -393,7 +394,7 @@ __device__ __forceinline__ void store8(void *p, const float (&v)[8]) {
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(u[0], u[1], u[2], u[3]));
   } else {
     __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    __stcs(reinterpret_cast<float4 *>(p) + 2, make_float4(v[4], v[5], v[6], v[7]));
   }
 }
 
@@ -492,6 +493,17 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
         }
         __syncwarp();
       }
+      // float32: two lanes write their 16 elements eight at a time, so that a store fills 32-byte sectors (halves of them cost
+      // the path to L2 as much as whole ones: 16381 tokens of 8 heads of 128 in 29.6 us)
+      if constexpr (!BF16) {
+#pragma unroll
+        for (int ps = 0; ps < PASSES; ps++) {
+          const uint32_t x = __shfl_xor_sync(0xffffffffu, m & 1 ? q[ps][0] : q[ps][1], 1);
+          if (m & 1) q[ps][0] = x;
+          else q[ps][1] = x;
+        }
+      }
+      const int d = BF16 ? 8 * m : 8 * (m & ~1) + 4 * (m & 1);
 #pragma unroll
       for (int ps = 0; ps < PASSES; ps++) {
         const int r = ps * RP + sub;
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
           if (slot < 0)
 #pragma unroll
             for (int i = 0; i < 8; i++) v[i] = __int_as_float(0x7FC00000);
-          store8<BF16>(dst + (((t + r) * g.kv_heads + h) * D + 8 * m) * (BF16 ? 2 : 4), v);
+          store8<BF16>(dst + (((t + r) * g.kv_heads + h) * D + d) * (BF16 ? 2 : 4), v);
         }
       }
     }
