@@ -3,8 +3,8 @@
 //
 // The cache of one layer is [pages][kv_heads][page / 16] tiles of 16 tokens.
 // Keeping a head's tiles of a page together makes a page one contiguous run
-// per head, and a tile is a multiple of 16 bytes, so any tile run is one bulk
-// copy.  A tile is
+// per head, and a tile is a multiple of 16 bytes, so that it is copied in
+// 16-byte pieces.  A tile is
 //
 //   K codes   8 * D bytes   32-bit words [max(1, D/128)][row 16][t 4][WC], WC = min(4, D/32):
 //                           nibble i of word w' of chunk c is element 32 (WC c + w') + 8t + i of the row's token

@@ -10,16 +10,20 @@
 // Roles of the persistent CTA, one an SM (16 warps):
 //   warp 0           TMEM and the MMA issue (one thread's)
 //   warp 1           items, from a ticket counter (longest first within a request)
-//   warps 2-3        none
+//   warps 2, 3       the cache's tiles of a block, keys and values, to shared
+//                    memory as they are (cp.async; a tile without a page: zeros)
 //   warps 4-7, 8-11  softmax of row tile 0 and 1, a row a thread: maximum,
 //                    exponentials, P, O's rescaling, and the tile's q and output
-//   warps 12-15      4-bit codes from the cache to binary16 in shared memory: keys, and values transposed (heads of
+//   warps 12-15      codes to binary16: keys, and values transposed (heads of
 //                    256 have one row tile: warps 8-11 then take the keys)
 // The two row tiles alternate: while one tile's softmax runs, the tensor core
 // has the other's products.  With one row tile (heads of 256, or the rest of a request) the
 // blocks alternate instead, between the same two score buffers.  Step i of an item uses score
 // buffer i % 2, and S(i + 2) is issued right after PV(i): it overwrites P(i),
 // which that product has read by then, since MMAs execute in order.
+// The converting warps finish keys of block n and values of block n - 1 as one
+// phase, so that the MMA warp waits once a block for both (a look at a barrier
+// takes it some 250 cycles, however long it has been complete).
 //
 // Shared memory holds the operands K-major with the 128-byte swizzle.  The cache's
 // row order (kv_layout.cuh) is the order of a tile's tokens in both key rows and
@@ -32,7 +36,14 @@
 // maximum follows the true one only when that has grown by 2^8, so O is seldom
 // rescaled); sums and accumulators are float32.
 //
-// Bound: tensor cores: 4 * D flops a row and key; a block of 128 keys for two row tiles of 128 is 16.8 MFLOP against 36 KB of cache.
+// Bound: 4 * D flops a row and key on the tensor cores (1024 cycles a step of 128 rows and 128 keys at D = 128).  Measured: a
+// prompt of 4096 tokens, 32 query and 8 kv heads of 128, 155 us: 45 % of the measured matrix rate; chunks over 700 to 9000
+// tokens, 16 and 4 heads of 256, 321 us: 37 %.  By its own clock a step takes some 2200 cycles: issue of its 16 MMAs 1300 (80
+// each; unrolled and rolled alike), waits 550; the softmax of a tile (2400 cycles of columns, 900 of waits and the mask's
+// test) and the conversion (3700 of the 4400 a block of two steps) are as long, so that no role has slack.
+// Slower, and gone: conversion from global memory (keys 1700 and values 1250 cycles, but 950 and 1050 for their loads:
+// 176 us), a wait by one lane of a warp (241 us), rolled MMA loops (188 against 179 us), TMEM loads of scores ahead (153 against
+// 155 us here, 323 against 320 for heads of 256).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <type_traits>
@@ -54,7 +65,7 @@ using namespace sm100;
 constexpr int QROWS = 128;                       // rows of a q tile (MMA M)
 constexpr int MMA_WARP = 0, ITEM_WARP = 1, COPY_WARP0 = 2, SOFT_WARP0 = 4, DQ_WARP0 = 12;
 constexpr int ITEM_READERS = 15;                 // warps that take every item: all but the one that hands them out
-// Four warpgroups (the first one's last two warps without work): 128 registers a thread, which every role fits in.
+// Four warpgroups: 128 registers a thread, which every role fits in.
 // Shared memory leaves the L1 cache a few KB, so that spilled registers would come back from L2.
 constexpr int THREADS = 32 * 16;
 constexpr int ITEM_SLOTS = 3;
@@ -91,7 +102,8 @@ struct Cfg {
   static constexpr int SMEM = OFF_END + SMALL + 1024;      // the last for alignment
 };
 
-// barriers (8 bytes each)
+// barriers (8 bytes each).  FULL has eight, taken in turn: the warps that arrive on one may be five phases ahead of the last one
+// complete (two blocks ahead, and an item of one block is two phases).
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, FULL = 8, K_EMPTY = 16, V_EMPTY = 18, IT_FULL = 20,
        IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, RAW_FULL, RAW_EMPTY = RAW_FULL + 2,
        BARS = RAW_EMPTY + 2 };
@@ -159,9 +171,8 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
 }
 // Keys stand in shared memory divided by 2^4: a nibble shifted to the top of the mantissa is the code times 2^-18 (a
 // binary16 subnormal), so that one multiply-add with scale * 2^14 makes the value, where 2^14 scale is in range.  (Nibbles
-// where they lie, divided by 2^10, take two instructions a word less (a 4096-token prompt in 181 instead of 184 us), but a
-// key below 2^-4 then loses bits to
-// binary16's subnormals instead of below 2^-10.)
+// where they lie, divided by 2^10, take two instructions a word less, 2 % of the kernel, but keys below 2^-4 then lose
+// bits to binary16's subnormals instead of keys below 2^-10.)
 constexpr float KEY_UNIT = 16.0f;
 __device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -315,7 +326,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           const uint32_t bytes = (valid >> tl) & 1u ? 16u : 0u, dst = raw + tl * C::HALF;   // zeros without a page
 #pragma unroll
           for (int c = 0; c < D / 64; c++) {
-            const int q = c * 32 + lane;                     // values: so that eight lanes with one quad of tokens each read 8 banks' groups
+            const int q = c * 32 + lane;                     // values: eight lanes later read one quad of tokens each, from
+                                                             // 8 different groups of banks
             cp_async16(dst + (vals ? q ^ ((q >> 3) & 3) : q) * 16, src + (vals ? 8 * D : 0) + c * 512, bytes);
           }
           if (lane < 4 * G) cp_async16(dst + 8 * D + lane * 16, src + 16 * D + (vals ? 64 * G : 0), bytes);
@@ -771,8 +783,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
           tmem_st_wait();
         }
-        // 32 columns at a time, read once: their maximum, then, with the reference, their exponentials.  Only where the maximum has outgrown the reference
-        // is what was summed before rescaled: l, O and the block's P so far.
+        // 32 columns at a time, read once: their maximum, then, with the reference, their exponentials.  Only where the
+        // maximum has outgrown the reference is what was summed before rescaled: l, O and the block's P so far.
         const f2 c2 = f2_make(c, c);
         auto columns = [&](const uint32_t (&v)[32], int h) {
           float m4[4] = {NINF, NINF, NINF, NINF};
