@@ -50,6 +50,7 @@
 #include <type_traits>
 
 #include "kv_attend.h"
+#include "kv_launch.h"
 #include "kv_layout.cuh"
 #include "qmm_device.cuh"
 #include "sm100_ptx.cuh"
@@ -1014,20 +1015,8 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   const double most = ((double)a.tokens * a.heads / C::ROWS + (double)a.tokens * a.kv_heads) *
                       ((double)a.max_blocks * a.page / C::UNIT + 2 + p.head);
   while (most / (1 << p.shift) > 1e9) p.shift++;
-  auto kern = attend_warp_kernel<D, G, NT, HL>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kv_max_ctas(1));
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  static std::atomic<int> set_for{0};
+  return launch_large(attend_warp_kernel<D, G, NT, HL>, kv_max_ctas(1), C::THREADS, C::SMEM, s, p, set_for);
 }
 
 }  // namespace kvw

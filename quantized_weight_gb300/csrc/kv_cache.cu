@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <type_traits>
 
+#include "kv_launch.h"
 #include "kv_layout.cuh"
 #include "qmm_device.cuh"
 #include "qmm_launch.h"
@@ -533,22 +534,6 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const ReadParams p) {
 }
 
 }  // namespace
-
-// One launch that may begin while the kernel before it ends (each kernel waits for it before its first access).
-template <class P>
-static cudaError_t launch_after(void (*kern)(P), int64_t grid, int threads, size_t smem, cudaStream_t s, const P &p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
 
 cudaError_t launch_kv_plan(const int32_t *cached, const int32_t *fresh, const int32_t *free_pages, int64_t n_free,
                            int32_t *table, int64_t B, int64_t max_blocks, int page, int64_t tokens, int32_t *slots,

@@ -50,6 +50,7 @@
 
 #include "bounded_wait.cuh"
 #include "kv_attend.h"
+#include "kv_launch.h"
 #include "kv_layout.cuh"
 #include "qmm_device.cuh"
 #include "sm100_ptx.cuh"
@@ -905,22 +906,10 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
   p.ratio = (int)(a.heads / a.kv_heads);
-  auto kern = prefill_kernel<D, G>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  if (e != cudaSuccess) return e;
   // never more CTAs than items
   const int64_t items = (a.tokens * p.ratio / (C::NQ * QROWS) + (a.tokens < a.B ? a.tokens : a.B)) * a.kv_heads;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(items < kv_max_ctas(1) ? items : kv_max_ctas(1)));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  static std::atomic<int> set_for{0};
+  return launch_large(prefill_kernel<D, G>, items < kv_max_ctas(1) ? items : kv_max_ctas(1), THREADS, C::SMEM, s, p, set_for);
 }
 
 }  // namespace

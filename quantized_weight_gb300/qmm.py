@@ -354,12 +354,15 @@ def kv_plan(cached, fresh, free_pages, block_table, tokens, page, out=None, stre
     pc, pf, pp = _i32(cached, "cached", shape), _i32(fresh, "fresh", (B,)), _i32(free_pages, "free_pages", free_pages.shape)
     blocks, pt = _kv_table(block_table, B)
     if out is None:
-        out = torch.empty(2 * (tokens + B + 1), dtype=_I32, device=cached.device).split_with_sizes((tokens, tokens, B + 1, B, 1))
-    slots, positions, cu, lens, need = out
-    _call("qmm_kv_plan", lib().qmm_kv_plan(
-        pc, pf, pp, free_pages.numel(), pt, B, blocks, page, tokens, _i32(slots, "slots", (tokens,)),
-        _i32(positions, "positions", (tokens,)), _i32(cu, "cu", (B + 1,)), _i32(lens, "lens", (B,)),
-        _i32(need, "need", (1,)), _stream(stream)))
+        buf = torch.empty(2 * (tokens + B + 1), dtype=_I32, device=cached.device)
+        out = buf.unsafe_split_with_sizes((tokens, tokens, B + 1, B, 1))     # no views that autograd follows: 2 us less
+        a = buf.data_ptr()
+        outs = a, a + 4 * tokens, a + 8 * tokens, a + 8 * tokens + 4 * (B + 1), a + 8 * tokens + 4 * (2 * B + 1)
+    else:
+        outs = tuple(_i32(t, name, (n,)) for t, name, n in zip(out, ("slots", "positions", "cu", "lens", "need"),
+                                                               (tokens, tokens, B + 1, B, 1)))
+    _call("qmm_kv_plan", lib().qmm_kv_plan(pc, pf, pp, free_pages.numel(), pt, B, blocks, page, tokens, *outs,
+                                           _stream(stream)))
     return out
 
 
@@ -386,10 +389,11 @@ def kv_read(slots, cache, head_dim, page, group=64, dtype=torch.float32, out=Non
     shape = (T, H, head_dim)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=cache.device), torch.empty(shape, dtype=dtype, device=cache.device)
-    k, v = out
-    _call("qmm_kv_read", lib().qmm_kv_read(ps, pc, _kv_out(k, "k", dtype, shape), _kv_out(v, "v", dtype, shape), dt, T,
-                                           pages, H, head_dim, page, group, _stream(stream)))
-    return k, v
+        pk, pv = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        pk, pv = _kv_out(out[0], "k", dtype, shape), _kv_out(out[1], "v", dtype, shape)
+    _call("qmm_kv_read", lib().qmm_kv_read(ps, pc, pk, pv, dt, T, pages, H, head_dim, page, group, _stream(stream)))
+    return out
 
 
 def kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh=1, device="cuda") -> torch.Tensor:
@@ -417,9 +421,12 @@ def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_
     if not (workspace.dtype is torch.uint8 and workspace.is_cuda and workspace.is_contiguous()):
         _need(workspace, "workspace", torch.uint8)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        po = out.data_ptr()
+    else:
+        po = _kv_out(out, "out", dtype, shape)
     _call("qmm_kv_attend", lib().qmm_kv_attend(
-        q.data_ptr(), dt, qt, qh, pc, pt, pl, pcu, _kv_out(out, "out", dtype, shape), T, B, blocks, max_fresh, pages, H,
+        q.data_ptr(), dt, qt, qh, pc, pt, pl, pcu, po, T, B, blocks, max_fresh, pages, H,
         heads, D, page, group, D ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
     return out
