@@ -326,7 +326,12 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
  *   max_fresh >= every request's queries (it picks the kernel).  scale > 0, finite.
  *   Scores, maxima, sums and the accumulation are float32; for QMM_F32 the
  *   queries and probabilities enter the tensor cores as two binary16 terms.
- *   For QMM_BF16 they enter as one, rounded to binary16 (11 bits).
+ *   For QMM_BF16 they enter as one (bfloat16 queries are exact in it, probabilities
+ *   are rounded to 11 bits), and where a step has rows enough to fill the GPU
+ *   with tiles of 128, keys and values may be rounded to binary16, too: keys to 11
+ *   bits down to 2^-10 and to multiples of 2^-21 below, values beyond 65504 become infinite.
+ *   A coefficient that is not finite makes what sees it not finite: a key's
+ *   its queries' outputs, a value's its group of elements in them.
  *   The result is the same on every run on the same GPU model.
  *   workspace: qmm_kv_attend_workspace_size() bytes, whose first 4096 bytes
  *   are zero before the first call; every call leaves them zero again.  Two calls in
