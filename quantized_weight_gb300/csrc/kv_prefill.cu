@@ -38,12 +38,12 @@
 //
 // Bound: 4 * D flops a row and key on the tensor cores (1024 cycles a step of 128 rows and 128 keys at D = 128).  Measured: a
 // prompt of 4096 tokens, 32 query and 8 kv heads of 128, 155 us: 45 % of the measured matrix rate; chunks over 700 to 9000
-// tokens, 16 and 4 heads of 256, 321 us: 37 %.  By its own clock a step takes some 2200 cycles: issue of its 16 MMAs 1300 (80
+// tokens, 16 and 4 heads of 256, 296 us: 40 %.  By its own clock a step takes some 2200 cycles: issue of its 16 MMAs 1300 (80
 // each; unrolled and rolled alike), waits 550; the softmax of a tile (2400 cycles of columns, 900 of waits and the mask's
 // test) and the conversion (3700 of the 4400 a block of two steps) are as long, so that no role has slack.
 // Slower, and gone: conversion from global memory (keys 1700 and values 1250 cycles, but 950 and 1050 for their loads:
 // 176 us), a wait by one lane of a warp (241 us), rolled MMA loops (188 against 179 us), TMEM loads of scores ahead (153 against
-// 155 us here, 323 against 320 for heads of 256).
+// 155 us here, slower for heads of 256).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <type_traits>
@@ -577,13 +577,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll
                 for (int k = 0; k < GK; k++) most = max(most, cf[i][k] & 0x7FFFu);
               const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
-#pragma unroll 1
-              for (int i = 0; i < PW; i++) {                         // rolled, the pieces moving up, as for the values
+#pragma unroll                                               // (rolled: chunks of heads of 256 in 320 instead of 295 us)
+              for (int i = 0; i < PW; i++) {
                 const int c = i / 2 % NC, row = (i & 1) * 8 + ((lane >> 2) & 1) * 4 + (lane >> 3);
                 const int pos = (w4 * TW + i / (2 * NC)) * 16 + row;
 #pragma unroll
                 for (int k = 0; k < WC; k++) {
-                  const uint32_t cc = cf[0][k / (WC / GK)], x = w[0][k];
+                  const uint32_t cc = cf[i][k / (WC / GK)], x = w[i][k];
                   const uint32_t b2 = hmul2(prmt(cc, cc, 0x3232), 0x2C002C00u /* 1/16 */);
                   // nibbles (0, 4), (1, 5), (2, 6), (3, 7) -> elements 0 .. 7 in order
                   uint32_t e04, e15, e26, e37;
@@ -599,13 +599,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                   const int d = 32 * (WC * c + k) + 8 * t, ch = (d & 63) >> 3;
                   sts128(dst + (d >> 6) * (KB * 128) + pos * 128 + ((ch ^ (row & 7)) << 4), prmt(e04, e15, 0x5410),
                          prmt(e26, e37, 0x5410), prmt(e04, e15, 0x7632), prmt(e26, e37, 0x7632));
-                }
-#pragma unroll
-                for (int n = 0; n + 1 < PW; n++) {
-#pragma unroll
-                  for (int k = 0; k < WC; k++) w[n][k] = w[n + 1][k];
-#pragma unroll
-                  for (int k = 0; k < GK; k++) cf[n][k] = cf[n + 1][k];
                 }
               }
             }
