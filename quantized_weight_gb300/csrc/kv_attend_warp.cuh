@@ -40,7 +40,7 @@
 //     busy (two MMAs a product for float32).
 //   64 requests of 64 to 8192 tokens, 32 and 8 heads of 128, bfloat16: 41 us, 20 us of bytes.  The start (lengths, list of items,
 //     q: 4 us) and the last items' joins are a fifth of it.
-//   1 request of 777 tokens, 16 and 8 heads of 128, float32: 12 us; 24 requests of drafts, heads of 64: 19 us.  Bound: latency of
+//   1 request of 777 tokens, 16 and 8 heads of 128, float32: 12 us; 24 requests of drafts, heads of 64: 18 us.  Bound: latency of
 //     the chain launch, lengths, pages, first tiles, join, parts.
 // Slower, and gone: bulk copies with barriers (a warp waits 250 cycles for a barrier long complete and 500 to issue a copy:
 // 126 against 118 us for the first case), four small CTAs an SM instead of teams in one (17.3 against 14.5 us for the third).
@@ -1005,10 +1005,14 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
   p.ratio = (int)(a.heads / a.kv_heads);
-  // Items that outnumber the SMs go to small teams, whose joins overlap; few
-  // items to whole CTAs, which leave fewer parts to add up.
+  // Items that far outnumber the SMs go to small teams, whose joins overlap; fewer
+  // items to whole CTAs, which leave fewer parts to add up.  Small teams against whole CTAs: 512 items of 64 to 8192 tokens 41.0
+  // and 46.0 us; 192 items of up to 1024 tokens 18.5 and 17.8; 8 items of 777 tokens 14.5 and 11.6; 32 of 60000 and more 119
+  // and 117.
   const int64_t items = a.B * a.kv_heads * ((a.max_fresh * p.ratio + C::ROWS - 1) / C::ROWS);
-  p.team = items > kv_max_ctas(1) ? C::TW : C::W;
+  p.team = items > 2 * kv_max_ctas(1) ? C::TW : C::W;
+  // (units a warp of 1 / 1.5 / 2 / 3 for an item's start: 46.0 / 42.4 / 41.0 / 42.8 us for the 512 items; one unit a warp as
+  // the least that is worth a team: 14.1 us for the 8 items)
   p.min_units = 2 * p.team;
   p.head = 2 * p.team;
   // the most steps that the line can have, in 32 bits
