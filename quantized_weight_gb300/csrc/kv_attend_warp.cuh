@@ -85,10 +85,12 @@ struct Seg {
   int c0, nseg;                   // first team and number of teams that share the item
 };
 
-// A team's place on the line of units (shared memory).
+// A team's place on the line of units (shared memory).  Once the team has begun, its first warp alone reads the place; `segs`
+// and `more` are written between the two barriers around the listing and read after the second.
 struct Line {
   int at, off, end;               // next step to list; the same from request b's first one on; end of the team's run
   int b, segs, last;              // request; items listed; this team adds the parts up
+  int more;                       // steps are left behind those listed
 };
 
 template <int D, int G, int NT, bool HL>
@@ -349,13 +351,13 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
   const int me = team * gridDim.x + blockIdx.x;
   if (me >= A) return;
   Line *line = lines + team;
+  if (line->at >= line->end) return;                                 // cuts moved onto one another: nothing to list
 
   int islot = 0, tslot = 0;                                          // this warp's ring: next slot to fill, to take
   uint32_t notes = 0;                                                // UT bits a slot: tiles without a page
-  for (;;) {
+  do {
     // -------------------------------------------------------------- list the next items: 32 requests, up to kMaxSegs items
     team_sync(team, tthreads);
-    if (line->at >= line->end) break;
     if (twarp == 0) {
       const int cb = line->b, b = cb + lane;
       const int lo = line->off, hi = lo + (line->end - line->at);    // the team's run, from request cb's first step on
@@ -438,11 +440,12 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         line->b = m ? cb + nx : cb + 32;
         line->off = m ? stop - nx_first : stop - nx_end;
         line->at = g + stop;
+        line->more = stop < hi && line->b < B;
       }
     }
     team_sync(team, tthreads);
     const int nsegs = line->segs;
-    if (nsegs == 0) continue;
+    if (nsegs == 0) continue;                                        // 32 requests without an item
 
     // -------------------------------------------------------------- producer: this warp's units, in order
     // Each lane holds the page of a part of one of the warp's next units (a unit
@@ -993,7 +996,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         }
       }
     }
-  }
+  } while (line->more);
 }
 
 // ---------------------------------------------------------------- host side

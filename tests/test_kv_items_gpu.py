@@ -1,0 +1,57 @@
+"""kv_attend where its teams and persistent CTAs take many items one after the other, against float64 (kv_vector.py)."""
+import numpy as np
+import pytest
+
+import kv_vector as vec
+from test_kv_gpu import dev, make_cache, tolerance
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qmm():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_weight_gb300 import build, qmm as q
+    build.build()
+    return q
+
+
+def check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, runs=3):
+    """One call, checked against float64, and `runs` more that have to give the same bits."""
+    import torch
+    B, scale = len(lens), D ** -0.5
+    per = [-(-n // page) for n in lens]
+    pages = sum(per) + 1
+    cache, perm = make_cache(rng, pages, Hkv, D, page, group), rng.permutation(pages).astype(np.int32)
+    table, at = np.full((B, max(1, max(per))), -1, np.int32), 0
+    for b in range(B):
+        table[b, :per[b]] = perm[at:at + per[b]]
+        at += per[b]
+    cu = np.concatenate(([0], np.cumsum(fresh))).astype(np.int32)
+    q = dev(rng.standard_normal((int(cu[-1]), H, D)).astype(np.float32)).to(getattr(torch, dtype))
+    most = max(1, max(fresh))
+    ws = qmm.kv_attend_workspace(B, H, Hkv, D, most)
+    args = (q, dev(cache), dev(table), dev(np.array(lens, np.int32)), page, group, ws)
+    kw = dict(cu=dev(cu), max_fresh=most, scale=scale, window=window)
+    out = qmm.kv_attend(*args, **kw, out=torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda"))
+    again = [qmm.kv_attend(*args, **kw) for _ in range(runs)]
+    qmm.check()
+    assert not ws[:4096].any()
+    want, sizes = vec.attend(q.float().cpu().numpy(), *vec.decode(cache, D, page, group), table, lens, cu, page, scale, window)
+    got = out.float().cpu().numpy().astype(np.float64)
+    tol = tolerance(sizes, want, max(lens), D, dtype)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all(), f"{np.max(np.abs(got - want) / tol):.2f} of the tolerance"
+    assert all(torch.equal(out, x) for x in again)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_teams_that_list_many_times(qmm, dtype):
+    """A team lists 32 requests, and as many items, at a time: here its run holds several lists, some of them empty."""
+    rng = np.random.default_rng(43)
+    lens, fresh = rng.integers(0, 50, 3000), rng.integers(1, 3, 3000)
+    fresh[200:290], fresh[1000:1064] = 0, 0                # runs of requests that ask nothing
+    fresh[2900:] = 0
+    check_items(qmm, rng, lens.tolist(), fresh.tolist(), 8, 8, 64, 64, 16, dtype, runs=20)
