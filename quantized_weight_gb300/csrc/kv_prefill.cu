@@ -99,7 +99,7 @@ struct Cfg {
   static constexpr int RAW = KB / 16 * HALF, OFF_END = OFF_RAW + 2 * RAW;
   static constexpr int EDGES = 8;                          // blocks of an item that only some rows see: at most 3 at either end
   static constexpr int NOTES = EDGES * G * (KB / 32);      // a bit a (block, group, position)
-  static constexpr int SMALL = 512 + 4 * NOTES * 4;
+  static constexpr int SMALL = 576 + 4 * NOTES * 4;
   static constexpr int SMEM = OFF_END + SMALL + 1024;      // the last for alignment
 };
 
@@ -107,7 +107,7 @@ struct Cfg {
 // complete (two blocks ahead, and an item of one block is two phases).
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, FULL = 8, K_EMPTY = 16, V_EMPTY = 18, IT_FULL = 20,
        IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, RAW_FULL, RAW_EMPTY = RAW_FULL + 2,
-       BARS = RAW_EMPTY + 2 };
+       S_LAST = RAW_EMPTY + 2, BARS = S_LAST + ITEM_SLOTS };
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -243,13 +243,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   const uint32_t sb = smem_addr(smem);
   const uint32_t bars = sb + C::OFF_END;
   uint8_t *small = smem + C::OFF_END;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 256);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 260);
-  uint32_t *kvalid = reinterpret_cast<uint32_t *>(small + 288);              // [8] blocks: tiles with a page
-  Item *items = reinterpret_cast<Item *>(small + 320);                       // [ITEM_SLOTS]
-  static_assert(8 * BARS <= 256 && 320 + ITEM_SLOTS * sizeof(Item) <= 512, "small arrays");
-  int *noted = reinterpret_cast<int *>(small + 264);                         // [4] items: has notes
-  uint32_t *notes = reinterpret_cast<uint32_t *>(small + 512);               // [4] items x NOTES: values taken out
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 304);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 308);
+  int *noted = reinterpret_cast<int *>(small + 312);                         // [4] items: has notes
+  uint32_t *kvalid = reinterpret_cast<uint32_t *>(small + 352);              // [8] blocks: tiles with a page
+  Item *items = reinterpret_cast<Item *>(small + 384);                       // [ITEM_SLOTS]
+  static_assert(8 * BARS <= 304 && 384 + ITEM_SLOTS * sizeof(Item) <= 576, "small arrays");
+  uint32_t *notes = reinterpret_cast<uint32_t *>(small + 576);               // [4] items x NOTES: values taken out
   auto bar = [&](int i) { return bars + 8 * i; };
   const WaitCtl ctl{abort_flag, &g_kv_status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     for (int i = 0; i < ITEM_SLOTS; i++) {
       mbar_init(bar(IT_FULL + i), 1);
       mbar_init(bar(IT_EMPTY + i), ITEM_READERS);        // a warp an arrival
+      mbar_init(bar(S_LAST + i), 1);
     }
     for (int i = 0; i < 2; i++) {
       mbar_init(bar(S_FULL + i), 1);
@@ -449,6 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                           desc(kd + (kk / 4) * (KB * 128 / 16) + 2 * (kk % 4)), id_s, kk != 0);
             umma_commit(bar(S_FULL + buf));
             if (x == nt - 1) umma_commit(bar(K_EMPTY + kbuf));
+            if (NQ == 2 && nt == 1 && i > 0 && i == N - 1) umma_commit(bar(S_LAST + it_slot));
           }
           __syncwarp();
         };
@@ -696,6 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     const float NINF = __int_as_float(0xFF800000);
     uint32_t s_base[2] = {0, 0};                   // score tiles finished in either buffer before this item
     int pv_base = 0, blk_base = 0, n_item = 0;     // this tile's PV products, the blocks and the items before this item
+    uint32_t last_ph = 0;                          // S_LAST's parities, a bit an item slot
     bool ok = true;
     for (; const Item *ip = next_item(); n_item++) {
       const Item &it = *ip;
@@ -705,7 +708,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         blk_base += it.blocks;
         release();
       };
+      // The first tile alone: its scores take turns in both buffers, the second of which is this tile's in the next item.  A
+      // parity tells apart only a phase and the next, so the item is left when its last scores are there.
       if (x >= it.tiles) {
+        if (it.blocks > 1) {
+          if (!warp_wait(bar(S_LAST + it_slot), (last_ph >> it_slot) & 1u, ctl)) break;
+          last_ph ^= 1u << it_slot;
+        }
         leave();
         continue;
       }

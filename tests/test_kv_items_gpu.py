@@ -55,3 +55,39 @@ def test_teams_that_list_many_times(qmm, dtype):
     fresh[200:290], fresh[1000:1064] = 0, 0                # runs of requests that ask nothing
     fresh[2900:] = 0
     check_items(qmm, rng, lens.tolist(), fresh.tolist(), 8, 8, 64, 64, 16, dtype, runs=20)
+
+
+def takes_tiles(B, H, Hkv, D, most):
+    """These cases have rows enough for the prompt kernel, which takes tiles of 128 of them, and items for several turns of
+    every SM (152)."""
+    rows = most * H // Hkv
+    items = B * Hkv * -(-rows // (128 if D == 256 else 256))
+    return items > 2 * 152 and B * Hkv * rows > 8000 * -(-items // 152)
+
+
+@pytest.mark.parametrize("blocks", [2, 1, 4, 3])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (128, 32), (256, 64)])
+def test_items_of_one_tile_before_items_of_two(qmm, D, group, blocks):
+    """A persistent CTA's score buffers belong to one row tile in turn or to two side by side, as its items come; here items
+    of one tile and two (an even number too) blocks of keys stand between items of two tiles, some of which see nothing."""
+    rng = np.random.default_rng(100 * D + blocks)
+    KB, H, Hkv, B = 64 if D == 256 else 128, 32, 8, 80
+    fresh = [20 if b % 2 else 64 for b in range(B)]        # 80 rows or 256
+    lens = [int(rng.integers(max(KB * (blocks - 1), 20) + 1, KB * blocks + 1)) if b % 2 else int(rng.integers(64, 3 * KB))
+            for b in range(B)]
+    fresh[7], lens[10], lens[33] = 0, 0, 9
+    assert takes_tiles(B, H, Hkv, D, 64)
+    check_items(qmm, rng, lens, fresh, H, Hkv, D, group, 32, "bfloat16", runs=8)
+
+
+@pytest.mark.parametrize("window", [0, 1, 130])
+@pytest.mark.parametrize("D,group,page", [(64, 32, 16), (128, 128, 64), (256, 64, 32)])
+def test_items_of_ragged_steps(qmm, D, group, page, window):
+    """Single tokens, drafts, chunks and empty requests in one step."""
+    rng = np.random.default_rng(D + window)
+    B, H, Hkv = 70, 32, 8
+    fresh = rng.choice([0, 1, 1, 1, 4, 17, 33, 70, 150], B)
+    fresh[0] = 150
+    lens = np.maximum(0, fresh + rng.integers(-4, 700, B))
+    assert takes_tiles(B, H, Hkv, D, 150)
+    check_items(qmm, rng, lens.tolist(), fresh.tolist(), H, Hkv, D, group, page, "bfloat16", window=window, runs=5)
