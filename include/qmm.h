@@ -329,7 +329,8 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
  *   For QMM_BF16 they enter as one (bfloat16 queries are exact in it, probabilities
  *   are rounded to 11 bits), and where a step has rows enough to fill the GPU
  *   with tiles of 128, keys and values may be rounded to binary16, too: keys to 11
- *   bits down to 2^-10 and to multiples of 2^-21 below, values beyond 65504 become infinite.
+ *   bits down to 2^-10 and to multiples of 2^-20 below, values to 11 bits down to 2^-14 and to
+ *   multiples of 2^-24 below (beside values beyond 32768, as keys).
  *   A coefficient that is not finite makes what sees it not finite: a key's
  *   its queries' outputs, a value's its group of elements in them.
  *   The result is the same on every run on the same GPU model.

@@ -32,7 +32,10 @@
 // tile shows only in the mask.
 //
 // Precision: q is exact in binary16 after a power of two per row; keys and values are s * q + b
-// rounded once to binary16; P is rounded to binary16, at most 2^8 (the reference
+// rounded once to binary16, keys as a 16th of themselves, which is in range for all finite s and b.  Values
+// stand as they are, for their low end; an item that meets coefficients with which one could pass
+// 65504 is done a second time with a 16th of its values (a look at every coefficient of a block: 158.7 against 156.4 us
+// for the prompt below; a masked value may not become infinite, since 0 times it is not 0).  P is rounded to binary16, at most 2^8 (the reference
 // maximum follows the true one only when that has grown by 2^8, so O is seldom
 // rescaled); sums and accumulators are float32.
 //
@@ -85,6 +88,7 @@ struct Item {
   int vlo, vhi;                     // tokens that any row sees
   int flo, fhi;                     // tokens that all rows see
   int base, hi, cu0;                // position of the first query; tokens that can be read; its token
+  int vexp;                         // values stand in shared memory divided by 2^vexp
 };
 
 template <int D_, int G_>
@@ -175,6 +179,9 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t x) {
 // where they lie, divided by 2^10, take two instructions a word less, 2 % of the kernel, but keys below 2^-4 then lose
 // bits to binary16's subnormals instead of keys below 2^-10.)
 constexpr float KEY_UNIT = 16.0f;
+// Values stand there as they are.  Scale and bias (magnitudes) from which on s * code + b may pass 65504: 15 * 2^11 + 2^15 does
+// not.  A 16th of a value is in range whatever they are.
+__device__ __forceinline__ bool large_value(uint32_t m) { return (m & 0xFFFFu) >= 0x6800u || m >= 0x78000000u; }
 __device__ __forceinline__ void sts128(uint32_t dst, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -246,6 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + 304);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(small + 308);
   int *noted = reinterpret_cast<int *>(small + 312);                         // [4] items: has notes
+  volatile int *over = reinterpret_cast<int *>(small + 328);                 // [4] items: values may pass binary16's range
   uint32_t *kvalid = reinterpret_cast<uint32_t *>(small + 352);              // [8] blocks: tiles with a page
   Item *items = reinterpret_cast<Item *>(small + 384);                       // [ITEM_SLOTS]
   static_assert(8 * BARS <= 304 && 384 + ITEM_SLOTS * sizeof(Item) <= 576, "small arrays");
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     }
     for (int i = 0; i < 8; i++) mbar_init(bar(FULL + i), NQ == 2 ? 128 : 256);
     mbar_init(bar(DRAIN), 1);
-    mbar_init(bar(IT_NEXT), 4);
+    mbar_init(bar(IT_NEXT), NQ == 2 ? 4 : 8);            // a warp that converts an arrival
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -348,15 +356,21 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     int cb = 0;                               // requests before cb are behind this CTA's tickets
     int64_t cfirst = 0;                       // items before request cb
     uint32_t ph = 1, next = 1;
-    for (int slot = 0;;) {
-      // A ticket is drawn when the keys of the item before it are done: earlier, CTAs would sit on items that others could begin.
+    int before = 0;                           // slot of the item before
+    bool again = false;
+    for (int slot = 0, n_item = 0;; n_item++) {
+      // A ticket is drawn when the conversion for the item before it is done: earlier, CTAs would sit on items that others
+      // could begin.
       if (!warp_wait(bar(IT_NEXT), next, ctl)) break;
       next ^= 1u;
+      // The item before had values beyond binary16's range: once more, with a 16th of them.  The same threads write the same
+      // rows, after those of the first time.
+      again = !again && n_item > 0 && over[(n_item - 1) & 3] != 0;
       unsigned t = 0;
-      if (lane == 0) t = atomicAdd(ticket, 1u);
+      if (lane == 0 && !again) t = atomicAdd(ticket, 1u);
       t = __shfl_sync(0xffffffffu, t, 0);
       Item it{};
-      for (; cb < a.B; cb += 32) {
+      for (; cb < a.B && !again; cb += 32) {
         const int b = cb + lane;
         int n = 0, len = 0, c0 = 0, tiles = 0;
         if (b < a.B) {
@@ -402,10 +416,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       }
       if (!warp_wait(bar(IT_EMPTY + slot), ph, ctl)) break;
       if (lane == 0) {
-        items[slot] = it;
+        items[slot] = again ? items[before] : it;
+        if (again) items[slot].vexp = 4;
         mbar_arrive(bar(IT_FULL + slot));
       }
-      if (it.tiles == 0) break;
+      if (!again && it.tiles == 0) break;
+      before = slot;
       if (++slot == ITEM_SLOTS) slot = 0, ph ^= 1u;
     }
     // the last CTA through leaves the counters zero for the next call
@@ -518,9 +534,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         uint32_t *my_notes = notes + (n_item & 3) * C::NOTES;
         if constexpr (VALUES) {
           for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
-          if (u == 0) noted[n_item & 3] = 0;
+          if (u == 0) noted[n_item & 3] = 0, over[n_item & 3] = 0;
           asm volatile("bar.sync 1, 128;" ::: "memory");
         }
+        const bool sixteenth = it.vexp != 0;
         uint32_t w[PW][WC], cf[PW][GK];
         auto take_keys = [&]() {
 #pragma unroll
@@ -608,6 +625,14 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           if (VALUES && n > 0) {
             const int j = n - 1, blk = it.blk0 + j, buf = (kb + j) & 1;
             if (!warp_wait(bar(RAW_FULL + 1), vr.next(), ctl)) { ok = false; break; }
+            if (sixteenth) {
+#pragma unroll 1
+              for (int i = u; i < KB * G; i += 128) {
+                uint32_t *c = reinterpret_cast<uint32_t *>(smem + C::OFF_RAW + C::RAW + i / (16 * G) * C::HALF + 8 * D) + i % (16 * G);
+                *c = hmul2(*c, 0x2C002C00u /* 1/16 */);
+              }
+              asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
             take_values();
             // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
             // non-finite coefficient must not meet the zero probability of a row that does not: it is taken out, too, and
@@ -630,6 +655,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                       atomicOr(&my_notes[(e * G + grp) * (KB / 32) + (pos >> 5)], 1u << (pos & 31));
                       noted[n_item & 3] = 1;
                       out[g] |= 1u << r;
+                    } else if (large_value(m)) {
+                      over[n_item & 3] = 1;
                     }
                   }
                 }
@@ -639,6 +666,14 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll
                 for (int g = 0; g < GV; g++)
                   if ((out[g] >> r) & 1u) vf[r][g] = 0u;
+            } else if (act) {                                    // the eight threads with the same coefficients look at two rows each
+              uint32_t most = 0;
+#pragma unroll
+              for (int r = 0; r < 2; r++)
+#pragma unroll
+                for (int g = 0; g < GV; g++)
+                  most = __vmaxu2(most, *(reinterpret_cast<const uint32_t *>(coefs + (2 * g8 + r) * G * 4) + g) & 0x7FFF7FFFu);
+              if (large_value(most)) over[n_item & 3] = 1;
             }
             mbar_arrive(bar(RAW_EMPTY + 1));
             if (!warp_wait(bar(V_EMPTY + buf), ve[buf].next(), ctl)) { ok = false; break; }
@@ -684,7 +719,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         }
         if (!ok) break;
         kb += it.blocks;
-        if (KEYS && lane == 0) mbar_arrive(bar(IT_NEXT));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(IT_NEXT));
         release();
       }
     };
@@ -861,7 +897,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
         }
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float inv = l == 0.0f ? 0.0f : (it.vexp == 0 ? 1.0f : 16.0f) / l;
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)(it.cu0 + qi) * a.heads + it.kvh * p.ratio + hq) * D;
 #pragma unroll 1
       for (int ch = 0; ch < D / 16; ch++) {

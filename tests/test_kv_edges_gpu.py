@@ -1,0 +1,111 @@
+"""The 4-bit key/value cache operators at the ends of what they accept."""
+import numpy as np
+import pytest
+
+import kv_vector as vec
+from test_kv_gpu import dev, make_cache, tolerance
+from test_kv_items_gpu import check_items, takes_tiles
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def qmm():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from quantized_weight_gb300 import build, qmm as q
+    build.build()
+    return q
+
+
+class Case:
+    """One request of `length` tokens, the last n of which ask; H = 64 over 2 kv heads are rows enough for the prompt kernel."""
+
+    def __init__(self, seed, D, group, H, dtype, n=140, length=150, page=16, Hkv=2):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.D, self.group, self.H, self.Hkv, self.n, self.length, self.page, self.dtype = D, group, H, Hkv, n, length, page, dtype
+        blocks = -(-length // page)
+        self.cache = make_cache(rng, blocks + 2, Hkv, D, page, group)
+        self.table = rng.permutation(blocks + 2).astype(np.int32)[None, :blocks]
+        self.q = dev(rng.standard_normal((n, H, D)).astype(np.float32)).to(getattr(torch, dtype))
+
+    def coef(self, token, head, value, g):
+        """[scale, bias] of a token's key or value as binary16 bits, to be written."""
+        tile = self.cache[self.table[0, token // self.page], head].reshape(self.page // 16, -1)[token % self.page // 16]
+        G = self.D // self.group
+        at = 16 * self.D + value * 64 * G + ((8 * (token % 2) + 2 * (token % 16 // 4) + (token // 2) % 2) * G + g) * 4
+        return tile[at:at + 4].view(np.uint16)
+
+    def want(self, scale=None, window=0, cache=None):
+        """(out, tolerance) in 64 bits."""
+        scale = self.D ** -0.5 if scale is None else scale
+        k, v = vec.decode(self.cache if cache is None else cache, self.D, self.page, self.group)
+        want, sizes = vec.attend(self.q.float().cpu().numpy(), k, v, self.table, [self.length], [0, self.n], self.page, scale,
+                                 window)
+        return want, np.broadcast_to(tolerance(sizes, want, self.length, self.D, self.dtype), want.shape)
+
+    def run(self, qmm, scale=None, window=0):
+        ws = qmm.kv_attend_workspace(1, self.H, self.Hkv, self.D, self.n)
+        out = qmm.kv_attend(self.q, dev(self.cache), dev(self.table), dev(np.array([self.length], np.int32)), self.page,
+                            self.group, ws, cu=dev(np.array([0, self.n], np.int32)), max_fresh=self.n, scale=scale, window=window)
+        qmm.check()
+        assert not ws[:4096].any()
+        return out.float().cpu().numpy().astype(np.float64)
+
+
+ROUTES = [(4, "float32"), (4, "bfloat16"), (64, "float32"), (64, "bfloat16")]
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D,group", [(64, 32), (64, 64), (128, 64), (128, 128), (256, 32), (256, 128)])
+def test_finite_values_beyond_binary16(qmm, D, group, H, dtype, window):
+    """Finite coefficients whose values pass 65504: finite outputs everywhere, and queries that do not see them as exact as ever."""
+    c = Case(D + H, D, group, H, dtype)
+    G = D // group
+    for token, head, g, s, b in ((149, 0, 0, 5332, 0), (149, 1, G - 1, 65504, 65504), (131, 0, G - 1, -5332, 0),
+                                 (64, 1, 0, 8000, -60000), (9, 0, 0, 65504, -65504)):
+        c.coef(token, head, 1, g)[:] = np.array([s, b], np.float16).view(np.uint16)
+    want, tol = c.want(window=window)
+    got = c.run(qmm, window=window)
+    assert np.isfinite(got).all()
+    # bounds by element: |v| of the groups that hold large values would hide the others
+    k, v = vec.decode(c.cache, D, c.page, group)
+    for g in range(G):
+        part = slice(g * group, (g + 1) * group)
+        _, sizes = vec.attend(c.q.float().cpu().numpy(), k, np.where(np.arange(D) // group == g, v, 0.0), c.table, [c.length],
+                              [0, c.n], c.page, D ** -0.5, window)
+        bound = tolerance(sizes, want[..., part], c.length, D, dtype)
+        assert (np.abs(got - want)[..., part] <= bound).all(), g
+
+
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 64)])
+def test_finite_values_beyond_binary16_in_some_of_many_items(qmm, D, group):
+    """Items with such values and without, one after the other on every SM."""
+    rng = np.random.default_rng(D)
+    B, H, Hkv, page = 80, 32, 8, 32
+    fresh = [20 if b % 2 else 64 for b in range(B)]
+    lens = rng.integers(64, 300, B).tolist()
+
+    def change(cache, table):
+        tiles = cache.reshape(len(cache), Hkv, page // 16, -1)
+        coef = tiles[..., 16 * D + 64 * (D // group):].reshape(len(cache), Hkv, -1)
+        for b in range(0, B, 3):
+            row = table[b, int(rng.integers(0, lens[b] // page))], int(rng.integers(0, Hkv))
+            coef[row][4:8].view(np.float16)[:] = 65504, -30000
+        tiles[..., 16 * D + 64 * (D // group):] = coef.reshape(len(cache), Hkv, page // 16, -1)
+
+    assert takes_tiles(B, H, Hkv, D, 64)
+    check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, "bfloat16", runs=5, change=change)
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 128)])
+def test_finite_keys_beyond_binary16(qmm, D, group, H, dtype):
+    c = Case(D + H, D, group, H, dtype)
+    for token, head, g, s, b in ((149, 0, 0, 5332, 0), (100, 1, 0, 65504, 65504), (64, 1, D // group - 1, 8000, -60000)):
+        c.coef(token, head, 0, g)[:] = np.array([s, b], np.float16).view(np.uint16)
+    want, tol = c.want(scale=1e-7)
+    assert (np.abs(c.run(qmm, scale=1e-7) - want) <= tol).all()

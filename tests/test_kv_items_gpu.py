@@ -18,8 +18,9 @@ def qmm():
     return q
 
 
-def check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, runs=3):
-    """One call, checked against float64, and `runs` more that have to give the same bits."""
+def check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, runs=3, change=None):
+    """One call, checked against float64, and `runs` more that have to give the same bits.  change(cache, table) may put
+    other bytes into the cache; each group of elements then has a bound by its own values."""
     import torch
     B, scale = len(lens), D ** -0.5
     per = [-(-n // page) for n in lens]
@@ -29,6 +30,8 @@ def check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, 
     for b in range(B):
         table[b, :per[b]] = perm[at:at + per[b]]
         at += per[b]
+    if change is not None:
+        change(cache, table)
     cu = np.concatenate(([0], np.cumsum(fresh))).astype(np.int32)
     q = dev(rng.standard_normal((int(cu[-1]), H, D)).astype(np.float32)).to(getattr(torch, dtype))
     most = max(1, max(fresh))
@@ -39,9 +42,16 @@ def check_items(qmm, rng, lens, fresh, H, Hkv, D, group, page, dtype, window=0, 
     again = [qmm.kv_attend(*args, **kw) for _ in range(runs)]
     qmm.check()
     assert not ws[:4096].any()
-    want, sizes = vec.attend(q.float().cpu().numpy(), *vec.decode(cache, D, page, group), table, lens, cu, page, scale, window)
+    k, v = vec.decode(cache, D, page, group)
+    qh, at = q.float().cpu().numpy(), (table, lens, cu, page, scale, window)
+    want, sizes = vec.attend(qh, k, v, *at)
     got = out.float().cpu().numpy().astype(np.float64)
-    tol = tolerance(sizes, want, max(lens), D, dtype)
+    tol = np.broadcast_to(tolerance(sizes, want, max(lens), D, dtype), want.shape).copy()
+    if change is not None:
+        for g in np.arange(0, D, group):
+            part = np.zeros(D)
+            part[g:g + group] = 1.0
+            tol[..., g:g + group] = tolerance(vec.attend(qh, k, v * part, *at)[1], want, max(lens), D, dtype)[..., g:g + group]
     assert np.isfinite(got).all()
     assert (np.abs(got - want) <= tol).all(), f"{np.max(np.abs(got - want) / tol):.2f} of the tolerance"
     assert all(torch.equal(out, x) for x in again)
