@@ -327,7 +327,7 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
  *   Scores, maxima, sums and the accumulation are float32; for QMM_F32 the
  *   queries and probabilities enter the tensor cores as two binary16 terms.
  *   For QMM_BF16 they enter as one (bfloat16 queries are exact in it, probabilities
- *   are rounded to 11 bits), and where a step has rows enough to fill the GPU
+ *   are rounded to 11 bits, those below 2^-21 of a query's largest to multiples of 2^-31 of it), and where a step has rows enough to fill the GPU
  *   with tiles of 128, keys and values may be rounded to binary16, too: keys to 11
  *   bits down to 2^-10 and to multiples of 2^-20 below, values to 11 bits down to 2^-14 and to
  *   multiples of 2^-24 below (beside values beyond 32768, as keys).

@@ -35,9 +35,11 @@
 // rounded once to binary16, keys as a 16th of themselves, which is in range for all finite s and b.  Values
 // stand as they are, for their low end; an item that meets coefficients with which one could pass
 // 65504 is done a second time with a 16th of its values (a look at every coefficient of a block: 158.7 against 156.4 us
-// for the prompt below; a masked value may not become infinite, since 0 times it is not 0).  P is rounded to binary16, at most 2^8 (the reference
+// for the prompt below; a masked value may not become infinite, since 0 times it is not 0).  P is
+// rounded to binary16 at 2^7 to 2^15 of the largest weight, which keeps 11 bits of weights down to 2^-21 of it (a
+// long context has many such beside a large one) and multiples of 2^-31 below; the reference
 // maximum follows the true one only when that has grown by 2^8, so O is seldom
-// rescaled); sums and accumulators are float32.
+// rescaled; sums and accumulators are float32.
 //
 // Bound: 4 * D flops a row and key on the tensor cores (1024 cycles a step of 128 rows and 128 keys at D = 128).  Measured: a
 // prompt of 4096 tokens, 32 query and 8 kv heads of 128, 155 us: 45 % of the measured matrix rate; chunks over 700 to 9000
@@ -74,6 +76,7 @@ constexpr int ITEM_READERS = 15;                 // warps that take every item: 
 constexpr int THREADS = 32 * 16;
 constexpr int ITEM_SLOTS = 3;
 constexpr float GROW = 8.0f;                     // log2 by which scores may exceed the reference maximum
+constexpr float P_EXP = 7.0f;                    // P is 2^7 at the reference maximum (2^15 at most); l and O carry the factor, too
 
 struct Params {
   KvAttendArgs a;
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             rescale<D>(k > 0 ? o_tm : 0xFFFFFFFFu, s_tm, h / 2, f);
           }
           const float mu = m == NINF ? 0.0f : m;
-          const f2 mu2 = f2_make(-mu, -mu);
+          const f2 mu2 = f2_make(P_EXP - mu, P_EXP - mu);
           f2 l2[2] = {f2_zero(), f2_zero()};
           uint32_t o[16];
 #pragma unroll

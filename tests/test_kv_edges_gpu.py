@@ -109,3 +109,41 @@ def test_finite_keys_beyond_binary16(qmm, D, group, H, dtype):
         c.coef(token, head, 0, g)[:] = np.array([s, b], np.float16).view(np.uint16)
     want, tol = c.want(scale=1e-7)
     assert (np.abs(c.run(qmm, scale=1e-7) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 64), (256, 64)])
+@pytest.mark.parametrize("sink", [9.0, 12.3, 14.2])
+def test_many_small_probabilities_beside_a_large_one(qmm, D, group, sink):
+    """One key takes nearly all the weight and its value is zero: the output is what 65535 tokens of e^-sink each add up to.
+    Their keys are zero and their values positive, so that the roundings of P (2^-11) and of the values (2^-11) bound the error
+    of each element before it is rounded to the output's type; float32 sums and factors stay below 2^-14."""
+    import torch
+    n, length, page, H, Hkv, G = 128, 65536, 256, 72, 2, D // group
+    assert Hkv * n * H // Hkv > 8000                       # the prompt kernel
+    rng = np.random.default_rng(D)
+    tiles = length // 16
+    codes = rng.integers(0, 256, (tiles, Hkv, 16 * D), dtype=np.uint8)
+    coef = np.zeros((tiles, Hkv, 2, 16, G, 2), np.float16)
+    coef[:, :, 1, ..., 0] = rng.uniform(0.01, 0.06, (tiles, Hkv, 16, G))
+    coef[:, :, 1, ..., 1] = rng.uniform(0.3, 0.6, (tiles, Hkv, 16, G))
+    coef[0, :, 0, 0, :, 1] = 1.0                           # token 0: a key of ones, a value of zeros
+    coef[0, :, 1, 0] = 0.0
+    cache = np.concatenate((codes, coef.view(np.uint8).reshape(tiles, Hkv, -1)), -1)
+    cache = np.ascontiguousarray(cache.reshape(length // page, page // 16, Hkv, -1).transpose(0, 2, 1, 3)).reshape(
+        length // page, Hkv, -1)
+    table = rng.permutation(length // page).astype(np.int32)
+    held = np.empty_like(cache)
+    held[table] = cache
+    q = dev((rng.uniform(0.9, 1.1, (n, H, D)) * sink * D ** -0.5).astype(np.float32)).bfloat16()
+    out = qmm.kv_attend(q, dev(held), dev(table[None]), dev(np.array([length], np.int32)), page, group,
+                        qmm.kv_attend_workspace(1, H, Hkv, D, n), cu=dev(np.array([0, n], np.int32)), max_fresh=n)
+    qmm.check()
+    _, v = vec.decode(cache, D, page, group)
+    v = torch.from_numpy(v).cuda().transpose(1, 2).reshape(length, Hkv, D)
+    upto = torch.cumsum(v, 0)[length - n:]                 # [n, Hkv, D]: sums of what each query sees
+    score = torch.exp(q.double().sum(-1) * D ** -0.5)      # the first key's weight beside ones
+    count = torch.arange(length - n, length, device="cuda")[:, None] + score
+    want = upto.repeat_interleave(H // Hkv, 1) / count[..., None]
+    off = 2 * 2.0 ** -11 + 2.0 ** -14
+    low, high = ((want * (1 + x)).to(out.dtype) for x in (-off, off))
+    assert bool(((low <= out) & (out <= high)).all()), f"{float(((out.double() - want).abs() / want).max()):.5f}"
