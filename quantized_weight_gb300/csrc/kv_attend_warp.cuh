@@ -151,6 +151,13 @@ __device__ __forceinline__ uint32_t sub_f16(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// x + 0 x in both halves: infinities become NaN, all else stays.  A key's infinite bias or scale may make its score -inf, which
+// the softmax would take for a key that is not there.
+__device__ __forceinline__ uint32_t nan_for_inf(uint32_t x) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %1;" : "=r"(d) : "r"(x), "r"(0u));
+  return d;
+}
 // Nibble I of both halves of a word as an MMA operand: the masked code as it lies is a binary16 subnormal, which the MMA
 // multiplies exactly.  Plain: nibbles 0 and 2 are code * 2^-24, 1 and 3 code * 2^-20.  But the MMA adds a product up to the
 // precision that its operands' exponents give, and a subnormal's leading zeros are lost from it: with codes of 2^-24 the
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
               for (int i = 0; i < 2; i++)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                  const float2 k = unpack_f16(kc[i][h][g]);          // scale, bias
+                  const float2 k = unpack_f16(nan_for_inf(kc[i][h][g]));     // scale, bias
                   const float t0 = g == 0 ? k.y * qs.x : fmaf(k.y, qs.x, y[i0 + i][n][2 * h]);
                   const float t1 = g == 0 ? k.y * qs.y : fmaf(k.y, qs.y, y[i0 + i][n][2 * h + 1]);
                   y[i0 + i][n][2 * h] = fmaf(k.x, c[i][n][2 * h], t0);

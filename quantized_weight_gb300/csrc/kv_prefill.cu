@@ -597,7 +597,12 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll
               for (int i = 0; i < PW; i++)
 #pragma unroll
-                for (int k = 0; k < GK; k++) most = max(most, cf[i][k] & 0x7FFFu);
+                for (int k = 0; k < GK; k++) {
+                  // x + 0 x: infinities become NaN.  (An infinite key's score may be -inf, which the softmax would take for a
+                  // key that is not there.)
+                  cf[i][k] = hfma2(cf[i][k], 0u, cf[i][k]);
+                  most = max(most, cf[i][k] & 0x7FFFu);
+                }
               const bool large = __any_sync(0xffffffffu, most >= 0x4400u);   // a scale of 4 or more
 #pragma unroll                                               // (rolled: chunks of heads of 256 in 320 instead of 295 us)
               for (int i = 0; i < PW; i++) {

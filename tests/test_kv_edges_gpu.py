@@ -56,6 +56,7 @@ class Case:
 
 
 ROUTES = [(4, "float32"), (4, "bfloat16"), (64, "float32"), (64, "bfloat16")]
+NAN, INF, MINUS_INF = 0x7E01, 0x7C00, 0xFC00
 
 
 @pytest.mark.parametrize("window", [0, 40])
@@ -147,3 +148,24 @@ def test_many_small_probabilities_beside_a_large_one(qmm, D, group, sink):
     off = 2 * 2.0 ** -11 + 2.0 ** -14
     low, high = ((want * (1 + x)).to(out.dtype) for x in (-off, off))
     assert bool(((low <= out) & (out <= high)).all()), f"{float(((out.double() - want).abs() / want).max()):.5f}"
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D,group", [(64, 32), (64, 64), (128, 64), (128, 32), (256, 64), (256, 128)])
+def test_keys_that_are_not_finite(qmm, D, group, H, dtype):
+    """Every query that sees such a key gets nothing finite, whichever the signs of its elements; no other is touched."""
+    c = Case(D + H, D, group, H, dtype)
+    c.q[::2] = c.q[::2].abs()                              # the sum over a group has one sign: a score of -inf alone
+    c.q[1::4] = -c.q[1::4].abs()
+    want, tol = c.want()
+    clean = c.cache.copy()
+    ratio, first = H // 2, c.length - c.n
+    for token, head, g in ((77, 1, D // group - 1), (149, 0, 0)):
+        hit = np.zeros(want.shape[:2], bool)
+        hit[token - first:, head * ratio:(head + 1) * ratio] = True
+        for k, bits in ((1, MINUS_INF), (1, INF), (0, INF), (0, MINUS_INF), (0, NAN), (1, NAN)):
+            c.cache[:] = clean
+            c.coef(token, head, 0, g)[k] = bits
+            got = c.run(qmm)
+            assert not np.isfinite(got[hit]).any(), (token, k, hex(bits))
+            assert (np.abs(got - want)[~hit] <= tol[~hit]).all(), (token, k, hex(bits))
