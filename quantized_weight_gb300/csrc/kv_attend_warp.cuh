@@ -702,7 +702,11 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         for (int i = 0; i < UT; i++)
 #pragma unroll
           for (int h = 0; h < 2; h++) load_coefs<G>(st + i * TILE + 16 * D + 64 * G + (lg + 8 * h) * G * 4, vc[i][h]);
+        // A token that some rows do not see may hold infinite or NaN value coefficients, which reach those that do see it whatever
+        // its weight there (0, where its exponential underflows).
+        bool guard = false;
         if (!full) {
+          uint32_t worst = 0;
 #pragma unroll
           for (int i = 0; i < UT; i++)
 #pragma unroll
@@ -716,10 +720,13 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
                   const int2 l = *reinterpret_cast<const int2 *>(lim + 2 * (8 * n + 2 * lt + c));
                   if (!there || tok < l.x || tok >= l.y) y[i][n][2 * h + c] = NINF;
                 }
-              if (!there)
 #pragma unroll
-                for (int g = 0; g < G; g++) vc[i][h][g] = 0u;
+              for (int g = 0; g < G; g++) {
+                if (!there) vc[i][h][g] = 0u;
+                worst = __vmaxu2(worst, vc[i][h][g] & 0x7FFF7FFFu);
+              }
             }
+          guard = __any_sync(0xffffffffu, (worst & 0xFFFFu) >= 0x7C00u || worst >= 0x7C000000u);
         }
 
         // ---------------------------------------------------------- running maximum and largest value scale
@@ -781,7 +788,23 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
               }
         // ---------------------------------------------------------- p * sv as B operands, bias sums
         uint32_t pf[UT][G][NT][HL ? 4 : 2];
-        auto weigh = [&](auto guard) {
+        auto weigh = [&](auto guarded) {
+          uint32_t hidden = 0;                                       // a bit a (tile, row half, row of q) that does not see the token
+          if constexpr (decltype(guarded)::value) {
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+              for (int c = 0; c < 2; c++) {
+                const int2 l = *reinterpret_cast<const int2 *>(lim + 2 * (8 * n + 2 * lt + c));
+#pragma unroll
+                for (int i = 0; i < UT; i++)
+#pragma unroll
+                  for (int h = 0; h < 2; h++) {
+                    const int tok = u * UNIT + 16 * i + tk + h;
+                    if (tok < l.x || tok >= l.y) hidden |= 1u << (((2 * i + h) * NT + n) * 2 + c);
+                  }
+              }
+          }
 #pragma unroll
           for (int g = 0; g < G; g++)
 #pragma unroll
@@ -794,10 +817,11 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
                 for (int n = 0; n < NT; n++) {
                   const float p0 = y[i][n][2 * h], p1 = y[i][n][2 * h + 1];
                   float e0 = p0 * ss, e1 = p1 * ss;
-                  if constexpr (decltype(guard)::value) {
-                    if (p0 == 0.0f) e0 = 0.0f;
+                  if constexpr (decltype(guarded)::value) {
+                    const int bit = ((2 * i + h) * NT + n) * 2;
+                    if ((hidden >> bit) & 1u) e0 = 0.0f;
                     else ob[n][0][g] = fmaf(p0, bias, ob[n][0][g]);
-                    if (p1 == 0.0f) e1 = 0.0f;
+                    if ((hidden >> (bit + 1)) & 1u) e1 = 0.0f;
                     else ob[n][1][g] = fmaf(p1, bias, ob[n][1][g]);
                   } else {
                     ob[n][0][g] = fmaf(p0, bias, ob[n][0][g]);
@@ -812,8 +836,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
                 }
               }
         };
-        // a token that some rows do not see may hold infinite or NaN coefficients
-        if (full) weigh(std::false_type());
+        if (!guard) weigh(std::false_type());
         else weigh(std::true_type());
         // ---------------------------------------------------------- values
 #pragma unroll

@@ -169,3 +169,27 @@ def test_keys_that_are_not_finite(qmm, D, group, H, dtype):
             got = c.run(qmm)
             assert not np.isfinite(got[hit]).any(), (token, k, hex(bits))
             assert (np.abs(got - want)[~hit] <= tol[~hit]).all(), (token, k, hex(bits))
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 128)])
+def test_values_that_are_not_finite_at_no_weight(qmm, D, group, H, dtype):
+    """Such a value reaches its group of every query that sees it, however small the probability."""
+    c = Case(D + H, D, group, H, dtype)
+    c.q[:] = c.q.abs()
+    ratio, first, G = H // 2, c.length - c.n, D // group
+    spots = [(77, 1, G - 1), (139, 0, 0), (5, 0, G - 1)]
+    for token, head, g in spots:
+        for i in range(G):
+            c.coef(token, head, 0, i)[:] = np.array([0.0, -1000.0], np.float16).view(np.uint16)    # exp() of it is 0
+    want, tol = c.want()
+    clean = c.cache.copy()
+    for k, bits in ((1, INF), (0, INF), (0, NAN)):
+        c.cache[:] = clean
+        hit = np.zeros(want.shape, bool)
+        for token, head, g in spots:
+            c.coef(token, head, 1, g)[k] = bits
+            hit[max(0, token - first):, head * ratio:(head + 1) * ratio, g * group:(g + 1) * group] = True
+        got = c.run(qmm)
+        assert not np.isfinite(got[hit]).any(), (k, hex(bits))
+        assert (np.abs(got - want)[~hit] <= tol[~hit]).all(), (k, hex(bits))
