@@ -557,7 +557,8 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
         for (int o = 1; o < D / G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (m % (D / G / 8) == 0) qsum[m / (D / G / 8) * ROWS + row] = sum * pow2i(-CODE);
         if (m == 0) {
-          fq[row] = ldexpf(a.scale * 1.44269504088896340736f, CODE - ex);   // log2(e)
+          // log2(e); never 0, which a masked score of -inf would make NaN
+          fq[row] = fmaxf(ldexpf(a.scale * 1.44269504088896340736f, CODE - ex), 1.17549435e-38f);
           const int qi = div_small(sg.r0 + row, p.ratio);
           const int64_t pos = (int64_t)sg.base + qi;
           const int64_t lo = a.window > 0 ? pos + 1 - a.window : 0;

@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         mx = max(mx & 0xFFFFu, mx >> 16);                      // bfloat16 bits of the largest |element|
         const int ex = mx == 0u || mx >= 0x7F80u ? 0 : min(126, 14 - ((int)(mx >> 7) - 127));
         const float f = __int_as_float((ex + 127) << 23);
-        c = ldexpf(a.scale * (KEY_UNIT * 1.44269504088896340736f), -ex);
+        // never 0, which a masked score of -inf would make NaN
+        c = fmaxf(ldexpf(a.scale * (KEY_UNIT * 1.44269504088896340736f), -ex), 1.17549435e-38f);
         const uint32_t dst = sb + x * C::Q_BYTES + row * 128;
 #pragma unroll 1
         for (int h0 = D / 8 - HOLD; h0 >= 0; h0 -= HOLD) {     // the last pieces read are still there

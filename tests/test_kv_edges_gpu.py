@@ -193,3 +193,14 @@ def test_values_that_are_not_finite_at_no_weight(qmm, D, group, H, dtype):
         got = c.run(qmm)
         assert not np.isfinite(got[hit]).any(), (k, hex(bits))
         assert (np.abs(got - want)[~hit] <= tol[~hit]).all(), (k, hex(bits))
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_scores_that_underflow(qmm, D, H, dtype):
+    """The least queries and scales: all scores are 0 in float32, so the outputs are means of what is seen."""
+    c = Case(D, D, 64, H, dtype)
+    c.q.mul_(2e-38)
+    want, tol = c.want(scale=1e-30)
+    got = c.run(qmm, scale=1e-30)
+    assert (np.abs(got - want) <= tol).all()
