@@ -823,10 +823,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
             uint32_t v[16];
             tmem_ld_32x32b_x16(s_tm + 16 * ch, v);
             tmem_ld_wait();
-            const int t1 = (pages >> ch) & 1u ? t0 + 16 * ch : 0x40000000;
+            const int t1 = t0 + 16 * ch, k1 = (pages >> ch) & 1u ? khi : 0;   // nothing of a tile without a page
 #pragma unroll
             for (int i = 0; i < 16; i++)
-              if (t1 + token_of(i) < klo || t1 + token_of(i) >= khi) v[i] = 0xFF800000u;
+              if (t1 + token_of(i) < klo || t1 + token_of(i) >= k1) v[i] = 0xFF800000u;
             tmem_st_x16(s_tm + 16 * ch, v);
           }
           tmem_st_wait();

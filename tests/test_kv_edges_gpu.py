@@ -204,3 +204,25 @@ def test_scores_that_underflow(qmm, D, H, dtype):
     want, tol = c.want(scale=1e-30)
     got = c.run(qmm, scale=1e-30)
     assert (np.abs(got - want) <= tol).all()
+
+
+def test_missing_pages_past_2_30_tokens(qmm):
+    """Positions beyond 2^30: a page that is not there is left out there, too."""
+    import torch
+    page, length, window, n, D, group, H, Hkv = 256, (1 << 30) + 300, 600, 140, 64, 64, 64, 2
+    rng = np.random.default_rng(3)
+    cache = make_cache(rng, 4, Hkv, D, page, group)
+    blocks = -(-length // page)
+    table = torch.full((1, blocks), -1, dtype=torch.int32, device="cuda")
+    table[0, -2:] = torch.tensor([2, 1], dtype=torch.int32)
+    table[0, -4] = 3                                       # positions 2^30 - 512 .. 2^30 - 257; the page after it is missing
+    for dtype in ("float32", "bfloat16"):
+        q = dev(rng.standard_normal((n, H, D)).astype(np.float32)).to(getattr(torch, dtype))
+        out = qmm.kv_attend(q, dev(cache), table, dev(np.array([length], np.int32)), page, group,
+                            qmm.kv_attend_workspace(1, H, Hkv, D, n), cu=dev(np.array([0, n], np.int32)), max_fresh=n,
+                            window=window)
+        qmm.check()
+        short = np.array([[3, -1, 2, 1]], np.int32)        # the same tokens without what lies before them
+        want, sizes = vec.attend(q.float().cpu().numpy(), *vec.decode(cache, D, page, group), short,
+                                 [length - (blocks - 4) * page], [0, n], page, D ** -0.5, window)
+        assert (np.abs(out.float().cpu().numpy() - want) <= tolerance(sizes, want, 1024, D, dtype)).all(), dtype
