@@ -16,6 +16,7 @@ namespace {
 // ---------------------------------------------------------------- plan
 
 constexpr int kPlanThreads = 512;
+constexpr size_t kPlanStatic = kPlanThreads / 32 * 2 * sizeof(int64_t);   // the scan's shared memory, beside two prefix sums a request
 
 struct PlanParams {
   const int32_t *cached, *fresh, *free_pages;
@@ -541,7 +542,7 @@ cudaError_t launch_kv_plan(const int32_t *cached, const int32_t *fresh, const in
   PlanParams p{cached, fresh, free_pages, table, slots, positions, cu, lens, need, n_free, max_blocks, tokens,
                (int)B, __builtin_ctz((unsigned)page)};
   const size_t smem = 2 * sizeof(int32_t) * (size_t)B;
-  if (smem > 48 * 1024) {
+  if (smem + kPlanStatic > 48 * 1024) {                    // beyond what a launch has without asking
     const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kKvPlanMaxB);
     if (e != cudaSuccess) return e;
   }

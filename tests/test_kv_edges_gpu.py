@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 import kv_vector as vec
-from test_kv_gpu import dev, make_cache, tolerance
+from test_kv_gpu import dev, make_cache, run_plan, tolerance
 from test_kv_items_gpu import check_items, takes_tiles
 
 pytestmark = pytest.mark.gpu
@@ -226,3 +226,11 @@ def test_missing_pages_past_2_30_tokens(qmm):
         want, sizes = vec.attend(q.float().cpu().numpy(), *vec.decode(cache, D, page, group), short,
                                  [length - (blocks - 4) * page], [0, n], page, D ** -0.5, window)
         assert (np.abs(out.float().cpu().numpy() - want) <= tolerance(sizes, want, 1024, D, dtype)).all(), dtype
+
+
+@pytest.mark.parametrize("B", [6112, 6113, 6144, 6145, 8192])
+def test_plan_of_wide_batches(qmm, B):
+    rng = np.random.default_rng(B)
+    cached, fresh = rng.integers(0, 60, B), rng.integers(0, 3, B)
+    table = rng.integers(0, 5000, (B, 5)).astype(np.int32)
+    run_plan(qmm, cached, fresh, rng.permutation(9000), table, int(fresh.sum()) + 3, 16)
