@@ -1,6 +1,7 @@
 // kv_attend.h -- arguments of the attention over the 4-bit cache, between the
 // C ABI (api.cu, which has validated them) and the kernels.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -24,20 +25,28 @@ struct KvAttendArgs {
   int64_t window;                       // 0: none
 };
 
+// SMs of the current device, asked once a device.  Without one (sizes can be asked for anywhere): a GB300's, not kept.
+constexpr int kKvMaxDevices = 64;
+inline int kv_sms() {
+  static std::atomic<int> known[kKvMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    const bool keep = dev >= 0 && dev < kKvMaxDevices;
+    if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0) {
+      if (keep) known[dev].store(n, std::memory_order_relaxed);
+      return n;
+    }
+  }
+  (void)cudaGetLastError();
+  return 152;
+}
+
 // CTAs of a launch with `per_sm` CTAs an SM: at most 1024 (their counters are the workspace's first 4096 bytes).
 constexpr int kKvMaxCtas = 1024;
 inline int kv_max_ctas(int per_sm) {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        v <= 0) {
-      (void)cudaGetLastError();          // no device here: the size that a GB300 needs
-      v = 152;
-    }
-    n = v;
-  }
-  return n * per_sm > kKvMaxCtas ? kKvMaxCtas : n * per_sm;
+  const int n = kv_sms() * per_sm;
+  return n > kKvMaxCtas ? kKvMaxCtas : n;
 }
 
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
