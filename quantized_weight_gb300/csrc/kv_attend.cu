@@ -4,8 +4,9 @@
 namespace qmm {
 
 size_t kv_attend_workspace(int64_t, int64_t, int64_t, int64_t head_dim, int64_t) {
-  // counters, then two partial results a team: 8 rows for each of 3 teams an SM, or 16 of 2, with maxima and sums
-  return 4 * 1024 + (size_t)kv_max_ctas(2) * 2 * 16 * (size_t)(head_dim + 2) * sizeof(float);
+  // Counters, then two partial results for each of two teams an SM: 16 rows (heads of 256: 8) with maxima and sums.  One size
+  // for all calls of a head dimension, since a few MB matter less than a buffer that the next call finds too small.
+  return 4 * kKvMaxCtas + (size_t)kv_max_ctas(2) * 2 * (head_dim == 256 ? 8 : 16) * (size_t)(head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s) {
