@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <type_traits>
 
+#include "kv_attend.h"
 #include "kv_launch.h"
 #include "kv_layout.cuh"
 #include "qmm_device.cuh"
@@ -165,9 +166,9 @@ inline int64_t row_grid(Rows &p) {
   // one token and row a warp while that gives no more than 16 warps an SM; beyond, the work of a token counts, not its
   // latency, and a warp takes as much as leaves 64 an SM
   const int64_t rows = 2 * p.g.kv_heads;
-  p.per_warp = p.tokens * rows <= 152 * 16 ? 1 : 4;
+  p.per_warp = p.tokens * rows <= kv_sms() * 16 ? 1 : 4;
   const int64_t units = (p.tokens + p.per_warp - 1) / p.per_warp;
-  int64_t part = units * rows / (152 * 64);
+  int64_t part = units * rows / (kv_sms() * 64);
   part = part < 1 ? 1 : part > rows ? rows : part;
   p.parts = (int)((rows + part - 1) / part);
   p.part = (int)((rows + p.parts - 1) / p.parts);
@@ -548,7 +549,7 @@ cudaError_t launch_kv_plan(const int32_t *cached, const int32_t *fresh, const in
   }
   int64_t work = tokens > B * 32 ? tokens : B * 32;
   int64_t grid = (work + 2 * kPlanThreads - 1) / (2 * kPlanThreads);
-  grid = grid < 1 ? 1 : grid > 152 ? 152 : grid;
+  grid = grid < 1 ? 1 : grid > kv_sms() ? kv_sms() : grid;
   return launch_after(plan_kernel, grid, kPlanThreads, smem, s, p);
 }
 
