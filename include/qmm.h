@@ -254,7 +254,9 @@ int qmm_gather_dequant(const int32_t *ids, int64_t T, const uint32_t *packed, co
  *
  * Common rules.  head_dim in {64, 128, 256}; group in {32, 64, 128} and a
  * divisor of head_dim; page in {16, 32, 64, 128, 256} (QMM_ERR_UNSUPPORTED
- * otherwise); pages * page < 2^31 (QMM_ERR_SHAPE).  int32 arrays need 4-byte alignment, everything
+ * otherwise); pages * page < 2^31, kv_heads <= 4096, in qmm_kv_attend heads <= 1024; append, read and
+ * attend take fewer than 2^19 = 524288 tokens a call (QMM_ERR_SHAPE; a longer plan's slots go to
+ * them in pieces).  int32 arrays need 4-byte alignment, everything
  * else 16 bytes: the base of a tensor and each of its strides, in bytes, are
  * multiples of 16 (QMM_ERR_ALIGN).  dtype is QMM_F32 or QMM_BF16.  Lengths,
  * slots, tables and offsets live in device memory, so one captured graph
@@ -323,7 +325,8 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
  *     out = sum_j softmax_j(scale * q . k_j) v_j
  *   A query that sees no key gets zeros.  A page id outside [0, pages), and what
  *   lies past max_blocks, is not read: its tokens are left out.  Tokens of no request are not written.
- *   max_fresh >= every request's queries (it picks the kernel).  scale > 0, finite.
+ *   max_fresh >= every request's queries (it picks the kernel), and < 2^19.  max_blocks * page <= 2^31 - 256.
+ *   scale > 0, finite.
  *   Scores, maxima, sums and the accumulation are float32; for QMM_F32 the
  *   queries and probabilities enter the tensor cores as two binary16 terms.
  *   For QMM_BF16 they enter as one (bfloat16 queries are exact in it, probabilities

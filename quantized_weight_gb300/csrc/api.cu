@@ -19,6 +19,7 @@ bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 bool bits_ok(int bits) { return bits == 1 || bits == 4 || bits == 8; }
 bool group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;   // N, K, M each fit in int for the kernels
+constexpr int64_t kKvMaxTokens = (int64_t)1 << 19, kKvMaxHeads = 1024;   // of a cache call: their product, too
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? QMM_OK : QMM_ERR_CUDA; }
 
@@ -212,7 +213,7 @@ int qmm_kv_append(const void *k, const void *v, int dtype, int64_t k_token_strid
   if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
   int st = check_kv(pages, kv_heads, head_dim, page, group);
   if (st != QMM_OK) return st;
-  if (tokens < 0 || tokens >= kMaxDim / 4096) return QMM_ERR_SHAPE;
+  if (tokens < 0 || tokens >= kKvMaxTokens) return QMM_ERR_SHAPE;
   if (tokens == 0 || pages == 0) return QMM_OK;
   if (!k || !v || !slots || !cache) return QMM_ERR_ARG;
   const int size = dtype == QMM_BF16 ? 2 : 4;
@@ -229,7 +230,7 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
   if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
   int st = check_kv(pages, kv_heads, head_dim, page, group);
   if (st != QMM_OK) return st;
-  if (tokens < 0 || tokens >= kMaxDim / 4096) return QMM_ERR_SHAPE;
+  if (tokens < 0 || tokens >= kKvMaxTokens) return QMM_ERR_SHAPE;
   if (tokens == 0) return QMM_OK;
   if (!slots || (pages > 0 && !cache) || !k || !v) return QMM_ERR_ARG;
   if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned4(slots)) return QMM_ERR_ALIGN;
@@ -238,7 +239,8 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
 }
 
 size_t qmm_kv_attend_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh) {
-  if (check_kv(0, kv_heads, head_dim, 16, 32) != QMM_OK || B < 0 || max_fresh < 0 || heads < 1 || heads % kv_heads != 0)
+  if (check_kv(0, kv_heads, head_dim, 16, 32) != QMM_OK || B < 0 || B >= kMaxDim || max_fresh < 0 ||
+      max_fresh >= kKvMaxTokens || heads < 1 || heads > kKvMaxHeads || heads % kv_heads != 0)
     return 0;
   return qmm::kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh);
 }
@@ -251,8 +253,10 @@ int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_he
   if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
   int st = check_kv(pages, kv_heads, head_dim, page, group);
   if (st != QMM_OK) return st;
-  if (tokens < 0 || tokens >= kMaxDim / 4096 || B < 0 || B >= kMaxDim || max_blocks < 0 || max_blocks * page >= kMaxDim ||
-      max_fresh < 1 || max_fresh >= kMaxDim / 4096 || heads < 1 || heads > 1024 || heads % kv_heads != 0 || window < 0)
+  // (positions are rounded up to a block of keys in 32 bits)
+  if (tokens < 0 || tokens >= kKvMaxTokens || B < 0 || B >= kMaxDim || max_blocks < 0 || max_blocks >= kMaxDim ||
+      max_blocks * page > kMaxDim - 256 || max_fresh < 1 || max_fresh >= kKvMaxTokens || heads < 1 || heads > kKvMaxHeads ||
+      heads % kv_heads != 0 || window < 0)
     return QMM_ERR_SHAPE;
   if (!cu && (tokens != B || max_fresh != 1)) return QMM_ERR_SHAPE;
   if (!(scale > 0.0f) || scale > 3.0e38f) return QMM_ERR_ARG;
