@@ -267,7 +267,8 @@ int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_he
     return QMM_ERR_ALIGN;
   if (workspace_bytes < qmm_kv_attend_workspace_size(B, heads, kv_heads, head_dim, max_fresh)) return QMM_ERR_SHAPE;
   qmm::KvAttendArgs a{};
-  a.q = q, a.out = out, a.cache = cache, a.table = block_table, a.lens = lens, a.cu = cu, a.workspace = workspace;
+  // (of an empty cache nothing is read, but copies of no bytes still name an address)
+  a.q = q, a.out = out, a.cache = pages > 0 ? cache : workspace, a.table = block_table, a.lens = lens, a.cu = cu, a.workspace = workspace;
   a.q_token = q_token_stride, a.q_head = q_head_stride;
   a.tokens = tokens, a.B = B, a.max_blocks = max_blocks, a.max_fresh = max_fresh;
   a.pages = pages, a.kv_heads = kv_heads, a.head_dim = head_dim, a.heads = heads;

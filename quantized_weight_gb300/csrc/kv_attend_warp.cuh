@@ -1038,6 +1038,7 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   Params p{};
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
+  if (a.pages == 0) p.g.head_bytes = 0;                // addresses stay in the workspace, which stands for an empty cache
   p.ratio = (int)(a.heads / a.kv_heads);
   // Items that far outnumber the SMs go to small teams, whose joins overlap; fewer
   // items to whole CTAs, which leave fewer parts to add up.  Small teams against whole CTAs: 512 items of 64 to 8192 tokens 41.0

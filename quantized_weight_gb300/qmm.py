@@ -340,10 +340,11 @@ def _kv_out(t, name, dtype, shape) -> int:
 
 def kv_cache(pages, kv_heads, head_dim, page, group=64, device="cuda") -> torch.Tensor:
     """The 4-bit key/value cache of one layer: uint8 [pages, kv_heads, bytes of a head's page]."""
-    n = int(lib().qmm_kv_cache_size(pages, kv_heads, head_dim, page, group))
-    if n == 0 and pages != 0:
+    size = lib().qmm_kv_cache_size
+    n = int(size(1, kv_heads, head_dim, page, group))
+    if n == 0 or (pages != 0 and size(pages, kv_heads, head_dim, page, group) == 0):
         raise ValueError(f"no cache of head_dim {head_dim}, page {page}, group {group} with {pages} pages of {kv_heads} heads")
-    return torch.zeros((pages, kv_heads, n // (pages * kv_heads) if pages else 0), dtype=torch.uint8, device=device)
+    return torch.zeros((pages, kv_heads, n // kv_heads), dtype=torch.uint8, device=device)
 
 
 def kv_plan(cached, fresh, free_pages, block_table, tokens, page, out=None, stream=None):

@@ -234,3 +234,23 @@ def test_plan_of_wide_batches(qmm, B):
     cached, fresh = rng.integers(0, 60, B), rng.integers(0, 3, B)
     table = rng.integers(0, 5000, (B, 5)).astype(np.int32)
     run_plan(qmm, cached, fresh, rng.permutation(9000), table, int(fresh.sum()) + 3, 16)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_empty_cache(qmm, D):
+    """A cache without pages takes every call: nothing is kept, nothing is seen."""
+    import torch
+    H, Hkv, n, page = 64, 2, 140, 16
+    cache = qmm.kv_cache(0, Hkv, D, page)
+    k, slots = torch.randn(n, Hkv, D, device="cuda"), torch.arange(n, dtype=torch.int32, device="cuda")
+    qmm.kv_append(k, k, slots, cache, page)
+    for x in qmm.kv_read(slots, cache, D, page):
+        assert bool(x.isnan().all())
+    lens, cu = dev(np.array([n], np.int32)), dev(np.array([0, n], np.int32))
+    for dtype in (torch.float32, torch.bfloat16):
+        q = torch.randn(n, H, D, device="cuda").to(dtype)
+        for table in (torch.zeros(1, 9, dtype=torch.int32, device="cuda"), torch.zeros(1, 0, dtype=torch.int32, device="cuda")):
+            out = qmm.kv_attend(q, cache, table, lens, page, 64, qmm.kv_attend_workspace(1, H, Hkv, D, n), cu=cu, max_fresh=n,
+                                out=torch.full_like(q, 7.0))
+            assert not bool(out.any())
+    qmm.check()

@@ -44,3 +44,10 @@ def test_workspace_has_a_size_where_attend_has_a_call(L):
     assert size((1 << 31) - 1, 4, 2, 128, 1) > 0 and size(1 << 31, 4, 2, 128, 1) == 0
     with pytest.raises(ValueError):
         qmm.kv_attend_workspace(1, 2048, 1, 128, device="cpu")
+
+
+def test_empty_cache_has_a_page_size(L):
+    assert qmm.kv_cache(0, 2, 128, 64, device="cpu").shape == (0, 2, qmm.kv_cache(3, 2, 128, 64, device="cpu").shape[2])
+    for bad in ((0, 2, 100, 64), (0, 0, 128, 64), (-1, 2, 128, 64), (0, 2, 128, 24)):
+        with pytest.raises(ValueError):
+            qmm.kv_cache(*bad, device="cpu")
