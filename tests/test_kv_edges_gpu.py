@@ -254,3 +254,36 @@ def test_empty_cache(qmm, D):
                                 out=torch.full_like(q, 7.0))
             assert not bool(out.any())
     qmm.check()
+
+
+def heads_first(x):
+    """The same [tokens, heads, head_dim] tensor, laid out as [heads, tokens, head_dim]."""
+    return x.transpose(0, 1).contiguous().transpose(0, 1)
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attend_heads_first(qmm, D, H, dtype):
+    c = Case(D + 1, D, 64, H, dtype)
+    plain = c.run(qmm)
+    c.q = heads_first(c.q)
+    assert c.q.stride(0) == D and np.array_equal(c.run(qmm), plain)
+    want, tol = c.want()
+    assert (np.abs(plain - want) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T", [1, 50, 700])
+def test_append_heads_first(qmm, T, dtype):
+    import torch
+    torch.manual_seed(T)
+    k, v = torch.randn(2, T, 24, 128, device="cuda").to(getattr(torch, dtype)).unbind(0)
+    slots = torch.randperm(T + 9, device="cuda")[:T].int()
+    caches = [qmm.kv_cache(T // 32 + 2, 24, 128, 32) for _ in range(2)]
+    qmm.kv_append(k, v, slots, caches[0], 32)
+    qmm.kv_append(heads_first(k), heads_first(v), slots, caches[1], 32)
+    assert torch.equal(*caches) and bool(caches[0].any())
+    shared = v[:, :1].expand(-1, 24, -1)                   # one value head for all key heads: a head stride of 0
+    qmm.kv_append(k, shared, slots, caches[0], 32)
+    qmm.kv_append(k, shared.contiguous(), slots, caches[1], 32)
+    assert torch.equal(*caches)
