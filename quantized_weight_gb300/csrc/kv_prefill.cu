@@ -507,10 +507,6 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       kb += it.blocks;
       release();
     }
-    if (*abort_flag && elect_one()) {         // wait (bounded) for the MMAs in flight before TMEM goes
-      umma_commit(bar(DRAIN));
-      wait_drain(bar(DRAIN), 0);
-    }
   } else if (warp >= (NQ == 2 ? DQ_WARP0 : SOFT_WARP0 + 4)) {
     // ------------------------------------------------------------ codes: keys
     // One warpgroup has both, or, where there is no second row tile, its softmax warps take the keys.
@@ -941,6 +937,13 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
+    // No wait is left that could give up, so the flag is final: if one did, MMAs may be in flight, which are waited for (bounded)
+    // before TMEM goes.
+    if (*abort_flag && elect_one()) {
+      umma_commit(bar(DRAIN));
+      wait_drain(bar(DRAIN), 0);
+    }
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
