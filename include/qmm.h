@@ -372,6 +372,15 @@ int qmm_check(qmm_stream_t stream);
  */
 int qmm_test_timeout_next_decode(int64_t limit_ns);
 
+/*
+ * qmm_test_timeout_next_attend -- the same for the attention: in the next
+ *   qmm_kv_attend launch whose rows go to tiles of 128 (see there), every block's first
+ *   wait for scores is one that nothing ends, with this limit.  The launch writes no row
+ *   that sees a key, waits for its matrix products in flight, frees its tensor memory and leaves the
+ *   workspace ready; the next qmm_check() returns QMM_ERR_DEVICE_TIMEOUT once.
+ */
+int qmm_test_timeout_next_attend(int64_t limit_ns);
+
 /* A static, human-readable name for a qmm_status value. */
 const char *qmm_status_string(int status);
 

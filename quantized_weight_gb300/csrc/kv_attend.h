@@ -55,6 +55,7 @@ cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
 // Many queries a request, bfloat16 (kv_prefill.cu); its waits are bounded and report here.
 cudaError_t launch_kv_prefill(const KvAttendArgs &a, cudaStream_t s);
 cudaError_t read_clear_kv_status(int *status, cudaStream_t s);
+void set_kv_test_wait(unsigned long long limit_ns);
 
 // Per head dimension (one translation unit each); nt: tiles of 8 rows of q an item
 // (heads of 256: one, since registers and shared memory hold no more).

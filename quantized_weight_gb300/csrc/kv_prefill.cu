@@ -82,7 +82,9 @@ struct Params {
   KvAttendArgs a;
   KvGeom g;
   int ratio;
+  unsigned long long test_wait_ns;  // test hook: a wait of every CTA runs out after so long
 };
+std::atomic<unsigned long long> g_test_wait_ns{0};
 
 struct Item {
   int b, kvh, r0, rows;             // rows r0 .. r0 + rows - 1 of the request
@@ -114,7 +116,7 @@ struct Cfg {
 // complete (two blocks ahead, and an item of one block is two phases).
 enum { S_FULL = 0, P_FULL = 2, PV_DONE = 4, Q_FULL = 6, FULL = 8, K_EMPTY = 16, V_EMPTY = 18, IT_FULL = 20,
        IT_EMPTY = IT_FULL + ITEM_SLOTS, DRAIN = IT_EMPTY + ITEM_SLOTS, IT_NEXT, RAW_FULL, RAW_EMPTY = RAW_FULL + 2,
-       S_LAST = RAW_EMPTY + 2, BARS = S_LAST + ITEM_SLOTS };
+       S_LAST = RAW_EMPTY + 2, DQ_SYNC = S_LAST + ITEM_SLOTS, NEVER, BARS };
 
 __device__ __forceinline__ void umma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -215,6 +217,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const W
   return wait_on(bar, parity, ctl.abort);
 }
 
+// The test hook's wait (out of line: it runs only when the hook is set).
+__device__ __noinline__ void test_wait(uint32_t never_bar, WaitCtl ctl, unsigned long long limit_ns) {
+  wait_bounded(never_bar, 0, ctl, limit_ns);
+}
+
 // One warp, the seldom path of the softmax: this lane's row of O (unless o_tm is all ones) and of the first `cols`
 // columns of P (two binary16 values each) times f.  Not inlined, so that it takes no registers from the path that is run.
 template <int D>
@@ -285,6 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
     }
     for (int i = 0; i < 8; i++) mbar_init(bar(FULL + i), NQ == 2 ? 128 : 256);
     mbar_init(bar(DRAIN), 1);
+    mbar_init(bar(DQ_SYNC), 4);
+    mbar_init(bar(NEVER), 1);                            // nothing arrives here (the test hook's wait)
     mbar_init(bar(IT_NEXT), NQ == 2 ? 4 : 8);            // a warp that converts an arrival
     *abort_flag = 0;
     fence_mbar_init();
@@ -523,7 +532,14 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       constexpr int UNITS = KB / 16 * CB * 8;                  // (tile, block, element % 8): the threads with work
       const int u = threadIdx.x & 127, g8 = u & 7, vc = (u >> 3) % CB, vt = (u >> 3) / CB;
       const bool act = u < UNITS;
-      Phase ke[2], ve[2], kr, vr;
+      Phase ke[2], ve[2], kr, vr, together;
+      // The four warps with the values, at one place.  Not a named barrier, whose wait has no end: one of them may have given
+      // up a wait that the others passed.
+      auto sync_values = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(DQ_SYNC));
+        return warp_wait(bar(DQ_SYNC), together.next(), ctl);
+      };
       ke[0].v = ke[1].v = ve[0].v = ve[1].v = 1;
       int kb = 0, full = 0, n_item = 0;                        // blocks, phases of FULL and items before
       bool ok = true;
@@ -534,7 +550,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         if constexpr (VALUES) {
           for (int i = u; i < C::NOTES; i += 128) my_notes[i] = 0u;
           if (u == 0) noted[n_item & 3] = 0, over[n_item & 3] = 0;
-          asm volatile("bar.sync 1, 128;" ::: "memory");
+          if (!sync_values()) break;
         }
         const bool sixteenth = it.vexp != 0;
         uint32_t w[PW][WC], cf[PW][GK];
@@ -635,7 +651,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
                 uint32_t *c = reinterpret_cast<uint32_t *>(smem + C::OFF_RAW + C::RAW + i / (16 * G) * C::HALF + 8 * D) + i % (16 * G);
                 *c = hmul2(*c, 0x2C002C00u /* 1/16 */);
               }
-              asm volatile("bar.sync 1, 128;" ::: "memory");
+              if (!sync_values()) { ok = false; break; }
             }
             take_values();
             // Tokens that no row sees become zeros, whatever the cache holds there.  Where only some rows see the block, a
@@ -801,6 +817,10 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
         fence_proxy_async_smem();
         mbar_arrive(bar(Q_FULL + x));
       }
+      if (p.test_wait_ns != 0 && warp == SOFT_WARP0 && it.blocks > 0) {    // score products are in flight
+        test_wait(bar(NEVER), ctl, p.test_wait_ns);
+        break;
+      }
       const int64_t pos = (int64_t)it.base + qi;
       const int khi = real ? (int)max((int64_t)0, min(pos + 1, (int64_t)it.hi)) : 0;
       const int klo = a.window > 0 ? (int)max((int64_t)0, min(pos + 1 - a.window, (int64_t)it.hi)) : 0;
@@ -956,6 +976,7 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   p.a = a;
   p.g = kv_geom(a.pages, a.kv_heads, a.head_dim, a.page, a.group);
   p.ratio = (int)(a.heads / a.kv_heads);
+  p.test_wait_ns = g_test_wait_ns.exchange(0, std::memory_order_relaxed);
   // never more CTAs than items
   const int64_t items = (a.tokens * p.ratio / (C::NQ * QROWS) + (a.tokens < a.B ? a.tokens : a.B)) * a.kv_heads;
   static std::atomic<int> set_for{0};
@@ -971,6 +992,8 @@ cudaError_t launch_kv_prefill(const KvAttendArgs &a, cudaStream_t s) {
   if (D == 256) return G == 2 ? launch<256, 2>(a, s) : G == 4 ? launch<256, 4>(a, s) : launch<256, 8>(a, s);
   return cudaErrorNotSupported;
 }
+
+void set_kv_test_wait(unsigned long long limit_ns) { g_test_wait_ns.store(limit_ns, std::memory_order_relaxed); }
 
 cudaError_t read_clear_kv_status(int *status, cudaStream_t s) {
   int v = 0;

@@ -80,13 +80,13 @@ def lib():
                                         i32, i32, f32, i64, vp, sz, vp]
             L.qmm_kv_cache_size.restype = L.qmm_kv_attend_workspace_size.restype = sz
             L.qmm_check.argtypes = [vp]
-            L.qmm_test_timeout_next_decode.argtypes = [i64]
+            L.qmm_test_timeout_next_decode.argtypes = L.qmm_test_timeout_next_attend.argtypes = [i64]
             L.qmm_status_string.argtypes = [i32]
             L.qmm_status_string.restype = ctypes.c_char_p
             L.qmm_abi_version.argtypes = []
             for f in ("qmm_pack", "qmm_unpack", "qmm_dequant", "qmm_gemv", "qmm_gemm", "qmm_quantize",
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
-                      "qmm_test_timeout_next_decode", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
+                      "qmm_test_timeout_next_decode", "qmm_test_timeout_next_attend", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
                       "qmm_kv_attend"):
                 getattr(L, f).restype = i32
             _lib = L
@@ -438,6 +438,12 @@ def test_timeout_next_decode(limit_ns: int) -> None:
     out after limit_ns; it writes no output and the next check() raises
     QMM_ERR_DEVICE_TIMEOUT."""
     _call("qmm_test_timeout_next_decode", lib().qmm_test_timeout_next_decode(int(limit_ns)))
+
+
+def test_timeout_next_attend(limit_ns: int) -> None:
+    """Test hook: the next kv_attend launch on tiles of 128 rows makes one wait a block that runs out after limit_ns; it
+    writes no row that sees a key and the next check() raises QMM_ERR_DEVICE_TIMEOUT."""
+    _call("qmm_test_timeout_next_attend", lib().qmm_test_timeout_next_attend(int(limit_ns)))
 
 
 def check(stream=None) -> None:

@@ -51,3 +51,8 @@ def test_empty_cache_has_a_page_size(L):
     for bad in ((0, 2, 100, 64), (0, 0, 128, 64), (-1, 2, 128, 64), (0, 2, 128, 24)):
         with pytest.raises(ValueError):
             qmm.kv_cache(*bad, device="cpu")
+
+
+def test_timeout_hook_limits(L):
+    for ns in (999, 100_000_001, -5):
+        assert L.qmm_test_timeout_next_attend(ns) == ARG
