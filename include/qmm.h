@@ -342,6 +342,9 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
  *   flight at the same time must not share one.
  */
 size_t qmm_kv_attend_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
+/* 1 if a call of these sizes goes to tiles of 128 rows on the current device (what it rounds is said above), 0 if not, or an
+ * error's status. */
+int qmm_kv_attend_tiles(int dtype, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
 int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_head_stride, const void *cache,
                   const int32_t *block_table, const int32_t *lens, const int32_t *cu, void *out, int64_t tokens,
                   int64_t B, int64_t max_blocks, int64_t max_fresh, int64_t pages, int64_t heads, int64_t kv_heads,

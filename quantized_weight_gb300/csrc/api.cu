@@ -245,6 +245,16 @@ size_t qmm_kv_attend_workspace_size(int64_t B, int64_t heads, int64_t kv_heads, 
   return qmm::kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh);
 }
 
+int qmm_kv_attend_tiles(int dtype, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh) {
+  if (dtype != QMM_F32 && dtype != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+  const int st = check_kv(0, kv_heads, head_dim, 16, 32);
+  if (st != QMM_OK) return st;
+  if (B < 0 || B >= kMaxDim || max_fresh < 1 || max_fresh >= kKvMaxTokens || heads < 1 || heads > kKvMaxHeads ||
+      heads % kv_heads != 0)
+    return QMM_ERR_SHAPE;
+  return qmm::kv_attend_tiles(dtype == QMM_BF16, B, heads, kv_heads, head_dim, max_fresh) ? 1 : 0;
+}
+
 int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_head_stride, const void *cache,
                   const int32_t *block_table, const int32_t *lens, const int32_t *cu, void *out, int64_t tokens,
                   int64_t B, int64_t max_blocks, int64_t max_fresh, int64_t pages, int64_t heads, int64_t kv_heads,

@@ -50,6 +50,8 @@ inline int kv_max_ctas(int per_sm) {
 }
 
 size_t kv_attend_workspace(int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
+// Whether a call takes the prompt kernel, tiles of 128 rows of q.
+bool kv_attend_tiles(bool bf16, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, cudaStream_t s);
 
 // Many queries a request, bfloat16 (kv_prefill.cu); its waits are bounded and report here.

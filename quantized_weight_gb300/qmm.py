@@ -78,6 +78,7 @@ def lib():
             L.qmm_kv_attend_workspace_size.argtypes = [i64, i64, i64, i64, i64]
             L.qmm_kv_attend.argtypes = [vp, i32, i64, i64, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, i64, i64,
                                         i32, i32, f32, i64, vp, sz, vp]
+            L.qmm_kv_attend_tiles.argtypes = [i32, i64, i64, i64, i64, i64]
             L.qmm_kv_cache_size.restype = L.qmm_kv_attend_workspace_size.restype = sz
             L.qmm_check.argtypes = [vp]
             L.qmm_test_timeout_next_decode.argtypes = L.qmm_test_timeout_next_attend.argtypes = [i64]
@@ -87,7 +88,7 @@ def lib():
             for f in ("qmm_pack", "qmm_unpack", "qmm_dequant", "qmm_gemv", "qmm_gemm", "qmm_quantize",
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
                       "qmm_test_timeout_next_decode", "qmm_test_timeout_next_attend", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
-                      "qmm_kv_attend"):
+                      "qmm_kv_attend", "qmm_kv_attend_tiles"):
                 getattr(L, f).restype = i32
             _lib = L
     return _lib
@@ -403,6 +404,13 @@ def kv_attend_workspace(B, heads, kv_heads, head_dim, max_fresh=1, device="cuda"
     if n == 0:
         raise ValueError(f"no attention of {heads} heads over {kv_heads} kv heads of {head_dim}")
     return torch.zeros(((n + 15) // 16 * 16,), dtype=torch.uint8, device=device)
+
+
+def kv_attend_tiles(dtype, B, heads, kv_heads, head_dim, max_fresh) -> bool:
+    """Whether kv_attend takes such a call on tiles of 128 rows of q (include/qmm.h says what is rounded there)."""
+    r = lib().qmm_kv_attend_tiles(_kv_dtype(dtype), B, heads, kv_heads, head_dim, max_fresh)
+    _call("qmm_kv_attend_tiles", min(r, 0))
+    return r == 1
 
 
 def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_fresh=1, scale=None, window=0, out=None,
