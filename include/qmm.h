@@ -317,7 +317,7 @@ int qmm_kv_read(const int32_t *slots, const void *cache, void *k, void *v, int d
 /*
  * qmm_kv_attend -- softmax attention of a step's queries over the cache.
  *   q [tokens, heads, head_dim] (strides as above), out the same, contiguous,
- *   q's type.  heads is a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads).
+ *   q's type; it may be q itself.  heads is a multiple of kv_heads; query head h reads kv head h / (heads / kv_heads).
  *   Request b's queries are tokens [cu[b], cu[b + 1]) (cu == NULL: one query a
  *   request, token b; then tokens == B).  lens[b] counts its tokens in the cache, those of the
  *   queries among them: query i of n stands at position p = lens[b] - n + i

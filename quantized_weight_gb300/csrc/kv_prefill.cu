@@ -375,8 +375,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
       // could begin.
       if (!warp_wait(bar(IT_NEXT), next, ctl)) break;
       next ^= 1u;
-      // The item before had values beyond binary16's range: once more, with a 16th of them.  The same threads write the same
-      // rows, after those of the first time.
+      // The item before had values beyond binary16's range, and wrote nothing: once more, with a 16th of them.
       again = !again && n_item > 0 && over[(n_item - 1) & 3] != 0;
       unsigned t = 0;
       if (lane == 0 && !again) t = atomicAdd(ticket, 1u);
@@ -922,6 +921,8 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
           }
         }
       }
+      // an item that is done again leaves its rows to the second time (q may be where they go)
+      const bool again = it.vexp == 0 && over[n_item & 3] != 0;
       const float inv = l == 0.0f ? 0.0f : (it.vexp == 0 ? 1.0f : 16.0f) / l;
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)(it.cu0 + qi) * a.heads + it.kvh * p.ratio + hq) * D;
 #pragma unroll 1
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(THREADS, 1) prefill_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 16; i++) v[i] = 0u;
         }
-        if (real) {
+        if (real && !again) {
           const bool bad = (nan_groups >> (16 * ch / (D / G))) & 1u;
           uint32_t o[8];
 #pragma unroll

@@ -46,10 +46,11 @@ class Case:
                                  window)
         return want, np.broadcast_to(tolerance(sizes, want, self.length, self.D, self.dtype), want.shape)
 
-    def run(self, qmm, scale=None, window=0):
+    def run(self, qmm, scale=None, window=0, out=None):
         ws = qmm.kv_attend_workspace(1, self.H, self.Hkv, self.D, self.n)
         out = qmm.kv_attend(self.q, dev(self.cache), dev(self.table), dev(np.array([self.length], np.int32)), self.page,
-                            self.group, ws, cu=dev(np.array([0, self.n], np.int32)), max_fresh=self.n, scale=scale, window=window)
+                            self.group, ws, cu=dev(np.array([0, self.n], np.int32)), max_fresh=self.n, scale=scale, window=window,
+                            out=out)
         qmm.check()
         assert not ws[:4096].any()
         return out.float().cpu().numpy().astype(np.float64)
@@ -287,3 +288,32 @@ def test_append_heads_first(qmm, T, dtype):
     qmm.kv_append(k, shared, slots, caches[0], 32)
     qmm.kv_append(k, shared.contiguous(), slots, caches[1], 32)
     assert torch.equal(*caches)
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_output_over_the_queries(qmm, D, H, dtype):
+    """out may be q, where an item is done twice for its large values, too."""
+    c = Case(D + 2, D, 64, H, dtype)
+    for large in (False, True):
+        if large:
+            c.coef(100, 1, 1, 0)[:] = np.array([65504, -30000], np.float16).view(np.uint16)
+        want = c.run(qmm)
+        held = c.q.clone()
+        assert np.array_equal(c.run(qmm, out=c.q), want)
+        c.q = held
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_queries_that_are_not_finite(qmm, D, H, dtype):
+    """They reach their own output and no other."""
+    c = Case(D + 3, D, 64, H, dtype)
+    want, tol = c.want()
+    hit = np.zeros(want.shape[:2], bool)
+    for token, head, value in ((0, 0, np.nan), (70, H - 1, np.inf), (139, H // 2, -np.inf)):
+        c.q[token, head, 3] = value
+        hit[token, head] = True
+    got = c.run(qmm)
+    assert not np.isfinite(got[hit]).any()
+    assert (np.abs(got - want)[~hit] <= tol[~hit]).all()
