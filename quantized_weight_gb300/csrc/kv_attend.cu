@@ -12,10 +12,10 @@ size_t kv_attend_workspace(int64_t, int64_t, int64_t, int64_t head_dim, int64_t)
 // The prompt kernel takes 2.6 us for a block of 128 keys and two tiles of 128 rows, 2.0 us with one tile (heads of 256:
 // 1.3 us, 64 keys, one tile), with an item on one SM; the warp kernel spreads any work over all SMs, at 0.39 ns a row and
 // 128 keys (0.43 ns, 64 keys).  So the prompt kernel pays from so many rows on for each round of its items over
-// the SMs.  Measured, prompt / warp kernel in us, 8 kv heads of 128: 2048 rows, 8000 keys 145 / 60; 8192 rows, 4000
-// keys 82 / 113; 16384 rows, 4000 keys 82 / 202; 128 items of 32 rows, 4000 keys 64 / 66; 512 items of 20 rows, 2000 keys
-// 137 / 117, of 64 rows 140 / 225.  Heads of 64: 32 items of 256 rows, 4000 keys 70 / 76.  Heads of 256: 64 items of 128
-// rows, 4000 keys 82 / 221; 512 items of 20 rows, 2000 keys 197 / 183.
+// the SMs.  Measured, prompt / warp kernel in us, 8 kv heads of 128: 2048 rows, 8000 keys 146 / 60; 8192 rows, 4000
+// keys 82 / 112; 16384 rows, 4000 keys 82 / 201; 128 items of 32 rows, 4000 keys 63 / 65; 512 items of 20 rows, 2000 keys
+// 134 / 117, of 64 rows 137 / 225.  Heads of 64: 32 items of 256 rows, 4000 keys 71 / 78.  Heads of 256: 64 items of 128
+// rows, 4000 keys 85 / 223; 512 items of 20 rows, 2000 keys 198 / 185.
 // (Requests of equal length and equal queries; the rule sees no more of a ragged or mixed step than max_fresh.)
 bool kv_attend_tiles(bool bf16, int64_t B, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t max_fresh) {
   const int64_t rows = max_fresh * (heads / kv_heads);         // of q, a request and kv head

@@ -35,7 +35,7 @@
 // last (a counter) adds them up in the line's order, so the result does not depend on which it is.
 //
 // Measured (GB300; the bytes are each visible token's codes and coefficients once, at 6.78 TB/s):
-//   4 requests of 60000 to 130000 tokens, 40 query and 8 kv heads of 128, float32: 117 us, 66 us of bytes (3.8 TB/s).
+//   4 requests of 60000 to 130000 tokens, 40 query and 8 kv heads of 128, float32: 116 us, 66 us of bytes (3.8 TB/s).
 //     Bound: two warps a scheduler (255 registers) issue in 49 % of the cycles, between fixed latencies; the tensor pipe is 38 %
 //     busy (two MMAs a product for float32).
 //   64 requests of 64 to 8192 tokens, 32 and 8 heads of 128, bfloat16: 41 us, 20 us of bytes.  The start (lengths, list of items,
@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t nan_for_inf(uint32_t x) {
 // multiplies exactly.  Plain: nibbles 0 and 2 are code * 2^-24, 1 and 3 code * 2^-20.  But the MMA adds a product up to the
 // precision that its operands' exponents give, and a subnormal's leading zeros are lost from it: with codes of 2^-24 the
 // errors of float32 outputs were 5 to 10 times float32's own.  HL therefore shifts every nibble to 2^-20 (the same errors as
-// with normal numbers, at 117 against 131 us for the 117 MB of 131072 tokens).
+// with normal numbers, at 116 against 131 us for the 117 MB of 131072 tokens).
 template <bool HL, int I>
 __device__ __forceinline__ uint32_t operand(uint32_t x) {
   if constexpr (HL) return (I == 0 ? x << 4 : x >> (4 * I - 4)) & 0x00F000F0u;
@@ -1041,9 +1041,12 @@ cudaError_t launch(const KvAttendArgs &a, cudaStream_t s) {
   if (a.pages == 0) p.g.head_bytes = 0;                // addresses stay in the workspace, which stands for an empty cache
   p.ratio = (int)(a.heads / a.kv_heads);
   // Items that far outnumber the SMs go to small teams, whose joins overlap; fewer
-  // items to whole CTAs, which leave fewer parts to add up.  Small teams against whole CTAs: 512 items of 64 to 8192 tokens 41.0
-  // and 46.0 us; 192 items of up to 1024 tokens 18.5 and 17.8; 8 items of 777 tokens 14.5 and 11.6; 32 of 60000 and more 119
-  // and 117.
+  // items to whole CTAs, which leave fewer parts to add up.  Small teams / whole CTAs in us, caches cold, bfloat16 of 64 to 8192
+  // tokens, heads of 128: 64 items 24.7 / 23.6, 192: 31.8 / 33.8, 288: 35.0 / 37.0, 312: 36.0 / 38.0, 400: 40.1 / 43.1, 768: 58.5 / 65.7.
+  // float32 of 600 tokens, heads of 64: 64 items 19.6 / 14.5, 192: 21.6 / 21.6, 288: 27.8 / 22.7, 312: 25.7 / 27.7, 400: 28.5 / 27.8,
+  // 768: 33.9 / 44.2.  bfloat16 of 4000 tokens, heads of 256: 64 items 37.0 / 36.0, 288: 83.1 / 84.1, 312: 87.2 / 89.2, 768: 173 / 179.
+  // So the border is not sharp: between 130 and 400 items either is ahead by a few us, after the tokens.  Captured in a
+  // graph: 8 items of 777 tokens 14.5 / 11.6, 32 of 60000 and more 119 / 117.
   const int64_t items = a.B * a.kv_heads * ((a.max_fresh * p.ratio + C::ROWS - 1) / C::ROWS);
   p.team = items > 2 * kv_max_ctas(1) ? C::TW : C::W;
   // (units a warp of 1 / 1.5 / 2 / 3 for an item's start: 46.0 / 42.4 / 41.0 / 42.8 us for the 512 items; one unit a warp as

@@ -42,10 +42,10 @@
 // rescaled; sums and accumulators are float32.
 //
 // Bound: 4 * D flops a row and key on the tensor cores (1024 cycles a step of 128 rows and 128 keys at D = 128).  Measured: a
-// prompt of 4096 tokens, 32 query and 8 kv heads of 128, 155 us: 45 % of the measured matrix rate; chunks over 700 to 9000
-// tokens, 16 and 4 heads of 256, 296 us: 40 %.  By its own clock a step takes some 2200 cycles: issue of its 16 MMAs 1300 (80
-// each; unrolled and rolled alike), waits 550; the softmax of a tile (2400 cycles of columns, 900 of waits and the mask's
-// test) and the conversion (3700 of the 4400 a block of two steps) are as long, so that no role has slack.
+// prompt of 4096 tokens, 32 query and 8 kv heads of 128, 158 us: 44 % of the measured matrix rate; chunks over 700 to 9000
+// tokens, 16 and 4 heads of 256, 305 us: 39 %.  By its own clock a step takes some 2100 cycles: issue of its 16 MMAs 1300 (80
+// each; unrolled and rolled alike), waits 700; the softmax of a tile (2200 to 2600 cycles of columns, 850 of the mask's test and
+// the tail, 1050 of waits) and the conversion (3000 of the 4200 a block of two steps) are as long, so that no role has slack.
 // Slower, and gone: conversion from global memory (keys 1700 and values 1250 cycles, but 950 and 1050 for their loads:
 // 176 us), a wait by one lane of a warp (241 us), rolled MMA loops (188 against 179 us), TMEM loads of scores ahead (153 against
 // 155 us here, slower for heads of 256).
