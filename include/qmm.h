@@ -243,7 +243,8 @@ int qmm_gather_dequant(const int32_t *ids, int64_t T, const uint32_t *packed, co
  * arena and fused online-softmax attention; "... Tesla C2075 ..." paper,
  * section 5); these entry points give that stage in this library's number
  * format, the group-affine INT4 of the weights: for each token, kv head and group
- * of `group` consecutive elements of the head, w = s * q + b with q in 0..15 and binary16 s and b.
+ * of `group` consecutive elements of the head, w = s * q + b with q in 0..15 and binary16 s and b
+ * (qmm_kv_append writes s >= 0; the other calls take either sign).
  *
  * The cache of one layer is caller-owned device memory of qmm_kv_cache_size()
  * bytes, [pages][kv_heads][page / 16] tiles of 16 tokens (16 * head_dim +

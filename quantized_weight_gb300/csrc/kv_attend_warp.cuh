@@ -740,8 +740,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
           for (int h = 0; h < 2; h++)
 #pragma unroll
             for (int g = 0; g < G; g++) smax = __vmaxu2(smax, vc[i][h][g]);
-        smax &= 0x7FFFu;
-        bool grow = (int)(smax >> 10) > ve;
+        bool grow = (int)((smax & 0xFFFFu) >> 10) > ve;              // a negative scale is above all others here
         float mx[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -754,6 +753,13 @@ __global__ void __launch_bounds__(Cfg<D, G, NT, HL>::THREADS, 1) attend_warp_ker
             grow |= mx[n][c] > mr[n][c];
           }
         if (__any_sync(0xffffffffu, grow)) {
+          smax = 0;                                                  // now of magnitudes
+#pragma unroll
+          for (int i = 0; i < UT; i++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+#pragma unroll
+              for (int g = 0; g < G; g++) smax = max(smax, vc[i][h][g] & 0x7FFFu);
           const int ve2 = max(ve, (int)(__reduce_max_sync(0xffffffffu, smax) >> 10));
           const float vr = pow2i(ve - ve2);                          // what is summed so far, in the new units
           ve = ve2;

@@ -317,3 +317,20 @@ def test_queries_that_are_not_finite(qmm, D, H, dtype):
     got = c.run(qmm)
     assert not np.isfinite(got[hit]).any()
     assert (np.abs(got - want)[~hit] <= tol[~hit]).all()
+
+
+@pytest.mark.parametrize("H,dtype", ROUTES)
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (128, 128), (256, 32)])
+def test_scales_of_either_sign(qmm, D, group, H, dtype):
+    """Small negative scales beside large positive ones, and the other way round."""
+    for sign in (1, -1):
+        c = Case(D + group, D, group, H, dtype)
+        rng = np.random.default_rng(D)
+        coef = c.cache.reshape(len(c.cache), 2, -1)[:, :, 16 * D:].copy().view(np.float16)      # one tile a page
+        s = coef[..., ::2]
+        s *= np.where(rng.random(s.shape) < 0.5, -1.0, 1.0).astype(np.float16)
+        c.cache.reshape(len(c.cache), 2, -1)[:, :, 16 * D:] = coef.view(np.uint8)
+        for token in range(0, c.length, 7):
+            c.coef(token, token % 2, 1, token % (D // group))[:] = np.array([sign * 900.0, -100.0], np.float16).view(np.uint16)
+        want, tol = c.want()
+        assert (np.abs(c.run(qmm) - want) <= tol).all(), sign
