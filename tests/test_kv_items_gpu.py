@@ -68,11 +68,12 @@ def test_teams_that_list_many_times(qmm, dtype):
 
 
 def takes_tiles(B, H, Hkv, D, most):
-    """These cases have rows enough for the prompt kernel, which takes tiles of 128 of them, and items for several turns of
-    every SM (152)."""
-    rows = most * H // Hkv
-    items = B * Hkv * -(-rows // (128 if D == 256 else 256))
-    return items > 2 * 152 and B * Hkv * rows > 8000 * -(-items // 152)
+    """These cases go to the prompt kernel, which takes tiles of 128 rows, with items for several turns of every SM."""
+    import torch
+    from quantized_weight_gb300 import qmm
+    items = B * Hkv * -(-most * H // Hkv // (128 if D == 256 else 256))
+    return items > 2 * torch.cuda.get_device_properties(0).multi_processor_count and \
+        qmm.kv_attend_tiles(torch.bfloat16, B, H, Hkv, D, most)
 
 
 @pytest.mark.parametrize("blocks", [2, 1, 4, 3])
