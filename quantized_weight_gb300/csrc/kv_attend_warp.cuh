@@ -35,7 +35,7 @@
 // last (a counter) adds them up in the line's order, so the result does not depend on which it is.
 //
 // Measured (GB300; the bytes are each visible token's codes and coefficients once, at 6.78 TB/s):
-//   4 requests of 60000 to 130000 tokens, 40 query and 8 kv heads of 128, float32: 116 us, 66 us of bytes (3.8 TB/s).
+//   4 requests of 60000 to 130000 tokens, 40 query and 8 kv heads of 128, float32: 115 us, 66 us of bytes (3.9 TB/s).
 //     Bound: two warps a scheduler (255 registers) issue in 49 % of the cycles, between fixed latencies; the tensor pipe is 38 %
 //     busy (two MMAs a product for float32).
 //   64 requests of 64 to 8192 tokens, 32 and 8 heads of 128, bfloat16: 41 us, 20 us of bytes.  The start (lengths, list of items,
@@ -162,7 +162,7 @@ __device__ __forceinline__ uint32_t nan_for_inf(uint32_t x) {
 // multiplies exactly.  Plain: nibbles 0 and 2 are code * 2^-24, 1 and 3 code * 2^-20.  But the MMA adds a product up to the
 // precision that its operands' exponents give, and a subnormal's leading zeros are lost from it: with codes of 2^-24 the
 // errors of float32 outputs were 5 to 10 times float32's own.  HL therefore shifts every nibble to 2^-20 (the same errors as
-// with normal numbers, at 116 against 131 us for the 117 MB of 131072 tokens).
+// with normal numbers, at 115 against 131 us for the 117 MB of 131072 tokens).
 template <bool HL, int I>
 __device__ __forceinline__ uint32_t operand(uint32_t x) {
   if constexpr (HL) return (I == 0 ? x << 4 : x >> (4 * I - 4)) & 0x00F000F0u;
