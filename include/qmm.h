@@ -353,6 +353,104 @@ int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_he
                   size_t workspace_bytes, qmm_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Microscaled 4-bit floating point: quantize, product, and the routing of tokens to experts
+ *
+ * The pages' other 4-bit formats take integer codes and leave the activations as they are; here both operands of a product
+ * have 4 bits and go to the tensor cores' block-scaled instructions as they are stored, without a dequantization on the
+ * way.  The format is that of the OCP Microscaling specification 1.0 (MXFP4): a code is e2m1,
+ *     code & 7:  0    1    2    3    4    5    6    7
+ *     value:     0    0.5  1    1.5  2    3    4    6      (negative where code & 8)
+ * and 32 consecutive elements of a row share a power of two 2^(s - 127), s a byte; 255 is NaN.
+ *
+ * Layouts.  A matrix [rows, K], K a multiple of 32:
+ *   codes   [rows, K/8] 32-bit words, the lowest nibble holds the lowest k (as bits = 4 above)
+ *   scales  qmm_mx4_scales_size(rows, K) bytes: tiles of 128 rows by 4 blocks (128 elements), 512 bytes each, those of 128
+ *           rows one after the other along K; the scale of row r and block b of a tile is its byte
+ *           16 * (r % 32) + 4 * (r / 32) + b.  The scales of blocks past K in the last tile of a row are read and must not be
+ *           255 (qmm_mx4_quantize and qmm_moe_quantize write 0); those of rows past the last are never used.
+ * Several matrices of one size follow one another, their codes and their scales each.
+ *
+ * Common rules.  rows, N, M, K, R < 2^31, and the rows of all matrices of a call together; K % 32 == 0.  int32 and float32
+ * arrays of the routing (places, experts, weights, starts, counts) need 4-byte alignment, everything else 16 bytes; a row of
+ * x begins at a multiple of 16 bytes.  dtype is QMM_F32 or QMM_BF16.  What the routing holds lies in device memory, so one
+ * captured graph serves changing tokens; no value in it makes a call read or write outside the arrays that it was given.
+ * No call has a workspace, so any two may be in flight at once.  Results are the same on every run on the same GPU model.
+ */
+
+/* Bytes of the scales of one matrix; 0 for sizes outside the common rules. */
+size_t qmm_mx4_scales_size(int64_t rows, int64_t K);
+
+/*
+ * qmm_mx4_quantize -- x [matrices, rows, K] (strides in elements between matrices and between rows, elements of a row
+ *   contiguous) to codes and scales.  s = floor(log2(max |x|)) - 2 + 127 of a block, at least 0; code = the value nearest to
+ *   x / 2^(s - 127), halves to the even code, at most 6; the sign is kept, also of a zero.  (The largest of a block lies
+ *   between 4 and 8 of the unit, so values beyond 7 lose more than half a step, as the specification has it.)  A block with
+ *   an infinity or a NaN has s = 255: all of it is NaN.
+ */
+int qmm_mx4_quantize(const void *x, int dtype, int64_t x_matrix_stride, int64_t x_row_stride, uint32_t *codes,
+                     uint8_t *scales, int64_t matrices, int64_t rows, int64_t K, qmm_stream_t stream);
+
+/* qmm_mx4_dequant -- the values w [matrices, rows, K] float32 that codes and scales stand for, exactly. */
+int qmm_mx4_dequant(const uint32_t *codes, const uint8_t *scales, float *w, int64_t matrices, int64_t rows, int64_t K,
+                    qmm_stream_t stream);
+
+/*
+ * qmm_mx4_gemm -- y[m, n] = sum_k x[m, k] * w[n, k], any M >= 0: decode steps and prompts.
+ *   gated != 0: codes and scales hold two matrices [N, K], g and u, and
+ *     y[m, n] = silu(x . g[n]) * (x . u[n]),  silu(z) = z / (1 + exp(-z)).
+ *   y [M, N] contiguous, float32 or bfloat16 (rounded once).  Products of codes are exact; sums are float32 on the tensor
+ *   cores.  A NaN block makes the results of its row NaN.  K >= 32.  M == 0 or N == 0 is a no-op.
+ */
+int qmm_mx4_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_t *codes, const uint8_t *scales, void *y,
+                 int dtype, int gated, int64_t M, int64_t N, int64_t K, qmm_stream_t stream);
+
+/*
+ * qmm_moe_rows -- R, the rows that the tokens sorted by expert take at most: T * k and 127 for each expert that can be met,
+ *   rounded up to a multiple of 128.  -1 for sizes outside qmm_moe_plan's.
+ */
+int64_t qmm_moe_rows(int64_t T, int64_t E, int64_t k);
+
+/*
+ * qmm_moe_plan -- each token's k best experts, and the tokens sorted by expert.
+ *   logits [T, E] (a stride in elements between rows, elements contiguous; their own alignment suffices).
+ *   experts [T, k]: by falling logit, equal ones (-0 and 0 are) by rising index, NaN first.  A logit of -infinity masks its
+ *     expert: it is never taken, and what a token lacks of k experts has expert -1, weight 0 and place -1.
+ *   weights [T, k] float32: the softmax over the token's chosen experts (normalize != 0), or over all E.
+ *   starts, counts [E]: expert e's rows are starts[e] .. starts[e] + counts[e] - 1, in the order of the tokens; starts are
+ *     multiples of 128, in the order of the experts (so that scale tiles belong to one expert).
+ *   places [T, k]: the row of token t for its j-th expert.
+ *   T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k + 127 * E < 2^31.
+ */
+int qmm_moe_plan(const void *logits, int dtype, int64_t stride, int64_t T, int64_t E, int64_t k, int normalize,
+                 int32_t *experts, float *weights, int32_t *places, int32_t *starts, int32_t *counts, qmm_stream_t stream);
+
+/*
+ * qmm_moe_quantize -- qmm_mx4_quantize of x [T, K], token t's row going to the rows places[t, 0 .. k - 1] of codes and scales
+ *   (R rows).  A place outside [0, R) is skipped; two entries must not have the same place.  Rows of no place are left alone.
+ */
+int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, const int32_t *places, uint32_t *codes,
+                     uint8_t *scales, int64_t T, int64_t k, int64_t R, int64_t K, qmm_stream_t stream);
+
+/*
+ * qmm_moe_gemm -- qmm_mx4_gemm of each expert's rows with its matrix (gated: its two matrices): for 0 <= i < counts[e],
+ *   y[starts[e] + i, n] from x[starts[e] + i, :] and matrix e.  x has R rows, codes and scales E matrices (gated: 2 * E, an
+ *   expert's two after one another).  Other rows of y are left alone.  An expert whose start is negative, past R or no
+ *   multiple of 128 has no rows, and rows past R are left out; no two experts may share a row.
+ *   routed: how many rows the experts have together, about (T * k); it only picks the launch's shape.  1 <= E <= 1024.
+ */
+int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_t *codes, const uint8_t *scales,
+                 const int32_t *starts, const int32_t *counts, void *y, int dtype, int gated, int64_t routed, int64_t R,
+                 int64_t E, int64_t N, int64_t K, qmm_stream_t stream);
+
+/*
+ * qmm_moe_combine -- out[t, n] = sum_j weights[t, j] * y[places[t, j], n], y [R, N] of y_dtype, out [T, N] of out_dtype, sums
+ *   float32 in the order of j.  weights == NULL: all 1.  A place outside [0, R) is left out, whatever its weight.
+ */
+int qmm_moe_combine(const void *y, int y_dtype, const float *weights, const int32_t *places, void *out, int out_dtype,
+                    int64_t T, int64_t k, int64_t R, int64_t N, qmm_stream_t stream);
+
+/*
  * qmm_check -- synchronize `stream`, then report QMM_ERR_CUDA if a kernel
  * failed, QMM_ERR_DEVICE_TIMEOUT if a bounded wait in any kernel ran out
  * since the last qmm_check (and clear that record), else QMM_OK.

@@ -9,6 +9,8 @@
 #include <cuda_runtime.h>
 
 #include "kv_attend.h"
+#include "mx4.cuh"
+#include "mx4_launch.h"
 #include "qmm.h"
 #include "qmm_launch.h"
 
@@ -46,6 +48,21 @@ int check_kv(int64_t pages, int64_t kv_heads, int64_t head_dim, int page, int gr
 }
 // A tensor's strides (elements of `size` bytes) keep every head's row 16-byte aligned.
 bool strides_ok(int64_t token, int64_t head, int size) { return token * size % 16 == 0 && head * size % 16 == 0; }
+
+// Shared checks for the microscaled entries: `rows` of all matrices together, of K elements.
+bool dtype_ok(int dtype) { return dtype == QMM_F32 || dtype == QMM_BF16; }
+int check_mx4(int64_t matrices, int64_t rows, int64_t K) {
+  if (matrices < 0 || matrices >= kMaxDim || rows < 0 || rows >= kMaxDim || K < 0 || K >= kMaxDim || K % 32 != 0 ||
+      (matrices > 0 && rows >= (kMaxDim + matrices - 1) / matrices))
+    return QMM_ERR_SHAPE;
+  return QMM_OK;
+}
+int check_moe(int64_t T, int64_t E, int64_t k) {
+  if (T < 0 || T >= kMaxDim || E < 1 || E > qmm::kMoeMaxExperts || k < 1 || k > qmm::kMoeMaxK || k > E ||
+      T * k + 127 * E >= kMaxDim)
+    return QMM_ERR_SHAPE;
+  return QMM_OK;
+}
 
 }  // namespace
 
@@ -287,6 +304,129 @@ int qmm_kv_attend(const void *q, int dtype, int64_t q_token_stride, int64_t q_he
   return cuda_status(qmm::launch_kv_attend(a, stream));
 }
 
+size_t qmm_mx4_scales_size(int64_t rows, int64_t K) {
+  return check_mx4(1, rows, K) == QMM_OK ? (size_t)qmm::mx4_scales_bytes(rows, K) : 0;
+}
+
+int qmm_mx4_quantize(const void *x, int dtype, int64_t x_matrix_stride, int64_t x_row_stride, uint32_t *codes,
+                     uint8_t *scales, int64_t matrices, int64_t rows, int64_t K, qmm_stream_t stream) {
+  if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
+  const int st = check_mx4(matrices, rows, K);
+  if (st != QMM_OK) return st;
+  if (matrices == 0 || rows == 0 || K == 0) return QMM_OK;
+  if (!x || !codes || !scales) return QMM_ERR_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) ||
+      !strides_ok(x_matrix_stride, x_row_stride, dtype == QMM_BF16 ? 2 : 4))
+    return QMM_ERR_ALIGN;
+  qmm::Mx4QuantArgs a{};
+  a.x = x, a.x_matrix = x_matrix_stride, a.x_row = x_row_stride, a.codes = codes, a.scales = scales;
+  a.matrices = matrices, a.rows = rows, a.K = K, a.bf16 = dtype == QMM_BF16;
+  return cuda_status(qmm::launch_mx4_quantize(a, stream));
+}
+
+int qmm_mx4_dequant(const uint32_t *codes, const uint8_t *scales, float *w, int64_t matrices, int64_t rows, int64_t K,
+                    qmm_stream_t stream) {
+  const int st = check_mx4(matrices, rows, K);
+  if (st != QMM_OK) return st;
+  if (matrices == 0 || rows == 0 || K == 0) return QMM_OK;
+  if (!codes || !scales || !w) return QMM_ERR_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(w)) return QMM_ERR_ALIGN;
+  return cuda_status(qmm::launch_mx4_dequant(codes, scales, w, matrices, rows, K, stream));
+}
+
+int qmm_mx4_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_t *codes, const uint8_t *scales, void *y,
+                 int dtype, int gated, int64_t M, int64_t N, int64_t K, qmm_stream_t stream) {
+  if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
+  int st = check_mx4(1, M, K);
+  if (st == QMM_OK) st = check_mx4(gated ? 2 : 1, N, K);
+  if (st != QMM_OK) return st;
+  if (K < 32) return QMM_ERR_SHAPE;
+  if (M == 0 || N == 0) return QMM_OK;
+  if (!x_codes || !x_scales || !codes || !scales || !y) return QMM_ERR_ARG;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(codes) || !aligned16(scales) || !aligned16(y))
+    return QMM_ERR_ALIGN;
+  qmm::Mx4GemmArgs a{};
+  a.x_codes = x_codes, a.x_scales = x_scales, a.codes = codes, a.scales = scales, a.y = y;
+  a.M = M, a.N = N, a.K = K, a.experts = 1, a.routed = M, a.bf16 = dtype == QMM_BF16, a.gated = gated != 0;
+  return cuda_status(qmm::launch_mx4_gemm(a, stream));
+}
+
+int64_t qmm_moe_rows(int64_t T, int64_t E, int64_t k) {
+  if (check_moe(T, E, k) != QMM_OK) return -1;
+  const int64_t n = T * k, met = n < E ? n : E;
+  return (n + 127 * met + 127) / 128 * 128;
+}
+
+int qmm_moe_plan(const void *logits, int dtype, int64_t stride, int64_t T, int64_t E, int64_t k, int normalize,
+                 int32_t *experts, float *weights, int32_t *places, int32_t *starts, int32_t *counts, qmm_stream_t stream) {
+  if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
+  const int st = check_moe(T, E, k);
+  if (st != QMM_OK) return st;
+  if (!starts || !counts || (T > 0 && (!logits || !experts || !weights || !places))) return QMM_ERR_ARG;
+  const uintptr_t own = dtype == QMM_BF16 ? 1 : 3;
+  for (const void *p : {(const void *)experts, (const void *)weights, (const void *)places, (const void *)starts,
+                        (const void *)counts})
+    if (!aligned4(p)) return QMM_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(logits) & own) return QMM_ERR_ALIGN;
+  qmm::MoePlanArgs a{};
+  a.logits = logits, a.stride = stride, a.T = T, a.E = E, a.k = k, a.bf16 = dtype == QMM_BF16;
+  a.normalize = normalize != 0, a.experts = experts, a.weights = weights, a.places = places, a.starts = starts;
+  a.counts = counts;
+  return cuda_status(qmm::launch_moe_plan(a, stream));
+}
+
+int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, const int32_t *places, uint32_t *codes,
+                     uint8_t *scales, int64_t T, int64_t k, int64_t R, int64_t K, qmm_stream_t stream) {
+  if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
+  int st = check_mx4(1, T, K);
+  if (st == QMM_OK) st = check_mx4(1, R, K);
+  if (st != QMM_OK) return st;
+  if (k < 1 || k > qmm::kMoeMaxK) return QMM_ERR_SHAPE;
+  if (T == 0 || R == 0 || K == 0) return QMM_OK;
+  if (!x || !places || !codes || !scales) return QMM_ERR_ARG;
+  if (!aligned16(x) || !aligned4(places) || !aligned16(codes) || !aligned16(scales) ||
+      !strides_ok(x_row_stride, 0, dtype == QMM_BF16 ? 2 : 4))
+    return QMM_ERR_ALIGN;
+  qmm::Mx4QuantArgs a{};
+  a.x = x, a.x_row = x_row_stride, a.places = places, a.codes = codes, a.scales = scales;
+  a.matrices = 1, a.rows = T, a.K = K, a.k = k, a.out_rows = R, a.bf16 = dtype == QMM_BF16;
+  return cuda_status(qmm::launch_mx4_quantize(a, stream));
+}
+
+int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_t *codes, const uint8_t *scales,
+                 const int32_t *starts, const int32_t *counts, void *y, int dtype, int gated, int64_t routed, int64_t R,
+                 int64_t E, int64_t N, int64_t K, qmm_stream_t stream) {
+  if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
+  if (E < 1 || E > qmm::kMoeMaxExperts || routed < 0 || routed >= kMaxDim || K < 32) return QMM_ERR_SHAPE;
+  int st = check_mx4(1, R, K);
+  if (st == QMM_OK) st = check_mx4(gated ? 2 * E : E, N, K);
+  if (st != QMM_OK) return st;
+  if (R == 0 || N == 0) return QMM_OK;
+  if (!x_codes || !x_scales || !codes || !scales || !starts || !counts || !y) return QMM_ERR_ARG;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(codes) || !aligned16(scales) || !aligned4(starts) ||
+      !aligned4(counts) || !aligned16(y))
+    return QMM_ERR_ALIGN;
+  qmm::Mx4GemmArgs a{};
+  a.x_codes = x_codes, a.x_scales = x_scales, a.codes = codes, a.scales = scales, a.starts = starts, a.counts = counts;
+  a.y = y, a.M = R, a.N = N, a.K = K, a.experts = E, a.routed = routed, a.bf16 = dtype == QMM_BF16;
+  a.gated = gated != 0;
+  return cuda_status(qmm::launch_mx4_gemm(a, stream));
+}
+
+int qmm_moe_combine(const void *y, int y_dtype, const float *weights, const int32_t *places, void *out, int out_dtype,
+                    int64_t T, int64_t k, int64_t R, int64_t N, qmm_stream_t stream) {
+  if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return QMM_ERR_UNSUPPORTED;
+  if (T < 0 || T >= kMaxDim || k < 1 || k > qmm::kMoeMaxK || R < 0 || R >= kMaxDim || N < 0 || N >= kMaxDim)
+    return QMM_ERR_SHAPE;
+  if (T == 0 || N == 0) return QMM_OK;
+  if (!places || !out || (R > 0 && !y)) return QMM_ERR_ARG;
+  if (!aligned16(y) || !aligned4(weights) || !aligned4(places) || !aligned16(out)) return QMM_ERR_ALIGN;
+  qmm::MoeCombineArgs a{};
+  a.y = y, a.weights = weights, a.places = places, a.out = out, a.T = T, a.k = k, a.R = R, a.N = N;
+  a.y_bf16 = y_dtype == QMM_BF16, a.out_bf16 = out_dtype == QMM_BF16;
+  return cuda_status(qmm::launch_moe_combine(a, stream));
+}
+
 int qmm_test_timeout_next_decode(int64_t limit_ns) {
   if (limit_ns < 1000 || limit_ns > 100000000) return QMM_ERR_ARG;
   qmm::set_tc_test_wait((unsigned long long)limit_ns);
@@ -301,14 +441,15 @@ int qmm_test_timeout_next_attend(int64_t limit_ns) {
 
 int qmm_check(qmm_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QMM_ERR_CUDA;
-  int st[6] = {0, 0, 0, 0, 0, 0};
+  int st[7] = {0, 0, 0, 0, 0, 0, 0};
   if (qmm::read_clear_gemm_status(&st[0], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_gemv_status(&st[1], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_q1_status(&st[2], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_batch_status(&st[3], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_tc_status(&st[4], stream) != cudaSuccess) return QMM_ERR_CUDA;
   if (qmm::read_clear_kv_status(&st[5], stream) != cudaSuccess) return QMM_ERR_CUDA;
-  return (st[0] | st[1] | st[2] | st[3] | st[4] | st[5]) != 0 ? QMM_ERR_DEVICE_TIMEOUT : QMM_OK;
+  if (qmm::read_clear_mx4_status(&st[6], stream) != cudaSuccess) return QMM_ERR_CUDA;
+  return (st[0] | st[1] | st[2] | st[3] | st[4] | st[5] | st[6]) != 0 ? QMM_ERR_DEVICE_TIMEOUT : QMM_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,46 @@
+// mx4.cuh -- the microscaled 4-bit format (include/qmm.h): e2m1 codes, blocks of 32 with a power of two each, and
+// where a block's scale stands.
+//
+// Scales are kept in tiles of 128 rows by 4 blocks (512 bytes), the shape in which tcgen05.cp hands them to the tensor
+// core: byte 16 * (row % 32) + 4 * (row / 32) + block of a tile.  The tiles of 128 rows follow one another along K.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+
+namespace qmm {
+
+constexpr int kMxBlock = 32;        // elements that share a scale
+constexpr int kMxRows = 128;        // rows of a scale tile
+constexpr int kMxTileK = 128;       // elements of a row in a scale tile
+constexpr int kMxTileBytes = 512;
+
+__host__ __device__ inline int64_t mx4_k_tiles(int64_t K) { return (K + kMxTileK - 1) / kMxTileK; }
+__host__ __device__ inline int64_t mx4_scales_bytes(int64_t rows, int64_t K) {
+  return (rows + kMxRows - 1) / kMxRows * mx4_k_tiles(K) * kMxTileBytes;
+}
+
+// Offset of the four scales of a row in K tile `kt` of a matrix with `k_tiles` of them a row.
+__device__ __forceinline__ int64_t mx4_scale_word(int64_t row, int64_t kt, int64_t k_tiles) {
+  return ((row >> 7) * k_tiles + kt) * kMxTileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// 2 ** (scale - 127); 255 is NaN.
+__device__ __forceinline__ float mx4_scale(uint32_t scale) {
+  return __uint_as_float(scale == 255 ? 0x7FC00000u : scale == 0 ? 0x00400000u : scale << 23);
+}
+
+// The two values of a byte of codes, the low nibble's first.
+__device__ __forceinline__ float2 mx4_pair(uint32_t byte) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(byte));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// Two values to a byte of codes: nearest, halves to the even code, at most 6.
+__device__ __forceinline__ uint32_t mx4_encode(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace qmm

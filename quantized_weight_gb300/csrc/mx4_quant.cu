@@ -1,0 +1,241 @@
+// mx4_quant.cu -- rows to microscaled 4-bit codes and back (format in mx4.cuh).
+//
+// A block's scale is the power of two 2 ** (floor(log2(max |x|)) - 2), so its largest value lies between 4 and 8 of it and
+// the codes reach 6: the exponent field of max |x| less 2, no arithmetic.  x times the inverse power is exact in float32
+// (or far below the first border), so the codes are the nearest ones to the exact quotient, halves to the even code.
+//
+// All three kernels are bound by memory: a value is read once (2 or 4 bytes) and leaves as 17/32 of a byte.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kv_launch.h"
+#include "mx4.cuh"
+#include "mx4_launch.h"
+#include "qmm_device.cuh"
+
+namespace qmm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 256;         // elements that a warp takes at once: 8 a lane, 4 lanes a block, 2 scale tiles
+
+// A lane's 8 elements.
+struct Eight {
+  float v[8];
+};
+
+template <bool BF16>
+struct Raw {
+  uint4 a, b;                       // b: float32 only
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load8(const void *x, int64_t at) {
+  Raw<BF16> r{};
+  if constexpr (BF16) {
+    r.a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at));
+  } else {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + at);
+    r.a = __ldcs(p);
+    r.b = __ldcs(p + 1);
+  }
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ Eight widen(const Raw<BF16> &r) {
+  Eight e;
+  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    e.v[i] = BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
+  return e;
+}
+
+// A lane's word of codes, and the scale of its block (the same in its 4 lanes).  The whole warp calls it.
+__device__ __forceinline__ uint32_t encode8(const Eight &e, uint32_t &scale) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(e.v[i]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  const uint32_t top = m >> 23;                       // exponent field; 255: an infinity or a NaN is there
+  scale = top == 255 ? 255 : top < 2 ? 0 : top - 2;
+  if (top == 255) return 0;
+  const float inv = __uint_as_float((254 - scale) << 23);   // 2 ** (127 - scale)
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) word |= mx4_encode(e.v[2 * i] * inv, e.v[2 * i + 1] * inv) << (8 * i);
+  return word;
+}
+
+// The four scales of a scale tile's row, in lanes 0..15 those of the first tile of a chunk, in 16..31 the second's.
+__device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane) {
+  uint32_t w = scale << (8 * ((lane >> 2) & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+  return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
+}
+
+struct QuantParams {
+  const void *x;
+  int64_t x_matrix, x_row;
+  const int32_t *places;
+  uint32_t *codes;
+  uint8_t *scales;
+  int64_t rows, K, chunks, k_tiles, units;   // units: warps' pieces of work
+  int64_t scale_bytes;                       // of a matrix
+  int64_t k, out_rows;
+  int lanes, row_tiles;                      // rows r of a tile with r % 32 < lanes exist in some tile; tiles a matrix
+};
+
+// A warp takes a chunk of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes in a row of the
+// scale tile, and four loads are in flight a lane.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= p.units) return;
+  const int64_t chunk = u % p.chunks;
+  u /= p.chunks;
+  const int64_t r32 = u % p.lanes;
+  u /= p.lanes;
+  const int64_t tile = u % p.row_tiles, matrix = u / p.row_tiles;
+  const int64_t row0 = tile * kMxRows + r32, col = chunk * kChunk + 8 * lane;
+  if (row0 >= p.rows) return;
+  const bool in = col < p.K;
+  Raw<BF16> raw[4];
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    raw[g] = Raw<BF16>{};
+    if (in && row0 + 32 * g < p.rows) raw[g] = load8<BF16>(p.x, matrix * p.x_matrix + (row0 + 32 * g) * p.x_row + col);
+  }
+  uint32_t words[4];
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    uint32_t scale;
+    const uint32_t code = encode8(widen(raw[g]), scale);
+    words[g] = scale_word(scale, lane);
+    if (in && row0 + 32 * g < p.rows) p.codes[((matrix * p.rows + row0 + 32 * g) * p.K + col) >> 3] = code;
+  }
+  const int64_t kt = chunk * 2 + (lane >> 4);
+  if ((lane & 15) == 0 && kt < p.k_tiles)
+    *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
+        make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+// A warp takes up to 4 chunks of a token's row, and stores them to each of its places.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) quantize_routed_kernel(const QuantParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= p.units) return;
+  const int64_t t = u / p.chunks, col0 = (u % p.chunks) * (4 * kChunk) + 8 * lane;
+  const int mine = lane < p.k ? p.places[t * p.k + lane] : -1;
+  Raw<BF16> raw[4];
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    raw[g] = Raw<BF16>{};
+    if (col0 + g * kChunk < p.K) raw[g] = load8<BF16>(p.x, t * p.x_row + col0 + g * kChunk);
+  }
+  uint32_t codes[4], words[4];
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    uint32_t scale;
+    codes[g] = encode8(widen(raw[g]), scale);
+    words[g] = scale_word(scale, lane);
+  }
+  for (int j = 0; j < (int)p.k; j++) {
+    const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
+    if (row < 0 || row >= p.out_rows) continue;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int64_t col = col0 + g * kChunk, kt = (col - 8 * lane) / kMxTileK + (lane >> 4);
+      if (col < p.K) p.codes[(row * p.K + col) >> 3] = codes[g];
+      if ((lane & 15) == 0 && kt < p.k_tiles)
+        *reinterpret_cast<uint32_t *>(p.scales + mx4_scale_word(row, kt, p.k_tiles)) = words[g];
+    }
+  }
+}
+
+struct DequantParams {
+  const uint32_t *codes;
+  const uint8_t *scales;
+  float *w;
+  int64_t rows, K8, words, k_tiles, scale_bytes;   // K8: words a row; words: of all matrices
+};
+
+constexpr int kWordsAThread = 4;
+
+__global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t first = (int64_t)blockIdx.x * (kThreads * kWordsAThread) + threadIdx.x;
+  uint32_t code[kWordsAThread], scale[kWordsAThread];
+#pragma unroll
+  for (int i = 0; i < kWordsAThread; i++) {
+    const int64_t at = first + i * kThreads;
+    code[i] = scale[i] = 0;
+    if (at >= p.words) continue;
+    code[i] = __ldcs(p.codes + at);
+    const int64_t r = at / p.K8, block = (at - r * p.K8) >> 2, matrix = r / p.rows;
+    scale[i] = p.scales[matrix * p.scale_bytes + mx4_scale_word(r - matrix * p.rows, block >> 2, p.k_tiles) + (block & 3)];
+  }
+#pragma unroll
+  for (int i = 0; i < kWordsAThread; i++) {
+    const int64_t at = first + i * kThreads;
+    if (at >= p.words) break;
+    const float s = mx4_scale(scale[i]);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const float2 f = mx4_pair((code[i] >> (8 * j)) & 255);
+      v[2 * j] = f.x * s;
+      v[2 * j + 1] = f.y * s;
+    }
+    float4 *o = reinterpret_cast<float4 *>(p.w) + 2 * at;
+    __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
+  QuantParams p{};
+  p.x = a.x, p.x_matrix = a.x_matrix, p.x_row = a.x_row, p.places = a.places;
+  p.codes = static_cast<uint32_t *>(a.codes), p.scales = static_cast<uint8_t *>(a.scales);
+  p.rows = a.rows, p.K = a.K, p.k_tiles = mx4_k_tiles(a.K), p.scale_bytes = mx4_scales_bytes(a.rows, a.K);
+  p.k = a.k, p.out_rows = a.out_rows;
+  if (a.places) {
+    p.chunks = (a.K + 4 * kChunk - 1) / (4 * kChunk);
+    p.units = a.rows * p.chunks;
+  } else {
+    p.chunks = (a.K + kChunk - 1) / kChunk;
+    p.lanes = a.rows < 32 ? (int)a.rows : 32;
+    p.row_tiles = (int)((a.rows + kMxRows - 1) / kMxRows);
+    p.units = a.matrices * p.row_tiles * p.lanes * p.chunks;
+  }
+  const int64_t grid = (p.units + kWarps - 1) / kWarps;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  auto kern = a.places ? (a.bf16 ? quantize_routed_kernel<true> : quantize_routed_kernel<false>)
+                       : (a.bf16 ? quantize_kernel<true> : quantize_kernel<false>);
+  return launch_after(kern, grid, kThreads, 0, s, p);
+}
+
+cudaError_t launch_mx4_dequant(const void *codes, const void *scales, float *w, int64_t matrices, int64_t rows, int64_t K,
+                               cudaStream_t s) {
+  DequantParams p{};
+  p.codes = static_cast<const uint32_t *>(codes), p.scales = static_cast<const uint8_t *>(scales), p.w = w;
+  p.rows = rows, p.K8 = K / 8, p.words = matrices * rows * p.K8;
+  p.k_tiles = mx4_k_tiles(K), p.scale_bytes = mx4_scales_bytes(rows, K);
+  const int64_t grid = (p.words + kThreads * kWordsAThread - 1) / (kThreads * kWordsAThread);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  return launch_after(dequant_kernel, grid, kThreads, 0, s, p);
+}
+
+}  // namespace qmm

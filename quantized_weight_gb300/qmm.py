@@ -80,6 +80,17 @@ def lib():
                                         i32, i32, f32, i64, vp, sz, vp]
             L.qmm_kv_attend_tiles.argtypes = [i32, i64, i64, i64, i64, i64]
             L.qmm_kv_cache_size.restype = L.qmm_kv_attend_workspace_size.restype = sz
+            L.qmm_mx4_scales_size.argtypes = [i64, i64]
+            L.qmm_mx4_scales_size.restype = sz
+            L.qmm_mx4_quantize.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i64, vp]
+            L.qmm_mx4_dequant.argtypes = [vp, vp, vp, i64, i64, i64, vp]
+            L.qmm_mx4_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, vp]
+            L.qmm_moe_rows.argtypes = [i64, i64, i64]
+            L.qmm_moe_rows.restype = i64
+            L.qmm_moe_plan.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+            L.qmm_moe_quantize.argtypes = [vp, i32, i64, vp, vp, vp, i64, i64, i64, i64, vp]
+            L.qmm_moe_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, i64, i64, vp]
+            L.qmm_moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
             L.qmm_check.argtypes = [vp]
             L.qmm_test_timeout_next_decode.argtypes = L.qmm_test_timeout_next_attend.argtypes = [i64]
             L.qmm_status_string.argtypes = [i32]
@@ -88,7 +99,8 @@ def lib():
             for f in ("qmm_pack", "qmm_unpack", "qmm_dequant", "qmm_gemv", "qmm_gemm", "qmm_quantize",
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
                       "qmm_test_timeout_next_decode", "qmm_test_timeout_next_attend", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
-                      "qmm_kv_attend", "qmm_kv_attend_tiles"):
+                      "qmm_kv_attend", "qmm_kv_attend_tiles", "qmm_mx4_quantize", "qmm_mx4_dequant", "qmm_mx4_gemm",
+                      "qmm_moe_plan", "qmm_moe_quantize", "qmm_moe_gemm", "qmm_moe_combine"):
                 getattr(L, f).restype = i32
             _lib = L
     return _lib
@@ -438,6 +450,204 @@ def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_
         q.data_ptr(), dt, qt, qh, pc, pt, pl, pcu, po, T, B, blocks, max_fresh, pages, H,
         heads, D, page, group, D ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- microscaled 4-bit products and experts
+
+_MX_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _mx_dtype(dtype) -> int:
+    dt = _MX_DTYPE.get(dtype)
+    if dt is None:
+        raise TypeError(f"values are float32 or bfloat16, got {dtype}")
+    return dt
+
+
+def _here(t, name, dtype, shape) -> int:
+    """Pointer of a contiguous tensor of the given type and shape on the current device (where the kernels run)."""
+    if not (t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, device, stream):
+    """An output of a call on `stream`: its memory belongs to that stream, so that no one else's work is in its way."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _mx_x(x):
+    """(strides between matrices and rows) of x [..., rows, K] on the current device, whose rows are contiguous and whose
+    leading dimensions are one after the other."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"x is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if x.dim() < 2:
+        raise ValueError(f"x must be [..., rows, K], got {tuple(x.shape)}")
+    if x.dim() > 3:
+        x = x.view(-1, *x.shape[-2:])
+    strides = x.stride()
+    if strides[-1] != 1 and x.shape[-1] > 1 and x.numel() > 0:
+        raise ValueError("x must be contiguous in its last dimension")
+    row = strides[-2] if x.shape[-2] > 1 else 0                       # a lone row or matrix has no stride to keep
+    return (strides[0] if x.dim() == 3 and x.shape[0] > 1 else 0), row
+
+
+def mx4_scales_size(rows, K) -> int:
+    """Bytes of the scales of a matrix [rows, K]."""
+    n = int(lib().qmm_mx4_scales_size(rows, K))
+    if n == 0 and (rows < 0 or K < 0 or K % 32 != 0 or rows * K != 0):
+        raise ValueError(f"no microscaled matrix of {rows} rows of {K}: K is a multiple of 32, both are below 2**31")
+    return n
+
+
+def mx4_scales(plain) -> torch.Tensor:
+    """Scales of a checkpoint, bytes [..., rows, K / 32], in the tiles that the products read (include/qmm.h)."""
+    lead, (rows, blocks) = plain.shape[:-2], plain.shape[-2:]
+    across, down = -(-blocks // 4), -(-rows // 128)
+    full = torch.zeros((*lead, down * 128, across * 4), dtype=torch.uint8, device=plain.device)
+    full[..., :rows, :blocks] = plain
+    n = len(lead)
+    tiles = full.view(*lead, down, 4, 32, across, 4).permute(*range(n), n, n + 3, n + 2, n + 1, n + 4)
+    return tiles.reshape(*lead, down * across * 512)
+
+
+def _mx_matrix(codes, scales, name, lead):
+    """(rows, K, pointers) of a microscaled matrix [*lead, rows, K / 8] and its scales."""
+    if codes.dim() != len(lead) + 2 or codes.shape[:-2] != lead:
+        raise ValueError(f"{name} must be [{', '.join(map(str, (*lead, 'rows', 'K / 8')))}], got {tuple(codes.shape)}")
+    rows, K = codes.shape[-2], codes.shape[-1] * 8
+    pc = _here(codes, name, torch.int32, codes.shape)
+    return rows, K, pc, _here(scales, name + "'s scales", torch.uint8, (*lead, mx4_scales_size(rows, K)))
+
+
+def mx4_quantize(x, out=None, stream=None):
+    """float32 or bfloat16 x [..., rows, K] to microscaled 4-bit (codes int32 [..., rows, K / 8], scales uint8 [..., bytes])."""
+    dt = _mx_dtype(x.dtype)
+    sm, sr = _mx_x(x)
+    lead, rows, K = x.shape[:-2], x.shape[-2], x.shape[-1]
+    size = mx4_scales_size(rows, K)
+    if out is None:
+        out = _new((*lead, rows, K // 8), torch.int32, x.device, stream), _new((*lead, size), torch.uint8, x.device, stream)
+    pc, ps = _here(out[0], "codes", torch.int32, (*lead, rows, K // 8)), _here(out[1], "scales", torch.uint8, (*lead, size))
+    _call("qmm_mx4_quantize", lib().qmm_mx4_quantize(x.data_ptr(), dt, sm, sr, pc, ps, lead.numel(), rows, K,
+                                                     _stream(stream)))
+    return out
+
+
+def mx4_dequant(codes, scales, out=None, stream=None) -> torch.Tensor:
+    """The float32 values [..., rows, K] of a microscaled matrix."""
+    lead = codes.shape[:-2]
+    rows, K, pc, ps = _mx_matrix(codes, scales, "codes", lead)
+    if out is None:
+        out = _new((*lead, rows, K), torch.float32, codes.device, stream)
+    po = _here(out, "out", torch.float32, (*lead, rows, K))
+    _call("qmm_mx4_dequant", lib().qmm_mx4_dequant(pc, ps, po, lead.numel(), rows, K, _stream(stream)))
+    return out
+
+
+def mx4_gemm(x_codes, x_scales, codes, scales, gated=False, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
+    """y [M, N] = x . w^T of microscaled x [M, K] and w [N, K], float32 or bfloat16; gated: codes and scales hold two matrices
+    [2, N, K], and y = silu(x . g^T) * (x . u^T)."""
+    M, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes", ())
+    N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (2,) if gated else ())
+    if KW != K:
+        raise ValueError(f"x has rows of {K}, the weights of {KW}")
+    if out is None:
+        out = _new((M, N), dtype, x_codes.device, stream)
+    dt = _mx_dtype(out.dtype)
+    po = _here(out, "out", out.dtype, (M, N))
+    _call("qmm_mx4_gemm", lib().qmm_mx4_gemm(px, pxs, pc, ps, po, dt, int(gated), M, N, K, _stream(stream)))
+    return out
+
+
+def moe_rows(T, E, k) -> int:
+    """Rows that T tokens, each with k of E experts, take at most once sorted by expert."""
+    n = int(lib().qmm_moe_rows(T, E, k))
+    if n < 0:
+        raise ValueError(f"no routing of {T} tokens to {k} of {E} experts")
+    return n
+
+
+def moe_plan(logits, k, normalize=True, out=None, stream=None):
+    """Each token's k best experts of logits [T, E] (float32 or bfloat16; -infinity masks an expert): (experts int32 [T, k],
+    weights float32 [T, k], places int32 [T, k], starts int32 [E], counts int32 [E]).  Expert e's rows are starts[e] ..
+    starts[e] + counts[e] - 1 of moe_rows(T, E, k); places says which is whose.  weights are the softmax over the chosen
+    experts (normalize) or over all."""
+    dt = _mx_dtype(logits.dtype)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    T, E = logits.shape
+    _, row = _mx_x(logits)
+    if out is None:
+        out = (_new((T, k), _I32, logits.device, stream), _new((T, k), torch.float32, logits.device, stream),
+               _new((T, k), _I32, logits.device, stream), _new((E,), _I32, logits.device, stream),
+               _new((E,), _I32, logits.device, stream))
+    names = (("experts", _I32, (T, k)), ("weights", torch.float32, (T, k)), ("places", _I32, (T, k)), ("starts", _I32, (E,)),
+             ("counts", _I32, (E,)))
+    ptrs = [_here(t, *n) for t, n in zip(out, names)]
+    _call("qmm_moe_plan", lib().qmm_moe_plan(logits.data_ptr(), dt, row, T, E, k, int(normalize), *ptrs, _stream(stream)))
+    return out
+
+
+def moe_quantize(x, places, rows, out=None, stream=None):
+    """mx4_quantize of x [T, K], each token's row to its places [T, k]: (codes int32 [rows, K / 8], scales).  Other rows are
+    left alone (without `out`: as memory happens to be; no product of another row reads them)."""
+    dt = _mx_dtype(x.dtype)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
+    _, row = _mx_x(x)
+    T, K = x.shape
+    k = places.shape[-1]
+    pp = _here(places, "places", _I32, (T, k))
+    size = mx4_scales_size(rows, K)
+    if out is None:
+        out = _new((rows, K // 8), torch.int32, x.device, stream), _new((size,), torch.uint8, x.device, stream)
+    pc, ps = _here(out[0], "codes", torch.int32, (rows, K // 8)), _here(out[1], "scales", torch.uint8, (size,))
+    _call("qmm_moe_quantize", lib().qmm_moe_quantize(x.data_ptr(), dt, row, pp, pc, ps, T, k, rows, K, _stream(stream)))
+    return out
+
+
+def moe_gemm(x_codes, x_scales, codes, scales, starts, counts, routed=None, gated=False, dtype=torch.float32, out=None,
+             stream=None) -> torch.Tensor:
+    """mx4_gemm of each expert's rows of x [R, K] with its matrix of codes [E, N, K / 8] (gated: [E, 2, N, K / 8]): y [R, N].
+    Rows of no expert are left alone (without `out`: as memory happens to be).  routed: how many rows the experts have
+    together, about (default: R); it picks the launch's shape."""
+    R, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes", ())
+    E = starts.shape[0]
+    N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (E, 2) if gated else (E,))
+    if KW != K:
+        raise ValueError(f"x has rows of {K}, the weights of {KW}")
+    pst, pco = _here(starts, "starts", _I32, (E,)), _here(counts, "counts", _I32, (E,))
+    if out is None:
+        out = _new((R, N), dtype, x_codes.device, stream)
+    dt = _mx_dtype(out.dtype)
+    po = _here(out, "out", out.dtype, (R, N))
+    _call("qmm_moe_gemm", lib().qmm_moe_gemm(px, pxs, pc, ps, pst, pco, po, dt, int(gated), R if routed is None else routed,
+                                             R, E, N, K, _stream(stream)))
+    return out
+
+
+def moe_combine(y, weights, places, dtype=None, out=None, stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[places[t, j]] of y [R, N]; weights None: all 1.  dtype defaults to y's."""
+    dt = _mx_dtype(y.dtype)
+    if y.dim() != 2 or places.dim() != 2:
+        raise ValueError(f"y must be [R, N] and places [T, k], got {tuple(y.shape)} and {tuple(places.shape)}")
+    (R, N), (T, k) = y.shape, places.shape
+    py, pp = _here(y, "y", y.dtype, y.shape), _here(places, "places", _I32, (T, k))
+    pw = None if weights is None else _here(weights, "weights", torch.float32, (T, k))
+    if out is None:
+        out = _new((T, N), y.dtype if dtype is None else dtype, y.device, stream)
+    do = _mx_dtype(out.dtype)
+    po = _here(out, "out", out.dtype, (T, N))
+    _call("qmm_moe_combine", lib().qmm_moe_combine(py, dt, pw, pp, po, do, T, k, R, N, _stream(stream)))
     return out
 
 
