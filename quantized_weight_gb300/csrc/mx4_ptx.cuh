@@ -1,0 +1,52 @@
+// mx4_ptx.cuh -- the block-scaled tensor-core instructions of the microscaled 4-bit product.
+#pragma once
+#include <cstdint>
+
+#include "sm100_ptx.cuh"
+
+namespace qmm {
+namespace sm100 {
+
+// D[tmem] (+)= A * B^T, e2m1 operands in shared memory (K-major, 64 elements = 32 bytes of a row), a scale for each 32
+// elements in TMEM (sfa, sfb; idesc says which two of a column's four bytes), f32 out.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// 32 rows of 16 bytes from shared memory to 4 columns of TMEM, the same in each of its four lane quarters.  In order with
+// the same thread's MMAs.
+__device__ __forceinline__ void tmem_cp_32x16b(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Bulk copy global -> shared: `bytes` and both addresses multiples of 16, completion as transaction bytes on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// Descriptor of 512 bytes in that order: no swizzle, 8 rows of 16 bytes after 8 rows.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
+}
+
+// Instruction descriptor, kind::mxf4: e2m1 operands, power-of-two scales, M x N; `half` selects the scales' bytes 0, 1 or
+// 2, 3 of both operands.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return (1u << 7) | (1u << 10)          // A, B: e2m1
+         | (uint32_t)(2 * half) << 4     // B's scales
+         | (uint32_t)(N >> 3) << 17      // N / 8
+         | (1u << 23)                    // scales: e8m0
+         | (uint32_t)(M >> 7) << 27      // M / 128
+         | (uint32_t)(2 * half) << 29;   // A's scales
+}
+
+}  // namespace sm100
+}  // namespace qmm
