@@ -56,13 +56,12 @@ struct Params {
   const int32_t *starts, *counts;          // null: one matrix, M rows
   void *y;
   int64_t M, N;                            // rows of x, rows of a matrix
-  int64_t m_tiles, n_tiles;                // (m_tiles: one matrix only)
+  int64_t n_tiles;
   int64_t w_scale_bytes;                   // of a matrix
   int k_tiles, k_stages, k_steps;          // scale tiles of a row, stages and MMAs along K
-  int experts, bf16;
-  int ts;                                  // tokens of a tile: 64, 128, 192 or 256
+  int experts;
   int box;                                 // rows of x in a copy
-  int stages, bufs;                        // ring depth, accumulators
+  int stages;                              // ring depth
   int split;                               // CTAs of a cluster, each with a part of K
 };
 
@@ -103,14 +102,27 @@ struct Ring {
   }
 };
 
-template <bool GATED>
+template <bool BF16>
+__device__ __forceinline__ void store(void *y, int64_t at, float v) {
+  if constexpr (BF16)
+    __stcs(static_cast<unsigned short *>(y) + at, __bfloat16_as_ushort(__float2bfloat16_rn(v)));
+  else
+    __stcs(static_cast<float *>(y) + at, v);
+}
+
+// silu(z) * u.  (Of a denominator beyond 2^126, z below -87, the quick division makes 0 instead of 2^-120 or less.)
+__device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1.0f + expf(-z)) * u; }
+
+// TS: tokens of a tile.
+template <bool GATED, bool BF16, int TS>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   constexpr int TWO = GATED ? 2 : 1;
+  constexpr int BUFS = 2 * TWO * TS + 2 * (8 * TWO + 16) <= TMEM_COLS ? 2 : 1;      // accumulators that TMEM holds
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_addr(smem);
-  const Layout l = layout(GATED, p.ts, p.stages, p.split, p.experts);
+  const Layout l = layout(GATED, TS, p.stages, p.split, p.experts);
   float *red = reinterpret_cast<float *>(smem + l.ring);
   int32_t *starts = reinterpret_cast<int32_t *>(smem + l.ring + l.red), *counts = starts + p.experts, *before = counts + p.experts;
   const uint32_t bars = sbase + l.ring + l.red + l.list;
@@ -156,7 +168,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (start < 0 || start >= p.M || start % kMxRows != 0 || count < 0) start = 0, count = 0;
         if (count > p.M - start) count = p.M - start;
       }
-      const int tiles = e < p.experts ? (int)((count + p.ts - 1) / p.ts) : 0;
+      const int tiles = e < p.experts ? (int)((count + TS - 1) / TS) : 0;
       int at = tiles;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -188,129 +200,160 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     const int64_t tiles = before[lo + 1] - before[lo], j = i - (int64_t)before[lo] * p.n_tiles;
     const int64_t nt = j / tiles;
-    const int m0 = (int)(j - nt * tiles) * p.ts;
+    const int m0 = (int)(j - nt * tiles) * TS;
     it.expert = lo;
     it.n0 = nt * BM;
     it.row = (int64_t)starts[lo] + m0;
-    it.rows = min(counts[lo] - m0, p.ts);
+    it.rows = min(counts[lo] - m0, TS);
     return it;
   };
 
-  Ring ring;                                   // (of the copying and the issuing thread)
+  // (a reduction over equal values leaves its result in a uniform register, where the operands of copies and MMAs have to
+  // be: from ordinary registers a stage's instructions took 1600 cycles to issue)
+  auto uniform = [](uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); };
+  auto uniform64 = [&](uint64_t v) { return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v); };
+  Ring ring;                                   // (of the copying and the issuing warp)
   int issued = 0;                              // stages so far
   int local = 0;                               // items so far
   bool ok = true;
   for (int64_t i = first; i < items; i += step, local++) {
     const Item it = item_at(i);
-    const int buf = local % p.bufs;
-    const uint32_t use = (local / p.bufs) & 1;
+    const int buf = local & (BUFS - 1);
+    const uint32_t use = (uint32_t)(BUFS == 2 ? local >> 1 : local) & 1;
     // tokens of the tile before its first: its scale tile may begin 64 rows earlier
     const int shift = (int)(it.row & (kMxRows - 1));
     const int sf_tiles = (shift + it.rows + kMxRows - 1) / kMxRows;
     if (warp == 0) {
       // -------------------------------------------------------- copies
-      if (lane == 0 && ok) {
-        const int boxes = (it.rows + p.box - 1) / p.box;
-        const int64_t w_row = (int64_t)it.expert * TWO * p.N + it.n0;
-        const uint8_t *ws = p.ws + (int64_t)it.expert * TWO * p.w_scale_bytes + (it.n0 >> 7) * p.k_tiles * kMxTileBytes;
-        const uint8_t *xs = p.xs + (it.row >> 7) * p.k_tiles * kMxTileBytes;
+      if (ok) {
+        const uint32_t boxes = uniform((it.rows + p.box - 1) / p.box), row = uniform((uint32_t)it.row);
+        const uint32_t w_row = uniform((uint32_t)((int64_t)it.expert * TWO * p.N + it.n0)), w_next = uniform((uint32_t)p.N);
+        const uint64_t ws = uniform64(reinterpret_cast<uint64_t>(p.ws) + (int64_t)it.expert * TWO * p.w_scale_bytes +
+                                      (it.n0 >> 7) * p.k_tiles * kMxTileBytes);
+        const uint64_t xs = uniform64(reinterpret_cast<uint64_t>(p.xs) + (it.row >> 7) * p.k_tiles * kMxTileBytes);
+        const uint32_t two_tiles = uniform(sf_tiles == 2), box_bytes = uniform(p.box * (BK / 2));
+        const uint32_t each = l.a + boxes * box_bytes, sfs = TWO + 1 + two_tiles;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
-          const uint32_t base = sbase + ring.s * l.stage, bar = full(ring.s);
-          if (!wait_bounded(empty(ring.s), ring.ph ^ 1, ctl)) { ok = false; break; }
-          const uint32_t sf = (uint32_t)min(2, p.k_tiles - 2 * ks) * kMxTileBytes;
-          mbar_arrive_expect_tx(bar, l.a + boxes * p.box * (BK / 2) + (TWO + sf_tiles) * sf);
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(empty(ring.s), ring.ph ^ 1, ctl))) { ok = false; break; }
+          const uint32_t base = uniform(sbase + ring.s * l.stage), bar = uniform(full(ring.s)), k = uniform(ks);
+          const uint32_t sf = uniform(min(2, p.k_tiles - 2 * ks)) * kMxTileBytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar, each + sfs * sf);
 #pragma unroll
-          for (int g = 0; g < TWO; g++) {
-            tma_load_2d(base + g * BM * (BK / 2), &tmap_w, ks * (BK / 2), (int)(w_row + g * p.N), bar);
-            bulk_copy(base + l.a + l.b + g * 2 * kMxTileBytes, ws + g * p.w_scale_bytes + (int64_t)ks * 2 * kMxTileBytes, sf, bar);
+            for (int g = 0; g < TWO; g++) {
+              tma_load_2d(base + g * BM * (BK / 2), &tmap_w, k * (BK / 2), w_row + g * w_next, bar);
+              bulk_copy(base + l.a + l.b + g * 2 * kMxTileBytes, ws + g * p.w_scale_bytes + (uint64_t)k * 2 * kMxTileBytes, sf, bar);
+            }
+            tma_load_2d(base + l.a, &tmap_x, k * (BK / 2), row, bar);
+            bulk_copy(base + l.a + l.b + l.sfa, xs + (uint64_t)k * 2 * kMxTileBytes, sf, bar);
+            if (two_tiles)
+              bulk_copy(base + l.a + l.b + l.sfa + 2 * kMxTileBytes, xs + ((uint64_t)p.k_tiles + 2 * k) * kMxTileBytes, sf, bar);
+            for (uint32_t b = 1; b < boxes; b++)
+              tma_load_2d(base + l.a + b * box_bytes, &tmap_x, k * (BK / 2), row + b * p.box, bar);
           }
-          for (int b = 0; b < boxes; b++)
-            tma_load_2d(base + l.a + b * p.box * (BK / 2), &tmap_x, ks * (BK / 2), (int)it.row + b * p.box, bar);
-          for (int t = 0; t < sf_tiles; t++)
-            bulk_copy(base + l.a + l.b + l.sfa + t * 2 * kMxTileBytes,
-                      xs + ((int64_t)t * p.k_tiles + 2 * ks) * kMxTileBytes, sf, bar);
+          __syncwarp();
         }
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- products
-      if (lane == 0 && ok) {
-        ok = wait_bounded(acc_empty(buf), use ^ 1, ctl);
+      if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(acc_empty(buf), use ^ 1, ctl));
+      if (ok) {
         tc_fence_after();
-        const int n = (it.rows + 15) & ~15;
-        const uint32_t id0 = idesc_mxf4(BM, n, 0), id1 = idesc_mxf4(BM, n, 1);
-        const uint32_t d = tmem + buf * TWO * p.ts;
-        for (int ks = ks0; ks < ks1 && ok; ks++, issued++, ring.next(p.stages)) {
-          if (!wait_bounded(full(ring.s), ring.ph, ctl)) { ok = false; break; }
+        const uint32_t id = uniform(idesc_mxf4(BM, (it.rows + 15) & ~15));
+        const uint32_t d = uniform(tmem + buf * TWO * TS), sf0 = uniform(tmem + BUFS * TWO * TS);
+        const uint32_t off = uniform(shift >> 5), two_tiles = uniform(sf_tiles == 2);
+        const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
+        for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
+          if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
           tc_fence_after();
-          const uint32_t base = sbase + ring.s * l.stage;
           // scales: by turns in two places, 8 columns a weight tile (4 a scale tile) and 16 for the tokens
-          const uint32_t sfa = tmem + p.bufs * TWO * p.ts + (issued & 1) * (8 * TWO + 16), sfb = sfa + 8 * TWO;
-          const int sts = min(2, p.k_tiles - 2 * ks);
-          for (int a = 0; a < sts; a++) {
+          const uint32_t sfa = uniform(sf0 + (issued & 1) * (8 * TWO + 16)), sfb = sfa + 8 * TWO;
+          const uint32_t at = uniform((sbase + ring.s * l.stage) >> 4), bar = uniform(empty(ring.s)), more = uniform(ks > ks0);
+          const uint64_t ad = ops | at, bd = ops | (at + (l.a >> 4));
+          const uint64_t sd = scales | (at + ((l.a + l.b) >> 4)), td = scales | (at + ((l.a + l.b + l.sfa) >> 4));
+          const uint32_t steps = uniform(min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)));
+          if (elect_one()) {
 #pragma unroll
-            for (int g = 0; g < TWO; g++)
-              tmem_cp_32x16b(sfa + g * 8 + a * 4, smem_desc_scales(base + l.a + l.b + (g * 2 + a) * kMxTileBytes));
-            for (int t = 0; t < sf_tiles; t++)
-              tmem_cp_32x16b(sfb + a * 8 + t * 4, smem_desc_scales(base + l.a + l.b + l.sfa + (t * 2 + a) * kMxTileBytes));
-          }
-          const uint64_t ad = smem_desc_sw128(base), bd = smem_desc_sw128(base + l.a);
-          const int steps = min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K));
-          for (int j = 0; j < steps; j++) {
+            for (int a = 0; a < 2; a++) {                // (two MMAs a scale tile)
+              if (2 * a >= steps) break;
 #pragma unroll
-            for (int g = 0; g < TWO; g++)
-              umma_mxf4(d + g * p.ts, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id1 : id0,
-                        sfa + g * 8 + (j >> 1) * 4, sfb + (j >> 1) * 8 + (shift >> 5), ks > ks0 || j > 0);
+              for (int g = 0; g < TWO; g++) tmem_cp_32x16b(sfa + g * 8 + a * 4, sd + (g * 2 + a) * (kMxTileBytes / 16));
+              tmem_cp_32x16b(sfb + a * 8, td + a * (kMxTileBytes / 16));
+              if (two_tiles) tmem_cp_32x16b(sfb + a * 8 + 4, td + (2 + a) * (kMxTileBytes / 16));
+#pragma unroll
+              for (int j = 2 * a; j < 2 * a + 2; j++) {
+                if (j >= steps) break;
+#pragma unroll
+                for (int g = 0; g < TWO; g++)
+                  umma_mxf4(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
+                            sfa + g * 8 + a * 4, sfb + a * 8 + off, j > 0 ? 1u : more);
+              }
+            }
+            umma_commit(bar);
           }
-          umma_commit(empty(ring.s));
+          __syncwarp();
         }
-        if (ok) umma_commit(acc_full(buf));
+        if (ok && elect_one()) umma_commit(acc_full(buf));
+        __syncwarp();
       }
     } else {
       // -------------------------------------------------------- epilogue
-      const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;      // TMEM lane quarter; which chunks of 16 tokens
+      const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;      // TMEM lane quarter; which half of the tile's tokens
       const int r = q * 32 + lane;
       const int64_t n = it.n0 + r;
       if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(acc_full(buf), use, ctl));
       if (ok) {
         tc_fence_after();
-        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + buf * TWO * p.ts;
-#pragma unroll 1
-        for (int c = 16 * half; c < it.rows; c += 32) {
-          uint32_t v[TWO][16];
-          __syncwarp();
+        // everything to registers, so that the next item's products can begin
+        constexpr int CHUNKS = TS / 32;                            // of 16 tokens, a warp
+        uint32_t v[CHUNKS][TWO][16];
+        const int c0 = half * (TS / 2), left = it.rows - c0;       // tokens of this half
+        const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + buf * TWO * TS + c0;
 #pragma unroll
-          for (int g = 0; g < TWO; g++) tmem_ld_32x32b_x16(d + g * p.ts + c, v[g]);
-          tmem_ld_wait();
-          if (p.split > 1) {
-            // token c + j of the tile belongs to rank (c + j) % split, as its row (c + j) / split
+        for (int c = 0; c < CHUNKS; c++)
+          if (16 * c < left) {
+#pragma unroll
+            for (int g = 0; g < TWO; g++) tmem_ld_32x32b_x16(d + g * TS + 16 * c, v[c][g]);
+          }
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive(acc_empty(buf));
+        if (TS == 64 && p.split > 1) {
+          // token t of the tile belongs to rank t % split, as its row t / split
+          const int sh = __ffs(p.split) - 1;
+          const uint32_t mine = smem_addr(red + (rank * (TS >> sh) * TWO) * BM + r);
+#pragma unroll
+          for (int c = 0; c < CHUNKS; c++)
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-              const int t = c + j;
-              if (t < it.rows)
+              const int t = 16 * c + j;
+              if (t >= left) break;
 #pragma unroll
-                for (int g = 0; g < TWO; g++)
-                  st_cluster_f32(mapa_shared(smem_addr(red + ((rank * (p.ts / p.split) + t / p.split) * TWO + g) * BM + r), t % p.split),
-                                 __uint_as_float(v[g][j]));
+              for (int g = 0; g < TWO; g++)
+                st_cluster_f32(mapa_shared(mine + (((c0 + t) >> sh) * TWO + g) * BM * 4, t & (p.split - 1)), __uint_as_float(v[c][g][j]));
             }
-          } else if (n < p.N) {
+        } else if (n < p.N) {
+          auto out = [&](int c, int j) {
+            return GATED ? gate(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][TWO - 1][j])) : __uint_as_float(v[c][0][j]);
+          };
+          int64_t at = (it.row + c0) * p.N + n;
 #pragma unroll
-            for (int j = 0; j < 16; j++) {
-              if (c + j >= it.rows) break;
-              float o = __uint_as_float(v[0][j]);
-              if constexpr (GATED) o = o / (1.0f + expf(-o)) * __uint_as_float(v[TWO - 1][j]);
-              const int64_t at = (it.row + c + j) * p.N + n;
-              if (p.bf16)
-                __stcs(static_cast<unsigned short *>(p.y) + at, __bfloat16_as_ushort(__float2bfloat16_rn(o)));
-              else
-                __stcs(static_cast<float *>(p.y) + at, o);
+          for (int c = 0; c < CHUNKS; c++) {
+            if (16 * c + 16 <= left) {
+#pragma unroll
+              for (int j = 0; j < 16; j++, at += p.N) store<BF16>(p.y, at, out(c, j));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; j++, at += p.N) {
+                if (16 * c + j >= left) break;
+                store<BF16>(p.y, at, out(c, j));
+              }
             }
           }
         }
-        tc_fence_before();
-        mbar_arrive(acc_empty(buf));
       }
     }
-    if (p.split > 1) {
+    if (TS == 64 && p.split > 1) {
       __syncthreads();                         // (every epilogue warp has sent its part, or none will)
       if (threadIdx.x < p.split) st_cluster_u32(mapa_shared(smem_addr(fine + rank), threadIdx.x), *abort_flag ? 0u : 1u);
       __syncwarp();
@@ -318,36 +361,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool whole = true;
       for (int s = 0; s < p.split; s++) whole = whole && fine[s] != 0;
       if (whole) {
-        const int own = (it.rows - rank + p.split - 1) / p.split;     // tokens of this CTA
+        const int sh = __ffs(p.split) - 1, own = (it.rows - rank + p.split - 1) >> sh;     // tokens of this CTA
         for (int x = threadIdx.x; x < own * BM; x += NUM_THREADS) {
           const int t = x / BM, r = x % BM;
           float sum[TWO];
 #pragma unroll
           for (int g = 0; g < TWO; g++) {
             sum[g] = 0.0f;
-            for (int s = 0; s < p.split; s++) sum[g] += red[((s * (p.ts / p.split) + t) * TWO + g) * BM + r];
+            for (int s = 0; s < p.split; s++) sum[g] += red[((s * (TS >> sh) + t) * TWO + g) * BM + r];
           }
-          float o = sum[0];
-          if constexpr (GATED) o = o / (1.0f + expf(-o)) * sum[TWO - 1];
-          if (it.n0 + r < p.N) {
-            const int64_t at = (it.row + t * p.split + rank) * p.N + it.n0 + r;
-            if (p.bf16)
-              __stcs(static_cast<unsigned short *>(p.y) + at, __bfloat16_as_ushort(__float2bfloat16_rn(o)));
-            else
-              __stcs(static_cast<float *>(p.y) + at, o);
-          }
+          if (it.n0 + r < p.N)
+            store<BF16>(p.y, (it.row + t * p.split + rank) * p.N + it.n0 + r, GATED ? gate(sum[0], sum[TWO - 1]) : sum[0]);
         }
       }
       __syncwarp();
       if (i + step < items) cluster_sync();    // (its neighbours read what the next item overwrites)
     }
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // every copy lands before this CTA's memory goes to another
     for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; j++) wait_drain(full(j % p.stages), (j / p.stages) & 1);
   }
-  if (warp == 1 && lane == 0 && !ok) {
-    umma_commit(drain_bar);
+  if (warp == 1 && !ok) {
+    if (elect_one()) umma_commit(drain_bar);
+    __syncwarp();
     wait_drain(drain_bar, 0);
   }
   tc_fence_before();
@@ -386,46 +423,33 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const
 
 }  // namespace
 
-cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
+namespace {
+
+template <bool GATED, bool BF16, int TS>
+cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, int64_t most, int sms, cudaStream_t s) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
   if (!encode) return cudaErrorNotSupported;
-  const int two = a.gated ? 2 : 1, sms = kv_max_ctas(1);
-  Params p{};
-  p.xs = static_cast<const uint8_t *>(a.x_scales), p.ws = static_cast<const uint8_t *>(a.scales);
-  p.starts = a.starts, p.counts = a.counts, p.y = a.y, p.M = a.M, p.N = a.N;
-  p.n_tiles = (a.N + BM - 1) / BM;
-  p.w_scale_bytes = mx4_scales_bytes(a.N, a.K);
-  p.k_tiles = (int)mx4_k_tiles(a.K), p.k_stages = (int)((a.K + BK - 1) / BK), p.k_steps = (int)((a.K + MMA_K - 1) / MMA_K);
-  p.experts = (int)a.experts, p.bf16 = a.bf16;
-  // rows that an expert has, about
-  const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
-  const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
-  p.ts = rows <= 64 ? 64 : a.gated || rows <= 128 ? 128 : 192;
-  p.box = rows <= 16 ? 16 : 64;
-  p.bufs = 2 * two * p.ts + 2 * (8 * two + 16) <= TMEM_COLS ? 2 : 1;
-  // items, about, and parts of K that give every SM one
-  const int64_t items = met * ((rows + p.ts - 1) / p.ts) * p.n_tiles;
-  p.split = 1;
-  if (p.ts == 64)
-    while (p.split < MAX_SPLIT && items * p.split * 2 <= sms && p.k_stages >= 2 * p.split) p.split *= 2;
-  const int tail = layout(a.gated, p.ts, 0, p.split, p.experts).total;
-  p.stages = (SMEM_LIMIT - tail) / layout(a.gated, p.ts, 1, p.split, p.experts).stage;
-  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-  const Layout l = layout(a.gated, p.ts, p.stages, p.split, p.experts);
   CUtensorMap tx, tw;
-  if (!encode_rows(encode, &tx, a.x_codes, a.M, a.K, p.box) ||
-      !encode_rows(encode, &tw, a.codes, a.experts * two * a.N, a.K, BM))
+  if (!encode_rows(encode, &tx, a.x_codes, a.M, a.K, box) ||
+      !encode_rows(encode, &tw, a.codes, a.experts * (GATED ? 2 : 1) * a.N, a.K, BM))
     return cudaErrorInvalidValue;
-  auto kern = a.gated ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>;
+  p.box = box;
+  // parts of K that give every SM some
+  p.split = 1;
+  if (TS == 64)
+    while (p.split < MAX_SPLIT && items * p.split * 2 <= sms && p.k_stages >= 2 * p.split) p.split *= 2;
+  p.stages = (SMEM_LIMIT - layout(GATED, TS, 0, p.split, p.experts).total) / layout(GATED, TS, 0, p.split, p.experts).stage;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  const int smem = layout(GATED, TS, p.stages, p.split, p.experts).total;
+  auto kern = mx4_gemm_kernel<GATED, BF16, TS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (e != cudaSuccess) return e;
-  int64_t most = a.starts ? (a.M / p.ts + a.experts + 1) * p.n_tiles : items;   // items at most
   int64_t grid = sms / p.split;
   if (most < grid) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(grid * p.split));
   cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = l.total;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -435,6 +459,34 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = p.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, tx, tw, p);
+}
+
+template <bool GATED, bool BF16>
+cudaError_t launch_type(const Mx4GemmArgs &a, const Params &p, cudaStream_t s) {
+  const int sms = kv_max_ctas(1);
+  // rows that an expert has, about
+  const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
+  const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
+  const int ts = rows <= 64 ? 64 : GATED || rows <= 128 ? 128 : 256;
+  const int64_t items = met * ((rows + ts - 1) / ts) * p.n_tiles;
+  const int64_t most = a.starts ? (a.M / ts + a.experts + 1) * p.n_tiles : items;
+  if (ts == 64) return launch_tile<GATED, BF16, 64>(a, p, rows <= 16 ? 16 : 64, items, most, sms, s);
+  if (GATED || ts == 128) return launch_tile<GATED, BF16, 128>(a, p, 128, items, most, sms, s);
+  return launch_tile<false, BF16, 256>(a, p, 256, items, most, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
+  Params p{};
+  p.xs = static_cast<const uint8_t *>(a.x_scales), p.ws = static_cast<const uint8_t *>(a.scales);
+  p.starts = a.starts, p.counts = a.counts, p.y = a.y, p.M = a.M, p.N = a.N;
+  p.n_tiles = (a.N + BM - 1) / BM;
+  p.w_scale_bytes = mx4_scales_bytes(a.N, a.K);
+  p.k_tiles = (int)mx4_k_tiles(a.K), p.k_stages = (int)((a.K + BK - 1) / BK), p.k_steps = (int)((a.K + MMA_K - 1) / MMA_K);
+  p.experts = (int)a.experts;
+  if (a.gated) return a.bf16 ? launch_type<true, true>(a, p, s) : launch_type<true, false>(a, p, s);
+  return a.bf16 ? launch_type<false, true>(a, p, s) : launch_type<false, false>(a, p, s);
 }
 
 cudaError_t read_clear_mx4_status(int *status, cudaStream_t s) {

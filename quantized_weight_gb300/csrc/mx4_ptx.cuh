@@ -26,7 +26,7 @@ __device__ __forceinline__ void tmem_cp_32x16b(uint32_t taddr, uint64_t desc) {
 }
 
 // Bulk copy global -> shared: `bytes` and both addresses multiples of 16, completion as transaction bytes on `bar`.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void bulk_copy(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
                : "memory");
@@ -37,15 +37,20 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
 }
 
-// Instruction descriptor, kind::mxf4: e2m1 operands, power-of-two scales, M x N; `half` selects the scales' bytes 0, 1 or
-// 2, 3 of both operands.
-__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+// Instruction descriptor, kind::mxf4: e2m1 operands, power-of-two scales, M x N, the scales' bytes 0 and 1 of a column.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N) {
   return (1u << 7) | (1u << 10)          // A, B: e2m1
-         | (uint32_t)(2 * half) << 4     // B's scales
          | (uint32_t)(N >> 3) << 17      // N / 8
          | (1u << 23)                    // scales: e8m0
-         | (uint32_t)(M >> 7) << 27      // M / 128
-         | (uint32_t)(2 * half) << 29;   // A's scales
+         | (uint32_t)(M >> 7) << 27;     // M / 128
+}
+constexpr uint32_t kSecondScales = 2u << 4 | 2u << 29;   // bytes 2 and 3, of B's and A's scales
+
+// One thread of a converged warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 }  // namespace sm100
