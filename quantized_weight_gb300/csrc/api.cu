@@ -57,6 +57,8 @@ int check_mx4(int64_t matrices, int64_t rows, int64_t K) {
     return QMM_ERR_SHAPE;
   return QMM_OK;
 }
+// Tiles of 64 rows by 128 are counted in 32 bits.
+bool mx4_tiles_ok(int64_t M, int64_t E, int64_t N) { return (M / 64 + E + 1) * ((N + 127) / 128) < kMaxDim; }
 int check_moe(int64_t T, int64_t E, int64_t k) {
   if (T < 0 || T >= kMaxDim || E < 1 || E > qmm::kMoeMaxExperts || k < 1 || k > qmm::kMoeMaxK || k > E ||
       T * k + 127 * E >= kMaxDim)
@@ -340,7 +342,7 @@ int qmm_mx4_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_
   int st = check_mx4(1, M, K);
   if (st == QMM_OK) st = check_mx4(gated ? 2 : 1, N, K);
   if (st != QMM_OK) return st;
-  if (K < 32) return QMM_ERR_SHAPE;
+  if (K < 32 || !mx4_tiles_ok(M, 1, N)) return QMM_ERR_SHAPE;
   if (M == 0 || N == 0) return QMM_OK;
   if (!x_codes || !x_scales || !codes || !scales || !y) return QMM_ERR_ARG;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(codes) || !aligned16(scales) || !aligned16(y))
@@ -400,6 +402,7 @@ int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_
   if (E < 1 || E > qmm::kMoeMaxExperts || routed < 0 || routed >= kMaxDim || K < 32) return QMM_ERR_SHAPE;
   int st = check_mx4(1, R, K);
   if (st == QMM_OK) st = check_mx4(gated ? 2 * E : E, N, K);
+  if (st == QMM_OK && !mx4_tiles_ok(R, E, N)) st = QMM_ERR_SHAPE;
   if (st != QMM_OK) return st;
   if (R == 0 || N == 0) return QMM_OK;
   if (!x_codes || !x_scales || !codes || !scales || !starts || !counts || !y) return QMM_ERR_ARG;

@@ -5,14 +5,13 @@
 
 #include "kv_attend.h"
 #include "kv_launch.h"
+#include "mx4.cuh"
 #include "mx4_launch.h"
 #include "qmm_device.cuh"
 #include "sm100_ptx.cuh"
 
 namespace qmm {
 namespace {
-
-using namespace sm100;
 
 // ---------------------------------------------------------------- the best experts of a token
 
@@ -31,83 +30,153 @@ struct PlanParams {
   const void *logits;
   int64_t stride, T;
   int E, k, bf16, normalize;
-  int64_t per_warp;        // tokens a warp of the sorting kernel takes
+  int whole;               // rows of logits can be read in vectors
+  int64_t tokens;          // of a CTA of the sorting kernel
+  int blocks;              // of 32 tokens, that its shared memory holds at once
   int32_t *experts;
   float *weights;
   int32_t *places, *starts, *counts;
 };
 
-// One token by one warp: lane holds the experts p * 32 + lane.
-template <int PER>
-__device__ __forceinline__ void best_experts(const PlanParams &p, int64_t t, int lane) {
+// One token by LANES lanes, each with PER experts in a row, so that of equal keys the lowest lane's is the lowest expert's.
+// A lane keeps its best; a round is one maximum over the lanes, and only the lane that had it looks for its next.  Eight
+// lanes a token rather than a warp: a round's instructions then serve four tokens (16381 tokens, 128 experts, 8 each: see
+// best_kernel).  `live`: the lanes' token exists.  The whole warp calls it.
+template <int LANES, int PER>
+__device__ __forceinline__ void best_experts(const PlanParams &p, int64_t t, bool live, int lane) {
+  constexpr int OWN = kMoeMaxK / LANES;        // of the token's choices, each lane keeps every LANES-th
+  const int sub = lane & (LANES - 1), e0 = PER * sub;
   uint32_t key[PER];
+  const int64_t row = t * p.stride + e0;
+  if (PER % 4 == 0 && p.whole) {      // E is a multiple of PER, rows begin at 16 bytes: eight bytes or more at a time
+    const bool in = live && e0 < p.E;
 #pragma unroll
-  for (int i = 0; i < PER; i++) {
-    const int e = i * 32 + lane;
-    key[i] = 0;
-    if (e < p.E) {
-      const int64_t at = t * p.stride + e;
-      key[i] = key_of(p.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.logits)[at] << 16)
-                             : static_cast<const float *>(p.logits)[at]);
+    for (int i = 0; i + 3 < PER; i += 4) {
+      float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (in && p.bf16) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.logits) + row + i);
+        v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xFFFF0000u);
+      } else if (in) {
+        const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.logits) + row + i);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) key[i + j] = key_of(v[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+      key[i] = 0;
+      if (live && e0 + i < p.E)
+        key[i] = key_of(p.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.logits)[row + i] << 16)
+                               : static_cast<const float *>(p.logits)[row + i]);
     }
   }
-  uint32_t top = 0;
+  uint32_t best = 0;
+  int at = 0;
+  auto look = [&]() {      // (no chain of comparisons: maxima by pairs, then which have it)
+    uint32_t m[PER];
 #pragma unroll
-  for (int i = 0; i < PER; i++) top = max(top, key[i]);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
-  const float most = value_of(top);
-  float all = 0.0f;        // of the softmax over every expert
+    for (int i = 0; i < PER; i++) m[i] = key[i];
+#pragma unroll
+    for (int o = PER / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < o; i++) m[i] = max(m[i], m[i + o]);
+    best = m[0];
+    uint32_t had = 0;
+#pragma unroll
+    for (int i = 0; i < PER; i++) had |= (key[i] == best ? 1u : 0u) << i;
+    at = __ffs(had) - 1;
+  };
+  auto over_lanes = [&](uint32_t v) {
+    if constexpr (LANES == 32) {
+      return __reduce_max_sync(0xFFFFFFFFu, v);
+    } else {
+#pragma unroll
+      for (int o = LANES / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+      return v;
+    }
+  };
+  auto sum_lanes = [&](float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+  };
+  look();
+  uint32_t win = over_lanes(best);
+  const float most = value_of(win);
+  float all = 0.0f;        // of the softmax
   if (!p.normalize) {
 #pragma unroll
     for (int i = 0; i < PER; i++)
       if (key[i] > kMasked) all += expf(value_of(key[i]) - most);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
   }
-  int mine = -1;           // lane j: the j-th expert, and its logit's key
-  uint32_t mine_key = 0;
+  int mine[OWN];
+  float w[OWN];
+#pragma unroll
+  for (int q = 0; q < OWN; q++) mine[q] = -1, w[q] = 0.0f;
   for (int j = 0; j < p.k; j++) {
-    uint32_t best = 0;
-    int at = 0;
+    if (__all_sync(0xFFFFFFFFu, win <= kMasked)) break;
+    const unsigned had = __ballot_sync(0xFFFFFFFFu, best == win) >> (lane & ~(LANES - 1));
+    const int from = __ffs(had) - 1;           // (of those with the lanes of this token; some lane has its maximum)
+    const int e = __shfl_sync(0xFFFFFFFFu, e0 + at, from, LANES);
+    if (win > kMasked) {
+      const float share = expf(value_of(win) - most);
 #pragma unroll
-    for (int i = 0; i < PER; i++)
-      if (key[i] > best) best = key[i], at = i * 32 + lane;
-    const uint32_t win = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (win <= kMasked) break;
-    const int e = (int)__reduce_min_sync(0xFFFFFFFFu, best == win ? (unsigned)at : 0xFFFFFFFFu);
+      for (int q = 0; q < OWN; q++)
+        if (j == q * LANES + sub) mine[q] = e, w[q] = share;
+      if (sub == from) {
 #pragma unroll
-    for (int i = 0; i < PER; i++)
-      if (i * 32 + lane == e) key[i] = 0;
-    if (lane == j) mine = e, mine_key = win;
+        for (int i = 0; i < PER; i++)
+          if (i == at) key[i] = 0;
+        look();
+      }
+    }
+    win = over_lanes(best);
   }
-  float w = mine >= 0 ? expf(value_of(mine_key) - most) : 0.0f;
   if (p.normalize) {
-    all = w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    for (int q = 0; q < OWN; q++) all += w[q];
   }
-  if (lane < p.k) {
-    p.experts[t * p.k + lane] = mine;
-    p.weights[t * p.k + lane] = mine >= 0 ? w / all : 0.0f;
+  all = sum_lanes(all);
+#pragma unroll
+  for (int q = 0; q < OWN; q++) {
+    const int j = q * LANES + sub;
+    if (live && j < p.k) {
+      p.experts[t * p.k + j] = mine[q];
+      p.weights[t * p.k + j] = mine[q] >= 0 ? w[q] / all : 0.0f;
+    }
   }
 }
 
-constexpr int kBestThreads = 256;
-template <int PER>
+// The tokens t0 .. t1 - 1 by `warps` warps, of which this one is `warp`.
+template <int LANES, int PER>
+__device__ __forceinline__ void best_of(const PlanParams &p, int64_t t0, int64_t t1, int warp, int warps, int lane) {
+  constexpr int AT_ONCE = 32 / LANES;
+  for (int64_t t = t0 + warp * AT_ONCE; t < t1; t += warps * AT_ONCE) {
+    const int64_t own = t + lane / LANES;
+    best_experts<LANES, PER>(p, own, own < t1, lane);
+  }
+}
+
+constexpr int kBestThreads = 128;
+template <int LANES, int PER>
 __global__ void __launch_bounds__(kBestThreads) best_kernel(const PlanParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t t = (int64_t)blockIdx.x * (kBestThreads / 32) + (threadIdx.x >> 5);
-  if (t < p.T) best_experts<PER>(p, t, threadIdx.x & 31);
+  constexpr int TOKENS = kBestThreads / LANES;
+  const int64_t t0 = (int64_t)blockIdx.x * TOKENS;
+  best_of<LANES, PER>(p, t0, min(p.T, t0 + TOKENS), threadIdx.x >> 5, kBestThreads / 32, threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------- the sort
-
-// A stable counting sort of the tokens' entries by one cluster: each warp counts its tokens' experts, the counts of the
-// warps before it (in its CTA by a thread an expert, in the other CTAs through shared memory) and the padded totals of
-// the experts before say where its entries begin, and it hands out places in order.  With PER > 0 the warps also choose
-// their tokens' experts, one launch in all.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 8;
+//
+// A stable counting sort.  Of 32 tokens and an expert, a word says which of the tokens have it (by atomic or, whose order
+// changes nothing); so an entry's place is where its expert's rows begin, plus that expert's entries in the words before
+// (sums of their bits), plus the bits below its own.  One CTA does few tokens, its warps choosing their experts first; a
+// cluster does many, the experts' totals of its CTAs going through shared memory.
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32, kSortCluster = 16, kSortBlocks = 64;
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
@@ -115,53 +184,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   return v;
 }
 
-template <int PER, bool CLUSTER>
-__global__ void __launch_bounds__(kSortThreads) sort_kernel(const PlanParams p) {
-  extern __shared__ uint32_t count[];          // [warp][E], then totals [E] of this CTA
-  __shared__ uint32_t sums[kSortWarps];
-  uint32_t *total = count + kSortWarps * p.E;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x, E = p.E;
-  const int rank = CLUSTER ? (int)cluster_ctarank() : 0;
-  uint32_t *own = count + warp * E;
-  for (int i = threadIdx.x; i < kSortWarps * E; i += kSortThreads) count[i] = 0;
-  __syncthreads();
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t t0 = min(p.T, (rank * kSortWarps + warp) * p.per_warp), t1 = min(p.T, t0 + p.per_warp);
-  if constexpr (PER > 0) {
-    for (int64_t t = t0; t < t1; t++) best_experts<PER>(p, t, lane);
-    __syncwarp();
-  }
-  const int64_t i0 = t0 * p.k, i1 = t1 * p.k;
-  for (int64_t i = i0 + lane; i < i1; i += 32) {
-    const int x = p.experts[i];
-    if (x >= 0) atomicAdd(own + x, 1u);
-  }
-  __syncthreads();
-  uint32_t mine = 0;                           // entries of expert e in this CTA
-  if (e < E) {
-    for (int w = 0; w < kSortWarps; w++) {
-      const uint32_t c = count[w * E + e];
-      count[w * E + e] = mine;
-      mine += c;
-    }
-    total[e] = mine;
-  }
-  uint32_t before = 0, whole = mine;           // entries of expert e in the CTAs before, and in all
-  if constexpr (CLUSTER) {
-    cluster_sync();
-    if (e < E) {
-      whole = 0;
-      for (int r = 0; r < kSortCluster; r++) {
-        const uint32_t c = ld_cluster_u32(mapa_shared(smem_addr(total + e), r));
-        if (r < rank) before += c;
-        whole += c;
-      }
-    }
-    cluster_sync();                            // (nobody leaves while its totals are read)
-  }
-  // where expert e's rows begin
-  const uint32_t padded = (whole + 127u) & ~127u;
+// Where the rows of expert threadIdx.x begin, given its entries (0 past the last expert): a block's exclusive sum of counts
+// rounded up to 128.
+__device__ __forceinline__ uint32_t begin_of(uint32_t entries, uint32_t *sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t padded = (entries + 127u) & ~127u;
   uint32_t at = padded;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -180,21 +207,137 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const PlanParams p) 
     sums[lane] = v;
   }
   __syncthreads();
-  at += (warp > 0 ? sums[warp - 1] : 0) - padded;
-  if (e < E) {
-    if (rank == 0) p.starts[e] = (int)at, p.counts[e] = (int)whole;
-    for (int w = 0; w < kSortWarps; w++) count[w * E + e] += at + before;
+  return at + (warp > 0 ? sums[warp - 1] : 0) - padded;
+}
+
+// LANES 0: the experts are chosen already, and a cluster sorts.
+template <int LANES, int PER>
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const PlanParams p) {
+  constexpr bool CLUSTER = LANES == 0;
+  extern __shared__ uint32_t mask[];           // [block][E] words, then [block][E] sums of 16 bits
+  __shared__ uint32_t total[kMoeMaxExperts], next[kMoeMaxExperts], part[kSortThreads], sums[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, E = p.E, k = p.k;
+  uint16_t *before = reinterpret_cast<uint16_t *>(mask + p.blocks * E);
+  const int rank = CLUSTER ? (int)sm100::cluster_ctarank() : 0;
+  // a thread an expert and group of blocks
+  int EP = 32;
+  while (EP < E) EP *= 2;
+  const int groups = kSortThreads / EP, e = threadIdx.x & (EP - 1), g = threadIdx.x / EP;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t c0 = min(p.T, rank * p.tokens), c1 = min(p.T, c0 + p.tokens);
+  if constexpr (!CLUSTER) {
+    best_of<LANES, PER>(p, c0, c1, warp, kSortWarps, lane);
+    __syncthreads();
+  }
+
+  // eight of a token's experts from the j-th on, -1 past its last (loads that wait for nothing between them)
+  auto load8 = [&](int64_t t, int j, int (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) x[i] = t < c1 && j + i < k ? p.experts[t * k + j + i] : -1;
+  };
+  // the words of the blocks from token t0 on, their sums, and the totals
+  auto count = [&](int64_t t0) {
+    const int n = (int)min((int64_t)p.blocks, (c1 - t0 + 31) / 32);
+    for (int i = threadIdx.x; i < n * E; i += kSortThreads) mask[i] = 0;
+    __syncthreads();
+    for (int b = warp; b < n; b += kSortWarps) {
+      const int64_t t = t0 + 32 * b + lane;
+      for (int j = 0; j < k; j += 8) {
+        int x[8];
+        load8(t, j, x);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          if (x[i] >= 0) atomicOr(mask + b * E + x[i], 1u << lane);
+      }
+    }
+    __syncthreads();
+    const int b0 = n * g / groups, b1 = n * (g + 1) / groups;
+    uint32_t sum = 0;
+    if (e < E)
+      for (int b = b0; b < b1; b++) sum += __popc(mask[b * E + e]);
+    part[threadIdx.x] = sum;
+    __syncthreads();
+    if (e < E) {
+      uint32_t at = 0;
+      for (int i = 0; i < g; i++) at += part[i * EP + e];
+      for (int b = b0; b < b1; b++) {
+        before[b * E + e] = (uint16_t)at;
+        at += __popc(mask[b * E + e]);
+      }
+      if (g == groups - 1) total[e] = at;
+    }
+    __syncthreads();
+  };
+  auto hand_out = [&](int64_t t0) {
+    const int n = (int)min((int64_t)p.blocks, (c1 - t0 + 31) / 32);
+    for (int b = warp; b < n; b += kSortWarps) {
+      const int64_t t = t0 + 32 * b + lane;
+      for (int j = 0; j < k; j += 8) {
+        int x[8];
+        load8(t, j, x);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          if (x[i] >= 0) x[i] = (int)(next[x[i]] + before[b * E + x[i]] + __popc(mask[b * E + x[i]] & ((1u << lane) - 1)));
+        if (t < c1) {
+          if (k % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4)
+              if (j + i < k) *reinterpret_cast<int4 *>(p.places + t * k + j + i) = make_int4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+              if (j + i < k) p.places[t * k + j + i] = x[i];
+          }
+        }
+      }
+    }
+  };
+
+  const bool once = c1 - c0 <= 32 * p.blocks;
+  if (once) {
+    count(c0);
+  } else {
+    for (int i = threadIdx.x; i < E; i += kSortThreads) total[i] = 0;
+    __syncthreads();
+    for (int64_t i = c0 * k + threadIdx.x; i < c1 * k; i += 8 * kSortThreads) {
+      int x[8];
+#pragma unroll
+      for (int a = 0; a < 8; a++) x[a] = i + a * kSortThreads < c1 * k ? p.experts[i + a * kSortThreads] : -1;
+#pragma unroll
+      for (int a = 0; a < 8; a++)
+        if (x[a] >= 0) atomicAdd(total + x[a], 1u);
+    }
+    __syncthreads();
+  }
+  uint32_t earlier = 0, whole = 0;             // entries of expert threadIdx.x in the CTAs before, and in all
+  if constexpr (CLUSTER) {
+    sm100::cluster_sync();
+    if (threadIdx.x < E)
+      for (int r = 0; r < kSortCluster; r++) {
+        const uint32_t c = ld_cluster_u32(sm100::mapa_shared(sm100::smem_addr(total + threadIdx.x), r));
+        if (r < rank) earlier += c;
+        whole += c;
+      }
+    sm100::cluster_sync();                     // (nobody leaves or counts on while its totals are read)
+  } else if (threadIdx.x < E) {
+    whole = total[threadIdx.x];
+  }
+  const uint32_t begin = begin_of(whole, sums);
+  if (threadIdx.x < E) {
+    next[threadIdx.x] = begin + earlier;
+    if (rank == 0) p.starts[threadIdx.x] = (int)begin, p.counts[threadIdx.x] = (int)whole;
   }
   __syncthreads();
-  for (int64_t i = i0; i < i1; i += 32) {
-    const int x = i + lane < i1 ? p.experts[i + lane] : -1;
-    const unsigned like = __match_any_sync(0xFFFFFFFFu, x);
-    const int ahead = __popc(like & ((1u << lane) - 1));
-    const uint32_t base = x >= 0 ? own[x] : 0;
-    __syncwarp();
-    if (x >= 0 && ahead == 0) own[x] = base + __popc(like);
-    __syncwarp();
-    if (i + lane < i1) p.places[i + lane] = x >= 0 ? (int)(base + ahead) : -1;
+  if (once) {
+    hand_out(c0);
+    return;
+  }
+  for (int64_t t0 = c0; t0 < c1; t0 += 32 * p.blocks) {
+    count(t0);
+    hand_out(t0);
+    __syncthreads();
+    if (threadIdx.x < E) next[threadIdx.x] += total[threadIdx.x];
   }
 }
 
@@ -205,7 +348,8 @@ struct CombineParams {
   const float *weights;
   const int32_t *places;
   void *out;
-  int64_t T, R, N, pieces;
+  int64_t T, R, N;
+  Divisor pieces;          // blocks of a token
   int k;
 };
 
@@ -223,16 +367,19 @@ __device__ __forceinline__ void put(void *y, int64_t at, float v) {
     static_cast<float *>(y)[at] = v;
 }
 
-// A block takes a piece of one token's row: V elements a thread (1 where rows are not made of whole 16-byte words).
+// A block takes a piece of one token's row: V elements in a row a thread or, where rows are not made of whole 16-byte words
+// (V = 1), four that are a block's threads apart.
 template <bool Y16, bool O16, int V>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t t = blockIdx.x / p.pieces, n = ((blockIdx.x % p.pieces) * kCombineThreads + threadIdx.x) * V;
+  constexpr int U = V == 1 ? 4 : 1, S = V == 1 ? kCombineThreads : 1, ALL = V * U;
+  uint32_t piece = blockIdx.x;
+  const int64_t t = p.pieces.split(piece), n = (int64_t)piece * (kCombineThreads * ALL) + threadIdx.x * V;
   if (n >= p.N) return;
-  float sum[V];
+  float sum[ALL];
 #pragma unroll
-  for (int v = 0; v < V; v++) sum[v] = 0.0f;
+  for (int v = 0; v < ALL; v++) sum[v] = 0.0f;
 #pragma unroll 4
   for (int j = 0; j < p.k; j++) {
     const int64_t row = p.places[t * p.k + j];
@@ -240,7 +387,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
     const float w = p.weights ? p.weights[t * p.k + j] : 1.0f;
     const int64_t at = row * p.N + n;
     if constexpr (V == 1) {
-      sum[0] += w * one<Y16>(p.y, at);
+#pragma unroll
+      for (int u = 0; u < U; u++)
+        if (n + u * S < p.N) sum[u] += w * one<Y16>(p.y, at + u * S);
     } else if constexpr (Y16) {
       const uint4 u = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.y) + at));
       const uint32_t x[4] = {u.x, u.y, u.z, u.w};
@@ -259,7 +408,9 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineP
   }
   const int64_t at = t * p.N + n;
   if constexpr (V == 1) {
-    put<O16>(p.out, at, sum[0]);
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (n + u * S < p.N) put<O16>(p.out, at + u * S, sum[u]);
   } else if constexpr (O16) {
     uint32_t x[V / 2];
 #pragma unroll
@@ -282,21 +433,22 @@ void (*combine_for(bool y16, bool o16))(CombineParams) {
   return o16 ? combine_kernel<false, true, V> : combine_kernel<false, false, V>;
 }
 
-template <int PER>
-cudaError_t launch_best(const PlanParams &p, cudaStream_t s) {
-  return launch_after(best_kernel<PER>, (p.T + kBestThreads / 32 - 1) / (kBestThreads / 32), kBestThreads, 0, s, p);
-}
+constexpr int64_t kFewTokens = 32;      // what one CTA plans
 
-template <int PER, bool CLUSTER>
-cudaError_t launch_sort(const PlanParams &p, cudaStream_t s) {
-  const size_t smem = (size_t)(kSortWarps + 1) * p.E * sizeof(uint32_t);
-  auto kern = sort_kernel<PER, CLUSTER>;
-  if (smem > 48 * 1024 - 512) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+template <int LANES, int PER>
+cudaError_t launch_sort(PlanParams p, int ctas, cudaStream_t s) {
+  p.tokens = (p.T + ctas - 1) / ctas;
+  // words of 32 bits and sums of 16, as far as 160 KB of shared memory go
+  const int64_t fit = 160 * 1024 / (6 * p.E), blocks = (p.tokens + 31) / 32;
+  p.blocks = (int)(blocks < fit ? blocks : fit);
+  if (p.blocks > kSortBlocks) p.blocks = kSortBlocks;
+  const size_t smem = (size_t)6 * p.blocks * p.E;
+  auto kern = sort_kernel<LANES, PER>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(CLUSTER ? kSortCluster : 1);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kSortThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -304,22 +456,22 @@ cudaError_t launch_sort(const PlanParams &p, cudaStream_t s) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim = {kSortCluster, 1, 1};
+  at[1].val.clusterDim = {(unsigned)ctas, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = CLUSTER ? 2 : 1;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// PER: experts of a lane where 32 lanes have a token.
 template <int PER>
 cudaError_t launch_plan(PlanParams p, cudaStream_t s) {
-  if (p.T <= 2 * kSortWarps) {
-    p.per_warp = (p.T + kSortWarps - 1) / kSortWarps;
-    return launch_sort<PER, false>(p, s);
-  }
-  const cudaError_t e = launch_best<PER>(p, s);
-  if (e != cudaSuccess) return e;
-  p.per_warp = (p.T + kSortWarps * kSortCluster - 1) / (kSortWarps * kSortCluster);
-  return launch_sort<0, true>(p, s);
+  constexpr int LANES = PER <= 8 ? 8 : 32, MANY = 32 / LANES * PER;      // experts of a lane where many tokens are planned
+  const int size = p.bf16 ? 2 : 4, per = p.T <= kFewTokens ? PER : MANY;
+  p.whole = per % 4 == 0 && p.E % per == 0 && reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.stride * size % 16 == 0;
+  if (p.T <= kFewTokens) return launch_sort<32, PER>(p, 1, s);
+  constexpr int TOKENS = kBestThreads / LANES;
+  const cudaError_t e = launch_after(best_kernel<LANES, MANY>, (p.T + TOKENS - 1) / TOKENS, kBestThreads, 0, s, p);
+  return e != cudaSuccess ? e : launch_sort<0, 0>(p, kSortCluster, s);
 }
 
 }  // namespace
@@ -329,12 +481,11 @@ cudaError_t launch_moe_plan(const MoePlanArgs &a, cudaStream_t s) {
   p.logits = a.logits, p.stride = a.stride, p.T = a.T, p.E = (int)a.E, p.k = (int)a.k;
   p.bf16 = a.bf16, p.normalize = a.normalize;
   p.experts = a.experts, p.weights = a.weights, p.places = a.places, p.starts = a.starts, p.counts = a.counts;
-  const int per = (p.E + 31) / 32;
-  if (per <= 1) return launch_plan<1>(p, s);
-  if (per <= 2) return launch_plan<2>(p, s);
-  if (per <= 4) return launch_plan<4>(p, s);
-  if (per <= 8) return launch_plan<8>(p, s);
-  if (per <= 16) return launch_plan<16>(p, s);
+  if (p.E <= 32) return launch_plan<1>(p, s);
+  if (p.E <= 64) return launch_plan<2>(p, s);
+  if (p.E <= 128) return launch_plan<4>(p, s);
+  if (p.E <= 256) return launch_plan<8>(p, s);
+  if (p.E <= 512) return launch_plan<16>(p, s);
   return launch_plan<32>(p, s);
 }
 
@@ -345,11 +496,12 @@ cudaError_t launch_moe_combine(const MoeCombineArgs &a, cudaStream_t s) {
   // whole 16-byte words on both sides (8 elements a thread where one of them is bfloat16)
   const int v = a.y_bf16 || a.out_bf16 ? 8 : 4;
   const bool wide = a.N % v == 0;
-  p.pieces = (a.N + kCombineThreads * (wide ? v : 1) - 1) / (kCombineThreads * (wide ? v : 1));
-  if (p.T * p.pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const int64_t each = kCombineThreads * (wide ? v : 4), pieces = (a.N + each - 1) / each;
+  if (p.T * pieces > 0x7FFFFFFF) return cudaErrorInvalidValue;       // (more of out than there is memory)
+  p.pieces = Divisor((uint32_t)pieces);
   auto kern = !wide ? combine_for<1>(a.y_bf16, a.out_bf16)
               : v == 8 ? combine_for<8>(a.y_bf16, a.out_bf16) : combine_kernel<false, false, 4>;
-  return launch_after(kern, p.T * p.pieces, kCombineThreads, 0, s, p);
+  return launch_after(kern, p.T * pieces, kCombineThreads, 0, s, p);
 }
 
 }  // namespace qmm

@@ -49,14 +49,13 @@ constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
-constexpr int TMEM_COLS = 512;
 
 struct Params {
   const uint8_t *xs, *ws;
   const int32_t *starts, *counts;          // null: one matrix, M rows
   void *y;
   int64_t M, N;                            // rows of x, rows of a matrix
-  int64_t n_tiles;
+  int n_tiles;
   int64_t w_scale_bytes;                   // of a matrix
   int k_tiles, k_stages, k_steps;          // scale tiles of a row, stages and MMAs along K
   int experts;
@@ -115,10 +114,12 @@ __device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1
 
 // TS: tokens of a tile.
 template <bool GATED, bool BF16, int TS>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   constexpr int TWO = GATED ? 2 : 1;
-  constexpr int BUFS = 2 * TWO * TS + 2 * (8 * TWO + 16) <= TMEM_COLS ? 2 : 1;      // accumulators that TMEM holds
+  constexpr int SF_COLS = 2 * (8 * TWO + 16);                             // of scales: two places by turns
+  constexpr int BUFS = 2 * TWO * TS + SF_COLS <= 512 ? 2 : 1;             // accumulators that TMEM holds
+  constexpr int TMEM_COLS = BUFS * TWO * TS + SF_COLS <= 256 ? 256 : 512; // (256: room for the next call's)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_addr(smem);
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint32_t *fine = reinterpret_cast<uint32_t *>(tail + 8);       // [split]: that CTA's part is whole
   const WaitCtl ctl{abort_flag, &g_mx4_status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = p.split > 1 ? (int)cluster_ctarank() : 0;
+  const int rank = TS == 64 && p.split > 1 ? (int)cluster_ctarank() : 0, split_log = TS == 64 ? __ffs(p.split) - 1 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; s++) {
@@ -155,6 +156,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&tmap_w);
   }
   if (warp == 1) tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
+  if (TS == 64 && warp == 0 && !p.starts && p.M <= TS) {
+    // the weights of the first item begin to move into L2 (where later writes reach them, too) before the kernel before has ended
+    const int nt = blockIdx.x >> split_log;
+    const int k0 = (int)((int64_t)p.k_stages * rank >> split_log), k1 = (int)((int64_t)p.k_stages * (rank + 1) >> split_log);
+    if (lane < TWO * p.stages && k0 + lane / TWO < k1)
+      tma_prefetch_2d(&tmap_w, (k0 + lane / TWO) * (BK / 2), (int)((lane % TWO) * p.N + (int64_t)nt * BM));
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (warp == 0) {
@@ -184,25 +192,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (p.split > 1) cluster_sync();             // (no CTA writes into one that has not begun)
+  if (TS == 64 && p.split > 1) cluster_arrive();
 
-  const int64_t items = (int64_t)before[p.experts] * p.n_tiles;
-  const int64_t first = p.split > 1 ? blockIdx.x / p.split : blockIdx.x, step = p.split > 1 ? gridDim.x / p.split : gridDim.x;
+  const int items = before[p.experts] * p.n_tiles;
+  const int first = blockIdx.x >> split_log, step = gridDim.x >> split_log;
   // this CTA's stages of K
-  const int ks0 = (int)((int64_t)p.k_stages * rank / p.split), ks1 = (int)((int64_t)p.k_stages * (rank + 1) / p.split);
+  const int ks0 = (int)((int64_t)p.k_stages * rank >> split_log), ks1 = (int)((int64_t)p.k_stages * (rank + 1) >> split_log);
 
-  auto item_at = [&](int64_t i) {
+  auto item_at = [&](int i) {
     Item it;
     int lo = 0, hi = p.experts;                // the last expert whose items begin at or before i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((int64_t)before[mid] * p.n_tiles <= i) lo = mid; else hi = mid;
+      if (before[mid] * p.n_tiles <= i) lo = mid; else hi = mid;
     }
-    const int64_t tiles = before[lo + 1] - before[lo], j = i - (int64_t)before[lo] * p.n_tiles;
-    const int64_t nt = j / tiles;
-    const int m0 = (int)(j - nt * tiles) * TS;
+    const int tiles = before[lo + 1] - before[lo], j = i - before[lo] * p.n_tiles;
+    const int nt = j / tiles, m0 = (j - nt * tiles) * TS;
     it.expert = lo;
-    it.n0 = nt * BM;
+    it.n0 = (int64_t)nt * BM;
     it.row = (int64_t)starts[lo] + m0;
     it.rows = min(counts[lo] - m0, TS);
     return it;
@@ -214,9 +221,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto uniform64 = [&](uint64_t v) { return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v); };
   Ring ring;                                   // (of the copying and the issuing warp)
   int issued = 0;                              // stages so far
+  int ready = 0;                               // stages known to have landed
   int local = 0;                               // items so far
   bool ok = true;
-  for (int64_t i = first; i < items; i += step, local++) {
+  for (int i = first; i < items; i += step, local++) {
     const Item it = item_at(i);
     const int buf = local & (BUFS - 1);
     const uint32_t use = (uint32_t)(BUFS == 2 ? local >> 1 : local) & 1;
@@ -232,11 +240,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                       (it.n0 >> 7) * p.k_tiles * kMxTileBytes);
         const uint64_t xs = uniform64(reinterpret_cast<uint64_t>(p.xs) + (it.row >> 7) * p.k_tiles * kMxTileBytes);
         const uint32_t two_tiles = uniform(sf_tiles == 2), box_bytes = uniform(p.box * (BK / 2));
+        const uint32_t base0 = uniform(sbase), full0 = uniform(full(0)), stage_bytes = uniform(l.stage);
         const uint32_t each = l.a + boxes * box_bytes, sfs = TWO + 1 + two_tiles;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded(empty(ring.s), ring.ph ^ 1, ctl))) { ok = false; break; }
-          const uint32_t base = uniform(sbase + ring.s * l.stage), bar = uniform(full(ring.s)), k = uniform(ks);
-          const uint32_t sf = uniform(min(2, p.k_tiles - 2 * ks)) * kMxTileBytes;
+          const uint32_t now = uniform(ring.s | (uint32_t)min(2, p.k_tiles - 2 * ks) << 4 | (uint32_t)ks << 8);
+          const uint32_t slot = now & 15, k = now >> 8, sf = (now >> 4 & 15) * kMxTileBytes;
+          const uint32_t base = base0 + slot * stage_bytes, bar = full0 + 8 * slot;
           if (elect_one()) {
             mbar_arrive_expect_tx(bar, each + sfs * sf);
 #pragma unroll
@@ -263,15 +273,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t d = uniform(tmem + buf * TWO * TS), sf0 = uniform(tmem + BUFS * TWO * TS);
         const uint32_t off = uniform(shift >> 5), two_tiles = uniform(sf_tiles == 2);
         const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
+        const uint32_t at0 = uniform(sbase >> 4), stage16 = uniform(l.stage >> 4), empty0 = uniform(empty(0));
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
-          if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
-          tc_fence_after();
+          if (ready == 0) {
+            // a lane a stage from this one on: one test (of some 150 cycles) says how many have landed
+            const int slot = ring.s + lane, wrap = slot >= p.stages;
+            const bool landed = lane < p.stages && mbar_test(full(slot - wrap * p.stages), ring.ph ^ wrap);
+            ready = __ffs(~__ballot_sync(0xFFFFFFFFu, landed)) - 1;
+            if (ready == 0) {
+              if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
+              ready = 1;
+            }
+            tc_fence_after();
+          }
+          ready--;
+          // (one reduction a stage: its slot, whether sums are there already, its MMAs)
+          const uint32_t now = uniform(ring.s | (uint32_t)(ks > ks0) << 8 | (uint32_t)min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)) << 16);
+          const uint32_t slot = now & 255, more = now >> 8 & 1, steps = now >> 16;
           // scales: by turns in two places, 8 columns a weight tile (4 a scale tile) and 16 for the tokens
-          const uint32_t sfa = uniform(sf0 + (issued & 1) * (8 * TWO + 16)), sfb = sfa + 8 * TWO;
-          const uint32_t at = uniform((sbase + ring.s * l.stage) >> 4), bar = uniform(empty(ring.s)), more = uniform(ks > ks0);
+          const uint32_t sfa = sf0 + (slot & 1) * (SF_COLS / 2), sfb = sfa + 8 * TWO;
+          const uint32_t at = at0 + slot * stage16, bar = empty0 + 8 * slot;
           const uint64_t ad = ops | at, bd = ops | (at + (l.a >> 4));
           const uint64_t sd = scales | (at + ((l.a + l.b) >> 4)), td = scales | (at + ((l.a + l.b + l.sfa) >> 4));
-          const uint32_t steps = uniform(min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)));
           if (elect_one()) {
 #pragma unroll
             for (int a = 0; a < 2; a++) {                // (two MMAs a scale tile)
@@ -319,6 +342,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_before();
         mbar_arrive(acc_empty(buf));
         if (TS == 64 && p.split > 1) {
+          if (local == 0) cluster_wait();      // (no CTA writes into one that has not begun)
           // token t of the tile belongs to rank t % split, as its row t / split
           const int sh = __ffs(p.split) - 1;
           const uint32_t mine = smem_addr(red + (rank * (TS >> sh) * TWO) * BM + r);
@@ -354,6 +378,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
     if (TS == 64 && p.split > 1) {
+      if (local == 0 && (warp < EPI_WARP0 || !ok)) cluster_wait();
       __syncthreads();                         // (every epilogue warp has sent its part, or none will)
       if (threadIdx.x < p.split) st_cluster_u32(mapa_shared(smem_addr(fine + rank), threadIdx.x), *abort_flag ? 0u : 1u);
       __syncwarp();
@@ -378,6 +403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (i + step < items) cluster_sync();    // (its neighbours read what the next item overwrites)
     }
   }
+  if (TS == 64 && p.split > 1 && local == 0) cluster_wait();
   if (warp == 0) {
     // every copy lands before this CTA's memory goes to another
     for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; j++) wait_drain(full(j % p.stages), (j / p.stages) & 1);
@@ -440,6 +466,9 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
     while (p.split < MAX_SPLIT && items * p.split * 2 <= sms && p.k_stages >= 2 * p.split) p.split *= 2;
   p.stages = (SMEM_LIMIT - layout(GATED, TS, 0, p.split, p.experts).total) / layout(GATED, TS, 0, p.split, p.experts).stage;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  // (a part of K that is shorter than the ring leaves the next call's CTAs room to begin)
+  const int part = (p.k_stages + p.split - 1) / p.split;
+  if (items * p.split <= sms && p.stages > part) p.stages = part;
   const int smem = layout(GATED, TS, p.stages, p.split, p.experts).total;
   auto kern = mx4_gemm_kernel<GATED, BF16, TS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
@@ -467,11 +496,26 @@ cudaError_t launch_type(const Mx4GemmArgs &a, const Params &p, cudaStream_t s) {
   // rows that an expert has, about
   const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
   const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
-  const int ts = rows <= 64 ? 64 : GATED || rows <= 128 ? 128 : 256;
-  const int64_t items = met * ((rows + ts - 1) / ts) * p.n_tiles;
-  const int64_t most = a.starts ? (a.M / ts + a.experts + 1) * p.n_tiles : items;
+  // Tokens of a tile.  A stage of 256 elements takes 290 ns and 0.46 ns a token (the tensor core's share, beyond the issue of
+  // its instructions), an item's end 8 ns a token, and the SMs take items in rounds: wide tiles where there are many tokens,
+  // narrow ones where they fill the SMs better.  8192 x 8192 x 8192: 543, 281, 219 and 183 us for 64, 128, 192 and 256 tokens;
+  // 1024 x 6144 x 2048: 21.3, 13.9, 12.3 and 15.1 us; 256 x 4096 x 4096: 9.1, 9.4, 10.1 and 11.1 us.
+  constexpr int WIDEST = GATED ? 128 : 256;
+  int ts = 64;
+  int64_t items = 0;
+  double cost = -1;
+  for (int t = 64; t <= WIDEST; t += 64) {
+    // (an expert's last tile is half empty on average)
+    const int64_t tiles = a.starts ? met * (rows <= t / 2 ? 1 : rows / t + 1) : (rows + t - 1) / t;
+    const int64_t rounds = (tiles * p.n_tiles + sms - 1) / sms;
+    const double c = (double)rounds * (p.k_stages * (GATED ? 2 : 1) * (290 + 0.46 * t) + 8 * t);
+    if (cost < 0 || c < cost) ts = t, cost = c, items = tiles * p.n_tiles;
+  }
+  const int64_t most = a.starts ? (a.M / ts + a.experts) * p.n_tiles : items;      // at most
+  if (most >= (int64_t)1 << 31) return cudaErrorInvalidValue;
   if (ts == 64) return launch_tile<GATED, BF16, 64>(a, p, rows <= 16 ? 16 : 64, items, most, sms, s);
   if (GATED || ts == 128) return launch_tile<GATED, BF16, 128>(a, p, 128, items, most, sms, s);
+  if (ts == 192) return launch_tile<false, BF16, 192>(a, p, 192, items, most, sms, s);
   return launch_tile<false, BF16, 256>(a, p, 256, items, most, sms, s);
 }
 
@@ -481,7 +525,7 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
   Params p{};
   p.xs = static_cast<const uint8_t *>(a.x_scales), p.ws = static_cast<const uint8_t *>(a.scales);
   p.starts = a.starts, p.counts = a.counts, p.y = a.y, p.M = a.M, p.N = a.N;
-  p.n_tiles = (a.N + BM - 1) / BM;
+  p.n_tiles = (int)((a.N + BM - 1) / BM);
   p.w_scale_bytes = mx4_scales_bytes(a.N, a.K);
   p.k_tiles = (int)mx4_k_tiles(a.K), p.k_stages = (int)((a.K + BK - 1) / BK), p.k_steps = (int)((a.K + MMA_K - 1) / MMA_K);
   p.experts = (int)a.experts;

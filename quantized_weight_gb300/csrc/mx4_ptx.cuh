@@ -32,6 +32,13 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, uint64_t src, uint32_t b
                : "memory");
 }
 
+// The box at (c0, c1) into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // Descriptor of 512 bytes in that order: no swizzle, 8 rows of 16 bytes after 8 rows.
 __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1 << 46;
@@ -52,6 +59,10 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
+
+// The two halves of a barrier of the cluster's threads, by whole warps.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 }  // namespace sm100
 }  // namespace qmm

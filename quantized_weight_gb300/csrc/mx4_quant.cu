@@ -83,10 +83,11 @@ struct QuantParams {
   const int32_t *places;
   uint32_t *codes;
   uint8_t *scales;
-  int64_t rows, K, chunks, k_tiles, units;   // units: warps' pieces of work
+  int64_t rows, K, k_tiles;
   int64_t scale_bytes;                       // of a matrix
   int64_t k, out_rows;
-  int lanes, row_tiles;                      // rows r of a tile with r % 32 < lanes exist in some tile; tiles a matrix
+  uint32_t units;                            // warps' pieces of work: of
+  Divisor chunks, lanes, row_tiles;          // chunks of a row, rows r % 32 of a tile that exist in some tile, tiles of a matrix
 };
 
 // A warp takes a chunk of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes in a row of the
@@ -96,14 +97,11 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= p.units) return;
-  const int64_t chunk = u % p.chunks;
-  u /= p.chunks;
-  const int64_t r32 = u % p.lanes;
-  u /= p.lanes;
-  const int64_t tile = u % p.row_tiles, matrix = u / p.row_tiles;
-  const int64_t row0 = tile * kMxRows + r32, col = chunk * kChunk + 8 * lane;
+  uint32_t chunk = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (chunk >= p.units) return;
+  uint32_t r32 = p.chunks.split(chunk), tile = p.lanes.split(r32);
+  const uint32_t matrix = p.row_tiles.split(tile);
+  const int64_t row0 = (int64_t)tile * kMxRows + r32, col = (int64_t)chunk * kChunk + 8 * lane;
   if (row0 >= p.rows) return;
   const bool in = col < p.K;
   Raw<BF16> raw[4];
@@ -120,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
     words[g] = scale_word(scale, lane);
     if (in && row0 + 32 * g < p.rows) p.codes[((matrix * p.rows + row0 + 32 * g) * p.K + col) >> 3] = code;
   }
-  const int64_t kt = chunk * 2 + (lane >> 4);
+  const int64_t kt = (int64_t)chunk * 2 + (lane >> 4);
   if ((lane & 15) == 0 && kt < p.k_tiles)
     *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
         make_uint4(words[0], words[1], words[2], words[3]);
@@ -132,9 +130,9 @@ __global__ void __launch_bounds__(kThreads) quantize_routed_kernel(const QuantPa
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= p.units) return;
-  const int64_t t = u / p.chunks, col0 = (u % p.chunks) * (4 * kChunk) + 8 * lane;
+  uint32_t chunk = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (chunk >= p.units) return;
+  const int64_t t = p.chunks.split(chunk), col0 = (int64_t)chunk * (4 * kChunk) + 8 * lane;
   const int mine = lane < p.k ? p.places[t * p.k + lane] : -1;
   Raw<BF16> raw[4];
 #pragma unroll
@@ -166,28 +164,34 @@ struct DequantParams {
   const uint32_t *codes;
   const uint8_t *scales;
   float *w;
-  int64_t rows, K8, words, k_tiles, scale_bytes;   // K8: words a row; words: of all matrices
+  int64_t rows, k_tiles, scale_bytes;
+  int64_t words, first;            // words of codes of all matrices; a launch's first row
+  Divisor k8, per_matrix;          // words of a row; rows of a matrix
 };
 
 constexpr int kWordsAThread = 4;
 
+// A thread takes words 256 apart; `first` rows come before the launch's.
 __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantParams p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t first = (int64_t)blockIdx.x * (kThreads * kWordsAThread) + threadIdx.x;
+  const uint32_t t0 = blockIdx.x * (kThreads * kWordsAThread) + threadIdx.x;
   uint32_t code[kWordsAThread], scale[kWordsAThread];
+  const int64_t base = p.first * p.k8.d;
 #pragma unroll
   for (int i = 0; i < kWordsAThread; i++) {
-    const int64_t at = first + i * kThreads;
+    uint32_t at = t0 + i * kThreads;
     code[i] = scale[i] = 0;
-    if (at >= p.words) continue;
-    code[i] = __ldcs(p.codes + at);
-    const int64_t r = at / p.K8, block = (at - r * p.K8) >> 2, matrix = r / p.rows;
-    scale[i] = p.scales[matrix * p.scale_bytes + mx4_scale_word(r - matrix * p.rows, block >> 2, p.k_tiles) + (block & 3)];
+    if (base + at >= p.words) continue;
+    code[i] = __ldcs(p.codes + base + at);
+    uint32_t r = (uint32_t)p.first + p.k8.split(at);     // (at is then the word of its row)
+    const int64_t matrix = p.per_matrix.split(r);
+    const uint32_t block = at >> 2;
+    scale[i] = p.scales[matrix * p.scale_bytes + mx4_scale_word(r, block >> 2, p.k_tiles) + (block & 3)];
   }
 #pragma unroll
   for (int i = 0; i < kWordsAThread; i++) {
-    const int64_t at = first + i * kThreads;
+    const int64_t at = base + t0 + i * kThreads;
     if (at >= p.words) break;
     const float s = mx4_scale(scale[i]);
     float v[8];
@@ -211,17 +215,19 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
   p.codes = static_cast<uint32_t *>(a.codes), p.scales = static_cast<uint8_t *>(a.scales);
   p.rows = a.rows, p.K = a.K, p.k_tiles = mx4_k_tiles(a.K), p.scale_bytes = mx4_scales_bytes(a.rows, a.K);
   p.k = a.k, p.out_rows = a.out_rows;
+  int64_t units;
   if (a.places) {
-    p.chunks = (a.K + 4 * kChunk - 1) / (4 * kChunk);
-    p.units = a.rows * p.chunks;
+    p.chunks = Divisor((uint32_t)((a.K + 4 * kChunk - 1) / (4 * kChunk)));
+    units = a.rows * p.chunks.d;
   } else {
-    p.chunks = (a.K + kChunk - 1) / kChunk;
-    p.lanes = a.rows < 32 ? (int)a.rows : 32;
-    p.row_tiles = (int)((a.rows + kMxRows - 1) / kMxRows);
-    p.units = a.matrices * p.row_tiles * p.lanes * p.chunks;
+    p.chunks = Divisor((uint32_t)((a.K + kChunk - 1) / kChunk));
+    p.lanes = Divisor(a.rows < 32 ? (uint32_t)a.rows : 32);
+    p.row_tiles = Divisor((uint32_t)((a.rows + kMxRows - 1) / kMxRows));
+    units = a.matrices * p.row_tiles.d * p.lanes.d * p.chunks.d;
   }
-  const int64_t grid = (p.units + kWarps - 1) / kWarps;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;      // (more than a TB of codes)
+  p.units = (uint32_t)units;
+  const int64_t grid = (units + kWarps - 1) / kWarps;
   auto kern = a.places ? (a.bf16 ? quantize_routed_kernel<true> : quantize_routed_kernel<false>)
                        : (a.bf16 ? quantize_kernel<true> : quantize_kernel<false>);
   return launch_after(kern, grid, kThreads, 0, s, p);
@@ -231,11 +237,20 @@ cudaError_t launch_mx4_dequant(const void *codes, const void *scales, float *w, 
                                cudaStream_t s) {
   DequantParams p{};
   p.codes = static_cast<const uint32_t *>(codes), p.scales = static_cast<const uint8_t *>(scales), p.w = w;
-  p.rows = rows, p.K8 = K / 8, p.words = matrices * rows * p.K8;
+  p.rows = rows, p.words = matrices * rows * (K / 8);
+  p.k8 = Divisor((uint32_t)(K / 8)), p.per_matrix = Divisor((uint32_t)rows);
   p.k_tiles = mx4_k_tiles(K), p.scale_bytes = mx4_scales_bytes(rows, K);
-  const int64_t grid = (p.words + kThreads * kWordsAThread - 1) / (kThreads * kWordsAThread);
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  return launch_after(dequant_kernel, grid, kThreads, 0, s, p);
+  // rows whose words are counted in 31 bits, a launch
+  constexpr int64_t BLOCK = kThreads * kWordsAThread;
+  const int64_t most = (0x7FFFFFFF - BLOCK) / (K / 8);
+  for (; p.first < matrices * rows; p.first += most) {
+    const int64_t left = matrices * rows - p.first, words = (left < most ? left : most) * (K / 8);
+    DequantParams q = p;
+    q.words = p.first * (K / 8) + words;
+    const cudaError_t e = launch_after(dequant_kernel, (words + BLOCK - 1) / BLOCK, kThreads, 0, s, q);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace qmm

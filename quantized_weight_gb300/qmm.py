@@ -454,8 +454,16 @@ def kv_attend(q, cache, block_table, lens, page, group, workspace, cu=None, max_
 
 
 # ---------------------------------------------------------------- microscaled 4-bit products and experts
+#
+# As for the cache calls, one test that a good argument passes comes first; what the call itself has made is not tested.
 
+_F32 = torch.float32
+_U8 = torch.uint8
 _MX_DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+try:
+    _device = torch._C._cuda_getDevice
+except AttributeError:
+    _device = torch.cuda.current_device
 
 
 def _mx_dtype(dtype) -> int:
@@ -469,8 +477,8 @@ def _here(t, name, dtype, shape) -> int:
     """Pointer of a contiguous tensor of the given type and shape on the current device (where the kernels run)."""
     if not (t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous()):
         _need(t, name, dtype, shape)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != _device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_device()}")
     return t.data_ptr()
 
 
@@ -482,30 +490,25 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _mx_x(x):
-    """(strides between matrices and rows) of x [..., rows, K] on the current device, whose rows are contiguous and whose
-    leading dimensions are one after the other."""
+def _mx_rows(x, name) -> int:
+    """Stride between the rows of x [..., rows, K] on the current device, whose rows are contiguous."""
     if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"x is on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.get_device() != _device():
+        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{_device()}")
     if x.dim() < 2:
-        raise ValueError(f"x must be [..., rows, K], got {tuple(x.shape)}")
-    if x.dim() > 3:
-        x = x.view(-1, *x.shape[-2:])
+        raise ValueError(f"{name} must have rows, got {tuple(x.shape)}")
     strides = x.stride()
     if strides[-1] != 1 and x.shape[-1] > 1 and x.numel() > 0:
-        raise ValueError("x must be contiguous in its last dimension")
-    row = strides[-2] if x.shape[-2] > 1 else 0                       # a lone row or matrix has no stride to keep
-    return (strides[0] if x.dim() == 3 and x.shape[0] > 1 else 0), row
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return strides[-2] if x.shape[-2] > 1 else 0                      # a lone row has no stride to keep
 
 
 def mx4_scales_size(rows, K) -> int:
     """Bytes of the scales of a matrix [rows, K]."""
-    n = int(lib().qmm_mx4_scales_size(rows, K))
-    if n == 0 and (rows < 0 or K < 0 or K % 32 != 0 or rows * K != 0):
+    if rows < 0 or K < 0 or K % 32 != 0 or rows >= 1 << 31 or K >= 1 << 31:
         raise ValueError(f"no microscaled matrix of {rows} rows of {K}: K is a multiple of 32, both are below 2**31")
-    return n
+    return ((rows + 127) // 128) * ((K + 127) // 128) * 512
 
 
 def mx4_scales(plain) -> torch.Tensor:
@@ -521,24 +524,32 @@ def mx4_scales(plain) -> torch.Tensor:
 
 def _mx_matrix(codes, scales, name, lead):
     """(rows, K, pointers) of a microscaled matrix [*lead, rows, K / 8] and its scales."""
-    if codes.dim() != len(lead) + 2 or codes.shape[:-2] != lead:
-        raise ValueError(f"{name} must be [{', '.join(map(str, (*lead, 'rows', 'K / 8')))}], got {tuple(codes.shape)}")
-    rows, K = codes.shape[-2], codes.shape[-1] * 8
-    pc = _here(codes, name, torch.int32, codes.shape)
-    return rows, K, pc, _here(scales, name + "'s scales", torch.uint8, (*lead, mx4_scales_size(rows, K)))
+    shape = codes.shape
+    if len(shape) != len(lead) + 2 or shape[:-2] != lead:
+        raise ValueError(f"{name} must be [{', '.join(map(str, (*lead, 'rows', 'K / 8')))}], got {tuple(shape)}")
+    rows, K = shape[-2], shape[-1] * 8
+    pc = _here(codes, name, _I32, shape)
+    return rows, K, pc, _here(scales, "scales", _U8, (*lead, mx4_scales_size(rows, K)))
 
 
 def mx4_quantize(x, out=None, stream=None):
     """float32 or bfloat16 x [..., rows, K] to microscaled 4-bit (codes int32 [..., rows, K / 8], scales uint8 [..., bytes])."""
-    dt = _mx_dtype(x.dtype)
-    sm, sr = _mx_x(x)
-    lead, rows, K = x.shape[:-2], x.shape[-2], x.shape[-1]
-    size = mx4_scales_size(rows, K)
+    dt, row = _mx_dtype(x.dtype), _mx_rows(x, "x")
+    if x.dim() == 2:
+        (rows, K), n, matrix = x.shape, 1, 0
+        codes, scales = (rows, K // 8), (mx4_scales_size(rows, K),)
+    else:
+        (*lead, rows, K), n = x.shape, x.shape[:-2].numel()
+        if len(lead) > 1:
+            x = x.view(n, rows, K)                                    # (leading dimensions one after the other)
+        matrix = x.stride(0) if n > 1 else 0
+        codes, scales = (*lead, rows, K // 8), (*lead, mx4_scales_size(rows, K))
     if out is None:
-        out = _new((*lead, rows, K // 8), torch.int32, x.device, stream), _new((*lead, size), torch.uint8, x.device, stream)
-    pc, ps = _here(out[0], "codes", torch.int32, (*lead, rows, K // 8)), _here(out[1], "scales", torch.uint8, (*lead, size))
-    _call("qmm_mx4_quantize", lib().qmm_mx4_quantize(x.data_ptr(), dt, sm, sr, pc, ps, lead.numel(), rows, K,
-                                                     _stream(stream)))
+        out = _new(codes, _I32, x.device, stream), _new(scales, _U8, x.device, stream)
+        pc, ps = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        pc, ps = _here(out[0], "codes", _I32, codes), _here(out[1], "scales", _U8, scales)
+    _call("qmm_mx4_quantize", lib().qmm_mx4_quantize(x.data_ptr(), dt, matrix, row, pc, ps, n, rows, K, _stream(stream)))
     return out
 
 
@@ -546,25 +557,34 @@ def mx4_dequant(codes, scales, out=None, stream=None) -> torch.Tensor:
     """The float32 values [..., rows, K] of a microscaled matrix."""
     lead = codes.shape[:-2]
     rows, K, pc, ps = _mx_matrix(codes, scales, "codes", lead)
+    shape = (*lead, rows, K)
     if out is None:
-        out = _new((*lead, rows, K), torch.float32, codes.device, stream)
-    po = _here(out, "out", torch.float32, (*lead, rows, K))
+        out = _new(shape, _F32, codes.device, stream)
+        po = out.data_ptr()
+    else:
+        po = _here(out, "out", _F32, shape)
     _call("qmm_mx4_dequant", lib().qmm_mx4_dequant(pc, ps, po, lead.numel(), rows, K, _stream(stream)))
     return out
 
 
+def _mx_out(out, shape, dtype, device, stream):
+    """(output, its type's number, its pointer)."""
+    if out is None:
+        dt = _mx_dtype(dtype)
+        out = _new(shape, dtype, device, stream)
+        return out, dt, out.data_ptr()
+    return out, _mx_dtype(out.dtype), _here(out, "out", out.dtype, shape)
+
+
 def mx4_gemm(x_codes, x_scales, codes, scales, gated=False, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """y [M, N] = x . w^T of microscaled x [M, K] and w [N, K], float32 or bfloat16; gated: codes and scales hold two matrices
-    [2, N, K], and y = silu(x . g^T) * (x . u^T)."""
+    [2, N, K], and y = silu(x . g^T) * (x . u^T).  With out, dtype is out's."""
     M, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes", ())
     N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (2,) if gated else ())
     if KW != K:
         raise ValueError(f"x has rows of {K}, the weights of {KW}")
-    if out is None:
-        out = _new((M, N), dtype, x_codes.device, stream)
-    dt = _mx_dtype(out.dtype)
-    po = _here(out, "out", out.dtype, (M, N))
-    _call("qmm_mx4_gemm", lib().qmm_mx4_gemm(px, pxs, pc, ps, po, dt, int(gated), M, N, K, _stream(stream)))
+    out, dt, po = _mx_out(out, (M, N), dtype, x_codes.device, stream)
+    _call("qmm_mx4_gemm", lib().qmm_mx4_gemm(px, pxs, pc, ps, po, dt, gated, M, N, K, _stream(stream)))
     return out
 
 
@@ -581,36 +601,35 @@ def moe_plan(logits, k, normalize=True, out=None, stream=None):
     weights float32 [T, k], places int32 [T, k], starts int32 [E], counts int32 [E]).  Expert e's rows are starts[e] ..
     starts[e] + counts[e] - 1 of moe_rows(T, E, k); places says which is whose.  weights are the softmax over the chosen
     experts (normalize) or over all."""
-    dt = _mx_dtype(logits.dtype)
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
+    dt, row = _mx_dtype(logits.dtype), _mx_rows(logits, "logits")
     T, E = logits.shape
-    _, row = _mx_x(logits)
     if out is None:
-        out = (_new((T, k), _I32, logits.device, stream), _new((T, k), torch.float32, logits.device, stream),
-               _new((T, k), _I32, logits.device, stream), _new((E,), _I32, logits.device, stream),
-               _new((E,), _I32, logits.device, stream))
-    names = (("experts", _I32, (T, k)), ("weights", torch.float32, (T, k)), ("places", _I32, (T, k)), ("starts", _I32, (E,)),
-             ("counts", _I32, (E,)))
-    ptrs = [_here(t, *n) for t, n in zip(out, names)]
-    _call("qmm_moe_plan", lib().qmm_moe_plan(logits.data_ptr(), dt, row, T, E, k, int(normalize), *ptrs, _stream(stream)))
+        device, tk = logits.device, (T, k)
+        out = (_new(tk, _I32, device, stream), _new(tk, _F32, device, stream), _new(tk, _I32, device, stream),
+               _new((E,), _I32, device, stream), _new((E,), _I32, device, stream))
+        pe, pw, pp, ps, pc = [t.data_ptr() for t in out]
+    else:
+        pe, pw, pp, ps, pc = [_here(t, *n) for t, n in zip(out, (
+            ("experts", _I32, (T, k)), ("weights", _F32, (T, k)), ("places", _I32, (T, k)), ("starts", _I32, (E,)),
+            ("counts", _I32, (E,))))]
+    _call("qmm_moe_plan", lib().qmm_moe_plan(logits.data_ptr(), dt, row, T, E, k, normalize, pe, pw, pp, ps, pc,
+                                             _stream(stream)))
     return out
 
 
 def moe_quantize(x, places, rows, out=None, stream=None):
     """mx4_quantize of x [T, K], each token's row to its places [T, k]: (codes int32 [rows, K / 8], scales).  Other rows are
     left alone (without `out`: as memory happens to be; no product of another row reads them)."""
-    dt = _mx_dtype(x.dtype)
-    if x.dim() != 2:
-        raise ValueError(f"x must be [T, K], got {tuple(x.shape)}")
-    _, row = _mx_x(x)
+    dt, row = _mx_dtype(x.dtype), _mx_rows(x, "x")
     T, K = x.shape
     k = places.shape[-1]
     pp = _here(places, "places", _I32, (T, k))
     size = mx4_scales_size(rows, K)
     if out is None:
-        out = _new((rows, K // 8), torch.int32, x.device, stream), _new((size,), torch.uint8, x.device, stream)
-    pc, ps = _here(out[0], "codes", torch.int32, (rows, K // 8)), _here(out[1], "scales", torch.uint8, (size,))
+        out = _new((rows, K // 8), _I32, x.device, stream), _new((size,), _U8, x.device, stream)
+        pc, ps = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        pc, ps = _here(out[0], "codes", _I32, (rows, K // 8)), _here(out[1], "scales", _U8, (size,))
     _call("qmm_moe_quantize", lib().qmm_moe_quantize(x.data_ptr(), dt, row, pp, pc, ps, T, k, rows, K, _stream(stream)))
     return out
 
@@ -626,27 +645,21 @@ def moe_gemm(x_codes, x_scales, codes, scales, starts, counts, routed=None, gate
     if KW != K:
         raise ValueError(f"x has rows of {K}, the weights of {KW}")
     pst, pco = _here(starts, "starts", _I32, (E,)), _here(counts, "counts", _I32, (E,))
-    if out is None:
-        out = _new((R, N), dtype, x_codes.device, stream)
-    dt = _mx_dtype(out.dtype)
-    po = _here(out, "out", out.dtype, (R, N))
-    _call("qmm_moe_gemm", lib().qmm_moe_gemm(px, pxs, pc, ps, pst, pco, po, dt, int(gated), R if routed is None else routed,
-                                             R, E, N, K, _stream(stream)))
+    out, dt, po = _mx_out(out, (R, N), dtype, x_codes.device, stream)
+    _call("qmm_moe_gemm", lib().qmm_moe_gemm(px, pxs, pc, ps, pst, pco, po, dt, gated, R if routed is None else routed, R, E,
+                                             N, K, _stream(stream)))
     return out
 
 
 def moe_combine(y, weights, places, dtype=None, out=None, stream=None) -> torch.Tensor:
     """out[t] = sum_j weights[t, j] * y[places[t, j]] of y [R, N]; weights None: all 1.  dtype defaults to y's."""
-    dt = _mx_dtype(y.dtype)
-    if y.dim() != 2 or places.dim() != 2:
-        raise ValueError(f"y must be [R, N] and places [T, k], got {tuple(y.shape)} and {tuple(places.shape)}")
-    (R, N), (T, k) = y.shape, places.shape
-    py, pp = _here(y, "y", y.dtype, y.shape), _here(places, "places", _I32, (T, k))
-    pw = None if weights is None else _here(weights, "weights", torch.float32, (T, k))
-    if out is None:
-        out = _new((T, N), y.dtype if dtype is None else dtype, y.device, stream)
-    do = _mx_dtype(out.dtype)
-    po = _here(out, "out", out.dtype, (T, N))
+    shape, tk, ydtype = y.shape, places.shape, y.dtype
+    if len(shape) != 2 or len(tk) != 2:
+        raise ValueError(f"y must be [R, N] and places [T, k], got {tuple(shape)} and {tuple(tk)}")
+    dt, py, pp = _mx_dtype(ydtype), _here(y, "y", ydtype, shape), _here(places, "places", _I32, tk)
+    pw = None if weights is None else _here(weights, "weights", _F32, tk)
+    (R, N), (T, k) = shape, tk
+    out, do, po = _mx_out(out, (T, N), ydtype if dtype is None else dtype, y.device, stream)
     _call("qmm_moe_combine", lib().qmm_moe_combine(py, dt, pw, pp, po, do, T, k, R, N, _stream(stream)))
     return out
 

@@ -76,6 +76,7 @@ def test_gemm(L):
     assert gemm(L, dtype=7) == UNSUP
     assert gemm(L, K=0) == SHAPE and gemm(L, K=33) == SHAPE and gemm(L, M=-1) == SHAPE and gemm(L, N=BIG) == SHAPE
     assert gemm(L, N=1 << 30, x=None) == ARG and gemm(L, N=1 << 30, gated=1) == SHAPE     # two matrices
+    assert gemm(L, M=BIG - 1, N=63 * 128, x=None) == ARG and gemm(L, M=BIG - 1, N=64 * 128) == SHAPE     # tiles in 32 bits
     for name in ("x", "xs", "c", "s", "y"):
         assert gemm(L, **{name: None}) == ARG and gemm(L, **{name: MIS}) == ALIGN
     assert gemm(L, M=0) == OK and gemm(L, N=0) == OK
@@ -91,6 +92,7 @@ def test_experts(L):
         assert experts(L, **{name: None}) == ARG and experts(L, **{name: MIS}) == ALIGN
     for name in ("st", "n"):
         assert experts(L, **{name: None}) == ARG and experts(L, **{name: ODD}) == ALIGN
+    assert experts(L, R=BIG - 1, N=63 * 128, x=None) == ARG and experts(L, R=BIG - 1, N=64 * 128) == SHAPE
     assert experts(L, R=0) == OK and experts(L, N=0) == OK
 
 
