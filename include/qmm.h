@@ -444,6 +444,13 @@ int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_
                  int64_t E, int64_t N, int64_t K, qmm_stream_t stream);
 
 /*
+ * qmm_mx4_gemm_tile -- which kernel takes such a call on the current device: 64, 128, 192 or 256 tokens of a tile, plus 1024
+ *   where a pair of CTAs shares it; or an error's status.  E == 0: qmm_mx4_gemm (M rows of x; routed is not looked at), else
+ *   qmm_moe_gemm (M its R).
+ */
+int qmm_mx4_gemm_tile(int gated, int64_t routed, int64_t M, int64_t E, int64_t N, int64_t K);
+
+/*
  * qmm_moe_combine -- out[t, n] = sum_j weights[t, j] * y[places[t, j], n], y [R, N] of y_dtype, out [T, N] of out_dtype, sums
  *   float32 in the order of j.  weights == NULL: all 1.  A place outside [0, R) is left out, whatever its weight.
  */

@@ -416,6 +416,19 @@ int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_
   return cuda_status(qmm::launch_mx4_gemm(a, stream));
 }
 
+int qmm_mx4_gemm_tile(int gated, int64_t routed, int64_t M, int64_t E, int64_t N, int64_t K) {
+  if (E < 0 || E > qmm::kMoeMaxExperts || routed < 0 || routed >= kMaxDim || K < 32) return QMM_ERR_SHAPE;
+  const int64_t matrices = E > 0 ? E : 1;
+  int st = check_mx4(1, M, K);
+  if (st == QMM_OK) st = check_mx4(gated ? 2 * matrices : matrices, N, K);
+  if (st != QMM_OK) return st;
+  if (!mx4_tiles_ok(M, matrices, N)) return QMM_ERR_SHAPE;
+  qmm::Mx4GemmArgs a{};
+  static const int32_t some = 0;
+  a.M = M, a.N = N, a.K = K, a.experts = matrices, a.routed = routed, a.gated = gated != 0, a.starts = E > 0 ? &some : nullptr;
+  return qmm::mx4_gemm_tile(a);
+}
+
 int qmm_moe_combine(const void *y, int y_dtype, const float *weights, const int32_t *places, void *out, int out_dtype,
                     int64_t T, int64_t k, int64_t R, int64_t N, qmm_stream_t stream) {
   if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return QMM_ERR_UNSUPPORTED;

@@ -55,7 +55,7 @@ struct Params {
   const int32_t *starts, *counts;          // null: one matrix, M rows
   void *y;
   int64_t M, N;                            // rows of x, rows of a matrix
-  int n_tiles;
+  int n_tiles, most_tiles;                 // weight tiles of 128 rows (a pair: 256) of a matrix, token tiles at most
   int64_t w_scale_bytes;                   // of a matrix
   int k_tiles, k_stages, k_steps;          // scale tiles of a row, stages and MMAs along K
   int experts;
@@ -68,11 +68,11 @@ struct Layout {                            // of a CTA's shared memory
   int a, b, sfa, sfb, stage;               // bytes: weights, tokens, scales, all
   int ring, red, list, bars, total;
 };
-__host__ __device__ inline Layout layout(bool gated, int ts, int stages, int split, int experts) {
+__host__ __device__ inline Layout layout(bool gated, int ts, int ctas, int stages, int split, int experts) {
   Layout l;
   const int two = gated ? 2 : 1;
   l.a = two * BM * (BK / 2);
-  l.b = ts * (BK / 2);
+  l.b = ts / ctas * (BK / 2);
   l.sfa = two * 2 * kMxTileBytes;
   l.sfb = (ts > kMxRows ? 2 : 1) * 2 * kMxTileBytes;
   l.stage = l.a + l.b + l.sfa + l.sfb;     // (multiples of 1024 bytes)
@@ -109,21 +109,33 @@ __device__ __forceinline__ void store(void *y, int64_t at, float v) {
     __stcs(static_cast<float *>(y) + at, v);
 }
 
-// silu(z) * u.  (Of a denominator beyond 2^126, z below -87, the quick division makes 0 instead of 2^-120 or less.)
-__device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1.0f + expf(-z)) * u; }
+// silu(z) * u.  For a bfloat16 result the quick exponential does, whose relative error is below |z| * 2^-23, where z is far
+// enough from 0 to make silu small.  (Of a denominator beyond 2^126, z below -87, the quick division makes 0 instead of
+// 2^-120 or less.)
+template <bool BF16>
+__device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1.0f + (BF16 ? __expf(-z) : expf(-z))) * u; }
 
-// TS: tokens of a tile.
-template <bool GATED, bool BF16, int TS>
+// wait_bounded on a barrier that another CTA arrives at.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  return wait_bounded(bar, parity, ctl) && mbar_try_wait_cluster(bar, parity);
+}
+
+// TS: tokens of a tile.  CTAS 2: a pair of CTAs has a tile of 256 weight rows, 128 each, and each half of the tokens in its
+// shared memory.
+template <bool GATED, bool BF16, int TS, int CTAS>
 __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
-    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                    const __grid_constant__ CUtensorMap tmap_xs, const __grid_constant__ CUtensorMap tmap_ws, const Params p) {
   constexpr int TWO = GATED ? 2 : 1;
+  constexpr bool PAIR = CTAS == 2, SPLITS = TS == 64 && !PAIR;
   constexpr int SF_COLS = 2 * (8 * TWO + 16);                             // of scales: two places by turns
   constexpr int BUFS = 2 * TWO * TS + SF_COLS <= 512 ? 2 : 1;             // accumulators that TMEM holds
   constexpr int TMEM_COLS = BUFS * TWO * TS + SF_COLS <= 256 ? 256 : 512; // (256: room for the next call's)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_addr(smem);
-  const Layout l = layout(GATED, TS, p.stages, p.split, p.experts);
+  const Layout l = layout(GATED, TS, CTAS, p.stages, p.split, p.experts);
   float *red = reinterpret_cast<float *>(smem + l.ring);
   int32_t *starts = reinterpret_cast<int32_t *>(smem + l.ring + l.red), *counts = starts + p.experts, *before = counts + p.experts;
   const uint32_t bars = sbase + l.ring + l.red + l.list;
@@ -138,7 +150,9 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   uint32_t *fine = reinterpret_cast<uint32_t *>(tail + 8);       // [split]: that CTA's part is whole
   const WaitCtl ctl{abort_flag, &g_mx4_status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = TS == 64 && p.split > 1 ? (int)cluster_ctarank() : 0, split_log = TS == 64 ? __ffs(p.split) - 1 : 0;
+  // the CTA of its cluster (one that splits K, or a pair)
+  const int rank = PAIR || (SPLITS && p.split > 1) ? (int)cluster_ctarank() : 0, cluster_log = PAIR ? 1 : SPLITS ? __ffs(p.split) - 1 : 0;
+  const int part = PAIR ? 0 : rank, split_log = PAIR ? 0 : cluster_log, in_pair = PAIR ? rank : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; s++) {
@@ -147,7 +161,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), EPI_THREADS);
+      mbar_init(acc_empty(b), CTAS * EPI_THREADS);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -155,11 +169,11 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     tma_prefetch_desc(&tmap_x);
     tma_prefetch_desc(&tmap_w);
   }
-  if (warp == 1) tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
-  if (TS == 64 && warp == 0 && !p.starts && p.M <= TS) {
+  if (warp == 1) tmem_alloc_for<CTAS>(smem_addr(tmem_slot), TMEM_COLS);
+  if (SPLITS && warp == 0 && !p.starts && p.M <= TS) {
     // the weights of the first item begin to move into L2 (where later writes reach them, too) before the kernel before has ended
-    const int nt = blockIdx.x >> split_log;
-    const int k0 = (int)((int64_t)p.k_stages * rank >> split_log), k1 = (int)((int64_t)p.k_stages * (rank + 1) >> split_log);
+    const int nt = blockIdx.x >> cluster_log;
+    const int k0 = (int)((int64_t)p.k_stages * part >> split_log), k1 = (int)((int64_t)p.k_stages * (part + 1) >> split_log);
     if (lane < TWO * p.stages && k0 + lane / TWO < k1)
       tma_prefetch_2d(&tmap_w, (k0 + lane / TWO) * (BK / 2), (int)((lane % TWO) * p.N + (int64_t)nt * BM));
   }
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   pdl_launch_dependents();
   if (warp == 0) {
     // the experts' rows, made to fit x, and the token tiles before each
-    int sum = 0;
+    uint32_t sum = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
       const int e = e0 + lane;
       int64_t start = 0, count = p.M;
@@ -176,15 +190,15 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
         if (start < 0 || start >= p.M || start % kMxRows != 0 || count < 0) start = 0, count = 0;
         if (count > p.M - start) count = p.M - start;
       }
-      const int tiles = e < p.experts ? (int)((count + TS - 1) / TS) : 0;
-      int at = tiles;
+      uint32_t at = e < p.experts ? (uint32_t)((count + TS - 1) / TS) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
         if (lane >= o) at += v;
       }
-      if (e < p.experts) starts[e] = (int)start, counts[e] = (int)count, before[e + 1] = sum + at;
-      sum += __shfl_sync(0xFFFFFFFFu, at, 31);
+      at = min(sum + at, (uint32_t)p.most_tiles);      // (more only where experts share rows)
+      if (e < p.experts) starts[e] = (int)start, counts[e] = (int)count, before[e + 1] = (int)at;
+      sum = __shfl_sync(0xFFFFFFFFu, at, 31);
     }
     if (lane == 0) before[0] = 0;
   }
@@ -192,13 +206,18 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (TS == 64 && p.split > 1) cluster_arrive();
+  if (PAIR)
+    cluster_sync();                            // (its barriers are waited for and arrived at by both)
+  else if (SPLITS && p.split > 1)
+    cluster_arrive();
 
   const int items = before[p.experts] * p.n_tiles;
-  const int first = blockIdx.x >> split_log, step = gridDim.x >> split_log;
+  const int first = blockIdx.x >> cluster_log, step = gridDim.x >> cluster_log;
   // this CTA's stages of K
-  const int ks0 = (int)((int64_t)p.k_stages * rank >> split_log), ks1 = (int)((int64_t)p.k_stages * (rank + 1) >> split_log);
+  const int ks0 = (int)((int64_t)p.k_stages * part >> split_log), ks1 = (int)((int64_t)p.k_stages * (part + 1) >> split_log);
 
+  // the tokens that a tile's MMAs take
+  auto tokens_of = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
   auto item_at = [&](int i) {
     Item it;
     int lo = 0, hi = p.experts;                // the last expert whose items begin at or before i
@@ -209,7 +228,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     const int tiles = before[lo + 1] - before[lo], j = i - before[lo] * p.n_tiles;
     const int nt = j / tiles, m0 = (j - nt * tiles) * TS;
     it.expert = lo;
-    it.n0 = (int64_t)nt * BM;
+    it.n0 = (int64_t)(nt * CTAS + in_pair) * BM;
     it.row = (int64_t)starts[lo] + m0;
     it.rows = min(counts[lo] - m0, TS);
     return it;
@@ -234,20 +253,39 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     if (warp == 0) {
       // -------------------------------------------------------- copies
       if (ok) {
-        const uint32_t boxes = uniform((it.rows + p.box - 1) / p.box), row = uniform((uint32_t)it.row);
+        // (a pair's second CTA has the second half of the tokens, and its weight rows may lie past the last)
+        const uint32_t boxes = PAIR ? 1 : uniform((it.rows + p.box - 1) / p.box);
+        const uint32_t row = uniform((uint32_t)it.row + in_pair * (tokens_of(it.rows) / 2));
+        const int64_t w_tile = PAIR ? min(it.n0 >> 7, (p.N - 1) >> 7) : it.n0 >> 7;
         const uint32_t w_row = uniform((uint32_t)((int64_t)it.expert * TWO * p.N + it.n0)), w_next = uniform((uint32_t)p.N);
         const uint64_t ws = uniform64(reinterpret_cast<uint64_t>(p.ws) + (int64_t)it.expert * TWO * p.w_scale_bytes +
-                                      (it.n0 >> 7) * p.k_tiles * kMxTileBytes);
+                                      w_tile * p.k_tiles * kMxTileBytes);
         const uint64_t xs = uniform64(reinterpret_cast<uint64_t>(p.xs) + (it.row >> 7) * p.k_tiles * kMxTileBytes);
         const uint32_t two_tiles = uniform(sf_tiles == 2), box_bytes = uniform(p.box * (BK / 2));
-        const uint32_t base0 = uniform(sbase), full0 = uniform(full(0)), stage_bytes = uniform(l.stage);
+        // (a pair's copies complete on the first CTA's barriers)
+        const uint32_t base0 = uniform(sbase), full0 = uniform(PAIR ? mapa_shared(full(0), 0) : full(0)), stage_bytes = uniform(l.stage);
+        const uint32_t ws_tile = uniform((uint32_t)(((int64_t)it.expert * TWO * ((p.N + 127) >> 7) + w_tile) * p.k_tiles));
+        const uint32_t ws_next = uniform((uint32_t)(((p.N + 127) >> 7) * p.k_tiles)), xs_tile = uniform((uint32_t)((it.row >> 7) * p.k_tiles));
         const uint32_t each = l.a + boxes * box_bytes, sfs = TWO + 1 + two_tiles;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded(empty(ring.s), ring.ph ^ 1, ctl))) { ok = false; break; }
           const uint32_t now = uniform(ring.s | (uint32_t)min(2, p.k_tiles - 2 * ks) << 4 | (uint32_t)ks << 8);
           const uint32_t slot = now & 15, k = now >> 8, sf = (now >> 4 & 15) * kMxTileBytes;
           const uint32_t base = base0 + slot * stage_bytes, bar = full0 + 8 * slot;
-          if (elect_one()) {
+          if (PAIR) {
+            if (elect_one()) {
+              if (in_pair == 0) mbar_arrive_expect_tx(full(0) + 8 * slot, 2 * (uint32_t)l.stage);
+#pragma unroll
+              for (int g = 0; g < TWO; g++) {
+                tma_load_2d_pair(base + g * BM * (BK / 2), &tmap_w, k * (BK / 2), w_row + g * w_next, bar);
+                tma_load_2d_pair(base + l.a + l.b + g * 2 * kMxTileBytes, &tmap_ws, 0, ws_tile + g * ws_next + 2 * k, bar);
+              }
+              tma_load_2d_pair(base + l.a, &tmap_x, k * (BK / 2), row, bar);
+#pragma unroll
+              for (int t = 0; t < (TS > kMxRows ? 2 : 1); t++)
+                tma_load_2d_pair(base + l.a + l.b + l.sfa + t * 2 * kMxTileBytes, &tmap_xs, 0, xs_tile + t * p.k_tiles + 2 * k, bar);
+            }
+          } else if (elect_one()) {
             mbar_arrive_expect_tx(bar, each + sfs * sf);
 #pragma unroll
             for (int g = 0; g < TWO; g++) {
@@ -266,16 +304,20 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- products
-      if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(acc_empty(buf), use ^ 1, ctl));
-      if (ok) {
+      if (ok && in_pair == 0)
+        ok = __all_sync(0xFFFFFFFFu, PAIR ? wait_cluster(acc_empty(buf), use ^ 1, ctl) : wait_bounded(acc_empty(buf), use ^ 1, ctl));
+      if (ok && in_pair == 0) {
         tc_fence_after();
-        const uint32_t id = uniform(idesc_mxf4(BM, (it.rows + 15) & ~15));
+        const uint32_t id = uniform(idesc_mxf4(CTAS * BM, tokens_of(it.rows)));
         const uint32_t d = uniform(tmem + buf * TWO * TS), sf0 = uniform(tmem + BUFS * TWO * TS);
         const uint32_t off = uniform(shift >> 5), two_tiles = uniform(sf_tiles == 2);
         const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
         const uint32_t at0 = uniform(sbase >> 4), stage16 = uniform(l.stage >> 4), empty0 = uniform(empty(0));
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
-          if (ready == 0) {
+          if constexpr (!SPLITS) {
+            if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
+            tc_fence_after();
+          } else if (ready == 0) {
             // a lane a stage from this one on: one test (of some 150 cycles) says how many have landed
             const int slot = ring.s + lane, wrap = slot >= p.stages;
             const bool landed = lane < p.stages && mbar_test(full(slot - wrap * p.stages), ring.ph ^ wrap);
@@ -286,7 +328,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             }
             tc_fence_after();
           }
-          ready--;
+          if constexpr (SPLITS) ready--;
           // (one reduction a stage: its slot, whether sums are there already, its MMAs)
           const uint32_t now = uniform(ring.s | (uint32_t)(ks > ks0) << 8 | (uint32_t)min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)) << 16);
           const uint32_t slot = now & 255, more = now >> 8 & 1, steps = now >> 16;
@@ -300,23 +342,23 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             for (int a = 0; a < 2; a++) {                // (two MMAs a scale tile)
               if (2 * a >= steps) break;
 #pragma unroll
-              for (int g = 0; g < TWO; g++) tmem_cp_32x16b(sfa + g * 8 + a * 4, sd + (g * 2 + a) * (kMxTileBytes / 16));
-              tmem_cp_32x16b(sfb + a * 8, td + a * (kMxTileBytes / 16));
-              if (two_tiles) tmem_cp_32x16b(sfb + a * 8 + 4, td + (2 + a) * (kMxTileBytes / 16));
+              for (int g = 0; g < TWO; g++) tmem_cp_32x16b<CTAS>(sfa + g * 8 + a * 4, sd + (g * 2 + a) * (kMxTileBytes / 16));
+              tmem_cp_32x16b<CTAS>(sfb + a * 8, td + a * (kMxTileBytes / 16));
+              if (two_tiles) tmem_cp_32x16b<CTAS>(sfb + a * 8 + 4, td + (2 + a) * (kMxTileBytes / 16));
 #pragma unroll
               for (int j = 2 * a; j < 2 * a + 2; j++) {
                 if (j >= steps) break;
 #pragma unroll
                 for (int g = 0; g < TWO; g++)
-                  umma_mxf4(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
+                  umma_mxf4<CTAS>(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
                             sfa + g * 8 + a * 4, sfb + a * 8 + off, j > 0 ? 1u : more);
               }
             }
-            umma_commit(bar);
+            commit_mxf4<CTAS>(bar);
           }
           __syncwarp();
         }
-        if (ok && elect_one()) umma_commit(acc_full(buf));
+        if (ok && elect_one()) commit_mxf4<CTAS>(acc_full(buf));
         __syncwarp();
       }
     } else {
@@ -340,12 +382,15 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
           }
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(acc_empty(buf));
-        if (TS == 64 && p.split > 1) {
+        if (in_pair == 0)
+          mbar_arrive(acc_empty(buf));
+        else
+          mbar_arrive_cluster(mapa_shared(acc_empty(buf), 0));
+        if (SPLITS && p.split > 1) {
           if (local == 0) cluster_wait();      // (no CTA writes into one that has not begun)
           // token t of the tile belongs to rank t % split, as its row t / split
           const int sh = __ffs(p.split) - 1;
-          const uint32_t mine = smem_addr(red + (rank * (TS >> sh) * TWO) * BM + r);
+          const uint32_t mine = smem_addr(red + (part * (TS >> sh) * TWO) * BM + r);
 #pragma unroll
           for (int c = 0; c < CHUNKS; c++)
 #pragma unroll
@@ -358,35 +403,36 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             }
         } else if (n < p.N) {
           auto out = [&](int c, int j) {
-            return GATED ? gate(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][TWO - 1][j])) : __uint_as_float(v[c][0][j]);
+            return GATED ? gate<BF16>(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][TWO - 1][j])) : __uint_as_float(v[c][0][j]);
           };
-          int64_t at = (it.row + c0) * p.N + n;
+          const int64_t step = p.N * (BF16 ? 2 : 4);
+          char *at = static_cast<char *>(p.y) + (it.row + c0) * step + n * (BF16 ? 2 : 4);
 #pragma unroll
           for (int c = 0; c < CHUNKS; c++) {
             if (16 * c + 16 <= left) {
 #pragma unroll
-              for (int j = 0; j < 16; j++, at += p.N) store<BF16>(p.y, at, out(c, j));
+              for (int j = 0; j < 16; j++, at += step) store<BF16>(at, 0, out(c, j));
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; j++, at += p.N) {
+              for (int j = 0; j < 16; j++, at += step) {
                 if (16 * c + j >= left) break;
-                store<BF16>(p.y, at, out(c, j));
+                store<BF16>(at, 0, out(c, j));
               }
             }
           }
         }
       }
     }
-    if (TS == 64 && p.split > 1) {
+    if (SPLITS && p.split > 1) {
       if (local == 0 && (warp < EPI_WARP0 || !ok)) cluster_wait();
       __syncthreads();                         // (every epilogue warp has sent its part, or none will)
-      if (threadIdx.x < p.split) st_cluster_u32(mapa_shared(smem_addr(fine + rank), threadIdx.x), *abort_flag ? 0u : 1u);
+      if (threadIdx.x < p.split) st_cluster_u32(mapa_shared(smem_addr(fine + part), threadIdx.x), *abort_flag ? 0u : 1u);
       __syncwarp();
       cluster_sync();
       bool whole = true;
       for (int s = 0; s < p.split; s++) whole = whole && fine[s] != 0;
       if (whole) {
-        const int sh = __ffs(p.split) - 1, own = (it.rows - rank + p.split - 1) >> sh;     // tokens of this CTA
+        const int sh = __ffs(p.split) - 1, own = (it.rows - part + p.split - 1) >> sh;     // tokens of this CTA
         for (int x = threadIdx.x; x < own * BM; x += NUM_THREADS) {
           const int t = x / BM, r = x % BM;
           float sum[TWO];
@@ -396,28 +442,33 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             for (int s = 0; s < p.split; s++) sum[g] += red[((s * (TS >> sh) + t) * TWO + g) * BM + r];
           }
           if (it.n0 + r < p.N)
-            store<BF16>(p.y, (it.row + t * p.split + rank) * p.N + it.n0 + r, GATED ? gate(sum[0], sum[TWO - 1]) : sum[0]);
+            store<BF16>(p.y, (it.row + t * p.split + part) * p.N + it.n0 + r, GATED ? gate<BF16>(sum[0], sum[TWO - 1]) : sum[0]);
         }
       }
       __syncwarp();
       if (i + step < items) cluster_sync();    // (its neighbours read what the next item overwrites)
     }
   }
-  if (TS == 64 && p.split > 1 && local == 0) cluster_wait();
+  if (SPLITS && p.split > 1 && local == 0) cluster_wait();
   if (warp == 0) {
     // every copy lands before this CTA's memory goes to another
-    for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; j++) wait_drain(full(j % p.stages), (j / p.stages) & 1);
+    if (in_pair == 0)
+      for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; j++) wait_drain(full(j % p.stages), (j / p.stages) & 1);
+    // (a second CTA's may be ahead of the first one's where a wait gave up: a ms is a thousand times what they take)
+    if (PAIR && !ok)
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) __nanosleep(10000);
   }
-  if (warp == 1 && !ok) {
-    if (elect_one()) umma_commit(drain_bar);
+  if (warp == 1 && !ok && in_pair == 0) {
+    if (elect_one()) commit_mxf4<CTAS>(drain_bar);
     __syncwarp();
     wait_drain(drain_bar, 0);
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();          // (each one's memory is the other's, too, until both have ended)
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc_for<CTAS>(tmem, TMEM_COLS);
   }
 }
 
@@ -437,6 +488,16 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   return fn;
 }
 
+// Scale tiles, two at a time.
+bool encode_scales(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const void *base, int64_t bytes) {
+  const cuuint64_t dims[2] = {kMxTileBytes / 4, (cuuint64_t)(bytes / kMxTileBytes)};
+  const cuuint64_t strides[1] = {kMxTileBytes};
+  const cuuint32_t boxes[2] = {kMxTileBytes / 4, 2}, one[2] = {1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, boxes, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Rows of K / 2 bytes, in boxes of 128 bytes by `box` rows.
 bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const void *base, int64_t rows, int64_t K, int box) {
   const cuuint64_t dims[2] = {(cuuint64_t)(K / 2), (cuuint64_t)rows};
@@ -451,32 +512,38 @@ bool encode_rows(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap *m, const
 
 namespace {
 
-template <bool GATED, bool BF16, int TS>
+template <bool GATED, bool BF16, int TS, int CTAS>
 cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, int64_t most, int sms, cudaStream_t s) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
   if (!encode) return cudaErrorNotSupported;
-  CUtensorMap tx, tw;
+  CUtensorMap tx, tw, txs{}, tws{};
   if (!encode_rows(encode, &tx, a.x_codes, a.M, a.K, box) ||
       !encode_rows(encode, &tw, a.codes, a.experts * (GATED ? 2 : 1) * a.N, a.K, BM))
     return cudaErrorInvalidValue;
+  if (CTAS == 2 && (!encode_scales(encode, &txs, a.x_scales, mx4_scales_bytes(a.M, a.K)) ||
+                    !encode_scales(encode, &tws, a.scales, a.experts * (GATED ? 2 : 1) * p.w_scale_bytes)))
+    return cudaErrorInvalidValue;
   p.box = box;
+  p.n_tiles = (p.n_tiles + CTAS - 1) / CTAS;
+  p.most_tiles = (int)(a.M / TS + a.experts);
   // parts of K that give every SM some
   p.split = 1;
-  if (TS == 64)
+  if (TS == 64 && CTAS == 1)
     while (p.split < MAX_SPLIT && items * p.split * 2 <= sms && p.k_stages >= 2 * p.split) p.split *= 2;
-  p.stages = (SMEM_LIMIT - layout(GATED, TS, 0, p.split, p.experts).total) / layout(GATED, TS, 0, p.split, p.experts).stage;
+  p.stages = (SMEM_LIMIT - layout(GATED, TS, CTAS, 0, p.split, p.experts).total) / layout(GATED, TS, CTAS, 0, p.split, p.experts).stage;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   // (a part of K that is shorter than the ring leaves the next call's CTAs room to begin)
   const int part = (p.k_stages + p.split - 1) / p.split;
   if (items * p.split <= sms && p.stages > part) p.stages = part;
-  const int smem = layout(GATED, TS, p.stages, p.split, p.experts).total;
-  auto kern = mx4_gemm_kernel<GATED, BF16, TS>;
+  const int smem = layout(GATED, TS, CTAS, p.stages, p.split, p.experts).total;
+  auto kern = mx4_gemm_kernel<GATED, BF16, TS, CTAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (e != cudaSuccess) return e;
-  int64_t grid = sms / p.split;
+  const int cluster = CTAS == 2 ? 2 : p.split;
+  int64_t grid = sms / cluster;
   if (most < grid) grid = most;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(grid * p.split));
+  cfg.gridDim = dim3((unsigned)(grid * cluster));
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -484,39 +551,62 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim = {(unsigned)p.split, 1, 1};
+  at[1].val.clusterDim = {(unsigned)cluster, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = p.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tx, tw, p);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tx, tw, txs, tws, p);
+}
+
+// How a call is cut: tokens of a tile, by one CTA (128 weight rows) or a pair (256), and about how many items that makes.
+struct Cut {
+  int ts, ctas;
+  int64_t items;
+};
+
+// A stage of 256 elements takes so many ns, an item's beginning and end so many more, and the SMs take items in rounds: wide
+// tiles and pairs where there are many tokens, narrow ones where those fill the SMs better.  Measured, us, for tiles of 64,
+// 128, 192, 256 tokens and pairs with 256: 8192 x 8192 x 8192: 543, 281, 219, 183, 150; 1024 x 6144 x 2048 (float32): 21.3,
+// 13.9, 12.3, 15.1, 13.3; 256 x 4096 x 4096: 9.1, 9.4, 10.1, 11.1, 10.3; 4096 x 4096 x 1024: 26, 17, 15, 14.4, 15.5.  Gated, 64,
+// 128 and pairs with 128: 1024 x 4096 x 4096: 32, 20.5, 17.4; 8191 tokens by 6 of 64 experts of 1408 x 2048: -, 147, 150.
+Cut cut_for(bool gated, const Mx4GemmArgs &a, int sms) {
+  // experts that are met and rows of each, about
+  const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
+  const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
+  const double stages = (double)((a.K + BK - 1) / BK);
+  struct { int ts, ctas; double stage, item; } const ways[2][5] = {
+      {{64, 1, 320, 560}, {128, 1, 350, 810}, {192, 1, 380, 1070}, {256, 1, 410, 1320}, {256, 2, 320, 1800}},
+      {{64, 1, 400, 700}, {128, 1, 450, 950}, {128, 2, 360, 1500}}};
+  Cut best{0, 1, 0};
+  double least = 0;
+  for (const auto &w : ways[gated]) {
+    if (w.ts == 0) break;
+    // (an expert's last tile is half empty on average)
+    const double each = (double)rows / w.ts + 0.5, tiles = a.starts ? met * (each > 1 ? each : 1) : (double)((rows + w.ts - 1) / w.ts);
+    const double items = tiles * (double)((a.N + BM * w.ctas - 1) / (BM * w.ctas));
+    double rounds = items * w.ctas / sms;
+    rounds = rounds < 1 ? 1 : rounds < 1e9 ? (double)(int64_t)(rounds + 0.999) : rounds;
+    const double cost = rounds * (stages * w.stage + w.item);
+    if (best.ts == 0 || cost < least) best = {w.ts, w.ctas, (int64_t)items}, least = cost;
+  }
+  if (best.items < 1) best.items = 1;
+  return best;
 }
 
 template <bool GATED, bool BF16>
 cudaError_t launch_type(const Mx4GemmArgs &a, const Params &p, cudaStream_t s) {
   const int sms = kv_max_ctas(1);
-  // rows that an expert has, about
-  const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
-  const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
-  // Tokens of a tile.  A stage of 256 elements takes 290 ns and 0.46 ns a token (the tensor core's share, beyond the issue of
-  // its instructions), an item's end 8 ns a token, and the SMs take items in rounds: wide tiles where there are many tokens,
-  // narrow ones where they fill the SMs better.  8192 x 8192 x 8192: 543, 281, 219 and 183 us for 64, 128, 192 and 256 tokens;
-  // 1024 x 6144 x 2048: 21.3, 13.9, 12.3 and 15.1 us; 256 x 4096 x 4096: 9.1, 9.4, 10.1 and 11.1 us.
-  constexpr int WIDEST = GATED ? 128 : 256;
-  int ts = 64;
-  int64_t items = 0;
-  double cost = -1;
-  for (int t = 64; t <= WIDEST; t += 64) {
-    // (an expert's last tile is half empty on average)
-    const int64_t tiles = a.starts ? met * (rows <= t / 2 ? 1 : rows / t + 1) : (rows + t - 1) / t;
-    const int64_t rounds = (tiles * p.n_tiles + sms - 1) / sms;
-    const double c = (double)rounds * (p.k_stages * (GATED ? 2 : 1) * (290 + 0.46 * t) + 8 * t);
-    if (cost < 0 || c < cost) ts = t, cost = c, items = tiles * p.n_tiles;
+  const Cut c = cut_for(GATED, a, sms);
+  const int64_t n_tiles = (p.n_tiles + c.ctas - 1) / c.ctas;
+  const int64_t most = (a.starts ? a.M / c.ts + a.experts : (a.M + c.ts - 1) / c.ts) * n_tiles;      // items at most
+  const bool few = a.starts ? a.routed <= 16 * a.experts : a.M <= 16;
+  if (c.ts == 64) return launch_tile<GATED, BF16, 64, 1>(a, p, few ? 16 : 64, c.items, most, sms, s);
+  if (c.ctas == 2) {
+    if constexpr (GATED) return launch_tile<true, BF16, 128, 2>(a, p, 64, c.items, most, sms, s);
+    return launch_tile<false, BF16, 256, 2>(a, p, 128, c.items, most, sms, s);
   }
-  const int64_t most = a.starts ? (a.M / ts + a.experts) * p.n_tiles : items;      // at most
-  if (most >= (int64_t)1 << 31) return cudaErrorInvalidValue;
-  if (ts == 64) return launch_tile<GATED, BF16, 64>(a, p, rows <= 16 ? 16 : 64, items, most, sms, s);
-  if (GATED || ts == 128) return launch_tile<GATED, BF16, 128>(a, p, 128, items, most, sms, s);
-  if (ts == 192) return launch_tile<false, BF16, 192>(a, p, 192, items, most, sms, s);
-  return launch_tile<false, BF16, 256>(a, p, 256, items, most, sms, s);
+  if (GATED || c.ts == 128) return launch_tile<GATED, BF16, 128, 1>(a, p, 128, c.items, most, sms, s);
+  if (c.ts == 192) return launch_tile<false, BF16, 192, 1>(a, p, 192, c.items, most, sms, s);
+  return launch_tile<false, BF16, 256, 1>(a, p, 256, c.items, most, sms, s);
 }
 
 }  // namespace
@@ -531,6 +621,11 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
   p.experts = (int)a.experts;
   if (a.gated) return a.bf16 ? launch_type<true, true>(a, p, s) : launch_type<true, false>(a, p, s);
   return a.bf16 ? launch_type<false, true>(a, p, s) : launch_type<false, false>(a, p, s);
+}
+
+int mx4_gemm_tile(const Mx4GemmArgs &a) {
+  const Cut c = cut_for(a.gated, a, kv_max_ctas(1));
+  return c.ts | (c.ctas == 2 ? 1024 : 0);
 }
 
 cudaError_t read_clear_mx4_status(int *status, cudaStream_t s) {

@@ -30,6 +30,8 @@ struct Mx4GemmArgs {
   int64_t routed;                  // rows of all experts together, about
   bool bf16, gated;
 };
+// Tokens of a tile of such a call (+ 1024: of a pair of CTAs).
+int mx4_gemm_tile(const Mx4GemmArgs &a);
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s);
 cudaError_t read_clear_mx4_status(int *status, cudaStream_t s);
 

@@ -90,8 +90,11 @@ struct QuantParams {
   Divisor chunks, lanes, row_tiles;          // chunks of a row, rows r % 32 of a tile that exist in some tile, tiles of a matrix
 };
 
-// A warp takes a chunk of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes in a row of the
-// scale tile, and four loads are in flight a lane.
+// A warp takes a chunk (of bfloat16, two) of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes
+// in a row of the scale tile, and 4 KB of loads are in flight a warp.
+template <bool BF16>
+constexpr int chunks_a_warp() { return BF16 ? 2 : 1; }
+
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
   pdl_wait();
@@ -100,28 +103,35 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   uint32_t chunk = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (chunk >= p.units) return;
   uint32_t r32 = p.chunks.split(chunk), tile = p.lanes.split(r32);
-  const uint32_t matrix = p.row_tiles.split(tile);
-  const int64_t row0 = (int64_t)tile * kMxRows + r32, col = (int64_t)chunk * kChunk + 8 * lane;
+  const int64_t matrix = p.row_tiles.split(tile);
+  constexpr int CHUNKS = chunks_a_warp<BF16>();
+  const int64_t row0 = (int64_t)tile * kMxRows + r32, col0 = (int64_t)chunk * (CHUNKS * kChunk) + 8 * lane;
   if (row0 >= p.rows) return;
-  const bool in = col < p.K;
-  Raw<BF16> raw[4];
+  Raw<BF16> raw[CHUNKS][4];
 #pragma unroll
-  for (int g = 0; g < 4; g++) {
-    raw[g] = Raw<BF16>{};
-    if (in && row0 + 32 * g < p.rows) raw[g] = load8<BF16>(p.x, matrix * p.x_matrix + (row0 + 32 * g) * p.x_row + col);
-  }
-  uint32_t words[4];
+  for (int c = 0; c < CHUNKS; c++)
 #pragma unroll
-  for (int g = 0; g < 4; g++) {
-    uint32_t scale;
-    const uint32_t code = encode8(widen(raw[g]), scale);
-    words[g] = scale_word(scale, lane);
-    if (in && row0 + 32 * g < p.rows) p.codes[((matrix * p.rows + row0 + 32 * g) * p.K + col) >> 3] = code;
+    for (int g = 0; g < 4; g++) {
+      raw[c][g] = Raw<BF16>{};
+      if (col0 + c * kChunk < p.K && row0 + 32 * g < p.rows)
+        raw[c][g] = load8<BF16>(p.x, matrix * p.x_matrix + (row0 + 32 * g) * p.x_row + col0 + c * kChunk);
+    }
+#pragma unroll
+  for (int c = 0; c < CHUNKS; c++) {
+    uint32_t words[4];
+    const int64_t col = col0 + c * kChunk;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      uint32_t scale;
+      const uint32_t code = encode8(widen(raw[c][g]), scale);
+      words[g] = scale_word(scale, lane);
+      if (col < p.K && row0 + 32 * g < p.rows) p.codes[((matrix * p.rows + row0 + 32 * g) * p.K + col) >> 3] = code;
+    }
+    const int64_t kt = ((int64_t)chunk * CHUNKS + c) * 2 + (lane >> 4);
+    if ((lane & 15) == 0 && kt < p.k_tiles)
+      *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
+          make_uint4(words[0], words[1], words[2], words[3]);
   }
-  const int64_t kt = (int64_t)chunk * 2 + (lane >> 4);
-  if ((lane & 15) == 0 && kt < p.k_tiles)
-    *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
-        make_uint4(words[0], words[1], words[2], words[3]);
 }
 
 // A warp takes up to 4 chunks of a token's row, and stores them to each of its places.
@@ -189,21 +199,20 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(const DequantParams p
     const uint32_t block = at >> 2;
     scale[i] = p.scales[matrix * p.scale_bytes + mx4_scale_word(r, block >> 2, p.k_tiles) + (block & 3)];
   }
+  // a store of the warp is 32 lanes' four values in a row: lane l's come from the word of lane 16 h + l / 2, its half l % 2
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < kWordsAThread; i++) {
-    const int64_t at = base + t0 + i * kThreads;
-    if (at >= p.words) break;
-    const float s = mx4_scale(scale[i]);
-    float v[8];
+    const int64_t first = base + t0 - lane + i * kThreads;          // the warp's first word
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      const float2 f = mx4_pair((code[i] >> (8 * j)) & 255);
-      v[2 * j] = f.x * s;
-      v[2 * j + 1] = f.y * s;
+    for (int h = 0; h < 2; h++) {
+      const int from = 16 * h + (lane >> 1);
+      const uint32_t word = __shfl_sync(0xFFFFFFFFu, code[i], from) >> (16 * (lane & 1));
+      const float s = mx4_scale(__shfl_sync(0xFFFFFFFFu, scale[i], from));
+      if (first + from >= p.words) continue;
+      const float2 lo = mx4_pair(word & 255), hi = mx4_pair((word >> 8) & 255);
+      __stcs(reinterpret_cast<float4 *>(p.w) + 2 * first + 32 * h + lane, make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s));
     }
-    float4 *o = reinterpret_cast<float4 *>(p.w) + 2 * at;
-    __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
   }
 }
 
@@ -220,7 +229,8 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
     p.chunks = Divisor((uint32_t)((a.K + 4 * kChunk - 1) / (4 * kChunk)));
     units = a.rows * p.chunks.d;
   } else {
-    p.chunks = Divisor((uint32_t)((a.K + kChunk - 1) / kChunk));
+    const int each = kChunk * (a.bf16 ? chunks_a_warp<true>() : chunks_a_warp<false>());
+    p.chunks = Divisor((uint32_t)((a.K + each - 1) / each));
     p.lanes = Divisor(a.rows < 32 ? (uint32_t)a.rows : 32);
     p.row_tiles = Divisor((uint32_t)((a.rows + kMxRows - 1) / kMxRows));
     units = a.matrices * p.row_tiles.d * p.lanes.d * p.chunks.d;

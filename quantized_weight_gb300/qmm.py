@@ -85,6 +85,7 @@ def lib():
             L.qmm_mx4_quantize.argtypes = [vp, i32, i64, i64, vp, vp, i64, i64, i64, vp]
             L.qmm_mx4_dequant.argtypes = [vp, vp, vp, i64, i64, i64, vp]
             L.qmm_mx4_gemm.argtypes = [vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, vp]
+            L.qmm_mx4_gemm_tile.argtypes = [i32, i64, i64, i64, i64, i64]
             L.qmm_moe_rows.argtypes = [i64, i64, i64]
             L.qmm_moe_rows.restype = i64
             L.qmm_moe_plan.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
@@ -100,7 +101,7 @@ def lib():
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
                       "qmm_test_timeout_next_decode", "qmm_test_timeout_next_attend", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
                       "qmm_kv_attend", "qmm_kv_attend_tiles", "qmm_mx4_quantize", "qmm_mx4_dequant", "qmm_mx4_gemm",
-                      "qmm_moe_plan", "qmm_moe_quantize", "qmm_moe_gemm", "qmm_moe_combine"):
+                      "qmm_mx4_gemm_tile", "qmm_moe_plan", "qmm_moe_quantize", "qmm_moe_gemm", "qmm_moe_combine"):
                 getattr(L, f).restype = i32
             _lib = L
     return _lib
@@ -492,16 +493,17 @@ def _new(shape, dtype, device, stream):
 
 def _mx_rows(x, name) -> int:
     """Stride between the rows of x [..., rows, K] on the current device, whose rows are contiguous."""
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.get_device() != _device():
-        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{_device()}")
-    if x.dim() < 2:
-        raise ValueError(f"{name} must have rows, got {tuple(x.shape)}")
-    strides = x.stride()
-    if strides[-1] != 1 and x.shape[-1] > 1 and x.numel() > 0:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return strides[-2] if x.shape[-2] > 1 else 0                      # a lone row has no stride to keep
+    strides, shape = x.stride(), x.shape
+    if not (x.is_cuda and len(strides) > 1 and strides[-1] == 1 and x.get_device() == _device()):
+        if not x.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if x.get_device() != _device():
+            raise ValueError(f"{name} is on {x.device}, the current device is cuda:{_device()}")
+        if len(strides) < 2:
+            raise ValueError(f"{name} must have rows, got {tuple(shape)}")
+        if shape[-1] > 1 and x.numel() > 0:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    return strides[-2] if shape[-2] > 1 else 0                        # a lone row has no stride to keep
 
 
 def mx4_scales_size(rows, K) -> int:
@@ -529,17 +531,18 @@ def _mx_matrix(codes, scales, name, lead):
         raise ValueError(f"{name} must be [{', '.join(map(str, (*lead, 'rows', 'K / 8')))}], got {tuple(shape)}")
     rows, K = shape[-2], shape[-1] * 8
     pc = _here(codes, name, _I32, shape)
-    return rows, K, pc, _here(scales, "scales", _U8, (*lead, mx4_scales_size(rows, K)))
+    size = mx4_scales_size(rows, K)
+    return rows, K, pc, _here(scales, "scales", _U8, (*lead, size) if lead else (size,))
 
 
 def mx4_quantize(x, out=None, stream=None):
     """float32 or bfloat16 x [..., rows, K] to microscaled 4-bit (codes int32 [..., rows, K / 8], scales uint8 [..., bytes])."""
-    dt, row = _mx_dtype(x.dtype), _mx_rows(x, "x")
-    if x.dim() == 2:
-        (rows, K), n, matrix = x.shape, 1, 0
+    dt, row, shape = _mx_dtype(x.dtype), _mx_rows(x, "x"), x.shape
+    if len(shape) == 2:
+        (rows, K), n, matrix = shape, 1, 0
         codes, scales = (rows, K // 8), (mx4_scales_size(rows, K),)
     else:
-        (*lead, rows, K), n = x.shape, x.shape[:-2].numel()
+        (*lead, rows, K), n = shape, shape[:-2].numel()
         if len(lead) > 1:
             x = x.view(n, rows, K)                                    # (leading dimensions one after the other)
         matrix = x.stride(0) if n > 1 else 0
@@ -557,13 +560,13 @@ def mx4_dequant(codes, scales, out=None, stream=None) -> torch.Tensor:
     """The float32 values [..., rows, K] of a microscaled matrix."""
     lead = codes.shape[:-2]
     rows, K, pc, ps = _mx_matrix(codes, scales, "codes", lead)
-    shape = (*lead, rows, K)
+    shape = (*lead, rows, K) if lead else (rows, K)
     if out is None:
         out = _new(shape, _F32, codes.device, stream)
         po = out.data_ptr()
     else:
         po = _here(out, "out", _F32, shape)
-    _call("qmm_mx4_dequant", lib().qmm_mx4_dequant(pc, ps, po, lead.numel(), rows, K, _stream(stream)))
+    _call("qmm_mx4_dequant", lib().qmm_mx4_dequant(pc, ps, po, lead.numel() if lead else 1, rows, K, _stream(stream)))
     return out
 
 
@@ -586,6 +589,14 @@ def mx4_gemm(x_codes, x_scales, codes, scales, gated=False, dtype=torch.float32,
     out, dt, po = _mx_out(out, (M, N), dtype, x_codes.device, stream)
     _call("qmm_mx4_gemm", lib().qmm_mx4_gemm(px, pxs, pc, ps, po, dt, gated, M, N, K, _stream(stream)))
     return out
+
+
+def mx4_gemm_tile(M, N, K, gated=False, experts=0, routed=0) -> int:
+    """Which kernel takes a call of mx4_gemm, or of moe_gemm with so many experts (M: its R): the tokens of a tile, plus 1024
+    where a pair of CTAs shares it."""
+    r = lib().qmm_mx4_gemm_tile(gated, routed, M, experts, N, K)
+    _call("qmm_mx4_gemm_tile", min(r, 0))
+    return r
 
 
 def moe_rows(T, E, k) -> int:

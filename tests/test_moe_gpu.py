@@ -157,7 +157,8 @@ def experts_case(T, rng, counts, N, K, gated):
 
 @pytest.mark.parametrize("counts,N,K", [([1], 1, 32), ([3, 0, 1], 130, 96), ([0, 0, 5, 0], 256, 512), ([8] * 9, 300, 1056),
                                         ([1, 1, 0, 1, 1, 0, 1, 1], 2048, 1408), ([129, 64, 65, 0, 300], 257, 288),
-                                        ([700, 5, 128, 256], 128, 640), ([40] * 30, 200, 352), ([33, 17, 250, 1, 0, 90], 384, 2080)])
+                                        ([700, 5, 128, 256], 128, 640), ([40] * 30, 200, 352), ([33, 17, 250, 1, 0, 90], 384, 2080), ([900, 0, 300, 1, 513], 2000, 2208),
+                                        ([257, 640, 128], 1100, 2080)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("gated", [False, True])
 def test_experts(T, qmm, counts, N, K, dtype, gated):
@@ -178,6 +179,26 @@ def test_experts(T, qmm, counts, N, K, dtype, gated):
                 want, bound = ref.product(xv[s:s + n], values[e], gated)
                 check_product(y[s:s + n], want, bound, dtype)
         assert (y[T.from_numpy(~own).cuda()] == 7).all()
+
+
+def test_experts_reach_pairs(qmm):
+    import torch
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("the rule counts SMs")
+    R = 1024 + 384 + 128 + 640
+    assert qmm.mx4_gemm_tile(R, 2000, 2208, experts=5, routed=1714) > 1024
+    assert qmm.mx4_gemm_tile(R, 2000, 2208, gated=True, experts=5, routed=1714) > 1024
+    assert qmm.mx4_gemm_tile(128 * 9, 300, 1056, experts=9, routed=72) == 64
+
+
+def test_experts_that_share_rows_stay_inside(T, qmm):
+    """Not allowed, but no reason to leave the arrays: every expert claims all rows."""
+    rng = np.random.default_rng(8)
+    xc, xs, xv, codes, scales, values, st, ct, _, R = experts_case(T, rng, [128] * 40, 130, 64, False)
+    y = T.full((R + 1, 130), 7.0, device="cuda")
+    qmm.moe_gemm(*on_gpu(T, xc, xs), codes, scales, T.zeros_like(st), T.full_like(ct, R), out=y[:R])
+    qmm.check()
+    assert (y[R] == 7).all() and T.isfinite(y).all()
 
 
 def test_experts_with_bad_starts_and_counts(T, qmm):

@@ -145,6 +145,26 @@ SIZES = [(1, 1, 32), (1, 128, 64), (3, 130, 96), (8, 257, 256), (9, 64, 1056), (
          (256, 256, 1024), (257, 390, 160), (300, 2000, 96), (500, 129, 5120), (1024, 1025, 512), (2500, 300, 256)]
 
 
+def test_every_kernel_is_reached(T, qmm):
+    """By the sizes of this file and of the experts' tests, on a GB300."""
+    if T.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("the rule counts SMs")
+    assert {qmm.mx4_gemm_tile(M, N, K) for M, N, K in SIZES + LARGE} == {64, 128, 192, 256, 256 + 1024}
+    assert {qmm.mx4_gemm_tile(M, N, K, gated=True) for M, N, K in SIZES + LARGE} == {64, 128, 128 + 1024}
+
+
+# the first two take pairs of CTAs (the second CTA without weight rows in the last tile, and tokens of one row), then gated
+# ones, then wide tiles of one
+LARGE = [(1500, 2900, 2208), (1281, 2900, 2048), (900, 1500, 2208), (641, 1300, 2080), (1281, 3000, 1024), (1000, 2900, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_large_product(T, qmm, M, N, K, dtype, gated):
+    test_product(T, qmm, M, N, K, dtype, gated)
+
+
 @pytest.mark.parametrize("M,N,K", SIZES)
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("gated", [False, True])

@@ -96,6 +96,17 @@ def test_experts(L):
     assert experts(L, R=0) == OK and experts(L, N=0) == OK
 
 
+def test_gemm_tile(L):
+    tile = L.qmm_mx4_gemm_tile
+    assert tile(0, 0, 8, 0, 4096, 4096) == 64 and tile(0, 0, 8192, 0, 8192, 8192) == 256 + 1024
+    assert tile(1, 48, 6144, 64, 1408, 2048) == 64
+    for bad in ((0, 0, 8, 0, 64, 0), (0, 0, -1, 0, 64, 64), (0, 0, 8, -1, 64, 64), (0, 0, 8, 1025, 64, 64), (0, -1, 8, 4, 64, 64),
+                (0, 0, 8, 64, 1 << 25, 64), (1, 0, 8, 0, 1 << 30, 64), (0, 0, BIG - 1, 0, 64 * 128, 64)):
+        assert tile(*bad) == SHAPE
+    with pytest.raises(qmm.QmmError):
+        qmm.mx4_gemm_tile(8, 64, 48)
+
+
 def test_plan(L):
     assert plan(L, dtype=3) == UNSUP
     assert plan(L, T=-1) == SHAPE and plan(L, E=0) == SHAPE and plan(L, E=1025) == SHAPE and plan(L, E=1024, l=None) == ARG
