@@ -526,21 +526,31 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
   p.box = box;
   p.n_tiles = (p.n_tiles + CTAS - 1) / CTAS;
   p.most_tiles = (int)(a.M / TS + a.experts);
-  // parts of K that give every SM some
+  // Parts of K where items leave SMs without work: two CTAs an SM with rings of half its shared memory (gated: one; and eight
+  // to a cluster do not all find room).  A stage takes 320 ns (gated: 400), joining the parts 3 us: 8 x 4096 x 4096 8.7, 8.9,
+  // 7.5, 7.1 us with 1, 2, 4, 8 parts, 8 x 5120 x 17408 25.6, 19.3, 14.0 us with 1, 2, 4, 8 x 12288 x 4096 9.8, 10.3 us with 1, 2.
+  constexpr bool TWO_AN_SM = TS == 64 && CTAS == 1 && !GATED;
+  const int64_t room = TWO_AN_SM ? 2 * sms : sms;
   p.split = 1;
-  if (TS == 64 && CTAS == 1)
-    while (p.split < MAX_SPLIT && items * p.split * 2 <= sms && p.k_stages >= 2 * p.split) p.split *= 2;
-  p.stages = (SMEM_LIMIT - layout(GATED, TS, CTAS, 0, p.split, p.experts).total) / layout(GATED, TS, CTAS, 0, p.split, p.experts).stage;
+  if (TS == 64 && CTAS == 1) {
+    int64_t least = (int64_t)p.k_stages * (GATED ? 400 : 320);
+    for (int split = 2; split <= (GATED ? 4 : MAX_SPLIT) && items * split <= room && p.k_stages >= split; split *= 2) {
+      const int64_t cost = (int64_t)((p.k_stages + split - 1) / split) * (GATED ? 400 : 320) + 2900 + 50 * split;
+      if (cost < least) least = cost, p.split = split;
+    }
+  }
+  const int64_t limit = TWO_AN_SM && items * p.split <= room ? SMEM_LIMIT / 2 : SMEM_LIMIT;
+  p.stages = (int)(limit - layout(GATED, TS, CTAS, 0, p.split, p.experts).total) / layout(GATED, TS, CTAS, 0, p.split, p.experts).stage;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   // (a part of K that is shorter than the ring leaves the next call's CTAs room to begin)
   const int part = (p.k_stages + p.split - 1) / p.split;
-  if (items * p.split <= sms && p.stages > part) p.stages = part;
+  if (items * p.split <= room && p.stages > part) p.stages = part;
   const int smem = layout(GATED, TS, CTAS, p.stages, p.split, p.experts).total;
   auto kern = mx4_gemm_kernel<GATED, BF16, TS, CTAS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
   if (e != cudaSuccess) return e;
   const int cluster = CTAS == 2 ? 2 : p.split;
-  int64_t grid = sms / cluster;
+  int64_t grid = (limit < SMEM_LIMIT ? room : sms) / cluster;
   if (most < grid) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(grid * cluster));

@@ -55,19 +55,17 @@ __device__ __forceinline__ Eight widen(const Raw<BF16> &r) {
 
 // A lane's word of codes, and the scale of its block (the same in its 4 lanes).  The whole warp calls it.
 __device__ __forceinline__ uint32_t encode8(const Eight &e, uint32_t &scale) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(e.v[i]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  const float a = max3_nan(max3_nan(fabsf(e.v[0]), fabsf(e.v[1]), fabsf(e.v[2])), fabsf(e.v[3]), fabsf(e.v[4]));
+  uint32_t m = __float_as_uint(max3_nan(max3_nan(a, fabsf(e.v[5]), fabsf(e.v[6])), fabsf(e.v[7]), 0.0f));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));     // (of values that are not negative, the bits order as they do)
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-  const uint32_t top = m >> 23;                       // exponent field; 255: an infinity or a NaN is there
+  const uint32_t top = (m >> 23) & 255;               // exponent field; 255: an infinity or a NaN is there
   scale = top == 255 ? 255 : top < 2 ? 0 : top - 2;
-  if (top == 255) return 0;
-  const float inv = __uint_as_float((254 - scale) << 23);   // 2 ** (127 - scale)
-  uint32_t word = 0;
+  const float inv = __uint_as_float((254 - min(scale, 253u)) << 23);      // 2 ** (127 - scale)
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 4; i++) word |= mx4_encode(e.v[2 * i] * inv, e.v[2 * i + 1] * inv) << (8 * i);
-  return word;
+  for (int i = 0; i < 8; i++) v[i] = e.v[i] * inv;
+  return mx4_encode(v);
 }
 
 // The four scales of a scale tile's row, in lanes 0..15 those of the first tile of a chunk, in 16..31 the second's.
