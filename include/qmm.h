@@ -490,6 +490,12 @@ int qmm_test_timeout_next_decode(int64_t limit_ns);
  */
 int qmm_test_timeout_next_attend(int64_t limit_ns);
 
+/*
+ * qmm_test_timeout_next_mx4 -- the same for the microscaled product: in the next qmm_mx4_gemm or qmm_moe_gemm launch, every
+ *   block's first wait for sums is one that nothing ends, with this limit.  The launch writes nothing.
+ */
+int qmm_test_timeout_next_mx4(int64_t limit_ns);
+
 /* A static, human-readable name for a qmm_status value. */
 const char *qmm_status_string(int status);
 

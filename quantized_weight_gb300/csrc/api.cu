@@ -455,6 +455,12 @@ int qmm_test_timeout_next_attend(int64_t limit_ns) {
   return QMM_OK;
 }
 
+int qmm_test_timeout_next_mx4(int64_t limit_ns) {
+  if (limit_ns < 1000 || limit_ns > 100000000) return QMM_ERR_ARG;
+  qmm::set_mx4_test_wait((unsigned long long)limit_ns);
+  return QMM_OK;
+}
+
 int qmm_check(qmm_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QMM_ERR_CUDA;
   int st[7] = {0, 0, 0, 0, 0, 0, 0};

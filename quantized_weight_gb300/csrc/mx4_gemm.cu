@@ -62,6 +62,7 @@ struct Params {
   int box;                                 // rows of x in a copy
   int stages;                              // ring depth
   int split;                               // CTAs of a cluster, each with a part of K
+  unsigned long long test_wait_ns;         // test hook: the epilogues' first wait is for nothing, and runs out after so long
 };
 
 struct Layout {                            // of a CTA's shared memory
@@ -80,7 +81,7 @@ __host__ __device__ inline Layout layout(bool gated, int ts, int ctas, int stage
   l.red = split > 1 ? two * ts * BM * 4 : 0;
   l.list = (3 * experts + 1) * 4;          // starts, counts, and token tiles before
   l.list = (l.list + 15) & ~15;
-  l.bars = 8 * (2 * MAX_STAGES + 4 + 1) + 16 + 4 * MAX_SPLIT;
+  l.bars = 8 * (2 * MAX_STAGES + 4 + 2) + 16 + 4 * MAX_SPLIT;
   l.total = l.ring + l.red + l.list + l.bars + 1024;   // (1024: the ring begins at a multiple of it)
   return l;
 }
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   auto empty = [&](int s) { return bars + 8 * (MAX_STAGES + s); };
   auto acc_full = [&](int b) { return bars + 8 * (2 * MAX_STAGES + b); };
   auto acc_empty = [&](int b) { return bars + 8 * (2 * MAX_STAGES + 2 + b); };
-  const uint32_t drain_bar = bars + 8 * (2 * MAX_STAGES + 4);
-  uint8_t *tail = smem + l.ring + l.red + l.list + 8 * (2 * MAX_STAGES + 5);
+  const uint32_t drain_bar = bars + 8 * (2 * MAX_STAGES + 4), never_bar = drain_bar + 8;
+  uint8_t *tail = smem + l.ring + l.red + l.list + 8 * (2 * MAX_STAGES + 6);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
   uint32_t *fine = reinterpret_cast<uint32_t *>(tail + 8);       // [split]: that CTA's part is whole
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
       mbar_init(acc_empty(b), CTAS * EPI_THREADS);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(never_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmap_x);
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
       const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;      // TMEM lane quarter; which half of the tile's tokens
       const int r = q * 32 + lane;
       const int64_t n = it.n0 + r;
+      if (p.test_wait_ns != 0 && local == 0) ok = __all_sync(0xFFFFFFFFu, wait_bounded(never_bar, 0, ctl, p.test_wait_ns));
       if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(acc_full(buf), use, ctl));
       if (ok) {
         tc_fence_after();
@@ -458,13 +461,13 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     if (PAIR && !ok)
       for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) __nanosleep(10000);
   }
-  if (warp == 1 && !ok && in_pair == 0) {
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1 && *abort_flag && in_pair == 0) {      // (whichever wait gave up, MMAs may be in flight)
     if (elect_one()) commit_mxf4<CTAS>(drain_bar);
     __syncwarp();
     wait_drain(drain_bar, 0);
   }
-  tc_fence_before();
-  __syncthreads();
   if constexpr (PAIR) cluster_sync();          // (each one's memory is the other's, too, until both have ended)
   if (warp == 1) {
     tc_fence_after();
@@ -473,6 +476,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
 }
 
 // ---------------------------------------------------------------- host side
+
+std::atomic<unsigned long long> g_test_wait_ns{0};
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
@@ -629,9 +634,12 @@ cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s) {
   p.w_scale_bytes = mx4_scales_bytes(a.N, a.K);
   p.k_tiles = (int)mx4_k_tiles(a.K), p.k_stages = (int)((a.K + BK - 1) / BK), p.k_steps = (int)((a.K + MMA_K - 1) / MMA_K);
   p.experts = (int)a.experts;
+  p.test_wait_ns = g_test_wait_ns.exchange(0, std::memory_order_relaxed);
   if (a.gated) return a.bf16 ? launch_type<true, true>(a, p, s) : launch_type<true, false>(a, p, s);
   return a.bf16 ? launch_type<false, true>(a, p, s) : launch_type<false, false>(a, p, s);
 }
+
+void set_mx4_test_wait(unsigned long long limit_ns) { g_test_wait_ns.store(limit_ns, std::memory_order_relaxed); }
 
 int mx4_gemm_tile(const Mx4GemmArgs &a) {
   const Cut c = cut_for(a.gated, a, kv_max_ctas(1));

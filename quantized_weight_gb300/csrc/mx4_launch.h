@@ -34,6 +34,7 @@ struct Mx4GemmArgs {
 int mx4_gemm_tile(const Mx4GemmArgs &a);
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, cudaStream_t s);
 cudaError_t read_clear_mx4_status(int *status, cudaStream_t s);
+void set_mx4_test_wait(unsigned long long limit_ns);
 
 struct MoePlanArgs {
   const void *logits;

@@ -94,6 +94,7 @@ def lib():
             L.qmm_moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
             L.qmm_check.argtypes = [vp]
             L.qmm_test_timeout_next_decode.argtypes = L.qmm_test_timeout_next_attend.argtypes = [i64]
+            L.qmm_test_timeout_next_mx4.argtypes = [i64]
             L.qmm_status_string.argtypes = [i32]
             L.qmm_status_string.restype = ctypes.c_char_p
             L.qmm_abi_version.argtypes = []
@@ -101,7 +102,7 @@ def lib():
                       "qmm_gather_dequant", "qmm_gemv_argmax", "qmm_gemv_argmax_noalloc", "qmm_check",
                       "qmm_test_timeout_next_decode", "qmm_test_timeout_next_attend", "qmm_abi_version", "qmm_kv_plan", "qmm_kv_append", "qmm_kv_read",
                       "qmm_kv_attend", "qmm_kv_attend_tiles", "qmm_mx4_quantize", "qmm_mx4_dequant", "qmm_mx4_gemm",
-                      "qmm_mx4_gemm_tile", "qmm_moe_plan", "qmm_moe_quantize", "qmm_moe_gemm", "qmm_moe_combine"):
+                      "qmm_mx4_gemm_tile", "qmm_test_timeout_next_mx4", "qmm_moe_plan", "qmm_moe_quantize", "qmm_moe_gemm", "qmm_moe_combine"):
                 getattr(L, f).restype = i32
             _lib = L
     return _lib
@@ -686,6 +687,12 @@ def test_timeout_next_attend(limit_ns: int) -> None:
     """Test hook: the next kv_attend launch on tiles of 128 rows makes one wait a block that runs out after limit_ns; it
     writes no row that sees a key and the next check() raises QMM_ERR_DEVICE_TIMEOUT."""
     _call("qmm_test_timeout_next_attend", lib().qmm_test_timeout_next_attend(int(limit_ns)))
+
+
+def test_timeout_next_mx4(limit_ns: int) -> None:
+    """Test hook: the next mx4_gemm or moe_gemm launch makes one wait a block that runs out after limit_ns; it writes nothing
+    and the next check() raises QMM_ERR_DEVICE_TIMEOUT."""
+    _call("qmm_test_timeout_next_mx4", lib().qmm_test_timeout_next_mx4(int(limit_ns)))
 
 
 def check(stream=None) -> None:

@@ -167,6 +167,11 @@ def test_reference_is_the_format():
     assert np.array_equal(ref.unpack(ref.pack(codes)), codes)
 
 
+def test_timeout_hook_limits(L):
+    for ns in (999, 100_000_001, -5):
+        assert L.qmm_test_timeout_next_mx4(ns) == ARG
+
+
 def test_cpu_tensors_are_refused(L):
     x, c, s = torch.zeros(4, 64), torch.zeros(4, 8, dtype=torch.int32), torch.zeros(512, dtype=torch.uint8)
     i = torch.zeros(4, 2, dtype=torch.int32)
