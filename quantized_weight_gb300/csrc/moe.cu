@@ -444,7 +444,8 @@ cudaError_t launch_sort(PlanParams p, int ctas, cudaStream_t s) {
   if (p.blocks > kSortBlocks) p.blocks = kSortBlocks;
   const size_t smem = (size_t)6 * p.blocks * p.E;
   auto kern = sort_kernel<LANES, PER>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  cudaError_t e = cudaSuccess;
+  if (smem > 32 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
   if (e == cudaSuccess && ctas > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};

@@ -65,6 +65,15 @@ struct Params {
   unsigned long long test_wait_ns;         // test hook: the epilogues' first wait is for nothing, and runs out after so long
 };
 
+// One piece of work: a weight tile and a token tile.
+struct alignas(16) Item {
+  int n0;                                  // first row of the weight tile (a pair's: of its first CTA's)
+  int row;                                 // first row of the token tile in x and y
+  int rows;                                // tokens of it
+  int expert;
+};
+constexpr int LISTED = 32;                 // items of a CTA that are found before it begins
+
 struct Layout {                            // of a CTA's shared memory
   int a, b, sfa, sfb, stage;               // bytes: weights, tokens, scales, all
   int ring, red, list, bars, total;
@@ -79,20 +88,12 @@ __host__ __device__ inline Layout layout(bool gated, int ts, int ctas, int stage
   l.stage = l.a + l.b + l.sfa + l.sfb;     // (multiples of 1024 bytes)
   l.ring = stages * l.stage;
   l.red = split > 1 ? two * ts * BM * 4 : 0;
-  l.list = (3 * experts + 1) * 4;          // starts, counts, and token tiles before
+  l.list = LISTED * (int)sizeof(Item) + (3 * experts + 1) * 4;     // items; starts, counts, and token tiles before
   l.list = (l.list + 15) & ~15;
   l.bars = 8 * (2 * MAX_STAGES + 4 + 2) + 16 + 4 * MAX_SPLIT;
   l.total = l.ring + l.red + l.list + l.bars + 1024;   // (1024: the ring begins at a multiple of it)
   return l;
 }
-
-// One piece of work: a weight tile and a token tile.
-struct Item {
-  int64_t n0;                              // first row of the weight tile
-  int64_t row;                             // first row of the token tile in x and y
-  int rows;                                // tokens of it
-  int expert;
-};
 
 struct Ring {
   int s = 0;
@@ -138,7 +139,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   const uint32_t sbase = smem_addr(smem);
   const Layout l = layout(GATED, TS, CTAS, p.stages, p.split, p.experts);
   float *red = reinterpret_cast<float *>(smem + l.ring);
-  int32_t *starts = reinterpret_cast<int32_t *>(smem + l.ring + l.red), *counts = starts + p.experts, *before = counts + p.experts;
+  Item *listed = reinterpret_cast<Item *>(smem + l.ring + l.red);
+  int32_t *starts = reinterpret_cast<int32_t *>(listed + LISTED), *counts = starts + p.experts, *before = counts + p.experts;
   const uint32_t bars = sbase + l.ring + l.red + l.list;
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (MAX_STAGES + s); };
@@ -184,23 +186,32 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   if (warp == 0) {
     // the experts' rows, made to fit x, and the token tiles before each
     uint32_t sum = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + lane;
-      int64_t start = 0, count = p.M;
-      if (p.starts) {
-        start = e < p.experts ? p.starts[e] : 0, count = e < p.experts ? p.counts[e] : 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 32 * 4) {
+      int s4[4], c4[4];                                // (loads that wait for nothing between them)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int e = e0 + 32 * q + lane;
+        s4[q] = p.starts && e < p.experts ? p.starts[e] : 0;
+        c4[q] = p.starts ? (e < p.experts ? p.counts[e] : 0) : (int)p.M;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int e = e0 + 32 * q + lane;
+        if (e - lane >= p.experts) break;
+        int start = s4[q];
+        int64_t count = c4[q];
         if (start < 0 || start >= p.M || start % kMxRows != 0 || count < 0) start = 0, count = 0;
         if (count > p.M - start) count = p.M - start;
-      }
-      uint32_t at = e < p.experts ? (uint32_t)((count + TS - 1) / TS) : 0;
+        uint32_t at = e < p.experts ? (uint32_t)((count + TS - 1) / TS) : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
-        if (lane >= o) at += v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, at, o);
+          if (lane >= o) at += v;
+        }
+        at = min(sum + at, (uint32_t)p.most_tiles);    // (more only where experts share rows)
+        if (e < p.experts) starts[e] = start, counts[e] = (int)count, before[e + 1] = (int)at;
+        sum = __shfl_sync(0xFFFFFFFFu, at, 31);
       }
-      at = min(sum + at, (uint32_t)p.most_tiles);      // (more only where experts share rows)
-      if (e < p.experts) starts[e] = (int)start, counts[e] = (int)count, before[e + 1] = (int)at;
-      sum = __shfl_sync(0xFFFFFFFFu, at, 31);
     }
     if (lane == 0) before[0] = 0;
   }
@@ -222,31 +233,41 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   auto tokens_of = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
   auto item_at = [&](int i) {
     Item it;
-    int lo = 0, hi = p.experts;                // the last expert whose items begin at or before i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] * p.n_tiles <= i) lo = mid; else hi = mid;
-    }
+    // the last expert whose items begin at or before i, by the whole warp
+    int lo = -1;
+    for (int e = lane; e - lane < p.experts; e += 32)
+      lo += __popc(__ballot_sync(0xFFFFFFFFu, e < p.experts && before[e] * p.n_tiles <= i));
     const int tiles = before[lo + 1] - before[lo], j = i - before[lo] * p.n_tiles;
-    const int nt = j / tiles, m0 = (j - nt * tiles) * TS;
+    const int nt = tiles == 1 ? j : j / tiles, m0 = (j - nt * tiles) * TS;
     it.expert = lo;
-    it.n0 = (int64_t)(nt * CTAS + in_pair) * BM;
-    it.row = (int64_t)starts[lo] + m0;
+    it.n0 = nt * (CTAS * BM);
+    it.row = starts[lo] + m0;
     it.rows = min(counts[lo] - m0, TS);
     return it;
   };
+
+  // (finding one takes some 600 cycles, which each role would else spend between two items)
+  for (int t = warp; t < LISTED && first + t * step < items; t += NUM_THREADS / 32) {
+    const Item it = item_at(first + t * step);
+    if (lane == 0) listed[t] = it;
+  }
+  __syncthreads();
 
   // (a reduction over equal values leaves its result in a uniform register, where the operands of copies and MMAs have to
   // be: from ordinary registers a stage's instructions took 1600 cycles to issue)
   auto uniform = [](uint32_t v) { return __reduce_max_sync(0xFFFFFFFFu, v); };
   auto uniform64 = [&](uint64_t v) { return (uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v); };
+  // (a pair's copies complete on the first CTA's barriers)
+  const uint32_t base0 = uniform(sbase), stage_bytes = uniform(l.stage), tmem0 = uniform(tmem), empty0 = uniform(empty(0));
+  const uint32_t full0 = uniform(PAIR ? mapa_shared(full(0), 0) : full(0)), box_bytes = uniform(p.box * (BK / 2));
   Ring ring;                                   // (of the copying and the issuing warp)
   int issued = 0;                              // stages so far
   int ready = 0;                               // stages known to have landed
   int local = 0;                               // items so far
   bool ok = true;
   for (int i = first; i < items; i += step, local++) {
-    const Item it = item_at(i);
+    const Item it = local < LISTED ? listed[local] : item_at(i);
+    const int64_t n0 = it.n0 + in_pair * BM;   // of this CTA
     const int buf = local & (BUFS - 1);
     const uint32_t use = (uint32_t)(BUFS == 2 ? local >> 1 : local) & 1;
     // tokens of the tile before its first: its scale tile may begin 64 rows earlier
@@ -258,16 +279,14 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
         // (a pair's second CTA has the second half of the tokens, and its weight rows may lie past the last)
         const uint32_t boxes = PAIR ? 1 : uniform((it.rows + p.box - 1) / p.box);
         const uint32_t row = uniform((uint32_t)it.row + in_pair * (tokens_of(it.rows) / 2));
-        const int64_t w_tile = PAIR ? min(it.n0 >> 7, (p.N - 1) >> 7) : it.n0 >> 7;
-        const uint32_t w_row = uniform((uint32_t)((int64_t)it.expert * TWO * p.N + it.n0)), w_next = uniform((uint32_t)p.N);
+        const int64_t w_tile = PAIR ? min(n0 >> 7, (p.N - 1) >> 7) : n0 >> 7;
+        const uint32_t w_row = uniform((uint32_t)((int64_t)it.expert * TWO * p.N + n0)), w_next = (uint32_t)p.N;
         const uint64_t ws = uniform64(reinterpret_cast<uint64_t>(p.ws) + (int64_t)it.expert * TWO * p.w_scale_bytes +
                                       w_tile * p.k_tiles * kMxTileBytes);
-        const uint64_t xs = uniform64(reinterpret_cast<uint64_t>(p.xs) + (it.row >> 7) * p.k_tiles * kMxTileBytes);
-        const uint32_t two_tiles = uniform(sf_tiles == 2), box_bytes = uniform(p.box * (BK / 2));
-        // (a pair's copies complete on the first CTA's barriers)
-        const uint32_t base0 = uniform(sbase), full0 = uniform(PAIR ? mapa_shared(full(0), 0) : full(0)), stage_bytes = uniform(l.stage);
+        const uint64_t xs = uniform64(reinterpret_cast<uint64_t>(p.xs) + ((int64_t)it.row >> 7) * p.k_tiles * kMxTileBytes);
+        const uint32_t two_tiles = uniform(sf_tiles == 2);
         const uint32_t ws_tile = uniform((uint32_t)(((int64_t)it.expert * TWO * ((p.N + 127) >> 7) + w_tile) * p.k_tiles));
-        const uint32_t ws_next = uniform((uint32_t)(((p.N + 127) >> 7) * p.k_tiles)), xs_tile = uniform((uint32_t)((it.row >> 7) * p.k_tiles));
+        const uint32_t ws_next = uniform((uint32_t)(((p.N + 127) >> 7) * p.k_tiles)), xs_tile = uniform((uint32_t)(((int64_t)it.row >> 7) * p.k_tiles));
         const uint32_t each = l.a + boxes * box_bytes, sfs = TWO + 1 + two_tiles;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
           if (!__all_sync(0xFFFFFFFFu, wait_bounded(empty(ring.s), ring.ph ^ 1, ctl))) { ok = false; break; }
@@ -310,11 +329,12 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
         ok = __all_sync(0xFFFFFFFFu, PAIR ? wait_cluster(acc_empty(buf), use ^ 1, ctl) : wait_bounded(acc_empty(buf), use ^ 1, ctl));
       if (ok && in_pair == 0) {
         tc_fence_after();
-        const uint32_t id = uniform(idesc_mxf4(CTAS * BM, tokens_of(it.rows)));
-        const uint32_t d = uniform(tmem + buf * TWO * TS), sf0 = uniform(tmem + BUFS * TWO * TS);
-        const uint32_t off = uniform(shift >> 5), two_tiles = uniform(sf_tiles == 2);
+        const uint32_t what = uniform((uint32_t)(tokens_of(it.rows) >> 3) | (uint32_t)(shift >> 5) << 8 | (uint32_t)(sf_tiles == 2) << 10 | (uint32_t)buf << 11);
+        const uint32_t id = idesc_mxf4(CTAS * BM, 0) | (what & 255) << 17;
+        const uint32_t off = what >> 8 & 3, two_tiles = what >> 10 & 1;
+        const uint32_t d = tmem0 + (what >> 11) * (TWO * TS), sf0 = tmem0 + BUFS * TWO * TS;
         const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
-        const uint32_t at0 = uniform(sbase >> 4), stage16 = uniform(l.stage >> 4), empty0 = uniform(empty(0));
+        const uint32_t at0 = base0 >> 4, stage16 = stage_bytes >> 4;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
           if constexpr (!SPLITS) {
             if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
@@ -353,7 +373,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
 #pragma unroll
                 for (int g = 0; g < TWO; g++)
                   umma_mxf4<CTAS>(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
-                            sfa + g * 8 + a * 4, sfb + a * 8 + off, j > 0 ? 1u : more);
+                                  sfa + g * 8 + a * 4, sfb + a * 8 + off, j > 0 ? 1u : more);
               }
             }
             commit_mxf4<CTAS>(bar);
@@ -367,7 +387,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
       // -------------------------------------------------------- epilogue
       const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;      // TMEM lane quarter; which half of the tile's tokens
       const int r = q * 32 + lane;
-      const int64_t n = it.n0 + r;
+      const int64_t n = n0 + r;
       if (p.test_wait_ns != 0 && local == 0) ok = __all_sync(0xFFFFFFFFu, wait_bounded(never_bar, 0, ctl, p.test_wait_ns));
       if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bounded(acc_full(buf), use, ctl));
       if (ok) {
@@ -409,7 +429,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             return GATED ? gate<BF16>(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][TWO - 1][j])) : __uint_as_float(v[c][0][j]);
           };
           const int64_t step = p.N * (BF16 ? 2 : 4);
-          char *at = static_cast<char *>(p.y) + (it.row + c0) * step + n * (BF16 ? 2 : 4);
+          char *at = static_cast<char *>(p.y) + ((int64_t)it.row + c0) * step + n * (BF16 ? 2 : 4);
 #pragma unroll
           for (int c = 0; c < CHUNKS; c++) {
             if (16 * c + 16 <= left) {
@@ -444,8 +464,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             sum[g] = 0.0f;
             for (int s = 0; s < p.split; s++) sum[g] += red[((s * (TS >> sh) + t) * TWO + g) * BM + r];
           }
-          if (it.n0 + r < p.N)
-            store<BF16>(p.y, (it.row + t * p.split + part) * p.N + it.n0 + r, GATED ? gate<BF16>(sum[0], sum[TWO - 1]) : sum[0]);
+          if (n0 + r < p.N)
+            store<BF16>(p.y, ((int64_t)it.row + t * p.split + part) * p.N + n0 + r, GATED ? gate<BF16>(sum[0], sum[TWO - 1]) : sum[0]);
         }
       }
       __syncwarp();
@@ -552,8 +572,6 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
   if (items * p.split <= room && p.stages > part) p.stages = part;
   const int smem = layout(GATED, TS, CTAS, p.stages, p.split, p.experts).total;
   auto kern = mx4_gemm_kernel<GATED, BF16, TS, CTAS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
-  if (e != cudaSuccess) return e;
   const int cluster = CTAS == 2 ? 2 : p.split;
   int64_t grid = (limit < SMEM_LIMIT ? room : sms) / cluster;
   if (most < grid) grid = most;
@@ -569,7 +587,22 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
   at[1].val.clusterDim = {(unsigned)cluster, 1, 1};
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tx, tw, txs, tws, p);
+  // (the limit of shared memory is raised once a device, and once more where a launch says that it was lost with the context)
+  static std::atomic<int> set_for{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool set = set_for.load(std::memory_order_relaxed) == dev + 1;
+  for (int pass = 0;; pass++) {
+    if (!set || pass > 0) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
+      if (e != cudaSuccess) return e;
+      set_for.store(dev + 1, std::memory_order_relaxed);
+    }
+    e = cudaLaunchKernelEx(&cfg, kern, tx, tw, txs, tws, p);
+    if (!(e == cudaErrorInvalidValue && set && pass == 0)) return e;
+    (void)cudaGetLastError();
+  }
 }
 
 // How a call is cut: tokens of a tile, by one CTA (128 weight rows) or a pair (256), and about how many items that makes.

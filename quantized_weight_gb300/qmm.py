@@ -525,15 +525,20 @@ def mx4_scales(plain) -> torch.Tensor:
     return tiles.reshape(*lead, down * across * 512)
 
 
-def _mx_matrix(codes, scales, name, lead):
+def _mx_matrix(codes, scales, name, lead=()):
     """(rows, K, pointers) of a microscaled matrix [*lead, rows, K / 8] and its scales."""
     shape = codes.shape
+    if len(shape) == 2 and not lead:
+        rows, k8 = shape
+        size = ((rows + 127) >> 7) * ((k8 + 15) >> 4) * 512
+        if (codes.dtype is _I32 and codes.is_cuda and codes.is_contiguous() and k8 & 3 == 0 and scales.dtype is _U8
+                and scales.shape == (size,) and scales.is_contiguous() and codes.get_device() == scales.get_device() == _device()):
+            return rows, k8 * 8, codes.data_ptr(), scales.data_ptr()
     if len(shape) != len(lead) + 2 or shape[:-2] != lead:
         raise ValueError(f"{name} must be [{', '.join(map(str, (*lead, 'rows', 'K / 8')))}], got {tuple(shape)}")
     rows, K = shape[-2], shape[-1] * 8
     pc = _here(codes, name, _I32, shape)
-    size = mx4_scales_size(rows, K)
-    return rows, K, pc, _here(scales, "scales", _U8, (*lead, size) if lead else (size,))
+    return rows, K, pc, _here(scales, "scales", _U8, (*lead, mx4_scales_size(rows, K)))
 
 
 def mx4_quantize(x, out=None, stream=None):
@@ -583,7 +588,7 @@ def _mx_out(out, shape, dtype, device, stream):
 def mx4_gemm(x_codes, x_scales, codes, scales, gated=False, dtype=torch.float32, out=None, stream=None) -> torch.Tensor:
     """y [M, N] = x . w^T of microscaled x [M, K] and w [N, K], float32 or bfloat16; gated: codes and scales hold two matrices
     [2, N, K], and y = silu(x . g^T) * (x . u^T).  With out, dtype is out's."""
-    M, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes", ())
+    M, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes")
     N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (2,) if gated else ())
     if KW != K:
         raise ValueError(f"x has rows of {K}, the weights of {KW}")
@@ -651,7 +656,7 @@ def moe_gemm(x_codes, x_scales, codes, scales, starts, counts, routed=None, gate
     """mx4_gemm of each expert's rows of x [R, K] with its matrix of codes [E, N, K / 8] (gated: [E, 2, N, K / 8]): y [R, N].
     Rows of no expert are left alone (without `out`: as memory happens to be).  routed: how many rows the experts have
     together, about (default: R); it picks the launch's shape."""
-    R, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes", ())
+    R, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes")
     E = starts.shape[0]
     N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (E, 2) if gated else (E,))
     if KW != K:
