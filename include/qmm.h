@@ -426,10 +426,13 @@ int qmm_moe_plan(const void *logits, int dtype, int64_t stride, int64_t T, int64
                  int32_t *experts, float *weights, int32_t *places, int32_t *starts, int32_t *counts, qmm_stream_t stream);
 
 /*
- * qmm_moe_quantize -- qmm_mx4_quantize of x [T, K], token t's row going to the rows places[t, 0 .. k - 1] of codes and scales
- *   (R rows).  A place outside [0, R) is skipped; two entries must not have the same place.  Rows of no place are left alone.
+ * qmm_moe_quantize -- qmm_mx4_quantize of the rows of tokens that are routed, to codes and scales of R rows.
+ *   sorted == 0: x [T, K], token t's row goes to the rows places[t, 0 .. k - 1] (what a first product of the experts takes);
+ *   sorted != 0: x [R, K] is sorted already, and each row places[t, j] stays that row (what a second one takes).
+ *   A place outside [0, R) is skipped; two entries must not have the same place.  Rows of no place are left alone, and not
+ *   read.  T * k < 2^31.
  */
-int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, const int32_t *places, uint32_t *codes,
+int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, int sorted, const int32_t *places, uint32_t *codes,
                      uint8_t *scales, int64_t T, int64_t k, int64_t R, int64_t K, qmm_stream_t stream);
 
 /*

@@ -377,13 +377,13 @@ int qmm_moe_plan(const void *logits, int dtype, int64_t stride, int64_t T, int64
   return cuda_status(qmm::launch_moe_plan(a, stream));
 }
 
-int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, const int32_t *places, uint32_t *codes,
+int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, int sorted, const int32_t *places, uint32_t *codes,
                      uint8_t *scales, int64_t T, int64_t k, int64_t R, int64_t K, qmm_stream_t stream) {
   if (!dtype_ok(dtype)) return QMM_ERR_UNSUPPORTED;
   int st = check_mx4(1, T, K);
   if (st == QMM_OK) st = check_mx4(1, R, K);
   if (st != QMM_OK) return st;
-  if (k < 1 || k > qmm::kMoeMaxK) return QMM_ERR_SHAPE;
+  if (k < 1 || k > qmm::kMoeMaxK || T * k >= kMaxDim) return QMM_ERR_SHAPE;
   if (T == 0 || R == 0 || K == 0) return QMM_OK;
   if (!x || !places || !codes || !scales) return QMM_ERR_ARG;
   if (!aligned16(x) || !aligned4(places) || !aligned16(codes) || !aligned16(scales) ||
@@ -392,6 +392,7 @@ int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, const int32
   qmm::Mx4QuantArgs a{};
   a.x = x, a.x_row = x_row_stride, a.places = places, a.codes = codes, a.scales = scales;
   a.matrices = 1, a.rows = T, a.K = K, a.k = k, a.out_rows = R, a.bf16 = dtype == QMM_BF16;
+  a.sorted = sorted != 0;
   return cuda_status(qmm::launch_mx4_quantize(a, stream));
 }
 

@@ -16,7 +16,7 @@ struct Mx4QuantArgs {
   void *codes, *scales;
   int64_t matrices, rows, K;
   int64_t k, out_rows;             // of places
-  bool bf16;
+  bool bf16, sorted;               // sorted: x has out_rows rows, and each place's row stays there
 };
 cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s);
 cudaError_t launch_mx4_dequant(const void *codes, const void *scales, float *w, int64_t matrices, int64_t rows, int64_t K,

@@ -84,6 +84,7 @@ struct QuantParams {
   int64_t rows, K, k_tiles;
   int64_t scale_bytes;                       // of a matrix
   int64_t k, out_rows;
+  int sorted;                                // x has the places' rows, and an entry of them is a token
   uint32_t units;                            // warps' pieces of work: of
   Divisor chunks, lanes, row_tiles;          // chunks of a row, rows r % 32 of a tile that exist in some tile, tiles of a matrix
 };
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   }
 }
 
-// A warp takes up to 4 chunks of a token's row, and stores them to each of its places.
+// A warp takes up to 4 chunks of a token's row, and stores them to each of its places (sorted: the place's own row).
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) quantize_routed_kernel(const QuantParams p) {
   pdl_wait();
@@ -142,11 +143,16 @@ __global__ void __launch_bounds__(kThreads) quantize_routed_kernel(const QuantPa
   if (chunk >= p.units) return;
   const int64_t t = p.chunks.split(chunk), col0 = (int64_t)chunk * (4 * kChunk) + 8 * lane;
   const int mine = lane < p.k ? p.places[t * p.k + lane] : -1;
+  int64_t from = t;
+  if (p.sorted) {
+    from = __shfl_sync(0xFFFFFFFFu, mine, 0);
+    if (from < 0 || from >= p.out_rows) return;
+  }
   Raw<BF16> raw[4];
 #pragma unroll
   for (int g = 0; g < 4; g++) {
     raw[g] = Raw<BF16>{};
-    if (col0 + g * kChunk < p.K) raw[g] = load8<BF16>(p.x, t * p.x_row + col0 + g * kChunk);
+    if (col0 + g * kChunk < p.K) raw[g] = load8<BF16>(p.x, from * p.x_row + col0 + g * kChunk);
   }
   uint32_t codes[4], words[4];
 #pragma unroll
@@ -221,11 +227,11 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
   p.x = a.x, p.x_matrix = a.x_matrix, p.x_row = a.x_row, p.places = a.places;
   p.codes = static_cast<uint32_t *>(a.codes), p.scales = static_cast<uint8_t *>(a.scales);
   p.rows = a.rows, p.K = a.K, p.k_tiles = mx4_k_tiles(a.K), p.scale_bytes = mx4_scales_bytes(a.rows, a.K);
-  p.k = a.k, p.out_rows = a.out_rows;
+  p.k = a.sorted ? 1 : a.k, p.out_rows = a.out_rows, p.sorted = a.sorted;
   int64_t units;
   if (a.places) {
     p.chunks = Divisor((uint32_t)((a.K + 4 * kChunk - 1) / (4 * kChunk)));
-    units = a.rows * p.chunks.d;
+    units = (a.sorted ? a.rows * a.k : a.rows) * p.chunks.d;
   } else {
     const int each = kChunk * (a.bf16 ? chunks_a_warp<true>() : chunks_a_warp<false>());
     p.chunks = Divisor((uint32_t)((a.K + each - 1) / each));

@@ -89,7 +89,7 @@ def lib():
             L.qmm_moe_rows.argtypes = [i64, i64, i64]
             L.qmm_moe_rows.restype = i64
             L.qmm_moe_plan.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
-            L.qmm_moe_quantize.argtypes = [vp, i32, i64, vp, vp, vp, i64, i64, i64, i64, vp]
+            L.qmm_moe_quantize.argtypes = [vp, i32, i64, i32, vp, vp, vp, i64, i64, i64, i64, vp]
             L.qmm_moe_gemm.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i64, i64, i64, i64, i64, vp]
             L.qmm_moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
             L.qmm_check.argtypes = [vp]
@@ -634,12 +634,15 @@ def moe_plan(logits, k, normalize=True, out=None, stream=None):
     return out
 
 
-def moe_quantize(x, places, rows, out=None, stream=None):
-    """mx4_quantize of x [T, K], each token's row to its places [T, k]: (codes int32 [rows, K / 8], scales).  Other rows are
-    left alone (without `out`: as memory happens to be; no product of another row reads them)."""
+def moe_quantize(x, places, rows, out=None, sorted=False, stream=None):
+    """mx4_quantize of x [T, K], each token's row to its places [T, k]: (codes int32 [rows, K / 8], scales).  sorted: x
+    [rows, K] is sorted by expert already, and the rows of the places stay where they are.  Other rows are left alone (without
+    `out`: as memory happens to be; no product of another row reads them)."""
     dt, row = _mx_dtype(x.dtype), _mx_rows(x, "x")
-    T, K = x.shape
-    k = places.shape[-1]
+    n, K = x.shape
+    T, k = places.shape
+    if n != (rows if sorted else T):
+        raise ValueError(f"x must be [{rows if sorted else T}, K], got {tuple(x.shape)}")
     pp = _here(places, "places", _I32, (T, k))
     size = mx4_scales_size(rows, K)
     if out is None:
@@ -647,7 +650,7 @@ def moe_quantize(x, places, rows, out=None, stream=None):
         pc, ps = out[0].data_ptr(), out[1].data_ptr()
     else:
         pc, ps = _here(out[0], "codes", _I32, (rows, K // 8)), _here(out[1], "scales", _U8, (size,))
-    _call("qmm_moe_quantize", lib().qmm_moe_quantize(x.data_ptr(), dt, row, pp, pc, ps, T, k, rows, K, _stream(stream)))
+    _call("qmm_moe_quantize", lib().qmm_moe_quantize(x.data_ptr(), dt, row, sorted, pp, pc, ps, T, k, rows, K, _stream(stream)))
     return out
 
 

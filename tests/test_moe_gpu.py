@@ -126,6 +126,37 @@ def test_quantize_routed(T, qmm, n, K, E, k, dtype):
     assert (codes[T.from_numpy(~held).cuda()] == 0x5A5A5A5A).all() and (got[every[~held]] == 99).all()
 
 
+@pytest.mark.parametrize("n,K,E,k", [(1, 32, 4, 1), (9, 160, 8, 3), (70, 1056, 5, 2), (300, 2048, 64, 8)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_quantize_sorted(T, qmm, n, K, E, k, dtype):
+    """Only the rows of the places: others are neither read (NaN there reaches nothing) nor written."""
+    rng = np.random.default_rng(n + K)
+    l = rng.standard_normal((n, E)).astype(np.float32)
+    l[rng.random((n, E)) < 0.3] = -np.inf
+    _, _, places, _, _ = qmm.moe_plan(T.from_numpy(l).cuda(), k)
+    R = qmm.moe_rows(n, E, k)
+    p = places.cpu().numpy()
+    held = np.zeros(R, bool)
+    held[p[p >= 0]] = True
+    x = spread(rng, R, K)
+    x[~held] = np.nan
+    x = T.from_numpy(x).cuda().to(getattr(T, dtype))
+    codes = T.full((R, K // 8), 0x5A5A5A5A, dtype=T.int32, device="cuda")
+    scales = T.full((qmm.mx4_scales_size(R, K),), 99, dtype=T.uint8, device="cuda")
+    qmm.moe_quantize(x, places, R, sorted=True, out=(codes, scales))
+    qmm.check()
+    want, s = ref.quantize(x.float().cpu().numpy()[held])
+    at, _ = ref.scale_at(R, K)
+    every, _ = ref.scale_at(R, -(-K // 128) * 128)
+    got = scales.cpu().numpy()
+    assert np.array_equal(got[at[held]], s) and (got[every[~held]] == 99).all() and not got[every[held][:, K // 32:]].any()
+    good = np.repeat(s != 255, 32, axis=1)
+    assert np.array_equal(ref.unpack(codes.cpu().numpy())[held][good], want[good])
+    assert (codes[T.from_numpy(~held).cuda()] == 0x5A5A5A5A).all()
+    with pytest.raises(ValueError):
+        qmm.moe_quantize(x, places, R + 128, sorted=True)
+
+
 def test_places_outside_are_skipped(T, qmm):
     x = T.ones(4, 64, device="cuda")
     places = T.tensor([[0, -1], [128, 3], [1 << 30, -(1 << 31)], [127, 1]], dtype=T.int32, device="cuda")
@@ -133,6 +164,9 @@ def test_places_outside_are_skipped(T, qmm):
     qmm.moe_quantize(x, places, 128, out=(codes[:128], scales[:512]))
     y = qmm.mx4_dequant(codes[:128], scales[:512])
     assert sorted(y[:, 0].nonzero().flatten().tolist()) == [0, 1, 3, 127] and not codes[128].any() and not scales[512:].any()
+    codes.zero_()
+    qmm.moe_quantize(T.ones(128, 64, device="cuda"), places, 128, sorted=True, out=(codes[:128], scales[:512]))
+    assert T.equal(y, qmm.mx4_dequant(codes[:128], scales[:512])) and not codes[128].any()
     out = qmm.moe_combine(y, T.full((4, 2), 2.0, device="cuda"), places)
     assert out[:, 5].tolist() == [2.0, 2.0, 0.0, 4.0]
     w = T.tensor([[1.0, float("nan")]] * 4, device="cuda")
@@ -242,7 +276,7 @@ def layer(qmm, x, logits, k, w1, w2):
     _, weights, places, starts, counts = qmm.moe_plan(logits, k)
     n, R = x.shape[0], qmm.moe_rows(*logits.shape, k)
     h = qmm.moe_gemm(*qmm.moe_quantize(x, places, R), *w1, starts, counts, routed=n * k, gated=True, dtype=x.dtype)
-    y = qmm.moe_gemm(*qmm.mx4_quantize(h), *w2, starts, counts, routed=n * k, dtype=x.dtype)
+    y = qmm.moe_gemm(*qmm.moe_quantize(h, places, R, sorted=True), *w2, starts, counts, routed=n * k, dtype=x.dtype)
     return qmm.moe_combine(y, weights, places), h, y
 
 

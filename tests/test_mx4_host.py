@@ -35,8 +35,8 @@ def plan(L, l=FAKE, dtype=0, stride=8, T=4, E=8, k=2, e=FAKE, w=FAKE, p=FAKE, st
     return L.qmm_moe_plan(l, dtype, stride, T, E, k, 1, e, w, p, st, n, None)
 
 
-def routed(L, x=FAKE, dtype=0, xr=64, p=FAKE, c=FAKE, s=FAKE, T=4, k=2, R=128, K=64):
-    return L.qmm_moe_quantize(x, dtype, xr, p, c, s, T, k, R, K, None)
+def routed(L, x=FAKE, dtype=0, xr=64, p=FAKE, c=FAKE, s=FAKE, T=4, k=2, R=128, K=64, sorted=0):
+    return L.qmm_moe_quantize(x, dtype, xr, sorted, p, c, s, T, k, R, K, None)
 
 
 def experts(L, x=FAKE, xs=FAKE, c=FAKE, s=FAKE, st=FAKE, n=FAKE, y=FAKE, dtype=0, gated=0, m=8, R=128, E=4, N=4, K=64):
@@ -62,6 +62,7 @@ def test_quantize(L):
     assert quantize(L, n=3, rows=715827882, x=None) == ARG and quantize(L, n=3, rows=715827883) == SHAPE
     assert routed(L, T=0) == OK and routed(L, R=0) == OK and routed(L, T=-1) == SHAPE and routed(L, R=BIG) == SHAPE
     assert routed(L, k=0) == SHAPE and routed(L, k=33) == SHAPE and routed(L, k=32, x=None) == ARG
+    assert routed(L, T=1 << 30, k=2) == SHAPE and routed(L, T=(1 << 30) - 1, k=2, sorted=1, x=None) == ARG
     assert routed(L, p=None) == ARG and routed(L, p=ODD) == ALIGN and routed(L, p=MIS, x=None) == ARG
 
 
