@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "kv_attend.h"
 #include "kv_launch.h"
 #include "mx4.cuh"
 #include "mx4_launch.h"
@@ -18,61 +19,87 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 256;         // elements that a warp takes at once: 8 a lane, 4 lanes a block, 2 scale tiles
-
-// A lane's 8 elements.
-struct Eight {
-  float v[8];
-};
-
+// Elements of a row that a lane takes: 64 or 32 bytes.  bfloat16 is bound by instructions as much as by memory, and what a
+// block costs once (its scale, the maximum over its lanes) is then shared by two lanes rather than four; float32 is not, and
+// its loads are better at 32 bytes a lane.
 template <bool BF16>
+constexpr int per_lane() { return BF16 ? 16 : 8; }
+template <bool BF16>
+constexpr int chunk_of() { return 32 * per_lane<BF16>(); }     // of a warp
+constexpr int kLoads = 2;                                      // of 16 bytes, a lane
+
 struct Raw {
-  uint4 a, b;                       // b: float32 only
+  uint4 a[kLoads];
 };
 
 template <bool BF16>
-__device__ __forceinline__ Raw<BF16> load8(const void *x, int64_t at) {
-  Raw<BF16> r{};
-  if constexpr (BF16) {
-    r.a = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + at));
-  } else {
-    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(x) + at);
-    r.a = __ldcs(p);
-    r.b = __ldcs(p + 1);
-  }
+__device__ __forceinline__ Raw load(const void *x, int64_t at) {
+  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + at * (BF16 ? 2 : 4));
+  Raw r;
+#pragma unroll
+  for (int i = 0; i < kLoads; i++) r.a[i] = __ldcs(p + i);
   return r;
 }
 
+// A lane's words of codes, and the scale of its block (the same in all of the block's lanes).  The whole warp calls it.
 template <bool BF16>
-__device__ __forceinline__ Eight widen(const Raw<BF16> &r) {
-  Eight e;
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+struct Codes {
+  uint32_t w[per_lane<BF16>() / 8];
+};
+template <bool BF16>
+__device__ __forceinline__ Codes<BF16> encode(const Raw &raw, uint32_t &scale) {
+  constexpr int N = per_lane<BF16>();
+  float v[N];
 #pragma unroll
-  for (int i = 0; i < 8; i++)
-    e.v[i] = BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
-  return e;
-}
-
-// A lane's word of codes, and the scale of its block (the same in its 4 lanes).  The whole warp calls it.
-__device__ __forceinline__ uint32_t encode8(const Eight &e, uint32_t &scale) {
-  const float a = max3_nan(max3_nan(fabsf(e.v[0]), fabsf(e.v[1]), fabsf(e.v[2])), fabsf(e.v[3]), fabsf(e.v[4]));
-  uint32_t m = __float_as_uint(max3_nan(max3_nan(a, fabsf(e.v[5]), fabsf(e.v[6])), fabsf(e.v[7]), 0.0f));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));     // (of values that are not negative, the bits order as they do)
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  for (int i = 0; i < kLoads; i++) {
+    const uint32_t w[4] = {raw.a[i].x, raw.a[i].y, raw.a[i].z, raw.a[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if constexpr (BF16) {
+        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        v[4 * i + j] = __uint_as_float(w[j]);
+      }
+  }
+  float most = fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i + 1 < N; i += 2) most = max3_nan(most, fabsf(v[i]), fabsf(v[i + 1]));
+  uint32_t m = __float_as_uint(max3_nan(most, fabsf(v[N - 1]), 0.0f));
+#pragma unroll
+  for (int o = 1; o < kMxBlock / N; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));   // (not negative: bits order as values)
   const uint32_t top = (m >> 23) & 255;               // exponent field; 255: an infinity or a NaN is there
   scale = top == 255 ? 255 : top < 2 ? 0 : top - 2;
-  const float inv = __uint_as_float((254 - min(scale, 253u)) << 23);      // 2 ** (127 - scale)
-  float v[8];
+  const float inv = __uint_as_float((254 - scale) << 23);     // 2 ** (127 - scale)
+  Codes<BF16> c;
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = e.v[i] * inv;
-  return mx4_encode(v);
+  for (int i = 0; i < N; i += 8) {
+    float u[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) u[j] = v[i + j] * inv;
+    c.w[i / 8] = mx4_encode(u);
+  }
+  return c;
 }
 
-// The four scales of a scale tile's row, in lanes 0..15 those of the first tile of a chunk, in 16..31 the second's.
+// The four scales of a scale tile's row, in all lanes of its 128 elements.
+template <bool BF16>
 __device__ __forceinline__ uint32_t scale_word(uint32_t scale, int lane) {
-  uint32_t w = scale << (8 * ((lane >> 2) & 3));
-  w |= __shfl_xor_sync(0xFFFFFFFFu, w, 4);
-  return w | __shfl_xor_sync(0xFFFFFFFFu, w, 8);
+  constexpr int LANES = kMxBlock / per_lane<BF16>();  // of a block
+  uint32_t w = scale << (8 * ((lane / LANES) & 3));
+  w |= __shfl_xor_sync(0xFFFFFFFFu, w, LANES);
+  return w | __shfl_xor_sync(0xFFFFFFFFu, w, 2 * LANES);
+}
+// Lanes of a scale tile's row.
+template <bool BF16>
+constexpr int tile_lanes() { return kMxTileK / per_lane<BF16>(); }
+
+template <bool BF16>
+__device__ __forceinline__ void put_codes(uint32_t *codes, int64_t at, const Codes<BF16> &c) {
+  if constexpr (BF16)
+    *reinterpret_cast<uint2 *>(codes + (at >> 3)) = make_uint2(c.w[0], c.w[1]);
+  else
+    codes[at >> 3] = c.w[0];
 }
 
 struct QuantParams {
@@ -89,11 +116,8 @@ struct QuantParams {
   Divisor chunks, lanes, row_tiles;          // chunks of a row, rows r % 32 of a tile that exist in some tile, tiles of a matrix
 };
 
-// A warp takes a chunk (of bfloat16, two) of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes
-// in a row of the scale tile, and 4 KB of loads are in flight a warp.
-template <bool BF16>
-constexpr int chunks_a_warp() { return BF16 ? 2 : 1; }
-
+// A warp takes a chunk of the four rows r, r + 32, r + 64 and r + 96 of a tile: their scales are 16 bytes in a row of the
+// scale tile, and 4 KB of loads are in flight a warp.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p) {
   pdl_wait();
@@ -103,73 +127,70 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantParams p)
   if (chunk >= p.units) return;
   uint32_t r32 = p.chunks.split(chunk), tile = p.lanes.split(r32);
   const int64_t matrix = p.row_tiles.split(tile);
-  constexpr int CHUNKS = chunks_a_warp<BF16>();
-  const int64_t row0 = (int64_t)tile * kMxRows + r32, col0 = (int64_t)chunk * (CHUNKS * kChunk) + 8 * lane;
+  const int64_t row0 = (int64_t)tile * kMxRows + r32, col = (int64_t)chunk * chunk_of<BF16>() + per_lane<BF16>() * lane;
   if (row0 >= p.rows) return;
-  Raw<BF16> raw[CHUNKS][4];
+  const bool in = col < p.K;
+  Raw raw[4];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; c++)
-#pragma unroll
-    for (int g = 0; g < 4; g++) {
-      raw[c][g] = Raw<BF16>{};
-      if (col0 + c * kChunk < p.K && row0 + 32 * g < p.rows)
-        raw[c][g] = load8<BF16>(p.x, matrix * p.x_matrix + (row0 + 32 * g) * p.x_row + col0 + c * kChunk);
-    }
-#pragma unroll
-  for (int c = 0; c < CHUNKS; c++) {
-    uint32_t words[4];
-    const int64_t col = col0 + c * kChunk;
-#pragma unroll
-    for (int g = 0; g < 4; g++) {
-      uint32_t scale;
-      const uint32_t code = encode8(widen(raw[c][g]), scale);
-      words[g] = scale_word(scale, lane);
-      if (col < p.K && row0 + 32 * g < p.rows) p.codes[((matrix * p.rows + row0 + 32 * g) * p.K + col) >> 3] = code;
-    }
-    const int64_t kt = ((int64_t)chunk * CHUNKS + c) * 2 + (lane >> 4);
-    if ((lane & 15) == 0 && kt < p.k_tiles)
-      *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
-          make_uint4(words[0], words[1], words[2], words[3]);
+  for (int g = 0; g < 4; g++) {
+    raw[g] = Raw{};
+    if (in && row0 + 32 * g < p.rows) raw[g] = load<BF16>(p.x, matrix * p.x_matrix + (row0 + 32 * g) * p.x_row + col);
   }
+  uint32_t words[4];
+#pragma unroll
+  for (int g = 0; g < 4; g++) {
+    uint32_t scale;
+    const Codes<BF16> codes = encode<BF16>(raw[g], scale);
+    words[g] = scale_word<BF16>(scale, lane);
+    if (in && row0 + 32 * g < p.rows) put_codes<BF16>(p.codes, (matrix * p.rows + row0 + 32 * g) * p.K + col, codes);
+  }
+  constexpr int TL = tile_lanes<BF16>();
+  const int64_t kt = (int64_t)chunk * (32 / TL) + lane / TL;
+  if (lane % TL == 0 && kt < p.k_tiles)
+    *reinterpret_cast<uint4 *>(p.scales + matrix * p.scale_bytes + mx4_scale_word(row0, kt, p.k_tiles)) =
+        make_uint4(words[0], words[1], words[2], words[3]);
 }
 
-// A warp takes up to 4 chunks of a token's row, and stores them to each of its places (sorted: the place's own row).
-template <bool BF16>
+// A warp takes CHUNKS chunks of a token's row, and stores them to each of its places (sorted: the place's own row).
+template <bool BF16, int CHUNKS>
 __global__ void __launch_bounds__(kThreads) quantize_routed_kernel(const QuantParams p) {
   pdl_wait();
   pdl_launch_dependents();
+  constexpr int CHUNK = chunk_of<BF16>(), TL = tile_lanes<BF16>();
   const int lane = threadIdx.x & 31;
   uint32_t chunk = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (chunk >= p.units) return;
-  const int64_t t = p.chunks.split(chunk), col0 = (int64_t)chunk * (4 * kChunk) + 8 * lane;
+  const int64_t t = p.chunks.split(chunk), col0 = (int64_t)chunk * (CHUNKS * CHUNK) + per_lane<BF16>() * lane;
   const int mine = lane < p.k ? p.places[t * p.k + lane] : -1;
   int64_t from = t;
   if (p.sorted) {
     from = __shfl_sync(0xFFFFFFFFu, mine, 0);
     if (from < 0 || from >= p.out_rows) return;
   }
-  Raw<BF16> raw[4];
+  Raw raw[CHUNKS];
 #pragma unroll
-  for (int g = 0; g < 4; g++) {
-    raw[g] = Raw<BF16>{};
-    if (col0 + g * kChunk < p.K) raw[g] = load8<BF16>(p.x, from * p.x_row + col0 + g * kChunk);
+  for (int g = 0; g < CHUNKS; g++) {
+    raw[g] = Raw{};
+    if (col0 + g * CHUNK < p.K) raw[g] = load<BF16>(p.x, from * p.x_row + col0 + g * CHUNK);
   }
-  uint32_t codes[4], words[4];
+  Codes<BF16> codes[CHUNKS];
+  uint32_t words[CHUNKS];
 #pragma unroll
-  for (int g = 0; g < 4; g++) {
+  for (int g = 0; g < CHUNKS; g++) {
     uint32_t scale;
-    codes[g] = encode8(widen(raw[g]), scale);
-    words[g] = scale_word(scale, lane);
+    codes[g] = encode<BF16>(raw[g], scale);
+    words[g] = scale_word<BF16>(scale, lane);
   }
+  const int64_t kt0 = (int64_t)chunk * (CHUNKS * 32 / TL) + lane / TL;
   for (int j = 0; j < (int)p.k; j++) {
     const int64_t row = __shfl_sync(0xFFFFFFFFu, mine, j);
     if (row < 0 || row >= p.out_rows) continue;
+    uint8_t *scales = p.scales + mx4_scale_word(row, kt0, p.k_tiles);
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-      const int64_t col = col0 + g * kChunk, kt = (col - 8 * lane) / kMxTileK + (lane >> 4);
-      if (col < p.K) p.codes[(row * p.K + col) >> 3] = codes[g];
-      if ((lane & 15) == 0 && kt < p.k_tiles)
-        *reinterpret_cast<uint32_t *>(p.scales + mx4_scale_word(row, kt, p.k_tiles)) = words[g];
+    for (int g = 0; g < CHUNKS; g++) {
+      if (col0 + g * CHUNK < p.K) put_codes<BF16>(p.codes, row * p.K + col0 + g * CHUNK, codes[g]);
+      if (lane % TL == 0 && kt0 + g * (32 / TL) < p.k_tiles)
+        *reinterpret_cast<uint32_t *>(scales + g * (32 / TL) * kMxTileBytes) = words[g];
     }
   }
 }
@@ -229,12 +250,17 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
   p.rows = a.rows, p.K = a.K, p.k_tiles = mx4_k_tiles(a.K), p.scale_bytes = mx4_scales_bytes(a.rows, a.K);
   p.k = a.sorted ? 1 : a.k, p.out_rows = a.out_rows, p.sorted = a.sorted;
   int64_t units;
+  const int chunk = a.bf16 ? chunk_of<true>() : chunk_of<false>();
+  int chunks = a.bf16 ? 2 : 4;       // of a warp, of routed rows
   if (a.places) {
-    p.chunks = Divisor((uint32_t)((a.K + 4 * kChunk - 1) / (4 * kChunk)));
-    units = (a.sorted ? a.rows * a.k : a.rows) * p.chunks.d;
+    // (fewer where a row has not so many, or where there are too few rows to occupy the SMs)
+    const int64_t rows = a.sorted ? a.rows * a.k : a.rows;
+    auto pieces = [&](int c) { return (a.K + c * chunk - 1) / (c * chunk); };
+    while (chunks > 1 && (rows * pieces(chunks) < 16 * kv_sms() || pieces(chunks / 2) == 1)) chunks /= 2;
+    p.chunks = Divisor((uint32_t)pieces(chunks));
+    units = rows * p.chunks.d;
   } else {
-    const int each = kChunk * (a.bf16 ? chunks_a_warp<true>() : chunks_a_warp<false>());
-    p.chunks = Divisor((uint32_t)((a.K + each - 1) / each));
+    p.chunks = Divisor((uint32_t)((a.K + chunk - 1) / chunk));
     p.lanes = Divisor(a.rows < 32 ? (uint32_t)a.rows : 32);
     p.row_tiles = Divisor((uint32_t)((a.rows + kMxRows - 1) / kMxRows));
     units = a.matrices * p.row_tiles.d * p.lanes.d * p.chunks.d;
@@ -242,8 +268,10 @@ cudaError_t launch_mx4_quantize(const Mx4QuantArgs &a, cudaStream_t s) {
   if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;      // (more than a TB of codes)
   p.units = (uint32_t)units;
   const int64_t grid = (units + kWarps - 1) / kWarps;
-  auto kern = a.places ? (a.bf16 ? quantize_routed_kernel<true> : quantize_routed_kernel<false>)
-                       : (a.bf16 ? quantize_kernel<true> : quantize_kernel<false>);
+  auto kern = a.bf16 ? quantize_kernel<true> : quantize_kernel<false>;
+  if (a.places && a.bf16) kern = chunks == 2 ? quantize_routed_kernel<true, 2> : quantize_routed_kernel<true, 1>;
+  if (a.places && !a.bf16)
+    kern = chunks == 4 ? quantize_routed_kernel<false, 4> : chunks == 2 ? quantize_routed_kernel<false, 2> : quantize_routed_kernel<false, 1>;
   return launch_after(kern, grid, kThreads, 0, s, p);
 }
 
