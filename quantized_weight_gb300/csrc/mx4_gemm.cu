@@ -345,6 +345,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
         const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
         const uint32_t at0 = base0 >> 4, stage16 = stage_bytes >> 4;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
+          // (one reduction a stage: its slot, whether sums are there already, its MMAs; before the wait, which takes as long)
+          const uint32_t now = uniform(ring.s | (uint32_t)(ks > ks0) << 8 | (uint32_t)min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)) << 16);
           if constexpr (!SPLITS) {
             if (!__all_sync(0xFFFFFFFFu, wait_bounded(full(ring.s), ring.ph, ctl))) { ok = false; break; }
             tc_fence_after();
@@ -360,8 +362,6 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             tc_fence_after();
           }
           if constexpr (SPLITS) ready--;
-          // (one reduction a stage: its slot, whether sums are there already, its MMAs)
-          const uint32_t now = uniform(ring.s | (uint32_t)(ks > ks0) << 8 | (uint32_t)min(BK / MMA_K, p.k_steps - ks * (BK / MMA_K)) << 16);
           const uint32_t slot = now & 255, more = now >> 8 & 1, steps = now >> 16;
           // scales: by turns in two places, 8 columns a weight tile (4 a scale tile) and 16 for the tokens
           const uint32_t sfa = sf0 + (slot & 1) * (SF_COLS / 2), sfb = sfa + 8 * TWO;
