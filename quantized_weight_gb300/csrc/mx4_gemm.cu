@@ -54,7 +54,6 @@ constexpr int BK = 256;                    // elements of a stage: 128 bytes of 
 constexpr int MMA_K = 64;
 constexpr int EPI_WARP0 = 2, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int MAX_STAGES = 8;
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), CTAS * EPI_THREADS);
+      mbar_init(acc_empty(b), CTAS * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     mbar_init(never_bar, 1);
@@ -414,10 +413,13 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
           }
         tmem_ld_wait();
         tc_fence_before();
-        if (in_pair == 0)
-          mbar_arrive(acc_empty(buf));
-        else
-          mbar_arrive_cluster(mapa_shared(acc_empty(buf), 0));
+        __syncwarp();
+        if (lane == 0) {                       // (an arrival a thread, and of a pair from the other CTA, took 1 us)
+          if (in_pair == 0)
+            mbar_arrive(acc_empty(buf));
+          else
+            mbar_arrive_cluster(mapa_shared(acc_empty(buf), 0));
+        }
         if (SPLITS && p.split > 1) {
           if (local == 0) cluster_wait();      // (no CTA writes into one that has not begun)
           // token t of the tile belongs to rank t % split, as its row t / split
@@ -618,21 +620,24 @@ struct Cut {
 
 // A stage of 256 elements takes so many ns, an item's beginning and end so many more, and the SMs take items in rounds: wide
 // tiles and pairs where there are many tokens, narrow ones where those fill the SMs better.  Measured, us, for tiles of 64,
-// 128, 192, 256 tokens and pairs with 256: 8192 x 8192 x 8192: 543, 281, 219, 183, 150; 1024 x 6144 x 2048 (float32): 21.3,
-// 13.9, 12.3, 15.1, 13.3; 256 x 4096 x 4096: 9.1, 9.4, 10.1, 11.1, 10.3; 4096 x 4096 x 1024: 26, 17, 15, 14.4, 15.5.  Gated, 64,
-// 128 and pairs with 128: 1024 x 4096 x 4096: 32, 20.5, 17.4; 8191 tokens by 6 of 64 experts of 1408 x 2048: -, 147, 150.
+// 128, 192, 256 tokens and pairs with 256: 8192 x 8192 x 8192: 543, 281, 219, 179, 152; 1024 x 6144 x 2048 (float32): 21.3,
+// 13.9, 12.1, 14.3, 14.2; 256 x 4096 x 4096: 9.1, 9.4, 10.1, 11.1, 10.3; 4096 x 4096 x 1024: 26, 17, 15, 14.6, 17.5.  8191 tokens by 6
+// of 64 experts of 2048 x 1408, 256 tokens and pairs: 87, 91; by 2 of 8 of 4096 x 4096: 107, 98.  Gated, 64 and 128 tokens and
+// pairs with 128: 1024 x 4096 x 4096: 32, 21.1, 18.6; 8191 tokens by 6 of 64 experts of 1408 x 2048: -, 139, 145, of 1536 x 4096:
+// -, 269, 234.
 Cut cut_for(bool gated, const Mx4GemmArgs &a, int sms) {
   // experts that are met and rows of each, about
   const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;
   const int64_t rows = a.starts ? (a.routed + met - 1) / met : a.M;
   const double stages = (double)((a.K + BK - 1) / BK);
   struct { int ts, ctas; double stage, item; } const ways[2][5] = {
-      {{64, 1, 320, 560}, {128, 1, 350, 810}, {192, 1, 380, 1070}, {256, 1, 410, 1320}, {256, 2, 320, 1800}},
-      {{64, 1, 400, 700}, {128, 1, 450, 950}, {128, 2, 360, 1500}}};
+      {{64, 1, 310, 500}, {128, 1, 320, 700}, {192, 1, 335, 1050}, {256, 1, 355, 1400}, {256, 2, 280, 2100}},
+      {{64, 1, 400, 400}, {128, 1, 450, 500}, {128, 2, 325, 1300}}};
   Cut best{0, 1, 0};
   double least = 0;
   for (const auto &w : ways[gated]) {
     if (w.ts == 0) break;
+    if (w.ts > 64 && 2 * rows <= w.ts) continue;       // (mostly empty)
     // (an expert's last tile is half empty on average)
     const double each = (double)rows / w.ts + 0.5, tiles = a.starts ? met * (each > 1 ? each : 1) : (double)((rows + w.ts - 1) / w.ts);
     const double items = tiles * (double)((a.N + BM * w.ctas - 1) / (BM * w.ctas));

@@ -191,7 +191,7 @@ def experts_case(T, rng, counts, N, K, gated):
 
 @pytest.mark.parametrize("counts,N,K", [([1], 1, 32), ([3, 0, 1], 130, 96), ([0, 0, 5, 0], 256, 512), ([8] * 9, 300, 1056),
                                         ([1, 1, 0, 1, 1, 0, 1, 1], 2048, 1408), ([129, 64, 65, 0, 300], 257, 288),
-                                        ([700, 5, 128, 256], 128, 640), ([40] * 30, 200, 352), ([33, 17, 250, 1, 0, 90], 384, 2080), ([900, 0, 300, 1, 513], 2000, 2208),
+                                        ([700, 5, 128, 256], 128, 640), ([40] * 30, 200, 352), ([33, 17, 250, 1, 0, 90], 384, 2080), ([900, 0, 300, 1, 513], 2000, 2720),
                                         ([257, 640, 128], 1100, 2080)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("gated", [False, True])
@@ -220,8 +220,8 @@ def test_experts_reach_pairs(qmm):
     if torch.cuda.get_device_properties(0).multi_processor_count != 152:
         pytest.skip("the rule counts SMs")
     R = 1024 + 384 + 128 + 640
-    assert qmm.mx4_gemm_tile(R, 2000, 2208, experts=5, routed=1714) > 1024
-    assert qmm.mx4_gemm_tile(R, 2000, 2208, gated=True, experts=5, routed=1714) > 1024
+    assert qmm.mx4_gemm_tile(R, 2000, 2720, experts=5, routed=1714) > 1024
+    assert qmm.mx4_gemm_tile(R, 2000, 2720, gated=True, experts=5, routed=1714) > 1024
     assert qmm.mx4_gemm_tile(128 * 9, 300, 1056, experts=9, routed=72) == 64
 
 

@@ -155,7 +155,7 @@ def test_every_kernel_is_reached(T, qmm):
 
 # the first two take pairs of CTAs (the second CTA without weight rows in the last tile, and tokens of one row), then gated
 # ones, then wide tiles of one
-LARGE = [(1500, 2900, 2208), (1281, 2900, 2048), (900, 1500, 2208), (641, 1300, 2080), (1281, 3000, 1024), (1000, 2900, 512)]
+LARGE = [(1500, 2900, 2720), (1281, 2900, 2592), (900, 1500, 2208), (641, 1300, 2080), (1281, 3000, 1024), (1000, 2900, 512)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)

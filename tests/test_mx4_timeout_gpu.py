@@ -30,7 +30,7 @@ def fails_once_then_is_right(T, qmm, call, out, check):
 
 # K in parts over a cluster; one item a block and several, by one CTA and by pairs; rings longer and shorter than K
 @pytest.mark.parametrize("M,N,K", [(8, 256, 4096), (3, 130, 96), (100, 20000, 512), (1000, 2900, 512), (1281, 3000, 1024),
-                                   (1500, 2900, 2208), (3000, 5000, 2048)])
+                                   (1500, 2900, 2720), (3000, 5000, 2048)])
 @pytest.mark.parametrize("gated", [False, True])
 def test_wait_runs_out(T, qmm, M, N, K, gated):
     rng = np.random.default_rng(M)
