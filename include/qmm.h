@@ -440,7 +440,8 @@ int qmm_moe_quantize(const void *x, int dtype, int64_t x_row_stride, int sorted,
  *   y[starts[e] + i, n] from x[starts[e] + i, :] and matrix e.  x has R rows, codes and scales E matrices (gated: 2 * E, an
  *   expert's two after one another).  Other rows of y are left alone.  An expert whose start is negative, past R or no
  *   multiple of 128 has no rows, and rows past R are left out; no two experts may share a row.
- *   routed: how many rows the experts have together, about (T * k); it only picks the launch's shape.  1 <= E <= 1024.
+ *   routed: how many rows the experts have together, about (T * k); it only picks the launch's shape (and so, for float32
+ *   sums that are not exact, their last bits).  1 <= E <= 1024.
  */
 int qmm_moe_gemm(const uint32_t *x_codes, const uint8_t *x_scales, const uint32_t *codes, const uint8_t *scales,
                  const int32_t *starts, const int32_t *counts, void *y, int dtype, int gated, int64_t routed, int64_t R,

@@ -4,7 +4,9 @@
 // the codes reach 6: the exponent field of max |x| less 2, no arithmetic.  x times the inverse power is exact in float32
 // (or far below the first border), so the codes are the nearest ones to the exact quotient, halves to the even code.
 //
-// All three kernels are bound by memory: a value is read once (2 or 4 bytes) and leaves as 17/32 of a byte.
+// A value is read once (2 or 4 bytes) and leaves as 17/32 of a byte.  Measured: 17408 x 5120 float32 56 us, all of measured HBM;
+// 8192 x 5120 bfloat16 18.3 us, 86 % (with 8 elements a lane 22.4: instructions); 4093 x 2048 bfloat16 to 8 places each 12.4 us,
+// 62 % (scattered rows, 4-byte scales); back, 17408 x 5120, 61 us, 98 % (with a lane's two stores 32 bytes apart 84).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -550,7 +550,10 @@ def mx4_quantize(x, out=None, stream=None):
     else:
         (*lead, rows, K), n = shape, shape[:-2].numel()
         if len(lead) > 1:
-            x = x.view(n, rows, K)                                    # (leading dimensions one after the other)
+            try:
+                x = x.view(n, rows, K)
+            except RuntimeError:
+                raise ValueError(f"the leading dimensions of x must be one after the other, got strides {x.stride()}") from None
         matrix = x.stride(0) if n > 1 else 0
         codes, scales = (*lead, rows, K // 8), (*lead, mx4_scales_size(rows, K))
     if out is None:
