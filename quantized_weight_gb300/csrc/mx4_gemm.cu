@@ -21,9 +21,9 @@
 // A call with few items splits K over the CTAs of a cluster: each writes its partial tile into the shared memory of the CTA
 // that owns the token, and the owner adds them up in the order of the ranks, so that the sum is the same every time.
 //
-// Measured: 8192 x 17408 x 5120 (bfloat16 out) 211 us, 6.9 PFLOP/s; what remains is the end of an item (its accumulator's
+// Measured: 8192 x 17408 x 5120 (bfloat16 out) 213 us, 6.9 PFLOP/s; what remains is the end of an item (its accumulator's
 // way to registers, the next one's first scales) and, of 8 %, the stores.  8 x 151936 x 2048 28 us, 86 % of measured HBM.  Few
-// and small items are bound by latency: 8 x 4096 x 4096 takes 7.1 us of a floor of 1.3, some 2 us of launch and set-up, 1.6 us
+// and small items are bound by latency: 8 x 4096 x 4096 takes 7.3 us of a floor of 1.3, some 2 us of launch and set-up, 1.6 us
 // for the first bytes, 0.6 us of products and 1.5 us to join the parts.
 //
 // Every wait is bounded (bounded_wait.cuh).  One that runs out ends the CTA's work: it writes nothing more, waits for its
@@ -125,10 +125,16 @@ __device__ __forceinline__ void store(void *y, int64_t at, float v) {
 template <bool BF16>
 __device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1.0f + (BF16 ? __expf(-z) : expf(-z))) * u; }
 
-// wait_bounded on a barrier that another CTA arrives at.
-__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  return wait_bounded(bar, parity, ctl) && mbar_try_wait_cluster(bar, parity);
+// wait_bounded for an accumulator, which of a pair the other CTA's epilogue frees, too.  The tensor core stands still
+// meanwhile, so the one warp that waits here tests for a while without sleeping (2 % of a gated prompt; the epilogue's eight
+// warps doing so cost more than they gain).
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, const WaitCtl &ctl) {
+  for (int i = 0; i < 4000; i++) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_test(bar, parity)) return true;
+    if (*ctl.abort) return false;
+  }
+  return wait_bounded(bar, parity, ctl) && (!CLUSTER || mbar_try_wait_cluster(bar, parity));
 }
 
 // TS: tokens of a tile.  CTAS 2: a pair of CTAs has a tile of 256 weight rows, 128 each, and each half of the tokens in its
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     } else if (warp == 1) {
       // -------------------------------------------------------- products
       if (ok && in_pair == 0)
-        ok = __all_sync(0xFFFFFFFFu, PAIR ? wait_cluster(acc_empty(buf), use ^ 1, ctl) : wait_bounded(acc_empty(buf), use ^ 1, ctl));
+        ok = __all_sync(0xFFFFFFFFu, wait_soon<PAIR>(acc_empty(buf), use ^ 1, ctl));
       if (ok && in_pair == 0) {
         tc_fence_after();
         const uint32_t what = uniform((uint32_t)(tokens_of(it.rows) >> 3) | (uint32_t)(shift >> 5) << 8 | (uint32_t)(sf_tiles == 2) << 10 | (uint32_t)buf << 11);

@@ -661,7 +661,7 @@ def moe_gemm(x_codes, x_scales, codes, scales, starts, counts, routed=None, gate
              stream=None) -> torch.Tensor:
     """mx4_gemm of each expert's rows of x [R, K] with its matrix of codes [E, N, K / 8] (gated: [E, 2, N, K / 8]): y [R, N].
     Rows of no expert are left alone (without `out`: as memory happens to be).  routed: how many rows the experts have
-    together, about (default: R); it picks the launch's shape."""
+    together, about; it picks the launch's shape (default: what moe_rows made R of)."""
     R, K, px, pxs = _mx_matrix(x_codes, x_scales, "x_codes")
     E = starts.shape[0]
     N, KW, pc, ps = _mx_matrix(codes, scales, "codes", (E, 2) if gated else (E,))
@@ -669,8 +669,9 @@ def moe_gemm(x_codes, x_scales, codes, scales, starts, counts, routed=None, gate
         raise ValueError(f"x has rows of {K}, the weights of {KW}")
     pst, pco = _here(starts, "starts", _I32, (E,)), _here(counts, "counts", _I32, (E,))
     out, dt, po = _mx_out(out, (R, N), dtype, x_codes.device, stream)
-    _call("qmm_moe_gemm", lib().qmm_moe_gemm(px, pxs, pc, ps, pst, pco, po, dt, gated, R if routed is None else routed, R, E,
-                                             N, K, _stream(stream)))
+    if routed is None:
+        routed = max(R // 128, R - 127 * E)                           # a row an expert, or full segments
+    _call("qmm_moe_gemm", lib().qmm_moe_gemm(px, pxs, pc, ps, pst, pco, po, dt, gated, routed, R, E, N, K, _stream(stream)))
     return out
 
 
