@@ -416,7 +416,8 @@ int64_t qmm_moe_rows(int64_t T, int64_t E, int64_t k);
  *   logits [T, E] (a stride in elements between rows, elements contiguous; their own alignment suffices).
  *   experts [T, k]: by falling logit, equal ones (-0 and 0 are) by rising index, NaN first.  A logit of -infinity masks its
  *     expert: it is never taken, and what a token lacks of k experts has expert -1, weight 0 and place -1.
- *   weights [T, k] float32: the softmax over the token's chosen experts (normalize != 0), or over all E.
+ *   weights [T, k] float32: the softmax over the token's chosen experts (normalize != 0), or over all E (NaN where the largest
+ *     logit is +infinity or NaN).
  *   starts, counts [E]: expert e's rows are starts[e] .. starts[e] + counts[e] - 1, in the order of the tokens; starts are
  *     multiples of 128, in the order of the experts (so that scale tiles belong to one expert).
  *   places [T, k]: the row of token t for its j-th expert.
