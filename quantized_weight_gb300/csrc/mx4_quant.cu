@@ -21,9 +21,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Elements of a row that a lane takes: 64 or 32 bytes.  bfloat16 is bound by instructions as much as by memory, and what a
-// block costs once (its scale, the maximum over its lanes) is then shared by two lanes rather than four; float32 is not, and
-// its loads are better at 32 bytes a lane.
+// Elements of a row that a lane takes: 32 bytes.  bfloat16 is bound by instructions as much as by memory, and what a block
+// costs once (its scale, the maximum over its lanes) is then shared by two lanes rather than four.
 template <bool BF16>
 constexpr int per_lane() { return BF16 ? 16 : 8; }
 template <bool BF16>
