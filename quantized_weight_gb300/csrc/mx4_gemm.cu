@@ -119,11 +119,19 @@ __device__ __forceinline__ void store(void *y, int64_t at, float v) {
     __stcs(static_cast<float *>(y) + at, v);
 }
 
-// silu(z) * u.  For a bfloat16 result the quick exponential does, whose relative error is below |z| * 2^-23, where z is far
-// enough from 0 to make silu small.  (Of a denominator beyond 2^126, z below -87, the quick division makes 0 instead of
-// 2^-120 or less.)
+// silu(z) * u, in six instructions for a bfloat16 result: the quick exponential does there, whose relative error is below
+// |z| * 2^-23, where z is far enough from 0 to make silu small.  (Of a denominator beyond 2^126, z below -87, the quick
+// reciprocal makes 0 instead of 2^-126 or less.)  A gated item's epilogue is as long as its products.
 template <bool BF16>
-__device__ __forceinline__ float gate(float z, float u) { return __fdividef(z, 1.0f + (BF16 ? __expf(-z) : expf(-z))) * u; }
+__device__ __forceinline__ float gate(float z, float u) {
+  float e, r;
+  if constexpr (BF16)
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));     // 2^(-z log2(e))
+  else
+    e = expf(-z);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r * u;
+}
 
 // wait_bounded for an accumulator, which of a pair the other CTA's epilogue frees, too.  The tensor core stands still
 // meanwhile, so the one warp that waits here tests for a while without sleeping (2 % of a gated prompt; the epilogue's eight
@@ -343,10 +351,10 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
         ok = __all_sync(0xFFFFFFFFu, wait_soon<PAIR>(acc_empty(buf), use ^ 1, ctl));
       if (ok && in_pair == 0) {
         tc_fence_after();
-        const uint32_t what = uniform((uint32_t)(tokens_of(it.rows) >> 3) | (uint32_t)(shift >> 5) << 8 | (uint32_t)(sf_tiles == 2) << 10 | (uint32_t)buf << 11);
+        const uint32_t what = uniform((uint32_t)(tokens_of(it.rows) >> 3) | (uint32_t)(shift >> 5) << 8 | (uint32_t)buf << 10);
         const uint32_t id = idesc_mxf4(CTAS * BM, 0) | (what & 255) << 17;
-        const uint32_t off = what >> 8 & 3, two_tiles = what >> 10 & 1;
-        const uint32_t d = tmem0 + (what >> 11) * (TWO * TS), sf0 = tmem0 + BUFS * TWO * TS;
+        const uint32_t off = TS % kMxRows == 0 ? 0 : what >> 8 & 3;
+        const uint32_t d = tmem0 + (what >> 10) * (TWO * TS), sf0 = tmem0 + BUFS * TWO * TS;
         const uint64_t ops = smem_desc_sw128(0), scales = smem_desc_scales(0);
         const uint32_t at0 = base0 >> 4, stage16 = stage_bytes >> 4;
         for (int ks = ks0; ks < ks1; ks++, issued++, ring.next(p.stages)) {
@@ -373,22 +381,28 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
           const uint32_t at = at0 + slot * stage16, bar = empty0 + 8 * slot;
           const uint64_t ad = ops | at, bd = ops | (at + (l.a >> 4));
           const uint64_t sd = scales | (at + ((l.a + l.b) >> 4)), td = scales | (at + ((l.a + l.b + l.sfa) >> 4));
+          // (where the tokens' second scale tile was not loaded, no MMA looks at what is copied from its place)
+          auto scales_of = [&](int a) {
+#pragma unroll
+            for (int g = 0; g < TWO; g++) tmem_cp_32x16b<CTAS>(sfa + g * 8 + a * 4, sd + (g * 2 + a) * (kMxTileBytes / 16));
+#pragma unroll
+            for (int t = 0; t < (TS > kMxRows ? 2 : 1); t++) tmem_cp_32x16b<CTAS>(sfb + a * 8 + 4 * t, td + (2 * t + a) * (kMxTileBytes / 16));
+          };
+          auto products_of = [&](int j) {
+#pragma unroll
+            for (int g = 0; g < TWO; g++)
+              umma_mxf4<CTAS>(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
+                              sfa + g * 8 + (j >> 1) * 4, sfb + (j >> 1) * 8 + off, j > 0 ? 1u : more);
+          };
           if (elect_one()) {
-#pragma unroll
-            for (int a = 0; a < 2; a++) {                // (two MMAs a scale tile)
-              if (2 * a >= steps) break;
-#pragma unroll
-              for (int g = 0; g < TWO; g++) tmem_cp_32x16b<CTAS>(sfa + g * 8 + a * 4, sd + (g * 2 + a) * (kMxTileBytes / 16));
-              tmem_cp_32x16b<CTAS>(sfb + a * 8, td + a * (kMxTileBytes / 16));
-              if (two_tiles) tmem_cp_32x16b<CTAS>(sfb + a * 8 + 4, td + (2 + a) * (kMxTileBytes / 16));
-#pragma unroll
-              for (int j = 2 * a; j < 2 * a + 2; j++) {
-                if (j >= steps) break;
-#pragma unroll
-                for (int g = 0; g < TWO; g++)
-                  umma_mxf4<CTAS>(d + g * TS, ad + g * (BM * (BK / 2) / 16) + 2 * j, bd + 2 * j, j & 1 ? id | kSecondScales : id,
-                                  sfa + g * 8 + a * 4, sfb + a * 8 + off, j > 0 ? 1u : more);
-              }
+            // two MMAs a scale tile; the last stage may have fewer
+            scales_of(0);
+            products_of(0);
+            if (steps > 1) products_of(1);
+            if (steps > 2) {
+              scales_of(1);
+              products_of(2);
+              if (steps > 3) products_of(3);
             }
             commit_mxf4<CTAS>(bar);
           }
