@@ -36,6 +36,7 @@ struct PlanParams {
   int64_t stride, T;
   int E, k, bf16, normalize;
   int whole;               // rows of logits can be read in vectors
+  int wide;                // four places of a token lie at a multiple of 16 bytes (the array itself needs only 4)
   int64_t tokens;          // of a CTA of the sorting kernel
   int blocks;              // of 32 tokens, that its shared memory holds at once
   int32_t *experts;
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const PlanParams p) 
         for (int i = 0; i < 8; i++)
           if (x[i] >= 0) x[i] = (int)(next[x[i]] + before[b * E + x[i]] + __popc(mask[b * E + x[i]] & ((1u << lane) - 1)));
         if (t < c1) {
-          if (k % 4 == 0) {
+          if (p.wide) {
 #pragma unroll
             for (int i = 0; i < 8; i += 4)
               if (j + i < k) *reinterpret_cast<int4 *>(p.places + t * k + j + i) = make_int4(x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -492,6 +493,7 @@ cudaError_t launch_moe_plan(const MoePlanArgs &a, cudaStream_t s) {
   p.logits = a.logits, p.stride = a.stride, p.T = a.T, p.E = (int)a.E, p.k = (int)a.k;
   p.bf16 = a.bf16, p.normalize = a.normalize;
   p.experts = a.experts, p.weights = a.weights, p.places = a.places, p.starts = a.starts, p.counts = a.counts;
+  p.wide = p.k % 4 == 0 && reinterpret_cast<uintptr_t>(p.places) % 16 == 0;
   if (p.E <= 32) return launch_plan<1>(p, s);
   if (p.E <= 64) return launch_plan<2>(p, s);
   if (p.E <= 128) return launch_plan<4>(p, s);

@@ -99,6 +99,43 @@ def test_plan_all_to_one_expert_and_strides(T, qmm):
     assert all(T.equal(a, b) for a, b in zip(out, again))
 
 
+@pytest.mark.parametrize("first", [1, 2, 3, 4])
+@pytest.mark.parametrize("k", [3, 4, 8, 12])
+@pytest.mark.parametrize("n", [5, 32, 33, 700])
+def test_routing_in_slices_of_one_array(T, qmm, n, k, first):
+    """Arrays of the routing need 4-byte alignment and no more: all five from one array, words that no call may touch between."""
+    E, K = 20, 64
+    g = T.Generator(device="cuda").manual_seed(n + k)
+    l, x = T.randn(n, E, generator=g, device="cuda"), T.randn(n, K, generator=g, device="cuda")
+    whole = T.full((3 * n * k + 2 * E + 64,), 0x5A5A5A5A, dtype=T.int32, device="cuda")
+    out, at, free = [], first, T.ones(len(whole), dtype=T.bool, device="cuda")
+    for shape in ((n, k), (n, k), (n, k), (E,), (E,)):
+        size = int(np.prod(shape))
+        out.append(whole[at:at + size].view(shape))
+        free[at:at + size] = False
+        at += size
+        at += (first - at) % 4 + 4                               # each begins as far from a multiple of 16 bytes as the first
+    assert all(t.data_ptr() % 16 == 4 * first % 16 for t in out)
+    out[1] = out[1].view(T.float32)
+    got = qmm.moe_plan(l, k, out=tuple(out))
+    qmm.check()
+    check_plan(got, plan_of(l.double().cpu().numpy(), k, True), E)
+    assert bool((whole[free] == 0x5A5A5A5A).all())
+    _, weights, places, starts, counts = got
+    R = qmm.moe_rows(n, E, k)
+    fresh = [t.clone() for t in got]
+    w = qmm.mx4_quantize(T.randn(E, 24, K, generator=g, device="cuda"))
+    ys, outs = [], []
+    for _, weights, places, starts, counts in (got, fresh):
+        y = T.zeros(R, 24, device="cuda")
+        qmm.moe_gemm(*qmm.moe_quantize(x, places, R), *w, starts, counts, routed=n * k, out=y)
+        qmm.moe_gemm(*qmm.moe_quantize(T.ones(R, K, device="cuda"), places, R, sorted=True), *w, starts, counts, routed=n * k)
+        ys.append(y)
+        outs.append(qmm.moe_combine(y, weights, places))
+    qmm.check()
+    assert T.equal(*ys) and T.equal(*outs) and bool((whole[free] == 0x5A5A5A5A).all())
+
+
 @pytest.mark.parametrize("n,K,E,k", [(1, 32, 4, 1), (9, 160, 8, 3), (70, 1056, 5, 2), (300, 2048, 64, 8), (33, 4096 + 32, 9, 4)])
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 def test_quantize_routed(T, qmm, n, K, E, k, dtype):
