@@ -119,9 +119,10 @@ __device__ __forceinline__ void store(void *y, int64_t at, float v) {
     __stcs(static_cast<float *>(y) + at, v);
 }
 
-// silu(z) * u, in six instructions for a bfloat16 result: the quick exponential does there, whose relative error is below
-// |z| * 2^-23, where z is far enough from 0 to make silu small.  (Of a denominator beyond 2^126, z below -87, the quick
-// reciprocal makes 0 instead of 2^-126 or less.)  A gated item's epilogue is as long as its products.
+// silu(z) * u of z from kFar up, in six instructions for a bfloat16 result: the quick exponential does there, whose relative
+// error is below 2^-22 of its own and |z| * 2^-23 of its argument's, 2^-16.9 in all.  A gated item's epilogue is as long as
+// its products.
+constexpr float kFar = -64.0f;
 template <bool BF16>
 __device__ __forceinline__ float gate(float z, float u) {
   float e, r;
@@ -131,6 +132,14 @@ __device__ __forceinline__ float gate(float z, float u) {
     e = expf(-z);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return z * r * u;
+}
+
+// Below, 1 + exp(z) is 1 and silu(z) * u = z * exp(z) * u, which a large u makes a whole result where exp(-z) is past float32
+// already.  So exp(z) is taken by halves, the second one last: no step of z * h * u * h loses what the result has (h is not
+// normal below -175, which costs the result 2^-140 at most).
+__device__ __forceinline__ float gate_far(float z, float u) {
+  const float h = expf(0.5f * z);
+  return z * h * u * h;
 }
 
 // wait_bounded for an accumulator, which of a pair the other CTA's epilogue frees, too.  The tensor core stands still
@@ -456,6 +465,23 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
                 st_cluster_f32(mapa_shared(mine + (((c0 + t) >> sh) * TWO + g) * BM * 4, t & (p.split - 1)), __uint_as_float(v[c][g][j]));
             }
         } else if (n < p.N) {
+          if constexpr (GATED) {
+            // a z below kFar (one test for 16) becomes 32, whose silu is 32, and its u what is then right
+#pragma unroll
+            for (int c = 0; c < CHUNKS; c++) {
+              bool far = false;
+#pragma unroll
+              for (int j = 0; j < 16; j++) far = far || __uint_as_float(v[c][0][j]) < kFar;
+              if (!far) continue;
+#pragma unroll
+              for (int j = 0; j < 16; j++) {
+                const float z = __uint_as_float(v[c][0][j]);
+                if (!(z < kFar)) continue;
+                v[c][TWO - 1][j] = __float_as_uint(gate_far(z, __uint_as_float(v[c][TWO - 1][j])) * 0.03125f);
+                v[c][0][j] = __float_as_uint(32.0f);
+              }
+            }
+          }
           auto out = [&](int c, int j) {
             return GATED ? gate<BF16>(__uint_as_float(v[c][0][j]), __uint_as_float(v[c][TWO - 1][j])) : __uint_as_float(v[c][0][j]);
           };
@@ -495,8 +521,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
             sum[g] = 0.0f;
             for (int s = 0; s < p.split; s++) sum[g] += red[((s * (TS >> sh) + t) * TWO + g) * BM + r];
           }
-          if (n0 + r < p.N)
-            store<BF16>(p.y, ((int64_t)it.row + t * p.split + part) * p.N + n0 + r, GATED ? gate<BF16>(sum[0], sum[TWO - 1]) : sum[0]);
+          if (GATED) sum[0] = sum[0] < kFar ? gate_far(sum[0], sum[TWO - 1]) : gate<BF16>(sum[0], sum[TWO - 1]);
+          if (n0 + r < p.N) store<BF16>(p.y, ((int64_t)it.row + t * p.split + part) * p.N + n0 + r, sum[0]);
         }
       }
       __syncwarp();

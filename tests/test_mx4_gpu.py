@@ -230,6 +230,36 @@ def test_gated_extremes(T, qmm):
     assert (np.abs(y.cpu().numpy() - want) <= bound + 2.0 ** -24 * np.abs(want)).all()
 
 
+# single CTAs of 64 tokens, K in parts over a cluster, 128 tokens, pairs
+@pytest.mark.parametrize("M,N,K", [(3, 400, 32), (8, 400, 4096), (300, 400, 512), (1500, 2900, 2720)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_gated_far_out(T, qmm, M, N, K, dtype):
+    """silu where exp(-z) nears the end of float32 and passes it, times a u that makes a whole result of it."""
+    v = np.arange(N) % 360 / 2                                   # -z, 0 to 179.5
+    g, u = np.zeros((N, K)), np.zeros((N, K))
+    full = (v // 6).astype(int)
+    rest = v - 6 * full                                          # of halves, as two values of the format
+    top = np.array([0, 0.5, 1, 1.5, 2, 2, 3, 3, 4, 4, 4, 4])[(2 * rest).astype(int)]
+    for n in range(N):
+        g[n, :full[n]] = -6
+        g[n, 30], g[n, 31] = -top[n], -(rest[n] - top[n])
+    u[:, 0] = np.where(v < 60, -1.5, 1.5 * 2.0 ** 120)
+    x = np.ones((M, K))
+    made = [ref.quantize(a) for a in (x, g, u)]
+    assert all(np.array_equal(ref.values(*m), a) for m, a in zip(made, (x, g, u)))
+    w = [on_gpu(T, *m) for m in made[1:]]
+    y = qmm.mx4_gemm(*on_gpu(T, *made[0]), T.stack([a[0] for a in w]), T.stack([a[1] for a in w]), gated=True, dtype=getattr(T, dtype))
+    qmm.check()
+    want = (-v / (1 + np.exp(v)) * u[:, 0])[None]
+    got = y.double().cpu().numpy()
+    # Both sums are exact.  float32: an exponential of 2 ulp, taken twice far out, and a quotient of 1 ulp, four roundings: 16
+    # halves of an ulp at most.  bfloat16: the quick exponential, 2^-22 and |z| * 2^-23 where it is used (z from -64 up), less
+    # than 2^-16.9 with the others, and one rounding to 8 bits.  Far below what is normal a result has fewer bits.
+    each = 2.0 ** -20 if dtype == "float32" else 2.0 ** -16.8 + 2.0 ** -8
+    assert (np.abs(got - want) <= each * np.abs(want) + 2.0 ** -126).all()
+    assert (np.abs(want) > 1e-6)[0, (v > 85) & (v < 95)].all()   # (whole results among them)
+
+
 def test_product_refusals(T, qmm):
     x = qmm.mx4_quantize(T.ones(4, 64, device="cuda"))
     w = qmm.mx4_quantize(T.ones(6, 64, device="cuda"))
