@@ -497,7 +497,8 @@ int qmm_test_timeout_next_attend(int64_t limit_ns);
 
 /*
  * qmm_test_timeout_next_mx4 -- the same for the microscaled product: in the next qmm_mx4_gemm or qmm_moe_gemm launch, every
- *   block's first wait for sums is one that nothing ends, with this limit.  The launch writes nothing.
+ *   block's first wait for sums is one that nothing ends, with this limit.  (Where pairs of blocks share a tile, one of each
+ *   copies nothing, either by turns.)  The launch writes nothing.
  */
 int qmm_test_timeout_next_mx4(int64_t limit_ns);
 

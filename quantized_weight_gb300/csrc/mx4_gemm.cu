@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   uint8_t *tail = smem + l.ring + l.red + l.list + 8 * (2 * MAX_STAGES + 6);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tail);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tail + 4);
-  uint32_t *fine = reinterpret_cast<uint32_t *>(tail + 8);       // [split]: that CTA's part is whole
+  uint32_t *fine = reinterpret_cast<uint32_t *>(tail + 8);       // [split]: that CTA's part is whole; of a pair: how it ended
   const WaitCtl ctl{abort_flag, &g_mx4_status};
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the CTA of its cluster (one that splits K, or a pair)
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
   int issued = 0;                              // stages so far
   int ready = 0;                               // stages known to have landed
   int local = 0;                               // items so far
-  bool ok = true;
+  // (test hook: the copying warp of one CTA of each pair, the first or the second by turns, is one that gave up)
+  bool ok = !(PAIR && p.test_wait_ns != 0 && warp == 0 && in_pair == (first & 1));
   for (int i = first; i < items; i += step, local++) {
     const Item it = local < LISTED ? listed[local] : item_at(i);
     const int64_t n0 = it.n0 + in_pair * BM;   // of this CTA
@@ -530,22 +531,48 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
     }
   }
   if (SPLITS && p.split > 1 && local == 0) cluster_wait();
-  if (warp == 0) {
+  bool gave_up = false;                        // some wait of the CTA, or of the pair
+  if constexpr (PAIR) {
+    // A stage that the MMAs have read has landed in both CTAs.
+    if (warp == 0 && ok)
+      for (int j = issued > p.stages ? issued - p.stages : 0; j < issued && ok; j++)
+        ok = __all_sync(0xFFFFFFFFu, wait_bounded(empty(j % p.stages), (j / p.stages) & 1, ctl));
+    tc_fence_before();
+    __syncthreads();                           // (no role issues anything more, or gives up)
+    // Each tells both how many stages it has copied, and whether a wait gave up.
+    if (threadIdx.x < 2) st_cluster_u32(mapa_shared(smem_addr(fine + in_pair), threadIdx.x), (uint32_t)issued << 1 | (*abort_flag ? 1u : 0u));
+    __syncwarp();
+    cluster_sync();                            // (and of what follows, only where a wait gave up does any touch the other's memory)
+    gave_up = (fine[0] | fine[1]) & 1;
+    if (gave_up && warp == 0 && in_pair == 0) {
+      // Every copy lands before any memory goes to others.  The first CTA's barriers have the bytes of both; of a stage that
+      // only the second has copied they expect them now, and of one that it has not they do without.
+      const int n0 = (int)(fine[0] >> 1), n1 = (int)(fine[1] >> 1), n = max(n0, n1);
+      for (int j = max(0, n - p.stages); j < n; j++) {
+        const uint32_t bar = full(j % p.stages);
+        if (lane == 0 && j >= n0) mbar_arrive_expect_tx(bar, (uint32_t)l.stage);
+        if (lane == 0 && j >= n1) mbar_complete_tx(bar, (uint32_t)l.stage);
+        __syncwarp();
+        wait_drain(bar, (j / p.stages) & 1);
+      }
+    }
+  } else {
     // every copy lands before this CTA's memory goes to another
-    if (in_pair == 0)
+    if (warp == 0)
       for (int j = issued > p.stages ? issued - p.stages : 0; j < issued; j++) wait_drain(full(j % p.stages), (j / p.stages) & 1);
-    // (a second CTA's may be ahead of the first one's where a wait gave up: a ms is a thousand times what they take)
-    if (PAIR && !ok)
-      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) __nanosleep(10000);
+    tc_fence_before();
+    __syncthreads();
+    gave_up = *abort_flag != 0;
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1 && *abort_flag && in_pair == 0) {      // (whichever wait gave up, MMAs may be in flight)
-    if (elect_one()) commit_mxf4<CTAS>(drain_bar);
+  if (gave_up && warp == 1) {                  // (whichever wait gave up, MMAs may be in flight)
+    if (in_pair == 0 && elect_one()) commit_mxf4<CTAS>(drain_bar);
     __syncwarp();
     wait_drain(drain_bar, 0);
   }
-  if constexpr (PAIR) cluster_sync();          // (each one's memory is the other's, too, until both have ended)
+  if (PAIR && gave_up) {
+    __syncwarp();
+    cluster_sync();                            // (each one's memory is the other's, too, until both have ended)
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_for<CTAS>(tmem, TMEM_COLS);

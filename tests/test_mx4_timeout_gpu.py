@@ -1,6 +1,8 @@
 """A bounded wait of the microscaled product that runs out, on the GPU, without faulting or hanging it: the test hook makes the
 epilogue of every block wait on a barrier that nothing completes, while copies and products are in flight.  All roles have to
 leave, nothing is written, the launch is reported once, and the next call is right."""
+import time
+
 import numpy as np
 import pytest
 
@@ -46,6 +48,32 @@ def test_wait_runs_out(T, qmm, M, N, K, gated):
         want, bound = ref.product(xv[some], np.stack([v for *_, v in ws]) if gated else ws[0][2], gated)
         check_product(out[T.from_numpy(some).cuda()], want, bound, "float32")
     fails_once_then_is_right(T, qmm, lambda: qmm.mx4_gemm(*x, codes, scales, gated=gated, out=out), out, check)
+
+
+# (under the hook one CTA of each pair copies nothing, the first or the second by turns, while the other fills its ring)
+@pytest.mark.parametrize("M,N,K", [(1500, 2900, 2720), (1281, 2900, 2592), (2500, 5000, 2720)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_pairs_know_of_each_others_copies(T, qmm, M, N, K, gated):
+    """Copies that only one CTA of a pair has begun are waited for by what has landed: at once, not until a limit of 2 s."""
+    if T.cuda.get_device_properties(0).multi_processor_count == 152:
+        assert qmm.mx4_gemm_tile(M, N, K, gated=gated) > 1024
+    x = T.randn(M, K, device="cuda")
+    w = T.randn(*((2, N, K) if gated else (N, K)), device="cuda") * K ** -0.5
+    x, w = qmm.mx4_quantize(x), qmm.mx4_quantize(w)
+    want = qmm.mx4_gemm(*x, *w, gated=gated)
+    qmm.check()
+    out = T.full((M, N), 7.0, device="cuda")
+    for limit in (50_000, 200_000):
+        begin = time.monotonic()
+        qmm.test_timeout_next_mx4(limit)
+        qmm.mx4_gemm(*x, *w, gated=gated, out=out)
+        with pytest.raises(qmm.QmmError) as e:
+            qmm.check()
+        assert time.monotonic() - begin < 1.0
+        assert e.value.status == TIMEOUT and bool((out == 7.0).all())
+    again = qmm.mx4_gemm(*x, *w, gated=gated)
+    qmm.check()
+    assert T.equal(again, want)
 
 
 def test_wait_runs_out_among_experts(T, qmm):
