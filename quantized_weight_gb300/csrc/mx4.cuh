@@ -7,17 +7,9 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 
+#include "mx4_layout.h"
+
 namespace qmm {
-
-constexpr int kMxBlock = 32;        // elements that share a scale
-constexpr int kMxRows = 128;        // rows of a scale tile
-constexpr int kMxTileK = 128;       // elements of a row in a scale tile
-constexpr int kMxTileBytes = 512;
-
-__host__ __device__ inline int64_t mx4_k_tiles(int64_t K) { return (K + kMxTileK - 1) / kMxTileK; }
-__host__ __device__ inline int64_t mx4_scales_bytes(int64_t rows, int64_t K) {
-  return (rows + kMxRows - 1) / kMxRows * mx4_k_tiles(K) * kMxTileBytes;
-}
 
 // Offset of the four scales of a row in K tile `kt` of a matrix with `k_tiles` of them a row.
 __device__ __forceinline__ int64_t mx4_scale_word(int64_t row, int64_t kt, int64_t k_tiles) {

@@ -47,16 +47,12 @@ __device__ int g_mx4_status = 0;   // QMM_OK or QMM_ERR_DEVICE_TIMEOUT (-6)
 
 namespace {
 
+using namespace mx4;
 using namespace sm100;
 
-constexpr int BM = 128;                    // weight rows of a tile
-constexpr int BK = 256;                    // elements of a stage: 128 bytes of a row, one swizzle atom wide
 constexpr int MMA_K = 64;
 constexpr int EPI_WARP0 = 2, EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-constexpr int MAX_STAGES = 8;
-constexpr int MAX_SPLIT = 8;
-constexpr int SMEM_LIMIT = 227 * 1024;
 
 struct Params {
   const uint8_t *xs, *ws;
@@ -72,36 +68,6 @@ struct Params {
   int split;                               // CTAs of a cluster, each with a part of K
   unsigned long long test_wait_ns;         // test hook: the epilogues' first wait is for nothing, and runs out after so long
 };
-
-// One piece of work: a weight tile and a token tile.
-struct alignas(16) Item {
-  int n0;                                  // first row of the weight tile (a pair's: of its first CTA's)
-  int row;                                 // first row of the token tile in x and y
-  int rows;                                // tokens of it
-  int expert;
-};
-constexpr int LISTED = 32;                 // items of a CTA that are found before it begins
-
-struct Layout {                            // of a CTA's shared memory
-  int a, b, sfa, sfb, stage;               // bytes: weights, tokens, scales, all
-  int ring, red, list, bars, total;
-};
-__host__ __device__ inline Layout layout(bool gated, int ts, int ctas, int stages, int split, int experts) {
-  Layout l;
-  const int two = gated ? 2 : 1;
-  l.a = two * BM * (BK / 2);
-  l.b = ts / ctas * (BK / 2);
-  l.sfa = two * 2 * kMxTileBytes;
-  l.sfb = (ts > kMxRows ? 2 : 1) * 2 * kMxTileBytes;
-  l.stage = l.a + l.b + l.sfa + l.sfb;     // (multiples of 1024 bytes)
-  l.ring = stages * l.stage;
-  l.red = split > 1 ? two * ts * BM * 4 : 0;
-  l.list = LISTED * (int)sizeof(Item) + (3 * experts + 1) * 4;     // items; starts, counts, and token tiles before
-  l.list = (l.list + 15) & ~15;
-  l.bars = 8 * (2 * MAX_STAGES + 4 + 2) + 16 + 4 * MAX_SPLIT;
-  l.total = l.ring + l.red + l.list + l.bars + 1024;   // (1024: the ring begins at a multiple of it)
-  return l;
-}
 
 struct Ring {
   int s = 0;
@@ -644,16 +610,15 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
       if (cost < least) least = cost, p.split = split;
     }
   }
-  const int64_t limit = TWO_AN_SM && items * p.split > sms ? SMEM_LIMIT / 2 : SMEM_LIMIT;
-  p.stages = (int)(limit - layout(GATED, TS, CTAS, 0, p.split, p.experts).total) / layout(GATED, TS, CTAS, 0, p.split, p.experts).stage;
-  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  const bool two_an_sm = TWO_AN_SM && items * p.split > sms;
+  p.stages = ring_stages(GATED, TS, CTAS, p.split, p.experts, two_an_sm);
   // (a part of K that is shorter than the ring leaves the next call's CTAs room to begin)
   const int part = (p.k_stages + p.split - 1) / p.split;
   if (items * p.split <= room && p.stages > part) p.stages = part;
   const int smem = layout(GATED, TS, CTAS, p.stages, p.split, p.experts).total;
   auto kern = mx4_gemm_kernel<GATED, BF16, TS, CTAS>;
   const int cluster = CTAS == 2 ? 2 : p.split;
-  int64_t grid = (limit < SMEM_LIMIT ? room : sms) / cluster;
+  int64_t grid = (two_an_sm ? room : sms) / cluster;
   if (most < grid) grid = most;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(grid * cluster));
