@@ -179,7 +179,9 @@ __global__ void __launch_bounds__(NUM_THREADS, TS == 64 && !GATED ? 2 : 1)
       tma_prefetch_2d(&tmap_w, (k0 + lane / TWO) * (BK / 2), (int)((lane % TWO) * p.N + (int64_t)nt * BM));
   }
   pdl_wait();
-  pdl_launch_dependents();
+  // (by the warp that has allocated: the next launch's CTAs may begin once one thread of each CTA says so, and one that took
+  // this SM's tensor memory first would wait for this launch, and this launch for the memory)
+  if (warp == 1) pdl_launch_dependents();
   if (warp == 0) {
     // the experts' rows, made to fit x, and the token tiles before each
     uint32_t sum = 0;

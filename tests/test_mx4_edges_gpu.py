@@ -146,6 +146,38 @@ def test_calls_beside_one_another(T, qmm):
     assert all(T.equal(a, b) for a, b in zip(got, alone)) and all(T.equal(a, b) for a, b in zip(again, plan))
 
 
+def test_calls_one_after_another(T, qmm):
+    """Each may begin while the one before it ends, beside it on an SM, whatever tensor memory both want: clusters, two CTAs an
+    SM, single ones and pairs in turns, also by a graph."""
+    g = T.Generator(device="cuda").manual_seed(1)
+    make = lambda *s: qmm.mx4_quantize(T.randn(*s, generator=g, device="cuda") * s[-1] ** -0.5)
+    sizes = [(8, 512, 4096, 1), (8, 512, 4096, 0), (8, 20000, 512, 0), (8, 20000, 512, 1), (100, 900, 512, 1), (1500, 2900, 2720, 0),
+             (300, 700, 512, 0), (1500, 2900, 2720, 1), (1, 128, 64, 0), (1, 128, 64, 1)]
+    calls = [(make(M, K), make(*((2, N, K) if gated else (N, K))), bool(gated)) for M, N, K, gated in sizes]
+    alone = []
+    for x, w, gated in calls:
+        alone.append(qmm.mx4_gemm(*x, *w, gated=gated))
+        T.cuda.synchronize()
+    order = [i for step in (1, 3, 7, 9) for i in (step * j % len(calls) for j in range(len(calls)))]
+    outs = [T.empty_like(alone[i]) for i in order]
+    graph = T.cuda.CUDAGraph()
+    with T.cuda.graph(graph):
+        for i, out in zip(order, outs):
+            x, w, gated = calls[i]
+            qmm.mx4_gemm(*x, *w, gated=gated, out=out)
+    for round in range(6):
+        for out in outs:
+            out.fill_(7.0)
+        if round % 2:
+            graph.replay()
+        else:
+            for i, out in zip(order, outs):
+                x, w, gated = calls[i]
+                qmm.mx4_gemm(*x, *w, gated=gated, out=out)
+        qmm.check()
+        assert all(T.equal(out, alone[i]) for i, out in zip(order, outs))
+
+
 def test_weights_written_right_before(T, qmm):
     """A product may follow the quantizer of its weights at once, whatever begins early."""
     g = T.Generator(device="cuda").manual_seed(0)
