@@ -516,6 +516,8 @@ def mx4_scales_size(rows, K) -> int:
 
 def mx4_scales(plain) -> torch.Tensor:
     """Scales of a checkpoint, bytes [..., rows, K / 32], in the tiles that the products read (include/qmm.h)."""
+    if plain.is_floating_point():
+        raise TypeError(f"scales are bytes, got {plain.dtype}: pass their bits, .view(torch.uint8)")
     lead, (rows, blocks) = plain.shape[:-2], plain.shape[-2:]
     across, down = -(-blocks // 4), -(-rows // 128)
     full = torch.zeros((*lead, down * 128, across * 4), dtype=torch.uint8, device=plain.device)

@@ -155,6 +155,16 @@ def test_scales_of_a_checkpoint(rows, blocks):
     assert np.array_equal(qmm.mx4_scales(plain[0]).numpy(), got[0].numpy())
 
 
+def test_scales_of_a_checkpoint_are_bytes():
+    """A floating-point type's numbers are not its bits: 2 ** (byte - 127) would be made a whole number."""
+    plain = torch.arange(100, 108, dtype=torch.uint8).view(2, 4)
+    for bad in (plain.view(torch.float8_e8m0fnu), plain.float(), plain.bfloat16()):
+        with pytest.raises(TypeError):
+            qmm.mx4_scales(bad)
+    bits = plain.view(torch.float8_e8m0fnu).view(torch.uint8)
+    assert np.array_equal(qmm.mx4_scales(bits).numpy(), ref.tiles(plain.numpy()))
+
+
 def test_reference_is_the_format():
     """The reference's own borders: halves go to the even code, 7 and more to 6, the sign of a zero stays."""
     x = np.zeros((1, 32))
