@@ -1,10 +1,11 @@
 // moe.cu -- tokens to experts and back: the plan (each token's best experts, and the tokens sorted by expert) and the
 // weighted sum of a token's rows.
 //
-// Measured: 8 tokens, 6 of 64 experts 5.3 us, one block: a launch, six rounds of maxima, the barriers of the sort.  16381
-// tokens, 8 of 128 19 us (11.5 and 10 us of cold caches): the choice is bound by its 380 instructions a token, the sort by the
-// shared memory of its 16 SMs (10.1 us; 8 SMs 13.8, and three kernels with the counts kept in `places` 16 + 5).  The sum is
-// bound by memory: 8191 tokens of 6 rows of 2048 bfloat16 39 us, 88 % of measured HBM (rows of an odd length 83 %).
+// Measured: 8 tokens, 6 of 64 experts 5.7 us, one block: a launch, six rounds of maxima, the barriers of the sort.  16381
+// tokens, 8 of 128 19 us (12.8 and 11.4 us of cold caches): the choice is bound by its 360 instructions a token, which keep the ALU
+// 72 % busy, the sort by what its 16 SMs wait for (loads, barriers and shared memory; 8 SMs took 3.7 us longer, and three kernels
+// with the counts kept in `places` 11).  The sum is bound by memory: 8191 tokens of 6 rows of 2048 bfloat16 39.7 us, 87 % of
+// measured HBM (rows of an odd length 83 %).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -21,10 +21,9 @@
 // A call with few items splits K over the CTAs of a cluster: each writes its partial tile into the shared memory of the CTA
 // that owns the token, and the owner adds them up in the order of the ranks, so that the sum is the same every time.
 //
-// Measured: 8192 x 17408 x 5120 (bfloat16 out) 213 us, 6.9 PFLOP/s; what remains is the end of an item (its accumulator's
-// way to registers, the next one's first scales) and, of 8 %, the stores.  8 x 151936 x 2048 28 us, 86 % of measured HBM.  Few
-// and small items are bound by latency: 8 x 4096 x 4096 takes 7.3 us of a floor of 1.3, some 2 us of launch and set-up, 1.6 us
-// for the first bytes, 0.6 us of products and 1.5 us to join the parts.
+// Measured: 8192 x 17408 x 5120 (bfloat16 out) 212 us, 6.9 PFLOP/s; what remains is the end of an item (its accumulator's
+// way to registers, the next one's first scales) and, of 8 %, the stores.  1 x 151936 x 2048 29.5 us, 83 % of measured HBM.  Few
+// and small items are bound by latency: 8 x 4096 x 4096 takes 7.2 us of a floor of 1.3.
 //
 // Every wait is bounded (bounded_wait.cuh).  One that runs out ends the CTA's work: it writes nothing more, waits for its
 // copies and MMAs in flight, frees its TMEM, and qmm_check() reports it.
@@ -600,8 +599,8 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, Params p, int box, int64_t items, 
   p.n_tiles = (p.n_tiles + CTAS - 1) / CTAS;
   p.most_tiles = (int)(a.M / TS + a.experts);
   // Parts of K where items leave SMs without work: two CTAs an SM with rings of half its shared memory (gated: one; and eight
-  // to a cluster do not all find room).  A stage takes 320 ns (gated: 400), joining the parts 3 us: 8 x 4096 x 4096 8.7, 8.9,
-  // 7.5, 7.1 us with 1, 2, 4, 8 parts, 8 x 5120 x 17408 25.6, 19.3, 14.0 us with 1, 2, 4, 8 x 12288 x 4096 9.8, 10.3 us with 1, 2.
+  // to a cluster do not all find room).  A stage takes 320 ns (gated: 400), joining the parts 3 us: 8 x 4096 x 4096 8.7, 9.6,
+  // 7.6, 7.2 us with 1, 2, 4, 8 parts, 8 x 5120 x 17408 23.4, 17.5, 14.2 us with 1, 2, 4, 8 x 12288 x 4096 9.3, 10.6 us with 1, 2.
   constexpr bool TWO_AN_SM = TS == 64 && CTAS == 1 && !GATED;
   const int64_t room = TWO_AN_SM ? 2 * sms : sms;
   p.split = 1;
@@ -660,11 +659,13 @@ struct Cut {
 
 // A stage of 256 elements takes so many ns, an item's beginning and end so many more, and the SMs take items in rounds: wide
 // tiles and pairs where there are many tokens, narrow ones where those fill the SMs better.  Measured, us, for tiles of 64,
-// 128, 192, 256 tokens and pairs with 256: 8192 x 8192 x 8192: 543, 281, 219, 179, 152; 1024 x 6144 x 2048 (float32): 21.3,
-// 13.9, 12.1, 14.3, 14.2; 256 x 4096 x 4096: 9.1, 9.4, 10.1, 11.1, 10.3; 4096 x 4096 x 1024: 26, 17, 15, 14.6, 17.5.  8191 tokens by 6
-// of 64 experts of 2048 x 1408, 256 tokens and pairs: 87, 91; by 2 of 8 of 4096 x 4096: 107, 98.  Gated, 64 and 128 tokens and
-// pairs with 128: 1024 x 4096 x 4096: 32, 21.1, 18.6; 8191 tokens by 6 of 64 experts of 1408 x 2048: -, 139, 145, of 1536 x 4096:
-// -, 269, 234.
+// 128, 192, 256 tokens and pairs with 256: 8192 x 8192 x 8192: 313, 270, 211, 176, 153; 1024 x 6144 x 2048 (float32): 15.8,
+// 13.1, 11.8, 14.7, 14.6; 256 x 4096 x 4096: 9.2, 9.1, 9.9, 10.9, 11.3; 4096 x 4096 x 1024: 18.8, 15.8, 13.9, 13.9, 17.2.  8191
+// tokens by 6 of 64 experts of 2048 x 1408: 129, 103, 90, 86, 91; by 2 of 8 of 4096 x 4096: 175, 149, 114, 104, 96.  Gated, 64
+// and 128 tokens and pairs with 128: 1024 x 4096 x 4096: 31, 20.5, 19.0; 8192 x 8192 x 8192: 691, 384, 303; 8191 tokens by 6 of 64
+// experts of 1408 x 2048: 220, 131, 145, of 1536 x 4096: 434, 251, 228; by 8 of 128 of 768 x 2048: 164, 100, 110
+// (where the rule takes pairs: its gated figures are of an earlier state, these times come to 417 and 900 ns for 128 tokens, 287
+// and 2100 for pairs).
 Cut cut_for(bool gated, const Mx4GemmArgs &a, int sms) {
   // experts that are met and rows of each, about
   const int64_t met = a.starts ? (a.routed < a.experts ? (a.routed > 1 ? a.routed : 1) : a.experts) : 1;

@@ -5,8 +5,9 @@
 // (or far below the first border), so the codes are the nearest ones to the exact quotient, halves to the even code.
 //
 // A value is read once (2 or 4 bytes) and leaves as 17/32 of a byte.  Measured: 17408 x 5120 float32 56 us, all of measured HBM;
-// 8192 x 5120 bfloat16 18.3 us, 86 % (with 8 elements a lane 22.4: instructions); 4093 x 2048 bfloat16 to 8 places each 12.4 us,
-// 62 % (scattered rows, 4-byte scales); back, 17408 x 5120, 61 us, 98 % (with a lane's two stores 32 bytes apart 84).
+// 8192 x 5120 bfloat16 18.4 us, 85 % (with 8 elements a lane 22.4: instructions); 4093 x 2048 bfloat16 to 8 places each 12.5 us,
+// 62 %, and 24576 sorted rows of 1408 20.9 us, 62 % (no unit is above 60 % there: places are loaded first, then rows); back,
+// 17408 x 5120, 61 us, 98 % (with a lane's two stores 32 bytes apart 84).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
