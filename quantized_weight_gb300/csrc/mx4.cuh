@@ -16,26 +16,6 @@ __device__ __forceinline__ int64_t mx4_scale_word(int64_t row, int64_t kt, int64
   return ((row >> 7) * k_tiles + kt) * kMxTileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
-// Quotients of whole numbers below 2^31 by a divisor known to the host, as a product's upper half (a 64-bit division is some
-// hundred instructions, more than all else that these kernels do for a word).
-struct Divisor {
-  uint32_t d = 1, m = 1, s = 0;
-  Divisor() = default;
-  explicit Divisor(uint32_t by) : d(by) {
-    while (((uint64_t)1 << s) < by) s++;
-    m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - by)) / by + 1);
-  }
-  __host__ __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
-    return (uint32_t)(((((uint64_t)m * n) >> 32) + n) >> s);
-  }
-  // n becomes the remainder
-  __host__ __device__ __forceinline__ uint32_t split(uint32_t &n) const {
-    const uint32_t q = quotient(n);
-    n -= q * d;
-    return q;
-  }
-};
-
 // 2 ** (scale - 127); 255 is NaN.
 __device__ __forceinline__ float mx4_scale(uint32_t scale) {
   return __uint_as_float(scale == 255 ? 0x7FC00000u : scale == 0 ? 0x00400000u : scale << 23);

@@ -1,4 +1,5 @@
-// mx4_layout.h -- sizes of the microscaled format's scale tiles, and what a CTA of its product holds in shared memory.
+// mx4_layout.h -- sizes of the microscaled format's scale tiles, quotients by sizes, and what a CTA of its product holds in
+// shared memory.
 #pragma once
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -14,6 +15,27 @@ __host__ __device__ inline int64_t mx4_k_tiles(int64_t K) { return (K + kMxTileK
 __host__ __device__ inline int64_t mx4_scales_bytes(int64_t rows, int64_t K) {
   return (rows + kMxRows - 1) / kMxRows * mx4_k_tiles(K) * kMxTileBytes;
 }
+
+// Quotients of whole numbers below 2^31 by a divisor known to the host, as a product's upper half (a 64-bit division is some
+// hundred instructions, more than all else that these kernels do for a word).  Granlund and Montgomery, "Division by invariant
+// integers using multiplication" (1994): m = floor(2^32 (2^s - d) / d) + 1 with s the least of 2^s >= d.
+struct Divisor {
+  uint32_t d = 1, m = 1, s = 0;
+  Divisor() = default;
+  explicit Divisor(uint32_t by) : d(by) {
+    while (((uint64_t)1 << s) < by) s++;
+    m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - by)) / by + 1);
+  }
+  __host__ __device__ __forceinline__ uint32_t quotient(uint32_t n) const {
+    return (uint32_t)(((((uint64_t)m * n) >> 32) + n) >> s);
+  }
+  // n becomes the remainder
+  __host__ __device__ __forceinline__ uint32_t split(uint32_t &n) const {
+    const uint32_t q = quotient(n);
+    n -= q * d;
+    return q;
+  }
+};
 
 namespace mx4 {                            // of the product (mx4_gemm.cu)
 
