@@ -1,7 +1,7 @@
 // moe.cu -- tokens to experts and back: the plan (each token's best experts, and the tokens sorted by expert) and the
 // weighted sum of a token's rows.
 //
-// Measured: 8 tokens, 6 of 64 experts 5.7 us, one block: a launch, six rounds of maxima, the barriers of the sort.  16381
+// Measured: 8 tokens, 6 of 64 experts 5.2 to 5.7 us, one block: a launch, six rounds of maxima, the barriers of the sort.  16381
 // tokens, 8 of 128 19 us (12.8 and 11.4 us of cold caches): the choice is bound by its 360 instructions a token, which keep the ALU
 // 72 % busy, the sort by what its 16 SMs wait for (loads, barriers and shared memory; 8 SMs took 3.7 us longer, and three kernels
 // with the counts kept in `places` 11).  The sum is bound by memory: 8191 tokens of 6 rows of 2048 bfloat16 39.7 us, 87 % of

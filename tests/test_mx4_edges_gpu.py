@@ -165,10 +165,10 @@ def test_calls_one_after_another(T, qmm):
         for i, out in zip(order, outs):
             x, w, gated = calls[i]
             qmm.mx4_gemm(*x, *w, gated=gated, out=out)
-    for round in range(6):
+    for turn in range(6):
         for out in outs:
             out.fill_(7.0)
-        if round % 2:
+        if turn % 2:
             graph.replay()
         else:
             for i, out in zip(order, outs):
